@@ -296,6 +296,114 @@ int muse_lmhead_forward_group_host(muse_lmhead *h, const float *hidden_host, con
                                    float eps, const muse_gemv_segment *segments,
                                    int n_segments, void *stream);
 
+/* Element types of the rows that muse_lmhead_score and muse_lmhead_distill read. */
+#define MUSE_DTYPE_F32 0
+#define MUSE_DTYPE_F16 1
+#define MUSE_DTYPE_BF16 2
+
+/* Most alternatives of a row that are returned (score) or given (distill). */
+#define MUSE_MAX_TOP 64
+
+/*
+ * Scores of n rows of finished logits: for row x of n_rows values (the
+ * handle's n_rows, the vocabulary), z = x / temperature,
+ *     lse      = log sum_i exp(z_i)
+ *     logprob  = z[token] - lse
+ *     rank     = how many i come before the token in (x descending, index ascending)
+ *     entropy  = -sum_i p_i log p_i,  p = exp(z - lse)   (natural log)
+ *     top_ids, top_logprobs = the n_top first i in that order, z_i - lse
+ * Sums are held in f32.  The pages take softmax and logprobs over the capped
+ * logits ("Chapter 20 — Final norm, LM head, and the soft cap", §20.7): pass
+ * the logits that a forward returned.
+ *   logits  device, dtype MUSE_DTYPE_*, rows ld >= n_rows elements apart,
+ *           aligned to one element only (any ld, any n_rows).
+ *   n       0 .. 2^31-1 rows, not bound by max_batch; 0 does nothing.
+ *   tokens  [n] int32, device; a value outside 0..n_rows-1 (a padded row) gives
+ *           logprob 0 and rank -1.  NULL when logprob and rank are NULL.
+ *   temperature  finite, > 0.
+ *   n_top   0 .. MUSE_MAX_TOP; top_ids and top_logprobs are [n][n_top] and
+ *           needed when n_top > 0.  Entries beyond n_rows are -1 and -infinity.
+ *   logprob [n] f32, rank [n] int32, lse [n] f32, entropy [n] f32: each may be
+ *           NULL (at least one output is needed).
+ * A logit of -infinity is a masked one: probability 0, and an alternative only
+ * where fewer others are left.  A row of nothing else has lse and logprobs
+ * -infinity and entropy 0.  With a NaN or +infinity in a row, its lse, logprob
+ * and entropy are NaN and its rank and alternatives are unspecified (ids stay in
+ * -1..n_rows-1).  Uses no workspace of the handle: calls may overlap.  One launch.
+ */
+int muse_lmhead_score(muse_lmhead *h, const void *logits, int dtype, int64_t n, int64_t ld,
+                      const int32_t *tokens, float temperature, int n_top, float *logprob, int32_t *rank,
+                      float *lse, float *entropy, int32_t *top_ids, float *top_logprobs, void *stream);
+
+/*
+ * muse_lmhead_forward followed by muse_lmhead_score of its logits, on `stream`:
+ * arguments as for the two (no argmax: it is top_ids[.][0]).  logits
+ * [batch][n_rows] f32 is written as by the forward; tokens [batch].
+ */
+int muse_lmhead_forward_score(muse_lmhead *h, const float *hidden, int batch, const float *gamma, float eps,
+                              const void *weights, float scale, float cap, float *logits, const int32_t *tokens,
+                              float temperature, int n_top, float *logprob, int32_t *rank, float *lse,
+                              float *entropy, int32_t *top_ids, float *top_logprobs, void *stream);
+
+/*
+ * Distillation from a teacher's top alternatives: per row the loss
+ * KL(teacher || student) over those alternatives and its gradient by the
+ * student's logits.  With z = x / temperature, q = softmax(z) over the row's
+ * n_rows values and the teacher's entries (id_j, l_j), j < n_top:
+ *   tail 0  p_j = exp(l_j) / sum exp(l): the teacher renormalised over its
+ *           entries (any shift of l gives the same: teacher logits divided by
+ *           its temperature serve as well)
+ *   tail 1  p_j = exp(l_j), and one more class for all other tokens with
+ *           p_t = max(0, 1 - sum p) and q_t = sum of q outside the ids
+ *   loss    = row_weight * ( sum_j p_j (log p_j - log q[id_j]) + p_t (log p_t - log q_t) )
+ *   grad_i  = row_weight / temperature * ( (sum p + p_t) q_i - sum_{j: id_j = i} p_j
+ *                                          - (i outside the ids ? p_t q_i / q_t : 0) )
+ * Sums are held in f32; the gradient is rounded once to the logits' dtype.
+ *   logits  device rows as for muse_lmhead_score.
+ *   teacher_ids, teacher_logprobs  [n][n_top] int32 and f32, device, n_top
+ *           1 .. MUSE_MAX_TOP, such as muse_lmhead_score returns.  An entry
+ *           with an id outside 0..n_rows-1 is left out; one with l = -infinity
+ *           has p = 0; an id given twice counts as two entries of one token.
+ *   row_weight  [n] f32, device, or NULL for 1.  It scales loss and gradient
+ *           (the caller's factors of temperature and of averaging, or the
+ *           upstream gradient of a row); a row of weight 0 gives 0 for both
+ *           whatever it holds.
+ *   loss    [n] f32, device, or NULL.  grad: device rows in the logits' dtype,
+ *           grad_ld >= n_rows elements apart, or NULL for the loss alone; it
+ *           may be the logits themselves (with grad_ld = ld).  One of the two
+ *           is needed.  Elements between n_rows and grad_ld are left alone.
+ * A row with no teacher entry left has loss and gradient 0, and so has a row
+ * whose logits are all -infinity.  Where the teacher expects a masked logit
+ * the loss is +infinity and the gradient finite.  A NaN or +infinity in a row
+ * gives NaN.  Uses no workspace of the handle: calls may overlap.  One launch.
+ */
+int muse_lmhead_distill(muse_lmhead *h, const void *logits, int dtype, int64_t n, int64_t ld,
+                        const int32_t *teacher_ids, const float *teacher_logprobs, int n_top, int tail,
+                        const float *row_weight, float temperature, float *loss, void *grad, int64_t grad_ld,
+                        void *stream);
+
+/*
+ * Backward pass of muse_lmhead_forward: from the gradient by its logits to
+ * the gradients by its hidden rows and gamma (the weights are frozen):
+ *     t[b][v]  = grad_logits[b][v] * scale * (cap > 0 ? (cap - l)(cap + l) / cap^2 : 1),  l = logits[b][v]
+ *     gx[b][j] = sum_v t[b][v] W[v][j]
+ *     gamma given: r = 1/sqrt(mean h^2 + eps), u = gx * gamma:
+ *         grad_hidden = r (u - h r^2 mean(u h)),  grad_gamma[j] = sum_b gx[b][j] h[b][j] r_b
+ *     gamma NULL:  grad_hidden = gx
+ *   grad_logits [batch][n_rows] f32; logits [batch][n_rows] f32, what the
+ *   forward returned, needed when cap > 0 (else unused, may be NULL).
+ *   hidden [batch][k] and gamma as in the forward; hidden is needed with gamma.
+ *   grad_hidden [batch][k] f32, written; grad_gamma [k] f32, written, or NULL
+ *   (needs gamma).  All 16-byte aligned, device, dense, batch 1..max_batch.
+ *   grad_hidden must not overlap the inputs.
+ * The sums run in a fixed order: the same inputs give the same bits.  Uses the
+ * handle's workspace: like forwards, two calls that may run at the same time
+ * on the GPU must use two handles.
+ */
+int muse_lmhead_backward(muse_lmhead *h, const float *grad_logits, const float *logits, const float *hidden,
+                         int batch, const float *gamma, float eps, const void *weights, float scale, float cap,
+                         float *grad_hidden, float *grad_gamma, void *stream);
+
 /* Argmax keys (muse_lmhead_set_argmax_key). */
 #define MUSE_ARGMAX_CAPPED 0   /* the returned logit, after scale and cap (the default) */
 #define MUSE_ARGMAX_PRECAP 1   /* scale * raw, before the cap */

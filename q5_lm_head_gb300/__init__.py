@@ -13,9 +13,10 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import Any, NamedTuple
 
 __all__ = [
-    "LMHead", "MuseError", "library_path", "load_library",
+    "LMHead", "TokenScores", "MuseError", "library_path", "load_library",
     "muse_lmhead_init", "muse_lmhead_forward", "muse_lmhead_forward_host",
     "muse_lmhead_launches_per_forward", "muse_lmhead_path_name", "muse_lmhead_device_status",
     "muse_lmhead_destroy", "muse_lmhead_status_string", "muse_lmhead_forward_b1_noalloc",
@@ -25,6 +26,7 @@ __all__ = [
     "muse_lmhead_init_format", "MUSE_FORMAT_Q5_K", "MUSE_FORMAT_Q4_K", "BLOCK_BYTES",
     "muse_lmhead_clear_device_status", "muse_lmhead_selftest_wait_timeout",
     "muse_lmhead_set_argmax_key", "MUSE_ARGMAX_CAPPED", "MUSE_ARGMAX_PRECAP",
+    "muse_lmhead_score", "muse_lmhead_forward_score", "muse_lmhead_distill", "muse_lmhead_backward", "MUSE_MAX_TOP",
     "EXPORTED_SYMBOLS",
     "LOGIT_SCALE", "SOFTCAP", "RMS_EPS",
 ]
@@ -47,6 +49,7 @@ EXPORTED_SYMBOLS = (
     "muse_lmhead_forward_group", "muse_lmhead_forward_group_host", "muse_lmhead_forward_logprobs",
     "muse_lmhead_init_format",
     "muse_lmhead_clear_device_status", "muse_lmhead_selftest_wait_timeout", "muse_lmhead_set_argmax_key",
+    "muse_lmhead_score", "muse_lmhead_forward_score", "muse_lmhead_distill", "muse_lmhead_backward",
 )
 
 MUSE_OK = 0
@@ -59,6 +62,8 @@ BLOCK_BYTES = {"q5_k": 176, "q4_k": 144}
 STATUS_WAIT_TIMEOUT = 1
 MUSE_ARGMAX_CAPPED = 0      # argmax key: the returned (capped) logit
 MUSE_ARGMAX_PRECAP = 1      # argmax key: scale * raw, before the cap
+MUSE_MAX_TOP = 64           # alternatives of a row that are returned (score) or given (distill), at most
+MUSE_DTYPE_F32, MUSE_DTYPE_F16, MUSE_DTYPE_BF16 = 0, 1, 2
 ARGMAX_KEYS = {"capped": MUSE_ARGMAX_CAPPED, "precap": MUSE_ARGMAX_PRECAP}
 
 _lib = None
@@ -125,6 +130,15 @@ def load_library():
     lib.muse_lmhead_forward_group.argtypes = [vp, vp, vp, f32, ctypes.POINTER(MuseGemvSegment), i32, vp]
     lib.muse_lmhead_forward_group_host.restype = i32
     lib.muse_lmhead_forward_group_host.argtypes = [vp, vp, vp, f32, ctypes.POINTER(MuseGemvSegment), i32, vp]
+    lib.muse_lmhead_score.restype = i32
+    lib.muse_lmhead_score.argtypes = [vp, vp, i32, i64, i64, vp, f32, i32, vp, vp, vp, vp, vp, vp, vp]
+    lib.muse_lmhead_forward_score.restype = i32
+    lib.muse_lmhead_forward_score.argtypes = [vp, vp, i32, vp, f32, vp, f32, f32, vp, vp, f32, i32, vp, vp, vp, vp,
+                                              vp, vp, vp]
+    lib.muse_lmhead_distill.restype = i32
+    lib.muse_lmhead_distill.argtypes = [vp, vp, i32, i64, i64, vp, vp, i32, i32, vp, f32, vp, vp, i64, vp]
+    lib.muse_lmhead_backward.restype = i32
+    lib.muse_lmhead_backward.argtypes = [vp, vp, vp, vp, i32, vp, f32, vp, f32, f32, vp, vp, vp]
     _lib = lib
     return lib
 
@@ -241,6 +255,47 @@ def muse_lmhead_forward_group_host(h: int | None, hidden_host: int, gamma: int |
     for i, (w, n, o, sc, cp) in enumerate(segments):
         arr[i] = MuseGemvSegment(w, n, o, sc, cp)
     return load_library().muse_lmhead_forward_group_host(h, hidden_host, gamma, eps, arr, len(segments), stream)
+
+
+def muse_lmhead_score(h: int | None, logits: int, dtype: int, n: int, ld: int, tokens: int | None,
+                      temperature: float, n_top: int, logprob: int | None, rank: int | None, lse: int | None,
+                      entropy: int | None, top_ids: int | None, top_logprobs: int | None, stream: int | None) -> int:
+    return load_library().muse_lmhead_score(h, logits, dtype, n, ld, tokens, temperature, n_top, logprob, rank, lse,
+                                            entropy, top_ids, top_logprobs, stream)
+
+
+def muse_lmhead_forward_score(h: int | None, hidden: int, batch: int, gamma: int | None, eps: float, weights: int,
+                              scale: float, cap: float, logits: int, tokens: int | None, temperature: float,
+                              n_top: int, logprob: int | None, rank: int | None, lse: int | None,
+                              entropy: int | None, top_ids: int | None, top_logprobs: int | None,
+                              stream: int | None) -> int:
+    return load_library().muse_lmhead_forward_score(h, hidden, batch, gamma, eps, weights, scale, cap, logits, tokens,
+                                                    temperature, n_top, logprob, rank, lse, entropy, top_ids,
+                                                    top_logprobs, stream)
+
+
+def muse_lmhead_distill(h: int | None, logits: int, dtype: int, n: int, ld: int, teacher_ids: int,
+                        teacher_logprobs: int, n_top: int, tail: int, row_weight: int | None, temperature: float,
+                        loss: int | None, grad: int | None, grad_ld: int, stream: int | None) -> int:
+    return load_library().muse_lmhead_distill(h, logits, dtype, n, ld, teacher_ids, teacher_logprobs, n_top, tail,
+                                              row_weight, temperature, loss, grad, grad_ld, stream)
+
+
+def muse_lmhead_backward(h: int | None, grad_logits: int, logits: int | None, hidden: int | None, batch: int,
+                         gamma: int | None, eps: float, weights: int, scale: float, cap: float, grad_hidden: int,
+                         grad_gamma: int | None, stream: int | None) -> int:
+    return load_library().muse_lmhead_backward(h, grad_logits, logits, hidden, batch, gamma, eps, weights, scale, cap,
+                                               grad_hidden, grad_gamma, stream)
+
+
+class TokenScores(NamedTuple):
+    """What LMHead.score returns, one entry a row (None for what was not asked for)."""
+    logprob: Any        # [n] f32, the given token's (0 in a padded row)
+    rank: Any           # [n] int32, how many tokens come before it (-1 in a padded row)
+    lse: Any            # [n] f32, the normaliser at the given temperature
+    entropy: Any        # [n] f32, natural log
+    top_ids: Any        # [n, n_top] int32
+    top_logprobs: Any   # [n, n_top] f32
 
 
 class LMHead:
@@ -415,6 +470,146 @@ class LMHead:
         if st != MUSE_OK:
             raise MuseError(st, "muse_lmhead_forward_group_host")
         return outs
+
+    def _rows(self, t, name):
+        """(pointer, MUSE_DTYPE, rows, distance) of a matrix of logits whose rows are contiguous."""
+        import torch
+        dtype = {torch.float32: MUSE_DTYPE_F32, torch.float16: MUSE_DTYPE_F16,
+                 torch.bfloat16: MUSE_DTYPE_BF16}.get(t.dtype)
+        if dtype is None or t.device.type != "cuda" or t.device.index != self.device:
+            raise ValueError(f"{name}: need a float32, float16 or bfloat16 tensor on cuda:{self.device}")
+        n = t.shape[0] if t.dim() == 2 else -1
+        if n < 0 or t.shape[1] != self.n_rows:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, need [n, {self.n_rows}]")
+        if (self.n_rows > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < self.n_rows):
+            raise ValueError(f"{name}: strides {tuple(t.stride())}, need contiguous rows that do not overlap")
+        return t.data_ptr(), dtype, n, t.stride(0) if n > 1 else self.n_rows
+
+    def _score_outputs(self, n, tokens, n_top, device):
+        import torch
+        if not 0 <= n_top <= MUSE_MAX_TOP:
+            raise ValueError(f"n_top: 0..{MUSE_MAX_TOP}")
+        if tokens is not None:
+            self._check(tokens, "tokens", torch.int32, (n,))
+        f, i = torch.float32, torch.int32
+        none = lambda want, *a, **k: torch.empty(*a, device=device, **k) if want else None  # noqa: E731
+        return TokenScores(none(tokens is not None, (n,), dtype=f), none(tokens is not None, (n,), dtype=i),
+                           torch.empty((n,), dtype=f, device=device), torch.empty((n,), dtype=f, device=device),
+                           none(n_top > 0, (n, n_top), dtype=i), none(n_top > 0, (n, n_top), dtype=f))
+
+    def score(self, logits, tokens=None, n_top: int = 0, temperature: float = 1.0, stream=None) -> TokenScores:
+        """Log probability and rank of tokens [n] int32, normaliser, entropy and top alternatives of each row.
+
+        logits [n, n_rows], f32, f16 or bf16, contiguous rows any distance
+        apart, any n: what a forward returned (softmax and logprobs are taken
+        over the capped logits).  Masked logits are -infinity; a token outside
+        0..n_rows-1 marks a padded row.  See muse_lmhead_score in the C header."""
+        import torch
+        if logits.dim() == 1:
+            logits = logits.unsqueeze(0)
+        ptr, dtype, n, ld = self._rows(logits, "logits")
+        out = self._score_outputs(n, tokens, n_top, logits.device)
+        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        at = [None if t is None else t.data_ptr() for t in (tokens, *out)]
+        st = muse_lmhead_score(self.handle, ptr, dtype, n, ld, at[0], float(temperature), n_top, *at[1:],
+                               s.cuda_stream)
+        if st != MUSE_OK:
+            raise MuseError(st, "muse_lmhead_score")
+        return out
+
+    def forward_score(self, hidden, weights, gamma=None, eps: float = RMS_EPS, scale: float = LOGIT_SCALE,
+                      cap: float = SOFTCAP, tokens=None, n_top: int = 0, temperature: float = 1.0, logits=None,
+                      stream=None):
+        """(logits [B, n_rows], TokenScores): the forward, and the scores of its logits."""
+        import torch
+        if hidden.dim() == 1:
+            hidden = hidden.unsqueeze(0)
+        b = hidden.shape[0]
+        hp = self._check(hidden, "hidden", torch.float32, (b, self.k))
+        wp = self._check(weights, "weights", torch.uint8)
+        if weights.numel() != self.n_rows * (self.k // 256) * self.block_bytes:
+            raise ValueError("weights: wrong number of bytes for this handle")
+        gp = None if gamma is None else self._check(gamma, "gamma", torch.float32, (self.k,))
+        if logits is None:
+            logits = torch.empty((b, self.n_rows), dtype=torch.float32, device=hidden.device)
+        lp = self._check(logits, "logits", torch.float32, (b, self.n_rows))
+        out = self._score_outputs(b, tokens, n_top, hidden.device)
+        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        at = [None if t is None else t.data_ptr() for t in (tokens, *out)]
+        st = muse_lmhead_forward_score(self.handle, hp, b, gp, float(eps), wp, float(scale), float(cap), lp, at[0],
+                                       float(temperature), n_top, *at[1:], s.cuda_stream)
+        if st != MUSE_OK:
+            raise MuseError(st, "muse_lmhead_forward_score")
+        return logits, out
+
+    def distill(self, logits, teacher_ids, teacher_logprobs, row_weight=None, temperature: float = 1.0,
+                tail: bool = False, want_grad: bool = True, grad=None, stream=None):
+        """(loss [n] f32, grad [n, n_rows] or None): distillation from a teacher's top alternatives.
+
+        logits [n, n_rows] as for score; teacher_ids [n, n_top] int32 and
+        teacher_logprobs [n, n_top] f32, such as score returns.  tail: the
+        tokens outside teacher_ids are one more class (else the teacher is
+        renormalised over its entries).  row_weight [n] f32 scales loss and
+        gradient.  grad (the logits' dtype; may be the logits themselves) is
+        made when not given, unless want_grad is false.  See
+        muse_lmhead_distill in the C header."""
+        import torch
+        ptr, dtype, n, ld = self._rows(logits, "logits")
+        top = teacher_ids.shape[1] if teacher_ids.dim() == 2 else 0
+        if not 1 <= top <= MUSE_MAX_TOP:
+            raise ValueError(f"teacher_ids: need [n, 1..{MUSE_MAX_TOP}]")
+        ip = self._check(teacher_ids, "teacher_ids", torch.int32, (n, top))
+        pp = self._check(teacher_logprobs, "teacher_logprobs", torch.float32, (n, top))
+        wp = None if row_weight is None else self._check(row_weight, "row_weight", torch.float32, (n,))
+        loss = torch.empty((n,), dtype=torch.float32, device=logits.device)
+        gp, gld = None, 0
+        if grad is None and want_grad:
+            grad = torch.empty((n, self.n_rows), dtype=logits.dtype, device=logits.device)
+        if grad is not None:
+            gp, gtype, gn, gld = self._rows(grad, "grad")
+            if gtype != dtype or gn != n:
+                raise ValueError("grad: need the logits' shape and dtype")
+        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        st = muse_lmhead_distill(self.handle, ptr, dtype, n, ld, ip, pp, top, int(bool(tail)), wp, float(temperature),
+                                 loss.data_ptr(), gp, gld, s.cuda_stream)
+        if st != MUSE_OK:
+            raise MuseError(st, "muse_lmhead_distill")
+        return loss, grad
+
+    def backward(self, grad_logits, weights, logits=None, hidden=None, gamma=None, eps: float = RMS_EPS,
+                 scale: float = LOGIT_SCALE, cap: float = SOFTCAP, grad_hidden=None, stream=None):
+        """(grad_hidden [B, k], grad_gamma [k] or None) from grad_logits [B, n_rows] f32.
+
+        weights, gamma, eps, scale and cap as in the forward; logits (what it
+        returned) is needed with a cap, hidden with gamma.  See
+        muse_lmhead_backward in the C header."""
+        import torch
+        if grad_logits.dim() == 1:
+            grad_logits = grad_logits.unsqueeze(0)
+        b = grad_logits.shape[0]
+        tp = self._check(grad_logits, "grad_logits", torch.float32, (b, self.n_rows))
+        wp = self._check(weights, "weights", torch.uint8)
+        if weights.numel() != self.n_rows * (self.k // 256) * self.block_bytes:
+            raise ValueError("weights: wrong number of bytes for this handle")
+        lp = hp = gp = ap = grad_gamma = None
+        if logits is not None:
+            lp = self._check(logits, "logits", torch.float32, (b, self.n_rows))
+        if gamma is not None:
+            if hidden is None:
+                raise ValueError("hidden: needed with gamma")
+            hp = self._check(hidden, "hidden", torch.float32, (b, self.k))
+            gp = self._check(gamma, "gamma", torch.float32, (self.k,))
+            grad_gamma = torch.empty((self.k,), dtype=torch.float32, device=grad_logits.device)
+            ap = grad_gamma.data_ptr()
+        if grad_hidden is None:
+            grad_hidden = torch.empty((b, self.k), dtype=torch.float32, device=grad_logits.device)
+        op = self._check(grad_hidden, "grad_hidden", torch.float32, (b, self.k))
+        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        st = muse_lmhead_backward(self.handle, tp, lp, hp, b, gp, float(eps), wp, float(scale), float(cap), op, ap,
+                                  s.cuda_stream)
+        if st != MUSE_OK:
+            raise MuseError(st, "muse_lmhead_backward")
+        return grad_hidden, grad_gamma
 
     def set_argmax_key(self, key: str) -> None:
         """"capped" (the returned logit; the default) or "precap" (scale * raw, before the cap)."""

@@ -23,6 +23,8 @@ struct Workspace {
   unsigned int *split_cnt;   // [num_sms][8] arrivals per shared tile and warp (per CTA boundary, or per tile when tiles < SMs), zero between forwards
   float *b1_part;            // split-K batch-1 path: [chunks][n_rows] chunk partial sums
   unsigned int *b1_cnt;      // split-K batch-1 path: [12-row tiles] chunk arrivals, zero between forwards
+  float *bwd_part;           // backward: partial sums of the gradient by the normed input
+  float *bwd_rms;            // backward: [MUSE_MAX_BATCH] RMS factors
 };
 
 constexpr int kMaxLseParts = 256;
@@ -96,5 +98,68 @@ size_t tc_split_floats(int num_sms, int max_batch);  // split_part size
 size_t tc_split_counters(int num_sms);                // split_cnt size
 cudaError_t tc_encode_weights(CUtensorMap *map, const void *weights, int64_t n_rows, int k, bool q4);
 cudaError_t launch_tc(const LaunchArgs &a, const CUtensorMap &map);
+
+// Scores of rows of logits [n][ld] (v of them used), dtype 0/1/2 = f32/f16/bf16.
+// Outputs may be null, apart from top_ids and top_logprobs when n_top > 0.
+constexpr int kMaxTop = 64;
+struct ScoreArgs {
+  const void *logits;
+  int dtype;
+  int64_t n, ld, v;
+  const int32_t *tokens;   // [n] or nullptr
+  float temperature;
+  int n_top;
+  float *logprob;          // [n]
+  int32_t *rank;           // [n]
+  float *lse, *entropy;    // [n]
+  int32_t *top_ids;        // [n][n_top]
+  float *top_logprobs;     // [n][n_top]
+  int num_sms;
+  cudaStream_t stream;
+};
+cudaError_t launch_score(const ScoreArgs &a);
+
+// Distillation loss and gradient over rows of logits as above.
+struct DistillArgs {
+  const void *logits;
+  int dtype;
+  int64_t n, ld, v;
+  const int32_t *teacher_ids;      // [n][n_top]
+  const float *teacher_logprobs;   // [n][n_top]
+  int n_top;
+  bool tail;
+  const float *row_weight;         // [n] or nullptr
+  float temperature;
+  float *loss;                     // [n] or nullptr
+  void *grad;                      // [n][grad_ld] or nullptr, the logits' dtype
+  int64_t grad_ld;
+  int num_sms;
+  cudaStream_t stream;
+};
+cudaError_t launch_distill(const DistillArgs &a);
+
+// Gradient by the logits back through cap, scale, matrix and final norm.
+struct BackwardArgs {
+  const float *grad_logits;   // [batch][n_rows]
+  const float *logits;        // [batch][n_rows], only when cap > 0
+  const float *hidden;        // [batch][k], only with gamma
+  const float *gamma;         // [k] or nullptr
+  float eps;
+  const uint8_t *w;
+  bool q4;
+  float scale, cap;
+  float *grad_hidden;         // [batch][k]
+  float *grad_gamma;          // [k] or nullptr
+  int batch;
+  int64_t n_rows;
+  int k;
+  int num_sms;
+  float *part;                // workspace of backward_part_floats
+  float *rms;                 // workspace [batch]
+  uint32_t *status;
+  cudaStream_t stream;
+};
+size_t backward_part_floats(int max_batch, int k);
+cudaError_t launch_backward(const BackwardArgs &a);
 
 }  // namespace muse

@@ -172,7 +172,7 @@ int muse_lmhead_init_format(muse_lmhead **out, int device, int64_t n_rows, int64
 
   // One zeroed allocation: keys | ticket | status | logprob pairs | x | activation packages |
   // shared-tile counters | shared-tile partial sums (those three for the tensor-core path) |
-  // chunk counters | chunk partial sums (the split-K batch-1 path)
+  // chunk counters | chunk partial sums (the split-K batch-1 path) | backward partial sums | RMS factors
   const size_t keys_b = sizeof(unsigned long long) * MUSE_MAX_BATCH;
   const size_t misc_b = 256;
   const size_t lse_b = sizeof(float2) * static_cast<size_t>(max_batch) * muse::kMaxLseParts;
@@ -187,7 +187,10 @@ int muse_lmhead_init_format(muse_lmhead **out, int device, int64_t n_rows, int64
   const size_t part_b = tc ? sizeof(float) * muse::tc_split_floats(h->num_sms, max_batch) : 0;
   const size_t bcnt_b = split ? (sizeof(unsigned int) * muse::b1_split_counters(n_rows) + 255) / 256 * 256 : 0;
   const size_t bpart_b = split ? sizeof(float) * muse::b1_split_floats(n_rows, static_cast<int>(k)) : 0;
-  const size_t total = keys_b + misc_b + lse_b + x_b + pkg_b + cnt_b + part_b + bcnt_b + bpart_b;
+  const size_t wpart_b = (sizeof(float) * muse::backward_part_floats(max_batch, static_cast<int>(k)) + 255) / 256 * 256;
+  const size_t wrms_b = sizeof(float) * MUSE_MAX_BATCH;
+  const size_t fwd_b = (keys_b + misc_b + lse_b + x_b + pkg_b + cnt_b + part_b + bcnt_b + bpart_b + 255) / 256 * 256;
+  const size_t total = fwd_b + wpart_b + wrms_b;
   void *base = nullptr;
   e = cudaMalloc(&base, total);
   if (e != cudaSuccess) {
@@ -216,6 +219,8 @@ int muse_lmhead_init_format(muse_lmhead **out, int device, int64_t n_rows, int64
   h->ws.b1_cnt = bcnt_b ? reinterpret_cast<unsigned int *>(pb) : nullptr;
   h->ws.b1_part = bpart_b ? reinterpret_cast<float *>(pb + bcnt_b) : nullptr;
   h->ws_b1_cnt_bytes = bcnt_b;
+  h->ws.bwd_part = reinterpret_cast<float *>(p + fwd_b);
+  h->ws.bwd_rms = reinterpret_cast<float *>(p + fwd_b + wpart_b);
   *out = h;
   return MUSE_OK;
 }
@@ -441,6 +446,166 @@ int muse_lmhead_forward_group_host(muse_lmhead *h, const float *hidden_host, con
   return MUSE_OK;
 }
 
+namespace {
+
+// Rows of logits that a call reads (or writes): n rows of h->n_rows values, ld apart.
+int validate_rows(const muse_lmhead *h, const void *p, int dtype, int64_t n, int64_t ld) {
+  if (dtype != MUSE_DTYPE_F32 && dtype != MUSE_DTYPE_F16 && dtype != MUSE_DTYPE_BF16) return MUSE_ERR_VALUE;
+  if (ld < h->n_rows || ld > (int64_t{1} << 60) / (n > 0 ? n : 1)) return MUSE_ERR_SHAPE;
+  return aligned(p, dtype == MUSE_DTYPE_F32 ? 4 : 2) ? MUSE_OK : MUSE_ERR_ALIGN;
+}
+
+int validate_score(const muse_lmhead *h, int64_t n, const int32_t *tokens, float temperature, int n_top,
+                   const float *logprob, const int32_t *rank, const float *lse, const float *entropy,
+                   const int32_t *top_ids, const float *top_logprobs) {
+  if (!h) return MUSE_ERR_NULL;
+  if (n < 0 || n > (int64_t{1} << 31) - 1 || n_top < 0 || n_top > MUSE_MAX_TOP) return MUSE_ERR_SHAPE;
+  if (!std::isfinite(temperature) || !(temperature > 0.0f)) return MUSE_ERR_VALUE;
+  if (n == 0) return MUSE_OK;                          // nothing is read or written
+  if ((logprob || rank) && !tokens) return MUSE_ERR_NULL;
+  if (n_top > 0 && (!top_ids || !top_logprobs)) return MUSE_ERR_NULL;
+  if (!logprob && !rank && !lse && !entropy && n_top == 0) return MUSE_ERR_NULL;
+  const void *ps[] = {tokens, logprob, rank, lse, entropy, top_ids, top_logprobs};
+  for (const void *p : ps)
+    if (!aligned(p, 4)) return MUSE_ERR_ALIGN;
+  return MUSE_OK;
+}
+
+int run_score(const muse_lmhead *h, const void *logits, int dtype, int64_t n, int64_t ld, const int32_t *tokens,
+              float temperature, int n_top, float *logprob, int32_t *rank, float *lse, float *entropy,
+              int32_t *top_ids, float *top_logprobs, cudaStream_t stream) {
+  muse::ScoreArgs a;
+  a.logits = logits;
+  a.dtype = dtype;
+  a.n = n;
+  a.ld = ld;
+  a.v = h->n_rows;
+  a.tokens = tokens;
+  a.temperature = temperature;
+  a.n_top = n_top;
+  a.logprob = logprob;
+  a.rank = rank;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.num_sms = h->num_sms;
+  a.stream = stream;
+  const cudaError_t e = muse::launch_score(a);
+  return e == cudaSuccess ? MUSE_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+int muse_lmhead_score(muse_lmhead *h, const void *logits, int dtype, int64_t n, int64_t ld, const int32_t *tokens,
+                      float temperature, int n_top, float *logprob, int32_t *rank, float *lse, float *entropy,
+                      int32_t *top_ids, float *top_logprobs, void *stream) {
+  int st = validate_score(h, n, tokens, temperature, n_top, logprob, rank, lse, entropy, top_ids, top_logprobs);
+  if (st != MUSE_OK) return st;
+  if (!logits && n > 0) return MUSE_ERR_NULL;
+  if ((st = validate_rows(h, logits, dtype, n, ld)) != MUSE_OK) return st;
+  if (n == 0) return MUSE_OK;
+  DeviceGuard g(h->device);
+  if (!g.ok) return MUSE_ERR_DEVICE;
+  return run_score(h, logits, dtype, n, ld, tokens, temperature, n_top, logprob, rank, lse, entropy, top_ids,
+                   top_logprobs, static_cast<cudaStream_t>(stream));
+}
+
+int muse_lmhead_forward_score(muse_lmhead *h, const float *hidden, int batch, const float *gamma, float eps,
+                              const void *weights, float scale, float cap, float *logits, const int32_t *tokens,
+                              float temperature, int n_top, float *logprob, int32_t *rank, float *lse,
+                              float *entropy, int32_t *top_ids, float *top_logprobs, void *stream) {
+  int st = validate_forward(h, hidden, batch, gamma, eps, weights, scale, cap, logits, nullptr);
+  if (st != MUSE_OK) return st;
+  st = validate_score(h, batch, tokens, temperature, n_top, logprob, rank, lse, entropy, top_ids, top_logprobs);
+  if (st != MUSE_OK) return st;
+  if (!aligned(hidden, 16) || !aligned(logits, 16)) return MUSE_ERR_ALIGN;
+  DeviceGuard g(h->device);
+  if (!g.ok) return MUSE_ERR_DEVICE;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = run_forward(h, hidden, batch, gamma, eps, weights, scale, cap, logits, nullptr, s);
+  if (st != MUSE_OK) return st;
+  return run_score(h, logits, MUSE_DTYPE_F32, batch, h->n_rows, tokens, temperature, n_top, logprob, rank, lse,
+                   entropy, top_ids, top_logprobs, s);
+}
+
+int muse_lmhead_distill(muse_lmhead *h, const void *logits, int dtype, int64_t n, int64_t ld,
+                        const int32_t *teacher_ids, const float *teacher_logprobs, int n_top, int tail,
+                        const float *row_weight, float temperature, float *loss, void *grad, int64_t grad_ld,
+                        void *stream) {
+  if (!h) return MUSE_ERR_NULL;
+  if (n < 0 || n > (int64_t{1} << 31) - 1 || n_top < 1 || n_top > MUSE_MAX_TOP) return MUSE_ERR_SHAPE;
+  if (!std::isfinite(temperature) || !(temperature > 0.0f)) return MUSE_ERR_VALUE;
+  if (tail != 0 && tail != 1) return MUSE_ERR_VALUE;
+  if (n > 0 && (!logits || !teacher_ids || !teacher_logprobs || (!loss && !grad))) return MUSE_ERR_NULL;
+  int st = validate_rows(h, logits, dtype, n, ld);
+  if (st == MUSE_OK && grad) st = validate_rows(h, grad, dtype, n, grad_ld);
+  if (st != MUSE_OK) return st;
+  if (grad == logits && grad && grad_ld != ld) return MUSE_ERR_SHAPE;
+  if (!aligned(teacher_ids, 4) || !aligned(teacher_logprobs, 4) || !aligned(row_weight, 4) || !aligned(loss, 4))
+    return MUSE_ERR_ALIGN;
+  if (n == 0) return MUSE_OK;
+  DeviceGuard g(h->device);
+  if (!g.ok) return MUSE_ERR_DEVICE;
+  muse::DistillArgs a;
+  a.logits = logits;
+  a.dtype = dtype;
+  a.n = n;
+  a.ld = ld;
+  a.v = h->n_rows;
+  a.teacher_ids = teacher_ids;
+  a.teacher_logprobs = teacher_logprobs;
+  a.n_top = n_top;
+  a.tail = tail != 0;
+  a.row_weight = row_weight;
+  a.temperature = temperature;
+  a.loss = loss;
+  a.grad = grad;
+  a.grad_ld = grad_ld;
+  a.num_sms = h->num_sms;
+  a.stream = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = muse::launch_distill(a);
+  return e == cudaSuccess ? MUSE_OK : cuda_fail(e);
+}
+
+int muse_lmhead_backward(muse_lmhead *h, const float *grad_logits, const float *logits, const float *hidden, int batch,
+                         const float *gamma, float eps, const void *weights, float scale, float cap,
+                         float *grad_hidden, float *grad_gamma, void *stream) {
+  if (cap > 0.0f && !logits) return MUSE_ERR_NULL;
+  if (gamma && !hidden) return MUSE_ERR_NULL;
+  if (grad_gamma && !gamma) return MUSE_ERR_NULL;
+  if (!grad_hidden) return MUSE_ERR_NULL;
+  const int st = validate_forward(h, grad_logits, batch, gamma, eps, weights, scale, cap, grad_hidden, nullptr);
+  if (st != MUSE_OK) return st;
+  if (!aligned(grad_logits, 16) || !aligned(logits, 16) || !aligned(hidden, 16) || !aligned(grad_hidden, 16) ||
+      !aligned(grad_gamma, 16))
+    return MUSE_ERR_ALIGN;
+  DeviceGuard g(h->device);
+  if (!g.ok) return MUSE_ERR_DEVICE;
+  muse::BackwardArgs a;
+  a.grad_logits = grad_logits;
+  a.logits = logits;
+  a.hidden = hidden;
+  a.gamma = gamma;
+  a.eps = eps;
+  a.w = static_cast<const uint8_t *>(weights);
+  a.q4 = h->format == MUSE_FORMAT_Q4_K;
+  a.scale = scale;
+  a.cap = cap;
+  a.grad_hidden = grad_hidden;
+  a.grad_gamma = grad_gamma;
+  a.batch = batch;
+  a.n_rows = h->n_rows;
+  a.k = static_cast<int>(h->k);
+  a.num_sms = h->num_sms;
+  a.part = h->ws.bwd_part;
+  a.rms = h->ws.bwd_rms;
+  a.status = h->ws.status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = muse::launch_backward(a);
+  return e == cudaSuccess ? MUSE_OK : cuda_fail(e);
+}
+
 int muse_lmhead_set_argmax_key(muse_lmhead *h, int key) {
   if (!h) return MUSE_ERR_NULL;
   if (key != MUSE_ARGMAX_CAPPED && key != MUSE_ARGMAX_PRECAP) return MUSE_ERR_VALUE;
@@ -513,10 +678,10 @@ const char *muse_lmhead_status_string(int status) {
   switch (status) {
     case MUSE_OK: return "ok";
     case MUSE_ERR_NULL: return "a required pointer is NULL";
-    case MUSE_ERR_SHAPE: return "bad shape: need n_rows >= 1 and k a positive multiple of 256";
+    case MUSE_ERR_SHAPE: return "bad shape: need n_rows >= 1, k a positive multiple of 256, a row count and row distance that fit, n_top at most 64";
     case MUSE_ERR_BATCH: return "batch outside 1..max_batch (max_batch at most 32)";
-    case MUSE_ERR_ALIGN: return "misaligned pointer: 16 bytes for hidden/gamma/weights/logits, 4 for argmax";
-    case MUSE_ERR_VALUE: return "non-finite scale or cap, or bad eps";
+    case MUSE_ERR_ALIGN: return "misaligned pointer: 16 bytes for hidden/gamma/weights/logits, 4 for argmax, the element size for scored rows";
+    case MUSE_ERR_VALUE: return "non-finite scale or cap, bad eps or temperature, or an unknown format, type or mode";
     case MUSE_ERR_DEVICE: return "bad device index or not an sm_103 GPU";
     case MUSE_ERR_CUDA: return g_cuda_msg;
     case MUSE_ERR_NOMEM: return "out of memory";
