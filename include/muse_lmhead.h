@@ -320,7 +320,7 @@ int muse_lmhead_forward_group_host(muse_lmhead *h, const float *hidden_host, con
  *   n       0 .. 2^31-1 rows, not bound by max_batch; 0 does nothing.
  *   tokens  [n] int32, device; a value outside 0..n_rows-1 (a padded row) gives
  *           logprob 0 and rank -1.  NULL when logprob and rank are NULL.
- *   temperature  finite, > 0.
+ *   temperature  2^-20 .. 2^20.
  *   n_top   0 .. MUSE_MAX_TOP; top_ids and top_logprobs are [n][n_top] and
  *           needed when n_top > 0.  Entries beyond n_rows are -1 and -infinity.
  *   logprob [n] f32, rank [n] int32, lse [n] f32, entropy [n] f32: each may be
@@ -364,6 +364,7 @@ int muse_lmhead_forward_score(muse_lmhead *h, const float *hidden, int batch, co
  *           1 .. MUSE_MAX_TOP, such as muse_lmhead_score returns.  An entry
  *           with an id outside 0..n_rows-1 is left out; one with l = -infinity
  *           has p = 0; an id given twice counts as two entries of one token.
+ *   temperature  2^-20 .. 2^20.
  *   row_weight  [n] f32, device, or NULL for 1.  It scales loss and gradient
  *           (the caller's factors of temperature and of averaging, or the
  *           upstream gradient of a row); a row of weight 0 gives 0 for both

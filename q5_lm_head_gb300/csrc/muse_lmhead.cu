@@ -455,12 +455,15 @@ int validate_rows(const muse_lmhead *h, const void *p, int dtype, int64_t n, int
   return aligned(p, dtype == MUSE_DTYPE_F32 ? 4 : 2) ? MUSE_OK : MUSE_ERR_ALIGN;
 }
 
+// Far outside any use, and within the range where log2(e) / temperature and its products stay normal.
+bool temperature_ok(float t) { return t >= 0x1p-20f && t <= 0x1p20f; }
+
 int validate_score(const muse_lmhead *h, int64_t n, const int32_t *tokens, float temperature, int n_top,
                    const float *logprob, const int32_t *rank, const float *lse, const float *entropy,
                    const int32_t *top_ids, const float *top_logprobs) {
   if (!h) return MUSE_ERR_NULL;
   if (n < 0 || n > (int64_t{1} << 31) - 1 || n_top < 0 || n_top > MUSE_MAX_TOP) return MUSE_ERR_SHAPE;
-  if (!std::isfinite(temperature) || !(temperature > 0.0f)) return MUSE_ERR_VALUE;
+  if (!temperature_ok(temperature)) return MUSE_ERR_VALUE;
   if (n == 0) return MUSE_OK;                          // nothing is read or written
   if ((logprob || rank) && !tokens) return MUSE_ERR_NULL;
   if (n_top > 0 && (!top_ids || !top_logprobs)) return MUSE_ERR_NULL;
@@ -535,7 +538,7 @@ int muse_lmhead_distill(muse_lmhead *h, const void *logits, int dtype, int64_t n
                         void *stream) {
   if (!h) return MUSE_ERR_NULL;
   if (n < 0 || n > (int64_t{1} << 31) - 1 || n_top < 1 || n_top > MUSE_MAX_TOP) return MUSE_ERR_SHAPE;
-  if (!std::isfinite(temperature) || !(temperature > 0.0f)) return MUSE_ERR_VALUE;
+  if (!temperature_ok(temperature)) return MUSE_ERR_VALUE;
   if (tail != 0 && tail != 1) return MUSE_ERR_VALUE;
   if (n > 0 && (!logits || !teacher_ids || !teacher_logprobs || (!loss && !grad))) return MUSE_ERR_NULL;
   int st = validate_rows(h, logits, dtype, n, ld);
