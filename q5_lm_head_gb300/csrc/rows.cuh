@@ -76,6 +76,41 @@ __device__ __forceinline__ float exp2_approx(float v) {   // 2 ulp, 0 below the 
   return r;
 }
 
+// Two f32 values in one 64-bit register: one instruction works on both.
+__device__ __forceinline__ unsigned long long pack2(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// (x - m) c, c = log2(e) / temperature: the exponent of x against the row's
+// reference m.  One fma with the rounded product m c as the reference itself,
+// which every use of it shares; where that product could overflow (masks of the
+// type's lowest value), the difference first.
+constexpr float kPlain = 1e30f;
+__device__ __forceinline__ float exponent(float x, float m, float c) {
+  return fabsf(m) < kPlain ? fmaf(x, c, -__fmul_rn(m, c)) : (x - m) * c;
+}
+// The exponent by which sums against reference `from` move to reference `to`.
+__device__ __forceinline__ float shift_exponent(float from, float to, float c) {
+  return fabsf(from) < kPlain && fabsf(to) < kPlain ? __fadd_rn(__fmul_rn(from, c), -__fmul_rn(to, c)) : (from - to) * c;
+}
+
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -92,6 +127,9 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same in two halves.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // The address of p (this CTA's shared memory) in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
   uint32_t a;
@@ -100,20 +138,11 @@ __device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
                : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
   return a;
 }
-__device__ __forceinline__ unsigned long long peer_load64(uint32_t a) {
-  unsigned long long v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void peer_store64(uint32_t a, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
-__device__ __forceinline__ float peer_loadf(uint32_t a) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t peer_loadu(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void peer_store32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
 }  // namespace muse

@@ -1,29 +1,28 @@
 // Scores of finished logits: the log probability and rank of a given token,
 // the normaliser, the entropy and the top alternatives of each row.
 //
-// For a row x of V logits, z = x / temperature and m = max x:
-//     a_i = (x_i - m) log2(e) / temperature,  S = sum_i 2^a_i,  U = sum_i 2^a_i a_i
-//     lse = m / temperature + log S,  logprob(t) = (x_t - m) / temperature - log S,
-//     entropy = log S - ln 2 U / S
+// For a row x of V logits, c = log2(e) / temperature and m = max x:
+//     a_i = (x_i - m) c,  S = sum_i 2^a_i,  U = sum_i 2^a_i a_i
+//     lse = ln 2 (m c + log2 S),  logprob(t) = ln 2 (a_t - log2 S),  entropy = ln 2 (log2 S - U / S)
 // Ranks and alternatives order by (x descending, index ascending), on x itself:
 // a division could merge neighbouring values.
 //
-// Bound: HBM (each logit is read once) for many rows, latency for a few.  A
-// cluster of 1, 2, 4, 8 or 16 CTAs takes a row (as many as keep the GPU's CTA
-// slots filled once), each a contiguous share of its 16-byte vectors; its
-// threads hold a running maximum with S and U, and the CTAs' results meet in
-// the first one's hands through distributed shared memory.  No global
+// Bound: HBM (each logit is read once) and, close to it, instruction issue for
+// many rows; latency for a few.  A cluster of 1, 2, 4, 8 or 16 CTAs takes a row
+// (as many as keep the GPU's CTA slots filled once), each a contiguous share of
+// its 16-byte vectors; a thread holds a running maximum with S and U, and the
+// CTAs' results are pushed into the first one's shared memory.  No global
 // workspace, so calls may overlap.
 //
-// Alternatives: a thread's running maximum stands for one element of its own,
-// so the n_top-th largest of the 512 maxima is a value that at least n_top
-// elements reach.  Elements above that bound go to a list in shared memory; the
-// bound is taken after the first step, on values still in registers, and again
-// after 1, 2, 4, 8 .. steps, so a row lists about n_top log2(steps) elements.
-// The bound's equals are not listed (a masked row would be nothing else): where
-// fewer than n_top lie above it, the rest are its first equals by index, found
-// by a scan that stops early.  A row whose list overflows (values rising along
-// the row) takes the bound from bitwise counts over the row instead.
+// Alternatives: a thread's running maximum stands for an element of its own, so
+// the n_top-th largest of the maxima (of groups of two or four threads) is a
+// value that at least n_top elements reach.  Elements from that bound up go to a
+// list in shared memory; the bound is taken after the first step, whose values
+// are still in registers, and again after 3, 7, 15 .. steps, so a row lists
+// about n_top log2(steps) elements.  A bound of -infinity (a masked row) lists
+// what is above it only.  A list that is short then, or that overflowed (equal
+// or rising values), is made up by scans over the row: the values above the
+// bound, then its first equals by index.
 #include <atomic>
 
 #include "common.cuh"
@@ -35,42 +34,58 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kList = 2048;              // listed elements, at least kMaxTop for each CTA of a cluster
+constexpr int kList = 2048;                      // listed elements of a CTA
 constexpr int kMaxCluster = 16;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kShort = kList / kMaxCluster;      // elements that a CTA hands on, and that are ranked directly
+constexpr int kVecs = 4;                         // 16-byte vectors of a thread and step
+static_assert(kShort >= kMaxTop && 4 * kShort <= kThreads, "rank_top: four threads a key");
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLn2 = 0.6931471805599453;
+constexpr float kLowest = -3.402823466e38f;
 constexpr uint32_t kKeyMinusInf = 0x007FFFFFu;   // float_order_key(-infinity): below it only NaNs
 
-// Maximum with the sums S and U against it; m = -infinity: nothing above -infinity seen
-// (S and U are then 0, or NaN).
+// Sums S and U against the reference m; m = -infinity: nothing above
+// -infinity seen (S and U are then 0, or NaN).
 struct Stat {
   float m, s, u;
 };
 
-__device__ __forceinline__ Stat stat_join(Stat a, Stat b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  if (m == -INFINITY) return {m, a.s + b.s, a.u + b.u};
-  auto move = [&](Stat &t) {             // onto the reference m
-    const float d = (t.m - m) * c, f = exp2_approx(d);
-    t.u = t.s == 0.0f ? 0.0f : (t.u + t.s * fmaxf(d, -1e30f)) * f;
+__device__ __forceinline__ Stat stat_move(Stat t, float m, float c) {
+  if (m == -INFINITY) return {m, t.s, t.u};
+  const float d = shift_exponent(t.m, m, c), f = exp2_approx(d);
+  if (t.s != 0.0f) {                             // 0 has nothing to move, and 0 times -infinity would be NaN
+    t.u = (t.u + t.s * fmaxf(d, -1e30f)) * f;
     t.s *= f;
-    if (t.m == -INFINITY) t.s = t.u = t.s != t.s ? t.s : 0.0f;
-  };
-  move(a);
-  move(b);
-  return {m, a.s + b.s, a.u + b.u};
+  }
+  return {m, t.s, t.u};
+}
+
+// Sum over the warp's lanes, in a fixed order.
+__device__ __forceinline__ Stat stat_warp(Stat t, float c) {
+  const uint32_t top = __reduce_max_sync(0xffffffffu, float_order_key(t.m));
+  t = stat_move(t, order_key_float(top), c);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    t.s += __shfl_xor_sync(0xffffffffu, t.s, o);
+    t.u += __shfl_xor_sync(0xffffffffu, t.u, o);
+  }
+  return t;
 }
 
 struct Shared {
   unsigned long long list[kList];
+  unsigned long long got[kList];                 // first CTA: kShort from each of the cluster's
   unsigned long long best[kMaxTop];
   float m[kWarps], s[kWarps], u[kWarps];
   int before[kWarps];
-  uint32_t low[kWarps];
+  uint32_t high[kWarps], low[kWarps];
+  uint32_t group[2][kThreads / 2];
   int cnt[2][kWarps];
-  float out_m, out_s, out_u;             // the CTA's, for the cluster's first
-  int out_before, out_n;
-  int n;                                 // listed (counted beyond kList)
-  int n_best;
+  int place[kShort];
+  float from_m[kMaxCluster], from_s[kMaxCluster], from_u[kMaxCluster];   // first CTA: the cluster's
+  int from_before[kMaxCluster], from_n[kMaxCluster];
+  int n;                                         // listed (counted beyond kList)
+  int kept;                                      // of trim
 };
 
 // Sum over the CTA of a small count; `flip` alternates between calls.
@@ -85,17 +100,18 @@ __device__ __forceinline__ int block_count(int c, Shared &sh, int &flip) {
   return t;
 }
 
-// Leaves in sh.best the k largest of the n keys in sh.list (all different, at
-// most kList, n >= k), in no order; sh.n_best = k.  By bits from the top: the
-// largest bound that at least k keys reach.
-__device__ __forceinline__ void block_select(Shared &sh, int n, int k, int &flip) {
+// Cuts the n keys of list (all different, at most kList) to at most kShort with
+// the k largest among them; returns how many.  By bits from the top: the
+// largest bound that at least k keys reach, until few enough do.
+__device__ __forceinline__ int trim(unsigned long long *list, int n, int k, Shared &sh, int &flip) {
+  if (n <= kShort) return n;
   constexpr int P = kList / kThreads;
   unsigned long long key[P];
   uint32_t hi = 0u, lo = ~0u;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const int at = threadIdx.x + i * kThreads;
-    key[i] = at < n ? sh.list[at] : 0ull;
+    key[i] = at < n ? list[at] : 0ull;
     if (at < n) {
       hi = max(hi, static_cast<uint32_t>(key[i] >> 32));
       lo = min(lo, static_cast<uint32_t>(key[i] >> 32));
@@ -103,23 +119,22 @@ __device__ __forceinline__ void block_select(Shared &sh, int n, int k, int &flip
   }
   hi = __reduce_max_sync(0xffffffffu, hi);
   lo = __reduce_min_sync(0xffffffffu, lo);
-  if (threadIdx.x == 0) sh.n_best = 0;
   if ((threadIdx.x & 31) == 0) {
-    sh.cnt[flip][threadIdx.x >> 5] = static_cast<int>(hi);
+    sh.high[threadIdx.x >> 5] = hi;
     sh.low[threadIdx.x >> 5] = lo;
   }
+  if (threadIdx.x == 0) sh.kept = 0;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    hi = max(hi, static_cast<uint32_t>(sh.cnt[flip][w]));
+    hi = max(hi, sh.high[w]);
     lo = min(lo, sh.low[w]);
   }
-  flip ^= 1;
   // bits above the first that differs between the smallest and largest are the bound's too
   int bit = hi == lo ? 31 : 63 - __clz(hi ^ lo);
   unsigned long long bound = (static_cast<unsigned long long>(hi) << 32) & ~((2ull << bit) - 1ull);
   int got = n;
-  while (bit >= 0 && got != k) {
+  for (; bit >= 0 && got > kShort; --bit) {
     const unsigned long long t = bound | (1ull << bit);
     int c = 0;
 #pragma unroll
@@ -129,21 +144,36 @@ __device__ __forceinline__ void block_select(Shared &sh, int n, int k, int &flip
       bound = t;
       got = c;
     }
-    --bit;
   }
 #pragma unroll
   for (int i = 0; i < P; ++i)
     if (key[i] >= bound && key[i] != 0ull) {
-      const int at = atomicAdd(&sh.n_best, 1);
-      if (at < kMaxTop) sh.best[at] = key[i];
+      const int at = atomicAdd(&sh.kept, 1);
+      if (at < kShort) list[at] = key[i];
     }
+  __syncthreads();
+  return min(got, kShort);
+}
+
+// The k largest of the n <= kShort keys of list, in order, to sh.best: a key's
+// place is how many are larger, counted by four threads.
+__device__ __forceinline__ void rank_top(const unsigned long long *list, int n, int k, Shared &sh) {
+  const int i = threadIdx.x % kShort, part = threadIdx.x / kShort;
+  constexpr int kParts = kThreads / kShort;
+  if (threadIdx.x < kShort) sh.place[threadIdx.x] = 0;
+  __syncthreads();
+  const unsigned long long mine = i < n ? list[i] : 0ull;
+  int larger = 0;
+  for (int j = n * part / kParts; j < n * (part + 1) / kParts; ++j) larger += list[j] > mine;
+  if (larger) atomicAdd(&sh.place[i], larger);
+  __syncthreads();
+  if (threadIdx.x < n && sh.place[threadIdx.x] < k) sh.best[sh.place[threadIdx.x]] = mine;
   __syncthreads();
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
-  constexpr int W = Vec<T>::W, U = 4;
-  constexpr int E = W * U;                // values of a thread and step
+  constexpr int W = Vec<T>::W;
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t cr = cluster_rank(), cs = cluster_size();
@@ -151,14 +181,9 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
   const T *x = static_cast<const T *>(a.logits) + row * a.ld;
   const int v = static_cast<int>(a.v), k = a.n_top;
   const float c = kLog2e / a.temperature;
+  if (cs > 1) cluster_arrive();           // waited for before the first store to a peer
   if (tid == 0) sh.n = 0;
   __syncthreads();
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the logits are complete
-
-  const int64_t tok = a.tokens ? a.tokens[row] : -1;
-  const bool has = tok >= 0 && tok < v;
-  // no value is above NaN: without a token nothing is counted
-  const float xt = has ? to_float(x[tok]) : __int_as_float(0x7FFFFFFF);
 
   // this CTA's share: values [lo, hi) = head values (first CTA) + vectors [v0, v1) + the rest (last CTA)
   const RowCut cut = cut_row(x, v);
@@ -167,44 +192,85 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
   const uint32_t lo = cr == 0 ? 0 : cut.head + v0 * W;
   const uint32_t hi = cr == cs - 1 ? v : cut.head + v1 * W;
   const uint4 *xv = reinterpret_cast<const uint4 *>(x + cut.head);
+  const int steps = (v1 - v0 + kThreads * kVecs - 1) / (kThreads * kVecs);
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the logits are complete
+  uint4 nxt[kVecs];
+  auto fetch = [&](int s) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const int at = v0 + (s * kVecs + j) * kThreads + tid;
+      nxt[j] = at < v1 ? __ldcs(xv + at) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  if (steps > 0) fetch(0);
+  const int64_t tok = a.tokens ? a.tokens[row] : -1;
+  const bool has = tok >= 0 && tok < v;
+  // no value reaches NaN: without a token nothing is counted
+  const float xt = has ? to_float(x[tok]) : __int_as_float(0x7FFFFFFF);
+  // the least value above xt: behind the token only those count
+  const float xt_up = nextafterf(xt, INFINITY);
 
   Stat st = {-INFINITY, 0.0f, 0.0f};
   float ref = 0.0f;                       // st.m, or 0 while that is -infinity
+  unsigned long long s2 = 0ull, u2 = 0ull;   // two lanes of S and U
   int before = 0, flip = 0;
-  // Too few vectors for a bound (at most 63, and 14 values beside them): every value is listed.
-  const bool all = min(v1 - v0, kThreads) < k;
-  float tau = __int_as_float(0x7FFFFFFF); // the bound; NaN: none yet
+  // Groups of threads whose maxima give the bound: two or four threads, at
+  // least n_top groups with a vector each; with fewer every value is listed
+  // (at most 128 vectors and 14 values beside them).
+  const int shift = k <= 32 ? 2 : 1;
+  const bool all = min(v1 - v0, kThreads) < (k << shift);
+  float bound = -INFINITY, lim = k > 0 && all ? -INFINITY : __int_as_float(0x7FFFFFFF);   // listed from lim up; NaN: nothing
 
   auto add_max = [&](float cm) {
     if (cm > st.m) {
-      const float d = (st.m - cm) * c, f = exp2_approx(d);
-      st.u = st.s == 0.0f ? 0.0f : (st.u + st.s * fmaxf(d, -1e30f)) * f;
-      st.s = st.m == -INFINITY ? st.s : st.s * f;   // -infinity seen alone left 0, a NaN stays
+      const float2 s = unpack2(s2), u = unpack2(u2);
+      const Stat p = stat_move({st.m, s.x, u.x}, cm, c), q = stat_move({st.m, s.y, u.y}, cm, c);
+      s2 = pack2(p.s, q.s);
+      u2 = pack2(p.u, q.u);
       st.m = ref = cm;
     }
   };
-  auto add = [&](float xi) {
-    const float d = (xi - ref) * c, e = exp2_approx(d);
-    st.s += e;
-    st.u = fmaf(e, fmaxf(d, -200.0f), st.u);        // 2^-200 is 0 here, and 0 times -infinity would be NaN
+  auto add = [&](float xi) {              // 2^-200 is 0 here, and 0 times -infinity would be NaN
+    const float d = exponent(xi, ref, c), e = exp2_approx(d);
+    s2 = add2(s2, pack2(e, 0.0f));
+    u2 = fma2(pack2(e, 0.0f), pack2(fmaxf(d, -200.0f), 0.0f), u2);
   };
   auto list = [&](float xi, int i) {
     if (*reinterpret_cast<volatile int *>(&sh.n) > kList) return;   // lost already: no queue at the counter
     const int at = atomicAdd(&sh.n, 1);
     if (at < kList) sh.list[at] = argmax_key(xi, static_cast<uint32_t>(i));
   };
-  // the bound: largest key (its upper 16 bits) that at least k of the threads' maxima reach
+  // the largest key (its upper 16 bits) that at least k groups' maxima reach
+  int gflip = 0;
   auto take_bound = [&]() {
-    const uint32_t mine = v0 + tid < v1 ? float_order_key(st.m) : 0u;
-    uint32_t b = 0u;
-    for (int bit = 31; bit >= 16; --bit) {
-      const uint32_t t = b | (1u << bit);
-      if (__syncthreads_count(mine >= t) >= k) b = t;
+    uint32_t mine = v0 + tid < v1 ? float_order_key(st.m) : 0u;
+    mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
+    if (shift == 2) mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, 2));
+    if ((tid & ((1 << shift) - 1)) == 0) sh.group[gflip][tid >> shift] = mine;
+    __syncthreads();
+    uint32_t key[8], top = 0u, low = ~0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      key[i] = i < 4 || shift == 1 ? sh.group[gflip][lane + 32 * i] : 0u;
+      top = max(top, key[i]);
+      if (i < 4 || shift == 1) low = min(low, key[i]);
     }
-    tau = order_key_float(b < kKeyMinusInf ? kKeyMinusInf : b);
+    gflip ^= 1;
+    top = __reduce_max_sync(0xffffffffu, top);
+    low = __reduce_min_sync(0xffffffffu, low);
+    int bit = top == low ? 0 : 31 - __clz(top ^ low);
+    uint32_t b = top == low ? top : top & ~((2u << bit) - 1u);
+    for (; bit >= 16; --bit) {
+      const uint32_t t = b | (1u << bit);
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n += key[i] >= t;
+      if (__reduce_add_sync(0xffffffffu, n) >= k) b = t;
+    }
+    bound = order_key_float(b < kKeyMinusInf ? kKeyMinusInf : b);
+    lim = fmaxf(bound, kLowest);
   };
-  // values at the bound are listed too, unless it is -infinity: masked values are too many
-  auto listed = [&](float xi) { return all || xi > tau || (xi == tau && tau != -INFINITY); };
 
   // head and rest: at most one value a thread of the first and last CTA
   int edge_i = -1;
@@ -221,59 +287,97 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
     }
   }
 
-  const int steps = (v1 - v0 + kThreads * U - 1) / (kThreads * U);
-  uint4 nxt[U];
-  auto fetch = [&](int s) {
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int at = v0 + (s * U + j) * kThreads + tid;
-      if (at < v1) nxt[j] = __ldcs(xv + at);
-    }
-  };
-  if (steps > 0) fetch(0);
+  const unsigned long long c2 = pack2(c, c);
   for (int s = 0; s < steps; ++s) {
-    uint4 cur[U];
+    uint4 cur[kVecs];
 #pragma unroll
-    for (int j = 0; j < U; ++j) cur[j] = nxt[j];
+    for (int j = 0; j < kVecs; ++j) cur[j] = nxt[j];
+    const int at0 = v0 + s * kVecs * kThreads + tid;
+    const int mine = min(kVecs, (v1 - at0 + kThreads - 1) / kThreads);   // vectors of this thread (may be <= 0)
     if (s + 1 < steps) fetch(s + 1);
-    const int at0 = v0 + s * U * kThreads + tid;
-    auto each = [&](auto &&f) {           // over this step's values of the thread
+    float top[kVecs], cm = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int at = at0 + j * kThreads;
-        if (at < v1) {
-          float o[W];
-          unpack(cur[j], o, T{});
-          const int i0 = cut.head + at * W;
+    for (int j = 0; j < kVecs; ++j) {
+      float o[W];
+      unpack(cur[j], o, T{});
+      top[j] = o[0];
 #pragma unroll
-          for (int i = 0; i < W; ++i) f(o[i], i0 + i);
+      for (int i = 1; i < W; ++i) top[j] = fmaxf(top[j], o[i]);
+      if (j >= mine) top[j] = -INFINITY;
+      cm = fmaxf(cm, top[j]);
+    }
+    add_max(cm);
+    if (mine == kVecs && fabsf(ref) < kPlain) {
+      const float rc = -__fmul_rn(ref, c);
+      const unsigned long long rc2 = pack2(rc, rc);
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        float o[W];
+        unpack(cur[j], o, T{});
+#pragma unroll
+        for (int i = 0; i < W; i += 2) {
+          const float2 d = unpack2(fma2(pack2(o[i], o[i + 1]), c2, rc2));
+          const unsigned long long e = pack2(exp2_approx(d.x), exp2_approx(d.y));
+          s2 = add2(s2, e);
+          u2 = fma2(e, pack2(fmaxf(d.x, -200.0f), fmaxf(d.y, -200.0f)), u2);
         }
       }
-    };
-    float cm = -INFINITY;
-    each([&](float xi, int) { cm = fmaxf(cm, xi); });
-    add_max(cm);
-    each([&](float xi, int) { add(xi); });
-    if (cm >= xt) each([&](float xi, int i) { before += xi > xt || (xi == xt && i < tok); });
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        float o[W];
+        unpack(cur[j], o, T{});
+        if (j < mine) {
+#pragma unroll
+          for (int i = 0; i < W; ++i) add(o[i]);
+        }
+      }
+    }
+    if (cm >= xt) {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        if (top[j] >= xt && j < mine) {
+          float o[W];
+          unpack(cur[j], o, T{});
+          const int i0 = cut.head + (at0 + j * kThreads) * W;
+          if (tok < i0 || tok >= i0 + W) {
+            const float from = i0 < tok ? xt : xt_up;
+#pragma unroll
+            for (int i = 0; i < W; ++i) before += o[i] >= from;
+          } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) before += o[i] >= (i0 + i < tok ? xt : xt_up);
+          }
+        }
+      }
+    }
     if (k > 0) {
-      if (!all && (s & (s - 1)) == 0) take_bound();   // after step 0, 1, 2, 4, 8, ..
-      if (listed(cm))
-        each([&](float xi, int i) {
-          if (listed(xi)) list(xi, i);
-        });
+      // after step 0, 2, 6, 14, ..; not for the last one's sake alone
+      if (!all && ((s + 2) & (s + 1)) == 0 && (s == 0 || s + 1 < steps)) take_bound();
+      if (cm >= lim) {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+          if (top[j] >= lim && j < mine) {
+            float o[W];
+            unpack(cur[j], o, T{});
+            const int i0 = cut.head + (at0 + j * kThreads) * W;
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+              if (o[i] >= lim) list(o[i], i0 + i);
+          }
+        }
+      }
     }
   }
-  if (k > 0 && edge_i >= 0 && listed(edge)) list(edge, edge_i);
+  if (edge_i >= 0 && edge >= lim) list(edge, edge_i);
 
   // the CTA's sums
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Stat b;
-    b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-    b.u = __shfl_xor_sync(0xffffffffu, st.u, o);
-    st = stat_join(st, b, c);
+  {
+    const float2 s = unpack2(s2), u = unpack2(u2);
+    st.s = s.x + s.y;
+    st.u = u.x + u.y;
   }
+  st = stat_warp(st, c);
   before = __reduce_add_sync(0xffffffffu, before);
   if (lane == 0) {
     sh.m[warp] = st.m;
@@ -284,27 +388,14 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
   __syncthreads();
   if (warp == 0) {
     st = lane < kWarps ? Stat{sh.m[lane], sh.s[lane], sh.u[lane]} : Stat{-INFINITY, 0.0f, 0.0f};
-#pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) {
-      Stat b;
-      b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-      b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-      b.u = __shfl_xor_sync(0xffffffffu, st.u, o);
-      st = stat_join(st, b, c);
-    }
+    st = stat_warp(st, c);
     before = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.before[lane] : 0);
-    if (lane == 0) {
-      sh.out_m = st.m;
-      sh.out_s = st.s;
-      sh.out_u = st.u;
-      sh.out_before = before;
-    }
   }
 
   // the CTA's alternatives: sh.list holds n values, the k first of its share among them
   int n = sh.n;
   if (k > 0 && !all && (n > kList || n < k)) {
-    uint32_t bound = float_order_key(tau);
+    uint32_t key = float_order_key(bound);
     auto key_at = [&](uint32_t i) { return float_order_key(to_float(x[i])); };
     auto count_from = [&](uint32_t t) {
       int m = 0;
@@ -312,23 +403,23 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
       return block_count(m, sh, flip);
     };
     if (n > kList) {
-      if (count_from(bound + 1) >= k) {   // rising values: the k-th largest key itself, bit by bit
+      if (count_from(key + 1) >= k) {     // rising values: the k-th largest key itself, bit by bit
         uint32_t b = 0u;
         for (int bit = 31; bit >= 0; --bit)
           if (count_from(b | (1u << bit)) >= k) b |= 1u << bit;
-        bound = b;
+        key = b;
       }
       __syncthreads();
       if (tid == 0) sh.n = 0;
       __syncthreads();
-      for (uint32_t i = lo + tid; i < hi; i += kThreads)   // fewer than k lie above the bound
-        if (key_at(i) > bound) list(to_float(x[i]), i);
+      for (uint32_t i = lo + tid; i < hi; i += kThreads)   // fewer than k lie above the key
+        if (key_at(i) > key) list(to_float(x[i]), i);
       __syncthreads();
-      n = sh.n;
+      n = min(sh.n, k);
     }
-    // then the bound's equals, by index
+    // then the key's equals, by index
     for (uint32_t base = lo; base < hi && n < k; base += kThreads) {
-      const bool eq = base + tid < hi && key_at(base + tid) == bound;
+      const bool eq = base + tid < hi && key_at(base + tid) == key;
       const uint32_t m = __ballot_sync(0xffffffffu, eq);
       if (lane == 0) sh.cnt[flip][warp] = __popc(m);
       __syncthreads();
@@ -337,92 +428,77 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
         if (w < warp) at += sh.cnt[flip][w];
         sum += sh.cnt[flip][w];
       }
-      if (eq && at < k) sh.list[at] = argmax_key(order_key_float(bound), base + tid);
+      if (eq && at < k) sh.list[at] = argmax_key(order_key_float(key), base + tid);
       n = min(n + sum, k);
       flip ^= 1;
     }
     __syncthreads();
   }
   if (cs > 1) {
-    if (n > kList / kMaxCluster) {        // what the first CTA has room for from each
-      block_select(sh, n, k, flip);
-      n = k;
-      if (tid < k) sh.list[tid] = sh.best[tid];
-    }
-    if (tid == 0) sh.out_n = n;
-    cluster_sync();
-    if (cr == 0) {
-      if (warp == 0) {
-        const uint32_t r = lane < static_cast<int>(cs) ? lane : 0;
-        st = {peer_loadf(peer_addr(&sh.out_m, r)), peer_loadf(peer_addr(&sh.out_s, r)),
-              peer_loadf(peer_addr(&sh.out_u, r))};
-        before = static_cast<int>(peer_loadu(peer_addr(&sh.out_before, r)));
-        if (lane >= static_cast<int>(cs)) {
-          st = {-INFINITY, 0.0f, 0.0f};
-          before = 0;
-        }
-#pragma unroll
-        for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
-          Stat b;
-          b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-          b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-          b.u = __shfl_xor_sync(0xffffffffu, st.u, o);
-          st = stat_join(st, b, c);
-        }
-        before = __reduce_add_sync(0xffffffffu, before);
-      }
-      // one warp a peer's list, behind the lists before it
-      int at = 0;
-      for (uint32_t r = 0; r < cs; ++r) {
-        const int nr = static_cast<int>(peer_loadu(peer_addr(&sh.out_n, r)));
-        if (r > 0 && r == static_cast<uint32_t>(warp)) {
-          const uint32_t from = peer_addr(sh.list, r);
-          for (int i = lane; i < nr; i += 32) sh.list[at + i] = peer_load64(from + 8 * i);
-        }
-        at += nr;
-      }
-      n = at;
-    }
-    cluster_sync();                       // the peers' shared memory has been read
-    if (cr != 0) return;
+    n = trim(sh.list, n, k, sh, flip);
+    cluster_wait();                       // every CTA of the cluster has started
+    const uint32_t to = peer_addr(sh.got, 0) + cr * kShort * 8u;
+    if (tid < n) peer_store64(to + 8 * tid, sh.list[tid]);
     if (tid == 0) {
-      sh.out_m = st.m;
-      sh.out_s = st.s;
-      sh.out_u = st.u;
-      sh.out_before = before;
+      peer_store32(peer_addr(&sh.from_m[cr], 0), __float_as_uint(st.m));
+      peer_store32(peer_addr(&sh.from_s[cr], 0), __float_as_uint(st.s));
+      peer_store32(peer_addr(&sh.from_u[cr], 0), __float_as_uint(st.u));
+      peer_store32(peer_addr(&sh.from_before[cr], 0), static_cast<uint32_t>(before));
+      peer_store32(peer_addr(&sh.from_n[cr], 0), static_cast<uint32_t>(n));
     }
+    cluster_sync();
+    if (cr != 0) return;
+    if (warp == 0) {
+      const bool in = lane < static_cast<int>(cs);
+      st = in ? Stat{sh.from_m[lane], sh.from_s[lane], sh.from_u[lane]} : Stat{-INFINITY, 0.0f, 0.0f};
+      st = stat_warp(st, c);
+      before = __reduce_add_sync(0xffffffffu, in ? sh.from_before[lane] : 0);
+    }
+    if (k > 0) {                          // close the lists up: one warp a CTA's
+      int at = 0, mine = 0;
+      n = 0;
+      for (uint32_t r = 0; r < cs; ++r) {
+        if (r == static_cast<uint32_t>(warp)) {
+          at = n;
+          mine = sh.from_n[r];
+        }
+        n += sh.from_n[r];
+      }
+      for (int i = lane; i < mine; i += 32) sh.list[at + i] = sh.got[warp * kShort + i];
+    }
+  }
+  if (tid == 0) {
+    sh.m[0] = st.m;
+    sh.s[0] = st.s;
+    sh.u[0] = st.u;
   }
   __syncthreads();
-  const float m = sh.out_m == -INFINITY ? 0.0f : sh.out_m, total = sh.out_s;
+  const float total = sh.s[0], m = sh.m[0] == -INFINITY ? 0.0f : sh.m[0];
   const bool empty = total == 0.0f;       // nothing above -infinity
-  const float logs = logf(total);
+  const float logs = log2f(total);
+  // from here a few values a row, in 64 bits: in log2's units a lowest value would overflow
+  const double lse = (fabsf(m) < kPlain ? kLn2 * static_cast<double>(__fmul_rn(m, c)) : m / static_cast<double>(a.temperature)) +
+                     kLn2 * static_cast<double>(logs);
+  auto logprob = [&](float xi) { return empty ? -INFINITY : static_cast<float>(xi / static_cast<double>(a.temperature) - lse); };
   if (tid == 0) {
-    if (a.lse) a.lse[row] = empty ? -INFINITY : m / a.temperature + logs;
-    if (a.entropy) a.entropy[row] = empty ? 0.0f : logs - kLn2 * (sh.out_u / total);
-    if (a.logprob) a.logprob[row] = !has ? 0.0f : empty ? -INFINITY : (xt - m) / a.temperature - logs;
-    if (a.rank) a.rank[row] = has ? sh.out_before : -1;
+    if (a.lse) a.lse[row] = empty ? -INFINITY : static_cast<float>(lse);
+    if (a.entropy) a.entropy[row] = empty ? 0.0f : static_cast<float>(kLn2) * (logs - sh.u[0] / total);
+    if (a.logprob) a.logprob[row] = has ? logprob(xt) : 0.0f;
+    if (a.rank) a.rank[row] = has ? before : -1;
   }
   if (k == 0) return;
-  const int got = min(n, k);
-  if (n > k) {
-    block_select(sh, n, k, flip);
-  } else {
-    if (tid < got) sh.best[tid] = sh.list[tid];
-    __syncthreads();
-  }
+  n = trim(sh.list, n, k, sh, flip);
+  rank_top(sh.list, n, k, sh);
   if (tid < k) {
-    int at = tid;
     int32_t id = -1;
     float lp = -INFINITY;
-    if (tid < got) {
+    if (tid < n) {
       const unsigned long long key = sh.best[tid];
-      at = 0;
-      for (int i = 0; i < got; ++i) at += sh.best[i] > key;
       id = static_cast<int32_t>(argmax_key_index(key));
-      if (!empty) lp = (order_key_float(static_cast<uint32_t>(key >> 32)) - m) / a.temperature - logs;
+      lp = logprob(order_key_float(static_cast<uint32_t>(key >> 32)));
     }
-    a.top_ids[row * k + at] = id;
-    a.top_logprobs[row * k + at] = lp;
+    a.top_ids[row * k + tid] = id;
+    a.top_logprobs[row * k + tid] = lp;
   }
 }
 
