@@ -288,6 +288,18 @@ def muse_lmhead_backward(h: int | None, grad_logits: int, logits: int | None, hi
                                                grad_hidden, grad_gamma, stream)
 
 
+_dtypes = None
+
+
+def _row_dtypes():
+    """MUSE_DTYPE of a torch dtype."""
+    global _dtypes
+    if _dtypes is None:
+        import torch
+        _dtypes = {torch.float32: MUSE_DTYPE_F32, torch.float16: MUSE_DTYPE_F16, torch.bfloat16: MUSE_DTYPE_BF16}
+    return _dtypes
+
+
 class TokenScores(NamedTuple):
     """What LMHead.score returns, one entry a row (None for what was not asked for)."""
     logprob: Any        # [n] f32, the given token's (0 in a padded row)
@@ -473,29 +485,40 @@ class LMHead:
 
     def _rows(self, t, name):
         """(pointer, MUSE_DTYPE, rows, distance) of a matrix of logits whose rows are contiguous."""
-        import torch
-        dtype = {torch.float32: MUSE_DTYPE_F32, torch.float16: MUSE_DTYPE_F16,
-                 torch.bfloat16: MUSE_DTYPE_BF16}.get(t.dtype)
-        if dtype is None or t.device.type != "cuda" or t.device.index != self.device:
+        dtype = _row_dtypes().get(t.dtype)
+        if dtype is None or t.get_device() != self.device:
             raise ValueError(f"{name}: need a float32, float16 or bfloat16 tensor on cuda:{self.device}")
-        n = t.shape[0] if t.dim() == 2 else -1
-        if n < 0 or t.shape[1] != self.n_rows:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, need [n, {self.n_rows}]")
-        if (self.n_rows > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < self.n_rows):
-            raise ValueError(f"{name}: strides {tuple(t.stride())}, need contiguous rows that do not overlap")
-        return t.data_ptr(), dtype, n, t.stride(0) if n > 1 else self.n_rows
+        shape, v = t.shape, self.n_rows
+        if len(shape) != 2 or shape[1] != v:
+            raise ValueError(f"{name}: shape {tuple(shape)}, need [n, {v}]")
+        n = shape[0]
+        ld, step = t.stride()
+        if (v > 1 and step != 1) or (n > 1 and ld < v):
+            raise ValueError(f"{name}: strides {t.stride()}, need contiguous rows that do not overlap")
+        return t.data_ptr(), dtype, n, ld if n > 1 else v
+
+    def _stream(self, stream):
+        import torch
+        return (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
 
     def _score_outputs(self, n, tokens, n_top, device):
+        """(TokenScores, pointers of tokens and outputs in the C order)"""
         import torch
         if not 0 <= n_top <= MUSE_MAX_TOP:
             raise ValueError(f"n_top: 0..{MUSE_MAX_TOP}")
+        empty, f, i, rows = torch.empty, torch.float32, torch.int32, (n,)
+        tp = lp = rp = ip = pp = logprob = rank = ids = top = None
         if tokens is not None:
-            self._check(tokens, "tokens", torch.int32, (n,))
-        f, i = torch.float32, torch.int32
-        none = lambda want, *a, **k: torch.empty(*a, device=device, **k) if want else None  # noqa: E731
-        return TokenScores(none(tokens is not None, (n,), dtype=f), none(tokens is not None, (n,), dtype=i),
-                           torch.empty((n,), dtype=f, device=device), torch.empty((n,), dtype=f, device=device),
-                           none(n_top > 0, (n, n_top), dtype=i), none(n_top > 0, (n, n_top), dtype=f))
+            tp = self._check(tokens, "tokens", i, rows)
+            logprob, rank = empty(rows, dtype=f, device=device), empty(rows, dtype=i, device=device)
+            lp, rp = logprob.data_ptr(), rank.data_ptr()
+        lse, entropy = empty(rows, dtype=f, device=device), empty(rows, dtype=f, device=device)
+        if n_top > 0:
+            ids = empty((n, n_top), dtype=i, device=device)
+            top = empty((n, n_top), dtype=f, device=device)
+            ip, pp = ids.data_ptr(), top.data_ptr()
+        return (TokenScores(logprob, rank, lse, entropy, ids, top),
+                tp, lp, rp, lse.data_ptr(), entropy.data_ptr(), ip, pp)
 
     def score(self, logits, tokens=None, n_top: int = 0, temperature: float = 1.0, stream=None) -> TokenScores:
         """Log probability and rank of tokens [n] int32, normaliser, entropy and top alternatives of each row.
@@ -504,15 +527,12 @@ class LMHead:
         apart, any n: what a forward returned (softmax and logprobs are taken
         over the capped logits).  Masked logits are -infinity; a token outside
         0..n_rows-1 marks a padded row.  See muse_lmhead_score in the C header."""
-        import torch
         if logits.dim() == 1:
             logits = logits.unsqueeze(0)
         ptr, dtype, n, ld = self._rows(logits, "logits")
-        out = self._score_outputs(n, tokens, n_top, logits.device)
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
-        at = [None if t is None else t.data_ptr() for t in (tokens, *out)]
-        st = muse_lmhead_score(self.handle, ptr, dtype, n, ld, at[0], float(temperature), n_top, *at[1:],
-                               s.cuda_stream)
+        out, tp, *at = self._score_outputs(n, tokens, n_top, logits.device)
+        st = load_library().muse_lmhead_score(self.handle, ptr, dtype, n, ld, tp, temperature, n_top, *at,
+                                              self._stream(stream))
         if st != MUSE_OK:
             raise MuseError(st, "muse_lmhead_score")
         return out
@@ -533,11 +553,9 @@ class LMHead:
         if logits is None:
             logits = torch.empty((b, self.n_rows), dtype=torch.float32, device=hidden.device)
         lp = self._check(logits, "logits", torch.float32, (b, self.n_rows))
-        out = self._score_outputs(b, tokens, n_top, hidden.device)
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
-        at = [None if t is None else t.data_ptr() for t in (tokens, *out)]
-        st = muse_lmhead_forward_score(self.handle, hp, b, gp, float(eps), wp, float(scale), float(cap), lp, at[0],
-                                       float(temperature), n_top, *at[1:], s.cuda_stream)
+        out, tp, *at = self._score_outputs(b, tokens, n_top, hidden.device)
+        st = muse_lmhead_forward_score(self.handle, hp, b, gp, float(eps), wp, float(scale), float(cap), lp, tp,
+                                       float(temperature), n_top, *at, self._stream(stream))
         if st != MUSE_OK:
             raise MuseError(st, "muse_lmhead_forward_score")
         return logits, out
@@ -569,9 +587,8 @@ class LMHead:
             gp, gtype, gn, gld = self._rows(grad, "grad")
             if gtype != dtype or gn != n:
                 raise ValueError("grad: need the logits' shape and dtype")
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
-        st = muse_lmhead_distill(self.handle, ptr, dtype, n, ld, ip, pp, top, int(bool(tail)), wp, float(temperature),
-                                 loss.data_ptr(), gp, gld, s.cuda_stream)
+        st = load_library().muse_lmhead_distill(self.handle, ptr, dtype, n, ld, ip, pp, top, 1 if tail else 0, wp,
+                                                temperature, loss.data_ptr(), gp, gld, self._stream(stream))
         if st != MUSE_OK:
             raise MuseError(st, "muse_lmhead_distill")
         return loss, grad
@@ -604,9 +621,8 @@ class LMHead:
         if grad_hidden is None:
             grad_hidden = torch.empty((b, self.k), dtype=torch.float32, device=grad_logits.device)
         op = self._check(grad_hidden, "grad_hidden", torch.float32, (b, self.k))
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
-        st = muse_lmhead_backward(self.handle, tp, lp, hp, b, gp, float(eps), wp, float(scale), float(cap), op, ap,
-                                  s.cuda_stream)
+        st = load_library().muse_lmhead_backward(self.handle, tp, lp, hp, b, gp, eps, wp, scale, cap, op, ap,
+                                                 self._stream(stream))
         if st != MUSE_OK:
             raise MuseError(st, "muse_lmhead_backward")
         return grad_hidden, grad_gamma
