@@ -7,6 +7,18 @@
 //     tail:         p_j = exp(l_j),  p_t = max(0, 1 - sum p),  q_t = sum_{i not in S} q_i
 //     loss = w [ sum_j p_j (log p_j - log q_{id_j}) + p_t (log p_t - log q_t) ]
 //     dloss/dx_i = w/T [ (sum p + p_t) q_i - sum_{j: id_j = i} p_j - [i not in S] p_t q_i / q_t ]
+//
+// Bound: HBM, each logit read once and each gradient written once.  A cluster
+// of CTAs holds a row in its shared memory (in the logits' type, up to 104 KB a
+// CTA, so that two CTAs of an SM overlap one's loads with the other's stores),
+// and one barrier of the cluster joins the CTAs' maxima and sums.  The sum
+// outside S is taken apart from the sum inside, not as a difference: where the
+// student is sure of the teacher's ids a difference would be rounding alone.
+// The ids' values are taken out of the row (set to -infinity) before the sum.
+// Nothing is kept in global memory, so calls may overlap.  A row that 16 CTAs
+// cannot hold is read twice by one CTA.
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "rows.cuh"
@@ -15,6 +27,283 @@ namespace muse {
 namespace {
 
 constexpr int kDistillThreads = 512;
+constexpr int kDistillWarps = kDistillThreads / 32;
+constexpr int kDistillCluster = 16;
+constexpr int kHeldTwo = 104 * 1024;     // bytes of a row in a CTA: two CTAs an SM
+constexpr int kHeldOne = 216 * 1024;     // one CTA an SM
+constexpr float kLog2eD = 1.4426950408889634f;
+constexpr double kLn2D = 0.6931471805599453;
+
+struct DistillShared {
+  int id[kMaxTop];                       // -1: left out
+  float p[kMaxTop], lp[kMaxTop];         // probability and its logarithm
+  float x[kMaxTop];                      // the ids' logits: this CTA's own; all of them in the first CTA
+  float m[kDistillWarps], s[kDistillWarps];
+  float mass;
+  float from_m[kDistillCluster], from_rest[kDistillCluster], from_in[kDistillCluster];
+};
+
+__device__ __forceinline__ void copy_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+
+// Sums against the maximum m (m = -infinity: only 0, or NaN) onto another one.
+__device__ __forceinline__ float move_sum(float s, float from, float to, float c) {
+  return to == -INFINITY || s == 0.0f ? s : s * exp2_approx(shift_exponent(from, to, c));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const DistillArgs a) {
+  constexpr int W = Vec<T>::W;
+  extern __shared__ __align__(16) uint8_t held[];
+  __shared__ DistillShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t cr = cluster_rank(), cs = cluster_size();
+  const int64_t row = blockIdx.x / cs;
+  const T *x = static_cast<const T *>(a.logits) + row * a.ld;
+  T *g = a.grad ? static_cast<T *>(a.grad) + row * a.grad_ld : nullptr;
+  const int v = static_cast<int>(a.v), k = a.n_top;
+  const float c = kLog2eD / a.temperature;
+  cluster_arrive();                       // waited for before the first store to a peer
+
+  // this CTA's share: head values (first CTA), vectors [v0, v1), the rest (last CTA)
+  const RowCut cut = cut_row(x, v);
+  const int v0 = static_cast<int>(static_cast<int64_t>(cut.vecs) * cr / cs);
+  const int v1 = static_cast<int>(static_cast<int64_t>(cut.vecs) * (cr + 1) / cs);
+  const int first = cut.head + v0 * W;    // index of the first held value
+  const int count = (v1 - v0) * W;
+  T *row_held = reinterpret_cast<T *>(held);
+  uint4 *vec_held = reinterpret_cast<uint4 *>(held);
+  const uint4 *xv = reinterpret_cast<const uint4 *>(x + cut.head) + v0;
+  const int rest_n = v - cut.head - cut.vecs * W;
+  int edge_i = -1;                        // a value beside the vectors, one thread's own
+  if (cr == 0 && tid < cut.head) edge_i = tid;
+  if (cr == cs - 1 && tid >= 32 && tid < 32 + rest_n) edge_i = v - rest_n + tid - 32;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the logits and the teacher's side are complete
+  const float w = a.row_weight ? a.row_weight[row] : 1.0f;
+  float scale = w / a.temperature, m = 0.0f, f_in = 0.0f, f_out = 0.0f;
+  float edge = -INFINITY;
+  bool edge_in = false;
+  int own = -1;                           // the place of this thread's teacher entry in row_held
+  if (w != 0.0f) {
+    for (int i = tid; i < v1 - v0; i += kDistillThreads) copy_async16(vec_held + i, xv + i);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (edge_i >= 0) edge = to_float(x[edge_i]);
+    if (tid < kMaxTop) {
+      const int id = tid < k ? a.teacher_ids[row * k + tid] : -1;
+      const float l = tid < k ? a.teacher_logprobs[row * k + tid] : -INFINITY;
+      const bool ok = id >= 0 && id < v;
+      sh.id[tid] = ok ? id : -1;
+      sh.lp[tid] = ok ? l : -INFINITY;
+      if (id >= first && id < first + count) own = id - first;
+    }
+    __syncthreads();
+    if (warp == 0) {                      // the teacher's probabilities
+      float l0 = sh.lp[lane], l1 = sh.lp[lane + 32], shift = 0.0f;
+      if (!a.tail) {
+        float top = fmaxf(l0, l1);
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (top > -INFINITY) {
+          float s = expf(l0 - top) + expf(l1 - top);
+          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          shift = top + logf(s);
+        }
+      }
+      l0 -= shift;
+      l1 -= shift;
+      const float p0 = expf(l0), p1 = expf(l1);
+      float mass = p0 + p1;
+      for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+      sh.lp[lane] = l0;
+      sh.lp[lane + 32] = l1;
+      sh.p[lane] = p0;
+      sh.p[lane + 32] = p1;
+      if (lane == 0) sh.mass = mass;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    // the ids' values out of the row
+    float mine = -INFINITY, in_m = -INFINITY;
+    if (own >= 0) mine = to_float(row_held[own]);
+    __syncthreads();
+    bool again = false;                   // an id that an earlier entry has
+    if (own >= 0) {
+      row_held[own] = from_float<T>(-INFINITY);
+      for (int j = 0; j < tid; ++j) again |= sh.id[j] == first + own;
+      in_m = mine;
+      sh.x[tid] = mine;
+    }
+    if (edge_i >= 0)
+      for (int j = 0; j < k; ++j)
+        if (sh.id[j] == edge_i) {
+          edge_in = true;
+          sh.x[j] = edge;
+        }
+    __syncthreads();
+
+    // maximum and sum of what is left
+    float top = -INFINITY, ref = 0.0f;
+    unsigned long long s2 = 0ull;
+    const unsigned long long c2 = pack2(c, c);
+    for (int i = tid; i < v1 - v0; i += kDistillThreads) {
+      float o[W];
+      unpack(vec_held[i], o, T{});
+      float cm = o[0];
+#pragma unroll
+      for (int j = 1; j < W; ++j) cm = fmaxf(cm, o[j]);
+      if (cm > top) {
+        const float2 s = unpack2(s2);
+        s2 = pack2(move_sum(s.x, top, cm, c), move_sum(s.y, top, cm, c));
+        top = ref = cm;
+      }
+      if (fabsf(ref) < kPlain) {
+        const float rc = -__fmul_rn(ref, c);
+        const unsigned long long rc2 = pack2(rc, rc);
+#pragma unroll
+        for (int j = 0; j < W; j += 2) {
+          const float2 d = unpack2(fma2(pack2(o[j], o[j + 1]), c2, rc2));
+          s2 = add2(s2, pack2(exp2_approx(d.x), exp2_approx(d.y)));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) s2 = add2(s2, pack2(exp2_approx(exponent(o[j], ref, c)), 0.0f));
+      }
+    }
+    float rest = unpack2(s2).x + unpack2(s2).y;
+    // the CTA's maximum, the edges and ids with it, then its sums against that
+    float cm = fmaxf(fmaxf(top, edge), in_m);
+    cm = order_key_float(__reduce_max_sync(0xffffffffu, float_order_key(cm)));
+    if (lane == 0) sh.m[warp] = cm;
+    __syncthreads();
+    cm = order_key_float(__reduce_max_sync(0xffffffffu, float_order_key(sh.m[lane & (kDistillWarps - 1)])));
+    const float cref = cm == -INFINITY ? 0.0f : cm;
+    rest = move_sum(rest, top, cm, c);
+    float in = 0.0f;
+    if (edge_i >= 0) (edge_in ? in : rest) += exp2_approx(exponent(edge, cref, c));
+    if (own >= 0 && !again) in += exp2_approx(exponent(mine, cref, c));
+    for (int o = 16; o > 0; o >>= 1) {
+      rest += __shfl_xor_sync(0xffffffffu, rest, o);
+      in += __shfl_xor_sync(0xffffffffu, in, o);
+    }
+    __syncthreads();
+    if (lane == 0) {
+      sh.m[warp] = rest;
+      sh.s[warp] = in;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      rest = lane < kDistillWarps ? sh.m[lane] : 0.0f;
+      in = lane < kDistillWarps ? sh.s[lane] : 0.0f;
+      for (int o = 16; o > 0; o >>= 1) {
+        rest += __shfl_xor_sync(0xffffffffu, rest, o);
+        in += __shfl_xor_sync(0xffffffffu, in, o);
+      }
+    }
+    cluster_wait();                       // every CTA of the cluster has started
+    if (tid < static_cast<int>(cs)) {     // to every CTA, so that all go on with the same bits
+      peer_store32(peer_addr(&sh.from_m[cr], tid), __float_as_uint(cm));
+      peer_store32(peer_addr(&sh.from_rest[cr], tid), __float_as_uint(rest));
+      peer_store32(peer_addr(&sh.from_in[cr], tid), __float_as_uint(in));
+    }
+    if (own >= 0) peer_store32(peer_addr(&sh.x[tid], 0), __float_as_uint(mine));
+    if (edge_in)
+      for (int j = 0; j < k; ++j)
+        if (sh.id[j] == edge_i) peer_store32(peer_addr(&sh.x[j], 0), __float_as_uint(edge));
+    cluster_sync();
+
+    const bool have = lane < static_cast<int>(cs);
+    cm = have ? sh.from_m[lane] : -INFINITY;
+    m = order_key_float(__reduce_max_sync(0xffffffffu, float_order_key(cm)));
+    rest = have ? move_sum(sh.from_rest[lane], cm, m, c) : 0.0f;
+    in = have ? move_sum(sh.from_in[lane], cm, m, c) : 0.0f;
+    for (int o = 16; o > 0; o >>= 1) {
+      rest += __shfl_xor_sync(0xffffffffu, rest, o);
+      in += __shfl_xor_sync(0xffffffffu, in, o);
+    }
+    if (m == -INFINITY) m = 0.0f;         // all masked (the sums stay 0), or NaN beside masked values
+    const float total = rest + in, mass = sh.mass;
+    const float pt = a.tail ? fmaxf(0.0f, 1.0f - mass) : 0.0f;
+    if (cr == 0 && warp == 0 && a.loss) {
+      // a few values a row, in 64 bits: a lowest value would overflow in log2's units
+      const double lse = (fabsf(m) < kPlain ? kLn2D * static_cast<double>(__fmul_rn(m, c))
+                                            : m / static_cast<double>(a.temperature)) +
+                         kLn2D * static_cast<double>(log2f(total));
+      double loss = 0.0;
+      for (int j = lane; j < k; j += 32)
+        if (sh.p[j] > 0.0f)
+          loss += sh.p[j] * (sh.lp[j] - (sh.x[j] / static_cast<double>(a.temperature) - lse));
+      for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
+      if (pt > 0.0f) loss += pt * (logf(pt) - kLn2D * (static_cast<double>(log2f(rest)) - log2f(total)));
+      if (lane == 0) a.loss[row] = total == 0.0f ? 0.0f : static_cast<float>(w * loss);
+    }
+    if (total == 0.0f) {
+      scale = 0.0f;
+    } else {
+      f_in = (mass + pt) / total * scale;
+      f_out = rest != 0.0f ? ((mass + pt) / total - pt / rest) * scale : 0.0f;
+    }
+    if (!g) return;
+    if (own >= 0) {
+      if (again) {
+        own = -1;                         // the first entry of the id writes for all
+      } else {
+        float r = 0.0f;
+        for (int j = 0; j < k; ++j)
+          if (sh.id[j] == first + own) r += sh.p[j];
+        in_m = exp2_approx(exponent(mine, m, c)) * f_in - r * scale;
+      }
+    }
+    if (edge_i >= 0) {
+      const float e = exp2_approx(exponent(edge, m, c));
+      if (edge_in) {
+        float r = 0.0f;
+        for (int j = 0; j < k; ++j)
+          if (sh.id[j] == edge_i) r += sh.p[j];
+        edge = e * f_in - r * scale;
+      } else {
+        edge = e * f_out;
+      }
+    }
+    if (scale == 0.0f) edge = in_m = 0.0f;
+    top = in_m;
+    // the gradient outside S; the ids' places are 0 here (-infinity in the row)
+    if (scale != 0.0f) {
+      const bool plain = fabsf(m) < kPlain;
+      const float rc = -__fmul_rn(m, c);
+      auto grad_of = [&](float xi) { return exp2_approx(plain ? fmaf(xi, c, rc) : (xi - m) * c) * f_out; };
+      if ((reinterpret_cast<uintptr_t>(g + first) & 15) == 0) {
+        uint4 *gv = reinterpret_cast<uint4 *>(g + first);
+        for (int i = tid; i < v1 - v0; i += kDistillThreads) {
+          float o[W];
+          unpack(vec_held[i], o, T{});
+          union {
+            uint4 q;
+            T t[W];
+          } r;
+#pragma unroll
+          for (int j = 0; j < W; ++j) r.t[j] = from_float<T>(grad_of(o[j]));
+          __stcs(gv + i, r.q);
+        }
+      } else {                            // rows of another alignment than the logits'
+        for (int i = tid; i < count; i += kDistillThreads) g[first + i] = from_float<T>(grad_of(to_float(row_held[i])));
+      }
+      __syncthreads();                    // the zeros at the ids' places are written
+      if (own >= 0) g[first + own] = from_float<T>(top);
+      if (edge_i >= 0) g[edge_i] = from_float<T>(edge);
+      return;
+    }
+  } else {
+    cluster_wait();
+    if (cr == 0 && tid == 0 && a.loss) a.loss[row] = 0.0f;
+    if (!g) return;
+  }
+  // no weight, or nothing above -infinity: zeros
+  for (int i = tid; i < count; i += kDistillThreads) g[first + i] = from_float<T>(0.0f);
+  if (edge_i >= 0) g[edge_i] = from_float<T>(0.0f);
+}
 
 __device__ __forceinline__ float block_sum(float v, float *s) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -26,8 +315,10 @@ __device__ __forceinline__ float block_sum(float v, float *s) {
   return r;
 }
 
+// One CTA a row, read once for the maximum, once for the sums and once for the
+// gradient: rows that a cluster's shared memory cannot hold.
 template <typename T>
-__global__ void __launch_bounds__(kDistillThreads) distill_kernel(const DistillArgs a) {
+__global__ void __launch_bounds__(kDistillThreads) distill_long_kernel(const DistillArgs a) {
   __shared__ float s_red[kDistillThreads / 32];
   __shared__ float s_max[kDistillThreads / 32];
   __shared__ int s_id[kMaxTop];
@@ -116,14 +407,62 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const DistillA
   }
 }
 
+template <typename T>
+cudaError_t launch_distill_long(const DistillArgs &a) {
+  distill_long_kernel<T><<<static_cast<unsigned>(a.n), kDistillThreads, 0, a.stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_distill_t(const DistillArgs &a) {
+  static std::atomic<unsigned long long> configured{0};   // one bit per device; host threads may race here
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(configured.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(distill_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(distill_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldOne);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  // As few CTAs as hold the row two to an SM, more while there are SMs to fill,
+  // 16 with one to an SM for the longest rows.
+  const int64_t bytes = a.v * static_cast<int64_t>(sizeof(T));
+  auto held = [&](int64_t cs) { return (bytes / 16 + cs - 1) / cs * 16; };   // a share is at most this
+  int cs = 1;
+  while (cs < kDistillCluster && held(cs) > kHeldTwo) cs *= 2;
+  while (cs < kDistillCluster && a.n * 2 * cs <= 2 * a.num_sms && a.v / (2 * cs) >= 2048) cs *= 2;
+  if (held(cs) > kHeldOne) return launch_distill_long<T>(a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.n * cs));
+  cfg.blockDim = dim3(kDistillThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(held(cs));
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // may start before the previous grid ends
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cs);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (held(cs) > kHeldTwo) {              // 16 SMs of one GPC at a time: not every device has them
+    int fit = 0;
+    e = cudaOccupancyMaxActiveClusters(&fit, distill_kernel<T>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (fit < 1) return launch_distill_long<T>(a);
+  }
+  return cudaLaunchKernelEx(&cfg, distill_kernel<T>, a);
+}
+
 }  // namespace
 
 cudaError_t launch_distill(const DistillArgs &a) {
-  const unsigned grid = static_cast<unsigned>(a.n);
-  if (a.dtype == 0) distill_kernel<float><<<grid, kDistillThreads, 0, a.stream>>>(a);
-  else if (a.dtype == 1) distill_kernel<__half><<<grid, kDistillThreads, 0, a.stream>>>(a);
-  else distill_kernel<__nv_bfloat16><<<grid, kDistillThreads, 0, a.stream>>>(a);
-  return cudaGetLastError();
+  if (a.dtype == 0) return launch_distill_t<float>(a);
+  if (a.dtype == 1) return launch_distill_t<__half>(a);
+  return launch_distill_t<__nv_bfloat16>(a);
 }
 
 }  // namespace muse

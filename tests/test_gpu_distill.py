@@ -119,7 +119,8 @@ def _case(torch, n, v, top, dtype, pad=0, offset=0, seed=0, dup=False):
 @pytest.mark.parametrize("n,v,top,pad,offset,temperature", [
     (1, 2, 1, 0, 0, 1.0), (3, 5, 4, 1, 1, 0.5), (2, 7, 64, 0, 0, 1.0), (4, 257, 3, 2, 3, 1.0), (33, 1000, 20, 0, 0, 2.0),
     (5, 2048, 64, 0, 0, 1.0), (7, 4099, 16, 1, 1, 1.0), (3, 32003, 16, 0, 0, 1.0), (2, 50257, 33, 3, 2, 2.0),
-    (170, 6007, 5, 0, 0, 1.0), (2, 202048, 32, 0, 0, 1.0), (1, 202048, 64, 0, 0, 2.0), (1, 260003, 8, 0, 0, 1.0)])
+    (170, 6007, 5, 0, 0, 1.0), (2, 202048, 32, 0, 0, 1.0), (1, 202048, 64, 0, 0, 2.0), (1, 260003, 8, 0, 0, 1.0),
+    (2, 500001, 20, 1, 1, 1.0), (2, 2000003, 20, 0, 0, 1.0)])
 def test_distill_shapes(torch_cuda, dtype, tail, n, v, top, pad, offset, temperature):
     import q5_lm_head_gb300 as mlh
     torch = torch_cuda
