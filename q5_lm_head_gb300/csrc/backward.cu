@@ -7,102 +7,692 @@
 // and with the norm, r = 1/sqrt(mean h^2 + eps), xh = h r, gg = gx gamma:
 //     gh = r (gg - xh mean(gg xh)),   ggamma = sum_b gx xh
 //
-// Two launches: partial sums over a share of the rows of W for one block column
-// (256 inputs), then their sum in a fixed order with the norm's backward.
+// Bound: HBM (the matrix is read once), and close to it the unpacking of the
+// quants by the CUDA cores.  The contraction runs along the rows v of W, across
+// the direction in which its blocks are packed, so the tensor cores' A operand is
+// W transposed: a lane of tensor memory is an input k, a column a pair of rows.
+//
+// Launches:
+// 1. gmax_kernel: the largest |gl| of parts of each row, for a power of two that
+//    brings a row's t into f16's range.
+// 2. backward_tc_kernel: a CTA takes two block columns (512 inputs) and a share
+//    of the rows, 64 rows a stage.
+//    * weight producer warp: a 2-D TMA box of 64 rows x two blocks a stage.
+//    * operand warps: read the blocks' d, dmin and scales.  With d = md 2^e,
+//      1 <= |md| < 2, the power of two goes to the A side (A = sc q 2^e, at most
+//      11 significant bits: exact in f16) and md to the B side: B = t md as the
+//      f16 pair (hi, lo), hi + lo = t md to 2^-22, rows of B side by side.  The
+//      mins are a product of their own, A' = m 2^e' for the 16 sub-blocks,
+//      B' = -t mdmin.
+//    * four unpack warpgroups, two for each block, alternating between units of
+//      16 or 32 rows: ldmatrix with transposition gives a thread four rows of
+//      one input, and tcgen05.st (16 lanes x 256 bits) takes exactly that
+//      fragment. 
+//    * MMA warp: per 16 rows four products of M = 128 (two nibble halves of two
+//      blocks) and two for the mins.  The tensor cores round their sums towards
+//      zero, about 2^-24 a step, which over a share's thousand steps would cost
+//      1e-4: every 128 rows the unpack warps add the accumulators to f32 sums of
+//      their own (two sets of accumulators, so that nobody waits).
+//    The shares' sums go to the workspace.
+// 3. finish_kernel: a cluster of CTAs a batch row adds the shares in their
+//    order, undoes the power of two and does the norm's backward.
+// 4. gamma_kernel (more than one batch row, gamma's gradient wanted).
+//
+// A block with |d| or |dmin| of 4 and more (weights in the thousands) would take
+// B out of f16's range: the operand warps then set a flag and finish_kernel sums
+// in f32 from the blocks themselves.
+#include <atomic>
+#include <cmath>
+#include <cuda.h>
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "internal.h"
+#include "ptx.cuh"
+#include "rows.cuh"
+#include "tc.cuh"
 
 namespace muse {
 namespace {
 
-constexpr int kTileB = 8;        // batch rows a CTA holds sums of
-constexpr int kShareRows = 64;   // rows of W whose t_v are staged at once
+constexpr int kStageRows = 64;
+constexpr int kMaxParts = 32;                 // of a row's largest |gl|
+constexpr int kTileCols = 2 * kBlockWeights;  // inputs of a CTA
+constexpr int kFlushStages = 2;               // between additions of the accumulators to the f32 sums
+constexpr int kUnpackWarps = 16;
+constexpr uint32_t kTmem = 512;
 
+// ---------------------------------------------------------------- operands' scale
+// t 2^-e with e = exponent of the row's largest |gl| (0 for a row of zeros); the
+// scale's mantissa in [2^11, 2^12) is applied by the host: |t| < 2^13.
+__device__ __forceinline__ int row_exponent(const float *gmax, int b, int parts) {
+  float m = 0.0f;
+  for (int i = 0; i < parts; ++i) m = fmaxf(m, gmax[b * kMaxParts + i]);
+  const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
+  return m == 0.0f ? 0 : e < -126 ? -126 : e;   // 128 for infinities: they stay what they are
+}
+__device__ __forceinline__ float pow2(int e) {   // -126 <= e <= 127
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+__device__ __forceinline__ float cap_slope(float l, float cap, float inv_cap2) { return (cap - l) * (cap + l) * inv_cap2; }
+
+__global__ void __launch_bounds__(256) gmax_kernel(const float *__restrict__ g, int64_t n, float *__restrict__ gmax,
+                                                   uint32_t *flag) {
+  __shared__ float s_max[8];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const float *row = g + blockIdx.y * n;
+  const int64_t lo = n * blockIdx.x / gridDim.x, hi = n * (blockIdx.x + 1) / gridDim.x;
+  float m = 0.0f;
+#pragma unroll 8
+  for (int64_t i = lo + threadIdx.x; i < hi; i += 256) m = fmaxf(m, fabsf(row[i]));
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, s_max[i]);
+    gmax[blockIdx.y * kMaxParts + blockIdx.x] = m;
+    if (blockIdx.x == 0 && blockIdx.y == 0) *flag = 0u;
+  }
+}
+
+// ---------------------------------------------------------------- main kernel
+template <int NM, bool kQ4>
+struct BwdCfg {
+  static constexpr int kBB = kQ4 ? kBlockBytesQ4 : kBlockBytes;
+  static constexpr int kRowBytes = 2 * kBB;
+  static constexpr int kWBytes = kStageRows * kRowBytes;
+  static constexpr int kN = 2 * NM;                               // B rows: hi, lo
+  // Accumulator columns: with 8 slots hi and lo side by side (an MMA has 16
+  // columns at least), else both into the same ones.
+  static constexpr int kD = NM == 8 ? 16 : NM;
+  static constexpr int kBTile = kN * kStageRows * 2;              // f16 [kN][64], K-major
+  static constexpr int kScl = 16 * kStageRows * 2;                // f16 [2 blocks x 8][64]
+  static constexpr int kSlot = 4 * kBTile + 2 * kScl;             // B of d, B' of dmin (two blocks each); scales; mins
+  // Groups of four operand warps, taking the stages in turn.  One with 32
+  // slots: its unpack threads need the registers for 32 sums.
+  static constexpr int kGroups = NM == 32 ? 1 : 2;
+  static constexpr int kSlots = NM == 32 ? 3 : 4;
+  static constexpr int kPrepWarps = 4 * kGroups;
+  static constexpr int kThreads = 32 * (kUnpackWarps + kPrepWarps + 2);
+  static constexpr int kTStride = kStageRows + 4;                 // floats: 16-byte loads of eight rows on all banks
+  static constexpr int kT = NM * kTStride * 4 + 4 * kStageRows * 4;   // a group's t [NM][64], mantissas [4][64]
+  static constexpr int kFixed = kSlots * kSlot + kGroups * kT + 1024;
+  static constexpr int kWFit = (226 * 1024 - kFixed) / kWBytes;
+  static constexpr int kWStages = kWFit > 6 ? 6 : kWFit;
+  static_assert(kWStages >= 3, "weight ring");
+  static constexpr int kSmem = kWStages * kWBytes + kFixed;
+  // tensor memory: two sets of sums of four M-tiles and two min products, then a ring of units of US x 16 rows
+  static constexpr int kUS = NM == 32 ? 1 : 2;
+  static constexpr int kUnits = kStageRows / (16 * kUS);          // units a stage
+  static constexpr int kSlab = 40;                                // columns of 16 rows: four M-tiles of 8, mins 8
+  static constexpr int kABase = 12 * kD;
+  static constexpr int kBufs = (512 - kABase) / (kSlab * kUS) > 4 ? 4 : (512 - kABase) / (kSlab * kUS);
+  static_assert(kBufs >= 2, "unit ring");
+  static constexpr uint32_t kIdesc = tc::idesc_f16_f32(128, kD);
+};
+
+__device__ __forceinline__ void st_16x256b(uint32_t ta, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1, %2, %3, %4};" ::"r"(ta), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// Two 16 x 16 byte matrices (rows at the addresses of lanes 0-15 and 16-31),
+// transposed: lane t gets, in order, bytes t/4, t/4 + 8 of the first matrix's
+// rows 4 (t%4) .. +3, and of the second's.
+__device__ __forceinline__ void load_transposed(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+constexpr uint32_t kNeg1024 = 0xE400E400u;   // f16 pair (-1024, -1024)
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void tma_box(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(ptx::smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(ptx::smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// d (an f16 value) as md 2^e with -23 <= e <= 0: 1 <= |md| < 2 apart from 0 and
+// the smallest subnormal, up to 4 where d is from 2 to 4; *big for more.
+__device__ __forceinline__ float split_d(float d, int &e, bool &big) {
+  const uint32_t bits = __float_as_uint(d);
+  const int ex = static_cast<int>((bits >> 23) & 255) - 127;      // of the f16 value: -24 .. 15, -127 for 0
+  big |= ex > 1;                                                  // infinities and NaN too
+  e = ex > 0 ? 0 : ex < -23 ? -23 : ex;
+  return d * pow2(-e);
+}
+
+template <int NM, bool kQ4>
+__global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
+    backward_tc_kernel(const __grid_constant__ CUtensorMap wmap, const BackwardArgs a, float scale_m, int gparts,
+                       int pairs, int splits) {
+  using C = BwdCfg<NM, kQ4>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *wst = smem;                                            // [kWStages][64][kRowBytes]
+  uint8_t *slots = smem + C::kWStages * C::kWBytes;               // [kSlots][kSlot]
+  float *s_t = reinterpret_cast<float *>(slots + C::kSlots * C::kSlot);   // [NM][kTStride]
+  uint64_t *bars = reinterpret_cast<uint64_t *>(slots + C::kSlots * C::kSlot + C::kGroups * C::kT);
+  uint64_t *wfull = bars, *wempty = wfull + C::kWStages;
+  uint64_t *pfull = wempty + C::kWStages, *pempty = pfull + C::kSlots;
+  uint64_t *tfull = pempty + C::kSlots, *tempty = tfull + C::kBufs;
+  uint64_t *dfull = tempty + C::kBufs, *dfree = dfull + 2, *done = dfree + 2;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(done + 1);
+  volatile uint32_t *s_abort = s_tmem + 1;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int pair = blockIdx.x % pairs, split = blockIdx.x / pairs;   // neighbours stream the same rows
+  const int64_t stages = (a.n_rows + kStageRows - 1) / kStageRows;
+  const int64_t st0 = stages * split / splits;
+  const int n_st = static_cast<int>(stages * (split + 1) / splits - st0);
+  constexpr int kPrepThreads = 128;                               // of a group
+  constexpr int kMmaWarp = kUnpackWarps + C::kPrepWarps, kTmaWarp = kMmaWarp + 1;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kWStages; ++i) {
+      ptx::mbar_init(&wfull[i], 1);
+      ptx::mbar_init(&wempty[i], kUnpackWarps + 4);
+    }
+    for (int i = 0; i < C::kSlots; ++i) {
+      ptx::mbar_init(&pfull[i], 4);
+      ptx::mbar_init(&pempty[i], kUnpackWarps + 1);               // the scales' readers, the MMAs
+    }
+    for (int i = 0; i < C::kBufs; ++i) {
+      ptx::mbar_init(&tfull[i], kUnpackWarps / 2);
+      ptx::mbar_init(&tempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&dfull[i], 1);
+      ptx::mbar_init(&dfree[i], kUnpackWarps);
+    }
+    ptx::mbar_init(done, 1);
+    *s_abort = 0u;
+    ptx::fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tc::alloc(s_tmem, kTmem);
+    tc::relinquish();
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tbase = *s_tmem;
+  auto fail = [&]() {
+    atomicOr(a.status, kStatusWaitTimeout);
+    *s_abort = 1u;
+  };
+  auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity)) != 0; };
+
+  if (warp == kTmaWarp) {
+    // ------------------------------------------------------------ weights
+    if (lane == 0) {
+      const uint64_t policy = ptx::policy_evict_first();
+      int issued = 0, ws = 0;
+      uint32_t ph = 0;
+      for (int i = 0; i < n_st && !*s_abort; ++i) {
+        if (i >= C::kWStages && !ptx::mbar_wait(&wempty[ws], ph ^ 1u)) { fail(); break; }
+        ptx::mbar_arrive_expect_tx(&wfull[ws], C::kWBytes);
+        tma_box(wst + ws * C::kWBytes, &wmap, pair * (C::kRowBytes / 4), static_cast<int>((st0 + i) * kStageRows), &wfull[ws],
+                policy);
+        issued = i + 1;
+        if (++ws == C::kWStages) { ws = 0; ph ^= 1u; }
+      }
+      // never leave copies in flight
+      for (int i = issued > C::kWStages ? issued - C::kWStages : 0; i < issued; ++i)
+        ptx::mbar_wait(&wfull[i % C::kWStages], static_cast<uint32_t>((i / C::kWStages) & 1));
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ products
+    const bool issuer = tc::elect_one();
+    bool ok = true;
+    int slot = 0, buf = 0;
+    uint32_t pph = 0, tph = 0;
+    for (int i = 0; i < n_st && ok; ++i) {
+      if (__any_sync(0xffffffffu, *s_abort != 0u)) break;
+      const int period = i / kFlushStages, db = period & 1;
+      const bool opens = i % kFlushStages == 0;
+      if (opens && period >= 2 && !(ok = wait(&dfree[db], ((period >> 1) & 1) ^ 1))) break;
+      if (!(ok = wait(&pfull[slot], pph))) break;
+      const uint32_t b0 = ptx::smem_u32(slots + slot * C::kSlot);
+      const uint32_t dbase = tbase + db * 6 * C::kD;
+      for (int u = 0; u < C::kUnits; ++u) {
+        if (!(ok = wait(&tfull[buf], tph))) break;
+        tc::fence_after();
+        if (issuer) {
+#pragma unroll
+          for (int s = 0; s < C::kUS; ++s) {
+            const uint32_t at = tbase + C::kABase + (buf * C::kUS + s) * C::kSlab;
+            const uint32_t kofs = static_cast<uint32_t>((u * C::kUS + s) * 2 * (C::kN / 8) * 128);
+            const bool acc = !opens || u > 0 || s > 0;
+#pragma unroll
+            for (int mt = 0; mt < 6; ++mt) {                      // four M-tiles, then the mins of both blocks
+              const int kind = mt < 4 ? mt >> 1 : mt - 2;
+              const uint32_t d = dbase + mt * C::kD, ta = at + (mt < 4 ? mt : 4) * 8;
+              const uint32_t tile = b0 + kind * C::kBTile + kofs;
+              tc::mma_f16_tmemA(d, ta, tc::smem_desc_kmajor(tile, C::kN * 16, 128), C::kIdesc, acc);
+              if (NM > 8)
+                tc::mma_f16_tmemA(d, ta, tc::smem_desc_kmajor(tile + (NM / 8) * 128, C::kN * 16, 128), C::kIdesc, true);
+            }
+          }
+          tc::commit(&tempty[buf]);
+        }
+        __syncwarp();
+        if (++buf == C::kBufs) { buf = 0; tph ^= 1u; }
+      }
+      if (!ok) break;
+      if (issuer) {
+        tc::commit(&pempty[slot]);
+        if ((i + 1) % kFlushStages == 0 || i + 1 == n_st) tc::commit(&dfull[db]);
+      }
+      __syncwarp();
+      if (++slot == C::kSlots) { slot = 0; pph ^= 1u; }
+    }
+    if (!ok && lane == 0) fail();
+    // the sums are read, and tensor memory freed, only after every MMA issued here completed
+    if (issuer) tc::commit(done);
+    __syncwarp();
+    if (!wait(done, 0) && lane == 0) fail();
+  } else if (warp >= kUnpackWarps) {
+    // ------------------------------------------------------------ operands
+    const int grp = (warp - kUnpackWarps) >> 2;                   // takes the stages grp, grp + kGroups, ..
+    const int pt = tid - 32 * kUnpackWarps - kPrepThreads * grp;
+    float *s_tg = s_t + grp * (C::kT / 4), *s_md = s_tg + NM * C::kTStride;
+    constexpr int kEach = NM * kStageRows / kPrepThreads;         // t values of a thread and stage
+    asm volatile("griddepcontrol.wait;" ::: "memory");            // the rows' largest values
+    const float inv_cap2 = a.cap > 0.0f ? 1.0f / (a.cap * a.cap) : 0.0f;
+    constexpr int kStepB = kPrepThreads / kStageRows;             // batch rows between a thread's values
+    const int tb = pt / kStageRows, tv = pt % kStageRows;
+    float g[kEach], l[kEach], e2[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int b = tb + j * kStepB;
+      e2[j] = b < a.batch ? pow2(-min(row_exponent(a.gmax, b, gparts), 126)) : 0.0f;
+    }
+    auto fetch = [&](int i) {
+      const int64_t v = (st0 + i) * kStageRows + tv;
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const int b = tb + j * kStepB;
+        const bool in = b < a.batch && v < a.n_rows && i < n_st;
+        const int64_t at = static_cast<int64_t>(b) * a.n_rows + v;
+        g[j] = in ? __ldg(a.grad_logits + at) : 0.0f;
+        l[j] = in && a.cap > 0.0f ? __ldg(a.logits + at) : 0.0f;
+      }
+    };
+    fetch(grp);
+    bool bad = false, big = false;
+    for (int i = grp; i < n_st; i += C::kGroups) {
+      const int ws = i % C::kWStages, slot = i % C::kSlots;
+      const uint32_t wph = (i / C::kWStages) & 1, pph = (i / C::kSlots) & 1;
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        float t = g[j] * e2[j] * scale_m;
+        if (a.cap > 0.0f) t *= cap_slope(l[j], a.cap, inv_cap2);
+        s_tg[(tb + j * kStepB) * C::kTStride + tv] = t;
+      }
+      fetch(i + C::kGroups);
+      bad = __any_sync(0xffffffffu, *s_abort != 0u) != 0;
+      if (!bad && i >= C::kSlots) bad = !wait(&pempty[slot], pph ^ 1u);
+      if (!bad) bad = !wait(&wfull[ws], wph);
+      uint8_t *sl = slots + slot * C::kSlot;
+      if (!bad) {
+        // one block's header: powers of two with its scales and mins, mantissas for B
+        const int blk = pt / kStageRows;
+        const uint4 hdr = *reinterpret_cast<const uint4 *>(wst + ws * C::kWBytes + tv * C::kRowBytes + blk * C::kBB);
+        const float2 dd = __half22float2(*reinterpret_cast<const __half2 *>(&hdr.x));
+        int ed, em;
+        s_md[blk * kStageRows + tv] = split_d(dd.x, ed, big);
+        s_md[(2 + blk) * kStageRows + tv] = -split_d(dd.y, em, big);
+        const uint32_t pd = pack_half2(pow2(ed), 0.5f * pow2(ed));   // even sub-blocks' scale, odd ones' halved
+        const uint32_t pm = pack_half2(pow2(em), pow2(em));
+        const uint32_t sc[2] = {hdr.y & 0x3F3F3F3Fu, (hdr.w & 0x0F0F0F0Fu) | ((hdr.y >> 2) & 0x30303030u)};
+        const uint32_t mn[2] = {hdr.z & 0x3F3F3F3Fu, ((hdr.w >> 4) & 0x0F0F0F0Fu) | ((hdr.z >> 2) & 0x30303030u)};
+        __half *scl = reinterpret_cast<__half *>(sl + 4 * C::kBTile) + blk * 8 * kStageRows + tv;
+        __half *mns = scl + 16 * kStageRows;
+        const uint32_t one = 0x3C003C00u;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {                             // sub-blocks 2h, 2h + 1
+          const uint32_t sel = h & 1 ? 0x4342u : 0x4140u;
+          const uint32_t s = hmul2(hfma2(__byte_perm(sc[h >> 1], 0x64u, sel), one, kNeg1024), pd);
+          const uint32_t m = hmul2(hfma2(__byte_perm(mn[h >> 1], 0x64u, sel), one, kNeg1024), pm);
+          scl[(2 * h) * kStageRows] = __ushort_as_half(static_cast<unsigned short>(s));
+          scl[(2 * h + 1) * kStageRows] = __ushort_as_half(static_cast<unsigned short>(s >> 16));
+          mns[(2 * h) * kStageRows] = __ushort_as_half(static_cast<unsigned short>(m));
+          mns[(2 * h + 1) * kStageRows] = __ushort_as_half(static_cast<unsigned short>(m >> 16));
+        }
+      }
+      if (ptx::named_bar_red_or(1 + grp, kPrepThreads, bad)) {
+        bad = true;
+        break;
+      }
+      if (lane == 0) ptx::mbar_arrive(&wempty[ws]);
+      // B tiles: eight rows of one batch row as hi and lo, for d and dmin of both blocks
+      constexpr int kTasks = NM * 8, kShare = kTasks < kPrepThreads ? kPrepThreads / kTasks : 1;   // threads a task
+      static_assert(4 % kShare == 0, "kinds a thread");
+#pragma unroll
+      for (int q = pt; q < kTasks * kShare; q += kPrepThreads) {
+        const int b = q % NM, oct = q / NM % 8, part = q / kTasks;
+        const float4 t0 = *reinterpret_cast<const float4 *>(s_tg + b * C::kTStride + 8 * oct);
+        const float4 t1 = *reinterpret_cast<const float4 *>(s_tg + b * C::kTStride + 8 * oct + 4);
+        const float t[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+#pragma unroll
+        for (int kk = 0; kk < 4 / kShare; ++kk) {
+          const int kind = part * (4 / kShare) + kk;
+          const float4 m0 = *reinterpret_cast<const float4 *>(s_md + kind * kStageRows + 8 * oct);
+          const float4 m1 = *reinterpret_cast<const float4 *>(s_md + kind * kStageRows + 8 * oct + 4);
+          const float md[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const float x0 = t[2 * p] * md[2 * p], x1 = t[2 * p + 1] * md[2 * p + 1];
+            hi[p] = pack_half2(x0, x1);
+            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi[p]));
+            lo[p] = pack_half2(x0 - h.x, x1 - h.y);
+          }
+          uint8_t *tile = sl + kind * C::kBTile + oct * (C::kN / 8) * 128 + (b & 7) * 16;
+          *reinterpret_cast<uint4 *>(tile + (b >> 3) * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4 *>(tile + ((NM + b) >> 3) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the tiles, to the tensor cores' reads
+      ptx::named_bar_sync(1 + grp, kPrepThreads);                 // t and mantissas are read
+      if (lane == 0) ptx::mbar_arrive(&pfull[slot]);
+    }
+    if (bad && lane == 0) fail();
+    if (big) atomicOr(a.flag, 1u);
+  } else {
+    // ------------------------------------------------------------ unpacking
+    const int blk = (warp >> 2) & 1, par = warp >> 3, wq = warp & 3;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * wq) << 16;
+    const uint32_t rot = static_cast<uint32_t>(4 - 2 * wq) & 31u;   // high bit 2wq -> 4, 2wq + 1 -> 5
+    const uint32_t src0 = ptx::smem_u32(wst) + (lane & 15) * C::kRowBytes + blk * C::kBB + 16 * (lane >> 4);
+    // the f32 sums: inputs of M-tile warp/4 by batch row, and mins (lane: sub-block) of eight batch rows
+    const int mt = warp >> 2;
+    const bool min_warp = wq == 0 && mt < NM / 8;
+    unsigned long long sum[NM / 2], msum[4];    // pairs of batch rows
+#pragma unroll
+    for (int j = 0; j < NM / 2; ++j) sum[j] = 0ull;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) msum[j] = 0ull;
+    int flushed = 0;
+    auto flush = [&]() {
+      const int db = flushed & 1;
+      if (!wait(&dfull[db], (flushed >> 1) & 1)) return false;
+      tc::fence_after();
+      const uint32_t d = tbase + db * 6 * C::kD;
+#pragma unroll
+      for (int c0 = 0; c0 < C::kD; c0 += 16) {
+        uint32_t x[16];
+        tc::ld_32x32b_x16(d + lane_base + mt * C::kD + c0, x);
+        tc::wait_ld();
+        auto two = [&](int j) { return pack2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])); };
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if constexpr (NM == 8) sum[j & 3] = add2(sum[j & 3], two(2 * j));   // hi, then lo
+          else sum[c0 / 2 + j] = add2(sum[c0 / 2 + j], two(2 * j));
+        }
+      }
+      if (min_warp) {
+#pragma unroll
+        for (int h = 0; h < (NM == 8 ? 2 : 1); ++h) {
+          uint32_t x[8], y[8];
+          tc::ld_32x32b_x8(d + 4 * C::kD + 8 * (NM == 8 ? h : mt), x);
+          tc::ld_32x32b_x8(d + 5 * C::kD + 8 * (NM == 8 ? h : mt), y);
+          tc::wait_ld();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            msum[j] = add2(msum[j], pack2(__uint_as_float(lane < 8 ? x[2 * j] : y[2 * j]),
+                                          __uint_as_float(lane < 8 ? x[2 * j + 1] : y[2 * j + 1])));
+        }
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&dfree[db]);
+      ++flushed;
+      return true;
+    };
+    bool ok = true;
+    int ws = 0, slot = 0, unit = par;           // unit: of the whole share; its buffer is unit % kBufs
+    int buf = par;
+    uint32_t wph = 0, pph = 0, tph = 0;
+    for (int i = 0; i < n_st && ok; ++i) {
+      if (__any_sync(0xffffffffu, *s_abort != 0u)) { ok = false; break; }
+      if (!(ok = wait(&wfull[ws], wph))) break;
+      if (!(ok = wait(&pfull[slot], pph))) break;
+      const uint8_t *sl = slots + slot * C::kSlot;
+      const __half *scl = reinterpret_cast<const __half *>(sl + 4 * C::kBTile) + (blk * 8 + 2 * wq) * kStageRows + 4 * (lane & 3);
+      const __half *mns = reinterpret_cast<const __half *>(sl + 4 * C::kBTile) + (16 + (lane >> 2)) * kStageRows + 4 * (lane & 3);
+      for (int u = par; u < C::kUnits; u += 2) {
+        if (unit >= C::kBufs && !(ok = wait(&tempty[buf], tph ^ 1u))) break;
+        tc::fence_after();
+#pragma unroll
+        for (int s = 0; s < C::kUS; ++s) {
+          const int slab = u * C::kUS + s;
+          const uint32_t src = src0 + ws * C::kWBytes + slab * 16 * C::kRowBytes;
+          uint32_t q[4], h[4];
+          load_transposed(src + (kQ4 ? kOffQsQ4 : kOffQs) + 32 * wq, q);
+          if constexpr (!kQ4) load_transposed(src + kOffQh, h);
+          const uint2 k0 = *reinterpret_cast<const uint2 *>(scl + 16 * slab);                 // low nibbles' scales
+          const uint2 k1 = *reinterpret_cast<const uint2 *>(scl + kStageRows + 16 * slab);    // high ones', halved
+          const uint32_t a00 = hmul2(k0.x, kNeg1024), a01 = hmul2(k0.y, kNeg1024);
+          const uint32_t a10 = hmul2(k1.x, kNeg1024), a11 = hmul2(k1.y, kNeg1024);
+          uint32_t lo[8], hi[8];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            uint32_t ql = q[r] & 0x0F0F0F0Fu, qh = (q[r] >> 3) & 0x1E1E1E1Eu;   // q, and twice q
+            if constexpr (!kQ4) {
+              const uint32_t hr = __funnelshift_l(h[r], h[r], rot);
+              ql |= hr & 0x10101010u;
+              qh |= hr & 0x20202020u;
+            }
+            lo[2 * r] = hfma2(__byte_perm(ql, 0x64u, 0x4140u), k0.x, a00);      // (1024 + q) s - 1024 s, exact
+            lo[2 * r + 1] = hfma2(__byte_perm(ql, 0x64u, 0x4342u), k0.y, a01);
+            hi[2 * r] = hfma2(__byte_perm(qh, 0x64u, 0x4140u), k1.x, a10);
+            hi[2 * r + 1] = hfma2(__byte_perm(qh, 0x64u, 0x4342u), k1.y, a11);
+          }
+          const uint32_t at = tbase + lane_base + C::kABase + (buf * C::kUS + s) * C::kSlab + 16 * blk;
+          st_16x256b(at, lo[0], lo[1], lo[2], lo[3]);
+          st_16x256b(at + (16u << 16), lo[4], lo[5], lo[6], lo[7]);
+          st_16x256b(at + 8, hi[0], hi[1], hi[2], hi[3]);
+          st_16x256b(at + 8 + (16u << 16), hi[4], hi[5], hi[6], hi[7]);
+          if (blk == 0 && wq == 0) {                              // the mins of both blocks: lanes 0-7 and 8-15
+            const uint2 m0 = *reinterpret_cast<const uint2 *>(mns + 16 * slab);
+            const uint2 m1 = *reinterpret_cast<const uint2 *>(mns + 8 * kStageRows + 16 * slab);
+            st_16x256b(at + 32, m0.x, m0.y, m1.x, m1.y);
+          }
+        }
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&tfull[buf]);
+        unit += 2;
+        if ((buf += 2) >= C::kBufs) {
+          buf -= C::kBufs;
+          tph ^= 1u;
+        }
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(&wempty[ws]);
+        ptx::mbar_arrive(&pempty[slot]);
+      }
+      if (++ws == C::kWStages) { ws = 0; wph ^= 1u; }
+      if (++slot == C::kSlots) { slot = 0; pph ^= 1u; }
+      // the accumulators before the ones now in use
+      if ((i + 1) % kFlushStages == 0 && i + 1 > kFlushStages) ok = flush();
+    }
+    while (ok && flushed < (n_st + kFlushStages - 1) / kFlushStages) ok = flush();
+    if (!ok && lane == 0) fail();
+    float *s_min = s_t;                         // [16 sub-blocks][NM]: every stage's t has been read
+    if (min_warp && ok && lane < 16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = unpack2(msum[j]);
+        s_min[lane * NM + 8 * mt + 2 * j] = x.x;
+        s_min[lane * NM + 8 * mt + 2 * j + 1] = x.y;
+      }
+    }
+    ptx::named_bar_sync(1 + C::kGroups, 32 * kUnpackWarps);
+    const int kc = pair * kTileCols + (mt >> 1) * kBlockWeights + 64 * wq + 32 * (mt & 1) + lane;
+    if (ok && kc < a.k) {
+      const float *mins = s_min + ((mt >> 1) * 8 + 2 * wq + (mt & 1)) * NM;
+      float *out = a.part + static_cast<int64_t>(split) * a.batch * a.k + kc;
+#pragma unroll
+      for (int b = 0; b < NM; b += 2) {
+        const float2 x = unpack2(sum[b / 2]);
+        if (b < a.batch) out[static_cast<int64_t>(b) * a.k] = x.x + mins[b];
+        if (b + 1 < a.batch) out[static_cast<int64_t>(b + 1) * a.k] = x.y + mins[b + 1];
+      }
+    }
+    tc::fence_before();
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after();
+    tc::dealloc(tbase, kTmem);
+  }
+}
+
+// ---------------------------------------------------------------- shares' sum and norm
+constexpr int kFinishThreads = 256;
+
+// gx of batch row b at column j from the blocks themselves, in f32.
 template <bool kQ4>
-__global__ void __launch_bounds__(256) backward_kernel(const BackwardArgs a) {
+__device__ float plain_sum(const BackwardArgs &a, int b, int j) {
   constexpr int kBB = kQ4 ? kBlockBytesQ4 : kBlockBytes;
   constexpr int kQs = kQ4 ? kOffQsQ4 : kOffQs;
-  __shared__ float s_t[kShareRows][kTileB];
-  const int nb = a.k / kBlockWeights;
-  const int kb = blockIdx.x, part = blockIdx.y, b0 = blockIdx.z * kTileB;
-  const int64_t lo = a.n_rows * part / gridDim.y, hi = a.n_rows * (part + 1) / gridDim.y;
-  const int e = threadIdx.x, s = e >> 5, l = e & 31;
-  float acc[kTileB] = {};
-  for (int64_t v0 = lo; v0 < hi; v0 += kShareRows) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kShareRows * kTileB; i += 256) {
-      const int b = i / kShareRows;
-      const int64_t v = v0 + i % kShareRows;
-      float t = 0.0f;
-      if (v < hi && b0 + b < a.batch) {
-        const int64_t at = static_cast<int64_t>(b0 + b) * a.n_rows + v;
-        t = a.grad_logits[at] * a.scale;
-        if (a.cap > 0.0f) t *= (a.cap - a.logits[at]) * (a.cap + a.logits[at]) / (a.cap * a.cap);
-      }
-      s_t[i % kShareRows][b] = t;
-    }
-    __syncthreads();
-    for (int64_t v = v0; v < hi && v < v0 + kShareRows; ++v) {
-      const uint8_t *blk = a.w + (v * nb + kb) * kBB;
+  const int kb = j / kBlockWeights, s = j % kBlockWeights / 32, l = j % 32;
+  float sum = 0.0f;
+  for (int64_t v0 = 0; v0 < a.n_rows; v0 += 512) {                // sums of 512, then of those: a short chain
+    float part = 0.0f;
+    for (int64_t v = v0; v < v0 + 512 && v < a.n_rows; ++v) {
+      const int64_t at = static_cast<int64_t>(b) * a.n_rows + v;
+      float t = a.grad_logits[at] * a.scale;
+      if (a.cap > 0.0f) t *= cap_slope(a.logits[at], a.cap, 1.0f / (a.cap * a.cap));
+      const uint8_t *blk = a.w + (v * (a.k / kBlockWeights) + kb) * kBB;
       const uint4 hdr = __ldg(reinterpret_cast<const uint4 *>(blk));
-      const float d = __half2float(__ushort_as_half(static_cast<unsigned short>(hdr.x & 0xFFFFu)));
-      const float dmin = __half2float(__ushort_as_half(static_cast<unsigned short>(hdr.x >> 16)));
+      const float2 dd = __half22float2(*reinterpret_cast<const __half2 *>(&hdr.x));
       int sc, mn;
       q5k_scale_min(hdr.y, hdr.z, hdr.w, s, sc, mn);
       int q = (blk[kQs + 32 * (s >> 1) + l] >> (4 * (s & 1))) & 15;
       if (!kQ4) q |= ((blk[kOffQh + l] >> s) & 1) << 4;
-      const float w = fmaf(d * static_cast<float>(sc), static_cast<float>(q), -dmin * static_cast<float>(mn));
-      for (int b = 0; b < kTileB; ++b) acc[b] = fmaf(s_t[v - v0][b], w, acc[b]);
+      part = fmaf(t, fmaf(dd.x * static_cast<float>(sc), static_cast<float>(q), -dd.y * static_cast<float>(mn)), part);
     }
+    sum += part;
   }
-  for (int b = 0; b < kTileB && b0 + b < a.batch; ++b)
-    a.part[(static_cast<int64_t>(part) * a.batch + b0 + b) * a.k + kb * kBlockWeights + e] = acc[b];
+  return sum;
 }
 
-// One CTA per batch row: gx = the parts' sum in order, then the norm's backward.
-// gx stays in the first part's place for the gamma gradient.
-__global__ void __launch_bounds__(256) backward_norm_kernel(const BackwardArgs a, int parts) {
-  __shared__ float s_red[2][8];
-  const int b = blockIdx.x;
+__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const BackwardArgs a, int splits, int gparts, int scale_e) {
+  __shared__ float s_red[2][kFinishThreads / 32];
+  __shared__ float s_from[2][16];
+  const int tid = threadIdx.x;
+  const uint32_t cr = cluster_rank(), cs = cluster_size();
+  const int b = blockIdx.x / cs;
+  const int lo = static_cast<int>(static_cast<int64_t>(a.k / 4) * cr / cs) * 4;
+  const int hi = static_cast<int>(static_cast<int64_t>(a.k / 4) * (cr + 1) / cs) * 4;
+  cluster_arrive();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const bool plain = *a.flag != 0u;
+  const double back = ldexp(1.0, min(row_exponent(a.gmax, b, gparts), 126) + scale_e);
   const int64_t stride = static_cast<int64_t>(a.batch) * a.k;
   float *gx = a.part + static_cast<int64_t>(b) * a.k;
-  const float *h = a.hidden + static_cast<int64_t>(b) * a.k;
+  const int64_t at = static_cast<int64_t>(b) * a.k;
   float ss = 0.0f, dot = 0.0f;
-  for (int j = threadIdx.x; j < a.k; j += 256) {
-    float v = 0.0f;
-    for (int p = 0; p < parts; ++p) v += gx[p * stride + j];
-    gx[j] = v;
-    if (a.gamma) {
-      ss = fmaf(h[j], h[j], ss);
-      dot = fmaf(v * a.gamma[j], h[j], dot);
+  for (int j = lo + 4 * tid; j < hi; j += 4 * kFinishThreads) {
+    float x[4] = {};
+    if (!plain) {
+      float4 s = *reinterpret_cast<const float4 *>(gx + j);
+      for (int p = 1; p < splits; ++p) {
+        const float4 o = *reinterpret_cast<const float4 *>(gx + p * stride + j);
+        s.x += o.x;
+        s.y += o.y;
+        s.z += o.z;
+        s.w += o.w;
+      }
+      x[0] = static_cast<float>(s.x * back);
+      x[1] = static_cast<float>(s.y * back);
+      x[2] = static_cast<float>(s.z * back);
+      x[3] = static_cast<float>(s.w * back);
     } else {
-      a.grad_hidden[static_cast<int64_t>(b) * a.k + j] = v;
+      for (int i = 0; i < 4; ++i) x[i] = a.q4 ? plain_sum<true>(a, b, j + i) : plain_sum<false>(a, b, j + i);
+    }
+    const float4 r = make_float4(x[0], x[1], x[2], x[3]);
+    if (!a.gamma) {
+      *reinterpret_cast<float4 *>(a.grad_hidden + at + j) = r;
+    } else {
+      *reinterpret_cast<float4 *>(gx + j) = r;                    // read again below, and for gamma
+      const float4 h = *reinterpret_cast<const float4 *>(a.hidden + at + j);
+      const float4 g = *reinterpret_cast<const float4 *>(a.gamma + j);
+      ss = fmaf(h.x, h.x, fmaf(h.y, h.y, fmaf(h.z, h.z, fmaf(h.w, h.w, ss))));
+      dot = fmaf(r.x * g.x, h.x, fmaf(r.y * g.y, h.y, fmaf(r.z * g.z, h.z, fmaf(r.w * g.w, h.w, dot))));
     }
   }
+  cluster_wait();                         // every CTA of the cluster has started
   if (!a.gamma) return;
   for (int o = 16; o > 0; o >>= 1) {
     ss += __shfl_xor_sync(0xffffffffu, ss, o);
     dot += __shfl_xor_sync(0xffffffffu, dot, o);
   }
-  if ((threadIdx.x & 31) == 0) {
-    s_red[0][threadIdx.x >> 5] = ss;
-    s_red[1][threadIdx.x >> 5] = dot;
+  if ((tid & 31) == 0) {
+    s_red[0][tid >> 5] = ss;
+    s_red[1][tid >> 5] = dot;
   }
   __syncthreads();
+  if (tid < static_cast<int>(cs)) {
+    ss = dot = 0.0f;
+    for (int i = 0; i < kFinishThreads / 32; ++i) {
+      ss += s_red[0][i];
+      dot += s_red[1][i];
+    }
+    peer_store32(peer_addr(&s_from[0][cr], tid), __float_as_uint(ss));
+    peer_store32(peer_addr(&s_from[1][cr], tid), __float_as_uint(dot));
+  }
+  cluster_sync();
   ss = dot = 0.0f;
-  for (int i = 0; i < 8; ++i) {
-    ss += s_red[0][i];
-    dot += s_red[1][i];
+  for (uint32_t i = 0; i < cs; ++i) {
+    ss += s_from[0][i];
+    dot += s_from[1][i];
   }
   const float r = 1.0f / sqrtf(ss / static_cast<float>(a.k) + a.eps);
   const float c = r * r * dot / static_cast<float>(a.k);
-  if (threadIdx.x == 0) a.rms[b] = r;
-  for (int j = threadIdx.x; j < a.k; j += 256)
-    a.grad_hidden[static_cast<int64_t>(b) * a.k + j] = r * (gx[j] * a.gamma[j] - h[j] * c);
+  if (cr == 0 && tid == 0) a.rms[b] = r;
+  for (int j = lo + 4 * tid; j < hi; j += 4 * kFinishThreads) {
+    const float4 x = *reinterpret_cast<const float4 *>(gx + j);
+    const float4 h = *reinterpret_cast<const float4 *>(a.hidden + at + j);
+    const float4 g = *reinterpret_cast<const float4 *>(a.gamma + j);
+    *reinterpret_cast<float4 *>(a.grad_hidden + at + j) = make_float4(
+        r * (x.x * g.x - h.x * c), r * (x.y * g.y - h.y * c), r * (x.z * g.z - h.z * c), r * (x.w * g.w - h.w * c));
+    if (a.grad_gamma && a.batch == 1)
+      *reinterpret_cast<float4 *>(a.grad_gamma + j) = make_float4(x.x * h.x * r, x.y * h.y * r, x.z * h.z * r, x.w * h.w * r);
+  }
 }
 
-__global__ void __launch_bounds__(256) backward_gamma_kernel(const BackwardArgs a) {
-  const int j = blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(128) gamma_kernel(const BackwardArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int j = blockIdx.x * 128 + threadIdx.x;
   float v = 0.0f;
   for (int b = 0; b < a.batch; ++b) {
     const int64_t at = static_cast<int64_t>(b) * a.k + j;
@@ -111,25 +701,90 @@ __global__ void __launch_bounds__(256) backward_gamma_kernel(const BackwardArgs 
   a.grad_gamma[j] = v;
 }
 
+// ---------------------------------------------------------------- host side
+int bwd_pairs(int k) { return (k / kBlockWeights + 1) / 2; }
+// As many shares of the rows as leave each SM one CTA.
+int bwd_splits(int64_t n_rows, int k, int num_sms) {
+  const int64_t stages = (n_rows + kStageRows - 1) / kStageRows;
+  int64_t s = num_sms / bwd_pairs(k);
+  if (s < 1) s = 1;
+  return static_cast<int>(s < stages ? s : stages);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                             A &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // may start before the previous grid ends
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<A &&>(args)...);
+}
+
+template <int NM, bool kQ4>
+cudaError_t launch_backward_nm(const BackwardArgs &a, const CUtensorMap &map, float scale_m, int gparts, int splits) {
+  using C = BwdCfg<NM, kQ4>;
+  static std::atomic<unsigned long long> configured{0};   // one bit per device; host threads may race here
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(configured.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(backward_tc_kernel<NM, kQ4>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  const int pairs = bwd_pairs(a.k);
+  return launch_dependent(backward_tc_kernel<NM, kQ4>, dim3(static_cast<unsigned>(pairs * splits)), C::kThreads, C::kSmem, 1,
+                          a.stream, map, a, scale_m, gparts, pairs, splits);
+}
+
 }  // namespace
 
-constexpr int kBackwardParts = 12;
-
-size_t backward_part_floats(int max_batch, int k) { return static_cast<size_t>(kBackwardParts) * max_batch * k; }
+size_t backward_part_floats(int64_t n_rows, int k, int max_batch, int num_sms) {
+  return static_cast<size_t>(bwd_splits(n_rows, k, num_sms)) * max_batch * k;
+}
+size_t backward_misc_floats() { return 32 * kMaxParts + 32 + 1; }   // largest |gl|, RMS factors, flag
 
 cudaError_t launch_backward(const BackwardArgs &a) {
-  const int nb = a.k / kBlockWeights;
-  const int parts = a.n_rows < kBackwardParts ? static_cast<int>(a.n_rows) : kBackwardParts;
-  const dim3 grid(nb, parts, (a.batch + kTileB - 1) / kTileB);
-  if (a.q4) backward_kernel<true><<<grid, 256, 0, a.stream>>>(a);
-  else backward_kernel<false><<<grid, 256, 0, a.stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  // the scale as scale_m 2^scale_e, 2^11 <= |scale_m| < 2^12
+  int scale_e = 0;
+  const float scale_m = std::ldexp(std::frexp(a.scale, &scale_e), 12);
+  scale_e -= 12;
+  CUtensorMap map;
+  cudaError_t e = tc_encode_boxes(&map, a.w, a.n_rows, a.k, a.q4, 2, kStageRows);
   if (e != cudaSuccess) return e;
-  backward_norm_kernel<<<a.batch, 256, 0, a.stream>>>(a, parts);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || !a.grad_gamma) return e;
-  backward_gamma_kernel<<<nb, 256, 0, a.stream>>>(a);
-  return cudaGetLastError();
+  // largest |gl|: at least 2,048 values a part
+  int gparts = static_cast<int>(a.n_rows / 2048);
+  gparts = gparts < 1 ? 1 : gparts > kMaxParts ? kMaxParts : gparts;
+  e = launch_dependent(gmax_kernel, dim3(static_cast<unsigned>(gparts), static_cast<unsigned>(a.batch)), 256, 0, 1, a.stream,
+                       a.grad_logits, a.n_rows, a.gmax, a.flag);
+  if (e != cudaSuccess) return e;
+  const int splits = bwd_splits(a.n_rows, a.k, a.num_sms);
+  const int slots = tc_batch_slots(a.batch);
+  if (a.q4)
+    e = slots == 8    ? launch_backward_nm<8, true>(a, map, scale_m, gparts, splits)
+        : slots == 16 ? launch_backward_nm<16, true>(a, map, scale_m, gparts, splits)
+                      : launch_backward_nm<32, true>(a, map, scale_m, gparts, splits);
+  else
+    e = slots == 8    ? launch_backward_nm<8, false>(a, map, scale_m, gparts, splits)
+        : slots == 16 ? launch_backward_nm<16, false>(a, map, scale_m, gparts, splits)
+                      : launch_backward_nm<32, false>(a, map, scale_m, gparts, splits);
+  if (e != cudaSuccess) return e;
+  const int cs = a.k >= 8192 ? 8 : a.k >= 4096 ? 4 : 1;
+  e = launch_dependent(finish_kernel, dim3(static_cast<unsigned>(a.batch * cs)), kFinishThreads, 0, cs, a.stream, a, splits,
+                       gparts, scale_e);
+  if (e != cudaSuccess || !a.grad_gamma || a.batch == 1) return e;
+  return launch_dependent(gamma_kernel, dim3(static_cast<unsigned>(a.k / 128)), 128, 0, 1, a.stream, a);
 }
 
 }  // namespace muse

@@ -23,8 +23,8 @@ struct Workspace {
   unsigned int *split_cnt;   // [num_sms][8] arrivals per shared tile and warp (per CTA boundary, or per tile when tiles < SMs), zero between forwards
   float *b1_part;            // split-K batch-1 path: [chunks][n_rows] chunk partial sums
   unsigned int *b1_cnt;      // split-K batch-1 path: [12-row tiles] chunk arrivals, zero between forwards
-  float *bwd_part;           // backward: partial sums of the gradient by the normed input
-  float *bwd_rms;            // backward: [MUSE_MAX_BATCH] RMS factors
+  float *bwd_part;           // backward: the row shares' sums of the gradient by the normed input
+  float *bwd_misc;           // backward: backward_misc_floats
 };
 
 constexpr int kMaxLseParts = 256;
@@ -97,6 +97,8 @@ int tc_batch_slots(int batch);                       // the kernel's batch slots
 size_t tc_split_floats(int num_sms, int max_batch);  // split_part size
 size_t tc_split_counters(int num_sms);                // split_cnt size
 cudaError_t tc_encode_weights(CUtensorMap *map, const void *weights, int64_t n_rows, int k, bool q4);
+// The same matrix in boxes of `rows` rows x `blocks` blocks.
+cudaError_t tc_encode_boxes(CUtensorMap *map, const void *weights, int64_t n_rows, int k, bool q4, int blocks, int rows);
 cudaError_t launch_tc(const LaunchArgs &a, const CUtensorMap &map);
 
 // Scores of rows of logits [n][ld] (v of them used), dtype 0/1/2 = f32/f16/bf16.
@@ -155,11 +157,13 @@ struct BackwardArgs {
   int k;
   int num_sms;
   float *part;                // workspace of backward_part_floats
-  float *rms;                 // workspace [batch]
+  float *gmax, *rms;          // workspace: largest |grad_logits| of parts of each row, RMS factors
+  uint32_t *flag;             // workspace: a block's d or dmin is beyond the tensor cores' operands
   uint32_t *status;
   cudaStream_t stream;
 };
-size_t backward_part_floats(int max_batch, int k);
+size_t backward_part_floats(int64_t n_rows, int k, int max_batch, int num_sms);
+size_t backward_misc_floats();
 cudaError_t launch_backward(const BackwardArgs &a);
 
 }  // namespace muse
