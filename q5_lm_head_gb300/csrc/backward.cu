@@ -13,11 +13,12 @@
 // W transposed: a lane of tensor memory is an input k, a column a pair of rows.
 //
 // Launches:
-// 1. gmax_kernel: the largest |gl| of parts of each row, for a power of two that
-//    brings a row's t into f16's range.
+// 1. slope_kernel: t of every row, eight consecutive v of a batch row together,
+//    and the largest |gl| of parts of each row, for a power of two that brings a
+//    row's t into f16's range.
 // 2. backward_tc_kernel: a CTA takes two block columns (512 inputs) and a share
-//    of the rows, 64 rows a stage.
-//    * weight producer warp: a 2-D TMA box of 64 rows x two blocks a stage.
+//    of the rows, 128 or 64 rows a stage.
+//    * weight producer warp: a 2-D TMA box of the stage's rows x two blocks.
 //    * operand warps: read the blocks' d, dmin and scales.  With d = md 2^e,
 //      1 <= |md| < 2, the power of two goes to the A side (A = sc q 2^e, at most
 //      11 significant bits: exact in f16) and md to the B side: B = t md as the
@@ -25,7 +26,7 @@
 //      mins are a product of their own, A' = m 2^e' for the 16 sub-blocks,
 //      B' = -t mdmin.
 //    * four unpack warpgroups, two for each block, alternating between units of
-//      16 or 32 rows: ldmatrix with transposition gives a thread four rows of
+//      16 to 64 rows: ldmatrix with transposition gives a thread four rows of
 //      one input, and tcgen05.st (16 lanes x 256 bits) takes exactly that
 //      fragment. 
 //    * MMA warp: per 16 rows four products of M = 128 (two nibble halves of two
@@ -45,6 +46,7 @@
 #include <cmath>
 #include <cuda.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -55,19 +57,23 @@
 namespace muse {
 namespace {
 
-constexpr int kStageRows = 64;
-constexpr int kMaxParts = 32;                 // of a row's largest |gl|
+constexpr int kMaxParts = 64;                 // of a row's largest |gl|
+constexpr int kPadRows = 128;                 // t is kept, as zeros, up to a multiple of this
 constexpr int kTileCols = 2 * kBlockWeights;  // inputs of a CTA
-constexpr int kFlushStages = 2;               // between additions of the accumulators to the f32 sums
+constexpr int kFlushRows = 128;               // between additions of the accumulators to the f32 sums
 constexpr int kUnpackWarps = 16;
 constexpr uint32_t kTmem = 512;
 
 // ---------------------------------------------------------------- operands' scale
-// t 2^-e with e = exponent of the row's largest |gl| (0 for a row of zeros); the
-// scale's mantissa in [2^11, 2^12) is applied by the host: |t| < 2^13.
+// What one of these kernels writes for the next is read through L2 (ld.cg): a
+// kernel may have started while the one before it was still writing, and the
+// read-only path is for data that no longer change.
+//
+// t 2^-e with e = exponent of the row's largest |gl| (0 for a row of zeros) and
+// the scale's mantissa in [2^11, 2^12) is below 2^13.
 __device__ __forceinline__ int row_exponent(const float *gmax, int b, int parts) {
   float m = 0.0f;
-  for (int i = 0; i < parts; ++i) m = fmaxf(m, gmax[b * kMaxParts + i]);
+  for (int i = 0; i < parts; ++i) m = fmaxf(m, __ldcg(gmax + b * kMaxParts + i));
   const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
   return m == 0.0f ? 0 : e < -126 ? -126 : e;   // 128 for infinities: they stay what they are
 }
@@ -77,23 +83,36 @@ __device__ __forceinline__ float pow2(int e) {   // -126 <= e <= 127
 
 __device__ __forceinline__ float cap_slope(float l, float cap, float inv_cap2) { return (cap - l) * (cap + l) * inv_cap2; }
 
-__global__ void __launch_bounds__(256) gmax_kernel(const float *__restrict__ g, int64_t n, float *__restrict__ gmax,
-                                                   uint32_t *flag) {
+// t[v/8][b][v%8] = gl * scale_m * slope, scale_m the scale's mantissa.
+__global__ void __launch_bounds__(256) slope_kernel(const BackwardArgs a, float scale_m) {
   __shared__ float s_max[8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const float *row = g + blockIdx.y * n;
-  const int64_t lo = n * blockIdx.x / gridDim.x, hi = n * (blockIdx.x + 1) / gridDim.x;
+  const int b = blockIdx.y;
+  const float *g = a.grad_logits + b * a.n_rows, *l = a.logits + b * a.n_rows;
+  const int64_t octs = (a.n_rows + kPadRows - 1) / kPadRows * (kPadRows / 8);
+  const int64_t lo = octs * blockIdx.x / gridDim.x * 8, hi = octs * (blockIdx.x + 1) / gridDim.x * 8;
+  const float inv_cap2 = a.cap > 0.0f ? 1.0f / (a.cap * a.cap) : 0.0f;
   float m = 0.0f;
 #pragma unroll 8
-  for (int64_t i = lo + threadIdx.x; i < hi; i += 256) m = fmaxf(m, fabsf(row[i]));
+  for (int64_t v = lo + threadIdx.x; v < hi; v += 256) {
+    float t = 0.0f;
+    if (v < a.n_rows) {
+      const float x = __ldcs(g + v);
+      m = fmaxf(m, fabsf(x));
+      t = x;
+      if (a.cap > 0.0f) t *= cap_slope(__ldcs(l + v), a.cap, inv_cap2);
+      t *= scale_m;
+    }
+    a.t[((v >> 3) * a.batch + b) * 8 + (v & 7)] = t;
+  }
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int i = 1; i < 8; ++i) m = fmaxf(m, s_max[i]);
-    gmax[blockIdx.y * kMaxParts + blockIdx.x] = m;
-    if (blockIdx.x == 0 && blockIdx.y == 0) *flag = 0u;
+    a.gmax[b * kMaxParts + blockIdx.x] = m;
+    if (blockIdx.x == 0 && b == 0) *a.flag = 0u;
   }
 }
 
@@ -102,39 +121,46 @@ template <int NM, bool kQ4>
 struct BwdCfg {
   static constexpr int kBB = kQ4 ? kBlockBytesQ4 : kBlockBytes;
   static constexpr int kRowBytes = 2 * kBB;
-  static constexpr int kWBytes = kStageRows * kRowBytes;
+  // Rows of a stage: 128 halve what every stage costs in barriers; with more
+  // than 8 slots the stage's B tiles leave room for 64.
+  static constexpr int kRows = NM == 8 ? 128 : 64;
+  static constexpr int kWBytes = kRows * kRowBytes;
   static constexpr int kN = 2 * NM;                               // B rows: hi, lo
   // Accumulator columns: with 8 slots hi and lo side by side (an MMA has 16
   // columns at least), else both into the same ones.
   static constexpr int kD = NM == 8 ? 16 : NM;
-  static constexpr int kBTile = kN * kStageRows * 2;              // f16 [kN][64], K-major
-  static constexpr int kScl = 16 * kStageRows * 2;                // f16 [2 blocks x 8][64]
-  static constexpr int kSlot = 4 * kBTile + 2 * kScl;             // B of d, B' of dmin (two blocks each); scales; mins
+  // B tiles: core matrices of 8 rows x 8 values, those along the rows v 16 bytes
+  // further apart than they are long: a warp's stores fall on all banks.
+  static constexpr int kLbo = kN * 16 + 16;
+  static constexpr int kBTile = kRows / 8 * kLbo;                 // f16 [kN][kRows]
+  static constexpr int kScl = 16 * kRows * 2;                     // f16 [2 blocks x 8][kRows]
+  static constexpr int kSide = 4 * kBTile + 2 * kScl;             // B of d, B' of dmin (two blocks each); scales; mins
+  static constexpr int kStage = kWBytes + (kSide + 127) / 128 * 128;
   // Groups of four operand warps, taking the stages in turn.  One with 32
   // slots: its unpack threads need the registers for 32 sums.
   static constexpr int kGroups = NM == 32 ? 1 : 2;
-  static constexpr int kSlots = NM == 32 ? 3 : 4;
-  static constexpr int kPrepWarps = 4 * kGroups;
-  static constexpr int kThreads = 32 * (kUnpackWarps + kPrepWarps + 2);
-  static constexpr int kTStride = kStageRows + 4;                 // floats: 16-byte loads of eight rows on all banks
-  static constexpr int kT = NM * kTStride * 4 + 4 * kStageRows * 4;   // a group's t [NM][64], mantissas [4][64]
-  static constexpr int kFixed = kSlots * kSlot + kGroups * kT + 1024;
-  static constexpr int kWFit = (226 * 1024 - kFixed) / kWBytes;
-  static constexpr int kWStages = kWFit > 6 ? 6 : kWFit;
-  static_assert(kWStages >= 3, "weight ring");
-  static constexpr int kSmem = kWStages * kWBytes + kFixed;
-  // tensor memory: two sets of sums of four M-tiles and two min products, then a ring of units of US x 16 rows
-  static constexpr int kUS = NM == 32 ? 1 : 2;
-  static constexpr int kUnits = kStageRows / (16 * kUS);          // units a stage
+  static constexpr int kThreads = 32 * (kUnpackWarps + 4 * kGroups + 2);
+  static constexpr int kT = 2 * 4 * kRows * 4;                    // a group's mantissas, two stages of [4][kRows]
+  static constexpr int kFixed = kGroups * kT + 1024;
+  static constexpr int kFit = (226 * 1024 - kFixed) / kStage;
+  static constexpr int kStages = kFit > 5 ? 5 : kFit;
+  static_assert(kStages >= 3, "stage ring");
+  static constexpr int kSmem = kStages * kStage + kFixed;
+  // tensor memory: two sets of sums of four M-tiles and two min products, then a ring of units of kUS x 16 rows
+  static constexpr int kUS = NM == 32 ? 1 : kRows / 32;
+  static constexpr int kUnits = kRows / (16 * kUS);               // units a stage
   static constexpr int kSlab = 40;                                // columns of 16 rows: four M-tiles of 8, mins 8
   static constexpr int kABase = 12 * kD;
-  static constexpr int kBufs = (512 - kABase) / (kSlab * kUS) > 4 ? 4 : (512 - kABase) / (kSlab * kUS);
-  static_assert(kBufs >= 2, "unit ring");
+  static constexpr int kBufs = (512 - kABase) / (kSlab * kUS);
+  static_assert(kBufs >= 2 && kUnits % 2 == 0, "unit ring");
+  static constexpr int kFlush = kFlushRows / kRows;               // stages between flushes
   static constexpr uint32_t kIdesc = tc::idesc_f16_f32(128, kD);
 };
 
+template <uint32_t kOffset>
 __device__ __forceinline__ void st_16x256b(uint32_t ta, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1, %2, %3, %4};" ::"r"(ta), "r"(a), "r"(b), "r"(c), "r"(d)
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0 + %5], {%1, %2, %3, %4};" ::"r"(ta), "r"(a), "r"(b), "r"(c),
+               "r"(d), "n"(kOffset)
                : "memory");
 }
 
@@ -174,49 +200,48 @@ __device__ __forceinline__ void tma_box(void *dst, const CUtensorMap *map, int x
       : "memory");
 }
 
-// d (an f16 value) as md 2^e with -23 <= e <= 0: 1 <= |md| < 2 apart from 0 and
-// the smallest subnormal, up to 4 where d is from 2 to 4; *big for more.
+// Odd sub-blocks' quants are taken out of the high nibbles as 2q (Q5_K, with the
+// fifth bit behind) or 16q (Q4_K): their scales are divided by as much.
+template <bool kQ4>
+constexpr float kHighFactor = kQ4 ? 0.0625f : 0.5f;
+
+// d (an f16 value) as md 2^e with -20 <= e <= 0 (a scale, and a sixteenth of it,
+// is then exact in f16): 1 <= |md| < 2 apart from smaller values of d, up to 4
+// where d is from 2 to 4; *big for more.
 __device__ __forceinline__ float split_d(float d, int &e, bool &big) {
   const uint32_t bits = __float_as_uint(d);
   const int ex = static_cast<int>((bits >> 23) & 255) - 127;      // of the f16 value: -24 .. 15, -127 for 0
   big |= ex > 1;                                                  // infinities and NaN too
-  e = ex > 0 ? 0 : ex < -23 ? -23 : ex;
+  e = ex > 0 ? 0 : ex < -20 ? -20 : ex;
   return d * pow2(-e);
 }
 
 template <int NM, bool kQ4>
 __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
-    backward_tc_kernel(const __grid_constant__ CUtensorMap wmap, const BackwardArgs a, float scale_m, int gparts,
-                       int pairs, int splits) {
+    backward_tc_kernel(const __grid_constant__ CUtensorMap wmap, const BackwardArgs a, int gparts, int pairs, int splits) {
   using C = BwdCfg<NM, kQ4>;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t *wst = smem;                                            // [kWStages][64][kRowBytes]
-  uint8_t *slots = smem + C::kWStages * C::kWBytes;               // [kSlots][kSlot]
-  float *s_t = reinterpret_cast<float *>(slots + C::kSlots * C::kSlot);   // [NM][kTStride]
-  uint64_t *bars = reinterpret_cast<uint64_t *>(slots + C::kSlots * C::kSlot + C::kGroups * C::kT);
-  uint64_t *wfull = bars, *wempty = wfull + C::kWStages;
-  uint64_t *pfull = wempty + C::kWStages, *pempty = pfull + C::kSlots;
-  uint64_t *tfull = pempty + C::kSlots, *tempty = tfull + C::kBufs;
+  extern __shared__ __align__(1024) uint8_t smem[];                // [kStages][weights, B tiles, scales, mins]
+  float *s_md = reinterpret_cast<float *>(smem + C::kStages * C::kStage);   // [kGroups][kT]
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kStages * C::kStage + C::kGroups * C::kT);
+  uint64_t *wfull = bars, *pfull = wfull + C::kStages, *empty = pfull + C::kStages;
+  uint64_t *tfull = empty + C::kStages, *tempty = tfull + C::kBufs;
   uint64_t *dfull = tempty + C::kBufs, *dfree = dfull + 2, *done = dfree + 2;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(done + 1);
   volatile uint32_t *s_abort = s_tmem + 1;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int pair = blockIdx.x % pairs, split = blockIdx.x / pairs;   // neighbours stream the same rows
-  const int64_t stages = (a.n_rows + kStageRows - 1) / kStageRows;
+  const int64_t stages = (a.n_rows + C::kRows - 1) / C::kRows;
   const int64_t st0 = stages * split / splits;
   const int n_st = static_cast<int>(stages * (split + 1) / splits - st0);
   constexpr int kPrepThreads = 128;                               // of a group
-  constexpr int kMmaWarp = kUnpackWarps + C::kPrepWarps, kTmaWarp = kMmaWarp + 1;
+  constexpr int kMmaWarp = kUnpackWarps + 4 * C::kGroups, kTmaWarp = kMmaWarp + 1;
 
   if (tid == 0) {
-    for (int i = 0; i < C::kWStages; ++i) {
+    for (int i = 0; i < C::kStages; ++i) {
       ptx::mbar_init(&wfull[i], 1);
-      ptx::mbar_init(&wempty[i], kUnpackWarps + 4);
-    }
-    for (int i = 0; i < C::kSlots; ++i) {
       ptx::mbar_init(&pfull[i], 4);
-      ptx::mbar_init(&pempty[i], kUnpackWarps + 1);               // the scales' readers, the MMAs
+      ptx::mbar_init(&empty[i], kUnpackWarps + 1);                // the unpack warps, the MMAs
     }
     for (int i = 0; i < C::kBufs; ++i) {
       ptx::mbar_init(&tfull[i], kUnpackWarps / 2);
@@ -242,25 +267,34 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     atomicOr(a.status, kStatusWaitTimeout);
     *s_abort = 1u;
   };
-  auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity)) != 0; };
+  // Bounded; gives up early once another role has.
+  auto wait_one = [&](uint64_t *bar, uint32_t parity) {
+    if (ptx::mbar_try_wait_nohint(bar, parity)) return true;
+    for (uint32_t i = 0; i < ptx::kSpinLimit; ++i) {
+      if (ptx::mbar_try_wait(bar, parity)) return true;
+      if (*s_abort) return false;
+    }
+    return false;
+  };
+  auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0; };
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------ weights
     if (lane == 0) {
       const uint64_t policy = ptx::policy_evict_first();
-      int issued = 0, ws = 0;
+      int issued = 0, slot = 0;
       uint32_t ph = 0;
-      for (int i = 0; i < n_st && !*s_abort; ++i) {
-        if (i >= C::kWStages && !ptx::mbar_wait(&wempty[ws], ph ^ 1u)) { fail(); break; }
-        ptx::mbar_arrive_expect_tx(&wfull[ws], C::kWBytes);
-        tma_box(wst + ws * C::kWBytes, &wmap, pair * (C::kRowBytes / 4), static_cast<int>((st0 + i) * kStageRows), &wfull[ws],
+      for (int i = 0; i < n_st; ++i) {
+        if (i >= C::kStages && !wait_one(&empty[slot], ph ^ 1u)) { fail(); break; }
+        ptx::mbar_arrive_expect_tx(&wfull[slot], C::kWBytes);
+        tma_box(smem + slot * C::kStage, &wmap, pair * (C::kRowBytes / 4), static_cast<int>((st0 + i) * C::kRows), &wfull[slot],
                 policy);
         issued = i + 1;
-        if (++ws == C::kWStages) { ws = 0; ph ^= 1u; }
+        if (++slot == C::kStages) { slot = 0; ph ^= 1u; }
       }
       // never leave copies in flight
-      for (int i = issued > C::kWStages ? issued - C::kWStages : 0; i < issued; ++i)
-        ptx::mbar_wait(&wfull[i % C::kWStages], static_cast<uint32_t>((i / C::kWStages) & 1));
+      for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
+        ptx::mbar_wait(&wfull[i % C::kStages], static_cast<uint32_t>((i / C::kStages) & 1));
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
@@ -269,12 +303,11 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     int slot = 0, buf = 0;
     uint32_t pph = 0, tph = 0;
     for (int i = 0; i < n_st && ok; ++i) {
-      if (__any_sync(0xffffffffu, *s_abort != 0u)) break;
-      const int period = i / kFlushStages, db = period & 1;
-      const bool opens = i % kFlushStages == 0;
+      const int period = i / C::kFlush, db = period & 1;
+      const bool opens = i % C::kFlush == 0;
       if (opens && period >= 2 && !(ok = wait(&dfree[db], ((period >> 1) & 1) ^ 1))) break;
       if (!(ok = wait(&pfull[slot], pph))) break;
-      const uint32_t b0 = ptx::smem_u32(slots + slot * C::kSlot);
+      const uint32_t b0 = ptx::smem_u32(smem + slot * C::kStage + C::kWBytes);
       const uint32_t dbase = tbase + db * 6 * C::kD;
       for (int u = 0; u < C::kUnits; ++u) {
         if (!(ok = wait(&tfull[buf], tph))) break;
@@ -283,16 +316,16 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
 #pragma unroll
           for (int s = 0; s < C::kUS; ++s) {
             const uint32_t at = tbase + C::kABase + (buf * C::kUS + s) * C::kSlab;
-            const uint32_t kofs = static_cast<uint32_t>((u * C::kUS + s) * 2 * (C::kN / 8) * 128);
+            const uint32_t kofs = static_cast<uint32_t>((u * C::kUS + s) * 2 * C::kLbo);
             const bool acc = !opens || u > 0 || s > 0;
 #pragma unroll
             for (int mt = 0; mt < 6; ++mt) {                      // four M-tiles, then the mins of both blocks
               const int kind = mt < 4 ? mt >> 1 : mt - 2;
               const uint32_t d = dbase + mt * C::kD, ta = at + (mt < 4 ? mt : 4) * 8;
               const uint32_t tile = b0 + kind * C::kBTile + kofs;
-              tc::mma_f16_tmemA(d, ta, tc::smem_desc_kmajor(tile, C::kN * 16, 128), C::kIdesc, acc);
+              tc::mma_f16_tmemA(d, ta, tc::smem_desc_kmajor(tile, C::kLbo, 128), C::kIdesc, acc);
               if (NM > 8)
-                tc::mma_f16_tmemA(d, ta, tc::smem_desc_kmajor(tile + (NM / 8) * 128, C::kN * 16, 128), C::kIdesc, true);
+                tc::mma_f16_tmemA(d, ta, tc::smem_desc_kmajor(tile + (NM / 8) * 128, C::kLbo, 128), C::kIdesc, true);
             }
           }
           tc::commit(&tempty[buf]);
@@ -302,14 +335,14 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       }
       if (!ok) break;
       if (issuer) {
-        tc::commit(&pempty[slot]);
-        if ((i + 1) % kFlushStages == 0 || i + 1 == n_st) tc::commit(&dfull[db]);
+        tc::commit(&empty[slot]);
+        if ((i + 1) % C::kFlush == 0 || i + 1 == n_st) tc::commit(&dfull[db]);
       }
       __syncwarp();
-      if (++slot == C::kSlots) { slot = 0; pph ^= 1u; }
+      if (++slot == C::kStages) { slot = 0; pph ^= 1u; }
     }
     if (!ok && lane == 0) fail();
-    // the sums are read, and tensor memory freed, only after every MMA issued here completed
+    // tensor memory is freed only after every MMA issued here completed
     if (issuer) tc::commit(done);
     __syncwarp();
     if (!wait(done, 0) && lane == 0) fail();
@@ -317,107 +350,103 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     // ------------------------------------------------------------ operands
     const int grp = (warp - kUnpackWarps) >> 2;                   // takes the stages grp, grp + kGroups, ..
     const int pt = tid - 32 * kUnpackWarps - kPrepThreads * grp;
-    float *s_tg = s_t + grp * (C::kT / 4), *s_md = s_tg + NM * C::kTStride;
-    constexpr int kEach = NM * kStageRows / kPrepThreads;         // t values of a thread and stage
-    asm volatile("griddepcontrol.wait;" ::: "memory");            // the rows' largest values
-    const float inv_cap2 = a.cap > 0.0f ? 1.0f / (a.cap * a.cap) : 0.0f;
-    constexpr int kStepB = kPrepThreads / kStageRows;             // batch rows between a thread's values
-    const int tb = pt / kStageRows, tv = pt % kStageRows;
-    float g[kEach], l[kEach], e2[kEach];
+    // this thread's tasks of a stage: eight rows v of one batch row
+    constexpr int kOcts = C::kRows / 8, kTasks = NM * kOcts / kPrepThreads;
+    static_assert(kTasks * kPrepThreads == NM * kOcts, "whole tasks");
+    const int oct = pt % kOcts, b_first = pt / kOcts;
+    constexpr int kStepB = kPrepThreads / kOcts;
+    asm volatile("griddepcontrol.wait;" ::: "memory");            // t and the rows' largest values
+    float e2[kTasks];
+    float4 t_next[kTasks][2];
+    const float4 *t_at = reinterpret_cast<const float4 *>(a.t) + ((st0 + grp) * kOcts + oct) * a.batch * 2 + 2 * b_first;
+    auto fetch = [&](bool any) {
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const int b = tb + j * kStepB;
+      for (int j = 0; j < kTasks; ++j)
+        if (any && b_first + j * kStepB < a.batch) {
+          t_next[j][0] = __ldcg(t_at + 2 * j * kStepB);
+          t_next[j][1] = __ldcg(t_at + 2 * j * kStepB + 1);
+        }
+      t_at += static_cast<int64_t>(C::kGroups) * kOcts * a.batch * 2;
+    };
+    fetch(grp < n_st);
+#pragma unroll
+    for (int j = 0; j < kTasks; ++j) {
+      const int b = b_first + j * kStepB;
       e2[j] = b < a.batch ? pow2(-min(row_exponent(a.gmax, b, gparts), 126)) : 0.0f;
     }
-    auto fetch = [&](int i) {
-      const int64_t v = (st0 + i) * kStageRows + tv;
-#pragma unroll
-      for (int j = 0; j < kEach; ++j) {
-        const int b = tb + j * kStepB;
-        const bool in = b < a.batch && v < a.n_rows && i < n_st;
-        const int64_t at = static_cast<int64_t>(b) * a.n_rows + v;
-        g[j] = in ? __ldg(a.grad_logits + at) : 0.0f;
-        l[j] = in && a.cap > 0.0f ? __ldg(a.logits + at) : 0.0f;
-      }
-    };
-    fetch(grp);
     bool bad = false, big = false;
-    for (int i = grp; i < n_st; i += C::kGroups) {
-      const int ws = i % C::kWStages, slot = i % C::kSlots;
-      const uint32_t wph = (i / C::kWStages) & 1, pph = (i / C::kSlots) & 1;
-#pragma unroll
-      for (int j = 0; j < kEach; ++j) {
-        float t = g[j] * e2[j] * scale_m;
-        if (a.cap > 0.0f) t *= cap_slope(l[j], a.cap, inv_cap2);
-        s_tg[(tb + j * kStepB) * C::kTStride + tv] = t;
-      }
-      fetch(i + C::kGroups);
-      bad = __any_sync(0xffffffffu, *s_abort != 0u) != 0;
-      if (!bad && i >= C::kSlots) bad = !wait(&pempty[slot], pph ^ 1u);
-      if (!bad) bad = !wait(&wfull[ws], wph);
-      uint8_t *sl = slots + slot * C::kSlot;
+    int turn = 0;
+    for (int i = grp; i < n_st; i += C::kGroups, turn ^= 1) {
+      const int slot = i % C::kStages;
+      float *md_at = s_md + grp * (C::kT / 4) + turn * 4 * C::kRows;
+      // the stage's weights: they were sent for only after the slot's last readers were done with it
+      bad = !wait(&wfull[slot], (i / C::kStages) & 1);
+      uint8_t *st = smem + slot * C::kStage, *side = st + C::kWBytes;
       if (!bad) {
-        // one block's header: powers of two with its scales and mins, mantissas for B
-        const int blk = pt / kStageRows;
-        const uint4 hdr = *reinterpret_cast<const uint4 *>(wst + ws * C::kWBytes + tv * C::kRowBytes + blk * C::kBB);
-        const float2 dd = __half22float2(*reinterpret_cast<const __half2 *>(&hdr.x));
-        int ed, em;
-        s_md[blk * kStageRows + tv] = split_d(dd.x, ed, big);
-        s_md[(2 + blk) * kStageRows + tv] = -split_d(dd.y, em, big);
-        const uint32_t pd = pack_half2(pow2(ed), 0.5f * pow2(ed));   // even sub-blocks' scale, odd ones' halved
-        const uint32_t pm = pack_half2(pow2(em), pow2(em));
-        const uint32_t sc[2] = {hdr.y & 0x3F3F3F3Fu, (hdr.w & 0x0F0F0F0Fu) | ((hdr.y >> 2) & 0x30303030u)};
-        const uint32_t mn[2] = {hdr.z & 0x3F3F3F3Fu, ((hdr.w >> 4) & 0x0F0F0F0Fu) | ((hdr.z >> 2) & 0x30303030u)};
-        __half *scl = reinterpret_cast<__half *>(sl + 4 * C::kBTile) + blk * 8 * kStageRows + tv;
-        __half *mns = scl + 16 * kStageRows;
-        const uint32_t one = 0x3C003C00u;
+        // a block's header: powers of two with its scales and mins, mantissas for B
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {                             // sub-blocks 2h, 2h + 1
-          const uint32_t sel = h & 1 ? 0x4342u : 0x4140u;
-          const uint32_t s = hmul2(hfma2(__byte_perm(sc[h >> 1], 0x64u, sel), one, kNeg1024), pd);
-          const uint32_t m = hmul2(hfma2(__byte_perm(mn[h >> 1], 0x64u, sel), one, kNeg1024), pm);
-          scl[(2 * h) * kStageRows] = __ushort_as_half(static_cast<unsigned short>(s));
-          scl[(2 * h + 1) * kStageRows] = __ushort_as_half(static_cast<unsigned short>(s >> 16));
-          mns[(2 * h) * kStageRows] = __ushort_as_half(static_cast<unsigned short>(m));
-          mns[(2 * h + 1) * kStageRows] = __ushort_as_half(static_cast<unsigned short>(m >> 16));
+        for (int task = pt; task < 2 * C::kRows; task += kPrepThreads) {
+          const int blk = task / C::kRows, row = task % C::kRows;
+          const uint4 hdr = *reinterpret_cast<const uint4 *>(st + row * C::kRowBytes + blk * C::kBB);
+          const float2 dd = __half22float2(*reinterpret_cast<const __half2 *>(&hdr.x));
+          int ed, em;
+          md_at[blk * C::kRows + row] = split_d(dd.x, ed, big);
+          md_at[(2 + blk) * C::kRows + row] = -split_d(dd.y, em, big);
+          const uint32_t pd = pack_half2(pow2(ed), kHighFactor<kQ4> * pow2(ed));   // odd sub-blocks' quants come multiplied
+          const uint32_t pm = pack_half2(pow2(em), pow2(em));
+          const uint32_t sc[2] = {hdr.y & 0x3F3F3F3Fu, (hdr.w & 0x0F0F0F0Fu) | ((hdr.y >> 2) & 0x30303030u)};
+          const uint32_t mn[2] = {hdr.z & 0x3F3F3F3Fu, ((hdr.w >> 4) & 0x0F0F0F0Fu) | ((hdr.z >> 2) & 0x30303030u)};
+          __half *scl = reinterpret_cast<__half *>(side + 4 * C::kBTile) + blk * 8 * C::kRows + row;
+          __half *mns = scl + 16 * C::kRows;
+          const uint32_t one = 0x3C003C00u;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {                           // sub-blocks 2h, 2h + 1
+            const uint32_t sel = h & 1 ? 0x4342u : 0x4140u;
+            const uint32_t s = hmul2(hfma2(__byte_perm(sc[h >> 1], 0x64u, sel), one, kNeg1024), pd);
+            const uint32_t m = hmul2(hfma2(__byte_perm(mn[h >> 1], 0x64u, sel), one, kNeg1024), pm);
+            scl[(2 * h) * C::kRows] = __ushort_as_half(static_cast<unsigned short>(s));
+            scl[(2 * h + 1) * C::kRows] = __ushort_as_half(static_cast<unsigned short>(s >> 16));
+            mns[(2 * h) * C::kRows] = __ushort_as_half(static_cast<unsigned short>(m));
+            mns[(2 * h + 1) * C::kRows] = __ushort_as_half(static_cast<unsigned short>(m >> 16));
+          }
         }
       }
       if (ptx::named_bar_red_or(1 + grp, kPrepThreads, bad)) {
         bad = true;
         break;
       }
-      if (lane == 0) ptx::mbar_arrive(&wempty[ws]);
-      // B tiles: eight rows of one batch row as hi and lo, for d and dmin of both blocks
-      constexpr int kTasks = NM * 8, kShare = kTasks < kPrepThreads ? kPrepThreads / kTasks : 1;   // threads a task
-      static_assert(4 % kShare == 0, "kinds a thread");
+      // B tiles: the eight rows as hi and lo, for d and dmin of both blocks; the
+      // columns of batch rows that are not there stay what they are, nobody reads their sums
 #pragma unroll
-      for (int q = pt; q < kTasks * kShare; q += kPrepThreads) {
-        const int b = q % NM, oct = q / NM % 8, part = q / kTasks;
-        const float4 t0 = *reinterpret_cast<const float4 *>(s_tg + b * C::kTStride + 8 * oct);
-        const float4 t1 = *reinterpret_cast<const float4 *>(s_tg + b * C::kTStride + 8 * oct + 4);
-        const float t[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+      for (int j = 0; j < kTasks; ++j) {
+        const int b = b_first + j * kStepB;
+        if (b < a.batch) {
+          const float4 t0 = t_next[j][0], t1 = t_next[j][1];
+          const float t[8] = {t0.x * e2[j], t0.y * e2[j], t0.z * e2[j], t0.w * e2[j],
+                              t1.x * e2[j], t1.y * e2[j], t1.z * e2[j], t1.w * e2[j]};
+          uint8_t *tile = side + oct * C::kLbo + (b & 7) * 16;
 #pragma unroll
-        for (int kk = 0; kk < 4 / kShare; ++kk) {
-          const int kind = part * (4 / kShare) + kk;
-          const float4 m0 = *reinterpret_cast<const float4 *>(s_md + kind * kStageRows + 8 * oct);
-          const float4 m1 = *reinterpret_cast<const float4 *>(s_md + kind * kStageRows + 8 * oct + 4);
-          const float md[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
-          uint32_t hi[4], lo[4];
+          for (int kind = 0; kind < 4; ++kind) {
+            const float4 m0 = *reinterpret_cast<const float4 *>(md_at + kind * C::kRows + 8 * oct);
+            const float4 m1 = *reinterpret_cast<const float4 *>(md_at + kind * C::kRows + 8 * oct + 4);
+            const float md[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+            uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const float x0 = t[2 * p] * md[2 * p], x1 = t[2 * p + 1] * md[2 * p + 1];
-            hi[p] = pack_half2(x0, x1);
-            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi[p]));
-            lo[p] = pack_half2(x0 - h.x, x1 - h.y);
+            for (int p = 0; p < 4; ++p) {
+              const float x0 = t[2 * p] * md[2 * p], x1 = t[2 * p + 1] * md[2 * p + 1];
+              hi[p] = pack_half2(x0, x1);
+              const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi[p]));
+              lo[p] = pack_half2(x0 - h.x, x1 - h.y);
+            }
+            *reinterpret_cast<uint4 *>(tile + kind * C::kBTile + (b >> 3) * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(tile + kind * C::kBTile + ((NM + b) >> 3) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
-          uint8_t *tile = sl + kind * C::kBTile + oct * (C::kN / 8) * 128 + (b & 7) * 16;
-          *reinterpret_cast<uint4 *>(tile + (b >> 3) * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4 *>(tile + ((NM + b) >> 3) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the tiles, to the tensor cores' reads
-      ptx::named_bar_sync(1 + grp, kPrepThreads);                 // t and mantissas are read
+      __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&pfull[slot]);
+      fetch(i + C::kGroups < n_st);
     }
     if (bad && lane == 0) fail();
     if (big) atomicOr(a.flag, 1u);
@@ -426,7 +455,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     const int blk = (warp >> 2) & 1, par = warp >> 3, wq = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(32 * wq) << 16;
     const uint32_t rot = static_cast<uint32_t>(4 - 2 * wq) & 31u;   // high bit 2wq -> 4, 2wq + 1 -> 5
-    const uint32_t src0 = ptx::smem_u32(wst) + (lane & 15) * C::kRowBytes + blk * C::kBB + 16 * (lane >> 4);
+    const uint32_t src0 = ptx::smem_u32(smem) + (lane & 15) * C::kRowBytes + blk * C::kBB + 16 * (lane >> 4);
     // the f32 sums: inputs of M-tile warp/4 by batch row, and mins (lane: sub-block) of eight batch rows
     const int mt = warp >> 2;
     const bool min_warp = wq == 0 && mt < NM / 8;
@@ -443,14 +472,19 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       const uint32_t d = tbase + db * 6 * C::kD;
 #pragma unroll
       for (int c0 = 0; c0 < C::kD; c0 += 16) {
-        uint32_t x[16];
-        tc::ld_32x32b_x16(d + lane_base + mt * C::kD + c0, x);
-        tc::wait_ld();
-        auto two = [&](int j) { return pack2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])); };
+        if (c0 == 0 || c0 < a.batch) {
+          uint32_t x[16];
+          tc::ld_32x32b_x16(d + lane_base + mt * C::kD + c0, x);
+          tc::wait_ld();
+          auto two = [&](int j) { return pack2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])); };
+          if constexpr (NM == 8) {              // hi and lo
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if constexpr (NM == 8) sum[j & 3] = add2(sum[j & 3], two(2 * j));   // hi, then lo
-          else sum[c0 / 2 + j] = add2(sum[c0 / 2 + j], two(2 * j));
+            for (int j = 0; j < 4; ++j)
+              if (2 * j < a.batch) sum[j] = add2(sum[j], add2(two(2 * j), two(8 + 2 * j)));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[c0 / 2 + j] = add2(sum[c0 / 2 + j], two(2 * j));
+          }
         }
       }
       if (min_warp) {
@@ -473,55 +507,61 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       return true;
     };
     bool ok = true;
-    int ws = 0, slot = 0, unit = par;           // unit: of the whole share; its buffer is unit % kBufs
-    int buf = par;
-    uint32_t wph = 0, pph = 0, tph = 0;
-    for (int i = 0; i < n_st && ok; ++i) {
-      if (__any_sync(0xffffffffu, *s_abort != 0u)) { ok = false; break; }
-      if (!(ok = wait(&wfull[ws], wph))) break;
-      if (!(ok = wait(&pfull[slot], pph))) break;
-      const uint8_t *sl = slots + slot * C::kSlot;
-      const __half *scl = reinterpret_cast<const __half *>(sl + 4 * C::kBTile) + (blk * 8 + 2 * wq) * kStageRows + 4 * (lane & 3);
-      const __half *mns = reinterpret_cast<const __half *>(sl + 4 * C::kBTile) + (16 + (lane >> 2)) * kStageRows + 4 * (lane & 3);
+    int slot = 0, buf = par, unit = par;        // unit: of the whole share; its buffer is unit % kBufs
+    uint32_t pph = 0, tph = 0;
+    for (int i = 0; i < n_st; ++i) {
+      if (!(ok = wait(&pfull[slot], pph))) break;   // the weights too: the operand warps have waited for them
+      const uint8_t *side = smem + slot * C::kStage + C::kWBytes;
+      const __half *scl = reinterpret_cast<const __half *>(side + 4 * C::kBTile) + (blk * 8 + 2 * wq) * C::kRows + 4 * (lane & 3);
+      const __half *mns = reinterpret_cast<const __half *>(side + 4 * C::kBTile) + (16 + (lane >> 2)) * C::kRows + 4 * (lane & 3);
       for (int u = par; u < C::kUnits; u += 2) {
         if (unit >= C::kBufs && !(ok = wait(&tempty[buf], tph ^ 1u))) break;
         tc::fence_after();
-#pragma unroll
-        for (int s = 0; s < C::kUS; ++s) {
+        const uint32_t at0 = tbase + lane_base + C::kABase + buf * C::kUS * C::kSlab;
+        const uint32_t src1 = src0 + slot * C::kStage + u * C::kUS * 16 * C::kRowBytes;
+        auto slab_to_tmem = [&](auto s_const) {
+          constexpr int s = decltype(s_const)::value;
           const int slab = u * C::kUS + s;
-          const uint32_t src = src0 + ws * C::kWBytes + slab * 16 * C::kRowBytes;
+          const uint32_t src = src1 + s * 16 * C::kRowBytes;
           uint32_t q[4], h[4];
           load_transposed(src + (kQ4 ? kOffQsQ4 : kOffQs) + 32 * wq, q);
           if constexpr (!kQ4) load_transposed(src + kOffQh, h);
-          const uint2 k0 = *reinterpret_cast<const uint2 *>(scl + 16 * slab);                 // low nibbles' scales
-          const uint2 k1 = *reinterpret_cast<const uint2 *>(scl + kStageRows + 16 * slab);    // high ones', halved
+          const uint2 k0 = *reinterpret_cast<const uint2 *>(scl + 16 * slab);              // low nibbles' scales
+          const uint2 k1 = *reinterpret_cast<const uint2 *>(scl + C::kRows + 16 * slab);   // high ones', divided
           const uint32_t a00 = hmul2(k0.x, kNeg1024), a01 = hmul2(k0.y, kNeg1024);
           const uint32_t a10 = hmul2(k1.x, kNeg1024), a11 = hmul2(k1.y, kNeg1024);
+          const uint32_t at = at0 + 16 * blk;
           uint32_t lo[8], hi[8];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            uint32_t ql = q[r] & 0x0F0F0F0Fu, qh = (q[r] >> 3) & 0x1E1E1E1Eu;   // q, and twice q
-            if constexpr (!kQ4) {
+            uint32_t ql = q[r] & 0x0F0F0F0Fu, qh;
+            if constexpr (kQ4) {
+              qh = q[r] & 0xF0F0F0F0u;                                          // 16 q
+            } else {
               const uint32_t hr = __funnelshift_l(h[r], h[r], rot);
               ql |= hr & 0x10101010u;
-              qh |= hr & 0x20202020u;
+              qh = ((q[r] >> 3) & 0x1E1E1E1Eu) | (hr & 0x20202020u);            // 2 q
             }
             lo[2 * r] = hfma2(__byte_perm(ql, 0x64u, 0x4140u), k0.x, a00);      // (1024 + q) s - 1024 s, exact
             lo[2 * r + 1] = hfma2(__byte_perm(ql, 0x64u, 0x4342u), k0.y, a01);
             hi[2 * r] = hfma2(__byte_perm(qh, 0x64u, 0x4140u), k1.x, a10);
             hi[2 * r + 1] = hfma2(__byte_perm(qh, 0x64u, 0x4342u), k1.y, a11);
           }
-          const uint32_t at = tbase + lane_base + C::kABase + (buf * C::kUS + s) * C::kSlab + 16 * blk;
-          st_16x256b(at, lo[0], lo[1], lo[2], lo[3]);
-          st_16x256b(at + (16u << 16), lo[4], lo[5], lo[6], lo[7]);
-          st_16x256b(at + 8, hi[0], hi[1], hi[2], hi[3]);
-          st_16x256b(at + 8 + (16u << 16), hi[4], hi[5], hi[6], hi[7]);
+          constexpr uint32_t kAt = s * C::kSlab, kUp = 16u << 16;
+          st_16x256b<kAt>(at, lo[0], lo[1], lo[2], lo[3]);
+          st_16x256b<kAt + kUp>(at, lo[4], lo[5], lo[6], lo[7]);
+          st_16x256b<kAt + 8>(at, hi[0], hi[1], hi[2], hi[3]);
+          st_16x256b<kAt + kUp + 8>(at, hi[4], hi[5], hi[6], hi[7]);
           if (blk == 0 && wq == 0) {                              // the mins of both blocks: lanes 0-7 and 8-15
             const uint2 m0 = *reinterpret_cast<const uint2 *>(mns + 16 * slab);
-            const uint2 m1 = *reinterpret_cast<const uint2 *>(mns + 8 * kStageRows + 16 * slab);
-            st_16x256b(at + 32, m0.x, m0.y, m1.x, m1.y);
+            const uint2 m1 = *reinterpret_cast<const uint2 *>(mns + 8 * C::kRows + 16 * slab);
+            st_16x256b<kAt + 32>(at, m0.x, m0.y, m1.x, m1.y);
           }
-        }
+        };
+        slab_to_tmem(std::integral_constant<int, 0>{});
+        if constexpr (C::kUS > 1) slab_to_tmem(std::integral_constant<int, 1>{});
+        if constexpr (C::kUS > 2) slab_to_tmem(std::integral_constant<int, 2>{});
+        if constexpr (C::kUS > 3) slab_to_tmem(std::integral_constant<int, 3>{});
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
@@ -534,18 +574,14 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       }
       if (!ok) break;
       __syncwarp();
-      if (lane == 0) {
-        ptx::mbar_arrive(&wempty[ws]);
-        ptx::mbar_arrive(&pempty[slot]);
-      }
-      if (++ws == C::kWStages) { ws = 0; wph ^= 1u; }
-      if (++slot == C::kSlots) { slot = 0; pph ^= 1u; }
+      if (lane == 0) ptx::mbar_arrive(&empty[slot]);
+      if (++slot == C::kStages) { slot = 0; pph ^= 1u; }
       // the accumulators before the ones now in use
-      if ((i + 1) % kFlushStages == 0 && i + 1 > kFlushStages) ok = flush();
+      if ((i + 1) % C::kFlush == 0 && i + 1 > C::kFlush && !(ok = flush())) break;
     }
-    while (ok && flushed < (n_st + kFlushStages - 1) / kFlushStages) ok = flush();
+    while (ok && flushed < (n_st + C::kFlush - 1) / C::kFlush) ok = flush();
     if (!ok && lane == 0) fail();
-    float *s_min = s_t;                         // [16 sub-blocks][NM]: every stage's t has been read
+    float *s_min = s_md;                        // [16 sub-blocks][NM]: every stage's mantissas have been read
     if (min_warp && ok && lane < 16) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -615,7 +651,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const BackwardAr
   const int hi = static_cast<int>(static_cast<int64_t>(a.k / 4) * (cr + 1) / cs) * 4;
   cluster_arrive();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const bool plain = *a.flag != 0u;
+  const bool plain = __ldcg(a.flag) != 0u;
   const double back = ldexp(1.0, min(row_exponent(a.gmax, b, gparts), 126) + scale_e);
   const int64_t stride = static_cast<int64_t>(a.batch) * a.k;
   float *gx = a.part + static_cast<int64_t>(b) * a.k;
@@ -624,9 +660,10 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const BackwardAr
   for (int j = lo + 4 * tid; j < hi; j += 4 * kFinishThreads) {
     float x[4] = {};
     if (!plain) {
-      float4 s = *reinterpret_cast<const float4 *>(gx + j);
+      float4 s = __ldcg(reinterpret_cast<const float4 *>(gx + j));
+#pragma unroll 8
       for (int p = 1; p < splits; ++p) {
-        const float4 o = *reinterpret_cast<const float4 *>(gx + p * stride + j);
+        const float4 o = __ldcg(reinterpret_cast<const float4 *>(gx + p * stride + j));
         s.x += o.x;
         s.y += o.y;
         s.z += o.z;
@@ -694,9 +731,10 @@ __global__ void __launch_bounds__(128) gamma_kernel(const BackwardArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int j = blockIdx.x * 128 + threadIdx.x;
   float v = 0.0f;
+#pragma unroll 8
   for (int b = 0; b < a.batch; ++b) {
     const int64_t at = static_cast<int64_t>(b) * a.k + j;
-    v = fmaf(a.part[at] * a.rms[b], a.hidden[at], v);
+    v = fmaf(__ldcg(a.part + at) * __ldcg(a.rms + b), a.hidden[at], v);
   }
   a.grad_gamma[j] = v;
 }
@@ -704,8 +742,8 @@ __global__ void __launch_bounds__(128) gamma_kernel(const BackwardArgs a) {
 // ---------------------------------------------------------------- host side
 int bwd_pairs(int k) { return (k / kBlockWeights + 1) / 2; }
 // As many shares of the rows as leave each SM one CTA.
-int bwd_splits(int64_t n_rows, int k, int num_sms) {
-  const int64_t stages = (n_rows + kStageRows - 1) / kStageRows;
+int bwd_splits(int64_t n_rows, int k, int num_sms, int rows) {
+  const int64_t stages = (n_rows + rows - 1) / rows;
   int64_t s = num_sms / bwd_pairs(k);
   if (s < 1) s = 1;
   return static_cast<int>(s < stages ? s : stages);
@@ -731,11 +769,14 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_
 }
 
 template <int NM, bool kQ4>
-cudaError_t launch_backward_nm(const BackwardArgs &a, const CUtensorMap &map, float scale_m, int gparts, int splits) {
+cudaError_t launch_backward_nm(const BackwardArgs &a, int gparts, int *splits) {
   using C = BwdCfg<NM, kQ4>;
+  CUtensorMap map;
+  cudaError_t e = tc_encode_boxes(&map, a.w, a.n_rows, a.k, a.q4, 2, C::kRows);
+  if (e != cudaSuccess) return e;
   static std::atomic<unsigned long long> configured{0};   // one bit per device; host threads may race here
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(configured.load(std::memory_order_acquire) & bit)) {
@@ -744,14 +785,18 @@ cudaError_t launch_backward_nm(const BackwardArgs &a, const CUtensorMap &map, fl
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
   const int pairs = bwd_pairs(a.k);
-  return launch_dependent(backward_tc_kernel<NM, kQ4>, dim3(static_cast<unsigned>(pairs * splits)), C::kThreads, C::kSmem, 1,
-                          a.stream, map, a, scale_m, gparts, pairs, splits);
+  *splits = bwd_splits(a.n_rows, a.k, a.num_sms, C::kRows);
+  return launch_dependent(backward_tc_kernel<NM, kQ4>, dim3(static_cast<unsigned>(pairs * *splits)), C::kThreads, C::kSmem,
+                          1, a.stream, map, a, gparts, pairs, *splits);
 }
 
 }  // namespace
 
 size_t backward_part_floats(int64_t n_rows, int k, int max_batch, int num_sms) {
-  return static_cast<size_t>(bwd_splits(n_rows, k, num_sms)) * max_batch * k;
+  return static_cast<size_t>(bwd_splits(n_rows, k, num_sms, 64)) * max_batch * k;
+}
+size_t backward_t_floats(int64_t n_rows, int max_batch) {
+  return static_cast<size_t>((n_rows + kPadRows - 1) / kPadRows * kPadRows) * max_batch;
 }
 size_t backward_misc_floats() { return 32 * kMaxParts + 32 + 1; }   // largest |gl|, RMS factors, flag
 
@@ -760,27 +805,24 @@ cudaError_t launch_backward(const BackwardArgs &a) {
   int scale_e = 0;
   const float scale_m = std::ldexp(std::frexp(a.scale, &scale_e), 12);
   scale_e -= 12;
-  CUtensorMap map;
-  cudaError_t e = tc_encode_boxes(&map, a.w, a.n_rows, a.k, a.q4, 2, kStageRows);
-  if (e != cudaSuccess) return e;
-  // largest |gl|: at least 2,048 values a part
-  int gparts = static_cast<int>(a.n_rows / 2048);
+  // at least 1,024 values a part
+  int gparts = static_cast<int>(a.n_rows / 1024);
   gparts = gparts < 1 ? 1 : gparts > kMaxParts ? kMaxParts : gparts;
-  e = launch_dependent(gmax_kernel, dim3(static_cast<unsigned>(gparts), static_cast<unsigned>(a.batch)), 256, 0, 1, a.stream,
-                       a.grad_logits, a.n_rows, a.gmax, a.flag);
+  cudaError_t e = launch_dependent(slope_kernel, dim3(static_cast<unsigned>(gparts), static_cast<unsigned>(a.batch)), 256, 0, 1,
+                                   a.stream, a, scale_m);
   if (e != cudaSuccess) return e;
-  const int splits = bwd_splits(a.n_rows, a.k, a.num_sms);
+  int splits = 1;
   const int slots = tc_batch_slots(a.batch);
   if (a.q4)
-    e = slots == 8    ? launch_backward_nm<8, true>(a, map, scale_m, gparts, splits)
-        : slots == 16 ? launch_backward_nm<16, true>(a, map, scale_m, gparts, splits)
-                      : launch_backward_nm<32, true>(a, map, scale_m, gparts, splits);
+    e = slots == 8    ? launch_backward_nm<8, true>(a, gparts, &splits)
+        : slots == 16 ? launch_backward_nm<16, true>(a, gparts, &splits)
+                      : launch_backward_nm<32, true>(a, gparts, &splits);
   else
-    e = slots == 8    ? launch_backward_nm<8, false>(a, map, scale_m, gparts, splits)
-        : slots == 16 ? launch_backward_nm<16, false>(a, map, scale_m, gparts, splits)
-                      : launch_backward_nm<32, false>(a, map, scale_m, gparts, splits);
+    e = slots == 8    ? launch_backward_nm<8, false>(a, gparts, &splits)
+        : slots == 16 ? launch_backward_nm<16, false>(a, gparts, &splits)
+                      : launch_backward_nm<32, false>(a, gparts, &splits);
   if (e != cudaSuccess) return e;
-  const int cs = a.k >= 8192 ? 8 : a.k >= 4096 ? 4 : 1;
+  const int cs = a.k >= 2048 ? 8 : 1;
   e = launch_dependent(finish_kernel, dim3(static_cast<unsigned>(a.batch * cs)), kFinishThreads, 0, cs, a.stream, a, splits,
                        gparts, scale_e);
   if (e != cudaSuccess || !a.grad_gamma || a.batch == 1) return e;

@@ -24,6 +24,7 @@ struct Workspace {
   float *b1_part;            // split-K batch-1 path: [chunks][n_rows] chunk partial sums
   unsigned int *b1_cnt;      // split-K batch-1 path: [12-row tiles] chunk arrivals, zero between forwards
   float *bwd_part;           // backward: the row shares' sums of the gradient by the normed input
+  float *bwd_t;              // backward: the gradient by the matrix product, eight rows v of a batch row together
   float *bwd_misc;           // backward: backward_misc_floats
 };
 
@@ -157,12 +158,14 @@ struct BackwardArgs {
   int k;
   int num_sms;
   float *part;                // workspace of backward_part_floats
+  float *t;                   // workspace of backward_t_floats
   float *gmax, *rms;          // workspace: largest |grad_logits| of parts of each row, RMS factors
   uint32_t *flag;             // workspace: a block's d or dmin is beyond the tensor cores' operands
   uint32_t *status;
   cudaStream_t stream;
 };
 size_t backward_part_floats(int64_t n_rows, int k, int max_batch, int num_sms);
+size_t backward_t_floats(int64_t n_rows, int max_batch);
 size_t backward_misc_floats();
 cudaError_t launch_backward(const BackwardArgs &a);
 

@@ -170,9 +170,9 @@ int muse_lmhead_init_format(muse_lmhead **out, int device, int64_t n_rows, int64
   h->max_batch = max_batch;
   h->num_sms = prop.multiProcessorCount;
 
-  // One zeroed allocation: keys | ticket | status | logprob pairs | x | activation packages |
+  // One allocation, zeroed but for the last two: keys | ticket | status | logprob pairs | x | activation packages |
   // shared-tile counters | shared-tile partial sums (those three for the tensor-core path) |
-  // chunk counters | chunk partial sums (the split-K batch-1 path) | backward shares' sums | its small arrays
+  // chunk counters | chunk partial sums (the split-K batch-1 path) | backward's small arrays | its shares' sums | its t
   const size_t keys_b = sizeof(unsigned long long) * MUSE_MAX_BATCH;
   const size_t misc_b = 256;
   const size_t lse_b = sizeof(float2) * static_cast<size_t>(max_batch) * muse::kMaxLseParts;
@@ -188,16 +188,18 @@ int muse_lmhead_init_format(muse_lmhead **out, int device, int64_t n_rows, int64
   const size_t bcnt_b = split ? (sizeof(unsigned int) * muse::b1_split_counters(n_rows) + 255) / 256 * 256 : 0;
   const size_t bpart_b = split ? sizeof(float) * muse::b1_split_floats(n_rows, static_cast<int>(k)) : 0;
   const size_t wpart_b = (sizeof(float) * muse::backward_part_floats(n_rows, static_cast<int>(k), max_batch, h->num_sms) + 255) / 256 * 256;
-  const size_t wrms_b = sizeof(float) * muse::backward_misc_floats();
   const size_t fwd_b = (keys_b + misc_b + lse_b + x_b + pkg_b + cnt_b + part_b + bcnt_b + bpart_b + 255) / 256 * 256;
-  const size_t total = fwd_b + wpart_b + wrms_b;
+  const size_t wt_b = sizeof(float) * muse::backward_t_floats(n_rows, max_batch);
+  const size_t wmisc_b = (sizeof(float) * muse::backward_misc_floats() + 255) / 256 * 256;
+  const size_t zeroed_b = fwd_b + wmisc_b;   // the rest is written before it is read
+  const size_t total = zeroed_b + wpart_b + wt_b;
   void *base = nullptr;
   e = cudaMalloc(&base, total);
   if (e != cudaSuccess) {
     delete h;
     return e == cudaErrorMemoryAllocation ? MUSE_ERR_NOMEM : cuda_fail(e);
   }
-  e = cudaMemset(base, 0, total);
+  e = cudaMemset(base, 0, zeroed_b);
   if (e != cudaSuccess) {
     cudaFree(base);
     delete h;
@@ -219,8 +221,9 @@ int muse_lmhead_init_format(muse_lmhead **out, int device, int64_t n_rows, int64
   h->ws.b1_cnt = bcnt_b ? reinterpret_cast<unsigned int *>(pb) : nullptr;
   h->ws.b1_part = bpart_b ? reinterpret_cast<float *>(pb + bcnt_b) : nullptr;
   h->ws_b1_cnt_bytes = bcnt_b;
-  h->ws.bwd_part = reinterpret_cast<float *>(p + fwd_b);
-  h->ws.bwd_misc = reinterpret_cast<float *>(p + fwd_b + wpart_b);
+  h->ws.bwd_misc = reinterpret_cast<float *>(p + fwd_b);
+  h->ws.bwd_part = reinterpret_cast<float *>(p + zeroed_b);
+  h->ws.bwd_t = reinterpret_cast<float *>(p + zeroed_b + wpart_b);
   *out = h;
   return MUSE_OK;
 }
@@ -602,6 +605,7 @@ int muse_lmhead_backward(muse_lmhead *h, const float *grad_logits, const float *
   a.k = static_cast<int>(h->k);
   a.num_sms = h->num_sms;
   a.part = h->ws.bwd_part;
+  a.t = h->ws.bwd_t;
   a.gmax = h->ws.bwd_misc;
   a.rms = a.gmax + muse::backward_misc_floats() - MUSE_MAX_BATCH - 1;
   a.flag = reinterpret_cast<uint32_t *>(a.rms + MUSE_MAX_BATCH);
