@@ -17,22 +17,22 @@
 //    and the largest |gl| of parts of each row, for a power of two that brings a
 //    row's t into f16's range.
 // 2. backward_tc_kernel: a CTA takes two block columns (512 inputs) and a share
-//    of the rows, 128 or 64 rows a stage.
+//    of the rows, 96 or 64 rows a stage.
 //    * weight producer warp: a 2-D TMA box of the stage's rows x two blocks.
 //    * operand warps: read the blocks' d, dmin and scales.  With d = md 2^e,
-//      1 <= |md| < 2, the power of two goes to the A side (A = sc q 2^e, at most
+//      1 <= |md| < 2, the power of two goes to the A side (A = sc (q - middle) 2^e, at most
 //      11 significant bits: exact in f16) and md to the B side: B = t md as the
 //      f16 pair (hi, lo), hi + lo = t md to 2^-22, rows of B side by side.  The
 //      mins are a product of their own, A' = m 2^e' for the 16 sub-blocks,
-//      B' = -t mdmin.
+//      B' = -t mdmin, with middle sc 2^e times B added to the same sums.
 //    * four unpack warpgroups, two for each block, alternating between units of
-//      16 to 64 rows: ldmatrix with transposition gives a thread four rows of
+//      16 to 48 rows: ldmatrix with transposition gives a thread four rows of
 //      one input, and tcgen05.st (16 lanes x 256 bits) takes exactly that
 //      fragment. 
 //    * MMA warp: per 16 rows four products of M = 128 (two nibble halves of two
-//      blocks) and two for the mins.  The tensor cores round their sums towards
-//      zero, about 2^-24 a step, which over a share's thousand steps would cost
-//      1e-4: every 128 rows the unpack warps add the accumulators to f32 sums of
+//      blocks) and four small ones for mins and middles.  The tensor cores round
+//      their sums towards zero, about 2^-24 a step, which over a share's thousand
+//      steps would cost 1e-4: every 256 or 288 rows the unpack warps add the accumulators to f32 sums of
 //      their own (two sets of accumulators, so that nobody waits).
 //    The shares' sums go to the workspace.
 // 3. finish_kernel: a cluster of CTAs a batch row adds the shares in their
@@ -58,9 +58,9 @@ namespace muse {
 namespace {
 
 constexpr int kMaxParts = 64;                 // of a row's largest |gl|
-constexpr int kPadRows = 128;                 // t is kept, as zeros, up to a multiple of this
+constexpr int kPadRows = 192;                 // t is kept, as zeros, up to a multiple of this
 constexpr int kTileCols = 2 * kBlockWeights;  // inputs of a CTA
-constexpr int kFlushRows = 128;               // between additions of the accumulators to the f32 sums
+constexpr int kFlushRows = 256;               // between additions of the accumulators to the f32 sums, about
 constexpr int kUnpackWarps = 16;
 constexpr uint32_t kTmem = 512;
 
@@ -86,8 +86,7 @@ __device__ __forceinline__ float cap_slope(float l, float cap, float inv_cap2) {
 // t[v/8][b][v%8] = gl * scale_m * slope, scale_m the scale's mantissa.
 __global__ void __launch_bounds__(256) slope_kernel(const BackwardArgs a, float scale_m) {
   __shared__ float s_max[8];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the main kernel's set-up beside this one
   const int b = blockIdx.y;
   const float *g = a.grad_logits + b * a.n_rows, *l = a.logits + b * a.n_rows;
   const int64_t octs = (a.n_rows + kPadRows - 1) / kPadRows * (kPadRows / 8);
@@ -121,20 +120,27 @@ template <int NM, bool kQ4>
 struct BwdCfg {
   static constexpr int kBB = kQ4 ? kBlockBytesQ4 : kBlockBytes;
   static constexpr int kRowBytes = 2 * kBB;
-  // Rows of a stage: 128 halve what every stage costs in barriers; with more
+  // Rows of a stage: the more, the less the barriers of a stage cost; with more
   // than 8 slots the stage's B tiles leave room for 64.
-  static constexpr int kRows = NM == 8 ? 128 : 64;
+  static constexpr int kRows = NM == 8 ? 96 : 64;
   static constexpr int kWBytes = kRows * kRowBytes;
   static constexpr int kN = 2 * NM;                               // B rows: hi, lo
   // Accumulator columns: with 8 slots hi and lo side by side (an MMA has 16
   // columns at least), else both into the same ones.
   static constexpr int kD = NM == 8 ? 16 : NM;
-  // B tiles: core matrices of 8 rows x 8 values, those along the rows v 16 bytes
-  // further apart than they are long: a warp's stores fall on all banks.
-  static constexpr int kLbo = kN * 16 + 16;
-  static constexpr int kBTile = kRows / 8 * kLbo;                 // f16 [kN][kRows]
+  // B: core matrices of 8 rows x 8 values; the rows are hi and lo of d and dmin
+  // of both blocks (kinds 0-3), ordered so that one MMA's rows lie together: hi
+  // and lo of a kind with 8 slots, else the kinds' hi, then their lo.  Core
+  // matrices along v lie 16 bytes further apart than the rows are long: a warp's
+  // stores fall on all banks.
+  static constexpr int kBRows = 4 * kN;
+  static constexpr int kLbo = kBRows * 16 + 16;
+  static constexpr int kB = kRows / 8 * kLbo;                     // f16 [kBRows][kRows]
+  __host__ __device__ static constexpr int row(int kind, int part) {
+    return NM == 8 ? kind * 16 + part * 8 : part * 4 * NM + kind * NM;
+  }
   static constexpr int kScl = 16 * kRows * 2;                     // f16 [2 blocks x 8][kRows]
-  static constexpr int kSide = 4 * kBTile + 2 * kScl;             // B of d, B' of dmin (two blocks each); scales; mins
+  static constexpr int kSide = kB + 2 * kScl;                     // B; scales; mins
   static constexpr int kStage = kWBytes + (kSide + 127) / 128 * 128;
   // Groups of four operand warps, taking the stages in turn.  One with 32
   // slots: its unpack threads need the registers for 32 sums.
@@ -147,14 +153,14 @@ struct BwdCfg {
   static_assert(kStages >= 3, "stage ring");
   static constexpr int kSmem = kStages * kStage + kFixed;
   // tensor memory: two sets of sums of four M-tiles and two min products, then a ring of units of kUS x 16 rows
-  static constexpr int kUS = NM == 32 ? 1 : kRows / 32;
+  static constexpr int kUS = NM == 32 ? 1 : NM == 16 ? 2 : 3;
   static constexpr int kUnits = kRows / (16 * kUS);               // units a stage
-  static constexpr int kSlab = 40;                                // columns of 16 rows: four M-tiles of 8, mins 8
+  static constexpr int kSlab = 48;                                // columns of 16 rows: four M-tiles of 8, mins 8, scales 8
   static constexpr int kABase = 12 * kD;
   static constexpr int kBufs = (512 - kABase) / (kSlab * kUS);
   static_assert(kBufs >= 2 && kUnits % 2 == 0, "unit ring");
-  static constexpr int kFlush = kFlushRows / kRows;               // stages between flushes
-  static constexpr uint32_t kIdesc = tc::idesc_f16_f32(128, kD);
+  static constexpr int kFlush = (kFlushRows + kRows - 1) / kRows;               // stages between flushes
+  static constexpr uint32_t kIdesc = tc::idesc_f16_f32(128, kD), kIdescPair = tc::idesc_f16_f32(128, 2 * kD);
 };
 
 template <uint32_t kOffset>
@@ -200,10 +206,20 @@ __device__ __forceinline__ void tma_box(void *dst, const CUtensorMap *map, int x
       : "memory");
 }
 
-// Odd sub-blocks' quants are taken out of the high nibbles as 2q (Q5_K, with the
-// fifth bit behind) or 16q (Q4_K): their scales are divided by as much.
+// Quants are taken out of a byte as 2^kLow q (low nibbles) and 2^kHigh q (high
+// ones), their scales divided by as much.  In A stands (q - middle) sc, middle =
+// 16 (Q5_K) or 8 (Q4_K): t sums to about 0 over a row, but its few large negative
+// and many small positive values do so apart, and around the quants' middle
+// neither part runs far ahead of the result (sums from 0 on had four times the
+// rounding).  With the multiples, 1024 + 2^k middle has five significant bits and
+// its product with a 6-bit scale is exact in f16, so one fma makes A.
 template <bool kQ4>
-constexpr float kHighFactor = kQ4 ? 0.0625f : 0.5f;
+struct Quant {
+  static constexpr int kLow = kQ4 ? 3 : 2, kHigh = kQ4 ? 4 : 3;
+  static constexpr float kMiddle = kQ4 ? 8.0f : 16.0f;
+  static constexpr uint32_t kNegLow = kQ4 ? 0xE440E440u : 0xE440E440u;    // -(1024 + 64): 8 x 8, 4 x 16
+  static constexpr uint32_t kNegHigh = kQ4 ? 0xE480E480u : 0xE480E480u;   // -(1024 + 128): 16 x 8, 8 x 16
+};
 
 // d (an f16 value) as md 2^e with -20 <= e <= 0 (a scale, and a sixteenth of it,
 // is then exact in f16): 1 <= |md| < 2 apart from smaller values of d, up to 4
@@ -262,7 +278,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tbase = *s_tmem;
+  constexpr uint32_t tbase = 0;                                   // the only allocation an SM has room for
   auto fail = [&]() {
     atomicOr(a.status, kStatusWaitTimeout);
     *s_abort = 1u;
@@ -280,6 +296,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------ weights
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // whatever wrote the weights is complete
     if (lane == 0) {
       const uint64_t policy = ptx::policy_evict_first();
       int issued = 0, slot = 0;
@@ -298,7 +315,12 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
+    // One thread issues all MMAs, so what it computes for each counts: tensor
+    // memory is addressed from 0 (all of it is this CTA's), descriptors are a
+    // slot's first one plus a constant (56 cycles an MMA when both were worked
+    // out each time, against 9 of the MMA itself).
     const bool issuer = tc::elect_one();
+    const uint64_t desc0 = tc::smem_desc_kmajor(ptx::smem_u32(smem + C::kWBytes), C::kLbo, 128);
     bool ok = true;
     int slot = 0, buf = 0;
     uint32_t pph = 0, tph = 0;
@@ -307,25 +329,29 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       const bool opens = i % C::kFlush == 0;
       if (opens && period >= 2 && !(ok = wait(&dfree[db], ((period >> 1) & 1) ^ 1))) break;
       if (!(ok = wait(&pfull[slot], pph))) break;
-      const uint32_t b0 = ptx::smem_u32(smem + slot * C::kStage + C::kWBytes);
-      const uint32_t dbase = tbase + db * 6 * C::kD;
+      const uint64_t desc = desc0 + static_cast<uint64_t>(slot) * (C::kStage >> 4);
+      const uint32_t d = db * 6 * C::kD;
+#pragma unroll
       for (int u = 0; u < C::kUnits; ++u) {
         if (!(ok = wait(&tfull[buf], tph))) break;
         tc::fence_after();
         if (issuer) {
+          const uint32_t ta = C::kABase + buf * (C::kUS * C::kSlab);
 #pragma unroll
           for (int s = 0; s < C::kUS; ++s) {
-            const uint32_t at = tbase + C::kABase + (buf * C::kUS + s) * C::kSlab;
-            const uint32_t kofs = static_cast<uint32_t>((u * C::kUS + s) * 2 * C::kLbo);
-            const bool acc = !opens || u > 0 || s > 0;
+            const bool acc = u > 0 || s > 0 || !opens;
 #pragma unroll
-            for (int mt = 0; mt < 6; ++mt) {                      // four M-tiles, then the mins of both blocks
-              const int kind = mt < 4 ? mt >> 1 : mt - 2;
-              const uint32_t d = dbase + mt * C::kD, ta = at + (mt < 4 ? mt : 4) * 8;
-              const uint32_t tile = b0 + kind * C::kBTile + kofs;
-              tc::mma_f16_tmemA(d, ta, tc::smem_desc_kmajor(tile, C::kLbo, 128), C::kIdesc, acc);
-              if (NM > 8)
-                tc::mma_f16_tmemA(d, ta, tc::smem_desc_kmajor(tile + (NM / 8) * 128, C::kLbo, 128), C::kIdesc, true);
+            for (int part = 0; part < (NM == 8 ? 1 : 2); ++part) {
+              // rows of B from (kind, part), 16 rows v from slab u * kUS + s
+              auto b_at = [&](int kind) {
+                return desc + ((C::row(kind, part) / 8 * 128 + (u * C::kUS + s) * 2 * C::kLbo) >> 4);
+              };
+#pragma unroll
+              for (int mt = 0; mt < 4; ++mt)
+                tc::mma_f16_tmemA(d + mt * C::kD, ta + s * C::kSlab + mt * 8, b_at(mt >> 1), C::kIdesc, acc || part > 0);
+              // mins of both blocks by B', scales by B: a block's own columns are read, the other's are not
+              tc::mma_f16_tmemA(d + 4 * C::kD, ta + s * C::kSlab + 32, b_at(2), C::kIdescPair, acc || part > 0);
+              tc::mma_f16_tmemA(d + 4 * C::kD, ta + s * C::kSlab + 40, b_at(0), C::kIdescPair, true);
             }
           }
           tc::commit(&tempty[buf]);
@@ -351,10 +377,9 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     const int grp = (warp - kUnpackWarps) >> 2;                   // takes the stages grp, grp + kGroups, ..
     const int pt = tid - 32 * kUnpackWarps - kPrepThreads * grp;
     // this thread's tasks of a stage: eight rows v of one batch row
-    constexpr int kOcts = C::kRows / 8, kTasks = NM * kOcts / kPrepThreads;
-    static_assert(kTasks * kPrepThreads == NM * kOcts, "whole tasks");
-    const int oct = pt % kOcts, b_first = pt / kOcts;
-    constexpr int kStepB = kPrepThreads / kOcts;
+    constexpr int kOcts = C::kRows / 8, kStepB = kPrepThreads / kOcts, kTasks = (NM + kStepB - 1) / kStepB;
+    static_assert(kTasks == 1 || kStepB * kOcts == kPrepThreads, "a thread without a first task has none");
+    const int oct = pt % kOcts, b_first = pt < kStepB * kOcts ? pt / kOcts : NM;
     asm volatile("griddepcontrol.wait;" ::: "memory");            // t and the rows' largest values
     float e2[kTasks];
     float4 t_next[kTasks][2];
@@ -392,11 +417,11 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
           int ed, em;
           md_at[blk * C::kRows + row] = split_d(dd.x, ed, big);
           md_at[(2 + blk) * C::kRows + row] = -split_d(dd.y, em, big);
-          const uint32_t pd = pack_half2(pow2(ed), kHighFactor<kQ4> * pow2(ed));   // odd sub-blocks' quants come multiplied
+          const uint32_t pd = pack_half2(pow2(ed - Quant<kQ4>::kLow), pow2(ed - Quant<kQ4>::kHigh));   // the quants come multiplied
           const uint32_t pm = pack_half2(pow2(em), pow2(em));
           const uint32_t sc[2] = {hdr.y & 0x3F3F3F3Fu, (hdr.w & 0x0F0F0F0Fu) | ((hdr.y >> 2) & 0x30303030u)};
           const uint32_t mn[2] = {hdr.z & 0x3F3F3F3Fu, ((hdr.w >> 4) & 0x0F0F0F0Fu) | ((hdr.z >> 2) & 0x30303030u)};
-          __half *scl = reinterpret_cast<__half *>(side + 4 * C::kBTile) + blk * 8 * C::kRows + row;
+          __half *scl = reinterpret_cast<__half *>(side + C::kB) + blk * 8 * C::kRows + row;
           __half *mns = scl + 16 * C::kRows;
           const uint32_t one = 0x3C003C00u;
 #pragma unroll
@@ -424,7 +449,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
           const float4 t0 = t_next[j][0], t1 = t_next[j][1];
           const float t[8] = {t0.x * e2[j], t0.y * e2[j], t0.z * e2[j], t0.w * e2[j],
                               t1.x * e2[j], t1.y * e2[j], t1.z * e2[j], t1.w * e2[j]};
-          uint8_t *tile = side + oct * C::kLbo + (b & 7) * 16;
+          uint8_t *tile = side + oct * C::kLbo + (b >> 3) * 128 + (b & 7) * 16;
 #pragma unroll
           for (int kind = 0; kind < 4; ++kind) {
             const float4 m0 = *reinterpret_cast<const float4 *>(md_at + kind * C::kRows + 8 * oct);
@@ -438,8 +463,8 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
               const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi[p]));
               lo[p] = pack_half2(x0 - h.x, x1 - h.y);
             }
-            *reinterpret_cast<uint4 *>(tile + kind * C::kBTile + (b >> 3) * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(tile + kind * C::kBTile + ((NM + b) >> 3) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4 *>(tile + C::row(kind, 0) / 8 * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(tile + C::row(kind, 1) / 8 * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
       }
@@ -454,7 +479,9 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     // ------------------------------------------------------------ unpacking
     const int blk = (warp >> 2) & 1, par = warp >> 3, wq = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(32 * wq) << 16;
-    const uint32_t rot = static_cast<uint32_t>(4 - 2 * wq) & 31u;   // high bit 2wq -> 4, 2wq + 1 -> 5
+    const uint32_t rot = static_cast<uint32_t>(6 - 2 * wq) & 31u;   // high bit 2wq -> 6, 2wq + 1 -> 7
+    const float middle1 = Quant<kQ4>::kMiddle * pow2((lane >> 2) & 1 ? Quant<kQ4>::kHigh : Quant<kQ4>::kLow);
+    const uint32_t middle = pack_half2(middle1, middle1);         // of sub-block lane/4, whose scale is divided
     const uint32_t src0 = ptx::smem_u32(smem) + (lane & 15) * C::kRowBytes + blk * C::kBB + 16 * (lane >> 4);
     // the f32 sums: inputs of M-tile warp/4 by batch row, and mins (lane: sub-block) of eight batch rows
     const int mt = warp >> 2;
@@ -512,8 +539,8 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     for (int i = 0; i < n_st; ++i) {
       if (!(ok = wait(&pfull[slot], pph))) break;   // the weights too: the operand warps have waited for them
       const uint8_t *side = smem + slot * C::kStage + C::kWBytes;
-      const __half *scl = reinterpret_cast<const __half *>(side + 4 * C::kBTile) + (blk * 8 + 2 * wq) * C::kRows + 4 * (lane & 3);
-      const __half *mns = reinterpret_cast<const __half *>(side + 4 * C::kBTile) + (16 + (lane >> 2)) * C::kRows + 4 * (lane & 3);
+      const __half *scl = reinterpret_cast<const __half *>(side + C::kB) + (blk * 8 + 2 * wq) * C::kRows + 4 * (lane & 3);
+      const __half *mns = reinterpret_cast<const __half *>(side + C::kB) + (16 + (lane >> 2)) * C::kRows + 4 * (lane & 3);
       for (int u = par; u < C::kUnits; u += 2) {
         if (unit >= C::kBufs && !(ok = wait(&tempty[buf], tph ^ 1u))) break;
         tc::fence_after();
@@ -528,21 +555,23 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
           if constexpr (!kQ4) load_transposed(src + kOffQh, h);
           const uint2 k0 = *reinterpret_cast<const uint2 *>(scl + 16 * slab);              // low nibbles' scales
           const uint2 k1 = *reinterpret_cast<const uint2 *>(scl + C::kRows + 16 * slab);   // high ones', divided
-          const uint32_t a00 = hmul2(k0.x, kNeg1024), a01 = hmul2(k0.y, kNeg1024);
-          const uint32_t a10 = hmul2(k1.x, kNeg1024), a11 = hmul2(k1.y, kNeg1024);
+          using Q = Quant<kQ4>;
+          const uint32_t a00 = hmul2(k0.x, Q::kNegLow), a01 = hmul2(k0.y, Q::kNegLow);
+          const uint32_t a10 = hmul2(k1.x, Q::kNegHigh), a11 = hmul2(k1.y, Q::kNegHigh);
           const uint32_t at = at0 + 16 * blk;
           uint32_t lo[8], hi[8];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            uint32_t ql = q[r] & 0x0F0F0F0Fu, qh;
+            uint32_t ql, qh;
             if constexpr (kQ4) {
-              qh = q[r] & 0xF0F0F0F0u;                                          // 16 q
+              ql = (q[r] << 3) & 0x78787878u;
+              qh = q[r] & 0xF0F0F0F0u;
             } else {
               const uint32_t hr = __funnelshift_l(h[r], h[r], rot);
-              ql |= hr & 0x10101010u;
-              qh = ((q[r] >> 3) & 0x1E1E1E1Eu) | (hr & 0x20202020u);            // 2 q
+              ql = ((q[r] << 2) & 0x3C3C3C3Cu) | (hr & 0x40404040u);
+              qh = ((q[r] >> 1) & 0x78787878u) | (hr & 0x80808080u);
             }
-            lo[2 * r] = hfma2(__byte_perm(ql, 0x64u, 0x4140u), k0.x, a00);      // (1024 + q) s - 1024 s, exact
+            lo[2 * r] = hfma2(__byte_perm(ql, 0x64u, 0x4140u), k0.x, a00);      // (1024 + 4q) s/4 - 1088 s/4, exact
             lo[2 * r + 1] = hfma2(__byte_perm(ql, 0x64u, 0x4342u), k0.y, a01);
             hi[2 * r] = hfma2(__byte_perm(qh, 0x64u, 0x4140u), k1.x, a10);
             hi[2 * r + 1] = hfma2(__byte_perm(qh, 0x64u, 0x4342u), k1.y, a11);
@@ -556,6 +585,10 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
             const uint2 m0 = *reinterpret_cast<const uint2 *>(mns + 16 * slab);
             const uint2 m1 = *reinterpret_cast<const uint2 *>(mns + 8 * C::kRows + 16 * slab);
             st_16x256b<kAt + 32>(at, m0.x, m0.y, m1.x, m1.y);
+            const __half *all = mns - 16 * C::kRows + 16 * slab;  // their scales, times the quants' middle
+            const uint2 s0 = *reinterpret_cast<const uint2 *>(all);
+            const uint2 s1 = *reinterpret_cast<const uint2 *>(all + 8 * C::kRows);
+            st_16x256b<kAt + 40>(at, hmul2(s0.x, middle), hmul2(s0.y, middle), hmul2(s1.x, middle), hmul2(s1.y, middle));
           }
         };
         slab_to_tmem(std::integral_constant<int, 0>{});
@@ -607,7 +640,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
   __syncthreads();
   if (warp == kMmaWarp) {
     tc::fence_after();
-    tc::dealloc(tbase, kTmem);
+    tc::dealloc(*s_tmem, kTmem);
   }
 }
 
@@ -808,8 +841,9 @@ cudaError_t launch_backward(const BackwardArgs &a) {
   // at least 1,024 values a part
   int gparts = static_cast<int>(a.n_rows / 1024);
   gparts = gparts < 1 ? 1 : gparts > kMaxParts ? kMaxParts : gparts;
-  cudaError_t e = launch_dependent(slope_kernel, dim3(static_cast<unsigned>(gparts), static_cast<unsigned>(a.batch)), 256, 0, 1,
-                                   a.stream, a, scale_m);
+  // an ordinary launch: after everything before it on the stream, the weights' own writer too
+  slope_kernel<<<dim3(static_cast<unsigned>(gparts), static_cast<unsigned>(a.batch)), 256, 0, a.stream>>>(a, scale_m);
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   int splits = 1;
   const int slots = tc_batch_slots(a.batch);

@@ -7,8 +7,14 @@ backward as a training step makes it.
 Tolerances (u = 2^-24): t_v carries six roundings; a weight or an operand split
 in two 16-bit halves is good to 2^-22 = 4u; a sum of V products in any order,
 kept in f32, is off by at most V u, and no kernel adds more than V/8 + 64 in a
-chain.  So |gx - exact| <= c sum_v |t_v W_vk| with c = (V/8 + 96) u.  The norm's
-backward passes that error on linearly and adds at most 40u of its terms.
+chain.  The products are those of a weight's parts, W = d sc (q - c0) + c0 d sc -
+dmin m with c0 the quants' middle: each part t_v P is rounded on its own scale,
+and where the parts of a W cancel (q = 0: -c0 d sc + c0 d sc) the rounding of
+each stays.  So |gx - exact| <= c sum_v |t_v| (|d sc (q - c0)| + |c0 d sc| + |dmin m|)
+with c = (V/8 + 96) u: a bound by sum |t_v W_vk| alone would hold for a kernel
+that adds rounded weights, and needs W's parts to be added before t, which no
+order of exact products does.  The norm's backward passes that error on linearly
+and adds at most 40u of its terms.
 """
 import numpy as np
 import pytest
@@ -38,19 +44,21 @@ def _weights(n, k, fmt, seed):
 
 
 def _dense(wq, n, k, fmt):
-    """The matrix in 64 bits, from the block layout (numpy, no code of the package)."""
+    """The matrix in 64 bits and the sizes of its weights' parts, from the block layout (numpy, no code of the package)."""
     size, qs0 = (176, 48) if fmt == "q5_k" else (144, 16)
     b = np.ascontiguousarray(wq).reshape(n, k // 256, size)
     half = b[:, :, :4].copy().view(np.float16).astype(np.float64)
-    out = np.empty((n, k // 256, 8, 32))
+    out, size_of, c0 = np.empty((n, k // 256, 8, 32)), np.empty((n, k // 256, 8, 32)), 16 if fmt == "q5_k" else 8
     for s in range(8):
         w0, w1, w2 = (b[:, :, 4 + 4 * i + s % 4].astype(np.int64) for i in range(3))
         sc, mn = (w0 & 63, w1 & 63) if s < 4 else ((w2 & 15) | (w0 >> 6 << 4), (w2 >> 4) | (w1 >> 6 << 4))
         q = (b[:, :, qs0 + 32 * (s // 2):qs0 + 32 * (s // 2) + 32].astype(np.int64) >> (4 * (s % 2))) & 15
         if fmt == "q5_k":
             q = q | (((b[:, :, 16:48].astype(np.int64) >> s) & 1) << 4)
-        out[:, :, s] = (half[:, :, 0] * sc)[..., None] * q - (half[:, :, 1] * mn)[..., None]
-    return out.reshape(n, k)
+        ds, dm = (half[:, :, 0] * sc)[..., None], (half[:, :, 1] * mn)[..., None]
+        out[:, :, s] = ds * q - dm
+        size_of[:, :, s] = np.abs(ds) * (np.abs(q - c0) + c0) + np.abs(dm)
+    return out.reshape(n, k), size_of.reshape(n, k)
 
 
 def _reference(gl, logits, hidden, gamma, w, scale, cap):
@@ -59,7 +67,8 @@ def _reference(gl, logits, hidden, gamma, w, scale, cap):
     if cap > 0:
         ld = logits.astype(np.float64)
         t = t * (cap - ld) * (cap + ld) / cap ** 2
-    gx, ax = t @ w, np.abs(t) @ np.abs(w)
+    w, parts = w
+    gx, ax = t @ w, np.abs(t) @ parts
     tol = (w.shape[0] / 8 + 96) * U * ax
     if gamma is None:
         return gx, tol, None, None
