@@ -245,7 +245,8 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(done + 1);
   volatile uint32_t *s_abort = s_tmem + 1;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the warp's index from one lane: the compiler then knows the roles' branches and loops to be uniform
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int pair = blockIdx.x % pairs, split = blockIdx.x / pairs;   // neighbours stream the same rows
   const int64_t stages = (a.n_rows + C::kRows - 1) / C::kRows;
   const int64_t st0 = stages * split / splits;
@@ -485,7 +486,9 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     const uint32_t src0 = ptx::smem_u32(smem) + (lane & 15) * C::kRowBytes + blk * C::kBB + 16 * (lane >> 4);
     // the f32 sums: inputs of M-tile warp/4 by batch row, and mins (lane: sub-block) of eight batch rows
     const int mt = warp >> 2;
-    const bool min_warp = wq == 0 && mt < NM / 8;
+    // mins: warpgroup mt's warp of quarter `mblk` reads block mblk's eight sub-blocks, batch rows 8 mt'..
+    const int mblk = wq, mcol = NM == 8 ? 0 : 8 * mt;
+    const bool min_warp = NM == 8 ? wq < 2 && mt == 2 * wq : wq < 2 && mt < NM / 8;
     unsigned long long sum[NM / 2], msum[4];    // pairs of batch rows
 #pragma unroll
     for (int j = 0; j < NM / 2; ++j) sum[j] = 0ull;
@@ -517,14 +520,12 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       if (min_warp) {
 #pragma unroll
         for (int h = 0; h < (NM == 8 ? 2 : 1); ++h) {
-          uint32_t x[8], y[8];
-          tc::ld_32x32b_x8(d + 4 * C::kD + 8 * (NM == 8 ? h : mt), x);
-          tc::ld_32x32b_x8(d + 5 * C::kD + 8 * (NM == 8 ? h : mt), y);
+          uint32_t x[8];
+          tc::ld_32x32b_x8(d + lane_base + (4 + mblk) * C::kD + mcol + 8 * h, x);
           tc::wait_ld();
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            msum[j] = add2(msum[j], pack2(__uint_as_float(lane < 8 ? x[2 * j] : y[2 * j]),
-                                          __uint_as_float(lane < 8 ? x[2 * j + 1] : y[2 * j + 1])));
+            msum[j] = add2(msum[j], pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])));
         }
       }
       tc::fence_before();
@@ -540,7 +541,8 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       if (!(ok = wait(&pfull[slot], pph))) break;   // the weights too: the operand warps have waited for them
       const uint8_t *side = smem + slot * C::kStage + C::kWBytes;
       const __half *scl = reinterpret_cast<const __half *>(side + C::kB) + (blk * 8 + 2 * wq) * C::kRows + 4 * (lane & 3);
-      const __half *mns = reinterpret_cast<const __half *>(side + C::kB) + (16 + (lane >> 2)) * C::kRows + 4 * (lane & 3);
+      // of sub-block lane/4 of block wq: the mins for one warpgroup, the scales for the other
+      const __half *small = reinterpret_cast<const __half *>(side + C::kB) + ((blk ? 0 : 16) + 8 * (wq & 1) + (lane >> 2)) * C::kRows + 4 * (lane & 3);
       for (int u = par; u < C::kUnits; u += 2) {
         if (unit >= C::kBufs && !(ok = wait(&tempty[buf], tph ^ 1u))) break;
         tc::fence_after();
@@ -581,14 +583,11 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
           st_16x256b<kAt + kUp>(at, lo[4], lo[5], lo[6], lo[7]);
           st_16x256b<kAt + 8>(at, hi[0], hi[1], hi[2], hi[3]);
           st_16x256b<kAt + kUp + 8>(at, hi[4], hi[5], hi[6], hi[7]);
-          if (blk == 0 && wq == 0) {                              // the mins of both blocks: lanes 0-7 and 8-15
-            const uint2 m0 = *reinterpret_cast<const uint2 *>(mns + 16 * slab);
-            const uint2 m1 = *reinterpret_cast<const uint2 *>(mns + 8 * C::kRows + 16 * slab);
-            st_16x256b<kAt + 32>(at, m0.x, m0.y, m1.x, m1.y);
-            const __half *all = mns - 16 * C::kRows + 16 * slab;  // their scales, times the quants' middle
-            const uint2 s0 = *reinterpret_cast<const uint2 *>(all);
-            const uint2 s1 = *reinterpret_cast<const uint2 *>(all + 8 * C::kRows);
-            st_16x256b<kAt + 40>(at, hmul2(s0.x, middle), hmul2(s0.y, middle), hmul2(s1.x, middle), hmul2(s1.y, middle));
+          // block wq's mins or scales times the middle: lanes 0-7 of this quarter (and, unread, 8-15)
+          if (wq < 2) {
+            const uint2 m = *reinterpret_cast<const uint2 *>(small + 16 * slab);
+            if (blk == 0) st_16x256b<kAt + 32>(at0, m.x, m.y, m.x, m.y);
+            else st_16x256b<kAt + 40>(at0, hmul2(m.x, middle), hmul2(m.y, middle), hmul2(m.x, middle), hmul2(m.y, middle));
           }
         };
         slab_to_tmem(std::integral_constant<int, 0>{});
@@ -615,12 +614,12 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     while (ok && flushed < (n_st + C::kFlush - 1) / C::kFlush) ok = flush();
     if (!ok && lane == 0) fail();
     float *s_min = s_md;                        // [16 sub-blocks][NM]: every stage's mantissas have been read
-    if (min_warp && ok && lane < 16) {
+    if (min_warp && ok && lane < 8) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 x = unpack2(msum[j]);
-        s_min[lane * NM + 8 * mt + 2 * j] = x.x;
-        s_min[lane * NM + 8 * mt + 2 * j + 1] = x.y;
+        s_min[(8 * mblk + lane) * NM + mcol + 2 * j] = x.x;
+        s_min[(8 * mblk + lane) * NM + mcol + 2 * j + 1] = x.y;
       }
     }
     ptx::named_bar_sync(1 + C::kGroups, 32 * kUnpackWarps);
