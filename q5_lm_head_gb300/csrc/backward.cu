@@ -145,7 +145,7 @@ struct BwdCfg {
   // Groups of four operand warps, taking the stages in turn.  One with 32
   // slots: its unpack threads need the registers for 32 sums.
   static constexpr int kGroups = NM == 32 ? 1 : 2;
-  static constexpr int kThreads = 32 * (kUnpackWarps + 4 * kGroups + 2);
+  static constexpr int kThreads = 32 * (kUnpackWarps + 4 * kGroups + 4);   // the weights' warp, two without a role, the MMAs'
   static constexpr int kT = 2 * 4 * kRows * 4;                    // a group's mantissas, two stages of [4][kRows]
   static constexpr int kFixed = kGroups * kT + 1024;
   static constexpr int kFit = (226 * 1024 - kFixed) / kStage;
@@ -252,7 +252,9 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
   const int64_t st0 = stages * split / splits;
   const int n_st = static_cast<int>(stages * (split + 1) / splits - st0);
   constexpr int kPrepThreads = 128;                               // of a group
-  constexpr int kMmaWarp = kUnpackWarps + 4 * C::kGroups, kTmaWarp = kMmaWarp + 1;
+  // The SM's scheduler of a warp is its index mod 4: the MMAs' goes to the one
+  // whose unpack warps have no mins to store, the weights' to another.
+  constexpr int kTmaWarp = kUnpackWarps + 4 * C::kGroups, kMmaWarp = kTmaWarp + 3;
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -373,14 +375,15 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     if (issuer) tc::commit(done);
     __syncwarp();
     if (!wait(done, 0) && lane == 0) fail();
-  } else if (warp >= kUnpackWarps) {
+  } else if (warp >= kUnpackWarps && warp < kTmaWarp) {
     // ------------------------------------------------------------ operands
     const int grp = (warp - kUnpackWarps) >> 2;                   // takes the stages grp, grp + kGroups, ..
     const int pt = tid - 32 * kUnpackWarps - kPrepThreads * grp;
     // this thread's tasks of a stage: eight rows v of one batch row
     constexpr int kOcts = C::kRows / 8, kStepB = kPrepThreads / kOcts, kTasks = (NM + kStepB - 1) / kStepB;
     static_assert(kTasks == 1 || kStepB * kOcts == kPrepThreads, "a thread without a first task has none");
-    const int oct = pt % kOcts, b_first = pt < kStepB * kOcts ? pt / kOcts : NM;
+    const int from_end = kPrepThreads - 1 - pt;                   // few batch rows: by the last warp, beside the MMAs'
+    const int oct = from_end % kOcts, b_first = from_end < kStepB * kOcts ? from_end / kOcts : NM;
     asm volatile("griddepcontrol.wait;" ::: "memory");            // t and the rows' largest values
     float e2[kTasks];
     float4 t_next[kTasks][2];
@@ -476,13 +479,14 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     }
     if (bad && lane == 0) fail();
     if (big) atomicOr(a.flag, 1u);
-  } else {
+  } else if (warp < kUnpackWarps) {
     // ------------------------------------------------------------ unpacking
     const int blk = (warp >> 2) & 1, par = warp >> 3, wq = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(32 * wq) << 16;
     const uint32_t rot = static_cast<uint32_t>(6 - 2 * wq) & 31u;   // high bit 2wq -> 6, 2wq + 1 -> 7
-    const float middle1 = Quant<kQ4>::kMiddle * pow2((lane >> 2) & 1 ? Quant<kQ4>::kHigh : Quant<kQ4>::kLow);
-    const uint32_t middle = pack_half2(middle1, middle1);         // of sub-block lane/4, whose scale is divided
+    // what this warpgroup's small operand is multiplied by: 1 for mins, the middle for scales (divided as sub-block lane/4's)
+    const float middle1 = blk ? Quant<kQ4>::kMiddle * pow2((lane >> 2) & 1 ? Quant<kQ4>::kHigh : Quant<kQ4>::kLow) : 1.0f;
+    const uint32_t middle = pack_half2(middle1, middle1);
     const uint32_t src0 = ptx::smem_u32(smem) + (lane & 15) * C::kRowBytes + blk * C::kBB + 16 * (lane >> 4);
     // the f32 sums: inputs of M-tile warp/4 by batch row, and mins (lane: sub-block) of eight batch rows
     const int mt = warp >> 2;
@@ -546,7 +550,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       for (int u = par; u < C::kUnits; u += 2) {
         if (unit >= C::kBufs && !(ok = wait(&tempty[buf], tph ^ 1u))) break;
         tc::fence_after();
-        const uint32_t at0 = tbase + lane_base + C::kABase + buf * C::kUS * C::kSlab;
+        const uint32_t at0 = tbase + lane_base + C::kABase + buf * C::kUS * C::kSlab, at_small = at0 + 8 * blk;
         const uint32_t src1 = src0 + slot * C::kStage + u * C::kUS * 16 * C::kRowBytes;
         auto slab_to_tmem = [&](auto s_const) {
           constexpr int s = decltype(s_const)::value;
@@ -557,6 +561,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
           if constexpr (!kQ4) load_transposed(src + kOffQh, h);
           const uint2 k0 = *reinterpret_cast<const uint2 *>(scl + 16 * slab);              // low nibbles' scales
           const uint2 k1 = *reinterpret_cast<const uint2 *>(scl + C::kRows + 16 * slab);   // high ones', divided
+          uint2 m = *reinterpret_cast<const uint2 *>(small + 16 * slab);
           using Q = Quant<kQ4>;
           const uint32_t a00 = hmul2(k0.x, Q::kNegLow), a01 = hmul2(k0.y, Q::kNegLow);
           const uint32_t a10 = hmul2(k1.x, Q::kNegHigh), a11 = hmul2(k1.y, Q::kNegHigh);
@@ -584,11 +589,9 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
           st_16x256b<kAt + 8>(at, hi[0], hi[1], hi[2], hi[3]);
           st_16x256b<kAt + kUp + 8>(at, hi[4], hi[5], hi[6], hi[7]);
           // block wq's mins or scales times the middle: lanes 0-7 of this quarter (and, unread, 8-15)
-          if (wq < 2) {
-            const uint2 m = *reinterpret_cast<const uint2 *>(small + 16 * slab);
-            if (blk == 0) st_16x256b<kAt + 32>(at0, m.x, m.y, m.x, m.y);
-            else st_16x256b<kAt + 40>(at0, hmul2(m.x, middle), hmul2(m.y, middle), hmul2(m.x, middle), hmul2(m.y, middle));
-          }
+          m.x = hmul2(m.x, middle);
+          m.y = hmul2(m.y, middle);
+          if (wq < 2) st_16x256b<kAt + 32>(at_small, m.x, m.y, m.x, m.y);
         };
         slab_to_tmem(std::integral_constant<int, 0>{});
         if constexpr (C::kUS > 1) slab_to_tmem(std::integral_constant<int, 1>{});
