@@ -21,8 +21,8 @@
 //    * weight producer warp: a 2-D TMA box of the stage's rows x two blocks.
 //    * operand warps: read the blocks' d, dmin and scales.  With d = md 2^e,
 //      1 <= |md| < 2, the power of two goes to the A side (A = sc (q - middle) 2^e, at most
-//      11 significant bits: exact in f16) and md to the B side: B = t md as the
-//      f16 pair (hi, lo), hi + lo = t md to 2^-22, rows of B side by side.  The
+//      11 significant bits: exact in f16) and md, exact in f16 too, to the B side: B = t md as the
+//      f16 pair (hi, lo), hi + lo = t md to 2^-21, rows of B side by side.  The
 //      mins are a product of their own, A' = m 2^e' for the 16 sub-blocks,
 //      B' = -t mdmin, with middle sc 2^e times B added to the same sums.
 //    * four unpack warpgroups, two for each block, alternating between units of
@@ -119,7 +119,9 @@ __global__ void __launch_bounds__(256) slope_kernel(const BackwardArgs a, float 
 template <int NM, bool kQ4>
 struct BwdCfg {
   static constexpr int kBB = kQ4 ? kBlockBytesQ4 : kBlockBytes;
-  static constexpr int kRowBytes = 2 * kBB;
+  // A box row is two blocks and the next 16 bytes: rows 368 (304) bytes apart put
+  // eight rows' 16-byte pieces, which a transposing load takes at once, on all banks.
+  static constexpr int kRowBytes = 2 * kBB + 16;
   // Rows of a stage: the more, the less the barriers of a stage cost; with more
   // than 8 slots the stage's B tiles leave room for 64.
   static constexpr int kRows = NM == 8 ? 96 : 64;
@@ -141,12 +143,11 @@ struct BwdCfg {
   }
   static constexpr int kScl = 16 * kRows * 2;                     // f16 [2 blocks x 8][kRows]
   static constexpr int kSide = kB + 2 * kScl;                     // B; scales; mins
-  static constexpr int kStage = kWBytes + (kSide + 127) / 128 * 128;
-  // Groups of four operand warps, taking the stages in turn.  One with 32
-  // slots: its unpack threads need the registers for 32 sums.
-  static constexpr int kGroups = NM == 32 ? 1 : 2;
+  static constexpr int kStage = (kWBytes + kSide + 127) / 128 * 128;
+  static constexpr int kGroups = 2;                               // of four operand warps, taking the stages in turn
   static constexpr int kThreads = 32 * (kUnpackWarps + 4 * kGroups + 4);   // the weights' warp, two without a role, the MMAs'
-  static constexpr int kT = 2 * 4 * kRows * 4;                    // a group's mantissas, two stages of [4][kRows]
+  static constexpr int kT = 2 * 4 * kRows * 2;                    // a group's mantissas, f16, two stages of [4][kRows]
+  static_assert(kGroups * kT >= 16 * NM * 4, "the mins' sums");
   static constexpr int kFixed = kGroups * kT + 1024;
   static constexpr int kFit = (226 * 1024 - kFixed) / kStage;
   static constexpr int kStages = kFit > 5 ? 5 : kFit;
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     backward_tc_kernel(const __grid_constant__ CUtensorMap wmap, const BackwardArgs a, int gparts, int pairs, int splits) {
   using C = BwdCfg<NM, kQ4>;
   extern __shared__ __align__(1024) uint8_t smem[];                // [kStages][weights, B tiles, scales, mins]
-  float *s_md = reinterpret_cast<float *>(smem + C::kStages * C::kStage);   // [kGroups][kT]
+  __half *s_md = reinterpret_cast<__half *>(smem + C::kStages * C::kStage);   // [kGroups][kT]
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kStages * C::kStage + C::kGroups * C::kT);
   uint64_t *wfull = bars, *pfull = wfull + C::kStages, *empty = pfull + C::kStages;
   uint64_t *tfull = empty + C::kStages, *tempty = tfull + C::kBufs;
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       for (int i = 0; i < n_st; ++i) {
         if (i >= C::kStages && !wait_one(&empty[slot], ph ^ 1u)) { fail(); break; }
         ptx::mbar_arrive_expect_tx(&wfull[slot], C::kWBytes);
-        tma_box(smem + slot * C::kStage, &wmap, pair * (C::kRowBytes / 4), static_cast<int>((st0 + i) * C::kRows), &wfull[slot],
+        tma_box(smem + slot * C::kStage, &wmap, pair * (C::kBB / 2), static_cast<int>((st0 + i) * C::kRows), &wfull[slot],
                 policy);
         issued = i + 1;
         if (++slot == C::kStages) { slot = 0; ph ^= 1u; }
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     int turn = 0;
     for (int i = grp; i < n_st; i += C::kGroups, turn ^= 1) {
       const int slot = i % C::kStages;
-      float *md_at = s_md + grp * (C::kT / 4) + turn * 4 * C::kRows;
+      __half *md_at = s_md + grp * (C::kT / 2) + turn * 4 * C::kRows;
       // the stage's weights: they were sent for only after the slot's last readers were done with it
       bad = !wait(&wfull[slot], (i / C::kStages) & 1);
       uint8_t *st = smem + slot * C::kStage, *side = st + C::kWBytes;
@@ -419,8 +420,8 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
           const uint4 hdr = *reinterpret_cast<const uint4 *>(st + row * C::kRowBytes + blk * C::kBB);
           const float2 dd = __half22float2(*reinterpret_cast<const __half2 *>(&hdr.x));
           int ed, em;
-          md_at[blk * C::kRows + row] = split_d(dd.x, ed, big);
-          md_at[(2 + blk) * C::kRows + row] = -split_d(dd.y, em, big);
+          md_at[blk * C::kRows + row] = __float2half_rn(split_d(dd.x, ed, big));
+          md_at[(2 + blk) * C::kRows + row] = __float2half_rn(-split_d(dd.y, em, big));
           const uint32_t pd = pack_half2(pow2(ed - Quant<kQ4>::kLow), pow2(ed - Quant<kQ4>::kHigh));   // the quants come multiplied
           const uint32_t pm = pack_half2(pow2(em), pow2(em));
           const uint32_t sc[2] = {hdr.y & 0x3F3F3F3Fu, (hdr.w & 0x0F0F0F0Fu) | ((hdr.y >> 2) & 0x30303030u)};
@@ -451,21 +452,26 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
         const int b = b_first + j * kStepB;
         if (b < a.batch) {
           const float4 t0 = t_next[j][0], t1 = t_next[j][1];
-          const float t[8] = {t0.x * e2[j], t0.y * e2[j], t0.z * e2[j], t0.w * e2[j],
-                              t1.x * e2[j], t1.y * e2[j], t1.z * e2[j], t1.w * e2[j]};
+          // t as th + tl, once for the four kinds
+          const float t[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+          uint32_t th[4], tl[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const float x0 = t[2 * p] * e2[j], x1 = t[2 * p + 1] * e2[j];
+            th[p] = pack_half2(x0, x1);
+            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&th[p]));
+            tl[p] = pack_half2(x0 - h.x, x1 - h.y);
+          }
           uint8_t *tile = side + oct * C::kLbo + (b >> 3) * 128 + (b & 7) * 16;
 #pragma unroll
           for (int kind = 0; kind < 4; ++kind) {
-            const float4 m0 = *reinterpret_cast<const float4 *>(md_at + kind * C::kRows + 8 * oct);
-            const float4 m1 = *reinterpret_cast<const float4 *>(md_at + kind * C::kRows + 8 * oct + 4);
-            const float md[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+            const uint4 m = *reinterpret_cast<const uint4 *>(md_at + kind * C::kRows + 8 * oct);
+            const uint32_t md[4] = {m.x, m.y, m.z, m.w};
             uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              const float x0 = t[2 * p] * md[2 * p], x1 = t[2 * p + 1] * md[2 * p + 1];
-              hi[p] = pack_half2(x0, x1);
-              const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi[p]));
-              lo[p] = pack_half2(x0 - h.x, x1 - h.y);
+            for (int p = 0; p < 4; ++p) {       // (th + tl) md: th md rounded, its remainder (exact) and tl md
+              hi[p] = hmul2(th[p], md[p]);
+              lo[p] = hfma2(tl[p], md[p], hfma2(th[p], md[p], hi[p] ^ 0x80008000u));
             }
             *reinterpret_cast<uint4 *>(tile + C::row(kind, 0) / 8 * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(tile + C::row(kind, 1) / 8 * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -561,7 +567,8 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
           if constexpr (!kQ4) load_transposed(src + kOffQh, h);
           const uint2 k0 = *reinterpret_cast<const uint2 *>(scl + 16 * slab);              // low nibbles' scales
           const uint2 k1 = *reinterpret_cast<const uint2 *>(scl + C::kRows + 16 * slab);   // high ones', divided
-          uint2 m = *reinterpret_cast<const uint2 *>(small + 16 * slab);
+          uint2 m = make_uint2(0u, 0u);
+          if (wq < 2) m = *reinterpret_cast<const uint2 *>(small + 16 * slab);
           using Q = Quant<kQ4>;
           const uint32_t a00 = hmul2(k0.x, Q::kNegLow), a01 = hmul2(k0.y, Q::kNegLow);
           const uint32_t a10 = hmul2(k1.x, Q::kNegHigh), a11 = hmul2(k1.y, Q::kNegHigh);
@@ -589,9 +596,11 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
           st_16x256b<kAt + 8>(at, hi[0], hi[1], hi[2], hi[3]);
           st_16x256b<kAt + kUp + 8>(at, hi[4], hi[5], hi[6], hi[7]);
           // block wq's mins or scales times the middle: lanes 0-7 of this quarter (and, unread, 8-15)
-          m.x = hmul2(m.x, middle);
-          m.y = hmul2(m.y, middle);
-          if (wq < 2) st_16x256b<kAt + 32>(at_small, m.x, m.y, m.x, m.y);
+          if (wq < 2) {
+            m.x = hmul2(m.x, middle);
+            m.y = hmul2(m.y, middle);
+            st_16x256b<kAt + 32>(at_small, m.x, m.y, m.x, m.y);
+          }
         };
         slab_to_tmem(std::integral_constant<int, 0>{});
         if constexpr (C::kUS > 1) slab_to_tmem(std::integral_constant<int, 1>{});
@@ -616,7 +625,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     }
     while (ok && flushed < (n_st + C::kFlush - 1) / C::kFlush) ok = flush();
     if (!ok && lane == 0) fail();
-    float *s_min = s_md;                        // [16 sub-blocks][NM]: every stage's mantissas have been read
+    float *s_min = reinterpret_cast<float *>(s_md);   // [16 sub-blocks][NM]: every stage's mantissas have been read
     if (min_warp && ok && lane < 8) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -807,7 +816,7 @@ template <int NM, bool kQ4>
 cudaError_t launch_backward_nm(const BackwardArgs &a, int gparts, int *splits) {
   using C = BwdCfg<NM, kQ4>;
   CUtensorMap map;
-  cudaError_t e = tc_encode_boxes(&map, a.w, a.n_rows, a.k, a.q4, 2, C::kRows);
+  cudaError_t e = tc_encode_boxes(&map, a.w, a.n_rows, a.k, a.q4, C::kRowBytes, C::kRows);
   if (e != cudaSuccess) return e;
   static std::atomic<unsigned long long> configured{0};   // one bit per device; host threads may race here
   int dev = 0;
