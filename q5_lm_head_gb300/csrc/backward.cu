@@ -33,7 +33,7 @@
 //      blocks) and four small ones for mins and middles.  The tensor cores round
 //      their sums towards zero, about 2^-24 a step, which over a share's thousand
 //      steps would cost 1e-4: every 256 or 288 rows the unpack warps add the accumulators to f32 sums of
-//      their own (two sets of accumulators, so that nobody waits).
+//      their own.
 //    The shares' sums go to the workspace.
 // 3. finish_kernel: a cluster of CTAs a batch row adds the shares in their
 //    order, undoes the power of two and does the norm's backward.
@@ -153,13 +153,17 @@ struct BwdCfg {
   static constexpr int kStages = kFit > 5 ? 5 : kFit;
   static_assert(kStages >= 3, "stage ring");
   static constexpr int kSmem = kStages * kStage + kFixed;
-  // tensor memory: two sets of sums of four M-tiles and two min products, then a ring of units of kUS x 16 rows
-  static constexpr int kUS = NM == 32 ? 1 : NM == 16 ? 2 : 3;
+  // Tensor memory: sets of sums of four M-tiles and two min products, then a ring
+  // of units of kUS x 16 rows.  Two sets, so that one is added up while the other
+  // is in use; with 32 slots one, or the ring would have two units of 16 rows only
+  // (532 us for a full head's 32 rows, REPLACE).
+  static constexpr int kSets = NM == 32 ? 1 : 2;
+  static constexpr int kUS = NM == 8 ? 3 : 2;
   static constexpr int kUnits = kRows / (16 * kUS);               // units a stage
   static constexpr int kSlab = 48;                                // columns of 16 rows: four M-tiles of 8, mins 8, scales 8
-  static constexpr int kABase = 12 * kD;
+  static constexpr int kABase = kSets * 6 * kD;
   static constexpr int kBufs = (512 - kABase) / (kSlab * kUS);
-  static_assert(kBufs >= 2 && kUnits % 2 == 0, "unit ring");
+  static_assert(kBufs >= 2 && kUnits % 2 == 0 && (kSets == 2 || kBufs >= kUnits), "unit ring");
   static constexpr int kFlush = (kFlushRows + kRows - 1) / kRows;               // stages between flushes
   static constexpr uint32_t kIdesc = tc::idesc_f16_f32(128, kD), kIdescPair = tc::idesc_f16_f32(128, 2 * kD);
 };
@@ -329,9 +333,9 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     int slot = 0, buf = 0;
     uint32_t pph = 0, tph = 0;
     for (int i = 0; i < n_st && ok; ++i) {
-      const int period = i / C::kFlush, db = period & 1;
+      const int period = i / C::kFlush, db = period % C::kSets;
       const bool opens = i % C::kFlush == 0;
-      if (opens && period >= 2 && !(ok = wait(&dfree[db], ((period >> 1) & 1) ^ 1))) break;
+      if (opens && period >= C::kSets && !(ok = wait(&dfree[db], ((period / C::kSets) & 1) ^ 1))) break;
       if (!(ok = wait(&pfull[slot], pph))) break;
       const uint64_t desc = desc0 + static_cast<uint64_t>(slot) * (C::kStage >> 4);
       const uint32_t d = db * 6 * C::kD;
@@ -506,8 +510,8 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     for (int j = 0; j < 4; ++j) msum[j] = 0ull;
     int flushed = 0;
     auto flush = [&]() {
-      const int db = flushed & 1;
-      if (!wait(&dfull[db], (flushed >> 1) & 1)) return false;
+      const int db = flushed % C::kSets;
+      if (!wait(&dfull[db], (flushed / C::kSets) & 1)) return false;
       tc::fence_after();
       const uint32_t d = tbase + db * 6 * C::kD;
 #pragma unroll
@@ -620,8 +624,9 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&empty[slot]);
       if (++slot == C::kStages) { slot = 0; pph ^= 1u; }
-      // the accumulators before the ones now in use
-      if ((i + 1) % C::kFlush == 0 && i + 1 > C::kFlush && !(ok = flush())) break;
+      // the set before the one now in use; or the only set, one stage after its last (the ring holds that stage)
+      const bool due = C::kSets == 2 ? (i + 1) % C::kFlush == 0 && i + 1 > C::kFlush : i % C::kFlush == 0 && i > 0;
+      if (due && !(ok = flush())) break;
     }
     while (ok && flushed < (n_st + C::kFlush - 1) / C::kFlush) ok = flush();
     if (!ok && lane == 0) fail();
