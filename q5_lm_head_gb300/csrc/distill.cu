@@ -9,9 +9,9 @@
 //     dloss/dx_i = w/T [ (sum p + p_t) q_i - sum_{j: id_j = i} p_j - [i not in S] p_t q_i / q_t ]
 //
 // Bound: HBM, each logit read once and each gradient written once.  A cluster
-// of CTAs holds a row in its shared memory (in the logits' type, up to 104 KB a
-// CTA, so that two CTAs of an SM overlap one's loads with the other's stores),
-// and one barrier of the cluster joins the CTAs' maxima and sums.  The sum
+// of CTAs holds a row in its shared memory (in the logits' type, up to 52 KB a
+// CTA, so that four CTAs of an SM overlap their loads, sums and stores), and one
+// barrier of the cluster joins the CTAs' maxima and sums.  The sum
 // outside S is taken apart from the sum inside, not as a difference: where the
 // student is sure of the teacher's ids a difference would be rounding alone.
 // The ids' values are taken out of the row (set to -infinity) before the sum.
@@ -21,15 +21,16 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 #include "rows.cuh"
 
 namespace muse {
 namespace {
 
-constexpr int kDistillThreads = 512;
+constexpr int kDistillThreads = 256;
 constexpr int kDistillWarps = kDistillThreads / 32;
 constexpr int kDistillCluster = 16;
-constexpr int kHeldTwo = 104 * 1024;     // bytes of a row in a CTA: two CTAs an SM
+constexpr int kHeldFour = 52 * 1024;     // bytes of a row in a CTA: four CTAs an SM
 constexpr int kHeldOne = 216 * 1024;     // one CTA an SM
 constexpr float kLog2eD = 1.4426950408889634f;
 constexpr double kLn2D = 0.6931471805599453;
@@ -38,7 +39,7 @@ struct DistillShared {
   int id[kMaxTop];                       // -1: left out
   float p[kMaxTop], lp[kMaxTop];         // probability and its logarithm
   float x[kMaxTop];                      // the ids' logits: this CTA's own; all of them in the first CTA
-  float m[kDistillWarps], s[kDistillWarps];
+  float m[kDistillWarps], rest[kDistillWarps], in[kDistillWarps];   // the warps' maxima and sums
   float mass;
   float from_m[kDistillCluster], from_rest[kDistillCluster], from_in[kDistillCluster];
 };
@@ -55,7 +56,7 @@ __device__ __forceinline__ float move_sum(float s, float from, float to, float c
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const DistillArgs a) {
+__global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const DistillArgs a) {
   constexpr int W = Vec<T>::W;
   extern __shared__ __align__(16) uint8_t held[];
   __shared__ DistillShared sh;
@@ -99,8 +100,8 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const Disti
       sh.id[tid] = ok ? id : -1;
       sh.lp[tid] = ok ? l : -INFINITY;
       if (id >= first && id < first + count) own = id - first;
+      ptx::named_bar_sync(1, kMaxTop);
     }
-    __syncthreads();
     if (warp == 0) {                      // the teacher's probabilities
       float l0 = sh.lp[lane], l1 = sh.lp[lane + 32], shift = 0.0f;
       if (!a.tail) {
@@ -127,14 +128,15 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const Disti
     __syncthreads();
     // the ids' values out of the row
     float mine = -INFINITY, in_m = -INFINITY;
-    if (own >= 0) mine = to_float(row_held[own]);
-    __syncthreads();
     bool again = false;                   // an id that an earlier entry has
-    if (own >= 0) {
-      row_held[own] = from_float<T>(-INFINITY);
-      for (int j = 0; j < tid; ++j) again |= sh.id[j] == first + own;
-      in_m = mine;
-      sh.x[tid] = mine;
+    if (tid < kMaxTop) {
+      if (own >= 0) in_m = mine = to_float(row_held[own]);
+      ptx::named_bar_sync(1, kMaxTop);    // an id given twice: both have read it
+      if (own >= 0) {
+        row_held[own] = from_float<T>(-INFINITY);
+        for (int j = 0; j < tid; ++j) again |= sh.id[j] == first + own;
+        sh.x[tid] = mine;
+      }
     }
     if (edge_i >= 0)
       for (int j = 0; j < k; ++j)
@@ -172,35 +174,35 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const Disti
         for (int j = 0; j < W; ++j) s2 = add2(s2, pack2(exp2_approx(exponent(o[j], ref, c)), 0.0f));
       }
     }
-    float rest = unpack2(s2).x + unpack2(s2).y;
-    // the CTA's maximum, the edges and ids with it, then its sums against that
-    float cm = fmaxf(fmaxf(top, edge), in_m);
-    cm = order_key_float(__reduce_max_sync(0xffffffffu, float_order_key(cm)));
-    if (lane == 0) sh.m[warp] = cm;
-    __syncthreads();
-    cm = order_key_float(__reduce_max_sync(0xffffffffu, float_order_key(sh.m[lane & (kDistillWarps - 1)])));
+    float rest = unpack2(s2).x + unpack2(s2).y, in = 0.0f;
+    // the warp's maximum, edges and ids with it, and its sums against that
+    float cm = order_key_float(__reduce_max_sync(0xffffffffu, float_order_key(fmaxf(fmaxf(top, edge), in_m))));
     const float cref = cm == -INFINITY ? 0.0f : cm;
     rest = move_sum(rest, top, cm, c);
-    float in = 0.0f;
     if (edge_i >= 0) (edge_in ? in : rest) += exp2_approx(exponent(edge, cref, c));
     if (own >= 0 && !again) in += exp2_approx(exponent(mine, cref, c));
     for (int o = 16; o > 0; o >>= 1) {
       rest += __shfl_xor_sync(0xffffffffu, rest, o);
       in += __shfl_xor_sync(0xffffffffu, in, o);
     }
-    __syncthreads();
     if (lane == 0) {
-      sh.m[warp] = rest;
-      sh.s[warp] = in;
+      sh.m[warp] = cm;
+      sh.rest[warp] = rest;
+      sh.in[warp] = in;
     }
     __syncthreads();
-    if (warp == 0) {
-      rest = lane < kDistillWarps ? sh.m[lane] : 0.0f;
-      in = lane < kDistillWarps ? sh.s[lane] : 0.0f;
-      for (int o = 16; o > 0; o >>= 1) {
-        rest += __shfl_xor_sync(0xffffffffu, rest, o);
-        in += __shfl_xor_sync(0xffffffffu, in, o);
-      }
+    // the CTA's, in every thread
+    const bool a_warp = lane < kDistillWarps;
+    cm = a_warp ? sh.m[lane] : -INFINITY;
+    {
+      const float all = order_key_float(__reduce_max_sync(0xffffffffu, float_order_key(cm)));
+      rest = a_warp ? move_sum(sh.rest[lane], cm, all, c) : 0.0f;
+      in = a_warp ? move_sum(sh.in[lane], cm, all, c) : 0.0f;
+      cm = all;
+    }
+    for (int o = 16; o > 0; o >>= 1) {   // lanes without a warp add 0
+      rest += __shfl_xor_sync(0xffffffffu, rest, o);
+      in += __shfl_xor_sync(0xffffffffu, in, o);
     }
     cluster_wait();                       // every CTA of the cluster has started
     if (tid < static_cast<int>(cs)) {     // to every CTA, so that all go on with the same bits
@@ -272,23 +274,26 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const Disti
     // the gradient outside S; the ids' places are 0 here (-infinity in the row)
     if (scale != 0.0f) {
       const bool plain = fabsf(m) < kPlain;
-      const float rc = -__fmul_rn(m, c);
-      auto grad_of = [&](float xi) { return exp2_approx(plain ? fmaf(xi, c, rc) : (xi - m) * c) * f_out; };
-      if ((reinterpret_cast<uintptr_t>(g + first) & 15) == 0) {
+      if (plain && (reinterpret_cast<uintptr_t>(g + first) & 15) == 0) {
         uint4 *gv = reinterpret_cast<uint4 *>(g + first);
+        const float rc = -__fmul_rn(m, c);
+        const unsigned long long rc2 = pack2(rc, rc), f2 = pack2(f_out, f_out);
         for (int i = tid; i < v1 - v0; i += kDistillThreads) {
           float o[W];
           unpack(vec_held[i], o, T{});
-          union {
-            uint4 q;
-            T t[W];
-          } r;
+          float r[W];
 #pragma unroll
-          for (int j = 0; j < W; ++j) r.t[j] = from_float<T>(grad_of(o[j]));
-          __stcs(gv + i, r.q);
+          for (int j = 0; j < W; j += 2) {
+            const float2 d = unpack2(fma2(pack2(o[j], o[j + 1]), c2, rc2));
+            const float2 q = unpack2(mul2(pack2(exp2_approx(d.x), exp2_approx(d.y)), f2));
+            r[j] = q.x;
+            r[j + 1] = q.y;
+          }
+          __stcs(gv + i, pack_vec(r, T{}));
         }
-      } else {                            // rows of another alignment than the logits'
-        for (int i = tid; i < count; i += kDistillThreads) g[first + i] = from_float<T>(grad_of(to_float(row_held[i])));
+      } else {                            // rows of another alignment than the logits', or of lowest values
+        for (int i = tid; i < count; i += kDistillThreads)
+          g[first + i] = from_float<T>(exp2_approx(exponent(to_float(row_held[i]), m, c)) * f_out);
       }
       __syncthreads();                    // the zeros at the ids' places are written
       if (own >= 0) g[first + own] = from_float<T>(top);
@@ -427,12 +432,12 @@ cudaError_t launch_distill_t(const DistillArgs &a) {
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
-  // As few CTAs as hold the row two to an SM, more while there are SMs to fill,
-  // 16 with one to an SM for the longest rows.
+  // As few CTAs as hold the row four to an SM, more while there are SMs to fill;
+  // 16 with fewer to an SM for the longest rows.
   const int64_t bytes = a.v * static_cast<int64_t>(sizeof(T));
   auto held = [&](int64_t cs) { return (bytes / 16 + cs - 1) / cs * 16; };   // a share is at most this
   int cs = 1;
-  while (cs < kDistillCluster && held(cs) > kHeldTwo) cs *= 2;
+  while (cs < kDistillCluster && held(cs) > kHeldFour) cs *= 2;
   while (cs < kDistillCluster && a.n * 2 * cs <= 2 * a.num_sms && a.v / (2 * cs) >= 2048) cs *= 2;
   if (held(cs) > kHeldOne) return launch_distill_long<T>(a);
   cudaLaunchConfig_t cfg = {};
@@ -448,7 +453,7 @@ cudaError_t launch_distill_t(const DistillArgs &a) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (held(cs) > kHeldTwo) {              // 16 SMs of one GPC at a time: not every device has them
+  if (held(cs) > kHeldFour) {             // up to 16 SMs of one GPC at a time: not every device has them
     int fit = 0;
     e = cudaOccupancyMaxActiveClusters(&fit, distill_kernel<T>, &cfg);
     if (e != cudaSuccess) return e;

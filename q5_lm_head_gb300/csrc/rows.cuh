@@ -52,6 +52,28 @@ __device__ __forceinline__ void unpack(const uint4 &r, float (&o)[8], __nv_bfloa
   }
 }
 
+__device__ __forceinline__ uint4 pack_vec(const float (&o)[4], float) {
+  return make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]), __float_as_uint(o[3]));
+}
+__device__ __forceinline__ uint4 pack_vec(const float (&o)[8], __half) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(o[2 * i], o[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 pack_vec(const float (&o)[8], __nv_bfloat16) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // A row of v values as `head` values before the first 16-byte boundary, `vecs`
 // aligned vectors and the rest: rows may start at any element.
 struct RowCut {
