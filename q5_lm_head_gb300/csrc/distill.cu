@@ -36,11 +36,12 @@ constexpr float kLog2eD = 1.4426950408889634f;
 constexpr double kLn2D = 0.6931471805599453;
 
 struct DistillShared {
-  int id[kMaxTop];                       // -1: left out
+  __align__(16) int id[kMaxTop];         // -1: left out
   float p[kMaxTop], lp[kMaxTop];         // probability and its logarithm
   float x[kMaxTop];                      // the ids' logits: this CTA's own; all of them in the first CTA
   float m[kDistillWarps], rest[kDistillWarps], in[kDistillWarps];   // the warps' maxima and sums
   float mass;
+  int twice[2];                          // an id of this half of the entries has come before
   float from_m[kDistillCluster], from_rest[kDistillCluster], from_in[kDistillCluster];
 };
 
@@ -89,6 +90,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
   float edge = -INFINITY;
   bool edge_in = false;
   int own = -1;                           // the place of this thread's teacher entry in row_held
+  bool again = false;                     // an earlier entry has the same id
   if (w != 0.0f) {
     for (int i = tid; i < v1 - v0; i += kDistillThreads) copy_async16(vec_held + i, xv + i);
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -100,7 +102,18 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
       sh.id[tid] = ok ? id : -1;
       sh.lp[tid] = ok ? l : -INFINITY;
       if (id >= first && id < first + count) own = id - first;
+      const uint32_t same = __match_any_sync(0xffffffffu, ok ? id : -1 - lane);
+      again = __ffs(same) - 1 != lane;
       ptx::named_bar_sync(1, kMaxTop);
+      if (warp == 1 && k > 32) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const int4 o = *reinterpret_cast<const int4 *>(sh.id + j);
+          again |= ok && (o.x == id || o.y == id || o.z == id || o.w == id);
+        }
+      }
+      const bool any = __any_sync(0xffffffffu, again);
+      if (lane == 0) sh.twice[warp] = any;
     }
     if (warp == 0) {                      // the teacher's probabilities
       float l0 = sh.lp[lane], l1 = sh.lp[lane + 32], shift = 0.0f;
@@ -128,13 +141,11 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
     __syncthreads();
     // the ids' values out of the row
     float mine = -INFINITY, in_m = -INFINITY;
-    bool again = false;                   // an id that an earlier entry has
     if (tid < kMaxTop) {
       if (own >= 0) in_m = mine = to_float(row_held[own]);
       ptx::named_bar_sync(1, kMaxTop);    // an id given twice: both have read it
       if (own >= 0) {
         row_held[own] = from_float<T>(-INFINITY);
-        for (int j = 0; j < tid; ++j) again |= sh.id[j] == first + own;
         sh.x[tid] = mine;
       }
     }
@@ -146,30 +157,36 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
         }
     __syncthreads();
 
-    // maximum and sum of what is left
-    float top = -INFINITY, ref = 0.0f;
+    // maximum and sum of what is left: two passes over shared memory, so that no
+    // sum moves onto a new maximum on the way
+    float top = -INFINITY;
+    {
+      uint4 most = vec_lowest(T{});
+      for (int i = tid; i < v1 - v0; i += kDistillThreads) most = vec_max(most, vec_held[i], T{});
+      float o[W];
+      unpack(most, o, T{});
+#pragma unroll
+      for (int j = 0; j < W; ++j) top = fmaxf(top, o[j]);
+    }
+    const float ref = top == -INFINITY ? 0.0f : top;
     unsigned long long s2 = 0ull;
     const unsigned long long c2 = pack2(c, c);
-    for (int i = tid; i < v1 - v0; i += kDistillThreads) {
-      float o[W];
-      unpack(vec_held[i], o, T{});
-      float cm = o[0];
-#pragma unroll
-      for (int j = 1; j < W; ++j) cm = fmaxf(cm, o[j]);
-      if (cm > top) {
-        const float2 s = unpack2(s2);
-        s2 = pack2(move_sum(s.x, top, cm, c), move_sum(s.y, top, cm, c));
-        top = ref = cm;
-      }
-      if (fabsf(ref) < kPlain) {
-        const float rc = -__fmul_rn(ref, c);
-        const unsigned long long rc2 = pack2(rc, rc);
+    if (fabsf(ref) < kPlain) {
+      const float rc = -__fmul_rn(ref, c);
+      const unsigned long long rc2 = pack2(rc, rc);
+      for (int i = tid; i < v1 - v0; i += kDistillThreads) {
+        float o[W];
+        unpack(vec_held[i], o, T{});
 #pragma unroll
         for (int j = 0; j < W; j += 2) {
           const float2 d = unpack2(fma2(pack2(o[j], o[j + 1]), c2, rc2));
           s2 = add2(s2, pack2(exp2_approx(d.x), exp2_approx(d.y)));
         }
-      } else {
+      }
+    } else {
+      for (int i = tid; i < v1 - v0; i += kDistillThreads) {
+        float o[W];
+        unpack(vec_held[i], o, T{});
 #pragma unroll
         for (int j = 0; j < W; ++j) s2 = add2(s2, pack2(exp2_approx(exponent(o[j], ref, c)), 0.0f));
       }
@@ -252,9 +269,10 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
       if (again) {
         own = -1;                         // the first entry of the id writes for all
       } else {
-        float r = 0.0f;
-        for (int j = 0; j < k; ++j)
-          if (sh.id[j] == first + own) r += sh.p[j];
+        float r = sh.p[tid];
+        if (sh.twice[0] | sh.twice[1])
+          for (int j = tid + 1; j < k; ++j)
+            if (sh.id[j] == first + own) r += sh.p[j];
         in_m = exp2_approx(exponent(mine, m, c)) * f_in - r * scale;
       }
     }

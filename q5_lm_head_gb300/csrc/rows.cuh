@@ -74,6 +74,28 @@ __device__ __forceinline__ uint4 pack_vec(const float (&o)[8], __nv_bfloat16) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Maxima of vectors, value by value; a NaN yields to the other value.
+__device__ __forceinline__ uint4 vec_lowest(float) { return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u); }
+__device__ __forceinline__ uint4 vec_lowest(__half) { return make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u); }
+__device__ __forceinline__ uint4 vec_lowest(__nv_bfloat16) { return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b, float) {
+  return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+}
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b, __half) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b, __nv_bfloat16) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ uint4 vec_max(const uint4 &a, const uint4 &b, T t) {
+  return make_uint4(max_word(a.x, b.x, t), max_word(a.y, b.y, t), max_word(a.z, b.z, t), max_word(a.w, b.w, t));
+}
+
 // A row of v values as `head` values before the first 16-byte boundary, `vecs`
 // aligned vectors and the rest: rows may start at any element.
 struct RowCut {
