@@ -32,7 +32,6 @@ constexpr int kDistillWarps = kDistillThreads / 32;
 constexpr int kDistillCluster = 16;
 constexpr int kHeldFour = 52 * 1024;     // bytes of a row in a CTA: four CTAs an SM
 constexpr int kHeldOne = 216 * 1024;     // one CTA an SM
-constexpr float kLog2eD = 1.4426950408889634f;
 constexpr double kLn2D = 0.6931471805599453;
 
 struct DistillShared {
@@ -63,17 +62,18 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
   __shared__ DistillShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t cr = cluster_rank(), cs = cluster_size();
-  const int64_t row = blockIdx.x / cs;
+  const int cs_log = 31 - __clz(cs);      // a power of two
+  const int64_t row = blockIdx.x >> cs_log;
   const T *x = static_cast<const T *>(a.logits) + row * a.ld;
   T *g = a.grad ? static_cast<T *>(a.grad) + row * a.grad_ld : nullptr;
   const int v = static_cast<int>(a.v), k = a.n_top;
-  const float c = kLog2eD / a.temperature;
+  const float c = a.exponent_scale;       // log2(e) / temperature
   cluster_arrive();                       // waited for before the first store to a peer
 
   // this CTA's share: head values (first CTA), vectors [v0, v1), the rest (last CTA)
   const RowCut cut = cut_row(x, v);
-  const int v0 = static_cast<int>(static_cast<int64_t>(cut.vecs) * cr / cs);
-  const int v1 = static_cast<int>(static_cast<int64_t>(cut.vecs) * (cr + 1) / cs);
+  const int v0 = static_cast<int>((static_cast<int64_t>(cut.vecs) * cr) >> cs_log);
+  const int v1 = static_cast<int>((static_cast<int64_t>(cut.vecs) * (cr + 1)) >> cs_log);
   const int first = cut.head + v0 * W;    // index of the first held value
   const int count = (v1 - v0) * W;
   T *row_held = reinterpret_cast<T *>(held);
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
 
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the logits and the teacher's side are complete
   const float w = a.row_weight ? a.row_weight[row] : 1.0f;
-  float scale = w / a.temperature, m = 0.0f, f_in = 0.0f, f_out = 0.0f;
+  float scale = w * a.inv_temperature, m = 0.0f, f_in = 0.0f, f_out = 0.0f;
   float edge = -INFINITY;
   bool edge_in = false;
   int own = -1;                           // the place of this thread's teacher entry in row_held
@@ -261,8 +261,9 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
     if (total == 0.0f) {
       scale = 0.0f;
     } else {
-      f_in = (mass + pt) / total * scale;
-      f_out = rest != 0.0f ? ((mass + pt) / total - pt / rest) * scale : 0.0f;
+      const float q = (mass + pt) / total;
+      f_in = q * scale;
+      f_out = rest == 0.0f ? 0.0f : (a.tail ? q - pt / rest : q) * scale;
     }
     if (!g) return;
     if (own >= 0) {
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_long_kernel(const Dis
   const T *x = static_cast<const T *>(a.logits) + row * a.ld;
   T *g = a.grad ? static_cast<T *>(a.grad) + row * a.grad_ld : nullptr;
   const int v = static_cast<int>(a.v), tid = threadIdx.x;
-  const float inv_t = 1.0f / a.temperature;
+  const float inv_t = a.inv_temperature;
   const float w = a.row_weight ? a.row_weight[row] : 1.0f;
 
   if (tid < 64) s_seen[tid] = 0u;

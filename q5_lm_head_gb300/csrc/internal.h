@@ -110,7 +110,7 @@ struct ScoreArgs {
   int dtype;
   int64_t n, ld, v;
   const int32_t *tokens;   // [n] or nullptr
-  float temperature;
+  float temperature, exponent_scale;   // log2(e) / temperature
   int n_top;
   float *logprob;          // [n]
   int32_t *rank;           // [n]
@@ -132,7 +132,7 @@ struct DistillArgs {
   int n_top;
   bool tail;
   const float *row_weight;         // [n] or nullptr
-  float temperature;
+  float temperature, inv_temperature, exponent_scale;   // 1 / temperature, log2(e) / temperature
   float *loss;                     // [n] or nullptr
   void *grad;                      // [n][grad_ld] or nullptr, the logits' dtype
   int64_t grad_ld;

@@ -488,6 +488,7 @@ int run_score(const muse_lmhead *h, const void *logits, int dtype, int64_t n, in
   a.v = h->n_rows;
   a.tokens = tokens;
   a.temperature = temperature;
+  a.exponent_scale = static_cast<float>(1.4426950408889634 / temperature);
   a.n_top = n_top;
   a.logprob = logprob;
   a.rank = rank;
@@ -565,6 +566,8 @@ int muse_lmhead_distill(muse_lmhead *h, const void *logits, int dtype, int64_t n
   a.tail = tail != 0;
   a.row_weight = row_weight;
   a.temperature = temperature;
+  a.inv_temperature = 1.0f / temperature;
+  a.exponent_scale = static_cast<float>(1.4426950408889634 / temperature);
   a.loss = loss;
   a.grad = grad;
   a.grad_ld = grad_ld;

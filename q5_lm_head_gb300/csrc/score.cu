@@ -39,7 +39,6 @@ constexpr int kMaxCluster = 16;
 constexpr int kShort = kList / kMaxCluster;      // elements that a CTA hands on, and that are ranked directly
 constexpr int kVecs = 4;                         // 16-byte vectors of a thread and step
 static_assert(kShort >= kMaxTop && 4 * kShort <= kThreads, "rank_top: four threads a key");
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kLn2 = 0.6931471805599453;
 constexpr float kLowest = -3.402823466e38f;
 constexpr uint32_t kKeyMinusInf = 0x007FFFFFu;   // float_order_key(-infinity): below it only NaNs
@@ -177,18 +176,19 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t cr = cluster_rank(), cs = cluster_size();
-  const int64_t row = blockIdx.x / cs;
+  const int cs_log = 31 - __clz(cs);      // a power of two
+  const int64_t row = blockIdx.x >> cs_log;
   const T *x = static_cast<const T *>(a.logits) + row * a.ld;
   const int v = static_cast<int>(a.v), k = a.n_top;
-  const float c = kLog2e / a.temperature;
+  const float c = a.exponent_scale;       // log2(e) / temperature
   if (cs > 1) cluster_arrive();           // waited for before the first store to a peer
   if (tid == 0) sh.n = 0;
   __syncthreads();
 
   // this CTA's share: values [lo, hi) = head values (first CTA) + vectors [v0, v1) + the rest (last CTA)
   const RowCut cut = cut_row(x, v);
-  const int v0 = static_cast<int>(static_cast<int64_t>(cut.vecs) * cr / cs);
-  const int v1 = static_cast<int>(static_cast<int64_t>(cut.vecs) * (cr + 1) / cs);
+  const int v0 = static_cast<int>((static_cast<int64_t>(cut.vecs) * cr) >> cs_log);
+  const int v1 = static_cast<int>((static_cast<int64_t>(cut.vecs) * (cr + 1)) >> cs_log);
   const uint32_t lo = cr == 0 ? 0 : cut.head + v0 * W;
   const uint32_t hi = cr == cs - 1 ? v : cut.head + v1 * W;
   const uint4 *xv = reinterpret_cast<const uint4 *>(x + cut.head);
