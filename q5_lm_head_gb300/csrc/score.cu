@@ -1,7 +1,7 @@
 // Scores of finished logits: the log probability and rank of a given token,
 // the normaliser, the entropy and the top alternatives of each row.
 //
-// For a row x of V logits, c = log2(e) / temperature and m = max x:
+// For a row x of V logits, c = log2(e) / temperature and m near max x:
 //     a_i = (x_i - m) c,  S = sum_i 2^a_i,  U = sum_i 2^a_i a_i
 //     lse = ln 2 (m c + log2 S),  logprob(t) = ln 2 (a_t - log2 S),  entropy = ln 2 (log2 S - U / S)
 // Ranks and alternatives order by (x descending, index ascending), on x itself:
@@ -10,7 +10,7 @@
 // Bound: HBM (each logit is read once) and, close to it, instruction issue for
 // many rows; latency for a few.  A cluster of 1, 2, 4, 8 or 16 CTAs takes a row
 // (as many as keep the GPU's CTA slots filled once), each a contiguous share of
-// its 16-byte vectors; a thread holds a running maximum with S and U, and the
+// its 16-byte vectors; a thread holds a reference m with S and U, and the
 // CTAs' results are pushed into the first one's shared memory.  No global
 // workspace, so calls may overlap.
 //
@@ -24,6 +24,7 @@
 // or rising values), is made up by scans over the row: the values above the
 // bound, then its first equals by index.
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -43,8 +44,8 @@ constexpr double kLn2 = 0.6931471805599453;
 constexpr float kLowest = -3.402823466e38f;
 constexpr uint32_t kKeyMinusInf = 0x007FFFFFu;   // float_order_key(-infinity): below it only NaNs
 
-// Sums S and U against the reference m; m = -infinity: nothing above
-// -infinity seen (S and U are then 0, or NaN).
+// Sums S and U against the reference m, a value of the row; m = -infinity:
+// nothing above -infinity seen (S and U are then 0, or NaN).
 struct Stat {
   float m, s, u;
 };
@@ -78,7 +79,7 @@ struct Shared {
   float m[kWarps], s[kWarps], u[kWarps];
   int before[kWarps];
   uint32_t high[kWarps], low[kWarps];
-  uint32_t group[2][kThreads / 2];
+  uint32_t group[kThreads / 2], bound;
   int cnt[2][kWarps];
   int place[kShort];
   float from_m[kMaxCluster], from_s[kMaxCluster], from_u[kMaxCluster];   // first CTA: the cluster's
@@ -195,12 +196,18 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
   const int steps = (v1 - v0 + kThreads * kVecs - 1) / (kThreads * kVecs);
 
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the logits are complete
+  // full steps, in which every thread has kVecs vectors, and a last one with fewer
+  const int full = (v1 - v0) / (kThreads * kVecs);
   uint4 nxt[kVecs];
   auto fetch = [&](int s) {
+    const uint4 *p = xv + v0 + s * kVecs * kThreads + tid;
+    if (s < full) {
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      const int at = v0 + (s * kVecs + j) * kThreads + tid;
-      nxt[j] = at < v1 ? __ldcs(xv + at) : make_uint4(0u, 0u, 0u, 0u);
+      for (int j = 0; j < kVecs; ++j) nxt[j] = __ldcs(p + j * kThreads);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+        if (v0 + (s * kVecs + j) * kThreads + tid < v1) nxt[j] = __ldcs(p + j * kThreads);
     }
   };
   if (steps > 0) fetch(0);
@@ -211,8 +218,13 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
   // the least value above xt: behind the token only those count
   const float xt_up = nextafterf(xt, INFINITY);
 
+  // The sums' reference is the first maximum seen, and a later one only where it
+  // lies 2^60 above: moving the sums onto every new maximum was most of a step's
+  // instructions (some thread of a warp has one in three steps of four).
   Stat st = {-INFINITY, 0.0f, 0.0f};
-  float ref = 0.0f;                       // st.m, or 0 while that is -infinity
+  float ref = 0.0f, reach = -INFINITY;    // st.m, or 0 while that is -infinity; the largest value it serves
+  float most = -INFINITY;                 // the thread's maximum
+  const float room = 60.0f / c;
   unsigned long long s2 = 0ull, u2 = 0ull;   // two lanes of S and U
   int before = 0, flip = 0;
   // Groups of threads whose maxima give the bound: two or four threads, at
@@ -223,12 +235,14 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
   float bound = -INFINITY, lim = k > 0 && all ? -INFINITY : __int_as_float(0x7FFFFFFF);   // listed from lim up; NaN: nothing
 
   auto add_max = [&](float cm) {
-    if (cm > st.m) {
+    most = fmaxf(most, cm);
+    if (cm > reach) {
       const float2 s = unpack2(s2), u = unpack2(u2);
       const Stat p = stat_move({st.m, s.x, u.x}, cm, c), q = stat_move({st.m, s.y, u.y}, cm, c);
       s2 = pack2(p.s, q.s);
       u2 = pack2(p.u, q.u);
       st.m = ref = cm;
+      reach = cm + room;
     }
   };
   auto add = [&](float xi) {              // 2^-200 is 0 here, and 0 times -infinity would be NaN
@@ -242,32 +256,35 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
     if (at < kList) sh.list[at] = argmax_key(xi, static_cast<uint32_t>(i));
   };
   // the largest key (its upper 16 bits) that at least k groups' maxima reach
-  int gflip = 0;
   auto take_bound = [&]() {
-    uint32_t mine = v0 + tid < v1 ? float_order_key(st.m) : 0u;
+    uint32_t mine = v0 + tid < v1 ? float_order_key(most) : 0u;
     mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
     if (shift == 2) mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, 2));
-    if ((tid & ((1 << shift) - 1)) == 0) sh.group[gflip][tid >> shift] = mine;
+    if ((tid & ((1 << shift) - 1)) == 0) sh.group[tid >> shift] = mine;
     __syncthreads();
-    uint32_t key[8], top = 0u, low = ~0u;
+    if (warp == 0) {                      // one warp: sixteen doing the same would cost issue slots
+      uint32_t key[8], top = 0u, low = ~0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      key[i] = i < 4 || shift == 1 ? sh.group[gflip][lane + 32 * i] : 0u;
-      top = max(top, key[i]);
-      if (i < 4 || shift == 1) low = min(low, key[i]);
-    }
-    gflip ^= 1;
-    top = __reduce_max_sync(0xffffffffu, top);
-    low = __reduce_min_sync(0xffffffffu, low);
-    int bit = top == low ? 0 : 31 - __clz(top ^ low);
-    uint32_t b = top == low ? top : top & ~((2u << bit) - 1u);
-    for (; bit >= 16; --bit) {
-      const uint32_t t = b | (1u << bit);
-      int n = 0;
+      for (int i = 0; i < 8; ++i) {
+        key[i] = i < 4 || shift == 1 ? sh.group[lane + 32 * i] : 0u;
+        top = max(top, key[i]);
+        if (i < 4 || shift == 1) low = min(low, key[i]);
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      low = __reduce_min_sync(0xffffffffu, low);
+      int bit = top == low ? 0 : 31 - __clz(top ^ low);
+      uint32_t b = top == low ? top : top & ~((2u << bit) - 1u);
+      for (; bit >= 16; --bit) {
+        const uint32_t t = b | (1u << bit);
+        int n = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) n += key[i] >= t;
-      if (__reduce_add_sync(0xffffffffu, n) >= k) b = t;
+        for (int i = 0; i < 8; ++i) n += key[i] >= t;
+        if (__reduce_add_sync(0xffffffffu, n) >= k) b = t;
+      }
+      if (lane == 0) sh.bound = b;
     }
+    __syncthreads();
+    const uint32_t b = sh.bound;
     bound = order_key_float(b < kKeyMinusInf ? kKeyMinusInf : b);
     lim = fmaxf(bound, kLowest);
   };
@@ -288,26 +305,26 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
   }
 
   const unsigned long long c2 = pack2(c, c);
-  for (int s = 0; s < steps; ++s) {
-    uint4 cur[kVecs];
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) cur[j] = nxt[j];
+  // One step: kVecs vectors of the thread, or the first `mine` of them (kFull false).
+  auto step = [&](const uint4 (&cur)[kVecs], int s, auto full_const) {
+    constexpr bool kFull = decltype(full_const)::value;
     const int at0 = v0 + s * kVecs * kThreads + tid;
-    const int mine = min(kVecs, (v1 - at0 + kThreads - 1) / kThreads);   // vectors of this thread (may be <= 0)
-    if (s + 1 < steps) fetch(s + 1);
+    const int mine = kFull ? kVecs : min(kVecs, (v1 - at0 + kThreads - 1) / kThreads);   // may be <= 0
     float top[kVecs], cm = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-      float o[W];
-      unpack(cur[j], o, T{});
-      top[j] = o[0];
+      top[j] = -INFINITY;
+      if (kFull || j < mine) {
+        float o[W];
+        unpack(cur[j], o, T{});
+        top[j] = o[0];
 #pragma unroll
-      for (int i = 1; i < W; ++i) top[j] = fmaxf(top[j], o[i]);
-      if (j >= mine) top[j] = -INFINITY;
+        for (int i = 1; i < W; ++i) top[j] = fmaxf(top[j], o[i]);
+      }
       cm = fmaxf(cm, top[j]);
     }
     add_max(cm);
-    if (mine == kVecs && fabsf(ref) < kPlain) {
+    if (kFull && fabsf(ref) < kPlain) {
       const float rc = -__fmul_rn(ref, c);
       const unsigned long long rc2 = pack2(rc, rc);
 #pragma unroll
@@ -368,6 +385,15 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
         }
       }
     }
+  };
+#pragma unroll 1
+  for (int s = 0; s < steps; ++s) {
+    uint4 cur[kVecs];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) cur[j] = nxt[j];
+    if (s + 1 < steps) fetch(s + 1);
+    if (s < full) step(cur, s, std::true_type{});
+    else step(cur, s, std::false_type{});
   }
   if (edge_i >= 0 && edge >= lim) list(edge, edge_i);
 
