@@ -33,13 +33,10 @@
 namespace muse {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kList = 2048;                      // listed elements of a CTA
 constexpr int kMaxCluster = 16;
 constexpr int kShort = kList / kMaxCluster;      // elements that a CTA hands on, and that are ranked directly
-constexpr int kVecs = 4;                         // 16-byte vectors of a thread and step
-static_assert(kShort >= kMaxTop && 4 * kShort <= kThreads, "rank_top: four threads a key");
+static_assert(kShort >= kMaxTop, "a CTA's own alternatives");
 constexpr double kLn2 = 0.6931471805599453;
 constexpr float kLowest = -3.402823466e38f;
 constexpr uint32_t kKeyMinusInf = 0x007FFFFFu;   // float_order_key(-infinity): below it only NaNs
@@ -72,7 +69,9 @@ __device__ __forceinline__ Stat stat_warp(Stat t, float c) {
   return t;
 }
 
+template <int kThreads>
 struct Shared {
+  static constexpr int kWarps = kThreads / 32;
   unsigned long long list[kList];
   unsigned long long got[kList];                 // first CTA: kShort from each of the cluster's
   unsigned long long best[kMaxTop];
@@ -89,13 +88,14 @@ struct Shared {
 };
 
 // Sum over the CTA of a small count; `flip` alternates between calls.
-__device__ __forceinline__ int block_count(int c, Shared &sh, int &flip) {
+template <int kThreads>
+__device__ __forceinline__ int block_count(int c, Shared<kThreads> &sh, int &flip) {
   c = __reduce_add_sync(0xffffffffu, c);
   if ((threadIdx.x & 31) == 0) sh.cnt[flip][threadIdx.x >> 5] = c;
   __syncthreads();
   int t = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) t += sh.cnt[flip][w];
+  for (int w = 0; w < kThreads / 32; ++w) t += sh.cnt[flip][w];
   flip ^= 1;
   return t;
 }
@@ -103,7 +103,8 @@ __device__ __forceinline__ int block_count(int c, Shared &sh, int &flip) {
 // Cuts the n keys of list (all different, at most kList) to at most kShort with
 // the k largest among them; returns how many.  By bits from the top: the
 // largest bound that at least k keys reach, until few enough do.
-__device__ __forceinline__ int trim(unsigned long long *list, int n, int k, Shared &sh, int &flip) {
+template <int kThreads>
+__device__ __forceinline__ int trim(unsigned long long *list, int n, int k, Shared<kThreads> &sh, int &flip) {
   if (n <= kShort) return n;
   constexpr int P = kList / kThreads;
   unsigned long long key[P];
@@ -126,7 +127,7 @@ __device__ __forceinline__ int trim(unsigned long long *list, int n, int k, Shar
   if (threadIdx.x == 0) sh.kept = 0;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     hi = max(hi, sh.high[w]);
     lo = min(lo, sh.low[w]);
   }
@@ -156,8 +157,9 @@ __device__ __forceinline__ int trim(unsigned long long *list, int n, int k, Shar
 }
 
 // The k largest of the n <= kShort keys of list, in order, to sh.best: a key's
-// place is how many are larger, counted by four threads.
-__device__ __forceinline__ void rank_top(const unsigned long long *list, int n, int k, Shared &sh) {
+// place is how many are larger, counted by two or four threads.
+template <int kThreads>
+__device__ __forceinline__ void rank_top(const unsigned long long *list, int n, int k, Shared<kThreads> &sh) {
   const int i = threadIdx.x % kShort, part = threadIdx.x / kShort;
   constexpr int kParts = kThreads / kShort;
   if (threadIdx.x < kShort) sh.place[threadIdx.x] = 0;
@@ -171,10 +173,11 @@ __device__ __forceinline__ void rank_top(const unsigned long long *list, int n, 
   __syncthreads();
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
-  constexpr int W = Vec<T>::W;
-  __shared__ Shared sh;
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const ScoreArgs a) {
+  constexpr int W = Vec<T>::W, kWarps = kThreads / 32;
+  constexpr int kVecs = 4;                // 16-byte vectors of a thread and step
+  __shared__ Shared<kThreads> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t cr = cluster_rank(), cs = cluster_size();
   const int cs_log = 31 - __clz(cs);      // a power of two
@@ -263,12 +266,13 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
     if ((tid & ((1 << shift) - 1)) == 0) sh.group[tid >> shift] = mine;
     __syncthreads();
     if (warp == 0) {                      // one warp: sixteen doing the same would cost issue slots
-      uint32_t key[8], top = 0u, low = ~0u;
+      constexpr int kKeys = kThreads / 64;   // of a lane, with groups of two threads
+      uint32_t key[kKeys], top = 0u, low = ~0u;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        key[i] = i < 4 || shift == 1 ? sh.group[lane + 32 * i] : 0u;
+      for (int i = 0; i < kKeys; ++i) {
+        key[i] = i < kKeys / 2 || shift == 1 ? sh.group[lane + 32 * i] : 0u;
         top = max(top, key[i]);
-        if (i < 4 || shift == 1) low = min(low, key[i]);
+        if (i < kKeys / 2 || shift == 1) low = min(low, key[i]);
       }
       top = __reduce_max_sync(0xffffffffu, top);
       low = __reduce_min_sync(0xffffffffu, low);
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
         const uint32_t t = b | (1u << bit);
         int n = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) n += key[i] >= t;
+        for (int i = 0; i < kKeys; ++i) n += key[i] >= t;
         if (__reduce_add_sync(0xffffffffu, n) >= k) b = t;
       }
       if (lane == 0) sh.bound = b;
@@ -528,20 +532,18 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreArgs a) {
   }
 }
 
-template <typename T>
-cudaError_t launch_score_t(const ScoreArgs &a) {
+template <typename T, int kThreads>
+cudaError_t launch_score_t(const ScoreArgs &a, int cs) {
   static std::atomic<unsigned long long> configured{0};   // one bit per device; host threads may race here
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(configured.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(score_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(score_kernel<T, kThreads>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
-  int cs = 1;
-  while (cs < kMaxCluster && a.n * 2 * cs <= 2 * a.num_sms && a.v / (2 * cs) >= 2048) cs *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.n * cs));
   cfg.blockDim = dim3(kThreads);
@@ -554,15 +556,25 @@ cudaError_t launch_score_t(const ScoreArgs &a) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, score_kernel<T>, a);
+  return cudaLaunchKernelEx(&cfg, score_kernel<T, kThreads>, a);
+}
+
+// As many CTAs a row as the SMs have room for at once, each with a step's work.
+// A row of its own CTA runs with 256 threads, four CTAs an SM: one's barriers
+// (the bound, the end) fall into the others' loads.  REPLACE
+template <typename T>
+cudaError_t launch_score_rows(const ScoreArgs &a) {
+  int cs = 1;
+  while (cs < kMaxCluster && a.n * 2 * cs <= 2 * a.num_sms && a.v / (2 * cs) >= 2048) cs *= 2;
+  return cs == 1 ? launch_score_t<T, 256>(a, cs) : launch_score_t<T, 512>(a, cs);
 }
 
 }  // namespace
 
 cudaError_t launch_score(const ScoreArgs &a) {
-  if (a.dtype == 0) return launch_score_t<float>(a);
-  if (a.dtype == 1) return launch_score_t<__half>(a);
-  return launch_score_t<__nv_bfloat16>(a);
+  if (a.dtype == 0) return launch_score_rows<float>(a);
+  if (a.dtype == 1) return launch_score_rows<__half>(a);
+  return launch_score_rows<__nv_bfloat16>(a);
 }
 
 }  // namespace muse
