@@ -27,8 +27,8 @@
 //      B' = -t mdmin, with middle sc 2^e times B added to the same sums.
 //    * four unpack warpgroups, two for each block, alternating between units of
 //      16 to 48 rows: ldmatrix with transposition gives a thread four rows of
-//      one input, and tcgen05.st (16 lanes x 256 bits) takes exactly that
-//      fragment. 
+//      one input, and tcgen05.st (16 lanes x 128 bits) takes that fragment, the
+//      rows in slab_order. 
 //    * MMA warp: per 16 rows four products of M = 128 (two nibble halves of two
 //      blocks) and four small ones for mins and middles.  The tensor cores round
 //      their sums towards zero, about 2^-24 a step, which over a share's thousand
@@ -77,13 +77,17 @@ __device__ __forceinline__ int row_exponent(const float *gmax, int b, int parts)
   const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
   return m == 0.0f ? 0 : e < -126 ? -126 : e;   // 128 for infinities: they stay what they are
 }
+// A slab's 16 rows v in the order in which a thread's transposed fragment goes to
+// tensor memory: the first two of every four, then the others.
+__device__ __forceinline__ int slab_order(int v) { return (v & ~15) | ((v & 2) << 2) | ((v >> 1) & 6) | (v & 1); }
+
 __device__ __forceinline__ float pow2(int e) {   // -126 <= e <= 127
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
 __device__ __forceinline__ float cap_slope(float l, float cap, float inv_cap2) { return (cap - l) * (cap + l) * inv_cap2; }
 
-// t[v/8][b][v%8] = gl * scale_m * slope, scale_m the scale's mantissa.
+// t[p/8][b][p%8] = gl * scale_m * slope of row v, p = slab_order(v), scale_m the scale's mantissa.
 __global__ void __launch_bounds__(256) slope_kernel(const BackwardArgs a, float scale_m) {
   __shared__ float s_max[8];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the main kernel's set-up beside this one
@@ -103,7 +107,8 @@ __global__ void __launch_bounds__(256) slope_kernel(const BackwardArgs a, float 
       if (a.cap > 0.0f) t *= cap_slope(__ldcs(l + v), a.cap, inv_cap2);
       t *= scale_m;
     }
-    a.t[((v >> 3) * a.batch + b) * 8 + (v & 7)] = t;
+    const int64_t at = (v & ~int64_t{15}) | slab_order(static_cast<int>(v & 15));
+    a.t[((at >> 3) * a.batch + b) * 8 + (at & 7)] = t;
   }
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
@@ -168,9 +173,12 @@ struct BwdCfg {
   static constexpr uint32_t kIdesc = tc::idesc_f16_f32(128, kD), kIdescPair = tc::idesc_f16_f32(128, 2 * kD);
 };
 
+// 16 lanes x 8 columns: a and c lane t/4, b and d lane t/4 + 8, a and b column
+// t%4, c and d column 4 + t%4.  (16x256b would take the rows in their order, at
+// half the rate: 16 cycles for 32 lanes x 8 columns against 8.)
 template <uint32_t kOffset>
-__device__ __forceinline__ void st_16x256b(uint32_t ta, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0 + %5], {%1, %2, %3, %4};" ::"r"(ta), "r"(a), "r"(b), "r"(c),
+__device__ __forceinline__ void st_16x128b(uint32_t ta, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0 + %5], {%1, %2, %3, %4};" ::"r"(ta), "r"(a), "r"(b), "r"(c),
                "r"(d), "n"(kOffset)
                : "memory");
 }
@@ -424,8 +432,8 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
           const uint4 hdr = *reinterpret_cast<const uint4 *>(st + row * C::kRowBytes + blk * C::kBB);
           const float2 dd = __half22float2(*reinterpret_cast<const __half2 *>(&hdr.x));
           int ed, em;
-          md_at[blk * C::kRows + row] = __float2half_rn(split_d(dd.x, ed, big));
-          md_at[(2 + blk) * C::kRows + row] = __float2half_rn(-split_d(dd.y, em, big));
+          md_at[blk * C::kRows + slab_order(row)] = __float2half_rn(split_d(dd.x, ed, big));
+          md_at[(2 + blk) * C::kRows + slab_order(row)] = __float2half_rn(-split_d(dd.y, em, big));
           const uint32_t pd = pack_half2(pow2(ed - Quant<kQ4>::kLow), pow2(ed - Quant<kQ4>::kHigh));   // the quants come multiplied
           const uint32_t pm = pack_half2(pow2(em), pow2(em));
           const uint32_t sc[2] = {hdr.y & 0x3F3F3F3Fu, (hdr.w & 0x0F0F0F0Fu) | ((hdr.y >> 2) & 0x30303030u)};
@@ -595,15 +603,15 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
             hi[2 * r + 1] = hfma2(__byte_perm(qh, 0x64u, 0x4342u), k1.y, a11);
           }
           constexpr uint32_t kAt = s * C::kSlab, kUp = 16u << 16;
-          st_16x256b<kAt>(at, lo[0], lo[1], lo[2], lo[3]);
-          st_16x256b<kAt + kUp>(at, lo[4], lo[5], lo[6], lo[7]);
-          st_16x256b<kAt + 8>(at, hi[0], hi[1], hi[2], hi[3]);
-          st_16x256b<kAt + kUp + 8>(at, hi[4], hi[5], hi[6], hi[7]);
+          st_16x128b<kAt>(at, lo[0], lo[2], lo[1], lo[3]);
+          st_16x128b<kAt + kUp>(at, lo[4], lo[6], lo[5], lo[7]);
+          st_16x128b<kAt + 8>(at, hi[0], hi[2], hi[1], hi[3]);
+          st_16x128b<kAt + kUp + 8>(at, hi[4], hi[6], hi[5], hi[7]);
           // block wq's mins or scales times the middle: lanes 0-7 of this quarter (and, unread, 8-15)
           if (wq < 2) {
             m.x = hmul2(m.x, middle);
             m.y = hmul2(m.y, middle);
-            st_16x256b<kAt + 32>(at_small, m.x, m.y, m.x, m.y);
+            st_16x128b<kAt + 32>(at_small, m.x, m.x, m.y, m.y);
           }
         };
         slab_to_tmem(std::integral_constant<int, 0>{});
