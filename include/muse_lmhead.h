@@ -371,8 +371,8 @@ int muse_lmhead_forward_score(muse_lmhead *h, const float *hidden, int batch, co
  *           whatever it holds.
  *   loss    [n] f32, device, or NULL.  grad: device rows in the logits' dtype,
  *           grad_ld >= n_rows elements apart, or NULL for the loss alone; it
- *           may be the logits themselves (with grad_ld = ld).  One of the two
- *           is needed.  Elements between n_rows and grad_ld are left alone.
+ *           may be the logits themselves (with grad_ld = ld), and must not
+ *           overlap them otherwise.  One of the two is needed.  Elements between n_rows and grad_ld are left alone.
  * A row with no teacher entry left has loss and gradient 0, and so has a row
  * whose logits are all -infinity.  Where the teacher expects a masked logit
  * the loss is +infinity and the gradient finite.  A NaN or +infinity in a row
@@ -396,10 +396,18 @@ int muse_lmhead_distill(muse_lmhead *h, const void *logits, int dtype, int64_t n
  *   hidden [batch][k] and gamma as in the forward; hidden is needed with gamma.
  *   grad_hidden [batch][k] f32, written; grad_gamma [k] f32, written, or NULL
  *   (needs gamma).  All 16-byte aligned, device, dense, batch 1..max_batch.
- *   grad_hidden must not overlap the inputs.
- * The sums run in a fixed order: the same inputs give the same bits.  Uses the
- * handle's workspace: like forwards, two calls that may run at the same time
- * on the GPU must use two handles.
+ *   grad_hidden and grad_gamma must not overlap the inputs or each other.
+ * Products are formed on the tensor cores from f16 pairs (a gradient times a
+ * block's factor to 2^-21) and summed in f32: an element is off by about
+ * 2^-21 of the sum of the sizes of its products.  The sums run in a fixed
+ * order: the same inputs give the same bits.  A NaN or infinity in a row of
+ * grad_logits stays in that row (and reaches grad_gamma).
+ * The first call allocates the handle's workspace for it (max_batch rows of
+ * n_rows floats and about 20 MB at most for the pages' shapes); while `stream`
+ * is being captured that first call returns MUSE_ERR_NOMEM, so make one before.
+ * The workspace is the handle's: like forwards, two calls that may run at the
+ * same time on the GPU must use two handles.  Three launches, four with
+ * grad_gamma and more than one row.
  */
 int muse_lmhead_backward(muse_lmhead *h, const float *grad_logits, const float *logits, const float *hidden,
                          int batch, const float *gamma, float eps, const void *weights, float scale, float cap,

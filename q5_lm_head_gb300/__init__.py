@@ -288,6 +288,19 @@ def muse_lmhead_backward(h: int | None, grad_logits: int, logits: int | None, hi
                                                grad_hidden, grad_gamma, stream)
 
 
+_stream_of = None
+
+
+def _current_stream():
+    """Function of a device index: its current stream's handle (without a Stream object, where torch has that call)."""
+    global _stream_of
+    if _stream_of is None:
+        import torch
+        _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _stream_of
+
+
 _dtypes = None
 
 
@@ -341,10 +354,9 @@ class LMHead:
         self.close()
 
     def _check(self, t, name, dtype, shape=None):
-        import torch
-        if t.dtype != dtype or not t.is_contiguous() or t.device.type != "cuda" or t.device.index != self.device:
+        if t.dtype != dtype or not t.is_contiguous() or t.get_device() != self.device:
             raise ValueError(f"{name}: need a contiguous {dtype} tensor on cuda:{self.device}")
-        if shape is not None and tuple(t.shape) != tuple(shape):
+        if shape is not None and t.shape != shape:
             raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
         return t.data_ptr()
 
@@ -498,8 +510,7 @@ class LMHead:
         return t.data_ptr(), dtype, n, ld if n > 1 else v
 
     def _stream(self, stream):
-        import torch
-        return (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+        return _current_stream()(self.device) if stream is None else stream.cuda_stream
 
     def _score_outputs(self, n, tokens, n_top, device):
         """(TokenScores, pointers of tokens and outputs in the C order)"""
@@ -598,8 +609,9 @@ class LMHead:
         """(grad_hidden [B, k], grad_gamma [k] or None) from grad_logits [B, n_rows] f32.
 
         weights, gamma, eps, scale and cap as in the forward; logits (what it
-        returned) is needed with a cap, hidden with gamma.  See
-        muse_lmhead_backward in the C header."""
+        returned) is needed with a cap, hidden with gamma.  The first call
+        allocates the handle's workspace: make it before a graph's capture.
+        See muse_lmhead_backward in the C header."""
         import torch
         if grad_logits.dim() == 1:
             grad_logits = grad_logits.unsqueeze(0)

@@ -32,7 +32,6 @@ constexpr int kDistillWarps = kDistillThreads / 32;
 constexpr int kDistillCluster = 16;
 constexpr int kHeldFour = 52 * 1024;     // bytes of a row in a CTA: four CTAs an SM
 constexpr int kHeldOne = 216 * 1024;     // one CTA an SM
-constexpr double kLn2D = 0.6931471805599453;
 
 struct DistillShared {
   __align__(16) int id[kMaxTop];         // -1: left out
@@ -247,15 +246,13 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
     const float pt = a.tail ? fmaxf(0.0f, 1.0f - mass) : 0.0f;
     if (cr == 0 && warp == 0 && a.loss) {
       // a few values a row, in 64 bits: a lowest value would overflow in log2's units
-      const double lse = (fabsf(m) < kPlain ? kLn2D * static_cast<double>(__fmul_rn(m, c))
-                                            : m / static_cast<double>(a.temperature)) +
-                         kLn2D * static_cast<double>(log2f(total));
+      const double lse = row_lse(m, c, log2f(total), a.temperature);
       double loss = 0.0;
       for (int j = lane; j < k; j += 32)
         if (sh.p[j] > 0.0f)
           loss += sh.p[j] * (sh.lp[j] - (sh.x[j] / static_cast<double>(a.temperature) - lse));
       for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
-      if (pt > 0.0f) loss += pt * (logf(pt) - kLn2D * (static_cast<double>(log2f(rest)) - log2f(total)));
+      if (pt > 0.0f) loss += pt * (logf(pt) - kLn2 * (static_cast<double>(log2f(rest)) - log2f(total)));
       if (lane == 0) a.loss[row] = total == 0.0f ? 0.0f : static_cast<float>(w * loss);
     }
     if (total == 0.0f) {

@@ -23,9 +23,6 @@ struct Workspace {
   unsigned int *split_cnt;   // [num_sms][8] arrivals per shared tile and warp (per CTA boundary, or per tile when tiles < SMs), zero between forwards
   float *b1_part;            // split-K batch-1 path: [chunks][n_rows] chunk partial sums
   unsigned int *b1_cnt;      // split-K batch-1 path: [12-row tiles] chunk arrivals, zero between forwards
-  float *bwd_part;           // backward: the row shares' sums of the gradient by the normed input
-  float *bwd_t;              // backward: the gradient by the matrix product, eight rows v of a batch row together
-  float *bwd_misc;           // backward: backward_misc_floats
 };
 
 constexpr int kMaxLseParts = 256;
@@ -157,8 +154,8 @@ struct BackwardArgs {
   int64_t n_rows;
   int k;
   int num_sms;
-  float *part;                // workspace of backward_part_floats
-  float *t;                   // workspace of backward_t_floats
+  float *part;                // workspace of backward_part_floats: the row shares' sums of the gradient by the normed input
+  float *t;                   // workspace of backward_t_floats: the gradient by the matrix product, eight rows v of a batch row together
   float *gmax, *rms;          // workspace: largest |grad_logits| of parts of each row, RMS factors
   uint32_t *flag;             // workspace: a block's d or dmin is beyond the tensor cores' operands
   uint32_t *status;

@@ -33,6 +33,7 @@ struct muse_lmhead {
   int32_t *stage_argmax;
   float *stage_group;      // forward_group_host staging of pageable outputs (lazy, grows)
   int64_t stage_group_n;   // its size in floats
+  float *bwd;              // workspace of the backward pass (lazy): its small arrays, its shares' sums, its t
 };
 
 namespace {
@@ -170,9 +171,9 @@ int muse_lmhead_init_format(muse_lmhead **out, int device, int64_t n_rows, int64
   h->max_batch = max_batch;
   h->num_sms = prop.multiProcessorCount;
 
-  // One allocation, zeroed but for the last two: keys | ticket | status | logprob pairs | x | activation packages |
+  // One zeroed allocation: keys | ticket | status | logprob pairs | x | activation packages |
   // shared-tile counters | shared-tile partial sums (those three for the tensor-core path) |
-  // chunk counters | chunk partial sums (the split-K batch-1 path) | backward's small arrays | its shares' sums | its t
+  // chunk counters | chunk partial sums (the split-K batch-1 path)
   const size_t keys_b = sizeof(unsigned long long) * MUSE_MAX_BATCH;
   const size_t misc_b = 256;
   const size_t lse_b = sizeof(float2) * static_cast<size_t>(max_batch) * muse::kMaxLseParts;
@@ -187,19 +188,14 @@ int muse_lmhead_init_format(muse_lmhead **out, int device, int64_t n_rows, int64
   const size_t part_b = tc ? sizeof(float) * muse::tc_split_floats(h->num_sms, max_batch) : 0;
   const size_t bcnt_b = split ? (sizeof(unsigned int) * muse::b1_split_counters(n_rows) + 255) / 256 * 256 : 0;
   const size_t bpart_b = split ? sizeof(float) * muse::b1_split_floats(n_rows, static_cast<int>(k)) : 0;
-  const size_t wpart_b = (sizeof(float) * muse::backward_part_floats(n_rows, static_cast<int>(k), max_batch, h->num_sms) + 255) / 256 * 256;
-  const size_t fwd_b = (keys_b + misc_b + lse_b + x_b + pkg_b + cnt_b + part_b + bcnt_b + bpart_b + 255) / 256 * 256;
-  const size_t wt_b = sizeof(float) * muse::backward_t_floats(n_rows, max_batch);
-  const size_t wmisc_b = (sizeof(float) * muse::backward_misc_floats() + 255) / 256 * 256;
-  const size_t zeroed_b = fwd_b + wmisc_b;   // the rest is written before it is read
-  const size_t total = zeroed_b + wpart_b + wt_b;
+  const size_t total = keys_b + misc_b + lse_b + x_b + pkg_b + cnt_b + part_b + bcnt_b + bpart_b;
   void *base = nullptr;
   e = cudaMalloc(&base, total);
   if (e != cudaSuccess) {
     delete h;
     return e == cudaErrorMemoryAllocation ? MUSE_ERR_NOMEM : cuda_fail(e);
   }
-  e = cudaMemset(base, 0, zeroed_b);
+  e = cudaMemset(base, 0, total);
   if (e != cudaSuccess) {
     cudaFree(base);
     delete h;
@@ -221,9 +217,6 @@ int muse_lmhead_init_format(muse_lmhead **out, int device, int64_t n_rows, int64
   h->ws.b1_cnt = bcnt_b ? reinterpret_cast<unsigned int *>(pb) : nullptr;
   h->ws.b1_part = bpart_b ? reinterpret_cast<float *>(pb + bcnt_b) : nullptr;
   h->ws_b1_cnt_bytes = bcnt_b;
-  h->ws.bwd_misc = reinterpret_cast<float *>(p + fwd_b);
-  h->ws.bwd_part = reinterpret_cast<float *>(p + zeroed_b);
-  h->ws.bwd_t = reinterpret_cast<float *>(p + zeroed_b + wpart_b);
   *out = h;
   return MUSE_OK;
 }
@@ -577,6 +570,31 @@ int muse_lmhead_distill(muse_lmhead *h, const void *logits, int dtype, int64_t n
   return e == cudaSuccess ? MUSE_OK : cuda_fail(e);
 }
 
+namespace {
+
+size_t padded_floats(size_t n) { return (n + 63) / 64 * 64; }
+
+// The backward pass's workspace for max_batch rows, allocated once; written before it is read.
+int ensure_backward(muse_lmhead *h, cudaStream_t stream) {
+  if (h->bwd) return MUSE_OK;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(stream, &cap);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (cap != cudaStreamCaptureStatusNone) return MUSE_ERR_NOMEM;   // an allocation would end the capture
+  const size_t n = padded_floats(muse::backward_misc_floats()) +
+                   padded_floats(muse::backward_part_floats(h->n_rows, static_cast<int>(h->k), h->max_batch, h->num_sms)) +
+                   muse::backward_t_floats(h->n_rows, h->max_batch);
+  void *p = nullptr;
+  if ((e = cudaMalloc(&p, sizeof(float) * n)) != cudaSuccess) {
+    cudaGetLastError();                   // a failed allocation is this call's answer, not the next one's
+    return e == cudaErrorMemoryAllocation ? MUSE_ERR_NOMEM : cuda_fail(e);
+  }
+  h->bwd = static_cast<float *>(p);
+  return MUSE_OK;
+}
+
+}  // namespace
+
 int muse_lmhead_backward(muse_lmhead *h, const float *grad_logits, const float *logits, const float *hidden, int batch,
                          const float *gamma, float eps, const void *weights, float scale, float cap,
                          float *grad_hidden, float *grad_gamma, void *stream) {
@@ -584,13 +602,14 @@ int muse_lmhead_backward(muse_lmhead *h, const float *grad_logits, const float *
   if (gamma && !hidden) return MUSE_ERR_NULL;
   if (grad_gamma && !gamma) return MUSE_ERR_NULL;
   if (!grad_hidden) return MUSE_ERR_NULL;
-  const int st = validate_forward(h, grad_logits, batch, gamma, eps, weights, scale, cap, grad_hidden, nullptr);
+  int st = validate_forward(h, grad_logits, batch, gamma, eps, weights, scale, cap, grad_hidden, nullptr);
   if (st != MUSE_OK) return st;
   if (!aligned(grad_logits, 16) || !aligned(logits, 16) || !aligned(hidden, 16) || !aligned(grad_hidden, 16) ||
       !aligned(grad_gamma, 16))
     return MUSE_ERR_ALIGN;
   DeviceGuard g(h->device);
   if (!g.ok) return MUSE_ERR_DEVICE;
+  if ((st = ensure_backward(h, static_cast<cudaStream_t>(stream))) != MUSE_OK) return st;
   muse::BackwardArgs a;
   a.grad_logits = grad_logits;
   a.logits = logits;
@@ -607,9 +626,9 @@ int muse_lmhead_backward(muse_lmhead *h, const float *grad_logits, const float *
   a.n_rows = h->n_rows;
   a.k = static_cast<int>(h->k);
   a.num_sms = h->num_sms;
-  a.part = h->ws.bwd_part;
-  a.t = h->ws.bwd_t;
-  a.gmax = h->ws.bwd_misc;
+  a.gmax = h->bwd;
+  a.part = a.gmax + padded_floats(muse::backward_misc_floats());
+  a.t = a.part + padded_floats(muse::backward_part_floats(h->n_rows, a.k, h->max_batch, h->num_sms));
   a.rms = a.gmax + muse::backward_misc_floats() - MUSE_MAX_BATCH - 1;
   a.flag = reinterpret_cast<uint32_t *>(a.rms + MUSE_MAX_BATCH);
   a.status = h->ws.status;
@@ -683,6 +702,7 @@ void muse_lmhead_destroy(muse_lmhead *h) {
   if (h->stage_logits) cudaFree(h->stage_logits);
   if (h->stage_argmax) cudaFree(h->stage_argmax);
   if (h->stage_group) cudaFree(h->stage_group);
+  if (h->bwd) cudaFree(h->bwd);
   delete h;
 }
 

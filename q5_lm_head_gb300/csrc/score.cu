@@ -37,7 +37,6 @@ constexpr int kList = 2048;                      // listed elements of a CTA
 constexpr int kMaxCluster = 16;
 constexpr int kShort = kList / kMaxCluster;      // elements that a CTA hands on, and that are ranked directly
 static_assert(kShort >= kMaxTop, "a CTA's own alternatives");
-constexpr double kLn2 = 0.6931471805599453;
 constexpr float kLowest = -3.402823466e38f;
 constexpr uint32_t kKeyMinusInf = 0x007FFFFFu;   // float_order_key(-infinity): below it only NaNs
 
@@ -507,8 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
   const bool empty = total == 0.0f;       // nothing above -infinity
   const float logs = log2f(total);
   // from here a few values a row, in 64 bits: in log2's units a lowest value would overflow
-  const double lse = (fabsf(m) < kPlain ? kLn2 * static_cast<double>(__fmul_rn(m, c)) : m / static_cast<double>(a.temperature)) +
-                     kLn2 * static_cast<double>(logs);
+  const double lse = row_lse(m, c, logs, a.temperature);
   auto logprob = [&](float xi) { return empty ? -INFINITY : static_cast<float>(xi / static_cast<double>(a.temperature) - lse); };
   if (tid == 0) {
     if (a.lse) a.lse[row] = empty ? -INFINITY : static_cast<float>(lse);

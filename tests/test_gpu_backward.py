@@ -283,3 +283,69 @@ def test_backward_full_head(torch_cuda):
         w = _dense(raw[:, kb], n, 256, "q5_k")
         want, tol, _, _ = _reference(gl, None, None, None, w, 1.0, 0.0)
         _within("grad_hidden", gh[:, kb * 256:kb * 256 + 256].cpu().numpy(), want, tol)
+
+
+@pytest.mark.parametrize("b,n,k,fmt", [(1, 6007, 6656, "q5_k"), (5, 2048, 6656, "q4_k"), (12, 3001, 1024, "q5_k"), (32, 1501, 2560, "q4_k")])
+def test_backward_back_to_back_with_other_gradients(torch_cuda, b, n, k, fmt):
+    """Calls one behind another on one handle: each kernel starts early and has to see its own call's values."""
+    import q5_lm_head_gb300 as mlh
+    torch = torch_cuda
+    rng = np.random.default_rng(b)
+    wq = torch.from_numpy(np.ascontiguousarray(_weights(n, k, fmt, 15))).cuda()
+    grads = [torch.from_numpy((_grads(rng, b, n) * s).astype(np.float32)).cuda() for s in (1.0, 1e-5, 300.0)]
+    hidden = torch.from_numpy(rng.standard_normal((b, k)).astype(np.float32)).cuda()
+    gamma = torch.from_numpy((1 + 0.1 * rng.standard_normal(k)).astype(np.float32)).cuda()
+    with mlh.LMHead(n, k, max_batch=b, device=0, fmt=fmt) as head:
+        call = lambda g: head.backward(g, wq, hidden=hidden, gamma=gamma, scale=0.7, cap=0.0)       # noqa: E731
+        want = []
+        for g in grads:
+            out = call(g)
+            torch.cuda.synchronize()
+            want.append([t.clone() for t in out])
+        got = [(i % 3, call(grads[i % 3])) for i in range(300)]
+        torch.cuda.synchronize()
+        assert head.device_status() == 0
+    for i, out in got:
+        assert all(torch.equal(p, q) for p, q in zip(out, want[i]))
+
+
+def test_backward_nan_and_infinity_stay_in_their_row(torch_cuda):
+    import q5_lm_head_gb300 as mlh
+    torch = torch_cuda
+    b, n, k = 4, 1001, 512
+    rng = np.random.default_rng(8)
+    w = torch.from_numpy(np.ascontiguousarray(_weights(n, k, "q5_k", 16))).cuda()
+    g = torch.from_numpy(_grads(rng, b, n)).cuda()
+    bad = g.clone()
+    bad[1, 77], bad[2, 500] = float("nan"), float("inf")
+    with mlh.LMHead(n, k, max_batch=b, device=0) as head:
+        want, _ = head.backward(g, w, scale=1.0, cap=0.0)
+        got, _ = head.backward(bad, w, scale=1.0, cap=0.0)
+        torch.cuda.synchronize()
+        assert head.device_status() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[3], want[3])
+    assert not bool(got[1].isfinite().any()) and not bool(got[2].isfinite().any())
+
+
+def test_backward_refuses_its_first_call_in_a_capture(torch_cuda):
+    import q5_lm_head_gb300 as mlh
+    torch = torch_cuda
+    n, k = 512, 256
+    w = torch.zeros(n * 176, dtype=torch.uint8, device="cuda")
+    g = torch.zeros((1, n), device="cuda")
+    s = torch.cuda.Stream()
+    with mlh.LMHead(n, k, max_batch=1, device=0) as head:
+        with torch.cuda.stream(s):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                with pytest.raises(mlh.MuseError) as err:
+                    head.backward(g, w, cap=0.0)
+                g.add_(0.0)                          # the capture goes on
+            assert err.value.status == -8
+            head.backward(g, w, cap=0.0)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                out, _ = head.backward(g, w, cap=0.0)
+            graph.replay()
+        torch.cuda.synchronize()
+    assert not out.any()

@@ -264,3 +264,34 @@ def test_distill_in_a_graph_and_on_two_streams(torch_cuda):
         torch.cuda.synchronize()
         for r, ref in res:
             assert all(torch.equal(p, q) for p, q in zip(r, ref))
+
+
+def test_distill_back_to_back_behind_a_forward(torch_cuda):
+    """Forward and distillation one behind another: each loss has to come from its own forward's logits."""
+    import numpy as np
+    import q5_lm_head_gb300 as mlh
+    import q5k_synth as synth
+    torch = torch_cuda
+    wl = synth.WORKLOADS["tiny"]
+    hidden, gamma, wq = synth.inputs_for(wl)
+    w, g = torch.from_numpy(np.ascontiguousarray(wq)).cuda(), torch.from_numpy(gamma).cuda()
+    rows = [torch.from_numpy((hidden * s).astype(np.float32)).cuda() for s in (1.0, 0.3, -2.0)]
+    for r in rows[1:]:
+        r += torch.arange(wl.k, device="cuda") % 3
+    _, ids, lp, _ = _case(torch, 1, wl.n_rows, 12, torch.float32)
+    with mlh.LMHead(wl.n_rows, wl.k, max_batch=1, device=0) as head:
+        logits = torch.empty((1, wl.n_rows), device="cuda")
+
+        def call(h):
+            head.forward(h, w, g, logits=logits)
+            return head.distill(logits, ids, lp, tail=True)
+
+        want = []
+        for h in rows:
+            out = call(h)
+            torch.cuda.synchronize()
+            want.append([t.clone() for t in out])
+        got = [(i % 3, call(rows[i % 3])) for i in range(300)]
+        torch.cuda.synchronize()
+    for i, out in got:
+        assert all(torch.equal(p, q) for p, q in zip(out, want[i]))

@@ -286,3 +286,39 @@ def test_forward_score_is_forward_then_score(torch_cuda, b):
     assert torch.equal(out.top_ids[:, 0], argmax)
     _check(torch, out, logits, tokens, 6, 1.0)
     assert float((lse - out.lse).abs().max()) <= 2e-5     # both within (V/256 + 80) u + 4u |lse| of the same value
+
+
+@pytest.mark.parametrize("b", [1, 5])
+def test_forward_score_back_to_back_with_other_rows(torch_cuda, b):
+    """The scores' kernel starts while the forward still runs: it has to see that forward's logits."""
+    import q5_lm_head_gb300 as mlh
+    import q5k_synth as synth
+    torch = torch_cuda
+    wl = synth.WORKLOADS["tiny"]
+    hidden, gamma, wq = synth.inputs_for(wl)
+    w, g = torch.from_numpy(np.ascontiguousarray(wq)).cuda(), torch.from_numpy(gamma).cuda()
+    rng = np.random.default_rng(b)
+    rows = [torch.from_numpy((hidden * (1 + i) + rng.standard_normal((b, wl.k))).astype(np.float32)).cuda() for i in range(3)]
+    tokens = torch.arange(b, dtype=torch.int32, device="cuda") * 31
+    with mlh.LMHead(wl.n_rows, wl.k, max_batch=b, device=0) as head:
+        want = []
+        for h in rows:
+            logits, out = head.forward_score(h, w, g, tokens=tokens, n_top=9)
+            torch.cuda.synchronize()
+            want.append([t.clone() for t in (logits, *out)])
+        logits = torch.empty((b, wl.n_rows), device="cuda")
+        got = [(i % 3, head.forward_score(rows[i % 3], w, g, tokens=tokens, n_top=9, logits=logits)[1]) for i in range(300)]
+        torch.cuda.synchronize()
+        assert head.device_status() == 0
+    for i, out in got:
+        assert all(torch.equal(p, q) for p, q in zip(out, want[i][1:]))
+
+
+@pytest.mark.parametrize("temperature", [2.0 ** -20, 0.01, 100.0, 2.0 ** 20])
+def test_score_temperatures(torch_cuda, temperature):
+    import q5_lm_head_gb300 as mlh
+    torch = torch_cuda
+    x = _rows(torch, 3, 5003, torch.float32)
+    tokens = torch.tensor([int(x[0].argmax()), 5, 6], dtype=torch.int32, device="cuda")
+    with mlh.LMHead(5003, 256, max_batch=1, device=0) as head:
+        _check(torch, head.score(x, tokens, 7, temperature), x, tokens, 7, temperature)
