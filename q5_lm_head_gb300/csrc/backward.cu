@@ -45,6 +45,7 @@
 #include <atomic>
 #include <cmath>
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 #include <type_traits>
 
@@ -806,6 +807,30 @@ int bwd_splits(int64_t n_rows, int k, int num_sms, int rows) {
   return static_cast<int>(s < stages ? s : stages);
 }
 
+// The matrix in boxes of `rows` rows x `bytes` bytes (a multiple of 16, as the
+// blocks are: every box starts on a 16-byte boundary), beyond its edges zeros.
+// Encoded anew by every call: nothing is kept by the weights' address.
+cudaError_t encode_boxes(CUtensorMap *map, const BackwardArgs &a, int bytes, int rows) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 enc = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    cudaDriverEntryPointQueryResult q;
+    void *p = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    return nullptr;
+  }();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t row = static_cast<cuuint64_t>(a.k / kBlockWeights) * (a.q4 ? kBlockBytesQ4 : kBlockBytes);
+  const cuuint64_t dims[2] = {row / 4, static_cast<cuuint64_t>(a.n_rows)};
+  const cuuint64_t strides[1] = {row};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(bytes / 4), static_cast<cuuint32_t>(rows)};
+  const cuuint32_t steps[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t *>(a.w), dims, strides, box, steps,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
                              A &&...args) {
@@ -829,7 +854,7 @@ template <int NM, bool kQ4>
 cudaError_t launch_backward_nm(const BackwardArgs &a, int gparts, int *splits) {
   using C = BwdCfg<NM, kQ4>;
   CUtensorMap map;
-  cudaError_t e = tc_encode_boxes(&map, a.w, a.n_rows, a.k, a.q4, C::kRowBytes, C::kRows);
+  cudaError_t e = encode_boxes(&map, a, C::kRowBytes, C::kRows);
   if (e != cudaSuccess) return e;
   static std::atomic<unsigned long long> configured{0};   // one bit per device; host threads may race here
   int dev = 0;

@@ -849,14 +849,10 @@ bool tc_supported(int batch, int k) {
 }
 
 cudaError_t tc_encode_weights(CUtensorMap *map, const void *weights, int64_t n_rows, int k, bool q4) {
-  return tc_encode_boxes(map, weights, n_rows, k, q4, q4 ? kBlockBytesQ4 : kBlockBytes, kTileRows);
-}
-
-cudaError_t tc_encode_boxes(CUtensorMap *map, const void *weights, int64_t n_rows, int k, bool q4, int bytes, int rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = get_encoder();
   if (!enc) return cudaErrorNotSupported;
-  // 32-bit elements: a block is 176 or 144 bytes and the box's inner extent a
-  // multiple of 16 too, so every box starts on a 16-byte boundary.  L2 fetches
+  // 32-bit elements: a block (176 or 144 bytes, both multiples of 16) is the
+  // box's inner extent, so every box starts on a 16-byte boundary.  L2 fetches
   // are promoted to 64 bytes only: a box row is 176 bytes, and with 256-byte
   // promotion the evict-first lines around it were often gone before the
   // neighbouring box came for them (2.5 % more DRAM reads than the matrix)
@@ -864,7 +860,7 @@ cudaError_t tc_encode_boxes(CUtensorMap *map, const void *weights, int64_t n_row
   const cuuint64_t gdim[2] = {static_cast<cuuint64_t>(k / kBlockWeights) * (bb / 4),
                               static_cast<cuuint64_t>(n_rows)};
   const cuuint64_t gstride[1] = {static_cast<cuuint64_t>(k / kBlockWeights) * bb};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(bytes / 4), static_cast<cuuint32_t>(rows)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(bb / 4), kTileRows};
   const cuuint32_t estr[2] = {1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(weights), gdim, gstride, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_64B,

@@ -95,8 +95,6 @@ int tc_batch_slots(int batch);                       // the kernel's batch slots
 size_t tc_split_floats(int num_sms, int max_batch);  // split_part size
 size_t tc_split_counters(int num_sms);                // split_cnt size
 cudaError_t tc_encode_weights(CUtensorMap *map, const void *weights, int64_t n_rows, int k, bool q4);
-// The same matrix in boxes of `rows` rows x `bytes` bytes (a multiple of 16).
-cudaError_t tc_encode_boxes(CUtensorMap *map, const void *weights, int64_t n_rows, int k, bool q4, int bytes, int rows);
 cudaError_t launch_tc(const LaunchArgs &a, const CUtensorMap &map);
 
 // Scores of rows of logits [n][ld] (v of them used), dtype 0/1/2 = f32/f16/bf16.
