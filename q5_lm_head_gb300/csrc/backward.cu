@@ -7,8 +7,11 @@
 // and with the norm, r = 1/sqrt(mean h^2 + eps), xh = h r, gg = gx gamma:
 //     gh = r (gg - xh mean(gg xh)),   ggamma = sum_b gx xh
 //
-// Bound: HBM (the matrix is read once), and close to it the unpacking of the
-// quants by the CUDA cores.  The contraction runs along the rows v of W, across
+// Bound: the unpacking of the quants by the CUDA cores, at 1.7 (up to 8 rows) and
+// 3.2 times (32 rows) the time that HBM needs to read the matrix once: the full
+// Q5_K head takes 240 us for one row, 460 us for 32, the Q4_K head 229 us for 8
+// (the main kernel issues in 72 % of all cycles and 84 % on its busiest
+// scheduler, its integer pipe is busy in 63 %).  The contraction runs along the rows v of W, across
 // the direction in which its blocks are packed, so the tensor cores' A operand is
 // W transposed: a lane of tensor memory is an input k, a column a pair of rows.
 //
@@ -20,20 +23,19 @@
 //    of the rows, 96 or 64 rows a stage.
 //    * weight producer warp: a 2-D TMA box of the stage's rows x two blocks.
 //    * operand warps: read the blocks' d, dmin and scales.  With d = md 2^e,
-//      1 <= |md| < 2, the power of two goes to the A side (A = sc (q - middle) 2^e, at most
-//      11 significant bits: exact in f16) and md, exact in f16 too, to the B side: B = t md as the
-//      f16 pair (hi, lo), hi + lo = t md to 2^-21, rows of B side by side.  The
-//      mins are a product of their own, A' = m 2^e' for the 16 sub-blocks,
+//      1 <= |md| < 2, the power of two goes to the A side (A = sc (q - middle) 2^e,
+//      at most 11 significant bits: exact in f16) and md, exact in f16 too, to the
+//      B side: B = t md as the f16 pair (hi, lo), hi + lo = t md to 2^-21.  The mins are a product of their own, A' = m 2^e' for the 16 sub-blocks,
 //      B' = -t mdmin, with middle sc 2^e times B added to the same sums.
 //    * four unpack warpgroups, two for each block, alternating between units of
 //      16 to 48 rows: ldmatrix with transposition gives a thread four rows of
 //      one input, and tcgen05.st (16 lanes x 128 bits) takes that fragment, the
-//      rows in slab_order. 
+//      rows in slab_order.
 //    * MMA warp: per 16 rows four products of M = 128 (two nibble halves of two
 //      blocks) and four small ones for mins and middles.  The tensor cores round
 //      their sums towards zero, about 2^-24 a step, which over a share's thousand
-//      steps would cost 1e-4: every 256 or 288 rows the unpack warps add the accumulators to f32 sums of
-//      their own.
+//      steps would cost 1e-4 of the result: every 256 or 288 rows the unpack warps
+//      add the accumulators to f32 sums of their own (5e-7).
 //    The shares' sums go to the workspace.
 // 3. finish_kernel: a cluster of CTAs a batch row adds the shares in their
 //    order, undoes the power of two and does the norm's backward.
@@ -332,10 +334,9 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
-    // One thread issues all MMAs, so what it computes for each counts: tensor
-    // memory is addressed from 0 (all of it is this CTA's), descriptors are a
-    // slot's first one plus a constant (56 cycles an MMA when both were worked
-    // out each time, against 9 of the MMA itself).
+    // Tensor memory is addressed from 0 (all of it is this CTA's), descriptors
+    // are a slot's first one plus a constant.  An MMA takes about 30 cycles here
+    // (9 by itself with N = 16): it shares tensor memory with the unpack warps.
     const bool issuer = tc::elect_one();
     const uint64_t desc0 = tc::smem_desc_kmajor(ptx::smem_u32(smem + C::kWBytes), C::kLbo, 128);
     bool ok = true;
@@ -905,6 +906,8 @@ cudaError_t launch_backward(const BackwardArgs &a) {
         : slots == 16 ? launch_backward_nm<16, false>(a, gparts, &splits)
                       : launch_backward_nm<32, false>(a, gparts, &splits);
   if (e != cudaSuccess) return e;
+  // eight CTAs a row, or one with little to add (5 rows of 2,048 x 6,656: 13.3 us as a
+  // whole, against 24.0 us with one each; one row of the full head 240 us against 253)
   const int cs = a.k >= 2048 ? 8 : 1;
   e = launch_dependent(finish_kernel, dim3(static_cast<unsigned>(a.batch * cs)), kFinishThreads, 0, cs, a.stream, a, splits,
                        gparts, scale_e);

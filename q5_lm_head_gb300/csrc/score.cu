@@ -7,8 +7,9 @@
 // Ranks and alternatives order by (x descending, index ascending), on x itself:
 // a division could merge neighbouring values.
 //
-// Bound: HBM (each logit is read once) and, close to it, instruction issue for
-// many rows; latency for a few.  A cluster of 1, 2, 4, 8 or 16 CTAs takes a row
+// Bound: HBM (each logit is read once) for many rows, latency for a few: 1,024 rows of
+// 202,048 f32 take 154 us, 5.4 TB/s (79 % of the measured copy rate); the last
+// of their 1.7 rounds of CTAs fills two SMs of three.  A cluster of 1, 2, 4, 8 or 16 CTAs takes a row
 // (as many as keep the GPU's CTA slots filled once), each a contiguous share of
 // its 16-byte vectors; a thread holds a reference m with S and U, and the
 // CTAs' results are pushed into the first one's shared memory.  No global
@@ -557,7 +558,9 @@ cudaError_t launch_score_t(const ScoreArgs &a, int cs) {
   return cudaLaunchKernelEx(&cfg, score_kernel<T, kThreads>, a);
 }
 
-// As many CTAs a row as the SMs have room for at once, each with a step's work.
+// As many CTAs a row as the SMs have room for at once, each with a step's work
+// (one row of 202,048 f32: 34.9 us with one CTA, 15.8, 13.7 and 11.5 us with 4, 8
+// and 16; sixteen rows: 16.7 us with 4 and 8, 17.2 us with 16).
 // A row of its own CTA runs with 256 threads, four CTAs an SM: one's barriers
 // (the bound, the end) fall into the others' loads (1,024 rows of 202,048 f32: 154
 // us, against 162 with 512 threads).
