@@ -11,9 +11,10 @@
 // 3.2 times (32 rows) the time that HBM needs to read the matrix once: the full
 // Q5_K head takes 240 us for one row, 460 us for 32, the Q4_K head 229 us for 8
 // (the main kernel issues in 72 % of all cycles and 84 % on its busiest
-// scheduler, its integer pipe is busy in 63 %).  The contraction runs along the rows v of W, across
-// the direction in which its blocks are packed, so the tensor cores' A operand is
-// W transposed: a lane of tensor memory is an input k, a column a pair of rows.
+// scheduler, its integer pipe is busy in 63 %).  The contraction runs along the
+// rows v of W, across the direction in which its blocks are packed, so the tensor
+// cores' A operand is W transposed: a lane of tensor memory is an input k, a
+// column a pair of rows.
 //
 // Launches:
 // 1. slope_kernel: t of every row, eight consecutive v of a batch row together,
@@ -25,7 +26,8 @@
 //    * operand warps: read the blocks' d, dmin and scales.  With d = md 2^e,
 //      1 <= |md| < 2, the power of two goes to the A side (A = sc (q - middle) 2^e,
 //      at most 11 significant bits: exact in f16) and md, exact in f16 too, to the
-//      B side: B = t md as the f16 pair (hi, lo), hi + lo = t md to 2^-21.  The mins are a product of their own, A' = m 2^e' for the 16 sub-blocks,
+//      B side: B = t md as the f16 pair (hi, lo), hi + lo = t md to 2^-21.  The
+//      mins are a product of their own, A' = m 2^e' for the 16 sub-blocks,
 //      B' = -t mdmin, with middle sc 2^e times B added to the same sums.
 //    * four unpack warpgroups, two for each block, alternating between units of
 //      16 to 48 rows: ldmatrix with transposition gives a thread four rows of
@@ -150,17 +152,20 @@ struct BwdCfg {
     return NM == 8 ? kind * 16 + part * 8 : part * 4 * NM + kind * NM;
   }
   static constexpr int kScl = 16 * kRows * 2;                     // f16 [2 blocks x 8][kRows]
-  static constexpr int kSide = kB + 2 * kScl;                     // B; scales; mins
-  static constexpr int kStage = (kWBytes + kSide + 127) / 128 * 128;
+  static constexpr int kSide = (kB + 2 * kScl + 127) / 128 * 128; // B; scales; mins
   static constexpr int kGroups = 2;                               // of four operand warps, taking the stages in turn
   static constexpr int kThreads = 32 * (kUnpackWarps + 4 * kGroups + 4);   // the weights' warp, two without a role, the MMAs'
   static constexpr int kT = 2 * 4 * kRows * 2;                    // a group's mantissas, f16, two stages of [4][kRows]
   static_assert(kGroups * kT >= 16 * NM * 4, "the mins' sums");
-  static constexpr int kFixed = kGroups * kT + 1024;
-  static constexpr int kFit = (226 * 1024 - kFixed) / kStage;
-  static constexpr int kStages = kFit > 5 ? 5 : kFit;
-  static_assert(kStages >= 3, "stage ring");
-  static constexpr int kSmem = kStages * kStage + kFixed;
+  static constexpr int kFixed = kGroups * kT + 512;               // and the barriers
+  // Two rings: weights are free again as soon as they are unpacked, their
+  // operands only when their products are done.
+  static constexpr int kSides = 3;
+  static constexpr int kFit = (227 * 1024 - kFixed - kSides * kSide) / kWBytes;
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
+  static_assert(kStages >= 3 && kWBytes % 128 == 0, "rings");
+  static constexpr int kSideAt = kStages * kWBytes, kMdAt = kSideAt + kSides * kSide;
+  static constexpr int kSmem = kMdAt + kFixed;
   // Tensor memory: sets of sums of four M-tiles and two min products, then a ring
   // of units of kUS x 16 rows.  Two sets, so that one is added up while the other
   // is in use; with 32 slots one, or the ring would have two units of 16 rows only
@@ -252,11 +257,11 @@ template <int NM, bool kQ4>
 __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     backward_tc_kernel(const __grid_constant__ CUtensorMap wmap, const BackwardArgs a, int gparts, int pairs, int splits) {
   using C = BwdCfg<NM, kQ4>;
-  extern __shared__ __align__(1024) uint8_t smem[];                // [kStages][weights, B tiles, scales, mins]
-  __half *s_md = reinterpret_cast<__half *>(smem + C::kStages * C::kStage);   // [kGroups][kT]
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kStages * C::kStage + C::kGroups * C::kT);
-  uint64_t *wfull = bars, *pfull = wfull + C::kStages, *empty = pfull + C::kStages;
-  uint64_t *tfull = empty + C::kStages, *tempty = tfull + C::kBufs;
+  extern __shared__ __align__(1024) uint8_t smem[];                // [kStages][weights], [kSides][B tiles, scales, mins]
+  __half *s_md = reinterpret_cast<__half *>(smem + C::kMdAt);      // [kGroups][kT]
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kMdAt + C::kGroups * C::kT);
+  uint64_t *wfull = bars, *wempty = wfull + C::kStages, *pfull = wempty + C::kStages, *pempty = pfull + C::kSides;
+  uint64_t *tfull = pempty + C::kSides, *tempty = tfull + C::kBufs;
   uint64_t *dfull = tempty + C::kBufs, *dfree = dfull + 2, *done = dfree + 2;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(done + 1);
   volatile uint32_t *s_abort = s_tmem + 1;
@@ -275,8 +280,11 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       ptx::mbar_init(&wfull[i], 1);
+      ptx::mbar_init(&wempty[i], kUnpackWarps);                   // the operand warps have read them before
+    }
+    for (int i = 0; i < C::kSides; ++i) {
       ptx::mbar_init(&pfull[i], 4);
-      ptx::mbar_init(&empty[i], kUnpackWarps + 1);                // the unpack warps, the MMAs
+      ptx::mbar_init(&pempty[i], 1);                              // the MMAs, which the unpack warps' reads come before
     }
     for (int i = 0; i < C::kBufs; ++i) {
       ptx::mbar_init(&tfull[i], kUnpackWarps / 2);
@@ -321,9 +329,9 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       int issued = 0, slot = 0;
       uint32_t ph = 0;
       for (int i = 0; i < n_st; ++i) {
-        if (i >= C::kStages && !wait_one(&empty[slot], ph ^ 1u)) { fail(); break; }
+        if (i >= C::kStages && !wait_one(&wempty[slot], ph ^ 1u)) { fail(); break; }
         ptx::mbar_arrive_expect_tx(&wfull[slot], C::kWBytes);
-        tma_box(smem + slot * C::kStage, &wmap, pair * (C::kBB / 2), static_cast<int>((st0 + i) * C::kRows), &wfull[slot],
+        tma_box(smem + slot * C::kWBytes, &wmap, pair * (C::kBB / 2), static_cast<int>((st0 + i) * C::kRows), &wfull[slot],
                 policy);
         issued = i + 1;
         if (++slot == C::kStages) { slot = 0; ph ^= 1u; }
@@ -338,7 +346,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     // are a slot's first one plus a constant.  An MMA takes about 30 cycles here
     // (9 by itself with N = 16): it shares tensor memory with the unpack warps.
     const bool issuer = tc::elect_one();
-    const uint64_t desc0 = tc::smem_desc_kmajor(ptx::smem_u32(smem + C::kWBytes), C::kLbo, 128);
+    const uint64_t desc0 = tc::smem_desc_kmajor(ptx::smem_u32(smem + C::kSideAt), C::kLbo, 128);
     bool ok = true;
     int slot = 0, buf = 0;
     uint32_t pph = 0, tph = 0;
@@ -347,7 +355,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       const bool opens = i % C::kFlush == 0;
       if (opens && period >= C::kSets && !(ok = wait(&dfree[db], ((period / C::kSets) & 1) ^ 1))) break;
       if (!(ok = wait(&pfull[slot], pph))) break;
-      const uint64_t desc = desc0 + static_cast<uint64_t>(slot) * (C::kStage >> 4);
+      const uint64_t desc = desc0 + static_cast<uint64_t>(slot) * (C::kSide >> 4);
       const uint32_t d = db * 6 * C::kD;
 #pragma unroll
       for (int u = 0; u < C::kUnits; ++u) {
@@ -379,11 +387,11 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       }
       if (!ok) break;
       if (issuer) {
-        tc::commit(&empty[slot]);
+        tc::commit(&pempty[slot]);
         if ((i + 1) % C::kFlush == 0 || i + 1 == n_st) tc::commit(&dfull[db]);
       }
       __syncwarp();
-      if (++slot == C::kStages) { slot = 0; pph ^= 1u; }
+      if (++slot == C::kSides) { slot = 0; pph ^= 1u; }
     }
     if (!ok && lane == 0) fail();
     // tensor memory is freed only after every MMA issued here completed
@@ -421,11 +429,12 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     bool bad = false, big = false;
     int turn = 0;
     for (int i = grp; i < n_st; i += C::kGroups, turn ^= 1) {
-      const int slot = i % C::kStages;
+      const int slot = i % C::kStages, side_slot = i % C::kSides;
       __half *md_at = s_md + grp * (C::kT / 2) + turn * 4 * C::kRows;
-      // the stage's weights: they were sent for only after the slot's last readers were done with it
-      bad = !wait(&wfull[slot], (i / C::kStages) & 1);
-      uint8_t *st = smem + slot * C::kStage, *side = st + C::kWBytes;
+      bad = !wait(&wfull[slot], (i / C::kStages) & 1) ||
+            (i >= C::kSides && !wait(&pempty[side_slot], ((i / C::kSides) & 1) ^ 1));
+      const uint8_t *st = smem + slot * C::kWBytes;
+      uint8_t *side = smem + C::kSideAt + side_slot * C::kSide;
       if (!bad) {
         // a block's header: powers of two with its scales and mins, mantissas for B
 #pragma unroll
@@ -494,7 +503,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the tiles, to the tensor cores' reads
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&pfull[slot]);
+      if (lane == 0) ptx::mbar_arrive(&pfull[side_slot]);
       fetch(i + C::kGroups < n_st);
     }
     if (bad && lane == 0) fail();
@@ -559,11 +568,11 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       return true;
     };
     bool ok = true;
-    int slot = 0, buf = par, unit = par;        // unit: of the whole share; its buffer is unit % kBufs
+    int slot = 0, side_slot = 0, buf = par, unit = par;   // unit: of the whole share; its buffer is unit % kBufs
     uint32_t pph = 0, tph = 0;
     for (int i = 0; i < n_st; ++i) {
-      if (!(ok = wait(&pfull[slot], pph))) break;   // the weights too: the operand warps have waited for them
-      const uint8_t *side = smem + slot * C::kStage + C::kWBytes;
+      if (!(ok = wait(&pfull[side_slot], pph))) break;    // the weights too: the operand warps have waited for them
+      const uint8_t *side = smem + C::kSideAt + side_slot * C::kSide;
       const __half *scl = reinterpret_cast<const __half *>(side + C::kB) + (blk * 8 + 2 * wq) * C::kRows + 4 * (lane & 3);
       // of sub-block lane/4 of block wq: the mins for one warpgroup, the scales for the other
       const __half *small = reinterpret_cast<const __half *>(side + C::kB) + ((blk ? 0 : 16) + 8 * (wq & 1) + (lane >> 2)) * C::kRows + 4 * (lane & 3);
@@ -571,7 +580,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
         if (unit >= C::kBufs && !(ok = wait(&tempty[buf], tph ^ 1u))) break;
         tc::fence_after();
         const uint32_t at0 = tbase + lane_base + C::kABase + buf * C::kUS * C::kSlab, at_small = at0 + 8 * blk;
-        const uint32_t src1 = src0 + slot * C::kStage + u * C::kUS * 16 * C::kRowBytes;
+        const uint32_t src1 = src0 + slot * C::kWBytes + u * C::kUS * 16 * C::kRowBytes;
         auto slab_to_tmem = [&](auto s_const) {
           constexpr int s = decltype(s_const)::value;
           const int slab = u * C::kUS + s;
@@ -632,8 +641,9 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       }
       if (!ok) break;
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&empty[slot]);
-      if (++slot == C::kStages) { slot = 0; pph ^= 1u; }
+      if (lane == 0) ptx::mbar_arrive(&wempty[slot]);
+      if (++slot == C::kStages) slot = 0;
+      if (++side_slot == C::kSides) { side_slot = 0; pph ^= 1u; }
       // the set before the one now in use; or the only set, one stage after its last (the ring holds that stage)
       const bool due = C::kSets == 2 ? (i + 1) % C::kFlush == 0 && i + 1 > C::kFlush : i % C::kFlush == 0 && i > 0;
       if (due && !(ok = flush())) break;
