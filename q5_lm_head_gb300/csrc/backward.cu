@@ -62,7 +62,7 @@
 namespace muse {
 namespace {
 
-constexpr int kMaxParts = 64;                 // of a row's largest |gl|
+constexpr int kMaxParts = 1216;                // of the rows' largest |gl|, all rows together: eight CTAs an SM
 constexpr int kPadRows = 192;                 // t is kept, as zeros, up to a multiple of this
 constexpr int kTileCols = 2 * kBlockWeights;  // inputs of a CTA
 constexpr int kFlushRows = 256;               // between additions of the accumulators to the f32 sums, about
@@ -78,7 +78,8 @@ constexpr uint32_t kTmem = 512;
 // the scale's mantissa in [2^11, 2^12) is below 2^13.
 __device__ __forceinline__ int row_exponent(const float *gmax, int b, int parts) {
   float m = 0.0f;
-  for (int i = 0; i < parts; ++i) m = fmaxf(m, __ldcg(gmax + b * kMaxParts + i));
+  for (int i = threadIdx.x & 31; i < parts; i += 32) m = fmaxf(m, __ldcg(gmax + b * parts + i));
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
   return m == 0.0f ? 0 : e < -126 ? -126 : e;   // 128 for infinities: they stay what they are
 }
@@ -93,34 +94,53 @@ __device__ __forceinline__ float pow2(int e) {   // -126 <= e <= 127
 __device__ __forceinline__ float cap_slope(float l, float cap, float inv_cap2) { return (cap - l) * (cap + l) * inv_cap2; }
 
 // t[p/8][b][p%8] = gl * scale_m * slope of row v, p = slab_order(v), scale_m the scale's mantissa.
-__global__ void __launch_bounds__(256) slope_kernel(const BackwardArgs a, float scale_m) {
+__global__ void __launch_bounds__(256) slope_kernel(const BackwardArgs a, float scale_m, int64_t share) {
   __shared__ float s_max[8];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the main kernel's set-up beside this one
   const int b = blockIdx.y;
-  const float *g = a.grad_logits + b * a.n_rows, *l = a.logits + b * a.n_rows;
-  const int64_t octs = (a.n_rows + kPadRows - 1) / kPadRows * (kPadRows / 8);
-  const int64_t lo = octs * blockIdx.x / gridDim.x * 8, hi = octs * (blockIdx.x + 1) / gridDim.x * 8;
+  const int64_t row = static_cast<int64_t>(b) * a.n_rows;
+  const float *g = a.grad_logits + row, *l = a.logits + row;
+  const bool aligned = (row & 3) == 0;
+  const int64_t fours = (a.n_rows + kPadRows - 1) / kPadRows * (kPadRows / 4);
+  const int64_t lo = share * blockIdx.x, hi = lo + share < fours ? lo + share : fours;
   const float inv_cap2 = a.cap > 0.0f ? 1.0f / (a.cap * a.cap) : 0.0f;
   float m = 0.0f;
-#pragma unroll 8
-  for (int64_t v = lo + threadIdx.x; v < hi; v += 256) {
-    float t = 0.0f;
-    if (v < a.n_rows) {
-      const float x = __ldcs(g + v);
-      m = fmaxf(m, fabsf(x));
-      t = x;
-      if (a.cap > 0.0f) t *= cap_slope(__ldcs(l + v), a.cap, inv_cap2);
-      t *= scale_m;
+#pragma unroll 4
+  for (int64_t i = lo + threadIdx.x; i < hi; i += 256) {
+    const int64_t v = 4 * i;
+    float x[4] = {}, y[4] = {};
+    if (aligned && v + 4 <= a.n_rows) {
+      const float4 t = __ldcs(reinterpret_cast<const float4 *>(g + v));
+      x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
+      if (a.cap > 0.0f) {
+        const float4 u = __ldcs(reinterpret_cast<const float4 *>(l + v));
+        y[0] = u.x, y[1] = u.y, y[2] = u.z, y[3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (v + j < a.n_rows) {
+          x[j] = __ldcs(g + v + j);
+          if (a.cap > 0.0f) y[j] = __ldcs(l + v + j);
+        }
     }
-    const int64_t at = (v & ~int64_t{15}) | slab_order(static_cast<int>(v & 15));
-    a.t[((at >> 3) * a.batch + b) * 8 + (at & 7)] = t;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      m = fmaxf(m, fabsf(x[j]));
+      if (a.cap > 0.0f) x[j] *= cap_slope(y[j], a.cap, inv_cap2);
+      x[j] *= scale_m;
+    }
+    // slab_order: rows 4j, 4j + 1 to places 2j, 2j + 1 of the slab's first eight, the others to its second
+    float *t = a.t + ((v >> 4 << 1) * a.batch + b) * 8 + ((v >> 1) & 6);
+    *reinterpret_cast<float2 *>(t) = make_float2(x[0], x[1]);
+    *reinterpret_cast<float2 *>(t + 8 * a.batch) = make_float2(x[2], x[3]);
   }
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int i = 1; i < 8; ++i) m = fmaxf(m, s_max[i]);
-    a.gmax[b * kMaxParts + blockIdx.x] = m;
+    a.gmax[b * gridDim.x + blockIdx.x] = m;
     if (blockIdx.x == 0 && b == 0) *a.flag = 0u;
   }
 }
@@ -265,6 +285,8 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
   uint64_t *dfull = tempty + C::kBufs, *dfree = dfull + 2, *done = dfree + 2;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(done + 1);
   volatile uint32_t *s_abort = s_tmem + 1;
+  float *s_e2 = reinterpret_cast<float *>(s_tmem + 2);            // [NM] powers of two that bring the rows' t into f16's range
+  static_assert((2 * C::kStages + 2 * C::kSides + 2 * C::kBufs + 5) * 8 + 8 + 4 * NM <= 512, "behind the mantissas");
 
   // the warp's index from one lane: the compiler then knows the roles' branches and loops to be uniform
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -408,6 +430,10 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     const int from_end = kPrepThreads - 1 - pt;                   // few batch rows: by the last warp, beside the MMAs'
     const int oct = from_end % kOcts, b_first = from_end < kStepB * kOcts ? from_end / kOcts : NM;
     asm volatile("griddepcontrol.wait;" ::: "memory");            // t and the rows' largest values
+    for (int b = warp - kUnpackWarps; b < a.batch; b += 4 * C::kGroups) {
+      const float e = pow2(-min(row_exponent(a.gmax, b, gparts), 126));
+      if (lane == 0) s_e2[b] = e;
+    }
     float e2[kTasks];
     float4 t_next[kTasks][2];
     const float4 *t_at = reinterpret_cast<const float4 *>(a.t) + ((st0 + grp) * kOcts + oct) * a.batch * 2 + 2 * b_first;
@@ -421,10 +447,11 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       t_at += static_cast<int64_t>(C::kGroups) * kOcts * a.batch * 2;
     };
     fetch(grp < n_st);
+    ptx::named_bar_sync(2 + C::kGroups, kPrepThreads * C::kGroups);
 #pragma unroll
     for (int j = 0; j < kTasks; ++j) {
       const int b = b_first + j * kStepB;
-      e2[j] = b < a.batch ? pow2(-min(row_exponent(a.gmax, b, gparts), 126)) : 0.0f;
+      e2[j] = b < a.batch ? s_e2[b] : 0.0f;
     }
     bool bad = false, big = false;
     int turn = 0;
@@ -720,6 +747,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const BackwardAr
   const int hi = static_cast<int>(static_cast<int64_t>(a.k / 4) * (cr + 1) / cs) * 4;
   cluster_arrive();
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (a.grad_gamma && a.batch > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // gamma_kernel follows
   const bool plain = __ldcg(a.flag) != 0u;
   const double back = ldexp(1.0, min(row_exponent(a.gmax, b, gparts), 126) + scale_e);
   const int64_t stride = static_cast<int64_t>(a.batch) * a.k;
@@ -891,18 +919,19 @@ size_t backward_part_floats(int64_t n_rows, int k, int max_batch, int num_sms) {
 size_t backward_t_floats(int64_t n_rows, int max_batch) {
   return static_cast<size_t>((n_rows + kPadRows - 1) / kPadRows * kPadRows) * max_batch;
 }
-size_t backward_misc_floats() { return 32 * kMaxParts + 32 + 1; }   // largest |gl|, RMS factors, flag
+size_t backward_misc_floats() { return kMaxParts + 32 + 1; }   // largest |gl|, RMS factors, flag
 
 cudaError_t launch_backward(const BackwardArgs &a) {
   // the scale as scale_m 2^scale_e, 2^11 <= |scale_m| < 2^12
   int scale_e = 0;
   const float scale_m = std::ldexp(std::frexp(a.scale, &scale_e), 12);
   scale_e -= 12;
-  // at least 1,024 values a part
-  int gparts = static_cast<int>(a.n_rows / 1024);
-  gparts = gparts < 1 ? 1 : gparts > kMaxParts ? kMaxParts : gparts;
+  // rows of t in fours: one a thread at least, shares of whole CTAs
+  const int64_t ctas = (a.n_rows + kPadRows - 1) / kPadRows * (kPadRows / 4) / 256 + 1, most = kMaxParts / a.batch;
+  const int64_t share = (ctas + most - 1) / most * 256;
+  const int gparts = static_cast<int>((ctas * 256 + share - 1) / share);
   // an ordinary launch: after everything before it on the stream, the weights' own writer too
-  slope_kernel<<<dim3(static_cast<unsigned>(gparts), static_cast<unsigned>(a.batch)), 256, 0, a.stream>>>(a, scale_m);
+  slope_kernel<<<dim3(static_cast<unsigned>(gparts), static_cast<unsigned>(a.batch)), 256, 0, a.stream>>>(a, scale_m, share);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   int splits = 1;
