@@ -7,11 +7,13 @@
 // and with the norm, r = 1/sqrt(mean h^2 + eps), xh = h r, gg = gx gamma:
 //     gh = r (gg - xh mean(gg xh)),   ggamma = sum_b gx xh
 //
-// Bound: the unpacking of the quants by the CUDA cores, at 1.7 (up to 8 rows) and
-// 3.2 times (32 rows) the time that HBM needs to read the matrix once: the full
-// Q5_K head takes 240 us for one row, 460 us for 32, the Q4_K head 229 us for 8
-// (the main kernel issues in 72 % of all cycles and 84 % on its busiest
-// scheduler, its integer pipe is busy in 63 %).  The contraction runs along the
+// Bound: the unpacking of the quants by the CUDA cores, at 1.6 (up to 8 rows) and
+// 2.8 times (32 rows) the time that HBM needs to read the matrix once: the full
+// Q5_K head takes 224 us for one row, 408 us for 32, the Q4_K head 207 us for 8
+// (for one row the main kernel, 216 us of it, issues in 72 % of all cycles and
+// 84 % on its busiest scheduler, its integer pipe is busy in 63 %; for 32 rows,
+// 398 us, in 64 %: there the operand warps' work is nearly half the unpacking's
+// and the products' N is four times as wide).  The contraction runs along the
 // rows v of W, across the direction in which its blocks are packed, so the tensor
 // cores' A operand is W transposed: a lane of tensor memory is an input k, a
 // column a pair of rows.
@@ -22,7 +24,9 @@
 //    row's t into f16's range.
 // 2. backward_tc_kernel: a CTA takes two block columns (512 inputs) and a share
 //    of the rows, 96 or 64 rows a stage.
-//    * weight producer warp: a 2-D TMA box of the stage's rows x two blocks.
+//    * weight producer warp: a 2-D TMA box of the stage's rows x two blocks, in a
+//      ring of its own: a slot is free again when it is unpacked, while the
+//      operands wait for their products (one ring of both: 240 and 460 us).
 //    * operand warps: read the blocks' d, dmin and scales.  With d = md 2^e,
 //      1 <= |md| < 2, the power of two goes to the A side (A = sc (q - middle) 2^e,
 //      at most 11 significant bits: exact in f16) and md, exact in f16 too, to the
@@ -152,8 +156,9 @@ struct BwdCfg {
   // A box row is two blocks and the next 16 bytes: rows 368 (304) bytes apart put
   // eight rows' 16-byte pieces, which a transposing load takes at once, on all banks.
   static constexpr int kRowBytes = 2 * kBB + 16;
-  // Rows of a stage: the more, the less the barriers of a stage cost; with more
-  // than 8 slots the stage's B tiles leave room for 64.
+  // Rows of a stage: the more, the less the barriers of a stage cost (one row 224
+  // us with units of 48 of them, 247 us with 64 rows in units of 32); with more than
+  // 8 slots the stage's B tiles leave room for 64.
   static constexpr int kRows = NM == 8 ? 96 : 64;
   static constexpr int kWBytes = kRows * kRowBytes;
   static constexpr int kN = 2 * NM;                               // B rows: hi, lo
@@ -179,7 +184,9 @@ struct BwdCfg {
   static_assert(kGroups * kT >= 16 * NM * 4, "the mins' sums");
   static constexpr int kFixed = kGroups * kT + 512;               // and the barriers
   // Two rings: weights are free again as soon as they are unpacked, their
-  // operands only when their products are done.
+  // operands only when their products are done.  Of these three, or four with
+  // 32 slots and fewer weights (414 us against 408), or two (one row 249 us
+  // against 224).
   static constexpr int kSides = 3;
   static constexpr int kFit = (227 * 1024 - kFixed - kSides * kSide) / kWBytes;
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
@@ -189,7 +196,7 @@ struct BwdCfg {
   // Tensor memory: sets of sums of four M-tiles and two min products, then a ring
   // of units of kUS x 16 rows.  Two sets, so that one is added up while the other
   // is in use; with 32 slots one, or the ring would have two units of 16 rows only
-  // (537 us for a full head of 32 rows, against 466).
+  // (491 us for a full head of 32 rows, against 408).
   static constexpr int kSets = NM == 32 ? 1 : 2;
   static constexpr int kUS = NM == 8 ? 3 : 2;
   static constexpr int kUnits = kRows / (16 * kUS);               // units a stage
@@ -285,7 +292,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
   uint64_t *dfull = tempty + C::kBufs, *dfree = dfull + 2, *done = dfree + 2;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(done + 1);
   volatile uint32_t *s_abort = s_tmem + 1;
-  float *s_e2 = reinterpret_cast<float *>(s_tmem + 2);            // [NM] powers of two that bring the rows' t into f16's range
+  float *s_e2 = reinterpret_cast<float *>(s_tmem + 2);            // [NM] powers of two: rows of t into f16's range
   static_assert((2 * C::kStages + 2 * C::kSides + 2 * C::kBufs + 5) * 8 + 8 + 4 * NM <= 512, "behind the mantissas");
 
   // the warp's index from one lane: the compiler then knows the roles' branches and loops to be uniform
@@ -472,7 +479,8 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
           int ed, em;
           md_at[blk * C::kRows + slab_order(row)] = __float2half_rn(split_d(dd.x, ed, big));
           md_at[(2 + blk) * C::kRows + slab_order(row)] = __float2half_rn(-split_d(dd.y, em, big));
-          const uint32_t pd = pack_half2(pow2(ed - Quant<kQ4>::kLow), pow2(ed - Quant<kQ4>::kHigh));   // the quants come multiplied
+          // the quants come multiplied
+          const uint32_t pd = pack_half2(pow2(ed - Quant<kQ4>::kLow), pow2(ed - Quant<kQ4>::kHigh));
           const uint32_t pm = pack_half2(pow2(em), pow2(em));
           const uint32_t sc[2] = {hdr.y & 0x3F3F3F3Fu, (hdr.w & 0x0F0F0F0Fu) | ((hdr.y >> 2) & 0x30303030u)};
           const uint32_t mn[2] = {hdr.z & 0x3F3F3F3Fu, ((hdr.w >> 4) & 0x0F0F0F0Fu) | ((hdr.z >> 2) & 0x30303030u)};
@@ -540,8 +548,10 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     const int blk = (warp >> 2) & 1, par = warp >> 3, wq = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(32 * wq) << 16;
     const uint32_t rot = static_cast<uint32_t>(6 - 2 * wq) & 31u;   // high bit 2wq -> 6, 2wq + 1 -> 7
-    // what this warpgroup's small operand is multiplied by: 1 for mins, the middle for scales (divided as sub-block lane/4's)
-    const float middle1 = blk ? Quant<kQ4>::kMiddle * pow2((lane >> 2) & 1 ? Quant<kQ4>::kHigh : Quant<kQ4>::kLow) : 1.0f;
+    // what this warpgroup's small operand is multiplied by: 1 for mins, the middle
+    // for scales (divided as sub-block lane/4's)
+    const int k_divided = (lane >> 2) & 1 ? Quant<kQ4>::kHigh : Quant<kQ4>::kLow;
+    const float middle1 = blk ? Quant<kQ4>::kMiddle * pow2(k_divided) : 1.0f;
     const uint32_t middle = pack_half2(middle1, middle1);
     const uint32_t src0 = ptx::smem_u32(smem) + (lane & 15) * C::kRowBytes + blk * C::kBB + 16 * (lane >> 4);
     // the f32 sums: inputs of M-tile warp/4 by batch row, and mins (lane: sub-block) of eight batch rows
@@ -600,9 +610,10 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     for (int i = 0; i < n_st; ++i) {
       if (!(ok = wait(&pfull[side_slot], pph))) break;    // the weights too: the operand warps have waited for them
       const uint8_t *side = smem + C::kSideAt + side_slot * C::kSide;
-      const __half *scl = reinterpret_cast<const __half *>(side + C::kB) + (blk * 8 + 2 * wq) * C::kRows + 4 * (lane & 3);
+      const __half *k_at = reinterpret_cast<const __half *>(side + C::kB) + 4 * (lane & 3);
+      const __half *scl = k_at + (blk * 8 + 2 * wq) * C::kRows;
       // of sub-block lane/4 of block wq: the mins for one warpgroup, the scales for the other
-      const __half *small = reinterpret_cast<const __half *>(side + C::kB) + ((blk ? 0 : 16) + 8 * (wq & 1) + (lane >> 2)) * C::kRows + 4 * (lane & 3);
+      const __half *small = k_at + ((blk ? 0 : 16) + 8 * (wq & 1) + (lane >> 2)) * C::kRows;
       for (int u = par; u < C::kUnits; u += 2) {
         if (unit >= C::kBufs && !(ok = wait(&tempty[buf], tph ^ 1u))) break;
         tc::fence_after();
@@ -945,8 +956,8 @@ cudaError_t launch_backward(const BackwardArgs &a) {
         : slots == 16 ? launch_backward_nm<16, false>(a, gparts, &splits)
                       : launch_backward_nm<32, false>(a, gparts, &splits);
   if (e != cudaSuccess) return e;
-  // eight CTAs a row, or one with little to add (5 rows of 2,048 x 6,656: 13.3 us as a
-  // whole, against 24.0 us with one each; one row of the full head 240 us against 253)
+  // eight CTAs a row, or one with little to add (5 rows of 2,048 x 6,656: 12.5 us as a
+  // whole, against 22.7 us with one each; one row of the full head 224 us against 238)
   const int cs = a.k >= 2048 ? 8 : 1;
   e = launch_dependent(finish_kernel, dim3(static_cast<unsigned>(a.batch * cs)), kFinishThreads, 0, cs, a.stream, a, splits,
                        gparts, scale_e);
