@@ -585,7 +585,11 @@ int ensure_backward(muse_lmhead *h, cudaStream_t stream) {
                    padded_floats(muse::backward_part_floats(h->n_rows, static_cast<int>(h->k), h->max_batch, h->num_sms)) +
                    muse::backward_t_floats(h->n_rows, h->max_batch);
   void *p = nullptr;
-  if ((e = cudaMalloc(&p, sizeof(float) * n)) != cudaSuccess) {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;   // another stream's capture by this thread goes on
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  e = cudaMalloc(&p, sizeof(float) * n);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) {
     cudaGetLastError();                   // a failed allocation is this call's answer, not the next one's
     return e == cudaErrorMemoryAllocation ? MUSE_ERR_NOMEM : cuda_fail(e);
   }

@@ -349,3 +349,25 @@ def test_backward_refuses_its_first_call_in_a_capture(torch_cuda):
             graph.replay()
         torch.cuda.synchronize()
     assert not out.any()
+
+
+def test_backward_first_call_beside_another_streams_capture(torch_cuda):
+    import q5_lm_head_gb300 as mlh
+    torch = torch_cuda
+    n, k = 512, 256
+    w = torch.zeros(n * 176, dtype=torch.uint8, device="cuda")
+    g = torch.zeros((1, n), device="cuda")
+    out = torch.ones((1, k), device="cuda")
+    x = torch.ones(8, device="cuda")
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with mlh.LMHead(n, k, max_batch=1, device=0) as head:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            x.add_(1.0)
+            head.backward(g, w, cap=0.0, grad_hidden=out, stream=other)   # allocates; runs at once on its stream
+        torch.cuda.synchronize()
+        assert not bool(out.any())
+        graph.replay()
+        torch.cuda.synchronize()
+        assert bool((x == 2.0).all())
