@@ -9,11 +9,11 @@
 //
 // Bound: HBM (each logit is read once) for many rows, latency for a few: 1,024 rows of
 // 202,048 f32 take 154 us, 5.4 TB/s (79 % of the measured copy rate); the last
-// of their 1.7 rounds of CTAs fills two SMs of three.  A cluster of 1, 2, 4, 8 or 16 CTAs takes a row
-// (as many as keep the GPU's CTA slots filled once), each a contiguous share of
-// its 16-byte vectors; a thread holds a reference m with S and U, and the
-// CTAs' results are pushed into the first one's shared memory.  No global
-// workspace, so calls may overlap.
+// of their 1.7 rounds of CTAs fills two SMs of three.  A cluster of 1, 2, 4, 8 or
+// 16 CTAs takes a row (about as many as give each SM one), each a contiguous share
+// of its 16-byte vectors; a thread holds a reference m with S and U, and the CTAs'
+// results are pushed into the first one's shared memory.  No global workspace, so
+// calls may overlap.
 //
 // Alternatives: a thread's running maximum stands for an element of its own, so
 // the n_top-th largest of the maxima (of groups of two or four threads) is a
@@ -484,17 +484,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
       st = stat_warp(st, c);
       before = __reduce_add_sync(0xffffffffu, in ? sh.from_before[lane] : 0);
     }
-    if (k > 0) {                          // close the lists up: one warp a CTA's
-      int at = 0, mine = 0;
+    if (k > 0) {                          // close the lists up
       n = 0;
-      for (uint32_t r = 0; r < cs; ++r) {
-        if (r == static_cast<uint32_t>(warp)) {
-          at = n;
-          mine = sh.from_n[r];
-        }
-        n += sh.from_n[r];
+      for (int r = 0; r < static_cast<int>(cs); ++r) {
+        const int theirs = sh.from_n[r];
+        if (r % kWarps == warp)
+          for (int i = lane; i < theirs; i += 32) sh.list[n + i] = sh.got[r * kShort + i];
+        n += theirs;
       }
-      for (int i = lane; i < mine; i += 32) sh.list[at + i] = sh.got[warp * kShort + i];
     }
   }
   if (tid == 0) {
@@ -558,17 +555,26 @@ cudaError_t launch_score_t(const ScoreArgs &a, int cs) {
   return cudaLaunchKernelEx(&cfg, score_kernel<T, kThreads>, a);
 }
 
-// As many CTAs a row as the SMs have room for at once, each with a step's work
-// (one row of 202,048 f32: 34.9 us with one CTA, 15.8, 13.7 and 11.5 us with 4, 8
-// and 16; sixteen rows: 16.7 us with 4 and 8, 17.2 us with 16).
-// A row of its own CTA runs with 256 threads, four CTAs an SM: one's barriers
-// (the bound, the end) fall into the others' loads (1,024 rows of 202,048 f32: 154
-// us, against 162 with 512 threads).
+// CTAs a row, and their threads (times in us for rows of 202,048 f32 and 8
+// alternatives, by threads/CTAs a row; rows of 32,000 f32 and 50,257 bf16 order
+// alike).  One CTA of 512 threads an SM (1 row: 512/16 11.6, 512/8 13.8, 512/1
+// 32.9; 16 rows: 512/8 17.4, 512/16 18.7), or of 256 threads where a share is
+// short (one row of 50,257 bf16: 256/8 9.1, 512/8 9.9, 512/16 11.2).  Where whole
+// powers of two would leave a third of the SMs without one, smaller and more of
+// them, two or three an SM (77 rows: 256/4 28.2, 512/2 30.2, 512/1 35.7).  Rows for
+// more than one round of SMs: 153 rows 256/2 41.9, 512/1 46.6, 256/1 55.2; 304 rows
+// 512/1 51.4, 256/2 54.9; beyond, four CTAs of 256 an SM, whose barriers fall into
+// the others' loads (400 rows 256/1 73.3, 512/1 79.6).
 template <typename T>
 cudaError_t launch_score_rows(const ScoreArgs &a) {
+  const int64_t n = a.n, sms = a.num_sms, bytes = a.v * static_cast<int64_t>(sizeof(T));
+  constexpr int64_t kLeast = 8192, kShortShare = 16384;   // bytes of a CTA
+  if (2 * n > 3 * sms) return n <= 2 * sms ? launch_score_t<T, 512>(a, 1) : launch_score_t<T, 256>(a, 1);
+  if (n > sms) return launch_score_t<T, 256>(a, bytes >= 2 * kLeast ? 2 : 1);
   int cs = 1;
-  while (cs < kMaxCluster && a.n * 2 * cs <= 2 * a.num_sms && a.v / (2 * cs) >= 2048) cs *= 2;
-  return cs == 1 ? launch_score_t<T, 256>(a, cs) : launch_score_t<T, 512>(a, cs);
+  while (cs < kMaxCluster && 2 * n * cs <= sms && bytes / (2 * cs) >= kLeast) cs *= 2;
+  if (cs <= 2 && 3 * n * cs <= 2 * sms && bytes / (4 * cs) >= kLeast) return launch_score_t<T, 256>(a, 4 * cs);
+  return bytes / cs < kShortShare ? launch_score_t<T, 256>(a, cs) : launch_score_t<T, 512>(a, cs);
 }
 
 }  // namespace

@@ -322,3 +322,16 @@ def test_score_temperatures(torch_cuda, temperature):
     tokens = torch.tensor([int(x[0].argmax()), 5, 6], dtype=torch.int32, device="cuda")
     with mlh.LMHead(5003, 256, max_batch=1, device=0) as head:
         _check(torch, head.score(x, tokens, 7, temperature), x, tokens, 7, temperature)
+
+
+@pytest.mark.parametrize("n,v", [(3, 2500), (5, 9000), (9, 60000), (20, 20000), (40, 30000), (77, 40000), (100, 33000),
+                                 (140, 9001), (153, 9001), (200, 2000), (228, 9000), (229, 5000), (304, 5000), (305, 5000)])
+def test_score_rows_by_every_number_of_ctas(torch_cuda, n, v):
+    import q5_lm_head_gb300 as mlh
+    torch = torch_cuda
+    x = _rows(torch, n, v, torch.bfloat16, pad=3, offset=1)
+    tokens = torch.arange(n, dtype=torch.int32, device="cuda") * 37 % v
+    with mlh.LMHead(v, 256, max_batch=1, device=0) as head:
+        out = head.score(x, tokens, n_top=64)
+        torch.cuda.synchronize()
+    _check(torch, out, x, tokens, 64, 1.0)
