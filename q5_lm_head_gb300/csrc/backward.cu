@@ -9,10 +9,10 @@
 //
 // Bound: the unpacking of the quants by the CUDA cores, at 1.6 (up to 8 rows) and
 // 2.8 times (32 rows) the time that HBM needs to read the matrix once: the full
-// Q5_K head takes 224 us for one row, 408 us for 32, the Q4_K head 207 us for 8
-// (for one row the main kernel, 216 us of it, issues in 72 % of all cycles and
+// Q5_K head takes 219 us for one row, 405 us for 32, the Q4_K head 206 us for 8
+// (for one row the main kernel, 211 us of it, issues in 72 % of all cycles and
 // 84 % on its busiest scheduler, its integer pipe is busy in 63 %; for 32 rows,
-// 398 us, in 64 %: there the operand warps' work is nearly half the unpacking's
+// 396 us, in 64 %: there the operand warps' work is nearly half the unpacking's
 // and the products' N is four times as wide).  The contraction runs along the
 // rows v of W, across the direction in which its blocks are packed, so the tensor
 // cores' A operand is W transposed: a lane of tensor memory is an input k, a
@@ -434,8 +434,15 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     // this thread's tasks of a stage: eight rows v of one batch row
     constexpr int kOcts = C::kRows / 8, kStepB = kPrepThreads / kOcts, kTasks = (NM + kStepB - 1) / kStepB;
     static_assert(kTasks == 1 || kStepB * kOcts == kPrepThreads, "a thread without a first task has none");
-    const int from_end = kPrepThreads - 1 - pt;                   // few batch rows: by the last warp, beside the MMAs'
-    const int oct = from_end % kOcts, b_first = from_end < kStepB * kOcts ? from_end / kOcts : NM;
+    // The schedulers' shares (a warp's is its index mod 4; 0 and 1 also have the
+    // mins' stores, 3 the MMAs): a stage's headers beyond one a thread go to warps 0
+    // and 2, B's tasks to warps 1, 3, 2, 0 in this order (one row of the full head 219
+    // us, eight of Q4_K 206; headers by 0 and 1, B by 3, 2, 1, 0: 230 and 212).
+    const int b_turn = 32 * (0x1203 >> (4 * (pt >> 5)) & 3) + lane;
+    constexpr int kPasses = 2 * C::kRows > kPrepThreads ? 2 : 1;  // of the headers
+    static_assert(2 * C::kRows <= kPrepThreads + 64, "the second by two warps");
+    const int second = (pt & 32) == 0 ? kPrepThreads + (pt >> 6) * 32 + lane : 2 * C::kRows;
+    const int oct = b_turn % kOcts, b_first = b_turn < kStepB * kOcts ? b_turn / kOcts : NM;
     asm volatile("griddepcontrol.wait;" ::: "memory");            // t and the rows' largest values
     for (int b = warp - kUnpackWarps; b < a.batch; b += 4 * C::kGroups) {
       const float e = pow2(-min(row_exponent(a.gmax, b, gparts), 126));
@@ -472,7 +479,9 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       if (!bad) {
         // a block's header: powers of two with its scales and mins, mantissas for B
 #pragma unroll
-        for (int task = pt; task < 2 * C::kRows; task += kPrepThreads) {
+        for (int pass = 0; pass < kPasses; ++pass) {
+          const int task = pass == 0 ? pt : second;
+          if (task >= 2 * C::kRows) break;
           const int blk = task / C::kRows, row = task % C::kRows;
           const uint4 hdr = *reinterpret_cast<const uint4 *>(st + row * C::kRowBytes + blk * C::kBB);
           const float2 dd = __half22float2(*reinterpret_cast<const __half2 *>(&hdr.x));
