@@ -10,13 +10,12 @@
 // Bound: the unpacking of the quants by the CUDA cores, at 1.6 (up to 8 rows) and
 // 2.8 times (32 rows) the time that HBM needs to read the matrix once: the full
 // Q5_K head takes 219 us for one row, 405 us for 32, the Q4_K head 206 us for 8
-// (for one row the main kernel, 211 us of it, issues in 72 % of all cycles and
-// 84 % on its busiest scheduler, its integer pipe is busy in 63 %; for 32 rows,
-// 396 us, in 64 %: there the operand warps' work is nearly half the unpacking's
-// and the products' N is four times as wide).  The contraction runs along the
-// rows v of W, across the direction in which its blocks are packed, so the tensor
-// cores' A operand is W transposed: a lane of tensor memory is an input k, a
-// column a pair of rows.
+// (for one row the main kernel, 211 us of it, issues in 77 % of all cycles, its
+// integer pipe is busy in 66 %; for 32 rows, 394 us, in 64 %: there the operand
+// warps' work is nearly half the unpacking's and the products have four times the
+// columns).  The contraction runs along the rows v of W, across the direction in
+// which its blocks are packed, so the tensor cores' A operand is W transposed: a
+// lane of tensor memory is an input k, a column a pair of rows.
 //
 // Launches:
 // 1. slope_kernel: t of every row, eight consecutive v of a batch row together,
@@ -156,7 +155,7 @@ struct BwdCfg {
   // A box row is two blocks and the next 16 bytes: rows 368 (304) bytes apart put
   // eight rows' 16-byte pieces, which a transposing load takes at once, on all banks.
   static constexpr int kRowBytes = 2 * kBB + 16;
-  // Rows of a stage: the more, the less the barriers of a stage cost (one row 224
+  // Rows of a stage: the more, the less the barriers of a stage cost (one row 223
   // us with units of 48 of them, 247 us with 64 rows in units of 32); with more than
   // 8 slots the stage's B tiles leave room for 64.
   static constexpr int kRows = NM == 8 ? 96 : 64;
@@ -185,8 +184,8 @@ struct BwdCfg {
   static constexpr int kFixed = kGroups * kT + 512;               // and the barriers
   // Two rings: weights are free again as soon as they are unpacked, their
   // operands only when their products are done.  Of these three, or four with
-  // 32 slots and fewer weights (414 us against 408), or two (one row 249 us
-  // against 224).
+  // 32 slots and fewer weights (414 us against 409), or two (one row 249 us
+  // against 223).
   static constexpr int kSides = 3;
   static constexpr int kFit = (227 * 1024 - kFixed - kSides * kSide) / kWBytes;
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
