@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
   auto list = [&](float xi, int i) {
     if (*reinterpret_cast<volatile int *>(&sh.n) > kList) return;   // lost already: no queue at the counter
     const int at = atomicAdd(&sh.n, 1);
-    if (at < kList) sh.list[at] = argmax_key(xi, static_cast<uint32_t>(i));
+    if (at < kList) sh.list[at] = argmax_key(xi + 0.0f, static_cast<uint32_t>(i));   // 0 and -0 are one value
   };
   // the largest key (its upper 16 bits) that at least k groups' maxima reach
   auto take_bound = [&]() {
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
   int n = sh.n;
   if (k > 0 && !all && (n > kList || n < k)) {
     uint32_t key = float_order_key(bound);
-    auto key_at = [&](uint32_t i) { return float_order_key(to_float(x[i])); };
+    auto key_at = [&](uint32_t i) { return float_order_key(to_float(x[i]) + 0.0f); };
     auto count_from = [&](uint32_t t) {
       int m = 0;
       for (uint32_t i = lo + tid; i < hi; i += kThreads) m += key_at(i) >= t;

@@ -335,3 +335,25 @@ def test_score_rows_by_every_number_of_ctas(torch_cuda, n, v):
         out = head.score(x, tokens, n_top=64)
         torch.cuda.synchronize()
     _check(torch, out, x, tokens, 64, 1.0)
+
+
+@pytest.mark.parametrize("n,v", [(1, 40), (2, 9000), (80, 6000), (400, 3000)])
+@pytest.mark.parametrize("largest", [False, True])
+def test_score_zeros_of_both_signs_are_one_value(torch_cuda, n, v, largest):
+    import q5_lm_head_gb300 as mlh
+    torch = torch_cuda
+    g = torch.Generator(device="cuda")
+    g.manual_seed(v)
+    x = torch.where(torch.rand((n, v), generator=g, device="cuda") < 0.5, 0.0, -0.0)
+    if not largest:
+        x[:, ::7] = 1.0
+        x[:, 3::5] = -1.0
+    tokens = torch.arange(n, dtype=torch.int32, device="cuda") * 13 % v
+    with mlh.LMHead(v, 256, max_batch=1, device=0) as head:
+        out = head.score(x, tokens, n_top=32)
+        torch.cuda.synchronize()
+    order = torch.sort(x + 0.0, dim=1, descending=True, stable=True).indices
+    assert torch.equal(out.top_ids.long(), order[:, :32])
+    place = torch.empty_like(order)
+    place.scatter_(1, order, torch.arange(v, device="cuda").expand(n, v).contiguous())
+    assert torch.equal(out.rank.long(), place.gather(1, tokens.long()[:, None])[:, 0])
