@@ -94,7 +94,10 @@ __device__ __forceinline__ float pow2(int e) {   // -126 <= e <= 127
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-__device__ __forceinline__ float cap_slope(float l, float cap, float inv_cap2) { return (cap - l) * (cap + l) * inv_cap2; }
+// Each factor divided by itself: caps of 1e20 and more, whose square overflows, too.
+__device__ __forceinline__ float cap_slope(float l, float cap, float inv_cap) {
+  return ((cap - l) * inv_cap) * ((cap + l) * inv_cap);
+}
 
 // t[p/8][b][p%8] = gl * scale_m * slope of row v, p = slab_order(v), scale_m the scale's mantissa.
 __global__ void __launch_bounds__(256) slope_kernel(const BackwardArgs a, float scale_m, int64_t share) {
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(256) slope_kernel(const BackwardArgs a, float 
   const bool aligned = (row & 3) == 0;
   const int64_t fours = (a.n_rows + kPadRows - 1) / kPadRows * (kPadRows / 4);
   const int64_t lo = share * blockIdx.x, hi = lo + share < fours ? lo + share : fours;
-  const float inv_cap2 = a.cap > 0.0f ? 1.0f / (a.cap * a.cap) : 0.0f;
+  const float inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
   float m = 0.0f;
 #pragma unroll 4
   for (int64_t i = lo + threadIdx.x; i < hi; i += 256) {
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(256) slope_kernel(const BackwardArgs a, float 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       m = fmaxf(m, fabsf(x[j]));
-      if (a.cap > 0.0f) x[j] *= cap_slope(y[j], a.cap, inv_cap2);
+      if (a.cap > 0.0f) x[j] *= cap_slope(y[j], a.cap, inv_cap);
       x[j] *= scale_m;
     }
     // slab_order: rows 4j, 4j + 1 to places 2j, 2j + 1 of the slab's first eight, the others to its second
@@ -741,7 +744,7 @@ __device__ float plain_sum(const BackwardArgs &a, int b, int j) {
     for (int64_t v = v0; v < v0 + 512 && v < a.n_rows; ++v) {
       const int64_t at = static_cast<int64_t>(b) * a.n_rows + v;
       float t = a.grad_logits[at] * a.scale;
-      if (a.cap > 0.0f) t *= cap_slope(a.logits[at], a.cap, 1.0f / (a.cap * a.cap));
+      if (a.cap > 0.0f) t *= cap_slope(a.logits[at], a.cap, 1.0f / a.cap);
       const uint8_t *blk = a.w + (v * (a.k / kBlockWeights) + kb) * kBB;
       const uint4 hdr = __ldg(reinterpret_cast<const uint4 *>(blk));
       const float2 dd = __half22float2(*reinterpret_cast<const __half2 *>(&hdr.x));

@@ -371,3 +371,38 @@ def test_backward_first_call_beside_another_streams_capture(torch_cuda):
         graph.replay()
         torch.cuda.synchronize()
         assert bool((x == 2.0).all())
+
+
+def test_backward_with_a_cap_whose_square_overflows(torch_cuda):
+    """The slope is 1 to 4 roundings there: against the call without a cap."""
+    import q5_lm_head_gb300 as mlh
+    torch = torch_cuda
+    b, n, k = 3, 700, 512
+    rng = np.random.default_rng(5)
+    wq, g = _weights(n, k, "q5_k", 5), _grads(rng, b, n)
+    w, gl = torch.from_numpy(wq).cuda(), torch.from_numpy(g).cuda()
+    logits = torch.randn((b, n), device="cuda")
+    want, tol, _, _ = _reference(g, None, None, None, _dense(wq, n, k, "q5_k"), 1.0, 0.0)
+    with mlh.LMHead(n, k, max_batch=b, device=0) as head:
+        for cap in (1e20, 1e30, 3e38):
+            got, _ = head.backward(gl, w, logits=logits, scale=1.0, cap=cap)
+            _within(f"cap {cap}", got.cpu().numpy(), want, tol)
+
+
+def test_backward_small_gradients_beside_a_large_one_without_weights(torch_cuda):
+    """The f16 pair of a gradient ends at 2^-24 where the row's largest lies at 2^11 or above: what it
+    drops is at most 2^-35 of the largest, times each weight's parts."""
+    import q5_lm_head_gb300 as mlh
+    torch = torch_cuda
+    n, k = 600, 512
+    rng = np.random.default_rng(6)
+    wq = _weights(n, k, "q5_k", 6).reshape(n, -1).copy()
+    wq[7] = 0
+    g = (rng.standard_normal((1, n)) * 2.0 ** -22).astype(np.float32)
+    g[0, 7] = 3.0
+    dense = _dense(wq, n, k, "q5_k")
+    want, tol, _, _ = _reference(g, None, None, None, dense, 1.0, 0.0)
+    tol = tol + 2.0 ** -34 * 3.0 * dense[1].sum(0)[None]       # once in the pair, once in its product with a block's factor
+    with mlh.LMHead(n, k, max_batch=1, device=0) as head:
+        got, _ = head.backward(torch.from_numpy(g).cuda(), torch.from_numpy(wq.reshape(-1)).cuda(), scale=1.0, cap=0.0)
+        _within("grad_hidden", got.cpu().numpy(), want, tol)
