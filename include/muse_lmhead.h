@@ -310,6 +310,7 @@ int muse_lmhead_forward_group_host(muse_lmhead *h, const float *hidden_host, con
  *     lse      = log sum_i exp(z_i)
  *     logprob  = z[token] - lse
  *     rank     = how many i come before the token in (x descending, index ascending)
+ *                (0 and -0 are equal)
  *     entropy  = -sum_i p_i log p_i,  p = exp(z - lse)   (natural log)
  *     top_ids, top_logprobs = the n_top first i in that order, z_i - lse
  * Sums are held in f32.  The pages take softmax and logprobs over the capped

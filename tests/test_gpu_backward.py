@@ -406,3 +406,40 @@ def test_backward_small_gradients_beside_a_large_one_without_weights(torch_cuda)
     with mlh.LMHead(n, k, max_batch=1, device=0) as head:
         got, _ = head.backward(torch.from_numpy(g).cuda(), torch.from_numpy(wq.reshape(-1)).cuda(), scale=1.0, cap=0.0)
         _within("grad_hidden", got.cpu().numpy(), want, tol)
+
+
+@pytest.mark.parametrize("fmt", ["q5_k", "q4_k"])
+def test_backward_batches_of_every_size_on_one_handle_eager_and_replayed(torch_cuda, fmt):
+    """The workspace is laid out for max_batch: every batch size gives the bits of a handle of its own."""
+    import q5_lm_head_gb300 as mlh
+    torch = torch_cuda
+    n, k = 1100, 768
+    rng = np.random.default_rng(11)
+    w = torch.from_numpy(_weights(n, k, fmt, 11)).cuda()
+    gamma = torch.randn(k, device="cuda")
+    stream = torch.cuda.Stream()
+    with mlh.LMHead(n, k, max_batch=32, device=0, fmt=fmt) as head:
+        calls = []
+        for b in (3, 32, 1, 17, 8, 9, 16, 2):
+            g, lo = torch.from_numpy(_grads(rng, b, n)).cuda(), torch.randn((b, n), device="cuda") * 5
+            h = torch.randn((b, k), device="cuda")
+            with mlh.LMHead(n, k, max_batch=b, device=0, fmt=fmt) as own:
+                want = own.backward(g, w, logits=lo, hidden=h, gamma=gamma, cap=20.0)
+                torch.cuda.synchronize()
+            calls.append((g, lo, h, want))
+            got = head.backward(g, w, logits=lo, hidden=h, gamma=gamma, cap=20.0)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=stream):
+                outs = [head.backward(g, w, logits=lo, hidden=h, gamma=gamma, cap=20.0) for g, lo, h, _ in calls]
+            for _ in range(3):
+                for a, c in outs:
+                    a.fill_(7.0)
+                    c.fill_(7.0)
+                graph.replay()
+        torch.cuda.synchronize()
+        for (a, c), (_, _, _, want) in zip(outs, calls):
+            assert torch.equal(a, want[0]) and torch.equal(c, want[1])
+        assert head.device_status() == 0
