@@ -9,7 +9,7 @@
 //
 // Bound: the unpacking of the quants by the CUDA cores, at 1.6 (up to 8 rows) and
 // 2.8 times (32 rows) the time that HBM needs to read the matrix once: the full
-// Q5_K head takes 219 us for one row, 405 us for 32, the Q4_K head 206 us for 8
+// Q5_K head takes 219 us for one row, 403 us for 32, the Q4_K head 199 us for 8
 // (for one row the main kernel, 211 us of it, issues in 77 % of all cycles, its
 // integer pipe is busy in 66 %; for 32 rows, 394 us, in 64 %: there the operand
 // warps' work is nearly half the unpacking's and the products have four times the
@@ -159,9 +159,10 @@ struct BwdCfg {
   // eight rows' 16-byte pieces, which a transposing load takes at once, on all banks.
   static constexpr int kRowBytes = 2 * kBB + 16;
   // Rows of a stage: the more, the less the barriers of a stage cost (one row 223
-  // us with units of 48 of them, 247 us with 64 rows in units of 32); with more than
-  // 8 slots the stage's B tiles leave room for 64.
-  static constexpr int kRows = NM == 8 ? 96 : 64;
+  // us with units of 48 of them, 247 us with 64 rows in units of 32; 16 rows 286 and
+  // 297 us); with 32 slots the stage's B tiles leave room for 64 (96 rows and two
+  // operand slots: 498 us, against 402).
+  static constexpr int kRows = NM <= 16 ? 96 : 64;
   static constexpr int kWBytes = kRows * kRowBytes;
   static constexpr int kN = 2 * NM;                               // B rows: hi, lo
   // Accumulator columns: with 8 slots hi and lo side by side (an MMA has 16
@@ -183,8 +184,14 @@ struct BwdCfg {
   static constexpr int kGroups = 2;                               // of four operand warps, taking the stages in turn
   static constexpr int kThreads = 32 * (kUnpackWarps + 4 * kGroups + 4);   // the weights' warp, two without a role, the MMAs'
   static constexpr int kT = 2 * 4 * kRows * 2;                    // a group's mantissas, f16, two stages of [4][kRows]
-  static_assert(kGroups * kT >= 16 * NM * 4, "the mins' sums");
-  static constexpr int kFixed = kGroups * kT + 512;               // and the barriers
+  // The mins' f32 sums (eight batch rows a warp): in shared memory, or in registers
+  // until the end.  8 slots of Q4_K 200 us in shared memory, 206 in registers;
+  // 16 slots 279 and 285; 8 slots of Q5_K 223 and 219; with 32 slots their 2 KB
+  // would cost a slot of the weights' ring (404 and 402).
+  static constexpr bool kMinsShared = NM == 16 || (NM == 8 && kQ4);
+  static constexpr int kMins = kMinsShared ? 16 * NM * 4 : 0;
+  static_assert(kMinsShared || kGroups * kT >= 16 * NM * 4, "the mantissas' place at the end");
+  static constexpr int kFixed = kGroups * kT + kMins + 512;       // and the barriers
   // Two rings: weights are free again as soon as they are unpacked, their
   // operands only when their products are done.  Of these three, or four with
   // 32 slots and fewer weights (414 us against 409), or two (one row 249 us
@@ -200,7 +207,7 @@ struct BwdCfg {
   // is in use; with 32 slots one, or the ring would have two units of 16 rows only
   // (491 us for a full head of 32 rows, against 408).
   static constexpr int kSets = NM == 32 ? 1 : 2;
-  static constexpr int kUS = NM == 8 ? 3 : 2;
+  static constexpr int kUS = NM <= 16 ? 3 : 2;
   static constexpr int kUnits = kRows / (16 * kUS);               // units a stage
   static constexpr int kSlab = 48;                                // columns of 16 rows: four M-tiles of 8, mins 8, scales 8
   static constexpr int kABase = kSets * 6 * kD;
@@ -288,7 +295,9 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
   using C = BwdCfg<NM, kQ4>;
   extern __shared__ __align__(1024) uint8_t smem[];                // [kStages][weights], [kSides][B tiles, scales, mins]
   __half *s_md = reinterpret_cast<__half *>(smem + C::kMdAt);      // [kGroups][kT]
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kMdAt + C::kGroups * C::kT);
+  // [16 sub-blocks][NM]; in the mantissas' place once every stage's have been read, if not all along
+  float *s_min = reinterpret_cast<float *>(smem + C::kMdAt + (C::kMinsShared ? C::kGroups * C::kT : 0));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kMdAt + C::kGroups * C::kT + C::kMins);
   uint64_t *wfull = bars, *wempty = wfull + C::kStages, *pfull = wempty + C::kStages, *pempty = pfull + C::kSides;
   uint64_t *tfull = pempty + C::kSides, *tempty = tfull + C::kBufs;
   uint64_t *dfull = tempty + C::kBufs, *dfree = dfull + 2, *done = dfree + 2;
@@ -333,6 +342,8 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     tc::alloc(s_tmem, kTmem);
     tc::relinquish();
   }
+  if constexpr (C::kMinsShared)
+    for (int i = tid; i < 16 * NM; i += C::kThreads) s_min[i] = 0.0f;
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -435,11 +446,10 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     const int pt = tid - 32 * kUnpackWarps - kPrepThreads * grp;
     // this thread's tasks of a stage: eight rows v of one batch row
     constexpr int kOcts = C::kRows / 8, kStepB = kPrepThreads / kOcts, kTasks = (NM + kStepB - 1) / kStepB;
-    static_assert(kTasks == 1 || kStepB * kOcts == kPrepThreads, "a thread without a first task has none");
     // The schedulers' shares (a warp's is its index mod 4; 0 and 1 also have the
     // mins' stores, 3 the MMAs): a stage's headers beyond one a thread go to warps 0
     // and 2, B's tasks to warps 1, 3, 2, 0 in this order (one row of the full head 219
-    // us, eight of Q4_K 206; headers by 0 and 1, B by 3, 2, 1, 0: 230 and 212).
+    // us, eight of Q4_K 206 then; headers by 0 and 1, B by 3, 2, 1, 0: 230 and 212).
     const int b_turn = 32 * (0x1203 >> (4 * (pt >> 5)) & 3) + lane;
     constexpr int kPasses = 2 * C::kRows > kPrepThreads ? 2 : 1;  // of the headers
     static_assert(2 * C::kRows <= kPrepThreads + 64, "the second by two warps");
@@ -570,11 +580,10 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     // mins: warpgroup mt's warp of quarter `mblk` reads block mblk's eight sub-blocks, batch rows 8 mt'..
     const int mblk = wq, mcol = NM == 8 ? 0 : 8 * mt;
     const bool min_warp = NM == 8 ? wq < 2 && mt == 2 * wq : wq < 2 && mt < NM / 8;
-    unsigned long long sum[NM / 2], msum[4];    // pairs of batch rows
+    unsigned long long sum[NM / 2];             // pairs of batch rows
+    float msum[8] = {};                         // eight batch rows, if not in s_min
 #pragma unroll
     for (int j = 0; j < NM / 2; ++j) sum[j] = 0ull;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) msum[j] = 0ull;
     int flushed = 0;
     auto flush = [&]() {
       const int db = flushed % C::kSets;
@@ -604,9 +613,21 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
           uint32_t x[8];
           tc::ld_32x32b_x8(d + lane_base + (4 + mblk) * C::kD + mcol + 8 * h, x);
           tc::wait_ld();
+          if constexpr (!C::kMinsShared) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            msum[j] = add2(msum[j], pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])));
+            for (int j = 0; j < 8; ++j) msum[j] += __uint_as_float(x[j]);
+          } else if (lane < 8) {
+            float4 *at = reinterpret_cast<float4 *>(s_min + (8 * mblk + lane) * NM + mcol);   // this warp's own
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float4 m = at[j];
+              m.x += __uint_as_float(x[4 * j]);
+              m.y += __uint_as_float(x[4 * j + 1]);
+              m.z += __uint_as_float(x[4 * j + 2]);
+              m.w += __uint_as_float(x[4 * j + 3]);
+              at[j] = m;
+            }
+          }
         }
       }
       tc::fence_before();
@@ -699,15 +720,11 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     }
     while (ok && flushed < (n_st + C::kFlush - 1) / C::kFlush) ok = flush();
     if (!ok && lane == 0) fail();
-    float *s_min = reinterpret_cast<float *>(s_md);   // [16 sub-blocks][NM]: every stage's mantissas have been read
-    if (min_warp && ok && lane < 8) {
+    if constexpr (!C::kMinsShared)
+      if (min_warp && ok && lane < 8) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 x = unpack2(msum[j]);
-        s_min[(8 * mblk + lane) * NM + mcol + 2 * j] = x.x;
-        s_min[(8 * mblk + lane) * NM + mcol + 2 * j + 1] = x.y;
+        for (int j = 0; j < 8; ++j) s_min[(8 * mblk + lane) * NM + mcol + j] = msum[j];
       }
-    }
     ptx::named_bar_sync(1 + C::kGroups, 32 * kUnpackWarps);
     const int kc = pair * kTileCols + (mt >> 1) * kBlockWeights + 64 * wq + 32 * (mt & 1) + lane;
     if (ok && kc < a.k) {
