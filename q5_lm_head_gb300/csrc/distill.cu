@@ -350,20 +350,21 @@ __global__ void __launch_bounds__(kDistillThreads) distill_long_kernel(const Dis
   const int64_t row = blockIdx.x;
   const T *x = static_cast<const T *>(a.logits) + row * a.ld;
   T *g = a.grad ? static_cast<T *>(a.grad) + row * a.grad_ld : nullptr;
-  const int v = static_cast<int>(a.v), tid = threadIdx.x;
+  const int tid = threadIdx.x;
+  const uint32_t v = static_cast<uint32_t>(a.v);       // below 2^31: a step past it stays a uint32_t
   const float inv_t = a.inv_temperature;
   const float w = a.row_weight ? a.row_weight[row] : 1.0f;
 
   if (tid < 64) s_seen[tid] = 0u;
   float m = -INFINITY;
-  for (int i = tid; i < v; i += kDistillThreads) m = fmaxf(m, to_float(x[i]));
+  for (uint32_t i = tid; i < v; i += kDistillThreads) m = fmaxf(m, to_float(x[i]));
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((tid & 31) == 0) s_max[tid >> 5] = m;
   __syncthreads();
   for (int i = 0; i < kDistillThreads / 32; ++i) m = fmaxf(m, s_max[i]);
   if (tid < a.n_top) {
     const int id = a.teacher_ids[row * a.n_top + tid];
-    const bool ok = id >= 0 && id < v;
+    const bool ok = id >= 0 && static_cast<uint32_t>(id) < v;
     s_id[tid] = ok ? id : -1;
     s_p[tid] = ok ? a.teacher_logprobs[row * a.n_top + tid] : -INFINITY;
     s_x[tid] = ok ? to_float(x[id]) : 0.0f;
@@ -371,14 +372,14 @@ __global__ void __launch_bounds__(kDistillThreads) distill_long_kernel(const Dis
   }
   __syncthreads();
   if (m == -INFINITY) m = 0.0f;        // all masked (the sum stays 0), or NaN beside masked values (it turns NaN)
-  auto named = [&](int i) {
+  auto named = [&](uint32_t i) {
     if (!((s_seen[(i & 2047) >> 5] >> (i & 31)) & 1u)) return false;
     for (int j = 0; j < a.n_top; ++j)
-      if (s_id[j] == i) return true;
+      if (s_id[j] == static_cast<int>(i)) return true;
     return false;
   };
   float rest = 0.0f, in = 0.0f;
-  for (int i = tid; i < v; i += kDistillThreads) {
+  for (uint32_t i = tid; i < v; i += kDistillThreads) {
     const float e = expf((to_float(x[i]) - m) * inv_t);
     if (named(i)) in += e;
     else rest += e;
@@ -389,11 +390,12 @@ __global__ void __launch_bounds__(kDistillThreads) distill_long_kernel(const Dis
   if (w == 0.0f || total == 0.0f) {                    // no weight, or a row without a distribution
     if (tid == 0 && a.loss) a.loss[row] = 0.0f;
     if (g)
-      for (int i = tid; i < v; i += kDistillThreads) g[i] = from_float<T>(0.0f);
+      for (uint32_t i = tid; i < v; i += kDistillThreads) g[i] = from_float<T>(0.0f);
     return;
   }
 
-  float lmax = -INFINITY, mass = 0.0f, loss = 0.0f;
+  float lmax = -INFINITY, mass = 0.0f;
+  double loss = 0.0;                                   // as in distill_kernel
   for (int j = 0; j < a.n_top; ++j) lmax = fmaxf(lmax, s_p[j]);
   if (lmax > -INFINITY) {
     float sum = 0.0f;
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_long_kernel(const Dis
     for (int j = 0; j < a.n_top; ++j) {
       const float lp = s_p[j] - c, p = expf(lp);
       mass += p;
-      if (p > 0.0f) loss += p * (lp - ((s_x[j] - m) * inv_t - logs));
+      if (p > 0.0f) loss += p * (lp - ((static_cast<double>(s_x[j]) - m) / a.temperature - logs));
     }
     __syncthreads();
     if (tid < a.n_top) s_p[tid] = expf(s_p[tid] - c);
@@ -411,14 +413,14 @@ __global__ void __launch_bounds__(kDistillThreads) distill_long_kernel(const Dis
     if (tid < a.n_top) s_p[tid] = 0.0f;
   }
   const float pt = a.tail ? fmaxf(0.0f, 1.0f - mass) : 0.0f;
-  if (pt > 0.0f) loss += pt * (logf(pt) - (logf(rest) - logs));
-  if (tid == 0 && a.loss) a.loss[row] = w * loss;
+  if (pt > 0.0f) loss += pt * (logf(pt) - (static_cast<double>(logf(rest)) - logs));
+  if (tid == 0 && a.loss) a.loss[row] = static_cast<float>(w * loss);
   if (!g) return;
   __syncthreads();
   const float scale = w * inv_t;
   const float f_in = (mass + pt) / total * scale;
   const float f_out = rest != 0.0f ? ((mass + pt) / total - pt / rest) * scale : 0.0f;
-  for (int i = tid; i < v; i += kDistillThreads) {
+  for (uint32_t i = tid; i < v; i += kDistillThreads) {
     const float e = expf((to_float(x[i]) - m) * inv_t);
     float r = e * f_out;
     if (named(i)) {

@@ -295,3 +295,31 @@ def test_distill_back_to_back_behind_a_forward(torch_cuda):
         torch.cuda.synchronize()
     for i, out in got:
         assert all(torch.equal(p, q) for p, q in zip(out, want[i]))
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("v", [5000, 300000, 2000003])
+def test_distill_masks_of_the_lowest_value_at_low_temperature(torch_cuda, tail, v):
+    """Exponents of lowest values overflow f32 at temperature 0.5; the loss of a row whose teacher
+    expects none of them is the one with -infinity in their place, and the gradient everywhere."""
+    import q5_lm_head_gb300 as mlh
+    torch = torch_cuda
+    x, ids, lp, w = _case(torch, 3, v, 16, torch.float32)
+    mask = torch.rand(x.shape, generator=torch.Generator(device="cuda").manual_seed(v), device="cuda") < 0.5
+    mask.scatter_(1, ids.long().clamp(0, v - 1), False)
+    low = x.masked_fill(mask, torch.finfo(torch.float32).min)
+    inf = x.masked_fill(mask, -math.inf)
+    with mlh.LMHead(v, 256, max_batch=1, device=0) as head:
+        _check(torch, head, inf, ids, lp, w, 0.5, tail)
+        want = head.distill(inf, ids, lp, w, 0.5, tail)
+        got = head.distill(low, ids, lp, w, 0.5, tail)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        # and one that the teacher does expect: a finite loss, as large as its logit
+        low[1, int(ids[1, 0])] = torch.finfo(torch.float32).min
+        lp = torch.full_like(lp, math.log(0.05))
+        loss, grad = head.distill(low, ids, lp, None, 2.0, tail)
+        torch.cuda.synchronize()
+        p = 0.05 if tail else 1 / 16
+        assert abs(float(loss[1]) / (p * torch.finfo(torch.float32).max / 2.0) - 1) < 1e-5
+        assert bool(grad.isfinite().all())
