@@ -212,7 +212,7 @@ struct BwdCfg {
   static constexpr int kSlab = 48;                                // columns of 16 rows: four M-tiles of 8, mins 8, scales 8
   static constexpr int kABase = kSets * 6 * kD;
   static constexpr int kBufs = (512 - kABase) / (kSlab * kUS);
-  static_assert(kBufs >= 2 && kUnits % 2 == 0 && (kSets == 2 || kBufs >= kUnits), "unit ring");
+  static_assert(kBufs >= 2 && kUnits == 2, "unit ring");
   static constexpr int kFlush = (kFlushRows + kRows - 1) / kRows;               // stages between flushes
   static constexpr uint32_t kIdesc = tc::idesc_f16_f32(128, kD), kIdescPair = tc::idesc_f16_f32(128, 2 * kD);
 };
@@ -646,8 +646,11 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
       const __half *scl = k_at + (blk * 8 + 2 * wq) * C::kRows;
       // of sub-block lane/4 of block wq: the mins for one warpgroup, the scales for the other
       const __half *small = k_at + ((blk ? 0 : 16) + 8 * (wq & 1) + (lane >> 2)) * C::kRows;
-      for (int u = par; u < C::kUnits; u += 2) {
-        if (unit >= C::kBufs && !(ok = wait(&tempty[buf], tph ^ 1u))) break;
+      // One unit of a stage's two.  With two buffers the compiler is to know that, and
+      // which buffer it is (one row 219 -> 215 us, eight of Q4_K 199 -> 194); with 32
+      // slots what it then keeps in registers makes others spill (403 -> 416 us).
+      for (int u = par; u < (C::kBufs == 2 ? par + 1 : C::kUnits); u += 2) {
+        if ((C::kBufs == 2 || unit >= C::kBufs) && !(ok = wait(&tempty[buf], tph ^ 1u))) break;   // the first finds it free
         tc::fence_after();
         const uint32_t at0 = tbase + lane_base + C::kABase + buf * C::kUS * C::kSlab, at_small = at0 + 8 * blk;
         const uint32_t src1 = src0 + slot * C::kWBytes + u * C::kUS * 16 * C::kRowBytes;
@@ -704,7 +707,9 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&tfull[buf]);
         unit += 2;
-        if ((buf += 2) >= C::kBufs) {
+        if constexpr (C::kBufs == 2) {
+          tph ^= 1u;
+        } else if ((buf += 2) >= C::kBufs) {
           buf -= C::kBufs;
           tph ^= 1u;
         }
