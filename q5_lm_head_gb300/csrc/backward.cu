@@ -9,9 +9,9 @@
 //
 // Bound: the unpacking of the quants by the CUDA cores, at 1.6 (up to 8 rows) and
 // 2.8 times (32 rows) the time that HBM needs to read the matrix once: the full
-// Q5_K head takes 219 us for one row, 403 us for 32, the Q4_K head 199 us for 8
-// (for one row the main kernel, 211 us of it, issues in 77 % of all cycles, its
-// integer pipe is busy in 66 %; for 32 rows, 394 us, in 64 %: there the operand
+// Q5_K head takes 214 us for one row, 403 us for 32, the Q4_K head 194 us for 8
+// (for one row the main kernel, 206 us of it, issues in 75 % of all cycles, its
+// integer pipe is busy in 67 %; for 32 rows, 380 us, in 65 %: there the operand
 // warps' work is nearly half the unpacking's and the products have four times the
 // columns).  The contraction runs along the rows v of W, across the direction in
 // which its blocks are packed, so the tensor cores' A operand is W transposed: a
