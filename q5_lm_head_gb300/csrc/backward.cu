@@ -184,11 +184,10 @@ struct BwdCfg {
   static constexpr int kGroups = 2;                               // of four operand warps, taking the stages in turn
   static constexpr int kThreads = 32 * (kUnpackWarps + 4 * kGroups + 4);   // the weights' warp, two without a role, the MMAs'
   static constexpr int kT = 2 * 4 * kRows * 2;                    // a group's mantissas, f16, two stages of [4][kRows]
-  // The mins' f32 sums (eight batch rows a warp): in shared memory, or in registers
-  // until the end.  8 slots of Q4_K 200 us in shared memory, 206 in registers;
-  // 16 slots 279 and 285; 8 slots of Q5_K 223 and 219; with 32 slots their 2 KB
-  // would cost a slot of the weights' ring (404 and 402).
-  static constexpr bool kMinsShared = NM == 16 || (NM == 8 && kQ4);
+  // The mins' f32 sums (eight batch rows a warp): in shared memory (16 rows 276 us,
+  // 283 in registers; eight of Q4_K 194 and 196); with 32 slots in registers until
+  // the end, for their 2 KB would cost a slot of the weights' ring (404 and 402).
+  static constexpr bool kMinsShared = NM <= 16;
   static constexpr int kMins = kMinsShared ? 16 * NM * 4 : 0;
   static_assert(kMinsShared || kGroups * kT >= 16 * NM * 4, "the mantissas' place at the end");
   static constexpr int kFixed = kGroups * kT + kMins + 512;       // and the barriers
