@@ -443,3 +443,33 @@ def test_backward_batches_of_every_size_on_one_handle_eager_and_replayed(torch_c
         for (a, c), (_, _, _, want) in zip(outs, calls):
             assert torch.equal(a, want[0]) and torch.equal(c, want[1])
         assert head.device_status() == 0
+
+
+def test_backward_of_two_handles_on_two_streams(torch_cuda):
+    import q5_lm_head_gb300 as mlh
+    torch = torch_cuda
+    rng = np.random.default_rng(13)
+    cases, streams = [(5, 9000, 1024, "q5_k"), (20, 4000, 2560, "q4_k")], [torch.cuda.Stream(), torch.cuda.Stream()]
+    heads, args, want = [], [], []
+    for b, n, k, fmt in cases:
+        heads.append(mlh.LMHead(n, k, max_batch=b, device=0, fmt=fmt))
+        g, lo = torch.from_numpy(_grads(rng, b, n)).cuda(), torch.randn((b, n), device="cuda") * 5
+        args.append((g, torch.from_numpy(_weights(n, k, fmt, 13)).cuda(), lo, torch.randn((b, k), device="cuda"),
+                     torch.randn(k, device="cuda")))
+    try:
+        for head, a in zip(heads, args):
+            want.append(head.backward(*a, cap=20.0))
+        torch.cuda.synchronize()
+        got = [[], []]
+        for _ in range(20):
+            for i in (0, 1):
+                out = torch.empty_like(want[i][0])
+                with torch.cuda.stream(streams[i]):
+                    got[i].append(heads[i].backward(*args[i], cap=20.0, grad_hidden=out))
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            assert all(torch.equal(x, want[i][0]) and torch.equal(y, want[i][1]) for x, y in got[i])
+            assert heads[i].device_status() == 0
+    finally:
+        for head in heads:
+            head.close()
