@@ -9,7 +9,7 @@
 //
 // Bound: the unpacking of the quants by the CUDA cores, at 1.6 (up to 8 rows) and
 // 2.8 times (32 rows) the time that HBM needs to read the matrix once: the full
-// Q5_K head takes 214 us for one row, 403 us for 32, the Q4_K head 194 us for 8
+// Q5_K head takes 214 us for one row, 401 us for 32, the Q4_K head 192 us for 8
 // (for one row the main kernel, 206 us of it, issues in 75 % of all cycles, its
 // integer pipe is busy in 67 %; for 32 rows, 380 us, in 65 %: there the operand
 // warps' work is nearly half the unpacking's and the products have four times the
@@ -65,7 +65,9 @@
 namespace muse {
 namespace {
 
-constexpr int kMaxParts = 1216;                // of the rows' largest |gl|, all rows together: eight CTAs an SM
+// Of the rows' largest |gl|, all rows together, and so slope_kernel's CTAs: five an
+// SM, all at once (32 rows 401 us; eight an SM, in two rounds, 404).
+constexpr int kMaxParts = 760;
 constexpr int kPadRows = 192;                 // t is kept, as zeros, up to a multiple of this
 constexpr int kTileCols = 2 * kBlockWeights;  // inputs of a CTA
 constexpr int kFlushRows = 256;               // between additions of the accumulators to the f32 sums, about
