@@ -200,7 +200,7 @@ struct BwdCfg {
   static constexpr int kSides = 3;
   static constexpr int kFit = (227 * 1024 - kFixed - kSides * kSide) / kWBytes;
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
-  static_assert(kStages >= 3 && kWBytes % 128 == 0, "rings");
+  static_assert(kStages >= kSides && kWBytes % 128 == 0, "rings; the operand warps' waits count on the first");
   static constexpr int kSideAt = kStages * kWBytes, kMdAt = kSideAt + kSides * kSide;
   static constexpr int kSmem = kMdAt + kFixed;
   // Tensor memory: sets of sums of four M-tiles and two min products, then a ring
@@ -485,8 +485,12 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     for (int i = grp; i < n_st; i += C::kGroups, turn ^= 1) {
       const int slot = i % C::kStages, side_slot = i % C::kSides;
       __half *md_at = s_md + grp * (C::kT / 2) + turn * 4 * C::kRows;
-      bad = !wait(&wfull[slot], (i / C::kStages) & 1) ||
-            (i >= C::kSides && !wait(&pempty[side_slot], ((i / C::kSides) & 1) ^ 1));
+      // The operands' slot first: stage i - kSides' products are done, so the box that was
+      // in this weight slot before (stage i - kStages, an earlier one or the same) has landed,
+      // and the parity means this stage's box.  With three weight slots that stage was the
+      // other group's, whose boxes may land later than this one's.
+      bad = (i >= C::kSides && !wait(&pempty[side_slot], ((i / C::kSides) & 1) ^ 1)) ||
+            !wait(&wfull[slot], (i / C::kStages) & 1);
       const uint8_t *st = smem + slot * C::kWBytes;
       uint8_t *side = smem + C::kSideAt + side_slot * C::kSide;
       if (!bad) {
