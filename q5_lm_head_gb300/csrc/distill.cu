@@ -9,7 +9,7 @@
 //     dloss/dx_i = w/T [ (sum p + p_t) q_i - sum_{j: id_j = i} p_j - [i not in S] p_t q_i / q_t ]
 //
 // Bound: HBM, each logit read once and each gradient written once (1,024 bf16 rows
-// of 202,048: 168 us, 4.9 TB/s, 73 % of the measured copy rate; the rest are the
+// of 202,048: 166 us, 5.0 TB/s, 73 % of the measured copy rate; the rest are the
 // row's barriers, which the SM's other CTAs do not quite cover).  A cluster
 // of CTAs holds a row in its shared memory (in the logits' type, up to 52 KB a
 // CTA, so that four CTAs of an SM overlap their loads, sums and stores), and one
@@ -17,6 +17,13 @@
 // outside S is taken apart from the sum inside, not as a difference: where the
 // student is sure of the teacher's ids a difference would be rounding alone.
 // The ids' values are taken out of the row (set to -infinity) before the sum.
+// Each of the two sums goes with a maximum of its own, m_r outside S and m_i inside,
+// for the two may lie hundreds of binary orders apart: against the row's maximum the
+// smaller would be 0 in 32 bits, its logarithm and its shares are ordinary numbers.
+// So, with R = sum_{i not in S} 2^((x_i - m_r) c) >= 1 and Z the row's sum against m,
+//     log q_t = (m_r - m)/T + log R - log Z
+//     dloss/dx_i = 2^((x_i - m_r) c) w/T [ (sum p + p_t) 2^((m_r - m) c) / Z - p_t / R ],  i not in S:
+// one factor for the whole row, which cannot overflow.
 // Nothing is kept in global memory, so calls may overlap.  A row that 16 CTAs
 // cannot hold is read twice by one CTA.
 #include <atomic>
@@ -39,10 +46,10 @@ struct DistillShared {
   __align__(16) int id[kMaxTop];         // -1: left out
   float p[kMaxTop], lp[kMaxTop];         // probability and its logarithm
   float x[kMaxTop];                      // the ids' logits: this CTA's own; all of them in the first CTA
-  float m[kDistillWarps], rest[kDistillWarps], in[kDistillWarps];   // the warps' maxima and sums
+  float rest_m[kDistillWarps], rest[kDistillWarps], in_m[kDistillWarps], in[kDistillWarps];   // the warps' maxima and sums
   float mass;
   int twice[2];                          // an id of this half of the entries has come before
-  float from_m[kDistillCluster], from_rest[kDistillCluster], from_in[kDistillCluster];
+  float from_rest_m[kDistillCluster], from_rest[kDistillCluster], from_in_m[kDistillCluster], from_in[kDistillCluster];
 };
 
 __device__ __forceinline__ void copy_async16(void *dst, const void *src) {
@@ -55,6 +62,11 @@ __device__ __forceinline__ void copy_async16(void *dst, const void *src) {
 __device__ __forceinline__ float move_sum(float s, float from, float to, float c) {
   return to == -INFINITY || s == 0.0f ? s : s * exp2_approx(shift_exponent(from, to, c));
 }
+__device__ __forceinline__ float warp_max(float v) {
+  return order_key_float(__reduce_max_sync(0xffffffffu, float_order_key(v)));
+}
+// -infinity as a reference: 0, against which nothing but 0 or NaN is summed.
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.0f : m; }
 
 template <typename T>
 __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const DistillArgs a) {
@@ -69,6 +81,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
   T *g = a.grad ? static_cast<T *>(a.grad) + row * a.grad_ld : nullptr;
   const int v = static_cast<int>(a.v), k = a.n_top;
   const float c = a.exponent_scale;       // log2(e) / temperature
+  const bool apart = a.tail;              // the sums inside and outside the ids are wanted one by one
   cluster_arrive();                       // waited for before the first store to a peer
 
   // this CTA's share: head values (first CTA), vectors [v0, v1), the rest (last CTA)
@@ -87,7 +100,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
 
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the logits and the teacher's side are complete
   const float w = a.row_weight ? a.row_weight[row] : 1.0f;
-  float scale = w * a.inv_temperature, m = 0.0f, f_in = 0.0f, f_out = 0.0f;
+  float scale = w * a.inv_temperature, f_in = 0.0f, f_out = 0.0f;
   float edge = -INFINITY;
   bool edge_in = false;
   int own = -1;                           // the place of this thread's teacher entry in row_held
@@ -169,7 +182,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
 #pragma unroll
       for (int j = 0; j < W; ++j) top = fmaxf(top, o[j]);
     }
-    const float ref = top == -INFINITY ? 0.0f : top;
+    const float ref = reference(top);
     unsigned long long s2 = 0ull;
     const unsigned long long c2 = pack2(c, c);
     if (fabsf(ref) < kPlain) {
@@ -193,40 +206,48 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
       }
     }
     float rest = unpack2(s2).x + unpack2(s2).y, in = 0.0f;
-    // the warp's maximum, edges and ids with it, and its sums against that
-    float cm = order_key_float(__reduce_max_sync(0xffffffffu, float_order_key(fmaxf(fmaxf(top, edge), in_m))));
-    const float cref = cm == -INFINITY ? 0.0f : cm;
-    rest = move_sum(rest, top, cm, c);
-    if (edge_i >= 0) (edge_in ? in : rest) += exp2_approx(exponent(edge, cref, c));
-    if (own >= 0 && !again) in += exp2_approx(exponent(mine, cref, c));
+    // the warp's maxima, edges and ids with them, and its sums against these; without
+    // the class for the rest only the whole row's sum is wanted, and `rest` is that
+    const bool edge_apart = apart && edge_in;
+    float rest_m = warp_max(fmaxf(fmaxf(top, edge_apart ? -INFINITY : edge), apart ? -INFINITY : in_m));
+    float ids_m = apart ? warp_max(fmaxf(in_m, edge_apart ? edge : -INFINITY)) : -INFINITY;
+    rest = move_sum(rest, top, rest_m, c);
+    if (edge_i >= 0) (edge_apart ? in : rest) += exp2_approx(exponent(edge, reference(edge_apart ? ids_m : rest_m), c));
+    if (own >= 0 && !again) (apart ? in : rest) += exp2_approx(exponent(mine, reference(apart ? ids_m : rest_m), c));
     for (int o = 16; o > 0; o >>= 1) {
       rest += __shfl_xor_sync(0xffffffffu, rest, o);
-      in += __shfl_xor_sync(0xffffffffu, in, o);
+      if (apart) in += __shfl_xor_sync(0xffffffffu, in, o);
     }
     if (lane == 0) {
-      sh.m[warp] = cm;
+      sh.rest_m[warp] = rest_m;
       sh.rest[warp] = rest;
+      sh.in_m[warp] = ids_m;
       sh.in[warp] = in;
     }
     __syncthreads();
-    // the CTA's, in every thread
-    const bool a_warp = lane < kDistillWarps;
-    cm = a_warp ? sh.m[lane] : -INFINITY;
-    {
-      const float all = order_key_float(__reduce_max_sync(0xffffffffu, float_order_key(cm)));
-      rest = a_warp ? move_sum(sh.rest[lane], cm, all, c) : 0.0f;
-      in = a_warp ? move_sum(sh.in[lane], cm, all, c) : 0.0f;
-      cm = all;
-    }
-    for (int o = 16; o > 0; o >>= 1) {   // lanes without a warp add 0
-      rest += __shfl_xor_sync(0xffffffffu, rest, o);
-      in += __shfl_xor_sync(0xffffffffu, in, o);
-    }
+    // the lanes' sums onto the maxima of all lanes, and their sums, in every lane
+    auto join = [&](bool have, const float *m_rest, const float *s_rest, const float *m_in, const float *s_in) {
+      const float of = have ? m_rest[lane] : -INFINITY, of_in = have && apart ? m_in[lane] : -INFINITY;
+      rest = have ? s_rest[lane] : 0.0f;        // lanes without one add 0
+      in = have && apart ? s_in[lane] : 0.0f;
+      rest_m = warp_max(of);
+      if (apart) ids_m = warp_max(of_in);
+      rest = move_sum(rest, of, rest_m, c);
+      in = move_sum(in, of_in, ids_m, c);
+      for (int o = 16; o > 0; o >>= 1) {
+        rest += __shfl_xor_sync(0xffffffffu, rest, o);
+        if (apart) in += __shfl_xor_sync(0xffffffffu, in, o);
+      }
+    };
+    join(lane < kDistillWarps, sh.rest_m, sh.rest, sh.in_m, sh.in);   // the CTA's, in every thread
     cluster_wait();                       // every CTA of the cluster has started
     if (tid < static_cast<int>(cs)) {     // to every CTA, so that all go on with the same bits
-      peer_store32(peer_addr(&sh.from_m[cr], tid), __float_as_uint(cm));
+      peer_store32(peer_addr(&sh.from_rest_m[cr], tid), __float_as_uint(rest_m));
       peer_store32(peer_addr(&sh.from_rest[cr], tid), __float_as_uint(rest));
-      peer_store32(peer_addr(&sh.from_in[cr], tid), __float_as_uint(in));
+      if (apart) {
+        peer_store32(peer_addr(&sh.from_in_m[cr], tid), __float_as_uint(ids_m));
+        peer_store32(peer_addr(&sh.from_in[cr], tid), __float_as_uint(in));
+      }
     }
     if (own >= 0) peer_store32(peer_addr(&sh.x[tid], 0), __float_as_uint(mine));
     if (edge_in)
@@ -234,27 +255,23 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
         if (sh.id[j] == edge_i) peer_store32(peer_addr(&sh.x[j], 0), __float_as_uint(edge));
     cluster_sync();
 
-    const bool have = lane < static_cast<int>(cs);
-    cm = have ? sh.from_m[lane] : -INFINITY;
-    m = order_key_float(__reduce_max_sync(0xffffffffu, float_order_key(cm)));
-    rest = have ? move_sum(sh.from_rest[lane], cm, m, c) : 0.0f;
-    in = have ? move_sum(sh.from_in[lane], cm, m, c) : 0.0f;
-    for (int o = 16; o > 0; o >>= 1) {
-      rest += __shfl_xor_sync(0xffffffffu, rest, o);
-      in += __shfl_xor_sync(0xffffffffu, in, o);
-    }
-    if (m == -INFINITY) m = 0.0f;         // all masked (the sums stay 0), or NaN beside masked values
-    const float total = rest + in, mass = sh.mass;
+    join(lane < static_cast<int>(cs), sh.from_rest_m, sh.from_rest, sh.from_in_m, sh.from_in);
+    const float most = fmaxf(rest_m, ids_m), mass = sh.mass;
+    const float total = apart ? move_sum(rest, rest_m, most, c) + move_sum(in, ids_m, most, c) : rest;
+    // all masked (the sums stay 0), or NaN beside masked values: against 0
+    const float m = reference(most), mr = reference(rest_m);
     const float pt = a.tail ? fmaxf(0.0f, 1.0f - mass) : 0.0f;
     if (cr == 0 && warp == 0 && a.loss) {
       // a few values a row, in 64 bits: a lowest value would overflow in log2's units
-      const double lse = row_lse(m, c, log2f(total), a.temperature);
+      const double lse = m * a.inv_temperature64 + row_log_sum(m, c, log2f(total));
       double loss = 0.0;
       for (int j = lane; j < k; j += 32)
         if (sh.p[j] > 0.0f)
-          loss += sh.p[j] * (sh.lp[j] - (sh.x[j] / static_cast<double>(a.temperature) - lse));
+          loss += sh.p[j] * (sh.lp[j] - (sh.x[j] * a.inv_temperature64 - lse));
       for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
-      if (pt > 0.0f) loss += pt * (logf(pt) - kLn2 * (static_cast<double>(log2f(rest)) - log2f(total)));
+      if (pt > 0.0f)
+        loss += pt * (logf(pt) - ((static_cast<double>(mr) - m) * a.inv_temperature64 +
+                                  row_log_sum(mr, c, log2f(rest)) - row_log_sum(m, c, log2f(total))));
       if (lane == 0) a.loss[row] = total == 0.0f ? 0.0f : static_cast<float>(w * loss);
     }
     if (total == 0.0f) {
@@ -262,7 +279,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
     } else {
       const float q = (mass + pt) / total;
       f_in = q * scale;
-      f_out = rest == 0.0f ? 0.0f : (a.tail ? q - pt / rest : q) * scale;
+      f_out = !apart ? f_in : rest == 0.0f ? 0.0f : (q * exp2_approx(shift_exponent(mr, m, c)) - pt / rest) * scale;
     }
     if (!g) return;
     if (own >= 0) {
@@ -277,7 +294,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
       }
     }
     if (edge_i >= 0) {
-      const float e = exp2_approx(exponent(edge, m, c));
+      const float e = exp2_approx(exponent(edge, edge_in ? m : mr, c));
       if (edge_in) {
         float r = 0.0f;
         for (int j = 0; j < k; ++j)
@@ -291,10 +308,10 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
     top = in_m;
     // the gradient outside S; the ids' places are 0 here (-infinity in the row)
     if (scale != 0.0f) {
-      const bool plain = fabsf(m) < kPlain;
+      const bool plain = fabsf(mr) < kPlain;
       if (plain && (reinterpret_cast<uintptr_t>(g + first) & 15) == 0) {
         uint4 *gv = reinterpret_cast<uint4 *>(g + first);
-        const float rc = -__fmul_rn(m, c);
+        const float rc = -__fmul_rn(mr, c);
         const unsigned long long rc2 = pack2(rc, rc), f2 = pack2(f_out, f_out);
         for (int i = tid; i < v1 - v0; i += kDistillThreads) {
           float o[W];
@@ -311,7 +328,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
         }
       } else {                            // rows of another alignment than the logits', or of lowest values
         for (int i = tid; i < count; i += kDistillThreads)
-          g[first + i] = from_float<T>(exp2_approx(exponent(to_float(row_held[i]), m, c)) * f_out);
+          g[first + i] = from_float<T>(exp2_approx(exponent(to_float(row_held[i]), mr, c)) * f_out);
       }
       __syncthreads();                    // the zeros at the ids' places are written
       if (own >= 0) g[first + own] = from_float<T>(top);
@@ -356,37 +373,41 @@ __global__ void __launch_bounds__(kDistillThreads) distill_long_kernel(const Dis
   const float w = a.row_weight ? a.row_weight[row] : 1.0f;
 
   if (tid < 64) s_seen[tid] = 0u;
-  float m = -INFINITY;
-  for (uint32_t i = tid; i < v; i += kDistillThreads) m = fmaxf(m, to_float(x[i]));
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((tid & 31) == 0) s_max[tid >> 5] = m;
   __syncthreads();
-  for (int i = 0; i < kDistillThreads / 32; ++i) m = fmaxf(m, s_max[i]);
   if (tid < a.n_top) {
     const int id = a.teacher_ids[row * a.n_top + tid];
     const bool ok = id >= 0 && static_cast<uint32_t>(id) < v;
     s_id[tid] = ok ? id : -1;
     s_p[tid] = ok ? a.teacher_logprobs[row * a.n_top + tid] : -INFINITY;
-    s_x[tid] = ok ? to_float(x[id]) : 0.0f;
+    s_x[tid] = ok ? to_float(x[id]) : -INFINITY;
     if (ok) atomicOr(&s_seen[(id & 2047) >> 5], 1u << (id & 31));
   }
   __syncthreads();
-  if (m == -INFINITY) m = 0.0f;        // all masked (the sum stays 0), or NaN beside masked values (it turns NaN)
   auto named = [&](uint32_t i) {
     if (!((s_seen[(i & 2047) >> 5] >> (i & 31)) & 1u)) return false;
     for (int j = 0; j < a.n_top; ++j)
       if (s_id[j] == static_cast<int>(i)) return true;
     return false;
   };
+  // maxima and sums outside the ids and of the ids, as in distill_kernel
+  float rest_m = -INFINITY, ids_m = -INFINITY;
+  for (uint32_t i = tid; i < v; i += kDistillThreads)
+    if (!named(i)) rest_m = fmaxf(rest_m, to_float(x[i]));
+  rest_m = warp_max(rest_m);
+  if ((tid & 31) == 0) s_max[tid >> 5] = rest_m;
+  __syncthreads();
+  for (int i = 0; i < kDistillThreads / 32; ++i) rest_m = fmaxf(rest_m, s_max[i]);
+  for (int j = 0; j < a.n_top; ++j) ids_m = fmaxf(ids_m, s_x[j]);
+  const float mr = reference(rest_m), mi = reference(ids_m), m = reference(fmaxf(rest_m, ids_m));
   float rest = 0.0f, in = 0.0f;
   for (uint32_t i = tid; i < v; i += kDistillThreads) {
-    const float e = expf((to_float(x[i]) - m) * inv_t);
-    if (named(i)) in += e;
-    else rest += e;
+    if (named(i)) in += expf((to_float(x[i]) - mi) * inv_t);
+    else rest += expf((to_float(x[i]) - mr) * inv_t);
   }
   rest = block_sum(rest, s_red);
   in = block_sum(in, s_red);
-  const float total = rest + in, logs = logf(total);
+  auto moved = [&](float s, float from) { return s == 0.0f ? s : s * expf((from - m) * inv_t); };   // a NaN stays one
+  const float total = moved(rest, rest_m) + moved(in, ids_m), logs = logf(total);
   if (w == 0.0f || total == 0.0f) {                    // no weight, or a row without a distribution
     if (tid == 0 && a.loss) a.loss[row] = 0.0f;
     if (g)
@@ -404,7 +425,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_long_kernel(const Dis
     for (int j = 0; j < a.n_top; ++j) {
       const float lp = s_p[j] - c, p = expf(lp);
       mass += p;
-      if (p > 0.0f) loss += p * (lp - ((static_cast<double>(s_x[j]) - m) / a.temperature - logs));
+      if (p > 0.0f) loss += p * (lp - ((static_cast<double>(s_x[j]) - m) * a.inv_temperature64 - logs));
     }
     __syncthreads();
     if (tid < a.n_top) s_p[tid] = expf(s_p[tid] - c);
@@ -413,18 +434,19 @@ __global__ void __launch_bounds__(kDistillThreads) distill_long_kernel(const Dis
     if (tid < a.n_top) s_p[tid] = 0.0f;
   }
   const float pt = a.tail ? fmaxf(0.0f, 1.0f - mass) : 0.0f;
-  if (pt > 0.0f) loss += pt * (logf(pt) - (static_cast<double>(logf(rest)) - logs));
+  if (pt > 0.0f) loss += pt * (logf(pt) - ((static_cast<double>(mr) - m) * a.inv_temperature64 + logf(rest) - logs));
   if (tid == 0 && a.loss) a.loss[row] = static_cast<float>(w * loss);
   if (!g) return;
   __syncthreads();
   const float scale = w * inv_t;
   const float f_in = (mass + pt) / total * scale;
-  const float f_out = rest != 0.0f ? ((mass + pt) / total - pt / rest) * scale : 0.0f;
+  const float f_out = rest != 0.0f ? ((mass + pt) / total * expf((mr - m) * inv_t) - pt / rest) * scale : 0.0f;
   for (uint32_t i = tid; i < v; i += kDistillThreads) {
-    const float e = expf((to_float(x[i]) - m) * inv_t);
-    float r = e * f_out;
-    if (named(i)) {
-      r = e * f_in;
+    float r;
+    if (!named(i)) {
+      r = expf((to_float(x[i]) - mr) * inv_t) * f_out;
+    } else {
+      r = expf((to_float(x[i]) - m) * inv_t) * f_in;
       for (int j = 0; j < a.n_top; ++j)
         if (s_id[j] == i) r -= s_p[j] * scale;
     }

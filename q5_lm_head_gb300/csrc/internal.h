@@ -127,7 +127,8 @@ struct DistillArgs {
   int n_top;
   bool tail;
   const float *row_weight;         // [n] or nullptr
-  float temperature, inv_temperature, exponent_scale;   // 1 / temperature, log2(e) / temperature
+  float inv_temperature, exponent_scale;   // 1 / temperature, log2(e) / temperature
+  double inv_temperature64;                // 1 / temperature, for the losses: a division in 64 bits costs a row's last warp dearly
   float *loss;                     // [n] or nullptr
   void *grad;                      // [n][grad_ld] or nullptr, the logits' dtype
   int64_t grad_ld;

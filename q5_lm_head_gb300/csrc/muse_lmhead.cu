@@ -558,8 +558,8 @@ int muse_lmhead_distill(muse_lmhead *h, const void *logits, int dtype, int64_t n
   a.n_top = n_top;
   a.tail = tail != 0;
   a.row_weight = row_weight;
-  a.temperature = temperature;
   a.inv_temperature = 1.0f / temperature;
+  a.inv_temperature64 = 1.0 / temperature;
   a.exponent_scale = static_cast<float>(1.4426950408889634 / temperature);
   a.loss = loss;
   a.grad = grad;

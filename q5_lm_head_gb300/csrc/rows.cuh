@@ -160,13 +160,16 @@ __device__ __forceinline__ float shift_exponent(float from, float to, float c) {
   return fabsf(from) < kPlain && fabsf(to) < kPlain ? __fadd_rn(__fmul_rn(from, c), -__fmul_rn(to, c)) : (from - to) * c;
 }
 
-// log sum exp(x / temperature) from log2 of the sum of exponents against m, in
+// log sum exp((x - m) / temperature) from log2 of the sum of exponents against m, in
 // 64 bits.  The sum's reference was the rounded product m c: the logarithm
 // against m itself takes the rounding off again.
 constexpr double kLn2 = 0.6931471805599453;
-__device__ __forceinline__ double row_lse(float m, float c, float log2_sum, float temperature) {
+__device__ __forceinline__ double row_log_sum(float m, float c, float log2_sum) {
   const float off = fabsf(m) < kPlain ? fmaf(m, c, -__fmul_rn(m, c)) : 0.0f;
-  return m / static_cast<double>(temperature) + kLn2 * (static_cast<double>(log2_sum) - off);
+  return kLn2 * (static_cast<double>(log2_sum) - off);
+}
+__device__ __forceinline__ double row_lse(float m, float c, float log2_sum, float temperature) {
+  return m / static_cast<double>(temperature) + row_log_sum(m, c, log2_sum);
 }
 
 // ---------------------------------------------------------------- clusters
