@@ -263,15 +263,16 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
     const float pt = a.tail ? fmaxf(0.0f, 1.0f - mass) : 0.0f;
     if (cr == 0 && warp == 0 && a.loss) {
       // a few values a row, in 64 bits: a lowest value would overflow in log2's units
-      const double lse = m * a.inv_temperature64 + row_log_sum(m, c, log2f(total));
+      // Differences of logits first: of 3.4e38 in size they would swallow the sum's logarithm.
+      const double log_sum = row_log_sum(m, c, log2f(total));
       double loss = 0.0;
       for (int j = lane; j < k; j += 32)
         if (sh.p[j] > 0.0f)
-          loss += sh.p[j] * (sh.lp[j] - (sh.x[j] * a.inv_temperature64 - lse));
+          loss += sh.p[j] * (sh.lp[j] - ((static_cast<double>(sh.x[j]) - m) * a.inv_temperature64 - log_sum));
       for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
       if (pt > 0.0f)
         loss += pt * (logf(pt) - ((static_cast<double>(mr) - m) * a.inv_temperature64 +
-                                  row_log_sum(mr, c, log2f(rest)) - row_log_sum(m, c, log2f(total))));
+                                  row_log_sum(mr, c, log2f(rest)) - log_sum));
       if (lane == 0) a.loss[row] = total == 0.0f ? 0.0f : static_cast<float>(w * loss);
     }
     if (total == 0.0f) {
