@@ -168,9 +168,6 @@ __device__ __forceinline__ double row_log_sum(float m, float c, float log2_sum) 
   const float off = fabsf(m) < kPlain ? fmaf(m, c, -__fmul_rn(m, c)) : 0.0f;
   return kLn2 * (static_cast<double>(log2_sum) - off);
 }
-__device__ __forceinline__ double row_lse(float m, float c, float log2_sum, float temperature) {
-  return m / static_cast<double>(temperature) + row_log_sum(m, c, log2_sum);
-}
 
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_rank() {

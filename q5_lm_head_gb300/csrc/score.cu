@@ -503,11 +503,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
   const float total = sh.s[0], m = sh.m[0] == -INFINITY ? 0.0f : sh.m[0];
   const bool empty = total == 0.0f;       // nothing above -infinity
   const float logs = log2f(total);
-  // from here a few values a row, in 64 bits: in log2's units a lowest value would overflow
-  const double lse = row_lse(m, c, logs, a.temperature);
-  auto logprob = [&](float xi) { return empty ? -INFINITY : static_cast<float>(xi / static_cast<double>(a.temperature) - lse); };
+  // From here a few values a row, in 64 bits: in log2's units a lowest value would overflow.
+  // Differences of logits first: of 3.4e38 in size they would swallow the sum's logarithm.
+  const double temperature = a.temperature, log_sum = row_log_sum(m, c, logs);
+  auto logprob = [&](float xi) {
+    return empty ? -INFINITY : static_cast<float>((static_cast<double>(xi) - m) / temperature - log_sum);
+  };
   if (tid == 0) {
-    if (a.lse) a.lse[row] = empty ? -INFINITY : static_cast<float>(lse);
+    if (a.lse) a.lse[row] = empty ? -INFINITY : static_cast<float>(m / temperature + log_sum);
     if (a.entropy) a.entropy[row] = empty ? 0.0f : static_cast<float>(kLn2) * (logs - sh.u[0] / total);
     if (a.logprob) a.logprob[row] = has ? logprob(xt) : 0.0f;
     if (a.rank) a.rank[row] = has ? before : -1;

@@ -54,3 +54,22 @@ def test_distill_rows_of_the_lowest_value(torch_cuda, dtype, masked, tail, tempe
         want += 0.2 * (math.log(0.2) - math.log((left - 3) / left))
     assert abs(float(loss[0]) - want) <= 45 * U * (1 + math.log(v)) + 200 * U
     assert bool(grad.isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("temperature", [1.0, 0.5, 3.0])
+@pytest.mark.parametrize("v", [70, 50257, 202048])
+def test_score_rows_of_the_lowest_value(torch_cuda, dtype, masked, temperature, v):
+    import q5_lm_head_gb300 as mlh
+    torch = torch_cuda
+    x, left = _row(torch, v, dtype, masked, 40)
+    at = (x[0] > -math.inf).nonzero()[:, 0].to(torch.int32)
+    with mlh.LMHead(v, 256, max_batch=1, device=0) as head:
+        out = head.score(x, at[7:8], 8, temperature)
+        torch.cuda.synchronize()
+    tol = 4 * U * math.log(left) + 2 * U
+    assert abs(float(out.logprob[0]) + math.log(left)) <= tol
+    assert abs(float(out.entropy[0]) - math.log(left)) <= tol
+    assert float((out.top_logprobs + math.log(left)).abs().max()) <= tol
+    assert torch.equal(out.top_ids[0], at[:8]) and int(out.rank[0]) == 7
