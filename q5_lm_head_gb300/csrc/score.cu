@@ -57,9 +57,9 @@ __device__ __forceinline__ Stat stat_move(Stat t, float m, float c) {
   return {m, t.s, t.u};
 }
 
-// Sum over the warp's lanes, in a fixed order.
-__device__ __forceinline__ Stat stat_warp(Stat t, float c) {
-  const uint32_t top = __reduce_max_sync(0xffffffffu, float_order_key(t.m));
+// Sum over the warp's lanes, in a fixed order, against the largest of their values `most`.
+__device__ __forceinline__ Stat stat_warp(Stat t, float most, float c) {
+  const uint32_t top = __reduce_max_sync(0xffffffffu, float_order_key(most));
   t = stat_move(t, order_key_float(top), c);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -222,12 +222,15 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
   const float xt_up = nextafterf(xt, INFINITY);
 
   // The sums' reference is the first maximum seen, and a later one only where it
-  // lies 2^60 above: moving the sums onto every new maximum was most of a step's
-  // instructions (some thread of a warp has one in three steps of four).
+  // lies 2^16 above: moving the sums onto every new maximum was most of a step's
+  // instructions (some thread of a warp has one in three steps of four; with 2^8
+  // 1,024 rows of 202,048 f32 take 162.6 us, 157.9 with this).  Each power of two
+  // of that room costs the entropy of a nearly certain row 1e-7: log2 S and U / S
+  // are that large, their difference small.
   Stat st = {-INFINITY, 0.0f, 0.0f};
   float ref = 0.0f, reach = -INFINITY;    // st.m, or 0 while that is -infinity; the largest value it serves
   float most = -INFINITY;                 // the thread's maximum
-  const float room = 60.0f / c;
+  const float room = 16.0f / c;
   unsigned long long s2 = 0ull, u2 = 0ull;   // two lanes of S and U
   int before = 0, flip = 0;
   // Groups of threads whose maxima give the bound: two or four threads, at
@@ -407,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
     st.s = s.x + s.y;
     st.u = u.x + u.y;
   }
-  st = stat_warp(st, c);
+  st = stat_warp(st, most, c);
   before = __reduce_add_sync(0xffffffffu, before);
   if (lane == 0) {
     sh.m[warp] = st.m;
@@ -418,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
   __syncthreads();
   if (warp == 0) {
     st = lane < kWarps ? Stat{sh.m[lane], sh.s[lane], sh.u[lane]} : Stat{-INFINITY, 0.0f, 0.0f};
-    st = stat_warp(st, c);
+    st = stat_warp(st, st.m, c);
     before = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.before[lane] : 0);
   }
 
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
     if (warp == 0) {
       const bool in = lane < static_cast<int>(cs);
       st = in ? Stat{sh.from_m[lane], sh.from_s[lane], sh.from_u[lane]} : Stat{-INFINITY, 0.0f, 0.0f};
-      st = stat_warp(st, c);
+      st = stat_warp(st, st.m, c);
       before = __reduce_add_sync(0xffffffffu, in ? sh.from_before[lane] : 0);
     }
     if (k > 0) {                          // close the lists up
@@ -511,7 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
   };
   if (tid == 0) {
     if (a.lse) a.lse[row] = empty ? -INFINITY : static_cast<float>(m / temperature + log_sum);
-    if (a.entropy) a.entropy[row] = empty ? 0.0f : static_cast<float>(kLn2) * (logs - sh.u[0] / total);
+    const float entropy = static_cast<float>(kLn2) * (logs - sh.u[0] / total);
+    if (a.entropy) a.entropy[row] = empty || entropy < 0.0f ? 0.0f : entropy;   // a NaN stays one
     if (a.logprob) a.logprob[row] = has ? logprob(xt) : 0.0f;
     if (a.rank) a.rank[row] = has ? before : -1;
   }
