@@ -393,7 +393,10 @@ int muse_lmhead_distill(muse_lmhead *h, const void *logits, int dtype, int64_t n
  *         grad_hidden = r (u - h r^2 mean(u h)),  grad_gamma[j] = sum_b gx[b][j] h[b][j] r_b
  *     gamma NULL:  grad_hidden = gx
  *   grad_logits [batch][n_rows] f32; logits [batch][n_rows] f32, what the
- *   forward returned, needed when cap > 0 (else unused, may be NULL).
+ *   forward returned, needed when cap > 0 (else unused, may be NULL).  Logits
+ *   may be masked: t = 0 where one is outside -cap..cap (-infinity, or a type's
+ *   lowest value), whatever grad_logits holds there.  Without a cap a masked
+ *   logit's gradient has to be 0, as muse_lmhead_distill writes it.
  *   hidden [batch][k] and gamma as in the forward; hidden is needed with gamma.
  *   grad_hidden [batch][k] f32, written; grad_gamma [k] f32, written, or NULL
  *   (needs gamma).  All 16-byte aligned, device, dense, batch 1..max_batch.

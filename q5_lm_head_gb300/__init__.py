@@ -609,7 +609,8 @@ class LMHead:
         """(grad_hidden [B, k], grad_gamma [k] or None) from grad_logits [B, n_rows] f32.
 
         weights, gamma, eps, scale and cap as in the forward; logits (what it
-        returned) is needed with a cap, hidden with gamma.  The first call
+        returned, masked or not: nothing goes back through one outside
+        -cap..cap) is needed with a cap, hidden with gamma.  The first call
         allocates the handle's workspace: make it before a graph's capture.
         See muse_lmhead_backward in the C header."""
         import torch

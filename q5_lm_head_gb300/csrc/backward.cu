@@ -4,6 +4,8 @@
 // Per batch row b, with gl = dloss/dlogits and the forward's logits l:
 //     t_v  = gl_v * scale * (cap > 0 ? (cap - l_v)(cap + l_v) / cap^2 : 1)
 //     gx_k = sum_v t_v W_vk,     W_vk = d sc q - dmin m
+// (t_v = 0 where l_v is outside -cap..cap: a masked logit, -infinity or a lowest
+// value, did not come through the cap)
 // and with the norm, r = 1/sqrt(mean h^2 + eps), xh = h r, gg = gx gamma:
 //     gh = r (gg - xh mean(gg xh)),   ggamma = sum_b gx xh
 //
@@ -96,6 +98,8 @@ __device__ __forceinline__ float pow2(int e) {   // -126 <= e <= 127
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// A masked logit, through which nothing goes back, whatever its gradient holds (a NaN is none).
+__device__ __forceinline__ bool beyond_cap(float l, float cap) { return fabsf(l) > cap; }
 // Each factor divided by itself: caps of 1e20 and more, whose square overflows, too.
 __device__ __forceinline__ float cap_slope(float l, float cap, float inv_cap) {
   return ((cap - l) * inv_cap) * ((cap + l) * inv_cap);
@@ -134,6 +138,7 @@ __global__ void __launch_bounds__(256) slope_kernel(const BackwardArgs a, float 
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      if (a.cap > 0.0f && beyond_cap(y[j], a.cap)) x[j] = y[j] = 0.0f;
       m = fmaxf(m, fabsf(x[j]));
       if (a.cap > 0.0f) x[j] *= cap_slope(y[j], a.cap, inv_cap);
       x[j] *= scale_m;
@@ -771,7 +776,7 @@ __device__ float plain_sum(const BackwardArgs &a, int b, int j) {
     for (int64_t v = v0; v < v0 + 512 && v < a.n_rows; ++v) {
       const int64_t at = static_cast<int64_t>(b) * a.n_rows + v;
       float t = a.grad_logits[at] * a.scale;
-      if (a.cap > 0.0f) t *= cap_slope(a.logits[at], a.cap, 1.0f / a.cap);
+      if (a.cap > 0.0f) t = beyond_cap(a.logits[at], a.cap) ? 0.0f : t * cap_slope(a.logits[at], a.cap, 1.0f / a.cap);
       const uint8_t *blk = a.w + (v * (a.k / kBlockWeights) + kb) * kBB;
       const uint4 hdr = __ldg(reinterpret_cast<const uint4 *>(blk));
       const float2 dd = __half22float2(*reinterpret_cast<const __half2 *>(&hdr.x));
