@@ -404,7 +404,7 @@ int muse_lmhead_distill(muse_lmhead *h, const void *logits, int dtype, int64_t n
  * Products are formed on the tensor cores from f16 pairs (a gradient times a
  * block's factor to 2^-21) and summed in f32: an element is off by about
  * 2^-21 of the sum of the sizes of its products, and what a pair holds ends
- * 2^-35 below the row's largest |grad_logits|.  The sums run in a fixed
+ * 2^-35 below the row's largest |t|.  The sums run in a fixed
  * order: the same inputs give the same bits.  A NaN or infinity in a row of
  * grad_logits stays in that row (and reaches grad_gamma).
  * The first call allocates the handle's workspace for it (max_batch rows of

@@ -21,7 +21,9 @@
 //
 // Launches:
 // 1. slope_kernel: t of every row, eight consecutive v of a batch row together,
-//    and the largest |gl| of parts of each row, for a power of two that brings a
+//    and the largest of them (without the scale) of parts of each row, behind the
+//    cap's slope: a label's gradient that a saturated logit lets nothing of through
+//    would cost the others their low bits.  From it comes a power of two that brings a
 //    row's t into f16's range.
 // 2. backward_tc_kernel: a CTA takes two block columns (512 inputs) and a share
 //    of the rows, 96 or 64 rows a stage.
@@ -67,7 +69,7 @@
 namespace muse {
 namespace {
 
-// Of the rows' largest |gl|, all rows together, and so slope_kernel's CTAs: five an
+// Of the rows' largest |t|, all rows together, and so slope_kernel's CTAs: five an
 // SM, all at once (32 rows 401 us; eight an SM, in two rounds, 404).
 constexpr int kMaxParts = 760;
 constexpr int kPadRows = 192;                 // t is kept, as zeros, up to a multiple of this
@@ -81,7 +83,7 @@ constexpr uint32_t kTmem = 512;
 // kernel may have started while the one before it was still writing, and the
 // read-only path is for data that no longer change.
 //
-// t 2^-e with e = exponent of the row's largest |gl| (0 for a row of zeros) and
+// t 2^-e with e = exponent of the row's largest |t| / scale (0 for a row of zeros) and
 // the scale's mantissa in [2^11, 2^12) is below 2^13.
 __device__ __forceinline__ int row_exponent(const float *gmax, int b, int parts) {
   float m = 0.0f;
@@ -139,8 +141,8 @@ __global__ void __launch_bounds__(256) slope_kernel(const BackwardArgs a, float 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (a.cap > 0.0f && beyond_cap(y[j], a.cap)) x[j] = y[j] = 0.0f;
-      m = fmaxf(m, fabsf(x[j]));
       if (a.cap > 0.0f) x[j] *= cap_slope(y[j], a.cap, inv_cap);
+      m = fmaxf(m, fabsf(x[j]));
       x[j] *= scale_m;
     }
     // slab_order: rows 4j, 4j + 1 to places 2j, 2j + 1 of the slab's first eight, the others to its second
@@ -973,7 +975,7 @@ size_t backward_part_floats(int64_t n_rows, int k, int max_batch, int num_sms) {
 size_t backward_t_floats(int64_t n_rows, int max_batch) {
   return static_cast<size_t>((n_rows + kPadRows - 1) / kPadRows * kPadRows) * max_batch;
 }
-size_t backward_misc_floats() { return kMaxParts + 32 + 1; }   // largest |gl|, RMS factors, flag
+size_t backward_misc_floats() { return kMaxParts + 32 + 1; }   // largest |t|, RMS factors, flag
 
 cudaError_t launch_backward(const BackwardArgs &a) {
   // the scale as scale_m 2^scale_e, 2^11 <= |scale_m| < 2^12
