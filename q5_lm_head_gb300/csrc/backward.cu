@@ -83,14 +83,16 @@ constexpr uint32_t kTmem = 512;
 // kernel may have started while the one before it was still writing, and the
 // read-only path is for data that no longer change.
 //
-// t 2^-e with e = exponent of the row's largest |t| / scale (0 for a row of zeros) and
-// the scale's mantissa in [2^11, 2^12) is below 2^13.
+// t is kept without the scale.  t 2^-e times the scale's mantissa in [2^11, 2^12) is
+// below 2^13, with e = exponent of the row's largest |t| (0 for a row of zeros).
+// Below 2^-115 it stays there, or the factor would leave f32's range: the operands
+// then end at 2^-150 at least.
 __device__ __forceinline__ int row_exponent(const float *gmax, int b, int parts) {
   float m = 0.0f;
   for (int i = threadIdx.x & 31; i < parts; i += 32) m = fmaxf(m, __ldcg(gmax + b * parts + i));
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
-  return m == 0.0f ? 0 : e < -126 ? -126 : e;   // 128 for infinities: they stay what they are
+  return m == 0.0f ? 0 : e < -115 ? -115 : e;   // 128 for infinities: they stay what they are
 }
 // A slab's 16 rows v in the order in which a thread's transposed fragment goes to
 // tensor memory: the first two of every four, then the others.
@@ -107,8 +109,8 @@ __device__ __forceinline__ float cap_slope(float l, float cap, float inv_cap) {
   return ((cap - l) * inv_cap) * ((cap + l) * inv_cap);
 }
 
-// t[p/8][b][p%8] = gl * scale_m * slope of row v, p = slab_order(v), scale_m the scale's mantissa.
-__global__ void __launch_bounds__(256) slope_kernel(const BackwardArgs a, float scale_m, int64_t share) {
+// t[p/8][b][p%8] = gl * slope of row v, p = slab_order(v).
+__global__ void __launch_bounds__(256) slope_kernel(const BackwardArgs a, int64_t share) {
   __shared__ float s_max[8];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the main kernel's set-up beside this one
   const int b = blockIdx.y;
@@ -143,7 +145,6 @@ __global__ void __launch_bounds__(256) slope_kernel(const BackwardArgs a, float 
       if (a.cap > 0.0f && beyond_cap(y[j], a.cap)) x[j] = y[j] = 0.0f;
       if (a.cap > 0.0f) x[j] *= cap_slope(y[j], a.cap, inv_cap);
       m = fmaxf(m, fabsf(x[j]));
-      x[j] *= scale_m;
     }
     // slab_order: rows 4j, 4j + 1 to places 2j, 2j + 1 of the slab's first eight, the others to its second
     float *t = a.t + ((v >> 4 << 1) * a.batch + b) * 8 + ((v >> 1) & 6);
@@ -299,7 +300,8 @@ __device__ __forceinline__ float split_d(float d, int &e, bool &big) {
 
 template <int NM, bool kQ4>
 __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
-    backward_tc_kernel(const __grid_constant__ CUtensorMap wmap, const BackwardArgs a, int gparts, int pairs, int splits) {
+    backward_tc_kernel(const __grid_constant__ CUtensorMap wmap, const BackwardArgs a, float scale_m, int gparts, int pairs,
+                       int splits) {
   using C = BwdCfg<NM, kQ4>;
   extern __shared__ __align__(1024) uint8_t smem[];                // [kStages][weights], [kSides][B tiles, scales, mins]
   __half *s_md = reinterpret_cast<__half *>(smem + C::kMdAt);      // [kGroups][kT]
@@ -311,7 +313,7 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
   uint64_t *dfull = tempty + C::kBufs, *dfree = dfull + 2, *done = dfree + 2;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(done + 1);
   volatile uint32_t *s_abort = s_tmem + 1;
-  float *s_e2 = reinterpret_cast<float *>(s_tmem + 2);            // [NM] powers of two: rows of t into f16's range
+  float *s_e2 = reinterpret_cast<float *>(s_tmem + 2);            // [NM] the scale's mantissa, rows of t into f16's range
   static_assert((2 * C::kStages + 2 * C::kSides + 2 * C::kBufs + 5) * 8 + 8 + 4 * NM <= 512, "behind the mantissas");
 
   // the warp's index from one lane: the compiler then knows the roles' branches and loops to be uniform
@@ -465,8 +467,8 @@ __global__ void __launch_bounds__(BwdCfg<NM, kQ4>::kThreads, 1)
     const int oct = b_turn % kOcts, b_first = b_turn < kStepB * kOcts ? b_turn / kOcts : NM;
     asm volatile("griddepcontrol.wait;" ::: "memory");            // t and the rows' largest values
     for (int b = warp - kUnpackWarps; b < a.batch; b += 4 * C::kGroups) {
-      const float e = pow2(-min(row_exponent(a.gmax, b, gparts), 126));
-      if (lane == 0) s_e2[b] = e;
+      const int e = row_exponent(a.gmax, b, gparts);
+      if (lane == 0) s_e2[b] = scale_m * pow2(-(e >> 1)) * pow2((e >> 1) - e);   // in two: e is up to 128
     }
     float e2[kTasks];
     float4 t_next[kTasks][2];
@@ -805,7 +807,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const BackwardAr
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (a.grad_gamma && a.batch > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // gamma_kernel follows
   const bool plain = __ldcg(a.flag) != 0u;
-  const double back = ldexp(1.0, min(row_exponent(a.gmax, b, gparts), 126) + scale_e);
+  const double back = ldexp(1.0, row_exponent(a.gmax, b, gparts) + scale_e);
   const int64_t stride = static_cast<int64_t>(a.batch) * a.k;
   float *gx = a.part + static_cast<int64_t>(b) * a.k;
   const int64_t at = static_cast<int64_t>(b) * a.k;
@@ -946,7 +948,7 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_
 }
 
 template <int NM, bool kQ4>
-cudaError_t launch_backward_nm(const BackwardArgs &a, int gparts, int *splits) {
+cudaError_t launch_backward_nm(const BackwardArgs &a, float scale_m, int gparts, int *splits) {
   using C = BwdCfg<NM, kQ4>;
   CUtensorMap map;
   cudaError_t e = encode_boxes(&map, a, C::kRowBytes, C::kRows);
@@ -964,7 +966,7 @@ cudaError_t launch_backward_nm(const BackwardArgs &a, int gparts, int *splits) {
   const int pairs = bwd_pairs(a.k);
   *splits = bwd_splits(a.n_rows, a.k, a.num_sms, C::kRows);
   return launch_dependent(backward_tc_kernel<NM, kQ4>, dim3(static_cast<unsigned>(pairs * *splits)), C::kThreads, C::kSmem,
-                          1, a.stream, map, a, gparts, pairs, *splits);
+                          1, a.stream, map, a, scale_m, gparts, pairs, *splits);
 }
 
 }  // namespace
@@ -987,19 +989,19 @@ cudaError_t launch_backward(const BackwardArgs &a) {
   const int64_t share = (ctas + most - 1) / most * 256;
   const int gparts = static_cast<int>((ctas * 256 + share - 1) / share);
   // an ordinary launch: after everything before it on the stream, the weights' own writer too
-  slope_kernel<<<dim3(static_cast<unsigned>(gparts), static_cast<unsigned>(a.batch)), 256, 0, a.stream>>>(a, scale_m, share);
+  slope_kernel<<<dim3(static_cast<unsigned>(gparts), static_cast<unsigned>(a.batch)), 256, 0, a.stream>>>(a, share);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   int splits = 1;
   const int slots = tc_batch_slots(a.batch);
   if (a.q4)
-    e = slots == 8    ? launch_backward_nm<8, true>(a, gparts, &splits)
-        : slots == 16 ? launch_backward_nm<16, true>(a, gparts, &splits)
-                      : launch_backward_nm<32, true>(a, gparts, &splits);
+    e = slots == 8    ? launch_backward_nm<8, true>(a, scale_m, gparts, &splits)
+        : slots == 16 ? launch_backward_nm<16, true>(a, scale_m, gparts, &splits)
+                      : launch_backward_nm<32, true>(a, scale_m, gparts, &splits);
   else
-    e = slots == 8    ? launch_backward_nm<8, false>(a, gparts, &splits)
-        : slots == 16 ? launch_backward_nm<16, false>(a, gparts, &splits)
-                      : launch_backward_nm<32, false>(a, gparts, &splits);
+    e = slots == 8    ? launch_backward_nm<8, false>(a, scale_m, gparts, &splits)
+        : slots == 16 ? launch_backward_nm<16, false>(a, scale_m, gparts, &splits)
+                      : launch_backward_nm<32, false>(a, scale_m, gparts, &splits);
   if (e != cudaSuccess) return e;
   // eight CTAs a row, or one with little to add (5 rows of 2,048 x 6,656: 12.5 us as a
   // whole, against 22.7 us with one each; one row of the full head 224 us against 238)

@@ -154,7 +154,7 @@ struct BackwardArgs {
   int k;
   int num_sms;
   float *part;                // workspace of backward_part_floats: the row shares' sums of the gradient by the normed input
-  float *t;                   // workspace of backward_t_floats: the gradient by the matrix product, eight rows v of a batch row together
+  float *t;                   // workspace of backward_t_floats: the gradient by the scaled product, eight rows v of a batch row together
   float *gmax, *rms;          // workspace: largest |t| of parts of each row, RMS factors
   uint32_t *flag;             // workspace: a block's d or dmin is beyond the tensor cores' operands
   uint32_t *status;
