@@ -324,7 +324,14 @@ class TokenScores(NamedTuple):
 
 
 class LMHead:
-    """A handle for one [n_rows x k] Q5_K (or, fmt="q4_k", Q4_K) matrix and batches up to max_batch."""
+    """A handle for one [n_rows x k] Q5_K (or, fmt="q4_k", Q4_K) matrix and batches up to max_batch.
+
+    Calls run on torch's current stream, or on the one given as `stream`.  A call
+    on another stream than the current one does not wait for it, nor does the
+    current one wait: that is the caller's, as with torch's own operations.  Its
+    tensors' memory is safe either way: results are allocated for `stream`, and
+    neither inputs nor results, once let go, are used again before both streams
+    are done with them."""
 
     def __init__(self, n_rows: int, k: int, max_batch: int = MUSE_MAX_BATCH, device: int | None = None,
                  fmt: str = "q5_k"):
@@ -353,6 +360,28 @@ class LMHead:
     def __exit__(self, *exc):
         self.close()
 
+    def _allocator(self, stream, *used):
+        """torch.empty for a call's results; with a stream of its own, for that stream's use, and
+        the call's other tensors are marked as used there."""
+        import torch
+        if stream is None:
+            return torch.empty
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream, device=self.device)
+        current = torch.cuda.current_stream(self.device)
+        for t in used:
+            if t is not None and t.is_cuda:
+                t.record_stream(stream)
+
+        def empty(shape, dtype, device):
+            # A block of the current stream's may still be in use by what is queued there.
+            with torch.cuda.stream(stream):
+                t = torch.empty(shape, dtype=dtype, device=device)
+            t.record_stream(current)
+            return t
+
+        return empty
+
     def _check(self, t, name, dtype, shape=None):
         if t.dtype != dtype or not t.is_contiguous() or t.get_device() != self.device:
             raise ValueError(f"{name}: need a contiguous {dtype} tensor on cuda:{self.device}")
@@ -372,13 +401,14 @@ class LMHead:
         if weights.numel() != self.n_rows * (self.k // 256) * self.block_bytes:
             raise ValueError("weights: wrong number of bytes for this handle")
         gp = None if gamma is None else self._check(gamma, "gamma", torch.float32, (self.k,))
+        empty = self._allocator(stream, hidden, weights, gamma, logits, argmax)
         if logits is None:
-            logits = torch.empty((b, self.n_rows), dtype=torch.float32, device=hidden.device)
+            logits = empty((b, self.n_rows), dtype=torch.float32, device=hidden.device)
         lp = self._check(logits, "logits", torch.float32, (b, self.n_rows))
         ap = None
         if want_argmax:
             if argmax is None:
-                argmax = torch.empty((b,), dtype=torch.int32, device=hidden.device)
+                argmax = empty((b,), dtype=torch.int32, device=hidden.device)
             ap = self._check(argmax, "argmax", torch.int32, (b,))
         s = torch.cuda.current_stream(self.device) if stream is None else stream
         st = muse_lmhead_forward(self.handle, hp, b, gp, float(eps), wp, float(scale), float(cap), lp, ap,
@@ -424,16 +454,17 @@ class LMHead:
         if weights.numel() != self.n_rows * (self.k // 256) * self.block_bytes:
             raise ValueError("weights: wrong number of bytes for this handle")
         gp = None if gamma is None else self._check(gamma, "gamma", torch.float32, (self.k,))
+        empty = self._allocator(stream, hidden, weights, gamma, logprobs, lse, argmax)
         if logprobs is None:
-            logprobs = torch.empty((b, self.n_rows), dtype=torch.float32, device=hidden.device)
+            logprobs = empty((b, self.n_rows), dtype=torch.float32, device=hidden.device)
         lp = self._check(logprobs, "logprobs", torch.float32, (b, self.n_rows))
         if lse is None:
-            lse = torch.empty((b,), dtype=torch.float32, device=hidden.device)
+            lse = empty((b,), dtype=torch.float32, device=hidden.device)
         sp = self._check(lse, "lse", torch.float32, (b,))
         ap = None
         if want_argmax:
             if argmax is None:
-                argmax = torch.empty((b,), dtype=torch.int32, device=hidden.device)
+                argmax = empty((b,), dtype=torch.int32, device=hidden.device)
             ap = self._check(argmax, "argmax", torch.int32, (b,))
         s = torch.cuda.current_stream(self.device) if stream is None else stream
         st = muse_lmhead_forward_logprobs(self.handle, hp, b, gp, float(eps), wp, float(scale), float(cap), lp, sp,
@@ -453,12 +484,14 @@ class LMHead:
         hp = self._check(h, "hidden", torch.float32, (self.k,))
         gp = None if gamma is None else self._check(gamma, "gamma", torch.float32, (self.k,))
         outs, descs = [], []
+        segments = list(segments)
+        empty = self._allocator(stream, hidden, gamma, *(seg[0] for seg in segments), *(seg[4] for seg in segments))
         for (w, n, scale, cap, out) in segments:
             wp = self._check(w, "weights", torch.uint8)
             if w.numel() != n * (self.k // 256) * self.block_bytes:
                 raise ValueError("weights: wrong number of bytes for n_rows")
             if out is None:
-                out = torch.empty((n,), dtype=torch.float32, device=hidden.device)
+                out = empty((n,), dtype=torch.float32, device=hidden.device)
             op = self._check(out, "out", torch.float32, (n,))
             outs.append(out)
             descs.append((wp, n, op, float(scale), float(cap)))
@@ -512,12 +545,12 @@ class LMHead:
     def _stream(self, stream):
         return _current_stream()(self.device) if stream is None else stream.cuda_stream
 
-    def _score_outputs(self, n, tokens, n_top, device):
+    def _score_outputs(self, n, tokens, n_top, device, empty):
         """(TokenScores, pointers of tokens and outputs in the C order)"""
         import torch
         if not 0 <= n_top <= MUSE_MAX_TOP:
             raise ValueError(f"n_top: 0..{MUSE_MAX_TOP}")
-        empty, f, i, rows = torch.empty, torch.float32, torch.int32, (n,)
+        f, i, rows = torch.float32, torch.int32, (n,)
         tp = lp = rp = ip = pp = logprob = rank = ids = top = None
         if tokens is not None:
             tp = self._check(tokens, "tokens", i, rows)
@@ -541,7 +574,7 @@ class LMHead:
         if logits.dim() == 1:
             logits = logits.unsqueeze(0)
         ptr, dtype, n, ld = self._rows(logits, "logits")
-        out, tp, *at = self._score_outputs(n, tokens, n_top, logits.device)
+        out, tp, *at = self._score_outputs(n, tokens, n_top, logits.device, self._allocator(stream, logits, tokens))
         st = load_library().muse_lmhead_score(self.handle, ptr, dtype, n, ld, tp, temperature, n_top, *at,
                                               self._stream(stream))
         if st != MUSE_OK:
@@ -561,10 +594,11 @@ class LMHead:
         if weights.numel() != self.n_rows * (self.k // 256) * self.block_bytes:
             raise ValueError("weights: wrong number of bytes for this handle")
         gp = None if gamma is None else self._check(gamma, "gamma", torch.float32, (self.k,))
+        empty = self._allocator(stream, hidden, weights, gamma, logits, tokens)
         if logits is None:
-            logits = torch.empty((b, self.n_rows), dtype=torch.float32, device=hidden.device)
+            logits = empty((b, self.n_rows), dtype=torch.float32, device=hidden.device)
         lp = self._check(logits, "logits", torch.float32, (b, self.n_rows))
-        out, tp, *at = self._score_outputs(b, tokens, n_top, hidden.device)
+        out, tp, *at = self._score_outputs(b, tokens, n_top, hidden.device, empty)
         st = muse_lmhead_forward_score(self.handle, hp, b, gp, float(eps), wp, float(scale), float(cap), lp, tp,
                                        float(temperature), n_top, *at, self._stream(stream))
         if st != MUSE_OK:
@@ -590,10 +624,11 @@ class LMHead:
         ip = self._check(teacher_ids, "teacher_ids", torch.int32, (n, top))
         pp = self._check(teacher_logprobs, "teacher_logprobs", torch.float32, (n, top))
         wp = None if row_weight is None else self._check(row_weight, "row_weight", torch.float32, (n,))
-        loss = torch.empty((n,), dtype=torch.float32, device=logits.device)
+        empty = self._allocator(stream, logits, teacher_ids, teacher_logprobs, row_weight, grad)
+        loss = empty((n,), dtype=torch.float32, device=logits.device)
         gp, gld = None, 0
         if grad is None and want_grad:
-            grad = torch.empty((n, self.n_rows), dtype=logits.dtype, device=logits.device)
+            grad = empty((n, self.n_rows), dtype=logits.dtype, device=logits.device)
         if grad is not None:
             gp, gtype, gn, gld = self._rows(grad, "grad")
             if gtype != dtype or gn != n:
@@ -622,6 +657,7 @@ class LMHead:
         if weights.numel() != self.n_rows * (self.k // 256) * self.block_bytes:
             raise ValueError("weights: wrong number of bytes for this handle")
         lp = hp = gp = ap = grad_gamma = None
+        empty = self._allocator(stream, grad_logits, weights, logits, hidden, gamma, grad_hidden)
         if logits is not None:
             lp = self._check(logits, "logits", torch.float32, (b, self.n_rows))
         if gamma is not None:
@@ -629,10 +665,10 @@ class LMHead:
                 raise ValueError("hidden: needed with gamma")
             hp = self._check(hidden, "hidden", torch.float32, (b, self.k))
             gp = self._check(gamma, "gamma", torch.float32, (self.k,))
-            grad_gamma = torch.empty((self.k,), dtype=torch.float32, device=grad_logits.device)
+            grad_gamma = empty((self.k,), dtype=torch.float32, device=grad_logits.device)
             ap = grad_gamma.data_ptr()
         if grad_hidden is None:
-            grad_hidden = torch.empty((b, self.k), dtype=torch.float32, device=grad_logits.device)
+            grad_hidden = empty((b, self.k), dtype=torch.float32, device=grad_logits.device)
         op = self._check(grad_hidden, "grad_hidden", torch.float32, (b, self.k))
         st = load_library().muse_lmhead_backward(self.handle, tp, lp, hp, b, gp, eps, wp, scale, cap, op, ap,
                                                  self._stream(stream))
