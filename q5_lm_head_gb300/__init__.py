@@ -659,10 +659,14 @@ class LMHead:
         lp = hp = gp = ap = grad_gamma = None
         empty = self._allocator(stream, grad_logits, weights, logits, hidden, gamma, grad_hidden)
         if logits is not None:
+            if logits.dim() == 1:
+                logits = logits.unsqueeze(0)
             lp = self._check(logits, "logits", torch.float32, (b, self.n_rows))
         if gamma is not None:
             if hidden is None:
                 raise ValueError("hidden: needed with gamma")
+            if hidden.dim() == 1:
+                hidden = hidden.unsqueeze(0)
             hp = self._check(hidden, "hidden", torch.float32, (b, self.k))
             gp = self._check(gamma, "gamma", torch.float32, (self.k,))
             grad_gamma = empty((self.k,), dtype=torch.float32, device=grad_logits.device)
