@@ -575,7 +575,7 @@ class LMHead:
             logits = logits.unsqueeze(0)
         ptr, dtype, n, ld = self._rows(logits, "logits")
         out, tp, *at = self._score_outputs(n, tokens, n_top, logits.device, self._allocator(stream, logits, tokens))
-        st = load_library().muse_lmhead_score(self.handle, ptr, dtype, n, ld, tp, float(temperature), n_top, *at,
+        st = load_library().muse_lmhead_score(self.handle, ptr, dtype, n, ld, tp, temperature, n_top, *at,
                                               self._stream(stream))
         if st != MUSE_OK:
             raise MuseError(st, "muse_lmhead_score")
@@ -634,7 +634,7 @@ class LMHead:
             if gtype != dtype or gn != n:
                 raise ValueError("grad: need the logits' shape and dtype")
         st = load_library().muse_lmhead_distill(self.handle, ptr, dtype, n, ld, ip, pp, top, 1 if tail else 0, wp,
-                                                float(temperature), loss.data_ptr(), gp, gld, self._stream(stream))
+                                                temperature, loss.data_ptr(), gp, gld, self._stream(stream))
         if st != MUSE_OK:
             raise MuseError(st, "muse_lmhead_distill")
         return loss, grad
@@ -674,8 +674,8 @@ class LMHead:
         if grad_hidden is None:
             grad_hidden = empty((b, self.k), dtype=torch.float32, device=grad_logits.device)
         op = self._check(grad_hidden, "grad_hidden", torch.float32, (b, self.k))
-        st = load_library().muse_lmhead_backward(self.handle, tp, lp, hp, b, gp, float(eps), wp, float(scale),
-                                                 float(cap), op, ap, self._stream(stream))
+        st = load_library().muse_lmhead_backward(self.handle, tp, lp, hp, b, gp, eps, wp, scale, cap, op, ap,
+                                                 self._stream(stream))
         if st != MUSE_OK:
             raise MuseError(st, "muse_lmhead_backward")
         return grad_hidden, grad_gamma
