@@ -376,8 +376,9 @@ int muse_lmhead_forward_score(muse_lmhead *h, const float *hidden, int batch, co
  *           overlap them otherwise.  One of the two is needed.  Elements between n_rows and grad_ld are left alone.
  * A row with no teacher entry left has loss and gradient 0, and so has a row
  * whose logits are all -infinity.  Where the teacher expects a masked logit
- * the loss is +infinity and the gradient finite.  A NaN or +infinity in a row
- * gives NaN.  Uses no workspace of the handle: calls may overlap.  One launch.
+ * the loss is +infinity and the gradient finite.  A NaN or +infinity in a row,
+ * or a NaN among its teacher's entries, gives NaN.  Uses no workspace of the
+ * handle: calls may overlap.  One launch.
  */
 int muse_lmhead_distill(muse_lmhead *h, const void *logits, int dtype, int64_t n, int64_t ld,
                         const int32_t *teacher_ids, const float *teacher_logprobs, int n_top, int tail,

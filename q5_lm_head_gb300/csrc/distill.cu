@@ -65,6 +65,8 @@ __device__ __forceinline__ float move_sum(float s, float from, float to, float c
 __device__ __forceinline__ float warp_max(float v) {
   return order_key_float(__reduce_max_sync(0xffffffffu, float_order_key(v)));
 }
+// What the teacher's entries leave for the rest; a NaN among them stays one.
+__device__ __forceinline__ float left_over(float mass) { return mass > 1.0f ? 0.0f : 1.0f - mass; }
 // -infinity as a reference: 0, against which nothing but 0 or NaN is summed.
 __device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.0f : m; }
 
@@ -260,14 +262,14 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
     const float total = apart ? move_sum(rest, rest_m, most, c) + move_sum(in, ids_m, most, c) : rest;
     // all masked (the sums stay 0), or NaN beside masked values: against 0
     const float m = reference(most), mr = reference(rest_m);
-    const float pt = a.tail ? fmaxf(0.0f, 1.0f - mass) : 0.0f;
+    const float pt = a.tail ? left_over(mass) : 0.0f;
     if (cr == 0 && warp == 0 && a.loss) {
       // a few values a row, in 64 bits: a lowest value would overflow in log2's units
       // Differences of logits first: of 3.4e38 in size they would swallow the sum's logarithm.
       const double log_sum = row_log_sum(m, c, log2f(total));
       double loss = 0.0;
       for (int j = lane; j < k; j += 32)
-        if (sh.p[j] > 0.0f)
+        if (sh.p[j] != 0.0f)              // NaNs too
           loss += sh.p[j] * (sh.lp[j] - ((static_cast<double>(sh.x[j]) - m) * a.inv_temperature64 - log_sum));
       for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
       if (pt > 0.0f)
@@ -419,22 +421,20 @@ __global__ void __launch_bounds__(kDistillThreads) distill_long_kernel(const Dis
   float lmax = -INFINITY, mass = 0.0f;
   double loss = 0.0;                                   // as in distill_kernel
   for (int j = 0; j < a.n_top; ++j) lmax = fmaxf(lmax, s_p[j]);
-  if (lmax > -INFINITY) {
+  float shift = 0.0f;
+  if (!a.tail && lmax > -INFINITY) {
     float sum = 0.0f;
     for (int j = 0; j < a.n_top; ++j) sum += expf(s_p[j] - lmax);
-    const float c = a.tail ? 0.0f : lmax + logf(sum);
-    for (int j = 0; j < a.n_top; ++j) {
-      const float lp = s_p[j] - c, p = expf(lp);
-      mass += p;
-      if (p > 0.0f) loss += p * (lp - ((static_cast<double>(s_x[j]) - m) * a.inv_temperature64 - logs));
-    }
-    __syncthreads();
-    if (tid < a.n_top) s_p[tid] = expf(s_p[tid] - c);
-  } else {
-    __syncthreads();
-    if (tid < a.n_top) s_p[tid] = 0.0f;
+    shift = lmax + logf(sum);
   }
-  const float pt = a.tail ? fmaxf(0.0f, 1.0f - mass) : 0.0f;
+  for (int j = 0; j < a.n_top; ++j) {
+    const float lp = s_p[j] - shift, p = expf(lp);
+    mass += p;
+    if (p != 0.0f) loss += p * (lp - ((static_cast<double>(s_x[j]) - m) * a.inv_temperature64 - logs));
+  }
+  __syncthreads();
+  if (tid < a.n_top) s_p[tid] = expf(s_p[tid] - shift);
+  const float pt = a.tail ? left_over(mass) : 0.0f;
   if (pt > 0.0f) loss += pt * (logf(pt) - ((static_cast<double>(mr) - m) * a.inv_temperature64 + logf(rest) - logs));
   if (tid == 0 && a.loss) a.loss[row] = static_cast<float>(w * loss);
   if (!g) return;
