@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
     const float ref = reference(top);
     unsigned long long s2 = 0ull;
     const unsigned long long c2 = pack2(c, c);
-    if (fabsf(ref) < kPlain) {
-      const float rc = -__fmul_rn(ref, c);
+    const float rc = -__fmul_rn(ref, c);
+    if (plain_product(rc)) {
       const unsigned long long rc2 = pack2(rc, rc);
       for (int i = tid; i < v1 - v0; i += kDistillThreads) {
         float o[W];
@@ -311,10 +311,9 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
     top = in_m;
     // the gradient outside S; the ids' places are 0 here (-infinity in the row)
     if (scale != 0.0f) {
-      const bool plain = fabsf(mr) < kPlain;
-      if (plain && (reinterpret_cast<uintptr_t>(g + first) & 15) == 0) {
+      const float rc = -__fmul_rn(mr, c);
+      if (plain_product(rc) && (reinterpret_cast<uintptr_t>(g + first) & 15) == 0) {
         uint4 *gv = reinterpret_cast<uint4 *>(g + first);
-        const float rc = -__fmul_rn(mr, c);
         const unsigned long long rc2 = pack2(rc, rc), f2 = pack2(f_out, f_out);
         for (int i = tid; i < v1 - v0; i += kDistillThreads) {
           float o[W];

@@ -149,24 +149,34 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigne
 
 // (x - m) c, c = log2(e) / temperature: the exponent of x against the row's
 // reference m.  One fma with the rounded product m c as the reference itself,
-// which every use of it shares; where that product could overflow (masks of the
-// type's lowest value), the difference first.
-constexpr float kPlain = 1e30f;
+// which every use of it shares.  The rounding moves the reference by up to
+// 2^-24 |m c|: below 2^20 by a sixteenth, but for masks of -1e10 by hundreds, which
+// would leave no value of the row in range.  From there on the difference is
+// taken first, and the reference is m c itself.
+constexpr float kPlain = 1048576.0f;
+__device__ __forceinline__ bool plain_product(float mc) { return fabsf(mc) < kPlain; }   // of no infinity or NaN
 __device__ __forceinline__ float exponent(float x, float m, float c) {
-  return fabsf(m) < kPlain ? fmaf(x, c, -__fmul_rn(m, c)) : (x - m) * c;
+  const float mc = __fmul_rn(m, c);
+  return plain_product(mc) ? fmaf(x, c, -mc) : (x - m) * c;
+}
+// What m c is above its reference.
+__device__ __forceinline__ float reference_off(float m, float c) {
+  const float mc = __fmul_rn(m, c);
+  return plain_product(mc) ? fmaf(m, c, -mc) : 0.0f;
 }
 // The exponent by which sums against reference `from` move to reference `to`.
 __device__ __forceinline__ float shift_exponent(float from, float to, float c) {
-  return fabsf(from) < kPlain && fabsf(to) < kPlain ? __fadd_rn(__fmul_rn(from, c), -__fmul_rn(to, c)) : (from - to) * c;
+  const float f = __fmul_rn(from, c), t = __fmul_rn(to, c);
+  if (plain_product(f) && plain_product(t)) return __fadd_rn(f, -t);
+  return (from - to) * c - reference_off(from, c) + reference_off(to, c);
 }
 
 // log sum exp((x - m) / temperature) from log2 of the sum of exponents against m, in
-// 64 bits.  The sum's reference was the rounded product m c: the logarithm
-// against m itself takes the rounding off again.
+// 64 bits.  The logarithm against m itself takes off again what the reference
+// was beside it.
 constexpr double kLn2 = 0.6931471805599453;
 __device__ __forceinline__ double row_log_sum(float m, float c, float log2_sum) {
-  const float off = fabsf(m) < kPlain ? fmaf(m, c, -__fmul_rn(m, c)) : 0.0f;
-  return kLn2 * (static_cast<double>(log2_sum) - off);
+  return kLn2 * (static_cast<double>(log2_sum) - reference_off(m, c));
 }
 
 // ---------------------------------------------------------------- clusters

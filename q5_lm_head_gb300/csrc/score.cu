@@ -49,12 +49,8 @@ struct Stat {
 
 __device__ __forceinline__ Stat stat_move(Stat t, float m, float c) {
   if (m == -INFINITY) return {m, t.s, t.u};
-  const float d = shift_exponent(t.m, m, c), f = exp2_approx(d);
-  if (t.s != 0.0f) {                             // 0 has nothing to move, and 0 times -infinity would be NaN
-    t.u = (t.u + t.s * fmaxf(d, -1e30f)) * f;
-    t.s *= f;
-  }
-  return {m, t.s, t.u};
+  const float d = shift_exponent(t.m, m, c), f = exp2_approx(d);   // 2^-200 is 0 here
+  return {m, t.s * f, (t.u + t.s * fmaxf(d, -200.0f)) * f};
 }
 
 // Sum over the warp's lanes, in a fixed order, against the largest of their values `most`.
@@ -243,10 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
   auto add_max = [&](float cm) {
     most = fmaxf(most, cm);
     if (cm > reach) {
-      const float2 s = unpack2(s2), u = unpack2(u2);
-      const Stat p = stat_move({st.m, s.x, u.x}, cm, c), q = stat_move({st.m, s.y, u.y}, cm, c);
-      s2 = pack2(p.s, q.s);
-      u2 = pack2(p.u, q.u);
+      const float d = shift_exponent(st.m, cm, c), f = exp2_approx(d), low = fmaxf(d, -200.0f);   // as in stat_move
+      u2 = mul2(fma2(s2, pack2(low, low), u2), pack2(f, f));
+      s2 = mul2(s2, pack2(f, f));
       st.m = ref = cm;
       reach = cm + room;
     }
@@ -331,8 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
       cm = fmaxf(cm, top[j]);
     }
     add_max(cm);
-    if (kFull && fabsf(ref) < kPlain) {
-      const float rc = -__fmul_rn(ref, c);
+    const float rc = -__fmul_rn(ref, c);
+    if (kFull && plain_product(rc)) {
       const unsigned long long rc2 = pack2(rc, rc);
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) {
