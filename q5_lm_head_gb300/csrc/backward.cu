@@ -9,13 +9,15 @@
 // and with the norm, r = 1/sqrt(mean h^2 + eps), xh = h r, gg = gx gamma:
 //     gh = r (gg - xh mean(gg xh)),   ggamma = sum_b gx xh
 //
-// Bound: the unpacking of the quants by the CUDA cores, at 1.6 (up to 8 rows) and
-// 2.8 times (32 rows) the time that HBM needs to read the matrix once: the full
-// Q5_K head takes 214 us for one row, 401 us for 32, the Q4_K head 192 us for 8
-// (for one row the main kernel, 206 us of it, issues in 75 % of all cycles, its
-// integer pipe is busy in 67 %; for 32 rows, 380 us, in 65 %: there the operand
-// warps' work is nearly half the unpacking's and the products have four times the
-// columns).  The contraction runs along the rows v of W, across the direction in
+// Bound: the CUDA cores' work between HBM and the tensor cores, no pipe of theirs
+// alone: the full Q5_K head takes 215 us for one row, 402 us for 32, the Q4_K head
+// 193 us for 8, 1.6, 2.8 and 1.7 times the time that HBM needs to read the matrix
+// once.  For one row the main kernel issues in 73 % of all cycles and its integer
+// pipe is busy in 67 % (Q4_K: 73 and 56 %: fewer operations a quant do not make it
+// as much faster); the rest is roles that wait for one another.  For 32 rows it
+// issues in 65 %: there the operand warps' work is nearly half the unpacking's and
+// the products have four times the columns.  9 of 152 SMs have no CTA.
+// The contraction runs along the rows v of W, across the direction in
 // which its blocks are packed, so the tensor cores' A operand is W transposed: a
 // lane of tensor memory is an input k, a column a pair of rows.
 //

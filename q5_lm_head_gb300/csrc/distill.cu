@@ -25,7 +25,7 @@
 //     dloss/dx_i = 2^((x_i - m_r) c) w/T [ (sum p + p_t) 2^((m_r - m) c) / Z - p_t / R ],  i not in S:
 // one factor for the whole row, which cannot overflow.
 // Nothing is kept in global memory, so calls may overlap.  A row that 16 CTAs
-// cannot hold is read twice by one CTA.
+// cannot hold is read by one CTA, twice for the loss and once more for the gradient.
 #include <atomic>
 
 #include "common.cuh"
@@ -474,8 +474,8 @@ cudaError_t launch_distill_t(const DistillArgs &a) {
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
-  // As few CTAs as hold the row four to an SM (1,024 bf16 rows of 202,048: 203 us,
-  // against 244 us three to an SM and 207 us eight), more while there are SMs to fill;
+  // As few CTAs as hold the row four to an SM (1,024 bf16 rows of 202,048: 166 us,
+  // against 194 us three to an SM and 266 us eight of half the share), more while there are SMs to fill;
   // 16 with fewer to an SM for the longest rows.
   const int64_t bytes = a.v * static_cast<int64_t>(sizeof(T));
   auto held = [&](int64_t cs) { return (bytes / 16 + cs - 1) / cs * 16; };   // a share is at most this

@@ -114,7 +114,10 @@ __device__ __forceinline__ float order_key_float(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
-__device__ __forceinline__ float exp2_approx(float v) {   // 2 ulp, 0 below the smallest normal
+// 2 ulp, 0 below the smallest normal: as good as expf to a sum of a row's
+// exponentials, which is off by more for its additions, and one instruction, of
+// which these kernels have few to spare beside their loads.
+__device__ __forceinline__ float exp2_approx(float v) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;

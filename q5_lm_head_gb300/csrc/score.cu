@@ -8,7 +8,7 @@
 // a division could merge neighbouring values.
 //
 // Bound: HBM (each logit is read once) for many rows, latency for a few: 1,024 rows of
-// 202,048 f32 take 154 us, 5.4 TB/s (79 % of the measured copy rate); the last
+// 202,048 f32 take 159 us, 5.2 TB/s (77 % of the measured copy rate); the last
 // of their 1.7 rounds of CTAs fills two SMs of three.  A cluster of 1, 2, 4, 8 or
 // 16 CTAs takes a row (about as many as give each SM one), each a contiguous share
 // of its 16-byte vectors; a thread holds a reference m with S and U, and the CTAs'
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
   // The sums' reference is the first maximum seen, and a later one only where it
   // lies 2^16 above: moving the sums onto every new maximum was most of a step's
   // instructions (some thread of a warp has one in three steps of four; with 2^8
-  // 1,024 rows of 202,048 f32 take 162.6 us, 157.9 with this).  Each power of two
+  // 1,024 rows of 202,048 f32 take 3 % longer).  Each power of two
   // of that room costs the entropy of a nearly certain row 1e-7: log2 S and U / S
   // are that large, their difference small.
   Stat st = {-INFINITY, 0.0f, 0.0f};
@@ -559,14 +559,14 @@ cudaError_t launch_score_t(const ScoreArgs &a, int cs) {
 
 // CTAs a row, and their threads (times in us for rows of 202,048 f32 and 8
 // alternatives, by threads/CTAs a row; rows of 32,000 f32 and 50,257 bf16 order
-// alike).  One CTA of 512 threads an SM (1 row: 512/16 11.6, 512/8 13.8, 512/1
-// 32.9; 16 rows: 512/8 17.4, 512/16 18.7), or of 256 threads where a share is
-// short (one row of 50,257 bf16: 256/8 9.1, 512/8 9.9, 512/16 11.2).  Where whole
+// alike).  One CTA of 512 threads an SM (1 row: 512/16 11.5, 512/8 13.9, 512/1
+// 32.7; 16 rows: 512/8 16.9, 512/16 19.8), or of 256 threads where a share is
+// short (one row of 50,257 bf16: 256/8 9.8, 512/8 10.0, 512/16 11.2).  Where whole
 // powers of two would leave a third of the SMs without one, smaller and more of
-// them, two or three an SM (77 rows: 256/4 28.2, 512/2 30.2, 512/1 35.7).  Rows for
-// more than one round of SMs: 153 rows 256/2 41.9, 512/1 46.6, 256/1 55.2; 304 rows
-// 512/1 51.4, 256/2 54.9; beyond, four CTAs of 256 an SM, whose barriers fall into
-// the others' loads (400 rows 256/1 73.3, 512/1 79.6).
+// them, two or three an SM (77 rows: 256/4 28.7, 512/2 30.4, 512/1 35.4).  Rows for
+// more than one round of SMs: 153 rows 256/2 42.5, 512/1 47.0, 256/1 57.2; 304 rows
+// 512/1 50.6, 256/2 56.2; beyond, four CTAs of 256 an SM, whose barriers fall into
+// the others' loads (400 rows 256/1 73.8, 512/1 83.5).
 template <typename T>
 cudaError_t launch_score_rows(const ScoreArgs &a) {
   const int64_t n = a.n, sms = a.num_sms, bytes = a.v * static_cast<int64_t>(sizeof(T));
