@@ -364,19 +364,24 @@ class LMHead:
         """torch.empty for a call's results; with a stream of its own, for that stream's use, and
         the call's other tensors are marked as used there."""
         import torch
-        if stream is None:
+        if stream is None or stream.cuda_stream == _current_stream()(self.device):
             return torch.empty
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(stream.cuda_stream, device=self.device)
-        current = torch.cuda.current_stream(self.device)
         for t in used:
             if t is not None and t.is_cuda:
                 t.record_stream(stream)
 
         def empty(shape, dtype, device):
             # A block of the current stream's may still be in use by what is queued there.
-            with torch.cuda.stream(stream):
+            current, device_before = torch.cuda.current_stream(self.device), torch.cuda.current_device()
+            torch.cuda.set_stream(stream)      # a context manager a tensor would cost the call 20 us
+            try:
                 t = torch.empty(shape, dtype=dtype, device=device)
+            finally:
+                torch.cuda.set_stream(current)
+                if device_before != self.device:
+                    torch.cuda.set_device(device_before)
             t.record_stream(current)
             return t
 
