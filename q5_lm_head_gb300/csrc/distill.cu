@@ -132,18 +132,20 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_kernel(const Disti
       if (lane == 0) sh.twice[warp] = any;
     }
     if (warp == 0) {                      // the teacher's probabilities
-      float l0 = sh.lp[lane], l1 = sh.lp[lane + 32], shift = 0.0f;
+      float l0 = sh.lp[lane], l1 = sh.lp[lane + 32];
       if (!a.tail) {
         float top = fmaxf(l0, l1);
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (top > -INFINITY) {
-          float s = expf(l0 - top) + expf(l1 - top);
+        if (top > -INFINITY) {            // the differences first: teacher logits may be thousands in size
+          l0 -= top;
+          l1 -= top;
+          float s = expf(l0) + expf(l1);
           for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          shift = top + logf(s);
+          s = logf(s);
+          l0 -= s;
+          l1 -= s;
         }
       }
-      l0 -= shift;
-      l1 -= shift;
       const float p0 = expf(l0), p1 = expf(l1);
       float mass = p0 + p1;
       for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
@@ -420,19 +422,21 @@ __global__ void __launch_bounds__(kDistillThreads) distill_long_kernel(const Dis
   float lmax = -INFINITY, mass = 0.0f;
   double loss = 0.0;                                   // as in distill_kernel
   for (int j = 0; j < a.n_top; ++j) lmax = fmaxf(lmax, s_p[j]);
-  float shift = 0.0f;
-  if (!a.tail && lmax > -INFINITY) {
+  float logsum = 0.0f;
+  if (a.tail || lmax == -INFINITY) {
+    lmax = 0.0f;
+  } else {
     float sum = 0.0f;
     for (int j = 0; j < a.n_top; ++j) sum += expf(s_p[j] - lmax);
-    shift = lmax + logf(sum);
+    logsum = logf(sum);
   }
   for (int j = 0; j < a.n_top; ++j) {
-    const float lp = s_p[j] - shift, p = expf(lp);
+    const float lp = s_p[j] - lmax - logsum, p = expf(lp);
     mass += p;
     if (p != 0.0f) loss += p * (lp - ((static_cast<double>(s_x[j]) - m) * a.inv_temperature64 - logs));
   }
   __syncthreads();
-  if (tid < a.n_top) s_p[tid] = expf(s_p[tid] - shift);
+  if (tid < a.n_top) s_p[tid] = expf(s_p[tid] - lmax - logsum);
   const float pt = a.tail ? left_over(mass) : 0.0f;
   if (pt > 0.0f) loss += pt * (logf(pt) - ((static_cast<double>(mr) - m) * a.inv_temperature64 + logf(rest) - logs));
   if (tid == 0 && a.loss) a.loss[row] = static_cast<float>(w * loss);
