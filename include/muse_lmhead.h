@@ -419,6 +419,60 @@ int muse_lmhead_backward(muse_lmhead *h, const float *grad_logits, const float *
                          int batch, const float *gamma, float eps, const void *weights, float scale, float cap,
                          float *grad_hidden, float *grad_gamma, void *stream);
 
+/* A token table whose rows are the blocks of the handle's format (muse_lmhead_embed). */
+#define MUSE_DTYPE_BLOCKS 3
+
+/*
+ * Rows of a token table, the way of a drawn token back into the model:
+ *     out[t][j] = scale * table[tokens[t]][j],  j < k
+ * rounded once to out's type (the product is formed in f32).  The handle gives
+ * k, the number of tokens (its n_rows) and, for a table of blocks, the format.
+ *   table   device: MUSE_DTYPE_F32, _F16 or _BF16: n_rows rows table_ld >= k
+ *           elements apart, aligned to one element only; MUSE_DTYPE_BLOCKS:
+ *           n_rows * (k/256) blocks as the head's weights, 16-byte aligned (a
+ *           tied head's own matrix; table_ld is ignored).
+ *   tokens  [n] int32, device; a value outside 0..n_rows-1 (a padded position)
+ *           gives a row of zeros.
+ *   n       0 .. 2^31-1, not bound by max_batch; 0 does nothing.
+ *   scale   finite.
+ *   out     device, out_dtype MUSE_DTYPE_F32, _F16 or _BF16, n rows out_ld >= k
+ *           elements apart, aligned to one element only; must not overlap the
+ *           inputs.  Elements between k and out_ld are left alone.
+ * Uses no workspace: calls may overlap.  One launch.
+ */
+int muse_lmhead_embed(muse_lmhead *h, const void *table, int table_type, int64_t table_ld, const int32_t *tokens,
+                      int64_t n, float scale, void *out, int out_dtype, int64_t out_ld, void *stream);
+
+/*
+ * Gradient by a dense token table from the gradient by the rows that were
+ * looked up:
+ *     grad_table[v][j] = (accumulate ? grad_table[v][j] : 0) + scale * sum_{t: tokens[t] = v} grad[t][j]
+ * With accumulate 0 every row is written, those without a token with zeros; with
+ * accumulate 1 only the rows of tokens that occur are read and written.  Sums are held
+ * in f32 in an order that depends on the tokens alone (the same inputs give the
+ * same bits) and rounded once to the table's type.
+ *   grad        device, dtype MUSE_DTYPE_F32, _F16 or _BF16, n rows grad_ld >= k
+ *               elements apart, aligned to one element only.
+ *   tokens      [n] int32, device; a position whose token lies outside
+ *               0..n_rows-1 is left out (its gradient is not read).
+ *   n           0 .. 2^31-1 - 2^20.
+ *   scale       finite.
+ *   grad_table  device, table_dtype as above, n_rows rows table_ld >= k elements
+ *               apart, aligned to one element only; must not overlap the
+ *               inputs.  Elements between k and table_ld are left alone.
+ *   workspace   device, 16-byte aligned, at least the bytes that
+ *               muse_lmhead_embed_backward_workspace gives for n (else
+ *               MUSE_ERR_NOMEM); its contents are of no use before or after.  Calls that
+ *               may overlap need a workspace each.
+ * Up to three launches.
+ */
+int muse_lmhead_embed_backward(muse_lmhead *h, const void *grad, int dtype, int64_t grad_ld, const int32_t *tokens,
+                               int64_t n, float scale, void *grad_table, int table_dtype, int64_t table_ld,
+                               int accumulate, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace for n positions (host-only query). */
+int muse_lmhead_embed_backward_workspace(const muse_lmhead *h, int64_t n, int64_t *bytes);
+
 /* Argmax keys (muse_lmhead_set_argmax_key). */
 #define MUSE_ARGMAX_CAPPED 0   /* the returned logit, after scale and cap (the default) */
 #define MUSE_ARGMAX_PRECAP 1   /* scale * raw, before the cap */

@@ -27,6 +27,7 @@ __all__ = [
     "muse_lmhead_clear_device_status", "muse_lmhead_selftest_wait_timeout",
     "muse_lmhead_set_argmax_key", "MUSE_ARGMAX_CAPPED", "MUSE_ARGMAX_PRECAP",
     "muse_lmhead_score", "muse_lmhead_forward_score", "muse_lmhead_distill", "muse_lmhead_backward", "MUSE_MAX_TOP",
+    "muse_lmhead_embed", "muse_lmhead_embed_backward", "muse_lmhead_embed_backward_workspace",
     "EXPORTED_SYMBOLS",
     "LOGIT_SCALE", "SOFTCAP", "RMS_EPS",
 ]
@@ -50,6 +51,7 @@ EXPORTED_SYMBOLS = (
     "muse_lmhead_init_format",
     "muse_lmhead_clear_device_status", "muse_lmhead_selftest_wait_timeout", "muse_lmhead_set_argmax_key",
     "muse_lmhead_score", "muse_lmhead_forward_score", "muse_lmhead_distill", "muse_lmhead_backward",
+    "muse_lmhead_embed", "muse_lmhead_embed_backward", "muse_lmhead_embed_backward_workspace",
 )
 
 MUSE_OK = 0
@@ -64,6 +66,7 @@ MUSE_ARGMAX_CAPPED = 0      # argmax key: the returned (capped) logit
 MUSE_ARGMAX_PRECAP = 1      # argmax key: scale * raw, before the cap
 MUSE_MAX_TOP = 64           # alternatives of a row that are returned (score) or given (distill), at most
 MUSE_DTYPE_F32, MUSE_DTYPE_F16, MUSE_DTYPE_BF16 = 0, 1, 2
+MUSE_DTYPE_BLOCKS = 3       # a token table of blocks in the handle's format
 ARGMAX_KEYS = {"capped": MUSE_ARGMAX_CAPPED, "precap": MUSE_ARGMAX_PRECAP}
 
 _lib = None
@@ -139,6 +142,12 @@ def load_library():
     lib.muse_lmhead_distill.argtypes = [vp, vp, i32, i64, i64, vp, vp, i32, i32, vp, f32, vp, vp, i64, vp]
     lib.muse_lmhead_backward.restype = i32
     lib.muse_lmhead_backward.argtypes = [vp, vp, vp, vp, i32, vp, f32, vp, f32, f32, vp, vp, vp]
+    lib.muse_lmhead_embed.restype = i32
+    lib.muse_lmhead_embed.argtypes = [vp, vp, i32, i64, vp, i64, f32, vp, i32, i64, vp]
+    lib.muse_lmhead_embed_backward.restype = i32
+    lib.muse_lmhead_embed_backward.argtypes = [vp, vp, i32, i64, vp, i64, f32, vp, i32, i64, i32, vp, i64, vp]
+    lib.muse_lmhead_embed_backward_workspace.restype = i32
+    lib.muse_lmhead_embed_backward_workspace.argtypes = [vp, i64, ctypes.POINTER(i64)]
     _lib = lib
     return lib
 
@@ -286,6 +295,28 @@ def muse_lmhead_backward(h: int | None, grad_logits: int, logits: int | None, hi
                          grad_gamma: int | None, stream: int | None) -> int:
     return load_library().muse_lmhead_backward(h, grad_logits, logits, hidden, batch, gamma, eps, weights, scale, cap,
                                                grad_hidden, grad_gamma, stream)
+
+
+def muse_lmhead_embed(h: int | None, table: int, table_type: int, table_ld: int, tokens: int, n: int, scale: float,
+                      out: int, out_dtype: int, out_ld: int, stream: int | None) -> int:
+    return load_library().muse_lmhead_embed(h, table, table_type, table_ld, tokens, n, scale, out, out_dtype, out_ld,
+                                            stream)
+
+
+def muse_lmhead_embed_backward(h: int | None, grad: int, dtype: int, grad_ld: int, tokens: int, n: int, scale: float,
+                               grad_table: int, table_dtype: int, table_ld: int, accumulate: int, workspace: int,
+                               workspace_bytes: int, stream: int | None) -> int:
+    return load_library().muse_lmhead_embed_backward(h, grad, dtype, grad_ld, tokens, n, scale, grad_table, table_dtype,
+                                                     table_ld, accumulate, workspace, workspace_bytes, stream)
+
+
+def muse_lmhead_embed_backward_workspace(h: int | None, n: int) -> int:
+    """Bytes of workspace for n positions, or raises MuseError."""
+    v = ctypes.c_int64()
+    st = load_library().muse_lmhead_embed_backward_workspace(h, n, ctypes.byref(v))
+    if st != MUSE_OK:
+        raise MuseError(st, "muse_lmhead_embed_backward_workspace")
+    return v.value
 
 
 _stream_of = None
@@ -533,12 +564,12 @@ class LMHead:
             raise MuseError(st, "muse_lmhead_forward_group_host")
         return outs
 
-    def _rows(self, t, name):
-        """(pointer, MUSE_DTYPE, rows, distance) of a matrix of logits whose rows are contiguous."""
+    def _rows(self, t, name, width=None):
+        """(pointer, MUSE_DTYPE, rows, distance) of a matrix of logits (or of `width` columns) whose rows are contiguous."""
         dtype = _row_dtypes().get(t.dtype)
         if dtype is None or t.get_device() != self.device:
             raise ValueError(f"{name}: need a float32, float16 or bfloat16 tensor on cuda:{self.device}")
-        shape, v = t.shape, self.n_rows
+        shape, v = t.shape, self.n_rows if width is None else width
         if len(shape) != 2 or shape[1] != v:
             raise ValueError(f"{name}: shape {tuple(shape)}, need [n, {v}]")
         n = shape[0]
@@ -684,6 +715,77 @@ class LMHead:
         if st != MUSE_OK:
             raise MuseError(st, "muse_lmhead_backward")
         return grad_hidden, grad_gamma
+
+    def embed(self, tokens, table, scale: float = 1.0, dtype=None, out=None, stream=None):
+        """out [n, k] = scale * table[tokens]: rows of a token table for tokens [n] int32.
+
+        table: the blocks of an [n_rows, k] matrix in the handle's format
+        (uint8, a tied head's own weights among others), or [n_rows, k] f32,
+        f16 or bf16, contiguous rows any distance apart.  A token outside
+        0..n_rows-1 marks a padded position: a row of zeros.  out (rows any
+        distance apart) is made when not given, in `dtype`: the dense table's,
+        or f32.  See muse_lmhead_embed in the C header."""
+        import torch
+        n = tokens.numel()
+        tp = self._check(tokens, "tokens", torch.int32, (n,))
+        if table.dtype == torch.uint8:
+            wp, kind, ld = self._check(table, "table", torch.uint8), MUSE_DTYPE_BLOCKS, 0
+            if table.numel() != self.n_rows * (self.k // 256) * self.block_bytes:
+                raise ValueError("table: wrong number of bytes for this handle")
+        else:
+            wp, kind, rows, ld = self._rows(table, "table", self.k)
+            if rows != self.n_rows:
+                raise ValueError(f"table: shape {tuple(table.shape)}, need [{self.n_rows}, {self.k}]")
+        if out is None:
+            if dtype is None:
+                dtype = torch.float32 if kind == MUSE_DTYPE_BLOCKS else table.dtype
+            out = self._allocator(stream, tokens, table)((n, self.k), dtype=dtype, device=tokens.device)
+        else:
+            self._allocator(stream, tokens, table, out)
+            if dtype is not None and out.dtype != dtype:
+                raise ValueError("out: not of the given dtype")
+        op, otype, rows, old = self._rows(out, "out", self.k)
+        if rows != n:
+            raise ValueError(f"out: shape {tuple(out.shape)}, need [{n}, {self.k}]")
+        st = load_library().muse_lmhead_embed(self.handle, wp, kind, ld, tp, n, scale, op, otype, old,
+                                              self._stream(stream))
+        if st != MUSE_OK:
+            raise MuseError(st, "muse_lmhead_embed")
+        return out
+
+    def embed_backward(self, grad, tokens, scale: float = 1.0, dtype=None, grad_table=None, accumulate: bool = False,
+                       stream=None):
+        """grad_table [n_rows, k]: the gradient by a dense table from grad [n, k] by embed's rows.
+
+        grad: f32, f16 or bf16, contiguous rows any distance apart; tokens [n]
+        int32 and scale as given to embed.  grad_table (rows any distance
+        apart) is made when not given, in `dtype` or grad's; accumulate adds to
+        the one that is given, and then only the rows of tokens that occur are
+        read and written.  The same inputs give the same bits.  See
+        muse_lmhead_embed_backward in the C header."""
+        import torch
+        gp, gtype, n, gld = self._rows(grad, "grad", self.k)
+        tp = self._check(tokens, "tokens", torch.int32, (n,))
+        if grad_table is None:
+            if accumulate:
+                raise ValueError("grad_table: needed to accumulate into")
+            empty = self._allocator(stream, grad, tokens)
+            grad_table = empty((self.n_rows, self.k), dtype=grad.dtype if dtype is None else dtype, device=grad.device)
+        else:
+            empty = self._allocator(stream, grad, tokens, grad_table)
+            if dtype is not None and grad_table.dtype != dtype:
+                raise ValueError("grad_table: not of the given dtype")
+        op, otype, rows, old = self._rows(grad_table, "grad_table", self.k)
+        if rows != self.n_rows:
+            raise ValueError(f"grad_table: shape {tuple(grad_table.shape)}, need [{self.n_rows}, {self.k}]")
+        need = muse_lmhead_embed_backward_workspace(self.handle, n)
+        work = empty((need,), dtype=torch.uint8, device=grad.device)
+        st = load_library().muse_lmhead_embed_backward(self.handle, gp, gtype, gld, tp, n, scale, op, otype, old,
+                                                       1 if accumulate else 0, work.data_ptr(), need,
+                                                       self._stream(stream))
+        if st != MUSE_OK:
+            raise MuseError(st, "muse_lmhead_embed_backward")
+        return grad_table
 
     def set_argmax_key(self, key: str) -> None:
         """"capped" (the returned logit; the default) or "precap" (scale * raw, before the cap)."""

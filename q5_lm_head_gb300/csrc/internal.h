@@ -165,4 +165,45 @@ size_t backward_t_floats(int64_t n_rows, int max_batch);
 size_t backward_misc_floats();
 cudaError_t launch_backward(const BackwardArgs &a);
 
+// Rows of a token table (embed.cu).
+struct EmbedArgs {
+  const void *table;       // table_type 0/1/2: [v][table_ld] f32/f16/bf16; 3: blocks of the handle's format
+  int table_type;
+  bool q4;
+  int64_t v, table_ld;
+  int k;
+  const int32_t *tokens;   // [n]
+  int64_t n;
+  float scale;
+  void *out;               // [n][out_ld], out_dtype
+  int out_dtype;
+  int64_t out_ld;
+  bool vec_in, vec_out;    // rows of table and out lie on 16 bytes
+  cudaStream_t stream;
+};
+cudaError_t launch_embed(const EmbedArgs &a);
+
+// Gradient by the table.
+struct EmbedBackwardArgs {
+  const void *grad;        // [n][grad_ld], dtype
+  int dtype;
+  int64_t n, grad_ld;
+  const int32_t *tokens;   // [n]
+  float scale;
+  void *grad_table;        // [v][table_ld], out_dtype
+  int out_dtype;
+  int64_t v, table_ld;
+  int k;
+  bool accumulate;
+  bool vec_in, vec_out;    // rows of grad and grad_table lie on 16 bytes
+  int num_sms;
+  cudaStream_t stream;
+  // set at the launch: the workspace's parts and the schedule
+  int *count, *order, *sorted;   // valid positions; they and their tokens by (token, position)
+  float *part;             // [chunks][2][k] sums of runs that chunks share
+  int chunk, range;        // sorted positions of a chunk, tokens of a CTA
+};
+size_t embed_backward_bytes(int64_t n, int k);
+cudaError_t launch_embed_backward(EmbedBackwardArgs a, void *workspace);
+
 }  // namespace muse

@@ -641,6 +641,104 @@ int muse_lmhead_backward(muse_lmhead *h, const float *grad_logits, const float *
   return e == cudaSuccess ? MUSE_OK : cuda_fail(e);
 }
 
+namespace {
+
+// A matrix of `rows` rows of h->k values: its row distance, the address of its elements.
+int validate_matrix(const muse_lmhead *h, const void *p, int dtype, int64_t rows, int64_t ld) {
+  if (dtype != MUSE_DTYPE_F32 && dtype != MUSE_DTYPE_F16 && dtype != MUSE_DTYPE_BF16) return MUSE_ERR_VALUE;
+  if (ld < h->k || ld > (int64_t{1} << 60) / (rows > 0 ? rows : 1)) return MUSE_ERR_SHAPE;
+  return aligned(p, dtype == MUSE_DTYPE_F32 ? 4 : 2) ? MUSE_OK : MUSE_ERR_ALIGN;
+}
+
+// Whether all rows of a matrix lie on 16 bytes.
+bool on_vectors(const void *p, int dtype, int64_t ld) {
+  return aligned(p, 16) && ld % (dtype == MUSE_DTYPE_F32 ? 4 : 8) == 0;
+}
+
+constexpr int64_t kMaxPositions = (int64_t{1} << 31) - 1;
+
+}  // namespace
+
+int muse_lmhead_embed(muse_lmhead *h, const void *table, int table_type, int64_t table_ld, const int32_t *tokens,
+                      int64_t n, float scale, void *out, int out_dtype, int64_t out_ld, void *stream) {
+  if (!h) return MUSE_ERR_NULL;
+  if (n < 0 || n > kMaxPositions) return MUSE_ERR_SHAPE;
+  if (!std::isfinite(scale)) return MUSE_ERR_VALUE;
+  if (n > 0 && (!table || !tokens || !out)) return MUSE_ERR_NULL;
+  int st = validate_matrix(h, out, out_dtype, n, out_ld);
+  if (st != MUSE_OK) return st;
+  if (table_type == MUSE_DTYPE_BLOCKS) {
+    if (!aligned(table, 16)) return MUSE_ERR_ALIGN;
+  } else if ((st = validate_matrix(h, table, table_type, h->n_rows, table_ld)) != MUSE_OK) {
+    return st;
+  }
+  if (!aligned(tokens, 4)) return MUSE_ERR_ALIGN;
+  if (n == 0) return MUSE_OK;
+  DeviceGuard g(h->device);
+  if (!g.ok) return MUSE_ERR_DEVICE;
+  muse::EmbedArgs a;
+  a.table = table;
+  a.table_type = table_type;
+  a.q4 = h->format == MUSE_FORMAT_Q4_K;
+  a.v = h->n_rows;
+  a.table_ld = table_ld;
+  a.k = static_cast<int>(h->k);
+  a.tokens = tokens;
+  a.n = n;
+  a.scale = scale;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.out_ld = out_ld;
+  a.vec_in = on_vectors(table, table_type, table_ld);
+  a.vec_out = on_vectors(out, out_dtype, out_ld);
+  a.stream = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = muse::launch_embed(a);
+  return e == cudaSuccess ? MUSE_OK : cuda_fail(e);
+}
+
+int muse_lmhead_embed_backward_workspace(const muse_lmhead *h, int64_t n, int64_t *bytes) {
+  if (!h || !bytes) return MUSE_ERR_NULL;
+  if (n < 0 || n > kMaxPositions - (1 << 20)) return MUSE_ERR_SHAPE;
+  *bytes = static_cast<int64_t>(muse::embed_backward_bytes(n, static_cast<int>(h->k)));
+  return MUSE_OK;
+}
+
+int muse_lmhead_embed_backward(muse_lmhead *h, const void *grad, int dtype, int64_t grad_ld, const int32_t *tokens,
+                               int64_t n, float scale, void *grad_table, int table_dtype, int64_t table_ld,
+                               int accumulate, void *workspace, int64_t workspace_bytes, void *stream) {
+  int64_t need = 0;
+  int st = muse_lmhead_embed_backward_workspace(h, n, &need);
+  if (st != MUSE_OK) return st;
+  if (!std::isfinite(scale) || (accumulate != 0 && accumulate != 1)) return MUSE_ERR_VALUE;
+  if (!grad_table || !workspace || (n > 0 && (!grad || !tokens))) return MUSE_ERR_NULL;
+  if ((st = validate_matrix(h, grad, dtype, n, grad_ld)) != MUSE_OK) return st;
+  if ((st = validate_matrix(h, grad_table, table_dtype, h->n_rows, table_ld)) != MUSE_OK) return st;
+  if (!aligned(tokens, 4) || !aligned(workspace, 16)) return MUSE_ERR_ALIGN;
+  if (workspace_bytes < need) return MUSE_ERR_NOMEM;
+  if (n == 0 && accumulate) return MUSE_OK;
+  DeviceGuard g(h->device);
+  if (!g.ok) return MUSE_ERR_DEVICE;
+  muse::EmbedBackwardArgs a = {};
+  a.grad = grad;
+  a.dtype = dtype;
+  a.n = n;
+  a.grad_ld = grad_ld;
+  a.tokens = tokens;
+  a.scale = scale;
+  a.grad_table = grad_table;
+  a.out_dtype = table_dtype;
+  a.v = h->n_rows;
+  a.table_ld = table_ld;
+  a.k = static_cast<int>(h->k);
+  a.accumulate = accumulate != 0;
+  a.vec_in = on_vectors(grad, dtype, grad_ld);
+  a.vec_out = on_vectors(grad_table, table_dtype, table_ld);
+  a.num_sms = h->num_sms;
+  a.stream = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = muse::launch_embed_backward(a, workspace);
+  return e == cudaSuccess ? MUSE_OK : cuda_fail(e);
+}
+
 int muse_lmhead_set_argmax_key(muse_lmhead *h, int key) {
   if (!h) return MUSE_ERR_NULL;
   if (key != MUSE_ARGMAX_CAPPED && key != MUSE_ARGMAX_PRECAP) return MUSE_ERR_VALUE;
