@@ -419,6 +419,63 @@ int muse_lmhead_backward(muse_lmhead *h, const float *grad_logits, const float *
                          int batch, const float *gamma, float eps, const void *weights, float scale, float cap,
                          float *grad_hidden, float *grad_gamma, void *stream);
 
+/*
+ * How muse_lmhead_sample draws: for each setting a device array of n values, or
+ * NULL for the same value in every row.
+ *   temperature  2^-20 .. 2^20, or 0 for the first of the largest logits.
+ *   top_k        at most this many; 0 or less, or n_rows and more: no limit.
+ *   top_p        the share of the mass to keep; 1 and more: all of it; 0 and less: one token.
+ *   min_p        the least probability as a share of the largest one; 0 and less:
+ *                none; 1 and more: the largest ones.
+ */
+typedef struct muse_sampling {
+  float temperature;
+  int32_t top_k;
+  float top_p;
+  float min_p;
+  const float *temperatures;
+  const int32_t *top_ks;
+  const float *top_ps;
+  const float *min_ps;
+} muse_sampling;
+
+/*
+ * The next token of each of n rows of finished logits, drawn from a given uniform
+ * number.  For row x of n_rows values, z = x / temperature, in the order (x
+ * descending, index ascending; 0 and -0 are equal):
+ *     top-k   keeps the first top_k values
+ *     top-p   of what top-k left those before which less than top_p of its mass lies
+ *     min-p   those with z - max z >= log(min_p)
+ *     token   = lowest kept i with  sum_{j <= i, kept} exp(z_j) > u * sum_{kept} exp(z_j)
+ *     logprob = z_token - log sum_{kept} exp(z_j), 0 at temperature 0
+ * The filters' borders and the token come from sums in whole numbers of 2^-38 of
+ * the largest weight's power of two (a weight is off by about 2^-35 of itself), so
+ * equal logits are drawn alike and the sums' order changes nothing.  A weight below
+ * 2^-42 of the largest is 0.
+ *   logits   device rows as for muse_lmhead_score.
+ *   n        0 .. 2^31-1 rows, not bound by max_batch; 0 does nothing.
+ *   how      host struct; read before the call returns, its arrays when it runs.
+ *   uniforms [n] f32, device: u; below 0 or NaN counts as 0, 1 and more draws the
+ *            last kept token.
+ *   tokens   [n] int32, device.  logprobs: [n] f32, device, or NULL.
+ * A logit of -infinity is a masked one.  A row of nothing else has token -1 and
+ * logprob -infinity; a row with a NaN or +infinity, or whose setting is a NaN or
+ * a temperature outside its range, token -1 and logprob NaN.  Uses no workspace:
+ * calls may overlap.  One launch.
+ */
+int muse_lmhead_sample(muse_lmhead *h, const void *logits, int dtype, int64_t n, int64_t ld, const muse_sampling *how,
+                       const float *uniforms, int32_t *tokens, float *logprobs, void *stream);
+
+/*
+ * muse_lmhead_forward followed by muse_lmhead_sample of its logits, on `stream`:
+ * arguments as for the two (no argmax: it is the token of temperature 0).
+ * logits [batch][n_rows] f32 is written as by the forward; uniforms, tokens and
+ * logprobs [batch].
+ */
+int muse_lmhead_forward_sample(muse_lmhead *h, const float *hidden, int batch, const float *gamma, float eps,
+                               const void *weights, float scale, float cap, float *logits, const muse_sampling *how,
+                               const float *uniforms, int32_t *tokens, float *logprobs, void *stream);
+
 /* A token table whose rows are the blocks of the handle's format (muse_lmhead_embed). */
 #define MUSE_DTYPE_BLOCKS 3
 

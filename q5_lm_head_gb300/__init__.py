@@ -28,6 +28,7 @@ __all__ = [
     "muse_lmhead_set_argmax_key", "MUSE_ARGMAX_CAPPED", "MUSE_ARGMAX_PRECAP",
     "muse_lmhead_score", "muse_lmhead_forward_score", "muse_lmhead_distill", "muse_lmhead_backward", "MUSE_MAX_TOP",
     "muse_lmhead_embed", "muse_lmhead_embed_backward", "muse_lmhead_embed_backward_workspace",
+    "muse_lmhead_sample", "muse_lmhead_forward_sample", "MuseSampling",
     "EXPORTED_SYMBOLS",
     "LOGIT_SCALE", "SOFTCAP", "RMS_EPS",
 ]
@@ -52,6 +53,7 @@ EXPORTED_SYMBOLS = (
     "muse_lmhead_clear_device_status", "muse_lmhead_selftest_wait_timeout", "muse_lmhead_set_argmax_key",
     "muse_lmhead_score", "muse_lmhead_forward_score", "muse_lmhead_distill", "muse_lmhead_backward",
     "muse_lmhead_embed", "muse_lmhead_embed_backward", "muse_lmhead_embed_backward_workspace",
+    "muse_lmhead_sample", "muse_lmhead_forward_sample",
 )
 
 MUSE_OK = 0
@@ -76,6 +78,13 @@ class MuseGemvSegment(ctypes.Structure):
     """struct muse_gemv_segment of the C header: one matrix of a grouped forward."""
     _fields_ = [("weights", ctypes.c_void_p), ("n_rows", ctypes.c_int64), ("out", ctypes.c_void_p),
                 ("scale", ctypes.c_float), ("cap", ctypes.c_float)]
+
+
+class MuseSampling(ctypes.Structure):
+    """struct muse_sampling of the C header: a value of each setting, or a device array of one a row."""
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int32), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("temperatures", ctypes.c_void_p), ("top_ks", ctypes.c_void_p),
+                ("top_ps", ctypes.c_void_p), ("min_ps", ctypes.c_void_p)]
 
 
 class MuseError(RuntimeError):
@@ -142,6 +151,11 @@ def load_library():
     lib.muse_lmhead_distill.argtypes = [vp, vp, i32, i64, i64, vp, vp, i32, i32, vp, f32, vp, vp, i64, vp]
     lib.muse_lmhead_backward.restype = i32
     lib.muse_lmhead_backward.argtypes = [vp, vp, vp, vp, i32, vp, f32, vp, f32, f32, vp, vp, vp]
+    how = ctypes.POINTER(MuseSampling)
+    lib.muse_lmhead_sample.restype = i32
+    lib.muse_lmhead_sample.argtypes = [vp, vp, i32, i64, i64, how, vp, vp, vp, vp]
+    lib.muse_lmhead_forward_sample.restype = i32
+    lib.muse_lmhead_forward_sample.argtypes = [vp, vp, i32, vp, f32, vp, f32, f32, vp, how, vp, vp, vp, vp]
     lib.muse_lmhead_embed.restype = i32
     lib.muse_lmhead_embed.argtypes = [vp, vp, i32, i64, vp, i64, f32, vp, i32, i64, vp]
     lib.muse_lmhead_embed_backward.restype = i32
@@ -295,6 +309,18 @@ def muse_lmhead_backward(h: int | None, grad_logits: int, logits: int | None, hi
                          grad_gamma: int | None, stream: int | None) -> int:
     return load_library().muse_lmhead_backward(h, grad_logits, logits, hidden, batch, gamma, eps, weights, scale, cap,
                                                grad_hidden, grad_gamma, stream)
+
+
+def muse_lmhead_sample(h: int | None, logits: int, dtype: int, n: int, ld: int, how: MuseSampling | None,
+                       uniforms: int, tokens: int, logprobs: int | None, stream: int | None) -> int:
+    return load_library().muse_lmhead_sample(h, logits, dtype, n, ld, how, uniforms, tokens, logprobs, stream)
+
+
+def muse_lmhead_forward_sample(h: int | None, hidden: int, batch: int, gamma: int | None, eps: float, weights: int,
+                               scale: float, cap: float, logits: int, how: MuseSampling | None, uniforms: int,
+                               tokens: int, logprobs: int | None, stream: int | None) -> int:
+    return load_library().muse_lmhead_forward_sample(h, hidden, batch, gamma, eps, weights, scale, cap, logits, how,
+                                                     uniforms, tokens, logprobs, stream)
 
 
 def muse_lmhead_embed(h: int | None, table: int, table_type: int, table_ld: int, tokens: int, n: int, scale: float,
@@ -715,6 +741,81 @@ class LMHead:
         if st != MUSE_OK:
             raise MuseError(st, "muse_lmhead_backward")
         return grad_hidden, grad_gamma
+
+    def _sampling(self, n, temperature, top_k, top_p, min_p):
+        """MuseSampling of settings that are numbers or tensors [n]."""
+        import torch
+        how = MuseSampling(1.0, 0, 1.0, 0.0)
+        if isinstance(temperature, torch.Tensor):
+            how.temperatures = self._check(temperature, "temperature", torch.float32, (n,))
+        else:
+            how.temperature = temperature
+        if isinstance(top_k, torch.Tensor):
+            how.top_ks = self._check(top_k, "top_k", torch.int32, (n,))
+        else:
+            how.top_k = max(0, min(int(top_k), self.n_rows))
+        if isinstance(top_p, torch.Tensor):
+            how.top_ps = self._check(top_p, "top_p", torch.float32, (n,))
+        else:
+            how.top_p = top_p
+        if isinstance(min_p, torch.Tensor):
+            how.min_ps = self._check(min_p, "min_p", torch.float32, (n,))
+        else:
+            how.min_p = min_p
+        return how
+
+    def sample(self, logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=None):
+        """(tokens [n] int32, logprobs [n] f32): the next token of each row, drawn from uniforms [n] f32 in 0..1.
+
+        logits [n, n_rows] as for score.  temperature (0: the first of the
+        largest logits), top_k (0: off), top_p (1: off) and min_p (0: off) are
+        numbers, or tensors [n] on the device (f32, top_k int32) with a setting
+        for each row.  The filters apply in this order; logprobs are those that
+        the tokens were drawn with, over what the filters left.  A row of
+        nothing but masked logits has token -1.  See muse_lmhead_sample in the C header."""
+        import torch
+        if logits.dim() == 1:
+            logits = logits.unsqueeze(0)
+        ptr, dtype, n, ld = self._rows(logits, "logits")
+        up = self._check(uniforms, "uniforms", torch.float32, (n,))
+        how = self._sampling(n, temperature, top_k, top_p, min_p)
+        empty = self._allocator(stream, logits, uniforms, *(s for s in (temperature, top_k, top_p, min_p)
+                                                            if isinstance(s, torch.Tensor)))
+        tokens = empty((n,), dtype=torch.int32, device=logits.device)
+        logprobs = empty((n,), dtype=torch.float32, device=logits.device)
+        st = load_library().muse_lmhead_sample(self.handle, ptr, dtype, n, ld, how, up, tokens.data_ptr(),
+                                               logprobs.data_ptr(), self._stream(stream))
+        if st != MUSE_OK:
+            raise MuseError(st, "muse_lmhead_sample")
+        return tokens, logprobs
+
+    def forward_sample(self, hidden, weights, uniforms, gamma=None, eps: float = RMS_EPS, scale: float = LOGIT_SCALE,
+                       cap: float = SOFTCAP, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, logits=None, stream=None):
+        """(logits [B, n_rows], tokens [B], logprobs [B]): the forward, and the next tokens drawn from its logits."""
+        import torch
+        if hidden.dim() == 1:
+            hidden = hidden.unsqueeze(0)
+        b = hidden.shape[0]
+        hp = self._check(hidden, "hidden", torch.float32, (b, self.k))
+        wp = self._check(weights, "weights", torch.uint8)
+        if weights.numel() != self.n_rows * (self.k // 256) * self.block_bytes:
+            raise ValueError("weights: wrong number of bytes for this handle")
+        gp = None if gamma is None else self._check(gamma, "gamma", torch.float32, (self.k,))
+        up = self._check(uniforms, "uniforms", torch.float32, (b,))
+        how = self._sampling(b, temperature, top_k, top_p, min_p)
+        empty = self._allocator(stream, hidden, weights, gamma, logits, uniforms,
+                                *(s for s in (temperature, top_k, top_p, min_p) if isinstance(s, torch.Tensor)))
+        if logits is None:
+            logits = empty((b, self.n_rows), dtype=torch.float32, device=hidden.device)
+        lp = self._check(logits, "logits", torch.float32, (b, self.n_rows))
+        tokens = empty((b,), dtype=torch.int32, device=hidden.device)
+        logprobs = empty((b,), dtype=torch.float32, device=hidden.device)
+        st = load_library().muse_lmhead_forward_sample(self.handle, hp, b, gp, float(eps), wp, float(scale), float(cap),
+                                                       lp, how, up, tokens.data_ptr(), logprobs.data_ptr(),
+                                                       self._stream(stream))
+        if st != MUSE_OK:
+            raise MuseError(st, "muse_lmhead_forward_sample")
+        return logits, tokens, logprobs
 
     def embed(self, tokens, table, scale: float = 1.0, dtype=None, out=None, stream=None):
         """out [n, k] = scale * table[tokens]: rows of a token table for tokens [n] int32.

@@ -165,6 +165,23 @@ size_t backward_t_floats(int64_t n_rows, int max_batch);
 size_t backward_misc_floats();
 cudaError_t launch_backward(const BackwardArgs &a);
 
+// The next token of rows of logits as above (sample.cu).  Settings: an array [n] each, or the value beside it.
+struct SampleArgs {
+  const void *logits;
+  int dtype;
+  int64_t n, ld, v;
+  float temperature, top_p, min_p;
+  int top_k;
+  const float *temperatures, *top_ps, *min_ps;
+  const int32_t *top_ks;
+  const float *uniforms;   // [n]
+  int32_t *tokens;         // [n]
+  float *logprobs;         // [n] or nullptr
+  int num_sms;
+  cudaStream_t stream;
+};
+cudaError_t launch_sample(const SampleArgs &a);
+
 // Rows of a token table (embed.cu).
 struct EmbedArgs {
   const void *table;       // table_type 0/1/2: [v][table_ld] f32/f16/bf16; 3: blocks of the handle's format

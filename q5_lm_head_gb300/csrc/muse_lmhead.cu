@@ -643,6 +643,75 @@ int muse_lmhead_backward(muse_lmhead *h, const float *grad_logits, const float *
 
 namespace {
 
+int validate_sample(const muse_lmhead *h, int64_t n, const muse_sampling *how, const float *uniforms,
+                    const int32_t *tokens, const float *logprobs) {
+  if (!h || !how) return MUSE_ERR_NULL;
+  if (n < 0 || n > (int64_t{1} << 31) - 1) return MUSE_ERR_SHAPE;
+  if (!how->temperatures && how->temperature != 0.0f && !temperature_ok(how->temperature)) return MUSE_ERR_VALUE;
+  if ((!how->top_ps && std::isnan(how->top_p)) || (!how->min_ps && std::isnan(how->min_p))) return MUSE_ERR_VALUE;
+  if (n > 0 && (!uniforms || !tokens)) return MUSE_ERR_NULL;
+  const void *ps[] = {how->temperatures, how->top_ks, how->top_ps, how->min_ps, uniforms, tokens, logprobs};
+  for (const void *p : ps)
+    if (!aligned(p, 4)) return MUSE_ERR_ALIGN;
+  return MUSE_OK;
+}
+
+int run_sample(const muse_lmhead *h, const void *logits, int dtype, int64_t n, int64_t ld, const muse_sampling *how,
+               const float *uniforms, int32_t *tokens, float *logprobs, cudaStream_t stream) {
+  muse::SampleArgs a;
+  a.logits = logits;
+  a.dtype = dtype;
+  a.n = n;
+  a.ld = ld;
+  a.v = h->n_rows;
+  a.temperature = how->temperature;
+  a.top_k = how->top_k;
+  a.top_p = how->top_p;
+  a.min_p = how->min_p;
+  a.temperatures = how->temperatures;
+  a.top_ks = how->top_ks;
+  a.top_ps = how->top_ps;
+  a.min_ps = how->min_ps;
+  a.uniforms = uniforms;
+  a.tokens = tokens;
+  a.logprobs = logprobs;
+  a.num_sms = h->num_sms;
+  a.stream = stream;
+  const cudaError_t e = muse::launch_sample(a);
+  return e == cudaSuccess ? MUSE_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+int muse_lmhead_sample(muse_lmhead *h, const void *logits, int dtype, int64_t n, int64_t ld, const muse_sampling *how,
+                       const float *uniforms, int32_t *tokens, float *logprobs, void *stream) {
+  int st = validate_sample(h, n, how, uniforms, tokens, logprobs);
+  if (st != MUSE_OK) return st;
+  if (!logits && n > 0) return MUSE_ERR_NULL;
+  if ((st = validate_rows(h, logits, dtype, n, ld)) != MUSE_OK) return st;
+  if (n == 0) return MUSE_OK;
+  DeviceGuard g(h->device);
+  if (!g.ok) return MUSE_ERR_DEVICE;
+  return run_sample(h, logits, dtype, n, ld, how, uniforms, tokens, logprobs, static_cast<cudaStream_t>(stream));
+}
+
+int muse_lmhead_forward_sample(muse_lmhead *h, const float *hidden, int batch, const float *gamma, float eps,
+                               const void *weights, float scale, float cap, float *logits, const muse_sampling *how,
+                               const float *uniforms, int32_t *tokens, float *logprobs, void *stream) {
+  int st = validate_forward(h, hidden, batch, gamma, eps, weights, scale, cap, logits, nullptr);
+  if (st != MUSE_OK) return st;
+  if ((st = validate_sample(h, batch, how, uniforms, tokens, logprobs)) != MUSE_OK) return st;
+  if (!aligned(hidden, 16) || !aligned(logits, 16)) return MUSE_ERR_ALIGN;
+  DeviceGuard g(h->device);
+  if (!g.ok) return MUSE_ERR_DEVICE;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = run_forward(h, hidden, batch, gamma, eps, weights, scale, cap, logits, nullptr, s);
+  if (st != MUSE_OK) return st;
+  return run_sample(h, logits, MUSE_DTYPE_F32, batch, h->n_rows, how, uniforms, tokens, logprobs, s);
+}
+
+namespace {
+
 // A matrix of `rows` rows of h->k values: its row distance, the address of its elements.
 int validate_matrix(const muse_lmhead *h, const void *p, int dtype, int64_t rows, int64_t ld) {
   if (dtype != MUSE_DTYPE_F32 && dtype != MUSE_DTYPE_F16 && dtype != MUSE_DTYPE_BF16) return MUSE_ERR_VALUE;
