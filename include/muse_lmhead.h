@@ -521,7 +521,7 @@ int muse_lmhead_embed(muse_lmhead *h, const void *table, int table_type, int64_t
  *               muse_lmhead_embed_backward_workspace gives for n (else
  *               MUSE_ERR_NOMEM); its contents are of no use before or after.  Calls that
  *               may overlap need a workspace each.
- * Up to three launches.
+ * Two launches.
  */
 int muse_lmhead_embed_backward(muse_lmhead *h, const void *grad, int dtype, int64_t grad_ld, const int32_t *tokens,
                                int64_t n, float scale, void *grad_table, int table_dtype, int64_t table_ld,

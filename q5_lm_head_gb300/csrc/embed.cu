@@ -8,9 +8,8 @@
 // of the matrix a token's; products and sums in f32, rounded once to the output's
 // type (sums of one token in the order of their positions).
 //
-// Lookup.  A warp takes 256 columns of a row, one block of a quantised table: a
-// lane's eight consecutive columns lie in one sub-block and are one or two 16-byte
-// vectors of the output.
+// Lookup.  A warp takes 256 columns of a dense row (a lane eight), half a warp a block
+// of a quantised one (a lane 16).
 //
 // Gradient.  The positions are sorted by token first, stable, so that a row of the
 // table is written once, by whoever holds its sum, and the order of the sum is
@@ -18,11 +17,12 @@
 // positions for them twice (counts, then places); a warp has a contiguous share of
 // the positions and a counter for each token of the range, whose prefix sums are
 // the places.  Reading n tokens in every CTA costs n * 4 bytes of L2 against the
-// n * k * 2 bytes of the gradient divided by the number of CTAs, 2 % at most.  It
-// also writes the zeros of rows without a token, whose counts it has.
+// n * k * 2 bytes of the gradient divided by the number of CTAs, 2 % at most.
 // sum_runs_kernel: a warp adds up 256 columns of a chunk of sorted positions and
-// writes the runs of one token that lie inside; a run that goes on leaves a part
-// for each chunk, which join_runs_kernel adds up in order.
+// writes the runs of one token that lie inside.  A run that goes on leaves a part
+// for each of its chunks; the warp that counts in last adds them up in order, so no
+// warp waits for another and the bits do not depend on which that is.  Behind them
+// in the same grid, a warp a row, CTAs write the zeros of rows without a token.
 #include <atomic>
 
 #include "common.cuh"
@@ -35,130 +35,234 @@ namespace {
 constexpr int kTile = 256;                 // columns of a warp: a block
 constexpr int kLane = 8;                   // of a lane
 
+// Eight consecutive values of a lane: one access where rows lie on its size (kWide: 16
+// bytes, of f32 32), two of 16 bytes for other f32 rows on 16 bytes, else value by value.
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, bool vec, float (&o)[kLane]) {
-  if (vec) {
-    if constexpr (sizeof(T) == 4) {
-      const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p)), b = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
-      float lo[4], hi[4];
-      unpack(a, lo, T{});
-      unpack(b, hi, T{});
+struct Lane8 {
+  __align__(16) T v[kLane];
+  __device__ __forceinline__ void load(const T *p, int access) {
+    if (access == kNarrow) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        o[i] = lo[i];
-        o[i + 4] = hi[i];
-      }
+      for (int i = 0; i < kLane; ++i) v[i] = p[i];
+    } else if (sizeof(T) == 2) {
+      *reinterpret_cast<uint4 *>(v) = reinterpret_cast<const uint4 *>(p)[0];
+    } else if (access == kWide) {
+      uint32_t *r = reinterpret_cast<uint32_t *>(v);
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                   : "l"(p));
     } else {
-      unpack(__ldcs(reinterpret_cast<const uint4 *>(p)), o, T{});
+      reinterpret_cast<uint4 *>(v)[0] = reinterpret_cast<const uint4 *>(p)[0];
+      reinterpret_cast<uint4 *>(v)[sizeof(T) / 4] = reinterpret_cast<const uint4 *>(p)[1];
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kLane; ++i) o[i] = to_float(p[i]);
   }
-}
+  __device__ __forceinline__ void store(T *p, int access) const {
+    if (access == kNarrow) {
+#pragma unroll
+      for (int i = 0; i < kLane; ++i) p[i] = v[i];
+    } else if (sizeof(T) == 2) {
+      *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(v);
+    } else if (access == kWide) {
+      const uint32_t *r = reinterpret_cast<const uint32_t *>(v);
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                   "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                   : "memory");
+    } else {
+      reinterpret_cast<uint4 *>(p)[0] = reinterpret_cast<const uint4 *>(v)[0];
+      reinterpret_cast<uint4 *>(p)[1] = reinterpret_cast<const uint4 *>(v)[sizeof(T) / 4];
+    }
+  }
+  __device__ __forceinline__ void values(int, float (&o)[kLane]) const {
+#pragma unroll
+    for (int i = 0; i < kLane; ++i) o[i] = to_float(v[i]);
+  }
+};
 
 template <typename T>
-__device__ __forceinline__ void store8(T *p, bool vec, const float (&o)[kLane]) {
-  if (vec) {
-    if constexpr (sizeof(T) == 4) {
-      float4 *q = reinterpret_cast<float4 *>(p);
-      q[0] = make_float4(o[0], o[1], o[2], o[3]);
-      q[1] = make_float4(o[4], o[5], o[6], o[7]);
-    } else {
-      *reinterpret_cast<uint4 *>(p) = pack_vec(o, T{});
-    }
+__device__ __forceinline__ void load8(const T *p, int access, float (&o)[kLane]) {
+  Lane8<T> r;
+  r.load(p, access);
+  r.values(0, o);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T *p, int access, const float (&o)[kLane]) {
+  Lane8<T> r;
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4 *>(r.v) = pack_vec(o, T{});
   } else {
 #pragma unroll
-    for (int i = 0; i < kLane; ++i) p[i] = from_float<T>(o[i]);
+    for (int i = 0; i < kLane; ++i) r.v[i] = o[i];
   }
+  r.store(p, access);
 }
 
-// Values 8 lane .. 8 lane + 7 of a block: one sub-block's.  The products are exact in
-// f32 (11 + 6 + 5 bits), so each value is rounded once.
+// A block's 16 values of a lane of 16: eight bytes' low nibbles (one sub-block) and
+// their high ones (the next).  Quants become floats as the last bits of 2^23 + q
+// (a conversion instruction takes as long as all of the rest).  The products are exact
+// in f32 (11 + 6 + 5 bits), so each value is rounded once.
 template <bool kQ4>
-__device__ __forceinline__ void block8(const uint8_t *block, int lane, float (&o)[kLane]) {
-  const uint4 head = *reinterpret_cast<const uint4 *>(block);
-  const float2 d = __half22float2(*reinterpret_cast<const __half2 *>(&head.x));
-  const int s = lane >> 2, at = (lane & 3) * 8;
-  int sc, m;
-  q5k_scale_min(head.y, head.z, head.w, s, sc, m);
-  const uint2 low = *reinterpret_cast<const uint2 *>(block + (kQ4 ? kOffQsQ4 : kOffQs) + (s >> 1) * 32 + at);
-  const uint32_t shift = (s & 1) * 4;
-  uint32_t q[2] = {(low.x >> shift) & 0x0F0F0F0Fu, (low.y >> shift) & 0x0F0F0F0Fu};
-  if constexpr (!kQ4) {
-    const uint2 high = *reinterpret_cast<const uint2 *>(block + kOffQh + at);
-    q[0] |= ((high.x >> s) & 0x01010101u) << 4;
-    q[1] |= ((high.y >> s) & 0x01010101u) << 4;
+struct Block16 {
+  uint4 head;
+  uint2 low, high;
+  __device__ __forceinline__ void load(const uint8_t *block, int part) {
+    head = *reinterpret_cast<const uint4 *>(block);
+    low = *reinterpret_cast<const uint2 *>(block + (kQ4 ? kOffQsQ4 : kOffQs) + part * 8);
+    if constexpr (!kQ4) high = *reinterpret_cast<const uint2 *>(block + kOffQh + (part & 3) * 8);
   }
-  const float ds = d.x * static_cast<float>(sc), dm = d.y * static_cast<float>(m);
+  static __device__ __forceinline__ uint32_t big(uint32_t word, int byte) {   // the bits of 2^23 + that byte
+    return __byte_perm(word, 0x4B000000u, 0x7650 + byte);
+  }
+  __device__ __forceinline__ void values(int part, float scale, float (&o)[2][kLane]) const {
+    const float2 d = __half22float2(*reinterpret_cast<const __half2 *>(&head.x));
+    const int s = (part >> 2) * 2;         // the first of the two sub-blocks
+    // scales and mins of four sub-blocks, a byte each: 0..3, or 4..7 (4 bits there, 2 above those of the first)
+    const bool late = s >= 4;
+    const uint32_t sc = late ? (head.w & 0x0F0F0F0Fu) | ((head.y >> 2) & 0x30303030u) : head.y & 0x3F3F3F3Fu;
+    const uint32_t mn = late ? ((head.w >> 4) & 0x0F0F0F0Fu) | ((head.z >> 2) & 0x30303030u) : head.z & 0x3F3F3F3Fu;
+    const unsigned long long off = pack2(-8388608.0f, -8388608.0f), by = pack2(scale, scale);
 #pragma unroll
-  for (int i = 0; i < kLane; ++i) o[i] = fmaf(ds, static_cast<float>((q[i >> 2] >> (8 * (i & 3))) & 255u), -dm);
-}
+    for (int h = 0; h < 2; ++h) {
+      const float ds = d.x * (__uint_as_float(big(sc, (s & 2) + h)) - 8388608.0f);
+      const float dm = -(d.y * (__uint_as_float(big(mn, (s & 2) + h)) - 8388608.0f));
+      uint32_t q[2] = {(low.x >> (4 * h)) & 0x0F0F0F0Fu, (low.y >> (4 * h)) & 0x0F0F0F0Fu};
+      if constexpr (!kQ4) {                // bit s + h of each byte, to bit 4
+        q[0] |= __funnelshift_l(high.x, high.x, 4 - s - h) & 0x10101010u;
+        q[1] |= __funnelshift_l(high.y, high.y, 4 - s - h) & 0x10101010u;
+      }
+      const unsigned long long ds2 = pack2(ds, ds), dm2 = pack2(dm, dm);
+#pragma unroll
+      for (int i = 0; i < kLane; i += 2) {
+        const unsigned long long x =
+            add2(pack2(__uint_as_float(big(q[i >> 2], i & 3)), __uint_as_float(big(q[i >> 2], (i & 3) + 1))), off);
+        const float2 r = unpack2(mul2(fma2(ds2, x, dm2), by));
+        o[h][i] = r.x;
+        o[h][i + 1] = r.y;
+      }
+    }
+  }
+};
 
-enum class Table { Dense, Q5, Q4 };
-
-template <Table kTable, typename TT, typename TO>
-__global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs a) {
+// Lookup in a dense table.  A warp takes kTiles tiles, all of whose loads are under way before the first is used.
+template <typename TT, typename TO, int kTiles>
+__global__ void __launch_bounds__(256) embed_dense_kernel(const EmbedArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the tokens are complete
   const int lane = threadIdx.x & 31, tiles = a.k / kTile;
-  const int64_t items = a.n * tiles, step = static_cast<int64_t>(gridDim.x) * (blockDim.x / 32);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5); i < items; i += step) {
-    const int64_t t = i / tiles;
-    const int tile = static_cast<int>(i - t * tiles);
-    const int64_t tok = a.tokens[t];
-    float o[kLane];
+  const int64_t items = a.n * tiles, step = static_cast<int64_t>(gridDim.x) * 8 * kTiles;
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * kTiles; i < items; i += step) {
+    int64_t t = i / tiles;
+    int tile = static_cast<int>(i - t * tiles);
+    Lane8<TT> raw[kTiles];
+    int64_t to[kTiles];
+    bool ok[kTiles];
 #pragma unroll
-    for (int j = 0; j < kLane; ++j) o[j] = 0.0f;
-    if (tok >= 0 && tok < a.v) {
-      if constexpr (kTable == Table::Dense) {
-        load8(static_cast<const TT *>(a.table) + tok * a.table_ld + tile * kTile + lane * kLane, a.vec_in, o);
-      } else {
-        constexpr int kBytes = kTable == Table::Q4 ? kBlockBytesQ4 : kBlockBytes;
-        block8<kTable == Table::Q4>(static_cast<const uint8_t *>(a.table) + (tok * tiles + tile) * kBytes, lane, o);
+    for (int j = 0; j < kTiles; ++j) {
+      const bool in = i + j < items;
+      to[j] = in ? t * a.out_ld + tile * kTile + lane * kLane : -1;
+      const int64_t tok = in ? a.tokens[t] : -1;
+      ok[j] = tok >= 0 && tok < a.v;
+      const int64_t from = ok[j] ? tok : 0;             // a padded position reads the first row and leaves it
+      raw[j].load(static_cast<const TT *>(a.table) + from * a.table_ld + tile * kTile + lane * kLane, a.access_in);
+      if (++tile == tiles) {
+        tile = 0;
+        ++t;
       }
-#pragma unroll
-      for (int j = 0; j < kLane; ++j) o[j] *= a.scale;
     }
-    store8(static_cast<TO *>(a.out) + t * a.out_ld + tile * kTile + lane * kLane, a.vec_out, o);
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) {
+      float o[kLane];
+      raw[j].values(lane, o);
+#pragma unroll
+      for (int e = 0; e < kLane; ++e) o[e] = ok[j] ? o[e] * a.scale : 0.0f;
+      if (to[j] >= 0) store8(static_cast<TO *>(a.out) + to[j], a.access_out, o);
+    }
   }
 }
 
-template <Table kTable, typename TT, typename TO>
-cudaError_t launch_embed_t(const EmbedArgs &a) {
-  const int64_t items = a.n * (a.k / kTile), blocks = (items + 7) / 8;
+// Lookup in a table of blocks.  Half a warp takes a block; a CTA kRounds * 16 of them
+// that follow one another, all loads of a warp under way before the first is used.
+template <bool kQ4, typename TO, int kRounds>
+__global__ void __launch_bounds__(256) embed_blocks_kernel(const EmbedArgs a) {
+  constexpr int kBytes = kQ4 ? kBlockBytesQ4 : kBlockBytes;
+  const int part = threadIdx.x & 15, tiles = a.k / kTile;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (16 * kRounds);
+  int64_t t = first / tiles;
+  int tile = static_cast<int>(first - t * tiles) + (threadIdx.x >> 4);
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the tokens are complete
+  Block16<kQ4> raw[kRounds];
+  int64_t to[kRounds];
+  bool ok[kRounds];
+#pragma unroll
+  for (int j = 0; j < kRounds; ++j) {
+    while (tile >= tiles) {
+      tile -= tiles;
+      ++t;
+    }
+    const int64_t tok = t < a.n ? a.tokens[t] : -1;
+    ok[j] = tok >= 0 && tok < a.v;
+    to[j] = t < a.n ? t * a.out_ld + tile * kTile + (part >> 2) * 64 + (part & 3) * 8 : -1;
+    if (ok[j]) raw[j].load(static_cast<const uint8_t *>(a.table) + (tok * tiles + tile) * kBytes, part);
+    tile += 16;
+  }
+#pragma unroll
+  for (int j = 0; j < kRounds; ++j) {
+    float o[2][kLane] = {};
+    if (ok[j]) raw[j].values(part, a.scale, o);
+    if (to[j] >= 0) {
+      store8(static_cast<TO *>(a.out) + to[j], a.access_out, o[0]);
+      store8(static_cast<TO *>(a.out) + to[j] + 32, a.access_out, o[1]);
+    }
+  }
+}
+
+template <typename A>
+cudaError_t launch_after(void (*kernel)(A), int64_t grid, int threads, size_t shared, cudaStream_t stream, A a) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks < (int64_t{1} << 30) ? blocks : int64_t{1} << 30));
-  cfg.blockDim = dim3(256);
-  cfg.stream = a.stream;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = shared;
+  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // may start before the previous grid ends
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, embed_kernel<kTable, TT, TO>, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <Table kTable, typename TT>
-cudaError_t launch_embed_out(const EmbedArgs &a) {
-  if (a.out_dtype == 0) return launch_embed_t<kTable, TT, float>(a);
-  if (a.out_dtype == 1) return launch_embed_t<kTable, TT, __half>(a);
-  return launch_embed_t<kTable, TT, __nv_bfloat16>(a);
+// Four tiles a warp (two rounds of 16 blocks a CTA) where that leaves enough of them, else one.
+template <typename TT, typename TO>
+cudaError_t launch_embed_dense(const EmbedArgs &a) {
+  const int64_t items = a.n * (a.k / kTile), most = int64_t{1} << 30;
+  const bool many = items >= 64 * static_cast<int64_t>(a.num_sms);
+  const int64_t blocks = (items + (many ? 31 : 7)) / (many ? 32 : 8);
+  void (*kernel)(EmbedArgs) = many ? embed_dense_kernel<TT, TO, 4> : embed_dense_kernel<TT, TO, 1>;
+  return launch_after(kernel, blocks < most ? blocks : most, 256, 0, a.stream, a);
+}
+template <bool kQ4, typename TO>
+cudaError_t launch_embed_blocks(const EmbedArgs &a) {
+  const int64_t items = a.n * (a.k / kTile);
+  const bool many = items >= 64 * static_cast<int64_t>(a.num_sms);
+  const int64_t blocks = (items + (many ? 63 : 15)) / (many ? 64 : 16);
+  void (*kernel)(EmbedArgs) = many ? embed_blocks_kernel<kQ4, TO, 4> : embed_blocks_kernel<kQ4, TO, 1>;
+  return launch_after(kernel, blocks, 256, 0, a.stream, a);
+}
+
+template <typename TO>
+cudaError_t launch_embed_to(const EmbedArgs &a) {
+  switch (a.table_type) {
+    case 0: return launch_embed_dense<float, TO>(a);
+    case 1: return launch_embed_dense<__half, TO>(a);
+    case 2: return launch_embed_dense<__nv_bfloat16, TO>(a);
+    default: return a.q4 ? launch_embed_blocks<true, TO>(a) : launch_embed_blocks<false, TO>(a);
+  }
 }
 
 // ---------------------------------------------------------------- gradient by the table
-constexpr int kOrderThreads = 512;
+constexpr int kOrderThreads = 1024;
 constexpr int kOrderWarps = kOrderThreads / 32;
-constexpr int kMaxRange = 1536;            // tokens of a CTA: 16 counters each, 96 KB
+constexpr int kMaxRange = 1536;            // tokens of a CTA: 32 counters each, 192 KB
 constexpr int kUnroll = 8;                 // positions of a lane in flight
 
-// Zeros of a row of the table by a warp.
-template <typename TO>
-__device__ __forceinline__ void zero_row(TO *row, int k, bool vec, int lane) {
-  const float o[kLane] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j = lane * kLane; j < k; j += kTile) store8(row + j, vec, o);
-}
-
-template <typename TO>
 __global__ void __launch_bounds__(kOrderThreads) token_order_kernel(const EmbedBackwardArgs a) {
   extern __shared__ int s_count[];         // [warps][range]: counts, then places
   __shared__ int s_warp[kOrderWarps], s_below[kOrderWarps];
@@ -189,7 +293,7 @@ __global__ void __launch_bounds__(kOrderThreads) token_order_kernel(const EmbedB
   __syncthreads();
 
   // places: tokens in order, a token's warps in order
-  constexpr int kEach = kMaxRange / kOrderThreads;
+  constexpr int kEach = (kMaxRange + kOrderThreads - 1) / kOrderThreads;
   int total[kEach], sum = 0;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
@@ -226,9 +330,12 @@ __global__ void __launch_bounds__(kOrderThreads) token_order_kernel(const EmbedB
   if (tid == 0 && blockIdx.x == gridDim.x - 1) *a.count = all;
   __syncthreads();
 
-  if (!a.accumulate)
-    for (int t = warp; t < size; t += kOrderWarps)
-      if (s_count[t] < 0) zero_row(static_cast<TO *>(a.grad_table) + (lo + t) * a.table_ld, a.k, a.vec_out, lane);
+  // which rows have a token, and counters of nothing
+  for (int t = warp * 32; t < size; t += kOrderThreads) {
+    const uint32_t used = __ballot_sync(0xffffffffu, t + lane < size && s_count[t + lane] >= 0);
+    if (lane == 0) a.used[(lo + t) / 32] = used;
+  }
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kOrderThreads + tid; i < a.done_n; i += static_cast<int64_t>(gridDim.x) * kOrderThreads) a.done[i] = 0;
 
   __syncthreads();                         // a place is moved on below
   for (int64_t p = p0; p < p1; p += 32 * kUnroll) {
@@ -262,30 +369,83 @@ __device__ __forceinline__ void write_sum(const EmbedBackwardArgs &a, int64_t to
   TO *p = static_cast<TO *>(a.grad_table) + tok * a.table_ld + col;
   float o[kLane];
   if (a.accumulate) {
-    load8(p, a.vec_out, o);
+    load8(p, a.access_out, o);
 #pragma unroll
     for (int i = 0; i < kLane; ++i) o[i] = fmaf(s[i], a.scale, o[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < kLane; ++i) o[i] = s[i] * a.scale;
   }
-  store8(p, a.vec_out, o);
+  store8(p, a.access_out, o);
+}
+
+// Chunks that the run of `tok` reaches into behind `chunk`, which it fills to the end.
+__device__ __forceinline__ int64_t chunks_behind(const EmbedBackwardArgs &a, int64_t chunk, int tok, int count, int lane) {
+  for (int64_t more = 1;; more += 32) {    // until one has another token at its end
+    const int64_t end = (chunk + more + lane + 1) * a.chunk;
+    const uint32_t stop = __ballot_sync(0xffffffffu, end >= count || a.sorted[end] != tok);
+    if (stop) return more + __ffs(stop) - 1;
+  }
+}
+// The chunk in which the run that `chunk` begins with has begun.
+__device__ __forceinline__ int64_t begun_in(const EmbedBackwardArgs &a, int64_t chunk, int tok, int lane) {
+  for (int64_t c = chunk - 1;; c -= 32) {
+    const int64_t at = c - lane;
+    const uint32_t stop = __ballot_sync(0xffffffffu, at <= 0 || a.sorted[at * a.chunk - 1] != tok);
+    if (stop) return c - (__ffs(stop) - 1);
+  }
+}
+
+// After a part of a run of several chunks is stored: the last warp to come adds them up.
+template <typename TO>
+__device__ __forceinline__ void join_run(const EmbedBackwardArgs &a, int64_t chunk, bool head, int tok, int count, int tile) {
+  const int lane = threadIdx.x & 31, tiles = a.k / kTile, col = tile * kTile + lane * kLane;
+  __threadfence();
+  const int64_t from = head ? begun_in(a, chunk, tok, lane) : chunk, more = chunks_behind(a, from, tok, count, lane);
+  int came = 0;
+  __syncwarp();
+  if (lane == 0) came = atomicAdd(a.done + from * tiles + tile, 1);
+  if (__shfl_sync(0xffffffffu, came, 0) != more) return;
+  __threadfence();                         // all parts are there
+  const float *part = a.part + from * 2 * a.k + col;
+  float sum[kLane];
+  load8(part + a.k, kWide, sum);
+  for (int64_t c = 1; c <= more; c += 4) {
+    float v[4][kLane];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (c + u <= more) load8(part + (c + u) * 2 * a.k, kWide, v[u]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (c + u <= more) {
+#pragma unroll
+        for (int i = 0; i < kLane; ++i) sum[i] += v[u][i];
+      }
+  }
+  write_sum<TO>(a, tok, col, sum);
 }
 
 template <typename TG, typename TO>
-__global__ void __launch_bounds__(256) sum_runs_kernel(const EmbedBackwardArgs a) {
+__global__ void __launch_bounds__(256, 3) sum_runs_kernel(const __grid_constant__ const EmbedBackwardArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, tiles = a.k / kTile;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tiles = a.k / kTile;
+  if (blockIdx.x >= a.sum_blocks) {        // rows without a token
+    const int64_t row = static_cast<int64_t>(blockIdx.x - a.sum_blocks) * 8 + warp;
+    if (row >= a.v || ((a.used[row / 32] >> (row % 32)) & 1u)) return;
+    const float o[kLane] = {};
+    TO *p = static_cast<TO *>(a.grad_table) + row * a.table_ld;
+    for (int j = lane * kLane; j < a.k; j += kTile) store8(p + j, a.access_out, o);
+    return;
+  }
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + warp;
   const int64_t chunk = item / tiles;
-  const int col = static_cast<int>(item - chunk * tiles) * kTile + lane * kLane;
+  const int tile = static_cast<int>(item - chunk * tiles), col = tile * kTile + lane * kLane;
   const int count = *a.count;
   const int64_t j0 = chunk * a.chunk;
   if (j0 >= count) return;
   const int64_t j1 = j0 + a.chunk < count ? j0 + a.chunk : count;
   const int before = j0 > 0 ? a.sorted[j0 - 1] : -1, after = j1 < count ? a.sorted[j1] : -1;
   const TG *g = static_cast<const TG *>(a.grad) + col;
-  float *part = a.part + chunk * 2 * a.k + col;
 
   float s[kLane];
 #pragma unroll
@@ -293,20 +453,25 @@ __global__ void __launch_bounds__(256) sum_runs_kernel(const EmbedBackwardArgs a
   int run = -1;
   bool first = true;                       // the run that the chunk begins with
   auto put = [&](int tok, bool last) {
-    if (first && tok == before) store8(part, true, s);
-    else if (last && tok == after) store8(part + a.k, true, s);
-    else write_sum<TO>(a, tok, col, s);
+    const bool head = first && tok == before;
+    if (!head && !(last && tok == after)) {
+      write_sum<TO>(a, tok, col, s);
+      return;
+    }
+    // a part of a run of several chunks: its first chunk's second one, the others' first ones
+    store8(a.part + (chunk * 2 + !head) * a.k + col, kWide, s);
   };
+  constexpr int kFlight = sizeof(TG) == 4 ? 4 : 8;   // positions in flight: 32 registers
   for (int64_t j = j0; j < j1; j += 32) {
     const int many = static_cast<int>(j1 - j < 32 ? j1 - j : 32);
     const int pos = lane < many ? a.order[j + lane] : 0, tok = lane < many ? a.sorted[j + lane] : -1;
-    for (int b = 0; b < many; b += kUnroll) {
-      float v[kUnroll][kLane];
+    for (int b = 0; b < many; b += kFlight) {
+      Lane8<TG> raw[kFlight];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-        if (b + u < many) load8(g + static_cast<int64_t>(__shfl_sync(0xffffffffu, pos, b + u)) * a.grad_ld, a.vec_in, v[u]);
+      for (int u = 0; u < kFlight; ++u)
+        if (b + u < many) raw[u].load(g + static_cast<int64_t>(__shfl_sync(0xffffffffu, pos, b + u)) * a.grad_ld, a.access_in);
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
+      for (int u = 0; u < kFlight; ++u)
         if (b + u < many) {
           const int t = __shfl_sync(0xffffffffu, tok, b + u);
           if (t != run) {
@@ -318,133 +483,105 @@ __global__ void __launch_bounds__(256) sum_runs_kernel(const EmbedBackwardArgs a
             }
             run = t;
           }
+          float v[kLane];
+          raw[u].values(lane, v);
 #pragma unroll
-          for (int i = 0; i < kLane; ++i) s[i] += v[u][i];
+          for (int i = 0; i < kLane; ++i) s[i] += v[i];
         }
     }
   }
   put(run, true);
-}
-
-// The runs that chunks share: by the chunk in which one begins.
-template <typename TO>
-__global__ void __launch_bounds__(256) join_runs_kernel(const EmbedBackwardArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, tiles = a.k / kTile;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t chunk = item / tiles;
-  const int col = static_cast<int>(item - chunk * tiles) * kTile + lane * kLane;
-  const int count = *a.count;
-  const int64_t j0 = chunk * a.chunk, j1 = j0 + a.chunk;
-  if (j1 >= count) return;
-  const int tok = a.sorted[j1];
-  if (a.sorted[j1 - 1] != tok) return;                                     // nothing goes on
-  if (j0 > 0 && a.sorted[j0] == tok && a.sorted[j0 - 1] == tok) return;    // begun before
-  // chunks after this one that the run reaches into: until one has another token at its end
-  int64_t more = 1;
-  for (;; more += 32) {
-    const int64_t end = (chunk + more + lane + 1) * a.chunk;
-    const uint32_t stop = __ballot_sync(0xffffffffu, end >= count || a.sorted[end] != tok);
-    if (stop) {
-      more += __ffs(stop) - 1;
-      break;
-    }
+  const bool whole = first && run == before;   // the chunk is all of one run that began before it
+#pragma unroll 1
+  for (int h = 1; h >= 0; --h) {
+    const int tok = h ? before : after;
+    if (h ? a.sorted[j0] == before : run == after && !whole) join_run<TO>(a, chunk, h, tok, count, tile);
   }
-  const float *part = a.part + chunk * 2 * a.k + col;
-  float s[kLane];
-  load8(part + a.k, true, s);
-  for (int64_t c = 1; c <= more; c += kUnroll) {
-    float v[kUnroll][kLane];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (c + u <= more) load8(part + (c + u) * 2 * a.k, true, v[u]);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (c + u <= more) {
-#pragma unroll
-        for (int i = 0; i < kLane; ++i) s[i] += v[u][i];
-      }
-  }
-  write_sum<TO>(a, tok, col, s);
 }
 
-template <typename... Args>
-cudaError_t launch_after(void (*kernel)(Args...), int64_t grid, int threads, size_t shared, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = shared;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-// Sorted positions of a chunk: at most 1,024 chunks, whose parts stay small beside the gradient.
+// Sorted positions of a chunk: short ones where there are few positions, and at most
+// 1,024 chunks, whose parts stay small beside the gradient.
 int64_t chunk_of(int64_t n) {
-  int64_t c = 16;
+  int64_t c = n <= 2048 ? 8 : n <= 8192 ? 16 : 32;
   while (c * 1024 < n) c *= 2;
   return c;
 }
 
+// The workspace: count, order, sorted [n], used [v / 32], done [chunks][tiles], parts
+// [chunks][2][k], each from 256 bytes on.
+struct BackwardSpace {
+  size_t order, sorted, used, done, part, bytes;
+  int64_t chunk, chunks;
+};
+BackwardSpace backward_space(int64_t n, int64_t v, int k) {
+  auto up = [](int64_t words) { return (static_cast<size_t>(words) * 4 + 255) / 256 * 256; };
+  BackwardSpace s;
+  s.chunk = chunk_of(n);
+  s.chunks = (n + s.chunk - 1) / s.chunk;
+  s.order = 256;
+  s.sorted = s.order + up(n);
+  s.used = s.sorted + up(n);
+  s.done = s.used + up((v + 31) / 32);
+  s.part = s.done + up(s.chunks * (k / kTile));
+  s.bytes = s.part + up(s.chunks * 2 * k);
+  return s;
+}
+
+template <typename TG, typename TO>
+cudaError_t launch_sum_runs(EmbedBackwardArgs a, int64_t chunks) {
+  a.sum_blocks = static_cast<unsigned>((chunks * (a.k / kTile) + 7) / 8);
+  const int64_t zero_blocks = a.accumulate ? 0 : (a.v + 7) / 8;
+  return launch_after(sum_runs_kernel<TG, TO>, a.sum_blocks + zero_blocks, 256, 0, a.stream, a);
+}
+
 template <typename TO>
-cudaError_t launch_embed_backward_t(EmbedBackwardArgs a) {
-  int64_t range = (a.v + a.num_sms - 1) / a.num_sms;
-  a.range = static_cast<int>(range < kMaxRange ? range : kMaxRange);
-  const size_t shared = sizeof(int) * kOrderWarps * a.range;
+cudaError_t launch_sum_runs_to(const EmbedBackwardArgs &a, int64_t chunks) {
+  if (a.dtype == 0) return launch_sum_runs<float, TO>(a, chunks);
+  if (a.dtype == 1) return launch_sum_runs<__half, TO>(a, chunks);
+  return launch_sum_runs<__nv_bfloat16, TO>(a, chunks);
+}
+
+}  // namespace
+
+cudaError_t launch_embed(const EmbedArgs &a) {
+  if (a.out_dtype == 0) return launch_embed_to<float>(a);
+  if (a.out_dtype == 1) return launch_embed_to<__half>(a);
+  return launch_embed_to<__nv_bfloat16>(a);
+}
+
+size_t embed_backward_bytes(int64_t n, int64_t v, int k) { return backward_space(n, v, k).bytes; }
+
+cudaError_t launch_embed_backward(EmbedBackwardArgs a, void *workspace) {
+  const BackwardSpace s = backward_space(a.n, a.v, a.k);
+  uint8_t *w = static_cast<uint8_t *>(workspace);
+  a.count = reinterpret_cast<int *>(w);
+  a.order = reinterpret_cast<int *>(w + s.order);
+  a.sorted = reinterpret_cast<int *>(w + s.sorted);
+  a.used = reinterpret_cast<uint32_t *>(w + s.used);
+  a.done = reinterpret_cast<int *>(w + s.done);
+  a.done_n = s.chunks * (a.k / kTile);
+  a.part = reinterpret_cast<float *>(w + s.part);
+  a.chunk = static_cast<int>(s.chunk);
+  // tokens of a CTA: a share of them, in whole words of `used`
+  const int64_t range = (a.v + a.num_sms - 1) / a.num_sms;
+  a.range = static_cast<int>(range < kMaxRange ? (range + 31) / 32 * 32 : kMaxRange);
   static std::atomic<unsigned long long> configured{0};   // one bit per device; host threads may race here
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(configured.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(token_order_kernel<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(token_order_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(sizeof(int) * kOrderWarps * kMaxRange));
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
-  e = launch_after(token_order_kernel<TO>, (a.v + a.range - 1) / a.range, kOrderThreads, shared, a.stream, a);
-  if (e != cudaSuccess || a.n == 0) return e;
-  const int64_t chunks = (a.n + a.chunk - 1) / a.chunk, grid = (chunks * (a.k / kTile) + 7) / 8;
-  if (a.dtype == 0) e = launch_after(sum_runs_kernel<float, TO>, grid, 256, 0, a.stream, a);
-  else if (a.dtype == 1) e = launch_after(sum_runs_kernel<__half, TO>, grid, 256, 0, a.stream, a);
-  else e = launch_after(sum_runs_kernel<__nv_bfloat16, TO>, grid, 256, 0, a.stream, a);
-  if (e != cudaSuccess || chunks == 1) return e;
-  return launch_after(join_runs_kernel<TO>, grid, 256, 0, a.stream, a);
-}
-
-}  // namespace
-
-cudaError_t launch_embed(const EmbedArgs &a) {
-  switch (a.table_type) {
-    case 0: return launch_embed_out<Table::Dense, float>(a);
-    case 1: return launch_embed_out<Table::Dense, __half>(a);
-    case 2: return launch_embed_out<Table::Dense, __nv_bfloat16>(a);
-    default: return a.q4 ? launch_embed_out<Table::Q4, float>(a) : launch_embed_out<Table::Q5, float>(a);
-  }
-}
-
-// order, sorted [n], count, parts [chunks][2][k], each on 256 bytes
-size_t embed_backward_bytes(int64_t n, int k) {
-  const int64_t c = chunk_of(n), chunks = (n + c - 1) / c;
-  const size_t list = (static_cast<size_t>(n) * 4 + 255) / 256 * 256;
-  return 256 + 2 * list + static_cast<size_t>(chunks) * 2 * k * sizeof(float);
-}
-
-cudaError_t launch_embed_backward(EmbedBackwardArgs a, void *workspace) {
-  const size_t list = (static_cast<size_t>(a.n) * 4 + 255) / 256 * 256;
-  uint8_t *w = static_cast<uint8_t *>(workspace);
-  a.count = reinterpret_cast<int *>(w);
-  a.order = reinterpret_cast<int *>(w + 256);
-  a.sorted = reinterpret_cast<int *>(w + 256 + list);
-  a.part = reinterpret_cast<float *>(w + 256 + 2 * list);
-  a.chunk = static_cast<int>(chunk_of(a.n));
-  if (a.out_dtype == 0) return launch_embed_backward_t<float>(a);
-  if (a.out_dtype == 1) return launch_embed_backward_t<__half>(a);
-  return launch_embed_backward_t<__nv_bfloat16>(a);
+  e = launch_after(token_order_kernel, (a.v + a.range - 1) / a.range, kOrderThreads, sizeof(int) * kOrderWarps * a.range,
+                   a.stream, a);
+  if (e != cudaSuccess) return e;
+  if (a.out_dtype == 0) return launch_sum_runs_to<float>(a, s.chunks);
+  if (a.out_dtype == 1) return launch_sum_runs_to<__half>(a, s.chunks);
+  return launch_sum_runs_to<__nv_bfloat16>(a, s.chunks);
 }
 
 }  // namespace muse

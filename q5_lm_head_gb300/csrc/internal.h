@@ -182,7 +182,9 @@ struct SampleArgs {
 };
 cudaError_t launch_sample(const SampleArgs &a);
 
-// Rows of a token table (embed.cu).
+// Rows of a token table (embed.cu).  How a lane reads and writes eight values of a row: in
+// one access (rows on 16 bytes, of f32 on 32), in two (f32 on 16 bytes), one by one.
+constexpr int kNarrow = 0, kTwice = 1, kWide = 2;
 struct EmbedArgs {
   const void *table;       // table_type 0/1/2: [v][table_ld] f32/f16/bf16; 3: blocks of the handle's format
   int table_type;
@@ -195,7 +197,8 @@ struct EmbedArgs {
   void *out;               // [n][out_ld], out_dtype
   int out_dtype;
   int64_t out_ld;
-  bool vec_in, vec_out;    // rows of table and out lie on 16 bytes
+  int access_in, access_out;   // of rows of table and out
+  int num_sms;
   cudaStream_t stream;
 };
 cudaError_t launch_embed(const EmbedArgs &a);
@@ -212,15 +215,19 @@ struct EmbedBackwardArgs {
   int64_t v, table_ld;
   int k;
   bool accumulate;
-  bool vec_in, vec_out;    // rows of grad and grad_table lie on 16 bytes
+  int access_in, access_out;   // of rows of grad and grad_table
   int num_sms;
   cudaStream_t stream;
   // set at the launch: the workspace's parts and the schedule
   int *count, *order, *sorted;   // valid positions; they and their tokens by (token, position)
+  uint32_t *used;          // [v / 32] which rows have a token
+  int *done;               // [chunks][k / 256] parts of the run that begins in a chunk
+  int64_t done_n;
   float *part;             // [chunks][2][k] sums of runs that chunks share
   int chunk, range;        // sorted positions of a chunk, tokens of a CTA
+  unsigned sum_blocks;
 };
-size_t embed_backward_bytes(int64_t n, int k);
+size_t embed_backward_bytes(int64_t n, int64_t v, int k);
 cudaError_t launch_embed_backward(EmbedBackwardArgs a, void *workspace);
 
 }  // namespace muse

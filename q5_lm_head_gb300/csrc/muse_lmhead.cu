@@ -719,9 +719,11 @@ int validate_matrix(const muse_lmhead *h, const void *p, int dtype, int64_t rows
   return aligned(p, dtype == MUSE_DTYPE_F32 ? 4 : 2) ? MUSE_OK : MUSE_ERR_ALIGN;
 }
 
-// Whether all rows of a matrix lie on 16 bytes.
-bool on_vectors(const void *p, int dtype, int64_t ld) {
-  return aligned(p, 16) && ld % (dtype == MUSE_DTYPE_F32 ? 4 : 8) == 0;
+// How rows of a matrix can be read (internal.h).
+int row_access(const void *p, int dtype, int64_t ld) {
+  auto on = [&](int64_t bytes) { return aligned(p, bytes) && ld * (dtype == MUSE_DTYPE_F32 ? 4 : 2) % bytes == 0; };
+  if (dtype == MUSE_DTYPE_F32) return on(32) ? muse::kWide : on(16) ? muse::kTwice : muse::kNarrow;
+  return on(16) ? muse::kWide : muse::kNarrow;
 }
 
 constexpr int64_t kMaxPositions = (int64_t{1} << 31) - 1;
@@ -758,8 +760,9 @@ int muse_lmhead_embed(muse_lmhead *h, const void *table, int table_type, int64_t
   a.out = out;
   a.out_dtype = out_dtype;
   a.out_ld = out_ld;
-  a.vec_in = on_vectors(table, table_type, table_ld);
-  a.vec_out = on_vectors(out, out_dtype, out_ld);
+  a.access_in = row_access(table, table_type, table_ld);
+  a.access_out = row_access(out, out_dtype, out_ld);
+  a.num_sms = h->num_sms;
   a.stream = static_cast<cudaStream_t>(stream);
   const cudaError_t e = muse::launch_embed(a);
   return e == cudaSuccess ? MUSE_OK : cuda_fail(e);
@@ -768,7 +771,7 @@ int muse_lmhead_embed(muse_lmhead *h, const void *table, int table_type, int64_t
 int muse_lmhead_embed_backward_workspace(const muse_lmhead *h, int64_t n, int64_t *bytes) {
   if (!h || !bytes) return MUSE_ERR_NULL;
   if (n < 0 || n > kMaxPositions - (1 << 20)) return MUSE_ERR_SHAPE;
-  *bytes = static_cast<int64_t>(muse::embed_backward_bytes(n, static_cast<int>(h->k)));
+  *bytes = static_cast<int64_t>(muse::embed_backward_bytes(n, h->n_rows, static_cast<int>(h->k)));
   return MUSE_OK;
 }
 
@@ -800,8 +803,8 @@ int muse_lmhead_embed_backward(muse_lmhead *h, const void *grad, int dtype, int6
   a.table_ld = table_ld;
   a.k = static_cast<int>(h->k);
   a.accumulate = accumulate != 0;
-  a.vec_in = on_vectors(grad, dtype, grad_ld);
-  a.vec_out = on_vectors(grad_table, table_dtype, table_ld);
+  a.access_in = row_access(grad, dtype, grad_ld);
+  a.access_out = row_access(grad_table, table_dtype, table_ld);
   a.num_sms = h->num_sms;
   a.stream = static_cast<cudaStream_t>(stream);
   const cudaError_t e = muse::launch_embed_backward(a, workspace);
