@@ -260,11 +260,11 @@ cudaError_t launch_embed_to(const EmbedArgs &a) {
 // ---------------------------------------------------------------- gradient by the table
 constexpr int kOrderThreads = 1024;
 constexpr int kOrderWarps = kOrderThreads / 32;
-constexpr int kMaxRange = 1536;            // tokens of a CTA: 32 counters each, 192 KB
-constexpr int kUnroll = 8;                 // positions of a lane in flight
+constexpr int kMaxRange = 1536;            // tokens of a CTA: 34 words each, 204 KB
+constexpr int kUnroll = 16;                // positions of a lane in flight
 
 __global__ void __launch_bounds__(kOrderThreads) token_order_kernel(const EmbedBackwardArgs a) {
-  extern __shared__ int s_count[];         // [warps][range]: counts, then places
+  extern __shared__ int s_count[];         // [warps][range]: counts, then places; [range] runs' first places, [range] their ends
   __shared__ int s_warp[kOrderWarps], s_below[kOrderWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, range = a.range;
   const int64_t lo = static_cast<int64_t>(blockIdx.x) * range;
@@ -276,16 +276,21 @@ __global__ void __launch_bounds__(kOrderThreads) token_order_kernel(const EmbedB
   // this warp's positions, a multiple of 32 of them
   const int64_t share = (a.n + kOrderThreads - 1) / kOrderThreads * 32;
   const int64_t p0 = warp * share, p1 = p0 + share < a.n ? p0 + share : a.n;
-  int *mine = s_count + warp * range;
+  const bool once = share <= 32 * kUnroll;   // then the second scan has its tokens still
+  const uint32_t first = static_cast<uint32_t>(lo);
+  int *mine = s_count + warp * range, *s_first = s_count + kOrderWarps * range, *s_end = s_first + range;
   int below = 0;
-  for (int64_t p = p0; p < p1; p += 32 * kUnroll) {
-    int64_t tok[kUnroll];
+  uint32_t tok[kUnroll];                   // a padded position is at least 2^31, beyond every range
+  auto fetch = [&](int64_t p) {
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) tok[j] = p + j * 32 + lane < p1 ? a.tokens[p + j * 32 + lane] : -1;
+    for (int j = 0; j < kUnroll; ++j) tok[j] = p + j * 32 + lane < p1 ? static_cast<uint32_t>(a.tokens[p + j * 32 + lane]) : ~0u;
+  };
+  for (int64_t p = p0; p < p1; p += 32 * kUnroll) {
+    fetch(p);
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
-      below += tok[j] >= 0 && tok[j] < lo;
-      if (tok[j] >= lo && tok[j] < lo + size) atomicAdd(mine + (tok[j] - lo), 1);
+      below += tok[j] < first;
+      if (tok[j] - first < static_cast<uint32_t>(size)) atomicAdd(mine + (tok[j] - first), 1);
     }
   }
   below = __reduce_add_sync(0xffffffffu, below);
@@ -299,8 +304,10 @@ __global__ void __launch_bounds__(kOrderThreads) token_order_kernel(const EmbedB
   for (int e = 0; e < kEach; ++e) {
     const int t = tid * kEach + e;
     total[e] = 0;
-    if (t < size)
+    if (t < size) {
+#pragma unroll
       for (int w = 0; w < kOrderWarps; ++w) total[e] += s_count[w * range + t];
+    }
     sum += total[e];
   }
   int upto = sum;
@@ -320,10 +327,19 @@ __global__ void __launch_bounds__(kOrderThreads) token_order_kernel(const EmbedB
   for (int e = 0; e < kEach; ++e) {
     const int t = tid * kEach + e;
     if (t < size) {
-      for (int w = 0; w < kOrderWarps; ++w) {
-        const int c = s_count[w * range + t];
-        s_count[w * range + t] = total[e] == 0 ? -1 : at;   // -1: a row without a token
-        at += c;
+      s_first[t] = at;
+      s_end[t] = at + total[e];
+      if (total[e] == 0) continue;         // its places are of no use
+#pragma unroll
+      for (int half = 0; half < kOrderWarps; half += 16) {
+        int c[16];
+#pragma unroll
+        for (int w = 0; w < 16; ++w) c[w] = s_count[(half + w) * range + t];
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+          s_count[(half + w) * range + t] = at;
+          at += c[w];
+        }
       }
     }
   }
@@ -332,32 +348,32 @@ __global__ void __launch_bounds__(kOrderThreads) token_order_kernel(const EmbedB
 
   // which rows have a token, and counters of nothing
   for (int t = warp * 32; t < size; t += kOrderThreads) {
-    const uint32_t used = __ballot_sync(0xffffffffu, t + lane < size && s_count[t + lane] >= 0);
+    const uint32_t used = __ballot_sync(0xffffffffu, t + lane < size && s_end[t + lane] > s_first[t + lane]);
     if (lane == 0) a.used[(lo + t) / 32] = used;
   }
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kOrderThreads + tid; i < a.done_n; i += static_cast<int64_t>(gridDim.x) * kOrderThreads) a.done[i] = 0;
 
   __syncthreads();                         // a place is moved on below
   for (int64_t p = p0; p < p1; p += 32 * kUnroll) {
-    int64_t tok[kUnroll];
-#pragma unroll
-    for (int j = 0; j < kUnroll; ++j) tok[j] = p + j * 32 + lane < p1 ? a.tokens[p + j * 32 + lane] : -1;
+    if (!once) fetch(p);
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
-      const bool in = tok[j] >= lo && tok[j] < lo + size;
+      const uint32_t t = tok[j] - first;
+      const bool in = t < static_cast<uint32_t>(size);
       const uint32_t some = __ballot_sync(0xffffffffu, in);
       if (some == 0u) continue;
       int place = 0;
       uint32_t same = 0u;
       if (in) {
-        same = __match_any_sync(some, static_cast<int>(tok[j] - lo));
-        place = mine[tok[j] - lo] + __popc(same & ((1u << lane) - 1u));
+        same = __match_any_sync(some, t);
+        place = mine[t] + __popc(same & ((1u << lane) - 1u));
       }
       __syncwarp();
       if (in) {
-        if (lane == 31 - __clz(same)) mine[tok[j] - lo] = place + 1;
+        if (lane == 31 - __clz(same)) mine[t] = place + 1;
         a.order[place] = static_cast<int>(p + j * 32 + lane);
         a.sorted[place] = static_cast<int>(tok[j]);
+        a.span[place] = make_int2(s_first[t], s_end[t]);
       }
       __syncwarp();
     }
@@ -379,29 +395,12 @@ __device__ __forceinline__ void write_sum(const EmbedBackwardArgs &a, int64_t to
   store8(p, a.access_out, o);
 }
 
-// Chunks that the run of `tok` reaches into behind `chunk`, which it fills to the end.
-__device__ __forceinline__ int64_t chunks_behind(const EmbedBackwardArgs &a, int64_t chunk, int tok, int count, int lane) {
-  for (int64_t more = 1;; more += 32) {    // until one has another token at its end
-    const int64_t end = (chunk + more + lane + 1) * a.chunk;
-    const uint32_t stop = __ballot_sync(0xffffffffu, end >= count || a.sorted[end] != tok);
-    if (stop) return more + __ffs(stop) - 1;
-  }
-}
-// The chunk in which the run that `chunk` begins with has begun.
-__device__ __forceinline__ int64_t begun_in(const EmbedBackwardArgs &a, int64_t chunk, int tok, int lane) {
-  for (int64_t c = chunk - 1;; c -= 32) {
-    const int64_t at = c - lane;
-    const uint32_t stop = __ballot_sync(0xffffffffu, at <= 0 || a.sorted[at * a.chunk - 1] != tok);
-    if (stop) return c - (__ffs(stop) - 1);
-  }
-}
-
 // After a part of a run of several chunks is stored: the last warp to come adds them up.
 template <typename TO>
-__device__ __forceinline__ void join_run(const EmbedBackwardArgs &a, int64_t chunk, bool head, int tok, int count, int tile) {
+__device__ __forceinline__ void join_run(const EmbedBackwardArgs &a, int2 span, int tok, int tile) {
   const int lane = threadIdx.x & 31, tiles = a.k / kTile, col = tile * kTile + lane * kLane;
   __threadfence();
-  const int64_t from = head ? begun_in(a, chunk, tok, lane) : chunk, more = chunks_behind(a, from, tok, count, lane);
+  const int64_t from = span.x / a.chunk, more = (span.y - 1) / a.chunk - from;
   int came = 0;
   __syncwarp();
   if (lane == 0) came = atomicAdd(a.done + from * tiles + tile, 1);
@@ -410,13 +409,14 @@ __device__ __forceinline__ void join_run(const EmbedBackwardArgs &a, int64_t chu
   const float *part = a.part + from * 2 * a.k + col;
   float sum[kLane];
   load8(part + a.k, kWide, sum);
-  for (int64_t c = 1; c <= more; c += 4) {
-    float v[4][kLane];
+  constexpr int kParts = 6;                // in flight
+  for (int64_t c = 1; c <= more; c += kParts) {
+    float v[kParts][kLane];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < kParts; ++u)
       if (c + u <= more) load8(part + (c + u) * 2 * a.k, kWide, v[u]);
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < kParts; ++u)
       if (c + u <= more) {
 #pragma unroll
         for (int i = 0; i < kLane; ++i) sum[i] += v[u][i];
@@ -430,21 +430,28 @@ __global__ void __launch_bounds__(256, 3) sum_runs_kernel(const __grid_constant_
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tiles = a.k / kTile;
   if (blockIdx.x >= a.sum_blocks) {        // rows without a token
-    const int64_t row = static_cast<int64_t>(blockIdx.x - a.sum_blocks) * 8 + warp;
+    const int64_t item = static_cast<int64_t>(blockIdx.x - a.sum_blocks) * 8 + warp, row = item / a.zero_parts;
     if (row >= a.v || ((a.used[row / 32] >> (row % 32)) & 1u)) return;
+    const int part = static_cast<int>(item - row * a.zero_parts);
     const float o[kLane] = {};
-    TO *p = static_cast<TO *>(a.grad_table) + row * a.table_ld;
-    for (int j = lane * kLane; j < a.k; j += kTile) store8(p + j, a.access_out, o);
+    TO *p = static_cast<TO *>(a.grad_table) + row * a.table_ld + lane * kLane;
+    const int end = tiles * (part + 1) / a.zero_parts;
+    for (int j = tiles * part / a.zero_parts; j < end; ++j) store8(p + j * kTile, a.access_out, o);
     return;
   }
   const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + warp;
   const int64_t chunk = item / tiles;
   const int tile = static_cast<int>(item - chunk * tiles), col = tile * kTile + lane * kLane;
+  // all that it needs to know at once: what lies behind the last position is there, but of no use
+  const int64_t j0 = chunk * a.chunk, all = j0 + a.chunk < a.n ? j0 + a.chunk : a.n;
+  if (j0 >= a.n) return;
   const int count = *a.count;
-  const int64_t j0 = chunk * a.chunk;
+  int pos = j0 + lane < all ? a.order[j0 + lane] : 0, tok = j0 + lane < all ? a.sorted[j0 + lane] : -1;
+  const int2 span0 = a.span[j0];
   if (j0 >= count) return;
-  const int64_t j1 = j0 + a.chunk < count ? j0 + a.chunk : count;
-  const int before = j0 > 0 ? a.sorted[j0 - 1] : -1, after = j1 < count ? a.sorted[j1] : -1;
+  const int64_t j1 = all < count ? all : count;
+  const int2 span1 = a.span[j1 - 1];
+  const bool begun = span0.x < j0, goes_on = span1.y > j1;   // runs that other chunks hold a part of
   const TG *g = static_cast<const TG *>(a.grad) + col;
 
   float s[kLane];
@@ -452,19 +459,18 @@ __global__ void __launch_bounds__(256, 3) sum_runs_kernel(const __grid_constant_
   for (int i = 0; i < kLane; ++i) s[i] = 0.0f;
   int run = -1;
   bool first = true;                       // the run that the chunk begins with
-  auto put = [&](int tok, bool last) {
-    const bool head = first && tok == before;
-    if (!head && !(last && tok == after)) {
-      write_sum<TO>(a, tok, col, s);
-      return;
-    }
-    // a part of a run of several chunks: its first chunk's second one, the others' first ones
-    store8(a.part + (chunk * 2 + !head) * a.k + col, kWide, s);
+  auto put = [&](bool last) {              // a part of a run of several chunks: its first chunk's second one, the others' first ones
+    const bool head = first && begun;
+    if (head || (last && goes_on)) store8(a.part + (chunk * 2 + !head) * a.k + col, kWide, s);
+    else write_sum<TO>(a, run, col, s);
   };
   constexpr int kFlight = sizeof(TG) == 4 ? 4 : 8;   // positions in flight: 32 registers
   for (int64_t j = j0; j < j1; j += 32) {
     const int many = static_cast<int>(j1 - j < 32 ? j1 - j : 32);
-    const int pos = lane < many ? a.order[j + lane] : 0, tok = lane < many ? a.sorted[j + lane] : -1;
+    if (j > j0) {
+      pos = lane < many ? a.order[j + lane] : 0;
+      tok = lane < many ? a.sorted[j + lane] : -1;
+    }
     for (int b = 0; b < many; b += kFlight) {
       Lane8<TG> raw[kFlight];
 #pragma unroll
@@ -476,7 +482,7 @@ __global__ void __launch_bounds__(256, 3) sum_runs_kernel(const __grid_constant_
           const int t = __shfl_sync(0xffffffffu, tok, b + u);
           if (t != run) {
             if (run >= 0) {
-              put(run, false);
+              put(false);
               first = false;
 #pragma unroll
               for (int i = 0; i < kLane; ++i) s[i] = 0.0f;
@@ -490,37 +496,34 @@ __global__ void __launch_bounds__(256, 3) sum_runs_kernel(const __grid_constant_
         }
     }
   }
-  put(run, true);
-  const bool whole = first && run == before;   // the chunk is all of one run that began before it
-#pragma unroll 1
-  for (int h = 1; h >= 0; --h) {
-    const int tok = h ? before : after;
-    if (h ? a.sorted[j0] == before : run == after && !whole) join_run<TO>(a, chunk, h, tok, count, tile);
-  }
+  put(true);
+  if (begun) join_run<TO>(a, span0, a.sorted[j0], tile);
+  if (goes_on && !(first && begun)) join_run<TO>(a, span1, run, tile);
 }
 
-// Sorted positions of a chunk: short ones where there are few positions, and at most
-// 1,024 chunks, whose parts stay small beside the gradient.
-int64_t chunk_of(int64_t n) {
-  int64_t c = n <= 2048 ? 8 : n <= 8192 ? 16 : 32;
-  while (c * 1024 < n) c *= 2;
+// Sorted positions of a chunk: few, until there are warps for all SMs; at most 1,024
+// chunks, whose parts stay small beside the gradient.
+int64_t chunk_of(int64_t n, int tiles) {
+  int64_t c = 8;
+  while (c * 1024 < n || n / c * tiles > 16384) c *= 2;
   return c;
 }
 
-// The workspace: count, order, sorted [n], used [v / 32], done [chunks][tiles], parts
+// The workspace: count, order, sorted [n], span [n], used [v / 32], done [chunks][tiles], parts
 // [chunks][2][k], each from 256 bytes on.
 struct BackwardSpace {
-  size_t order, sorted, used, done, part, bytes;
+  size_t order, sorted, span, used, done, part, bytes;
   int64_t chunk, chunks;
 };
 BackwardSpace backward_space(int64_t n, int64_t v, int k) {
   auto up = [](int64_t words) { return (static_cast<size_t>(words) * 4 + 255) / 256 * 256; };
   BackwardSpace s;
-  s.chunk = chunk_of(n);
+  s.chunk = chunk_of(n, k / kTile);
   s.chunks = (n + s.chunk - 1) / s.chunk;
   s.order = 256;
   s.sorted = s.order + up(n);
-  s.used = s.sorted + up(n);
+  s.span = s.sorted + up(n);
+  s.used = s.span + up(2 * n);
   s.done = s.used + up((v + 31) / 32);
   s.part = s.done + up(s.chunks * (k / kTile));
   s.bytes = s.part + up(s.chunks * 2 * k);
@@ -530,7 +533,11 @@ BackwardSpace backward_space(int64_t n, int64_t v, int k) {
 template <typename TG, typename TO>
 cudaError_t launch_sum_runs(EmbedBackwardArgs a, int64_t chunks) {
   a.sum_blocks = static_cast<unsigned>((chunks * (a.k / kTile) + 7) / 8);
-  const int64_t zero_blocks = a.accumulate ? 0 : (a.v + 7) / 8;
+  // a warp zeroes a row, or a part of it where there are few
+  const int tiles = a.k / kTile;
+  a.zero_parts = 1;
+  while (a.zero_parts < tiles && a.v * a.zero_parts < 48 * static_cast<int64_t>(a.num_sms)) a.zero_parts *= 2;
+  const int64_t zero_blocks = a.accumulate ? 0 : (a.v * a.zero_parts + 7) / 8;
   return launch_after(sum_runs_kernel<TG, TO>, a.sum_blocks + zero_blocks, 256, 0, a.stream, a);
 }
 
@@ -557,6 +564,7 @@ cudaError_t launch_embed_backward(EmbedBackwardArgs a, void *workspace) {
   a.count = reinterpret_cast<int *>(w);
   a.order = reinterpret_cast<int *>(w + s.order);
   a.sorted = reinterpret_cast<int *>(w + s.sorted);
+  a.span = reinterpret_cast<int2 *>(w + s.span);
   a.used = reinterpret_cast<uint32_t *>(w + s.used);
   a.done = reinterpret_cast<int *>(w + s.done);
   a.done_n = s.chunks * (a.k / kTile);
@@ -572,11 +580,11 @@ cudaError_t launch_embed_backward(EmbedBackwardArgs a, void *workspace) {
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(configured.load(std::memory_order_acquire) & bit)) {
     e = cudaFuncSetAttribute(token_order_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(sizeof(int) * kOrderWarps * kMaxRange));
+                             static_cast<int>(sizeof(int) * (kOrderWarps + 2) * kMaxRange));
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
-  e = launch_after(token_order_kernel, (a.v + a.range - 1) / a.range, kOrderThreads, sizeof(int) * kOrderWarps * a.range,
+  e = launch_after(token_order_kernel, (a.v + a.range - 1) / a.range, kOrderThreads, sizeof(int) * (kOrderWarps + 2) * a.range,
                    a.stream, a);
   if (e != cudaSuccess) return e;
   if (a.out_dtype == 0) return launch_sum_runs_to<float>(a, s.chunks);

@@ -220,12 +220,14 @@ struct EmbedBackwardArgs {
   cudaStream_t stream;
   // set at the launch: the workspace's parts and the schedule
   int *count, *order, *sorted;   // valid positions; they and their tokens by (token, position)
+  int2 *span;              // [n] first place and end of a place's run
   uint32_t *used;          // [v / 32] which rows have a token
   int *done;               // [chunks][k / 256] parts of the run that begins in a chunk
   int64_t done_n;
   float *part;             // [chunks][2][k] sums of runs that chunks share
   int chunk, range;        // sorted positions of a chunk, tokens of a CTA
   unsigned sum_blocks;
+  int zero_parts;          // warps of a row of zeros
 };
 size_t embed_backward_bytes(int64_t n, int64_t v, int k);
 cudaError_t launch_embed_backward(EmbedBackwardArgs a, void *workspace);
