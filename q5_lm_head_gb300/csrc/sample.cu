@@ -21,10 +21,20 @@
 //
 // Bound: HBM for many rows, latency for a few.  A cluster of CTAs holds a row in its
 // shared memory, each CTA a contiguous share, each warp a contiguous part of that, so
-// that prefix sums over warps and CTAs follow the index.  The thresholds are found
-// by histograms over the ordered bits of the logits (11, 11, 10 bits).  Nothing is
-// kept in global memory, so calls may overlap.  A row that 16 CTAs cannot hold is
-// read again for each pass.
+// that prefix sums over CTAs and warps follow the index.  Passes over the share find
+//   the maximum;
+//   top-k up to 512: the k-th largest of at least k maxima of groups of threads is a
+//     bound that k values reach; what reaches it goes to the first CTA, which does the
+//     rest with these few;
+//   else the row's mass, where the whole of it or top-p wants that;
+//   top-p: a value below (1 - p) of the mean weight cannot be the border; the others go
+//     into a list, and by their distance from the maximum into a histogram of mass; the bin
+//     in which it reaches the share of the mass is handed round and settled value by value;
+//   the kept mass of each CTA, and in the one where the number falls, of its warps,
+//     sixteenths of the warp's part, and values.
+// What does not fit the lists (equal logits, wide borders) is selected by histograms over the
+// ordered bits of the logits, 10 bits at a time.  Nothing is kept in global memory,
+// so calls may overlap.  A row that 16 CTAs cannot hold is read again for each pass.
 #include <atomic>
 
 #include "common.cuh"
@@ -34,11 +44,14 @@
 namespace muse {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kCluster = 16;
-constexpr int kBins = 2048;
-constexpr int kHeldTwo = 72 * 1024;      // bytes of a row in a CTA: two CTAs an SM
-constexpr int kHeldOne = 184 * 1024;     // one CTA an SM
+constexpr int kBins = 1024;
+constexpr int kFew = 512;                // values settled one by one
+constexpr int kBand = 2048;              // listed values of a CTA
+constexpr int kGroups = 1024;            // maxima of groups
+constexpr int kHeldTwo = 56 * 1024;      // bytes of a row in a CTA: two CTAs an SM
+constexpr int kHeldOne = 168 * 1024;     // one CTA an SM
 
 constexpr int kSteps = 512;              // table: 2^(i / 512)
 constexpr int kFraction = 38;            // fractional bits of a weight
@@ -148,23 +161,32 @@ __device__ __forceinline__ float max_nan(float a, float b) {     // a NaN stays
 struct Cross {
   unsigned long long mass;               // before the bin
   uint32_t count, bin;
+  uint32_t in, place;                    // values in the bin; of the CTAs before this one
 };
 
 struct Shared {
   float2 table[kSteps];
-  uint32_t count[kBins], low[kBins], high[kBins];   // histogram: elements, their weights' sum in two words
+  uint32_t count[kBins], low[kBins], high[kBins];   // histogram: values, their weights' sum in two words
+  unsigned long long mass[kBins];        // of the cluster, this CTA's slice; top-k's values, of all CTAs
+  uint32_t number[kBins];
+  float queue[kWarps][64];               // values on their way to the histogram
+  float band[kBand];                     // those that have been there
+  float few[kFew];                       // values to settle one by one, their weights, their indices
+  unsigned long long few_mass[kFew];
+  uint32_t few_at[kFew];
+  float group[kGroups];                  // of the cluster
   Weigher w;
-  float row_max[kWarps];
+  double least_off, inv_t;               // T log(min_p), 1 / T
+  float bound, least;                    // of top-k, min-p
+  int n, few_n;                          // listed
   unsigned long long warp_mass[kWarps];
   uint32_t warp_count[kWarps];
+  float edge;                            // settled: the threshold, how many of its equals
+  unsigned long long ties;
   Cross cross;
   // from the cluster's CTAs
-  float from_max[kCluster];
-  unsigned long long from_total[kCluster];
-  unsigned long long slice_mass[kCluster];
-  uint32_t slice_count[kCluster];
-  unsigned long long from_mass[kCluster];
-  uint32_t from_ties[kCluster];
+  unsigned long long from_total[kCluster], slice_mass[kCluster], from_mass[kCluster];
+  uint32_t slice_count[kCluster], from_ties[kCluster], from_n[kCluster];
 };
 
 __device__ __forceinline__ uint32_t peer_load32(uint32_t a) {
@@ -179,6 +201,17 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
   return v;
 }
 
+// Sum over the CTA; `out` [kWarps] is free again after the next barrier.
+__device__ __forceinline__ unsigned long long block_sum(unsigned long long v, unsigned long long *out) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) out[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0ull;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) v += out[i];
+  return v;
+}
+
 // Adds a weight to a bin: two 32-bit sums with the carry.
 __device__ __forceinline__ void add_mass(Shared &sh, uint32_t bin, unsigned long long w) {
   const uint32_t lo = static_cast<uint32_t>(w);
@@ -188,28 +221,38 @@ __device__ __forceinline__ void add_mass(Shared &sh, uint32_t bin, unsigned long
   if (hi) atomicAdd(&sh.high[bin], hi);
 }
 
-// The first bin at which the cluster's histograms reach `target` (elements, or
-// mass when by_mass), in every CTA; false when they do not.  Each CTA adds up a slice of the bins.
+// The first bin at which the cluster's histograms reach `target` (values, or mass
+// when by_mass), in every CTA; false when they do not.  Each CTA adds up a slice of
+// the bins, a thread a bin of a CTA.
 __device__ __forceinline__ bool find_cross(Shared &sh, bool by_mass, unsigned long long target, Cross &out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cr = cluster_rank(), cs = cluster_size(), slice = kBins / cs;
-  const int per = slice > kThreads ? slice / kThreads : 1;
   cluster_sync();                         // the histograms are complete
-  constexpr int kMost = kBins / kThreads;
-  unsigned long long mass[kMost], sum = 0ull;
-  uint32_t count[kMost], number = 0u;
 #pragma unroll
-  for (int i = 0; i < kMost; ++i) {
-    mass[i] = 0ull;
-    count[i] = 0u;
-    if (i < per && tid * per < slice) {
-      const int bin = cr * slice + tid * per + i;
-      for (int r = 0; r < cs; ++r) {
-        count[i] += peer_load32(peer_addr(&sh.count[bin], r));
-        mass[i] += (static_cast<unsigned long long>(peer_load32(peer_addr(&sh.high[bin], r))) << 32) +
-                   peer_load32(peer_addr(&sh.low[bin], r));
-      }
+  for (int i = 0; i < kBins / kThreads; ++i) {
+    const int p = tid + i * kThreads, r = p & (cs - 1), bin = p / cs, at = cr * slice + bin;
+    uint32_t count = peer_load32(peer_addr(&sh.count[at], r));
+    unsigned long long mass = (static_cast<unsigned long long>(peer_load32(peer_addr(&sh.high[at], r))) << 32) +
+                              peer_load32(peer_addr(&sh.low[at], r));
+    for (int o = cs >> 1; o > 0; o >>= 1) {
+      count += __shfl_xor_sync(0xffffffffu, count, o);
+      mass += __shfl_xor_sync(0xffffffffu, mass, o);
     }
+    if (r == 0) {
+      sh.number[bin] = count;
+      sh.mass[bin] = mass;
+    }
+  }
+  __syncthreads();
+  constexpr int kEach = kBins / kThreads;   // bins of a thread, with one CTA
+  const int each = slice > kThreads ? slice / kThreads : 1;
+  unsigned long long mass[kEach], sum = 0ull;
+  uint32_t count[kEach], number = 0u;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const bool in = i < each && tid * each + i < slice;
+    mass[i] = in ? sh.mass[tid * each + i] : 0ull;
+    count[i] = in ? sh.number[tid * each + i] : 0u;
     sum += mass[i];
     number += count[i];
   }
@@ -256,15 +299,19 @@ __device__ __forceinline__ bool find_cross(Shared &sh, bool by_mass, unsigned lo
   }
   if ((by_mass ? total : total_n) < target) return false;
 #pragma unroll
-  for (int i = 0; i < kMost; ++i) {
-    if (i < per && tid * per < slice) {
-      const unsigned long long b = by_mass ? before : before_n, in = by_mass ? mass[i] : count[i];
-      if (b < target && b + in >= target)
-        for (int r = 0; r < cs; ++r) {
-          peer_store64(peer_addr(&sh.cross.mass, r), before);
-          peer_store32(peer_addr(&sh.cross.count, r), before_n);
-          peer_store32(peer_addr(&sh.cross.bin, r), cr * slice + tid * per + i);
-        }
+  for (int i = 0; i < kEach; ++i) {
+    const unsigned long long b = by_mass ? before : before_n, in = by_mass ? mass[i] : count[i];
+    if (in > 0ull && b < target && b + in >= target) {
+      const int bin = cr * slice + tid * each + i;
+      uint32_t place = 0u;
+      for (int r = 0; r < cs; ++r) {
+        peer_store64(peer_addr(&sh.cross.mass, r), before);
+        peer_store32(peer_addr(&sh.cross.count, r), before_n);
+        peer_store32(peer_addr(&sh.cross.bin, r), bin);
+        peer_store32(peer_addr(&sh.cross.in, r), count[i]);
+        peer_store32(peer_addr(&sh.cross.place, r), place);
+        place += peer_load32(peer_addr(&sh.count[bin], r));
+      }
     }
     before += mass[i];
     before_n += count[i];
@@ -274,8 +321,24 @@ __device__ __forceinline__ bool find_cross(Shared &sh, bool by_mass, unsigned lo
   return true;
 }
 
+// log(total / one) of whole numbers, total >= one: 512ths of the exponent from the
+// table, what is left (below 2^-9) by its series.
+__device__ __forceinline__ double log_ratio(const float2 *table, unsigned long long total, unsigned long long one) {
+  const double r = static_cast<double>(total) / static_cast<double>(one);
+  const int e = static_cast<int>((__double_as_longlong(r) >> 52) & 2047) - 1023;
+  const double man = __longlong_as_double((__double_as_longlong(r) & 0xFFFFFFFFFFFFFll) | 0x3FF0000000000000ll);
+  int i = static_cast<int>(__log2f(static_cast<float>(man)) * kSteps);
+  i = min(max(i, 0), kSteps - 1);
+  const float2 t = table[i];
+  const double d = man - (static_cast<double>(t.x) + t.y);
+  const float f = static_cast<float>(d) / t.x;
+  const double correction = (d - static_cast<double>(f) * (static_cast<double>(t.x) + t.y));   // of the division, in units of t
+  return static_cast<double>(e * kSteps + i) * (0.6931471805599453 / kSteps) +
+         (static_cast<double>(f) + static_cast<double>(fmaf(f * f, fmaf(f, 1.0f / 3.0f, -0.5f), static_cast<float>(correction) / t.x)));
+}
+
 template <typename T, bool kHeld>
-__global__ void __launch_bounds__(kThreads, kHeld ? 2 : 4) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
   constexpr int W = Vec<T>::W;
   extern __shared__ __align__(16) uint8_t held[];
   __shared__ Shared sh;
@@ -291,8 +354,9 @@ __global__ void __launch_bounds__(kThreads, kHeld ? 2 : 4) sample_kernel(const S
   const T *x0 = x - off;
   const int64_t vecs = (off + v + W - 1) / W;
   const int64_t v0 = (vecs * cr) >> cs_log, v1 = (vecs * (cr + 1)) >> cs_log;
-  // this warp's part of this CTA's share
-  const int64_t w0 = v0 + (((v1 - v0) * warp) / kWarps), w1 = v0 + (((v1 - v0) * (warp + 1)) / kWarps);
+  // a warp's part of this CTA's share
+  const auto part_begin = [&](int i) { return v0 + (((v1 - v0) * i) / kWarps); };
+  const int64_t w0 = part_begin(warp), w1 = part_begin(warp + 1);
   uint4 *vec_held = reinterpret_cast<uint4 *>(held);
   const auto whole = [&](int64_t i) { return i * W >= off && (i + 1) * W <= off + v; };
   const auto edge = [&](int64_t i) {      // a vector that the row only begins or ends in
@@ -304,14 +368,20 @@ __global__ void __launch_bounds__(kThreads, kHeld ? 2 : 4) sample_kernel(const S
     }
     return pack_vec(o, T{});
   };
-  const auto load = [&](int64_t i, float (&o)[W]) {
+  const auto load_vec = [&](int64_t i) {
+    if constexpr (kHeld) return vec_held[i - v0];
+    else return whole(i) ? __ldg(reinterpret_cast<const uint4 *>(x0) + i) : edge(i);
+  };
+  const auto value_at = [&](int64_t i, int e) {   // of a vector: -infinity beside the row
     if constexpr (kHeld) {
-      unpack(vec_held[i - v0], o, T{});
+      return to_float(reinterpret_cast<const T *>(vec_held + (i - v0))[e]);
     } else {
-      unpack(whole(i) ? __ldg(reinterpret_cast<const uint4 *>(x0) + i) : edge(i), o, T{});
+      const int64_t at = i * W + e - off;
+      return at >= 0 && at < v ? to_float(x[at]) : -INFINITY;
     }
   };
   for (int i = tid; i < kSteps; i += kThreads) sh.table[i] = kPowers.at[i];
+  if (tid == 0) sh.n = sh.few_n = 0;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the logits and settings are complete
   if constexpr (kHeld) {
@@ -333,29 +403,45 @@ __global__ void __launch_bounds__(kThreads, kHeld ? 2 : 4) sample_kernel(const S
   if (temperature == 0.0f || top_p <= 0.0f) top_k = 1;   // the first
   if (temperature == 0.0f) temperature = 1.0f;
   bad |= !(temperature >= 0x1p-20f && temperature <= 0x1p20f);
-  const bool by_k = top_k > 0 && top_k < v, by_p = top_p < 1.0f && top_p > 0.0f;
+  const bool by_k = top_k > 0 && top_k < v, by_p = top_p < 1.0f && top_p > 0.0f, by_m = min_p > 0.0f;
+  // groups of top-k: as few of the CTA's threads in one as leave top_k groups in the cluster
+  const bool few_k = by_k && top_k <= kFew && top_k <= static_cast<int64_t>(kThreads) * cs;
+  int per_warp = 1;
+  if (few_k)
+    while (kWarps * cs * per_warp < top_k) per_warp *= 2;
+  if (tid == 0) {                         // 64 bits take their time: beside the loads
+    const double c = 1.4426950408889634 / temperature;
+    sh.w.table = sh.table;
+    sh.w.c1 = static_cast<float>(c * kSteps);
+    sh.w.c2 = static_cast<float>(c * kSteps - sh.w.c1);
+    sh.w.c = c;
+    sh.w.drop = v > (int64_t{1} << 24) ? 40 - __clzll(v - 1) : 0;   // bits of v - 1 beyond 24
+    sh.inv_t = 1.0 / temperature;
+    sh.least_off = by_m ? temperature * log(min_p < 1.0f ? static_cast<double>(min_p) : 1.0) : 0.0;
+  }
   if constexpr (kHeld) {
     asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
+    __syncwarp();                         // a warp reads what it has fetched itself
   }
 
-  // the row's maximum; a NaN stays one
+  // the row's maximum, and those of its groups; a NaN stays one
   float m = -INFINITY;
   for (int64_t i = w0 + lane; i < w1; i += 32) {
     float o[W];
-    load(i, o);
+    unpack(load_vec(i), o, T{});
 #pragma unroll
     for (int e = 0; e < W; ++e) m = max_nan(m, o[e]);
   }
+  for (int o = 16; o >= per_warp; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  cluster_wait();                         // every CTA of the cluster has started
+  if (lane < per_warp)
+    for (int r = 0; r < cs; ++r) peer_store32(peer_addr(&sh.group[(cr * kWarps + warp) * per_warp + lane], r), __float_as_uint(m));
+  cluster_sync();
+  const int groups = kWarps * cs * per_warp;
+  m = -INFINITY;
+  for (int i = lane; i < groups; i += 32) m = max_nan(m, sh.group[i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) sh.row_max[warp] = m;
-  __syncthreads();
-  for (int i = 0; i < kWarps; ++i) m = max_nan(m, sh.row_max[i]);
-  cluster_wait();                         // every CTA of the cluster has started
-  if (tid < cs) peer_store32(peer_addr(&sh.from_max[cr], tid), __float_as_uint(m));
-  cluster_sync();
-  for (int i = 0; i < cs; ++i) m = max_nan(m, sh.from_max[i]);
   if (bad || !(fabsf(m) < INFINITY)) {    // settings or logits that are not numbers, an infinity, or nothing at all
     if (cr == 0 && tid == 0) {
       a.tokens[row] = -1;
@@ -363,48 +449,156 @@ __global__ void __launch_bounds__(kThreads, kHeld ? 2 : 4) sample_kernel(const S
     }
     return;
   }
-  if (tid == 0) {
-    const double c = 1.4426950408889634 / temperature;
-    Weigher w;
-    w.table = sh.table;
-    w.c1 = static_cast<float>(c * kSteps);
-    w.c2 = static_cast<float>(c * kSteps - w.c1);
-    w.floor = __double2float_rd(m - kOrders / c);
-    w.wide = !(fmaxf(fabsf(m), fabsf(w.floor)) * w.c1 < 4000000.0f);
-    w.drop = v > (int64_t{1} << 24) ? 40 - __clzll(v - 1) : 0;   // bits of v - 1 beyond 24
-    w.m = m;
-    w.c = c;
-    const uint32_t top = __float_as_uint(fmaf(m, w.c1, kShift)) & ~(kSteps - 1u);
-    w.base = ((127u + kFraction) << 23) - top * (1u << 14);
-    sh.w = w;
-    sh.row_max[0] = min_p > 0.0f ? __double2float_ru(m + temperature * log(min_p < 1.0f ? static_cast<double>(min_p) : 1.0)) : -INFINITY;
+  if (warp == 0) {
+    float bound = -INFINITY;
+    if (few_k) {                          // the largest value (its upper 16 bits) that top_k groups reach
+      uint32_t b = 0u;
+      for (int bit = 31; bit >= 16; --bit) {
+        const uint32_t t = b | (1u << bit);
+        int n = 0;
+        for (int i = lane; i < groups; i += 32) n += float_order_key(sh.group[i]) >= t;
+        if (__reduce_add_sync(0xffffffffu, n) >= top_k) b = t;
+      }
+      bound = b < 0x00800000u ? -INFINITY : order_key_float(b);   // NaNs have no place here, -infinity is masked
+    }
+    if (lane == 0) {
+      sh.w.floor = __fsub_rd(m, __fmul_ru(temperature, kOrders * 0.6931472f));
+      sh.w.wide = !(fmaxf(fabsf(m), fabsf(sh.w.floor)) * sh.w.c1 < 4000000.0f);
+      sh.w.m = m;
+      const uint32_t top = __float_as_uint(fmaf(m, sh.w.c1, kShift)) & ~(kSteps - 1u);
+      sh.w.base = ((127u + kFraction) << 23) - top * (1u << 14);
+      sh.bound = fmaxf(bound, sh.w.floor);
+      sh.least = by_m ? __double2float_ru(m + sh.least_off) : -INFINITY;
+    }
   }
   __syncthreads();
   const Weigher w = sh.w;
-  const float least = sh.row_max[0];      // of min-p
+  const float least = sh.least;
+
+  const auto write = [&](float xi, int64_t index, unsigned long long total) {
+    a.tokens[row] = static_cast<int32_t>(index);
+    if (a.logprobs)
+      a.logprobs[row] = static_cast<float>((static_cast<double>(xi) - m) * sh.inv_t - log_ratio(sh.table, total, weight<kHeld>(w, m)));
+  };
+  const auto drawn = [&](unsigned long long total) {
+    return u >= 1.0f ? total - 1 : u > 0.0f ? part_of(u, total, false) : 0ull;
+  };
+  // the values from `from` up of this warp's part: each(value, index), a few lanes at a time
+  const auto each_from = [&](float from, auto &&each) {
+    for (int64_t i = w0; i < w1; i += 32) {
+      uint32_t some = 0u;
+      if (i + lane < w1) {
+        float o[W];
+        unpack(load_vec(i + lane), o, T{});
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          if (o[e] >= from) some |= 1u << e;
+      }
+      while (__any_sync(0xffffffffu, some != 0u)) {
+        if (some != 0u) {
+          const int e = __ffs(some) - 1;
+          some &= some - 1;
+          each(value_at(i + lane, e), (i + lane) * W + e - off);
+        }
+      }
+    }
+  };
+
+  // top-k: what reaches the bound, to the first CTA
+  if (few_k) {
+    const int room = kBins / cs;
+    const uint32_t to = peer_addr(&sh.mass[cr * room], 0);
+    each_from(sh.bound, [&](float xi, int64_t index) {
+      const int at = atomicAdd(&sh.few_n, 1);
+      if (at < room)
+        peer_store64(to + 8 * at, (static_cast<unsigned long long>(__float_as_uint(xi)) << 32) | static_cast<uint32_t>(index));
+    });
+    __syncthreads();
+    if (tid < cs) peer_store32(peer_addr(&sh.from_n[cr], tid), sh.few_n);
+    cluster_sync();
+    int n = 0;
+    bool fits = true;
+    for (int r = 0; r < cs; ++r) {
+      fits &= sh.from_n[r] <= static_cast<uint32_t>(room);
+      n += sh.from_n[r] <= static_cast<uint32_t>(room) ? static_cast<int>(sh.from_n[r]) : 0;
+    }
+    if (fits && n <= kFew) {
+      if (cr != 0) return;
+      float xi = 0.0f;
+      uint32_t index = 0u;
+      unsigned long long mine = 0ull;
+      if (tid < n) {
+        int r = 0, at = tid;
+        for (; at >= static_cast<int>(sh.from_n[r]); ++r) at -= sh.from_n[r];
+        const unsigned long long entry = sh.mass[r * room + at];
+        xi = __uint_as_float(static_cast<uint32_t>(entry >> 32));
+        index = static_cast<uint32_t>(entry);
+        mine = weight<kHeld>(w, xi);
+        sh.few[tid] = xi;
+        sh.few_at[tid] = index;
+        sh.few_mass[tid] = mine;
+      }
+      __syncthreads();
+      int64_t rank = 0;
+      unsigned long long before = 0ull;
+      if (tid < n)
+        for (int j = 0; j < n; ++j) {
+          const float xj = sh.few[j];
+          if (xj > xi || (xj == xi && sh.few_at[j] < index)) {
+            ++rank;
+            before += sh.few_mass[j];
+          }
+        }
+      bool keep = tid < n && rank < top_k;
+      const unsigned long long all = block_sum(keep ? mine : 0ull, sh.warp_mass);
+      keep = keep && xi >= least && (!by_p || before < part_of(top_p, all, true));
+      if (!keep) mine = 0ull;
+      if (tid < n) sh.few_mass[tid] = mine;
+      const unsigned long long total = block_sum(mine, sh.from_total);
+      static_assert(kCluster >= kWarps, "from_total serves as the CTA's sums");
+      const unsigned long long target = drawn(total);
+      if (mine > 0ull) {
+        before = 0ull;
+        for (int j = 0; j < n; ++j)
+          if (sh.few_at[j] < index) before += sh.few_mass[j];
+        if (before <= target && target < before + mine) write(xi, index, total);
+      }
+      return;
+    }
+  }
 
   // thresholds of top-k and top-p
   float t = least;                        // kept: x > t, and the first `ties` x = t
   unsigned long long ties = ~0ull;
   unsigned long long mass_k = 0ull;       // of what top-k left
+  const auto lower = [&](float edge_x, unsigned long long many) {
+    if (edge_x > t || (edge_x == t && many < ties)) {
+      t = edge_x;
+      ties = many;
+    }
+  };
+  const auto clear = [&]() {
+    for (int i = tid; i < kBins; i += kThreads) sh.count[i] = sh.low[i] = sh.high[i] = 0u;
+    __syncthreads();
+  };
+  // by the ordered bits, 10 at a time
   const auto select = [&](bool by_mass, unsigned long long target, bool want_mass) {
     unsigned long long mass = 0ull;
     uint32_t key = 0u;                    // of ~float_order_key, from the top
 #pragma unroll 1
-    for (int level = 0; level < 3; ++level) {
-      const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
-      const uint32_t mask = level == 2 ? 1023u : 2047u, fixed = level == 0 ? 0u : level == 1 ? ~0u << 21 : ~0u << 10;
-      for (int i = tid; i < kBins; i += kThreads) sh.count[i] = sh.low[i] = sh.high[i] = 0u;
+    for (int level = 0; level < 4; ++level) {
+      const int shift = level < 3 ? 22 - 10 * level : 0;
+      const uint32_t mask = level < 3 ? 1023u : 3u, fixed = level == 0 ? 0u : ~0u << (32 - 10 * level);
       __syncthreads();
+      clear();
       for (int64_t i = w0 + lane; i < w1; i += 32) {
-        float o[W];
-        load(i, o);
-#pragma unroll
+#pragma unroll 1
         for (int e = 0; e < W; ++e) {
-          const uint32_t k = ~float_order_key(o[e]);
-          if (o[e] >= w.floor && (k & fixed) == key) {
-            if (!by_mass) atomicAdd(&sh.count[(k >> shift) & mask], 1u);
-            if (want_mass) add_mass(sh, (k >> shift) & mask, weight<kHeld>(w, o[e]));
+          const float xi = value_at(i, e);
+          const uint32_t k = ~float_order_key(xi);
+          if (xi >= w.floor && (k & fixed) == key) {
+            atomicAdd(&sh.count[(k >> shift) & mask], 1u);
+            if (want_mass) add_mass(sh, (k >> shift) & mask, weight<kHeld>(w, xi));
           }
         }
       }
@@ -418,111 +612,286 @@ __global__ void __launch_bounds__(kThreads, kHeld ? 2 : 4) sample_kernel(const S
     const unsigned long long of_one = weight<kHeld>(w, edge_x);
     const unsigned long long many = by_mass ? (target + of_one - 1) / of_one : target;
     mass_k = mass + many * of_one;
-    if (edge_x > t || (edge_x == t && many < ties)) {
-      t = edge_x;
-      ties = many;
-    }
+    lower(edge_x, many);
     return true;
   };
-  const auto total_mass = [&](float from) {   // of this warp's x >= from
+  // the mass of this warp's part
+  const auto part_mass = [&]() {
     unsigned long long s = 0ull;
-    for (int64_t i = w0 + lane; i < w1; i += 32) {
-      float o[W];
-      load(i, o);
+    if (!kHeld || w.wide) {
+      for (int64_t i = w0 + lane; i < w1; i += 32) {
+#pragma unroll 1
+        for (int e = 0; e < W; ++e) s += weight<kHeld>(w, value_at(i, e));
+      }
+    } else {                              // high parts fit 32 bits: at most 2^17 each, and 336 values a thread
+      uint32_t highs = 0u;
+      long long lows = 0ll;
+      for (int64_t i = w0 + lane; i < w1; i += 32) {
+        float o[W];
+        unpack(load_vec(i), o, T{});
 #pragma unroll
-      for (int e = 0; e < W; ++e)
-        if (o[e] >= from) s += weight<kHeld>(w, o[e]);
+        for (int e = 0; e < W; e += 4) {
+          int low4 = 0;                   // below 2^29 each
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t high;
+            int low;
+            weight_parts(w, o[e + j], high, low);
+            highs += high;
+            low4 += low;
+          }
+          lows += low4;
+        }
+      }
+      s = (static_cast<unsigned long long>(highs) << kRoundBits) + static_cast<unsigned long long>(lows);
     }
     return warp_sum(s);
   };
-  if (by_p || by_k) {
-    bool all = !by_k;
-    if (by_k) all = !select(false, static_cast<unsigned long long>(top_k), by_p);
-    if (by_p) {
-      if (all) {                          // the mass of the whole row
-        const unsigned long long s = total_mass(w.floor);
-        if (lane == 0) sh.warp_mass[warp] = s;
-        __syncthreads();
-        unsigned long long sum = 0ull;
-        for (int i = 0; i < kWarps; ++i) sum += sh.warp_mass[i];
-        if (tid < cs) peer_store64(peer_addr(&sh.from_total[cr], tid), sum);
-        cluster_sync();
-        mass_k = 0ull;
-        for (int i = 0; i < cs; ++i) mass_k += sh.from_total[i];
+  // its values above t, and those equal to it
+  const auto part_kept = [&](int64_t i0, int64_t i1, uint32_t &equal) {
+    unsigned long long s = 0ull;
+    uint32_t n = 0u;
+    for (int64_t i = i0; i < i1; i += 32) {
+      uint32_t some = 0u;
+      if (i + lane < i1) {
+        float o[W];
+        unpack(load_vec(i + lane), o, T{});
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          if (o[e] > t && o[e] >= w.floor) some |= 1u << e;
+          n += o[e] == t;
+        }
       }
-      const unsigned long long need = part_of(top_p, mass_k, true);
-      if (need > 0ull) select(true, need, true);
+      while (__any_sync(0xffffffffu, some != 0u)) {
+        if (some != 0u) {
+          const int e = __ffs(some) - 1;
+          some &= some - 1;
+          s += weight<kHeld>(w, value_at(i + lane, e));
+        }
+      }
     }
+    equal = __reduce_add_sync(0xffffffffu, n);
+    return warp_sum(s);
+  };
+
+  const bool plain = !by_k && !by_p && !by_m;
+  bool whole_row = !by_k;
+  float listed = INFINITY;                // all values from this one up are listed
+  if (by_k) whole_row = !select(false, static_cast<unsigned long long>(top_k), by_p);
+  if (plain || (by_p && whole_row)) {     // the mass of the whole row
+    const unsigned long long s = part_mass();
+    __syncthreads();
+    if (lane == 0) {
+      sh.warp_mass[warp] = s;
+      sh.warp_count[warp] = 0u;
+    }
+    __syncthreads();
+    unsigned long long sum = 0ull;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) sum += sh.warp_mass[i];
+    if (tid < cs) {
+      peer_store64(peer_addr(&sh.from_mass[cr], tid), sum);
+      peer_store32(peer_addr(&sh.from_ties[cr], tid), 0u);
+    }
+    if (by_p) clear();
+    cluster_sync();
+    mass_k = 0ull;
+    for (int i = 0; i < cs; ++i) mass_k += sh.from_mass[i];
+  }
+  if (by_p) {
+    const unsigned long long need = part_of(top_p, mass_k, true);
+    bool found = false;
+    if (whole_row && !w.wide) {
+      // below this a value cannot be the border: all such values together weigh less than 1 - p
+      const float share = (1.0f - top_p) * (static_cast<float>(mass_k) / static_cast<float>(weight<kHeld>(w, m))) / static_cast<float>(v);
+      const float from = fmaxf(fmaxf(w.floor, least), __fsub_rd(m, __fmul_ru(temperature, 1e-4f - 1.0001f * logf(share * 0.999f))));
+      const float reach = m - from, scale = reach > 0.0f ? fminf((kBins - 0.5f) / reach, 1e30f) : 0.0f;
+      const auto bin_of = [&](float xi) { return min(static_cast<int>((m - xi) * scale), kBins - 1); };
+      float *queue = sh.queue[warp];
+      int waiting = 0;
+      const auto flush = [&](int many) {
+        __syncwarp();
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&sh.n, many);
+        at = __shfl_sync(0xffffffffu, at, 0) + lane;
+        if (lane < many) {
+          const float xi = queue[lane];
+          const int bin = bin_of(xi);
+          atomicAdd(&sh.count[bin], 1u);
+          add_mass(sh, bin, weight<kHeld>(w, xi));
+          if (at < kBand) sh.band[at] = xi;
+        }
+        __syncwarp();
+      };
+      for (int64_t i = w0; i < w1; i += 32) {
+        float o[W];
+        unpack(i + lane < w1 ? load_vec(i + lane) : vec_lowest(T{}), o, T{});
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const uint32_t some = __ballot_sync(0xffffffffu, o[e] >= from);
+          if (o[e] >= from) queue[waiting + __popc(some & ((1u << lane) - 1u))] = o[e];
+          waiting += __popc(some);
+          if (waiting >= 32) {
+            flush(32);
+            waiting -= 32;
+            const float rest = queue[32 + lane];
+            __syncwarp();
+            queue[lane] = rest;
+            __syncwarp();
+          }
+        }
+      }
+      flush(waiting);
+      Cross at;
+      found = find_cross(sh, true, need, at);
+      if (sh.n <= kBand) listed = from;
+      if (found && at.in <= kFew) {       // the bin's values to all CTAs
+        const auto hand = [&](float xi) {
+          if (xi >= from && bin_of(xi) == static_cast<int>(at.bin)) {
+            const int place = static_cast<int>(at.place) + atomicAdd(&sh.few_n, 1);
+            for (int r = 0; r < cs; ++r) peer_store32(peer_addr(&sh.few[place], r), __float_as_uint(xi));
+          }
+        };
+        if (tid == 0) sh.few_n = 0;       // of top-k
+        __syncthreads();
+        if (listed == from) {
+          for (int i = tid; i < sh.n; i += kThreads) hand(sh.band[i]);
+        } else {
+          each_from(from, [&](float xi, int64_t) { hand(xi); });
+        }
+        cluster_sync();
+        const int n = static_cast<int>(at.in);
+        const float xi = tid < n ? sh.few[tid] : 0.0f;
+        const unsigned long long mine = tid < n ? weight<kHeld>(w, xi) : 0ull;
+        if (tid < n) sh.few_mass[tid] = mine;
+        __syncthreads();
+        unsigned long long before = at.mass;
+        uint32_t equal = 0u;
+        if (tid < n) {
+          for (int j = 0; j < n; ++j) {
+            const float xj = sh.few[j];
+            if (xj > xi) before += sh.few_mass[j];
+            equal += xj == xi;
+          }
+          if (before < need && need <= before + equal * mine) {   // all of its equals agree
+            sh.edge = xi;
+            sh.ties = (need - before + mine - 1) / mine;
+          }
+        }
+        __syncthreads();
+        lower(sh.edge, sh.ties);
+      } else if (found) {
+        found = false;
+      } else {
+        found = least > w.floor && from == least;   // min-p keeps less
+      }
+    }
+    if (!found) select(true, need, true);
   }
 
-  // kept masses and ties of warps, CTAs
-  unsigned long long mass = 0ull;
-  uint32_t equal = 0u;
-  for (int64_t i = w0 + lane; i < w1; i += 32) {
-    float o[W];
-    load(i, o);
-#pragma unroll
-    for (int e = 0; e < W; ++e) {
-      if (o[e] > t && o[e] >= w.floor) mass += weight<kHeld>(w, o[e]);
-      equal += o[e] == t;
+  // kept mass and ties of the CTAs (the whole row's are known)
+  if (!plain) {
+    unsigned long long mass = 0ull;
+    uint32_t equal = 0u;
+    if (t >= listed) {                    // what is kept is among the listed
+      for (int i = tid; i < sh.n; i += kThreads) {
+        const float xi = sh.band[i];
+        if (xi > t) mass += weight<kHeld>(w, xi);
+        equal += xi == t;
+      }
+      mass = warp_sum(mass);
+      equal = __reduce_add_sync(0xffffffffu, equal);
+    } else {
+      mass = part_kept(w0, w1, equal);
     }
+    __syncthreads();
+    if (lane == 0) {
+      sh.warp_mass[warp] = mass;
+      sh.warp_count[warp] = equal;
+    }
+    __syncthreads();
+    unsigned long long sum = 0ull;
+    uint32_t sum_n = 0u;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      sum += sh.warp_mass[i];
+      sum_n += sh.warp_count[i];
+    }
+    if (tid < cs) {
+      peer_store64(peer_addr(&sh.from_mass[cr], tid), sum);
+      peer_store32(peer_addr(&sh.from_ties[cr], tid), sum_n);
+    }
+    cluster_sync();
   }
-  mass = warp_sum(mass);
-  equal = __reduce_add_sync(0xffffffffu, equal);
-  __syncthreads();                        // of total_mass
-  if (lane == 0) {
-    sh.warp_mass[warp] = mass;
-    sh.warp_count[warp] = equal;
-  }
-  __syncthreads();
-  unsigned long long sum = 0ull;
-  uint32_t sum_n = 0u;
-  for (int i = 0; i < kWarps; ++i) {
-    sum += sh.warp_mass[i];
-    sum_n += sh.warp_count[i];
-  }
-  if (tid < cs) {
-    peer_store64(peer_addr(&sh.from_mass[cr], tid), sum);
-    peer_store32(peer_addr(&sh.from_ties[cr], tid), sum_n);
-  }
-  cluster_sync();
   const unsigned long long of_tie = t >= w.floor ? weight<kHeld>(w, t) : 0ull;
-  const auto kept_ties = [&](uint32_t n, unsigned long long &left) {
+  unsigned long long left = ties;
+  const auto kept_ties = [&](uint32_t n) {  // of the next n ties; takes them off what is left
     const unsigned long long k = n < left ? n : left;
     left -= k;
     return k * of_tie;
   };
-  unsigned long long total = 0ull, left = ties;
-  for (int i = 0; i < cs; ++i) total += sh.from_mass[i] + kept_ties(sh.from_ties[i], left);
-  const unsigned long long target = u >= 1.0f ? total - 1 : u > 0.0f ? part_of(u, total, false) : 0ull;
+  unsigned long long total = 0ull;
+  for (int i = 0; i < cs; ++i) total += sh.from_mass[i] + kept_ties(sh.from_ties[i]);
+  const unsigned long long target = drawn(total);
 
-  // the CTA and the warp in which the sum passes the target
-  unsigned long long upto = 0ull, add = 0ull;
+  // the CTA in which the sum passes the target
+  unsigned long long upto = 0ull;
   left = ties;
-  int at = 0;
-  for (; at < cr; ++at) upto += sh.from_mass[at] + kept_ties(sh.from_ties[at], left);
+  for (int i = 0; i < cr; ++i) upto += sh.from_mass[i] + kept_ties(sh.from_ties[i]);
+  if (target < upto) return;
   {
-    unsigned long long l = left;
-    add = sh.from_mass[cr] + kept_ties(sh.from_ties[cr], l);
+    const unsigned long long l = left, add = sh.from_mass[cr] + kept_ties(sh.from_ties[cr]);
+    if (target >= upto + add) return;
+    left = l;
   }
-  if (target < upto || target >= upto + add) return;
-  for (at = 0; at < warp; ++at) upto += sh.warp_mass[at] + kept_ties(sh.warp_count[at], left);
-  {
-    unsigned long long l = left;
-    add = sh.warp_mass[warp] + kept_ties(sh.warp_count[warp], l);
+  // its warp's part
+  if (t >= listed) {                      // sums of parts are still to come
+    uint32_t equal;
+    const unsigned long long mass = part_kept(w0, w1, equal);
+    __syncthreads();
+    if (lane == 0) {
+      sh.warp_mass[warp] = mass;
+      sh.warp_count[warp] = equal;
+    }
+    __syncthreads();
   }
-  if (target < upto || target >= upto + add) return;
-  for (int64_t i = w0; i < w1; i += 32) {
-    float o[W];
-    unsigned long long sum_above = 0ull;
-    uint32_t n = 0u;
-    if (i + lane < w1) {
-      load(i + lane, o);
-#pragma unroll
-      for (int e = 0; e < W; ++e) {
-        if (o[e] > t && o[e] >= w.floor) sum_above += weight<kHeld>(w, o[e]);
-        n += o[e] == t;
+  // the first of kWarps parts in which the sum passes the target; moves upto and left there
+  const auto pass = [&]() {
+    for (int i = 0;; ++i) {
+      const unsigned long long l = left, add = sh.warp_mass[i] + kept_ties(sh.warp_count[i]);
+      if (i == kWarps - 1 || target < upto + add) {
+        left = l;
+        return i;
       }
+      upto += add;
+    }
+  };
+  const int in_part = pass();
+  int64_t i0 = part_begin(in_part), i1 = part_begin(in_part + 1);
+  {                                       // and of its sixteenths, a warp each
+    const int64_t b0 = i0 + (i1 - i0) * warp / kWarps, b1 = i0 + (i1 - i0) * (warp + 1) / kWarps;
+    uint32_t equal;
+    const unsigned long long mass = part_kept(b0, b1, equal);
+    __syncthreads();
+    if (lane == 0) {
+      sh.warp_mass[warp] = mass;
+      sh.warp_count[warp] = equal;
+    }
+    __syncthreads();
+    const int sixteenth = pass();
+    if (warp != sixteenth) return;
+    i0 = b0;
+    i1 = b1;
+  }
+  for (int64_t i = i0; i < i1; i += 32) {
+    float o[W];
+    unsigned long long weights[W], lane_sum = 0ull;
+    uint32_t n = 0u;
+    unpack(i + lane < i1 ? load_vec(i + lane) : vec_lowest(T{}), o, T{});
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      weights[e] = o[e] > t && o[e] >= w.floor ? weight<kHeld>(w, o[e]) : 0ull;
+      n += o[e] == t && i + lane < i1;
     }
     uint32_t n_upto = n;
 #pragma unroll
@@ -531,9 +900,14 @@ __global__ void __launch_bounds__(kThreads, kHeld ? 2 : 4) sample_kernel(const S
       if (lane >= s) n_upto += b;
     }
     unsigned long long mine_left = left > n_upto - n ? left - (n_upto - n) : 0ull;
-    const unsigned long long left_here = mine_left;
-    unsigned long long l = mine_left;
-    const unsigned long long lane_sum = sum_above + kept_ties(n, l);
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      if (o[e] == t && mine_left > 0ull) {
+        --mine_left;
+        weights[e] = of_tie;
+      }
+      lane_sum += weights[e];
+    }
     unsigned long long s_upto = lane_sum;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
@@ -542,22 +916,14 @@ __global__ void __launch_bounds__(kThreads, kHeld ? 2 : 4) sample_kernel(const S
     }
     unsigned long long here = upto + s_upto - lane_sum;
     if (target >= here && target < here + lane_sum) {
-      unsigned long long tie = left_here;
+      bool done = false;
+#pragma unroll
       for (int e = 0; e < W; ++e) {
-        unsigned long long k = 0ull;
-        if (o[e] > t && o[e] >= w.floor) k = weight<kHeld>(w, o[e]);
-        else if (o[e] == t && tie > 0ull) {
-          --tie;
-          k = of_tie;
+        if (!done && target < here + weights[e]) {
+          write(o[e], (i + lane) * W + e - off, total);
+          done = true;
         }
-        if (target < here + k) {
-          a.tokens[row] = static_cast<int32_t>((i + lane) * W + e - off);
-          if (a.logprobs)
-            a.logprobs[row] = static_cast<float>((static_cast<double>(o[e]) - m) / temperature -
-                                                 log(static_cast<double>(total) / static_cast<double>(weight<kHeld>(w, m))));
-          break;
-        }
-        here += k;
+        here += weights[e];
       }
     }
     upto += __shfl_sync(0xffffffffu, s_upto, 31);
