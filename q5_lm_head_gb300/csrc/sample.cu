@@ -48,8 +48,8 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kCluster = 16;
 constexpr int kBins = 1024;
 constexpr int kFew = 512;                // values settled one by one
-constexpr int kBand = 2048;              // listed values of a CTA
-constexpr int kGroups = 1024;            // maxima of groups
+constexpr int kBand = 4096;              // listed values of a CTA
+constexpr int kGroups = 512;             // maxima of groups
 constexpr int kHeldTwo = 56 * 1024;      // bytes of a row in a CTA: two CTAs an SM
 constexpr int kHeldOne = 168 * 1024;     // one CTA an SM
 
@@ -59,6 +59,8 @@ constexpr float kShift = 12582912.0f;    // 1.5 * 2^23: adding it rounds to a wh
 constexpr float kRound = 192.0f * 274877906944.0f;   // 1.5 * 2^7 * 2^38: adding it rounds to 2^-16 * 2^38
 constexpr int kRoundBits = kFraction - 16;
 constexpr float kOrders = 42.0f;         // a weight of 2^-42 is 0
+constexpr int kCuts = 4;                 // where the mass below is estimated, in units of T below the maximum
+__device__ __forceinline__ constexpr float cut(int c) { return 4.0f + 2.0f * c; }
 // p(v) = 2^(v / 512) - 1: the cubic term, (ln 2 / 512)^3 / 6 v^3, goes into the linear one as its best
 // linear fit on |v| <= 1/2, 3/16 v
 constexpr double kP1 = 0.6931471805599453 / kSteps;
@@ -106,8 +108,8 @@ __device__ __noinline__ unsigned long long wide_weight(float x, float m, double 
   return d < -kOrders ? 0ull : static_cast<unsigned long long>(rint(exp2(d) * static_cast<double>(1ull << kFraction)));
 }
 
-// The weight's upper part, a multiple of 2^22, and the rest.
-__device__ __forceinline__ void weight_parts(const Weigher &w, float x, uint32_t &high, int &low) {
+// The weight's upper part, a multiple of 2^22, and the rest; returns it to about a thousandth.
+__device__ __forceinline__ float weight_parts(const Weigher &w, float x, uint32_t &high, int &low) {
   x = fmaxf(x, w.floor);
   const float q = fmaf(x, w.c1, kShift), whole = q - kShift;
   const float v = fmaf(x, w.c2, fmaf(x, w.c1, -whole));
@@ -118,6 +120,7 @@ __device__ __forceinline__ void weight_parts(const Weigher &w, float x, uint32_t
   const float a = t.x * s, up = a + kRound;
   high = __float_as_uint(up) - __float_as_uint(kRound);
   low = __float2int_rn(fmaf(fmaf(t.x, p, t.y), s, a - (up - kRound)));
+  return a;
 }
 template <bool kShort>                    // rows of at most 2^24 values
 __device__ __forceinline__ unsigned long long weight(const Weigher &w, float x) {
@@ -164,16 +167,23 @@ struct Cross {
   uint32_t in, place;                    // values in the bin; of the CTAs before this one
 };
 
+struct __align__(16) Histogram {         // values, their weights' sum in two words
+  uint32_t count[kBins], low[kBins], high[kBins];
+};
+struct Few {                             // values to settle one by one
+  unsigned long long key[kFew], mass[kFew];
+  float x[kFew];
+};
 struct Shared {
   float2 table[kSteps];
-  uint32_t count[kBins], low[kBins], high[kBins];   // histogram: values, their weights' sum in two words
+  union {                                // the few come from the histogram, when all CTAs have read it
+    Histogram h;
+    Few few;
+  };
   unsigned long long mass[kBins];        // of the cluster, this CTA's slice; top-k's values, of all CTAs
   uint32_t number[kBins];
-  float queue[kWarps][64];               // values on their way to the histogram
-  float band[kBand];                     // those that have been there
-  float few[kFew];                       // values to settle one by one, their weights, their indices
-  unsigned long long few_mass[kFew];
-  uint32_t few_at[kFew];
+  uint16_t place[kBins];                 // of a slice's bin and a CTA: values of the CTAs before it, up to kFew
+  float band[kBand];                     // values that can be top-p's border, and those above
   float group[kGroups];                  // of the cluster
   Weigher w;
   double least_off, inv_t;               // T log(min_p), 1 / T
@@ -187,12 +197,11 @@ struct Shared {
   // from the cluster's CTAs
   unsigned long long from_total[kCluster], slice_mass[kCluster], from_mass[kCluster];
   uint32_t slice_count[kCluster], from_ties[kCluster], from_n[kCluster];
+  float from_tail[kCuts][kCluster * kWarps];
 };
 
-__device__ __forceinline__ uint32_t peer_load32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void peer_load128(uint32_t a, uint32_t (&v)[4]) {
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a) : "memory");
 }
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
@@ -216,31 +225,41 @@ __device__ __forceinline__ unsigned long long block_sum(unsigned long long v, un
 __device__ __forceinline__ void add_mass(Shared &sh, uint32_t bin, unsigned long long w) {
   const uint32_t lo = static_cast<uint32_t>(w);
   uint32_t hi = static_cast<uint32_t>(w >> 32);
-  const uint32_t old = atomicAdd(&sh.low[bin], lo);
+  const uint32_t old = atomicAdd(&sh.h.low[bin], lo);
   hi += old + lo < old;
-  if (hi) atomicAdd(&sh.high[bin], hi);
+  if (hi) atomicAdd(&sh.h.high[bin], hi);
 }
 
 // The first bin at which the cluster's histograms reach `target` (values, or mass
 // when by_mass), in every CTA; false when they do not.  Each CTA adds up a slice of
-// the bins, a thread a bin of a CTA.
+// the bins, a thread four bins of a CTA (single words from 16 CTAs took 8 us).
 __device__ __forceinline__ bool find_cross(Shared &sh, bool by_mass, unsigned long long target, Cross &out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cr = cluster_rank(), cs = cluster_size(), slice = kBins / cs;
   cluster_sync();                         // the histograms are complete
+  if (tid < kBins / 4) {
+    const int r = tid & (cs - 1), bin = tid / cs * 4, at = cr * slice + bin;
+    uint32_t count[4], low[4], high[4];
+    peer_load128(peer_addr(&sh.h.count[at], r), count);
+    peer_load128(peer_addr(&sh.h.low[at], r), low);
+    peer_load128(peer_addr(&sh.h.high[at], r), high);
 #pragma unroll
-  for (int i = 0; i < kBins / kThreads; ++i) {
-    const int p = tid + i * kThreads, r = p & (cs - 1), bin = p / cs, at = cr * slice + bin;
-    uint32_t count = peer_load32(peer_addr(&sh.count[at], r));
-    unsigned long long mass = (static_cast<unsigned long long>(peer_load32(peer_addr(&sh.high[at], r))) << 32) +
-                              peer_load32(peer_addr(&sh.low[at], r));
-    for (int o = cs >> 1; o > 0; o >>= 1) {
-      count += __shfl_xor_sync(0xffffffffu, count, o);
-      mass += __shfl_xor_sync(0xffffffffu, mass, o);
-    }
-    if (r == 0) {
-      sh.number[bin] = count;
-      sh.mass[bin] = mass;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t own = count[i];
+      unsigned long long mass = (static_cast<unsigned long long>(high[i]) << 32) + low[i];
+      for (int o = 1; o < cs; o <<= 1) {  // prefix sums over the CTAs
+        const uint32_t n = __shfl_up_sync(0xffffffffu, count[i], o, cs);
+        const unsigned long long s = __shfl_up_sync(0xffffffffu, mass, o, cs);
+        if (r >= o) {
+          count[i] += n;
+          mass += s;
+        }
+      }
+      sh.place[(bin + i) * cs + r] = static_cast<uint16_t>(min(count[i] - own, static_cast<uint32_t>(kFew)));
+      if (r == cs - 1) {
+        sh.number[bin + i] = count[i];
+        sh.mass[bin + i] = mass;
+      }
     }
   }
   __syncthreads();
@@ -301,16 +320,17 @@ __device__ __forceinline__ bool find_cross(Shared &sh, bool by_mass, unsigned lo
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const unsigned long long b = by_mass ? before : before_n, in = by_mass ? mass[i] : count[i];
-    if (in > 0ull && b < target && b + in >= target) {
-      const int bin = cr * slice + tid * each + i;
-      uint32_t place = 0u;
-      for (int r = 0; r < cs; ++r) {
-        peer_store64(peer_addr(&sh.cross.mass, r), before);
-        peer_store32(peer_addr(&sh.cross.count, r), before_n);
-        peer_store32(peer_addr(&sh.cross.bin, r), bin);
-        peer_store32(peer_addr(&sh.cross.in, r), count[i]);
-        peer_store32(peer_addr(&sh.cross.place, r), place);
-        place += peer_load32(peer_addr(&sh.count[bin], r));
+    const uint32_t here = __ballot_sync(0xffffffffu, in > 0ull && b < target && b + in >= target);
+    if (here) {                           // a lane for each CTA
+      const int from = __ffs(here) - 1, at = __shfl_sync(0xffffffffu, tid * each + i, from);
+      const unsigned long long mass_before = __shfl_sync(0xffffffffu, before, from);
+      const uint32_t count_before = __shfl_sync(0xffffffffu, before_n, from), number_in = __shfl_sync(0xffffffffu, count[i], from);
+      if (lane < cs) {
+        peer_store64(peer_addr(&sh.cross.mass, lane), mass_before);
+        peer_store32(peer_addr(&sh.cross.count, lane), count_before);
+        peer_store32(peer_addr(&sh.cross.bin, lane), cr * slice + at);
+        peer_store32(peer_addr(&sh.cross.in, lane), number_in);
+        peer_store32(peer_addr(&sh.cross.place, lane), sh.place[at * cs + lane]);
       }
     }
     before += mass[i];
@@ -434,8 +454,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
   for (int o = 16; o >= per_warp; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   cluster_wait();                         // every CTA of the cluster has started
-  if (lane < per_warp)
-    for (int r = 0; r < cs; ++r) peer_store32(peer_addr(&sh.group[(cr * kWarps + warp) * per_warp + lane], r), __float_as_uint(m));
+  for (int i = lane; i < cs * per_warp; i += 32)   // a lane's m is its group's, of lane i mod per_warp
+    peer_store32(peer_addr(&sh.group[(cr * kWarps + warp) * per_warp + (i & (per_warp - 1))], i / per_warp), __float_as_uint(m));
   cluster_sync();
   const int groups = kWarps * cs * per_warp;
   m = -INFINITY;
@@ -452,12 +472,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (warp == 0) {
     float bound = -INFINITY;
     if (few_k) {                          // the largest value (its upper 16 bits) that top_k groups reach
-      uint32_t b = 0u;
-      for (int bit = 31; bit >= 16; --bit) {
-        const uint32_t t = b | (1u << bit);
-        int n = 0;
-        for (int i = lane; i < groups; i += 32) n += float_order_key(sh.group[i]) >= t;
-        if (__reduce_add_sync(0xffffffffu, n) >= top_k) b = t;
+      uint32_t key[kGroups / 32], high = 0u, low = ~0u;
+#pragma unroll
+      for (int i = 0; i < kGroups / 32; ++i) {
+        key[i] = lane + 32 * i < groups ? float_order_key(sh.group[lane + 32 * i]) : 0u;
+        high = max(high, key[i]);
+        if (lane + 32 * i < groups) low = min(low, key[i]);
+      }
+      high = __reduce_max_sync(0xffffffffu, high);
+      low = __reduce_min_sync(0xffffffffu, low);
+      // bits above the first that differs are the bound's too; then two bits at a time
+      int bit = high == low ? 0 : 31 - __clz(high ^ low);
+      uint32_t b = high == low ? high : high & ~((2u << bit) - 1u);
+      for (; bit >= 15; bit -= 2) {
+        const uint32_t two = 1u << bit, one = two >> 1;
+        uint32_t n = 0u;                  // of three bounds, 10 bits each
+#pragma unroll
+        for (int i = 0; i < kGroups / 32; ++i)
+          n += (key[i] >= (b | one) ? 1u : 0u) + (key[i] >= (b | two) ? 1u << 10 : 0u) + (key[i] >= (b | two | one) ? 1u << 20 : 0u);
+        n = __reduce_add_sync(0xffffffffu, n);
+        if ((n >> 20) >= top_k) b |= two | one;
+        else if (((n >> 10) & 1023u) >= top_k) b |= two;
+        else if ((n & 1023u) >= top_k) b |= one;
       }
       bound = b < 0x00800000u ? -INFINITY : order_key_float(b);   // NaNs have no place here, -infinity is masked
     }
@@ -524,45 +560,51 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     if (fits && n <= kFew) {
       if (cr != 0) return;
-      float xi = 0.0f;
-      uint32_t index = 0u;
-      unsigned long long mine = 0ull;
       if (tid < n) {
         int r = 0, at = tid;
         for (; at >= static_cast<int>(sh.from_n[r]); ++r) at -= sh.from_n[r];
         const unsigned long long entry = sh.mass[r * room + at];
-        xi = __uint_as_float(static_cast<uint32_t>(entry >> 32));
-        index = static_cast<uint32_t>(entry);
-        mine = weight<kHeld>(w, xi);
-        sh.few[tid] = xi;
-        sh.few_at[tid] = index;
-        sh.few_mass[tid] = mine;
+        const float xi = __uint_as_float(static_cast<uint32_t>(entry >> 32));
+        sh.few.x[tid] = xi;
+        sh.few.key[tid] = argmax_key(xi, static_cast<uint32_t>(entry));
+        sh.few.mass[tid] = weight<kHeld>(w, xi);
       }
       __syncthreads();
-      int64_t rank = 0;
-      unsigned long long before = 0ull;
-      if (tid < n)
-        for (int j = 0; j < n; ++j) {
-          const float xj = sh.few[j];
-          if (xj > xi || (xj == xi && sh.few_at[j] < index)) {
+      // a value's place in the order and the mass before it, by some threads each
+      int split = 1;
+      while (split < 32 && 2 * split * n <= kThreads) split *= 2;
+      const int i = tid / split, first = tid & (split - 1);
+      unsigned long long key = 0ull, mine = 0ull, before = 0ull;
+      float xi = 0.0f;
+      int rank = 0;
+      if (i < n) {
+        key = sh.few.key[i];
+        mine = sh.few.mass[i];
+        xi = sh.few.x[i];
+        for (int j = first; j < n; j += split)
+          if (sh.few.key[j] > key) {
             ++rank;
-            before += sh.few_mass[j];
+            before += sh.few.mass[j];
           }
-        }
-      bool keep = tid < n && rank < top_k;
-      const unsigned long long all = block_sum(keep ? mine : 0ull, sh.warp_mass);
+      }
+      for (int o = split >> 1; o > 0; o >>= 1) {
+        rank += __shfl_xor_sync(0xffffffffu, rank, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+      }
+      bool keep = i < n && rank < top_k;
+      const unsigned long long all = block_sum(keep && first == 0 ? mine : 0ull, sh.warp_mass);
       keep = keep && xi >= least && (!by_p || before < part_of(top_p, all, true));
       if (!keep) mine = 0ull;
-      if (tid < n) sh.few_mass[tid] = mine;
-      const unsigned long long total = block_sum(mine, sh.from_total);
+      if (i < n && first == 0) sh.few.mass[i] = mine;
+      const unsigned long long total = block_sum(first == 0 ? mine : 0ull, sh.from_total);
       static_assert(kCluster >= kWarps, "from_total serves as the CTA's sums");
       const unsigned long long target = drawn(total);
-      if (mine > 0ull) {
-        before = 0ull;
-        for (int j = 0; j < n; ++j)
-          if (sh.few_at[j] < index) before += sh.few_mass[j];
-        if (before <= target && target < before + mine) write(xi, index, total);
-      }
+      before = 0ull;                      // by index: the key's lower half falls with it
+      if (mine > 0ull)
+        for (int j = first; j < n; j += split)
+          if (static_cast<uint32_t>(sh.few.key[j]) > static_cast<uint32_t>(key)) before += sh.few.mass[j];
+      for (int o = split >> 1; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+      if (first == 0 && mine > 0ull && before <= target && target < before + mine) write(xi, argmax_key_index(key), total);
       return;
     }
   }
@@ -578,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
   };
   const auto clear = [&]() {
-    for (int i = tid; i < kBins; i += kThreads) sh.count[i] = sh.low[i] = sh.high[i] = 0u;
+    for (int i = tid; i < kBins; i += kThreads) sh.h.count[i] = sh.h.low[i] = sh.h.high[i] = 0u;
     __syncthreads();
   };
   // by the ordered bits, 10 at a time
@@ -597,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           const float xi = value_at(i, e);
           const uint32_t k = ~float_order_key(xi);
           if (xi >= w.floor && (k & fixed) == key) {
-            atomicAdd(&sh.count[(k >> shift) & mask], 1u);
+            atomicAdd(&sh.h.count[(k >> shift) & mask], 1u);
             if (want_mass) add_mass(sh, (k >> shift) & mask, weight<kHeld>(w, xi));
           }
         }
@@ -616,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     return true;
   };
   // the mass of this warp's part
+  float tail[kCuts] = {};                 // of a fourth of the values, those below m - T kCut[j]
   const auto part_mass = [&]() {
     unsigned long long s = 0ull;
     if (!kHeld || w.wide) {
@@ -636,7 +679,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           for (int j = 0; j < 4; ++j) {
             uint32_t high;
             int low;
-            weight_parts(w, o[e + j], high, low);
+            const float about = weight_parts(w, o[e + j], high, low);
+            if (j == 0) {
+#pragma unroll
+              for (int c = 0; c < kCuts; ++c)
+                if (o[e] < fmaf(-temperature, cut(c), m)) tail[c] += about;
+            }
             highs += high;
             low4 += low;
           }
@@ -693,6 +741,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       peer_store64(peer_addr(&sh.from_mass[cr], tid), sum);
       peer_store32(peer_addr(&sh.from_ties[cr], tid), 0u);
     }
+    if (by_p) {
+#pragma unroll
+      for (int c = 0; c < kCuts; ++c) {
+        for (int o = 16; o > 0; o >>= 1) tail[c] += __shfl_xor_sync(0xffffffffu, tail[c], o);
+        if (lane < cs) peer_store32(peer_addr(&sh.from_tail[c][cr * kWarps + warp], lane), __float_as_uint(tail[c]));
+      }
+    }
     if (by_p) clear();
     cluster_sync();
     mass_k = 0ull;
@@ -704,56 +759,75 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (whole_row && !w.wide) {
       // below this a value cannot be the border: all such values together weigh less than 1 - p
       const float share = (1.0f - top_p) * (static_cast<float>(mass_k) / static_cast<float>(weight<kHeld>(w, m))) / static_cast<float>(v);
-      const float from = fmaxf(fmaxf(w.floor, least), __fsub_rd(m, __fmul_ru(temperature, 1e-4f - 1.0001f * logf(share * 0.999f))));
-      const float reach = m - from, scale = reach > 0.0f ? fminf((kBins - 0.5f) / reach, 1e30f) : 0.0f;
-      const auto bin_of = [&](float xi) { return min(static_cast<int>((m - xi) * scale), kBins - 1); };
-      float *queue = sh.queue[warp];
-      int waiting = 0;
-      const auto flush = [&](int many) {
-        __syncwarp();
-        int at = 0;
-        if (lane == 0) at = atomicAdd(&sh.n, many);
-        at = __shfl_sync(0xffffffffu, at, 0) + lane;
-        if (lane < many) {
-          const float xi = queue[lane];
-          const int bin = bin_of(xi);
-          atomicAdd(&sh.count[bin], 1u);
-          add_mass(sh, bin, weight<kHeld>(w, xi));
-          if (at < kBand) sh.band[at] = xi;
-        }
-        __syncwarp();
-      };
-      for (int64_t i = w0; i < w1; i += 32) {
-        float o[W];
-        unpack(i + lane < w1 ? load_vec(i + lane) : vec_lowest(T{}), o, T{});
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-          const uint32_t some = __ballot_sync(0xffffffffu, o[e] >= from);
-          if (o[e] >= from) queue[waiting + __popc(some & ((1u << lane) - 1u))] = o[e];
-          waiting += __popc(some);
-          if (waiting >= 32) {
-            flush(32);
-            waiting -= 32;
-            const float rest = queue[32 + lane];
-            __syncwarp();
-            queue[lane] = rest;
-            __syncwarp();
-          }
+      float from = fmaxf(fmaxf(w.floor, least), __fsub_rd(m, __fmul_ru(temperature, 1e-4f - 1.0001f * logf(share * 0.999f))));
+      // that counts every value at its most; where the estimate says that less than enough lies below a cut, the
+      // border lies above it (and if it does not, it is not found below)
+#pragma unroll 1
+      for (int c = 0; c < kCuts; ++c) {
+        float below = 0.0f;
+        for (int i = lane; i < cs * kWarps; i += 32) below += sh.from_tail[c][i];
+        for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
+        if (4.0f * below < 0.8f * (1.0f - top_p) * static_cast<float>(mass_k)) {
+          from = fmaxf(from, fmaf(-temperature, cut(c), m));
+          break;
         }
       }
-      flush(waiting);
+      const float reach = m - from, scale = reach > 0.0f ? fminf((kBins - 0.5f) / reach, 1e30f) : 0.0f;
+      const auto bin_of = [&](float xi) { return min(static_cast<int>((m - xi) * scale), kBins - 1); };
+      // into the list, 32 values of a lane at a time
+      constexpr int kAtOnce = 32 / W;
+      if (tid == 0) sh.few_n = 0;         // of top-k
+      for (int64_t i = w0 + lane; i - lane < w1; i += 32 * kAtOnce) {
+        uint32_t some = 0u;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+          if (i + 32 * j < w1) {
+            float o[W];
+            unpack(load_vec(i + 32 * j), o, T{});
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+              if (o[e] >= from) some |= 1u << (j * W + e);
+          }
+        const int many = __popc(some);
+        int to = many;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+          const int b = __shfl_up_sync(0xffffffffu, to, s);
+          if (lane >= s) to += b;
+        }
+        const int all = __shfl_sync(0xffffffffu, to, 31);
+        if (all == 0) continue;
+        int first = 0;
+        if (lane == 0) first = atomicAdd(&sh.n, all);
+        first = __shfl_sync(0xffffffffu, first, 0);
+        if (first + all > kBand) break;   // too many for it
+        to += first - many;
+        for (; some != 0u; some &= some - 1) {
+          const int b = __ffs(some) - 1;
+          sh.band[to++] = value_at(i + 32 * (b / W), b % W);
+        }
+      }
+      __syncthreads();
+      const auto count_in = [&](float xi) {
+        const int bin = bin_of(xi);
+        atomicAdd(&sh.h.count[bin], 1u);
+        add_mass(sh, bin, weight<kHeld>(w, xi));
+      };
+      if (sh.n <= kBand) {
+        listed = from;
+        for (int i = tid; i < sh.n; i += kThreads) count_in(sh.band[i]);
+      } else {
+        each_from(from, [&](float xi, int64_t) { count_in(xi); });
+      }
       Cross at;
       found = find_cross(sh, true, need, at);
-      if (sh.n <= kBand) listed = from;
       if (found && at.in <= kFew) {       // the bin's values to all CTAs
         const auto hand = [&](float xi) {
           if (xi >= from && bin_of(xi) == static_cast<int>(at.bin)) {
             const int place = static_cast<int>(at.place) + atomicAdd(&sh.few_n, 1);
-            for (int r = 0; r < cs; ++r) peer_store32(peer_addr(&sh.few[place], r), __float_as_uint(xi));
+            for (int r = 0; r < cs; ++r) peer_store32(peer_addr(&sh.few.x[place], r), __float_as_uint(xi));
           }
         };
-        if (tid == 0) sh.few_n = 0;       // of top-k
-        __syncthreads();
         if (listed == from) {
           for (int i = tid; i < sh.n; i += kThreads) hand(sh.band[i]);
         } else {
@@ -761,21 +835,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
         cluster_sync();
         const int n = static_cast<int>(at.in);
-        const float xi = tid < n ? sh.few[tid] : 0.0f;
-        const unsigned long long mine = tid < n ? weight<kHeld>(w, xi) : 0ull;
-        if (tid < n) sh.few_mass[tid] = mine;
+        if (tid < n) sh.few.mass[tid] = weight<kHeld>(w, sh.few.x[tid]);
         __syncthreads();
-        unsigned long long before = at.mass;
-        uint32_t equal = 0u;
-        if (tid < n) {
-          for (int j = 0; j < n; ++j) {
-            const float xj = sh.few[j];
-            if (xj > xi) before += sh.few_mass[j];
-            equal += xj == xi;
+        if (warp == 0) {
+          // the largest key at which the mass from it up reaches what is needed: between the bin's ends, bit by bit
+          uint32_t high = 0u, low = ~0u;
+          for (int j = lane; j < n; j += 32) {
+            const uint32_t k = float_order_key(sh.few.x[j]);
+            high = max(high, k);
+            low = min(low, k);
           }
-          if (before < need && need <= before + equal * mine) {   // all of its equals agree
-            sh.edge = xi;
-            sh.ties = (need - before + mine - 1) / mine;
+          high = __reduce_max_sync(0xffffffffu, high);
+          low = __reduce_min_sync(0xffffffffu, low);
+          const auto mass_from = [&](uint32_t k) {
+            unsigned long long s = 0ull;
+            for (int j = lane; j < n; j += 32)
+              if (float_order_key(sh.few.x[j]) >= k) s += sh.few.mass[j];
+            return at.mass + warp_sum(s);
+          };
+          while (low < high) {            // mass_from(low) reaches it
+            const uint32_t mid = low + (high - low) / 2 + 1;
+            if (mass_from(mid) >= need) low = mid;
+            else high = mid - 1;
+          }
+          const unsigned long long above = low == ~0u ? at.mass : mass_from(low + 1), of_one = weight<kHeld>(w, order_key_float(low));
+          if (lane == 0) {
+            sh.edge = order_key_float(low);
+            sh.ties = (need - above + of_one - 1) / of_one;
           }
         }
         __syncthreads();
