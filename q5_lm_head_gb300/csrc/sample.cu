@@ -48,10 +48,12 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kCluster = 16;
 constexpr int kBins = 1024;
 constexpr int kFew = 512;                // values settled one by one
-constexpr int kBand = 4096;              // listed values of a CTA
+constexpr int kBandBytes = 16 * 1024;    // list of a CTA's values that can be top-p's border or lie above it
+constexpr int kBandAlone = 72 * 1024;    // of a row's only CTA
+constexpr int kOctaves = 48;
 constexpr int kGroups = 512;             // maxima of groups
-constexpr int kHeldTwo = 56 * 1024;      // bytes of a row in a CTA: two CTAs an SM
-constexpr int kHeldOne = 168 * 1024;     // one CTA an SM
+constexpr int kHeldTwo = 72 * 1024;      // bytes of a row in a CTA and its list: two CTAs an SM
+constexpr int kHeldOne = 184 * 1024;     // one CTA an SM
 
 constexpr int kSteps = 512;              // table: 2^(i / 512)
 constexpr int kFraction = 38;            // fractional bits of a weight
@@ -59,8 +61,6 @@ constexpr float kShift = 12582912.0f;    // 1.5 * 2^23: adding it rounds to a wh
 constexpr float kRound = 192.0f * 274877906944.0f;   // 1.5 * 2^7 * 2^38: adding it rounds to 2^-16 * 2^38
 constexpr int kRoundBits = kFraction - 16;
 constexpr float kOrders = 42.0f;         // a weight of 2^-42 is 0
-constexpr int kCuts = 4;                 // where the mass below is estimated, in units of T below the maximum
-__device__ __forceinline__ constexpr float cut(int c) { return 4.0f + 2.0f * c; }
 // p(v) = 2^(v / 512) - 1: the cubic term, (ln 2 / 512)^3 / 6 v^3, goes into the linear one as its best
 // linear fit on |v| <= 1/2, 3/16 v
 constexpr double kP1 = 0.6931471805599453 / kSteps;
@@ -183,12 +183,13 @@ struct Shared {
   unsigned long long mass[kBins];        // of the cluster, this CTA's slice; top-k's values, of all CTAs
   uint32_t number[kBins];
   uint16_t place[kBins];                 // of a slice's bin and a CTA: values of the CTAs before it, up to kFew
-  float band[kBand];                     // values that can be top-p's border, and those above
+  uint32_t octave[kOctaves];             // mass of sampled values by the weight's power of two
   float group[kGroups];                  // of the cluster
   Weigher w;
   double least_off, inv_t;               // T log(min_p), 1 / T
   float bound, least;                    // of top-k, min-p
   int n, few_n;                          // listed
+  uint32_t sampled;
   unsigned long long warp_mass[kWarps];
   uint32_t warp_count[kWarps];
   float edge;                            // settled: the threshold, how many of its equals
@@ -197,7 +198,7 @@ struct Shared {
   // from the cluster's CTAs
   unsigned long long from_total[kCluster], slice_mass[kCluster], from_mass[kCluster];
   uint32_t slice_count[kCluster], from_ties[kCluster], from_n[kCluster];
-  float from_tail[kCuts][kCluster * kWarps];
+  uint32_t from_octave[kCluster][kOctaves], from_sampled[kCluster];
 };
 
 __device__ __forceinline__ void peer_load128(uint32_t a, uint32_t (&v)[4]) {
@@ -293,6 +294,7 @@ __device__ __forceinline__ bool find_cross(Shared &sh, bool by_mass, unsigned lo
   __syncthreads();
   unsigned long long total = 0ull, before = upto - sum;
   uint32_t total_n = 0u, before_n = upto_n - number;
+#pragma unroll
   for (int i = 0; i < kWarps; ++i) {
     if (i < warp) {
       before += sh.warp_mass[i];
@@ -308,7 +310,9 @@ __device__ __forceinline__ bool find_cross(Shared &sh, bool by_mass, unsigned lo
   cluster_sync();
   total = 0ull;
   total_n = 0u;
-  for (int r = 0; r < cs; ++r) {
+#pragma unroll
+  for (int r = 0; r < kCluster; ++r) {
+    if (r >= cs) break;
     if (r < cr) {
       before += sh.slice_mass[r];
       before_n += sh.slice_count[r];
@@ -378,6 +382,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const auto part_begin = [&](int i) { return v0 + (((v1 - v0) * i) / kWarps); };
   const int64_t w0 = part_begin(warp), w1 = part_begin(warp + 1);
   uint4 *vec_held = reinterpret_cast<uint4 *>(held);
+  // values that can be top-p's border, and those above: behind the share
+  T *band = reinterpret_cast<T *>(held + a.held_bytes);
   const auto whole = [&](int64_t i) { return i * W >= off && (i + 1) * W <= off + v; };
   const auto edge = [&](int64_t i) {      // a vector that the row only begins or ends in
     float o[W];
@@ -401,7 +407,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
   };
   for (int i = tid; i < kSteps; i += kThreads) sh.table[i] = kPowers.at[i];
-  if (tid == 0) sh.n = sh.few_n = 0;
+  if (tid == 0) sh.n = sh.few_n = 0, sh.sampled = 0u;
+  if (tid < kOctaves) sh.octave[tid] = 0u;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the logits and settings are complete
   if constexpr (kHeld) {
@@ -657,41 +664,46 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     lower(edge_x, many);
     return true;
   };
-  // the mass of this warp's part
-  float tail[kCuts] = {};                 // of a fourth of the values, those below m - T kCut[j]
+  // The mass of this warp's part; of a vector's first value in every fourth step also what octave it is in.
   const auto part_mass = [&]() {
     unsigned long long s = 0ull;
-    if (!kHeld || w.wide) {
+    if (w.wide || w.drop > 0) {
       for (int64_t i = w0 + lane; i < w1; i += 32) {
 #pragma unroll 1
         for (int e = 0; e < W; ++e) s += weight<kHeld>(w, value_at(i, e));
       }
-    } else {                              // high parts fit 32 bits: at most 2^17 each, and 336 values a thread
-      uint32_t highs = 0u;
-      long long lows = 0ll;
-      for (int64_t i = w0 + lane; i < w1; i += 32) {
-        float o[W];
-        unpack(load_vec(i), o, T{});
+    } else {
+      uint32_t sampled = 0u;
+      for (int64_t i = w0 + lane; i < w1; i += 32 * 1024) {   // high parts fit 32 bits: at most 2^17 each, 2^13 values
+        uint32_t highs = 0u;
+        long long lows = 0ll;
+        const int steps = static_cast<int>(min((w1 - i + 31) / 32, static_cast<int64_t>(1024)));
+        for (int step = 0; step < steps; ++step) {
+          float o[W];
+          unpack(load_vec(i + 32 * step), o, T{});
 #pragma unroll
-        for (int e = 0; e < W; e += 4) {
-          int low4 = 0;                   // below 2^29 each
+          for (int e = 0; e < W; e += 4) {
+            int low4 = 0;                 // below 2^29 each
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t high;
-            int low;
-            const float about = weight_parts(w, o[e + j], high, low);
-            if (j == 0) {
-#pragma unroll
-              for (int c = 0; c < kCuts; ++c)
-                if (o[e] < fmaf(-temperature, cut(c), m)) tail[c] += about;
+            for (int j = 0; j < 4; ++j) {
+              uint32_t high;
+              int low;
+              const float about = weight_parts(w, o[e + j], high, low);
+              if (e + j == 0 && (step & 3) == 0) {
+                const uint32_t bits = __float_as_uint(about);
+                atomicAdd(&sh.octave[min(127u + kFraction - (bits >> 23), kOctaves - 1u)], 256u + ((bits >> 15) & 255u));
+                ++sampled;
+              }
+              highs += high;
+              low4 += low;
             }
-            highs += high;
-            low4 += low;
+            lows += low4;
           }
-          lows += low4;
         }
+        s += (static_cast<unsigned long long>(highs) << kRoundBits) + static_cast<unsigned long long>(lows);
       }
-      s = (static_cast<unsigned long long>(highs) << kRoundBits) + static_cast<unsigned long long>(lows);
+      sampled = __reduce_add_sync(0xffffffffu, sampled);
+      if (lane == 0) atomicAdd(&sh.sampled, sampled);
     }
     return warp_sum(s);
   };
@@ -741,12 +753,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       peer_store64(peer_addr(&sh.from_mass[cr], tid), sum);
       peer_store32(peer_addr(&sh.from_ties[cr], tid), 0u);
     }
-    if (by_p) {
-#pragma unroll
-      for (int c = 0; c < kCuts; ++c) {
-        for (int o = 16; o > 0; o >>= 1) tail[c] += __shfl_xor_sync(0xffffffffu, tail[c], o);
-        if (lane < cs) peer_store32(peer_addr(&sh.from_tail[c][cr * kWarps + warp], lane), __float_as_uint(tail[c]));
-      }
+    if (by_p && !w.wide) {
+      for (int i = tid; i < cs * kOctaves; i += kThreads)
+        peer_store32(peer_addr(&sh.from_octave[cr][i % kOctaves], i / kOctaves), sh.octave[i % kOctaves]);
+      if (tid < cs) peer_store32(peer_addr(&sh.from_sampled[cr], tid), sh.sampled);
     }
     if (by_p) clear();
     cluster_sync();
@@ -756,22 +766,49 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (by_p) {
     const unsigned long long need = part_of(top_p, mass_k, true);
     bool found = false;
-    if (whole_row && !w.wide) {
+    // first above an estimate, then above what cannot fail but for too many equals
+    for (int attempt = 0; attempt < 2 && !found && whole_row && !w.wide; ++attempt) {
       // below this a value cannot be the border: all such values together weigh less than 1 - p
       const float share = (1.0f - top_p) * (static_cast<float>(mass_k) / static_cast<float>(weight<kHeld>(w, m))) / static_cast<float>(v);
       float from = fmaxf(fmaxf(w.floor, least), __fsub_rd(m, __fmul_ru(temperature, 1e-4f - 1.0001f * logf(share * 0.999f))));
-      // that counts every value at its most; where the estimate says that less than enough lies below a cut, the
-      // border lies above it (and if it does not, it is not found below)
-#pragma unroll 1
-      for (int c = 0; c < kCuts; ++c) {
-        float below = 0.0f;
-        for (int i = lane; i < cs * kWarps; i += 32) below += sh.from_tail[c][i];
-        for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
-        if (4.0f * below < 0.8f * (1.0f - top_p) * static_cast<float>(mass_k)) {
-          from = fmaxf(from, fmaf(-temperature, cut(c), m));
-          break;
+      // That counts every value at its most.  By the sampled values' octaves, the border lies above where less than
+      // four fifths of 1 - p lie below; if it does not, it is not found there.
+      bool estimated = false;
+      if (w.drop == 0 && attempt == 0) {
+        float below = 0.0f, sampled = 0.0f;   // of the lane's two octaves, down to the last
+        float mine[2] = {0.0f, 0.0f};
+        for (int r = 0; r < cs; ++r) {
+          sampled += static_cast<float>(sh.from_sampled[r]);
+          mine[0] += static_cast<float>(sh.from_octave[r][lane]);
+          if (lane < kOctaves - 32) mine[1] += static_cast<float>(sh.from_octave[r][lane + 32]);
         }
+        const float unit = static_cast<float>(v) / fmaxf(sampled, 1.0f) * static_cast<float>(1ull << (kFraction - 8));
+        const float enough = 0.8f * (1.0f - top_p) * static_cast<float>(mass_k);
+        int cut = kOctaves;
+#pragma unroll
+        for (int h = 1; h >= 0; --h) {
+          float s = mine[h] * unit * exp2f(-static_cast<float>(lane + 32 * h));
+          for (int o = 1; o < 32; o <<= 1) {
+            const float t = __shfl_down_sync(0xffffffffu, s, o);
+            if (lane + o < 32) s += t;
+          }
+          // an octave and all below it
+          const uint32_t little = __ballot_sync(0xffffffffu, s + below < enough);
+          if (little) cut = 32 * h + __ffs(little) - 1;
+          below += __shfl_sync(0xffffffffu, s, 0);
+        }
+        const float top = __log2f(static_cast<float>(weight<kHeld>(w, m))) - kFraction;   // the maximum's place in its octave
+        const float above = cut < kOctaves ? fmaf(-temperature * 0.6931472f, cut - 1 + top + 0.01f, m) : from;
+        estimated = above > from;
+        from = fmaxf(from, above);
       }
+      if (attempt > 0) {
+        __syncthreads();
+        clear();
+        if (tid == 0) sh.n = 0;
+        __syncthreads();
+      }
+      listed = INFINITY;
       const float reach = m - from, scale = reach > 0.0f ? fminf((kBins - 0.5f) / reach, 1e30f) : 0.0f;
       const auto bin_of = [&](float xi) { return min(static_cast<int>((m - xi) * scale), kBins - 1); };
       // into the list, 32 values of a lane at a time
@@ -800,11 +837,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         int first = 0;
         if (lane == 0) first = atomicAdd(&sh.n, all);
         first = __shfl_sync(0xffffffffu, first, 0);
-        if (first + all > kBand) break;   // too many for it
+        if (first + all > a.band) break;   // too many for it
         to += first - many;
         for (; some != 0u; some &= some - 1) {
           const int b = __ffs(some) - 1;
-          sh.band[to++] = value_at(i + 32 * (b / W), b % W);
+          band[to++] = from_float<T>(value_at(i + 32 * (b / W), b % W));
         }
       }
       __syncthreads();
@@ -813,9 +850,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         atomicAdd(&sh.h.count[bin], 1u);
         add_mass(sh, bin, weight<kHeld>(w, xi));
       };
-      if (sh.n <= kBand) {
+      if (sh.n <= a.band) {
         listed = from;
-        for (int i = tid; i < sh.n; i += kThreads) count_in(sh.band[i]);
+        for (int i = tid; i < sh.n; i += kThreads) count_in(to_float(band[i]));
       } else {
         each_from(from, [&](float xi, int64_t) { count_in(xi); });
       }
@@ -829,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           }
         };
         if (listed == from) {
-          for (int i = tid; i < sh.n; i += kThreads) hand(sh.band[i]);
+          for (int i = tid; i < sh.n; i += kThreads) hand(to_float(band[i]));
         } else {
           each_from(from, [&](float xi, int64_t) { hand(xi); });
         }
@@ -853,6 +890,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
               if (float_order_key(sh.few.x[j]) >= k) s += sh.few.mass[j];
             return at.mass + warp_sum(s);
           };
+          if (n <= 32) {                  // a lane a value
+            const float xi = lane < n ? sh.few.x[lane] : 0.0f;
+            const unsigned long long mine = lane < n ? sh.few.mass[lane] : 0ull;
+            unsigned long long from_me = at.mass;   // of its equals and those above
+            for (int j = 0; j < n; ++j) {
+              const unsigned long long s = __shfl_sync(0xffffffffu, mine, j);
+              if (__shfl_sync(0xffffffffu, xi, j) >= xi) from_me += s;
+            }
+            low = __reduce_max_sync(0xffffffffu, lane < n && from_me >= need ? float_order_key(xi) : 0u);
+            high = low;
+          }
           while (low < high) {            // mass_from(low) reaches it
             const uint32_t mid = low + (high - low) / 2 + 1;
             if (mass_from(mid) >= need) low = mid;
@@ -866,10 +914,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
         __syncthreads();
         lower(sh.edge, sh.ties);
-      } else if (found) {
+      } else if (found) {                 // too many of them
         found = false;
-      } else {
-        found = least > w.floor && from == least;   // min-p keeps less
+        break;
+      } else if (!estimated) {
+        found = from == least;            // min-p keeps less
+        break;
       }
     }
     if (!found) select(true, need, true);
@@ -881,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     uint32_t equal = 0u;
     if (t >= listed) {                    // what is kept is among the listed
       for (int i = tid; i < sh.n; i += kThreads) {
-        const float xi = sh.band[i];
+        const float xi = to_float(band[i]);
         if (xi > t) mass += weight<kHeld>(w, xi);
         equal += xi == t;
       }
@@ -1019,6 +1069,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
 }
 
+template <typename T>
+cudaError_t launch_sample_read(const SampleArgs &a, int cs);
+
 template <typename T, bool kHeld>
 cudaError_t launch_sample_t(const SampleArgs &a, int cs, size_t shared) {
   static std::atomic<unsigned long long> configured{0};   // one bit per device; host threads may race here
@@ -1028,7 +1081,7 @@ cudaError_t launch_sample_t(const SampleArgs &a, int cs, size_t shared) {
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(configured.load(std::memory_order_acquire) & bit)) {
     e = cudaFuncSetAttribute(sample_kernel<T, kHeld>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess && kHeld)
+    if (e == cudaSuccess)
       e = cudaFuncSetAttribute(sample_kernel<T, kHeld>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldOne);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_acq_rel);
@@ -1046,24 +1099,38 @@ cudaError_t launch_sample_t(const SampleArgs &a, int cs, size_t shared) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (shared > kHeldTwo) {                // up to 16 SMs of one GPC at a time: not every device has them
+  if (kHeld && shared > kHeldTwo) {       // up to 16 SMs of one GPC at a time: not every device has them
     int fit = 0;
     e = cudaOccupancyMaxActiveClusters(&fit, sample_kernel<T, kHeld>, &cfg);
     if (e != cudaSuccess) return e;
-    if (fit < 1) return launch_sample_t<T, false>(a, 8, 0);
+    if (fit < 1) return launch_sample_read<T>(a, 8);
   }
   return cudaLaunchKernelEx(&cfg, sample_kernel<T, kHeld>, a);
 }
 
+// Rows read again for each pass.
+template <typename T>
+cudaError_t launch_sample_read(const SampleArgs &a, int cs) {
+  SampleArgs b = a;
+  b.held_bytes = 0;
+  const int bytes = cs == 1 ? kBandAlone : kBandBytes;
+  b.band = bytes / static_cast<int>(sizeof(T));
+  return launch_sample_t<T, false>(b, cs, bytes);
+}
+
 template <typename T>
 cudaError_t launch_sample_rows(const SampleArgs &a) {
-  const int64_t vecs = a.v / Vec<T>::W + 2;
+  const int64_t vecs = a.v / Vec<T>::W + 2, band = kBandBytes;
   auto held = [&](int64_t cs) { return (vecs + cs - 1) / cs * 16; };   // a share is at most this
+  if (a.n >= 2 * a.num_sms) return launch_sample_read<T>(a, 1);
   int cs = 1;
-  while (cs < kCluster && held(cs) > kHeldTwo) cs *= 2;
+  while (cs < kCluster && held(cs) + band > kHeldTwo) cs *= 2;
   while (cs < kCluster && a.n * 2 * cs <= 2 * a.num_sms && a.v / (2 * cs) >= 2048) cs *= 2;
-  if (held(cs) > kHeldOne || a.n * cs >= (int64_t{1} << 31)) return launch_sample_t<T, false>(a, a.n * 8 < (int64_t{1} << 31) ? 8 : 1, 0);
-  return launch_sample_t<T, true>(a, cs, static_cast<size_t>(held(cs)));
+  if (held(cs) + band > kHeldOne) return launch_sample_read<T>(a, 8);
+  SampleArgs b = a;
+  b.held_bytes = static_cast<int>(held(cs));
+  b.band = kBandBytes / static_cast<int>(sizeof(T));
+  return launch_sample_t<T, true>(b, cs, static_cast<size_t>(held(cs) + band));
 }
 
 }  // namespace
