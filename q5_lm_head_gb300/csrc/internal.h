@@ -179,7 +179,7 @@ struct SampleArgs {
   float *logprobs;         // [n] or nullptr
   int num_sms;
   cudaStream_t stream;
-  int held_bytes = 0, band = 0;   // set at the launch: of a CTA's share in shared memory, values of its list
+  int held_bytes = 0;      // set at the launch: of a CTA's share in shared memory
 };
 cudaError_t launch_sample(const SampleArgs &a);
 

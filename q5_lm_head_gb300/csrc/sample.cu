@@ -48,11 +48,11 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kCluster = 16;
 constexpr int kBins = 1024;
 constexpr int kFew = 512;                // values settled one by one
-constexpr int kBandBytes = 16 * 1024;    // list of a CTA's values that can be top-p's border or lie above it
-constexpr int kBandAlone = 72 * 1024;    // of a row's only CTA
-constexpr int kOctaves = 48;
 constexpr int kGroups = 512;             // maxima of groups
-constexpr int kHeldTwo = 72 * 1024;      // bytes of a row in a CTA and its list: two CTAs an SM
+constexpr int kStaged = 2;               // 16-byte vectors of a lane and step, of rows in shared memory
+constexpr int kRead = 4;                 // and of rows that are read again
+constexpr int kQueue = 32 * 16 * kWarps; // bytes of the warps' queues, for each vector of a step
+constexpr int kHeldTwo = 74 * 1024;      // bytes of a row in a CTA and its queues: two CTAs an SM
 constexpr int kHeldOne = 184 * 1024;     // one CTA an SM
 
 constexpr int kSteps = 512;              // table: 2^(i / 512)
@@ -61,6 +61,7 @@ constexpr float kShift = 12582912.0f;    // 1.5 * 2^23: adding it rounds to a wh
 constexpr float kRound = 192.0f * 274877906944.0f;   // 1.5 * 2^7 * 2^38: adding it rounds to 2^-16 * 2^38
 constexpr int kRoundBits = kFraction - 16;
 constexpr float kOrders = 42.0f;         // a weight of 2^-42 is 0
+constexpr int kOctaves = 48;
 // p(v) = 2^(v / 512) - 1: the cubic term, (ln 2 / 512)^3 / 6 v^3, goes into the linear one as its best
 // linear fit on |v| <= 1/2, 3/16 v
 constexpr double kP1 = 0.6931471805599453 / kSteps;
@@ -122,6 +123,24 @@ __device__ __forceinline__ float weight_parts(const Weigher &w, float x, uint32_
   low = __float2int_rn(fmaf(fmaf(t.x, p, t.y), s, a - (up - kRound)));
   return a;
 }
+// The same of two values at once, added to sums; returns the first one's to about a thousandth.
+__device__ __forceinline__ float weight_pair(const Weigher &w, float x0, float x1, uint32_t &highs, int &lows) {
+  const unsigned long long x = pack2(fmaxf(x0, w.floor), fmaxf(x1, w.floor)), c1 = pack2(w.c1, w.c1), shift = pack2(kShift, kShift),
+                           minus = pack2(-1.0f, -1.0f), round = pack2(kRound, kRound);
+  const unsigned long long q = fma2(x, c1, shift), v = fma2(x, pack2(w.c2, w.c2), fma2(x, c1, fma2(q, minus, shift)));
+  const unsigned long long p = mul2(v, fma2(v, pack2(kPoly2, kPoly2), pack2(kPoly1, kPoly1)));
+  const float2 qf = unpack2(q);
+  const uint32_t b0 = __float_as_uint(qf.x), b1 = __float_as_uint(qf.y);
+  const float2 t0 = w.table[b0 & (kSteps - 1)], t1 = w.table[b1 & (kSteps - 1)];
+  const unsigned long long s = pack2(__uint_as_float((b0 & ~(kSteps - 1u)) * (1u << 14) + w.base),
+                                     __uint_as_float((b1 & ~(kSteps - 1u)) * (1u << 14) + w.base));
+  const unsigned long long t = pack2(t0.x, t1.x), a = mul2(t, s), up = add2(a, round);
+  const unsigned long long rest = add2(a, fma2(up, minus, round));
+  const float2 low = unpack2(fma2(fma2(t, p, pack2(t0.y, t1.y)), s, rest)), upf = unpack2(up);
+  highs += __float_as_uint(upf.x) + __float_as_uint(upf.y) - 2u * __float_as_uint(kRound);
+  lows += __float2int_rn(low.x) + __float2int_rn(low.y);
+  return unpack2(a).x;
+}
 template <bool kShort>                    // rows of at most 2^24 values
 __device__ __forceinline__ unsigned long long weight(const Weigher &w, float x) {
   unsigned long long r;
@@ -160,12 +179,57 @@ __device__ __forceinline__ float max_nan(float a, float b) {     // a NaN stays
   return r;
 }
 
+__device__ __forceinline__ uint32_t max_nan_word(uint32_t a, uint32_t b, float) {
+  return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+}
+__device__ __forceinline__ uint32_t max_nan_word(uint32_t a, uint32_t b, __half) {
+  uint32_t r;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_word(uint32_t a, uint32_t b, __nv_bfloat16) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ uint4 vec_max_nan(const uint4 &a, const uint4 &b, T t) {
+  return make_uint4(max_nan_word(a.x, b.x, t), max_nan_word(a.y, b.y, t), max_nan_word(a.z, b.z, t), max_nan_word(a.w, b.w, t));
+}
+
 // Where the running count or mass of a histogram reaches a target.
 struct Cross {
   unsigned long long mass;               // before the bin
   uint32_t count, bin;
   uint32_t in, place;                    // values in the bin; of the CTAs before this one
 };
+
+// The least value of the logits' type from `v` up, in both halves of a word.
+__device__ __forceinline__ float least_from(float v, float) { return v; }
+__device__ __forceinline__ __half2 least_from(float v, __half) { return __half2half2(__float2half_ru(v)); }
+__device__ __forceinline__ __nv_bfloat162 least_from(float v, __nv_bfloat16) { return __bfloat162bfloat162(__float2bfloat16_ru(v)); }
+// Bits of a vector's values from there up: value e of vector j at bit 4 j + e, of 16-bit
+// types at 4 j + e / 2 + 16 (e mod 2).
+__device__ __forceinline__ uint32_t values_from(const uint4 &r, int j, float from) {
+  uint32_t m = 0u;
+  if (__uint_as_float(r.x) >= from) m |= 1u << (4 * j);
+  if (__uint_as_float(r.y) >= from) m |= 2u << (4 * j);
+  if (__uint_as_float(r.z) >= from) m |= 4u << (4 * j);
+  if (__uint_as_float(r.w) >= from) m |= 8u << (4 * j);
+  return m;
+}
+template <typename T2>
+__device__ __forceinline__ uint32_t values_from(const uint4 &r, int j, T2 from) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m |= __hge2_mask(*reinterpret_cast<const T2 *>(&w[i]), from) & (0x00010001u << (4 * j + i));
+  return m;
+}
+template <typename T>
+__device__ __forceinline__ int vector_of(int bit) { return (bit & 15) >> 2; }
+template <typename T>
+__device__ __forceinline__ int value_of(int bit) { return sizeof(T) == 4 ? bit & 3 : 2 * (bit & 3) + (bit >> 4); }
 
 struct __align__(16) Histogram {         // values, their weights' sum in two words
   uint32_t count[kBins], low[kBins], high[kBins];
@@ -188,7 +252,7 @@ struct Shared {
   Weigher w;
   double least_off, inv_t;               // T log(min_p), 1 / T
   float bound, least;                    // of top-k, min-p
-  int n, few_n;                          // listed
+  int few_n;                             // listed
   uint32_t sampled;
   unsigned long long warp_mass[kWarps];
   uint32_t warp_count[kWarps];
@@ -382,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const auto part_begin = [&](int i) { return v0 + (((v1 - v0) * i) / kWarps); };
   const int64_t w0 = part_begin(warp), w1 = part_begin(warp + 1);
   uint4 *vec_held = reinterpret_cast<uint4 *>(held);
-  // values that can be top-p's border, and those above: behind the share
-  T *band = reinterpret_cast<T *>(held + a.held_bytes);
+  constexpr int kVecs = kHeld ? kStaged : kRead;
+  T *queue = reinterpret_cast<T *>(held + a.held_bytes) + warp * (kVecs * 32 * W);
   const auto whole = [&](int64_t i) { return i * W >= off && (i + 1) * W <= off + v; };
   const auto edge = [&](int64_t i) {      // a vector that the row only begins or ends in
     float o[W];
@@ -407,7 +471,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
   };
   for (int i = tid; i < kSteps; i += kThreads) sh.table[i] = kPowers.at[i];
-  if (tid == 0) sh.n = sh.few_n = 0, sh.sampled = 0u;
+  if (tid == 0) {
+    sh.few_n = 0;
+    sh.sampled = 0u;
+  }
   if (tid < kOctaves) sh.octave[tid] = 0u;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the logits and settings are complete
@@ -438,7 +505,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     while (kWarps * cs * per_warp < top_k) per_warp *= 2;
   if (tid == 0) {                         // 64 bits take their time: beside the loads
     const double c = 1.4426950408889634 / temperature;
-    sh.w.table = sh.table;
     sh.w.c1 = static_cast<float>(c * kSteps);
     sh.w.c2 = static_cast<float>(c * kSteps - sh.w.c1);
     sh.w.c = c;
@@ -451,11 +517,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     __syncwarp();                         // a warp reads what it has fetched itself
   }
 
+  // a step's vectors of a lane from vector i on; nothing beside the part
+  const auto fetch = [&](int64_t i, int64_t end, uint4 (&r)[kVecs]) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) r[j] = i + 32 * j < end ? load_vec(i + 32 * j) : vec_lowest(T{});
+  };
+
   // the row's maximum, and those of its groups; a NaN stays one
   float m = -INFINITY;
-  for (int64_t i = w0 + lane; i < w1; i += 32) {
+  {
+    uint4 most = vec_lowest(T{});
+    for (int64_t i = w0 + lane; i - lane < w1; i += 32 * kVecs) {
+      uint4 r[kVecs];
+      fetch(i, w1, r);
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) most = vec_max_nan(most, r[j], T{});
+    }
     float o[W];
-    unpack(load_vec(i), o, T{});
+    unpack(most, o, T{});
 #pragma unroll
     for (int e = 0; e < W; ++e) m = max_nan(m, o[e]);
   }
@@ -505,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       bound = b < 0x00800000u ? -INFINITY : order_key_float(b);   // NaNs have no place here, -infinity is masked
     }
     if (lane == 0) {
-      sh.w.floor = __fsub_rd(m, __fmul_ru(temperature, kOrders * 0.6931472f));
+      sh.w.floor = fmaxf(__fsub_rd(m, __fmul_ru(temperature, kOrders * 0.6931472f)), -3.402823466e38f);
       sh.w.wide = !(fmaxf(fabsf(m), fabsf(sh.w.floor)) * sh.w.c1 < 4000000.0f);
       sh.w.m = m;
       const uint32_t top = __float_as_uint(fmaf(m, sh.w.c1, kShift)) & ~(kSteps - 1u);
@@ -515,7 +594,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
   }
   __syncthreads();
-  const Weigher w = sh.w;
+  Weigher w = sh.w;
+  w.table = sh.table;                     // known to be in shared memory
   const float least = sh.least;
 
   const auto write = [&](float xi, int64_t index, unsigned long long total) {
@@ -526,24 +606,48 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const auto drawn = [&](unsigned long long total) {
     return u >= 1.0f ? total - 1 : u > 0.0f ? part_of(u, total, false) : 0ull;
   };
-  // the values from `from` up of this warp's part: each(value, index), a few lanes at a time
-  const auto each_from = [&](float from, auto &&each) {
-    for (int64_t i = w0; i < w1; i += 32) {
+  // the values from `from` up of vectors [i0, i1), a few: each(value, index)
+  const auto each_from = [&](int64_t i0, int64_t i1, float from, auto &&each) {
+    const auto least_in = least_from(from, T{});
+    for (int64_t i = i0 + lane; i - lane < i1; i += 32 * kVecs) {
+      uint4 r[kVecs];
+      fetch(i, i1, r);
       uint32_t some = 0u;
-      if (i + lane < w1) {
-        float o[W];
-        unpack(load_vec(i + lane), o, T{});
 #pragma unroll
-        for (int e = 0; e < W; ++e)
-          if (o[e] >= from) some |= 1u << e;
+      for (int j = 0; j < kVecs; ++j) some |= values_from(r[j], j, least_in);
+      for (; some != 0u; some &= some - 1) {
+        const int bit = __ffs(some) - 1;
+        const int64_t at = i + 32 * vector_of<T>(bit);
+        each(value_at(at, value_of<T>(bit)), at * W + value_of<T>(bit) - off);
       }
-      while (__any_sync(0xffffffffu, some != 0u)) {
-        if (some != 0u) {
-          const int e = __ffs(some) - 1;
-          some &= some - 1;
-          each(value_at(i + lane, e), (i + lane) * W + e - off);
-        }
+    }
+  };
+  // the same of many: through the warp's queue, so that all lanes have one at a time
+  const auto many_from = [&](int64_t i0, int64_t i1, float from, auto &&each) {
+    const auto least_in = least_from(from, T{});
+    for (int64_t i = i0 + lane; i - lane < i1; i += 32 * kVecs) {
+      uint4 r[kVecs];
+      fetch(i, i1, r);
+      uint32_t some = 0u;
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) some |= values_from(r[j], j, least_in);
+      const int many = __popc(some);
+      int to = many;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const int b = __shfl_up_sync(0xffffffffu, to, s);
+        if (lane >= s) to += b;
       }
+      const int all = __shfl_sync(0xffffffffu, to, 31);
+      if (all == 0) continue;
+      to -= many;
+      for (; some != 0u; some &= some - 1) {
+        const int bit = __ffs(some) - 1;
+        queue[to++] = from_float<T>(value_at(i + 32 * vector_of<T>(bit), value_of<T>(bit)));
+      }
+      __syncwarp();
+      for (int k = lane; k < all; k += 32) each(to_float(queue[k]));
+      __syncwarp();
     }
   };
 
@@ -551,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (few_k) {
     const int room = kBins / cs;
     const uint32_t to = peer_addr(&sh.mass[cr * room], 0);
-    each_from(sh.bound, [&](float xi, int64_t index) {
+    each_from(w0, w1, sh.bound, [&](float xi, int64_t index) {
       const int at = atomicAdd(&sh.few_n, 1);
       if (at < room)
         peer_store64(to + 8 * at, (static_cast<unsigned long long>(__float_as_uint(xi)) << 32) | static_cast<uint32_t>(index));
@@ -664,7 +768,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     lower(edge_x, many);
     return true;
   };
-  // The mass of this warp's part; of a vector's first value in every fourth step also what octave it is in.
+  // The mass of this warp's part; of some vectors' first values also what octave it is in.
+  const bool short_row = v <= 65536;
   const auto part_mass = [&]() {
     unsigned long long s = 0ull;
     if (w.wide || w.drop > 0) {
@@ -674,69 +779,57 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
     } else {
       uint32_t sampled = 0u;
-      for (int64_t i = w0 + lane; i < w1; i += 32 * 1024) {   // high parts fit 32 bits: at most 2^17 each, 2^13 values
-        uint32_t highs = 0u;
-        long long lows = 0ll;
-        const int steps = static_cast<int>(min((w1 - i + 31) / 32, static_cast<int64_t>(1024)));
-        for (int step = 0; step < steps; ++step) {
+      uint32_t highs = 0u;                // parts of at most 2^17 each
+      long long lows = 0ll;
+      int steps = 0;
+      for (int64_t i = w0 + lane; i - lane < w1; i += 32 * kVecs) {
+        uint4 r[kVecs];
+        fetch(i, w1, r);
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
           float o[W];
-          unpack(load_vec(i + 32 * step), o, T{});
+          unpack(r[j], o, T{});
 #pragma unroll
           for (int e = 0; e < W; e += 4) {
             int low4 = 0;                 // below 2^29 each
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t high;
-              int low;
-              const float about = weight_parts(w, o[e + j], high, low);
-              if (e + j == 0 && (step & 3) == 0) {
+            for (int k = 0; k < 4; k += 2) {
+              const float about = weight_pair(w, o[e + k], o[e + k + 1], highs, low4);
+              if (e + k == 0 && (j == 0 || short_row) && i + 32 * j < w1) {
                 const uint32_t bits = __float_as_uint(about);
                 atomicAdd(&sh.octave[min(127u + kFraction - (bits >> 23), kOctaves - 1u)], 256u + ((bits >> 15) & 255u));
                 ++sampled;
               }
-              highs += high;
-              low4 += low;
             }
             lows += low4;
           }
         }
-        s += (static_cast<unsigned long long>(highs) << kRoundBits) + static_cast<unsigned long long>(lows);
+        if (++steps == 256) {             // 2^13 values
+          s += static_cast<unsigned long long>(highs) << kRoundBits;
+          highs = 0u;
+          steps = 0;
+        }
       }
+      s += (static_cast<unsigned long long>(highs) << kRoundBits) + static_cast<unsigned long long>(lows);
       sampled = __reduce_add_sync(0xffffffffu, sampled);
       if (lane == 0) atomicAdd(&sh.sampled, sampled);
     }
     return warp_sum(s);
   };
-  // its values above t, and those equal to it
+  // the mass above t in vectors [i0, i1), and how many equal it
   const auto part_kept = [&](int64_t i0, int64_t i1, uint32_t &equal) {
     unsigned long long s = 0ull;
     uint32_t n = 0u;
-    for (int64_t i = i0; i < i1; i += 32) {
-      uint32_t some = 0u;
-      if (i + lane < i1) {
-        float o[W];
-        unpack(load_vec(i + lane), o, T{});
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-          if (o[e] > t && o[e] >= w.floor) some |= 1u << e;
-          n += o[e] == t;
-        }
-      }
-      while (__any_sync(0xffffffffu, some != 0u)) {
-        if (some != 0u) {
-          const int e = __ffs(some) - 1;
-          some &= some - 1;
-          s += weight<kHeld>(w, value_at(i + lane, e));
-        }
-      }
-    }
+    many_from(i0, i1, fmaxf(t, w.floor), [&](float xi) {
+      if (xi == t) ++n;
+      else s += weight<kHeld>(w, xi);
+    });
     equal = __reduce_add_sync(0xffffffffu, n);
     return warp_sum(s);
   };
 
   const bool plain = !by_k && !by_p && !by_m;
   bool whole_row = !by_k;
-  float listed = INFINITY;                // all values from this one up are listed
   if (by_k) whole_row = !select(false, static_cast<unsigned long long>(top_k), by_p);
   if (plain || (by_p && whole_row)) {     // the mass of the whole row
     const unsigned long long s = part_mass();
@@ -771,8 +864,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       // below this a value cannot be the border: all such values together weigh less than 1 - p
       const float share = (1.0f - top_p) * (static_cast<float>(mass_k) / static_cast<float>(weight<kHeld>(w, m))) / static_cast<float>(v);
       float from = fmaxf(fmaxf(w.floor, least), __fsub_rd(m, __fmul_ru(temperature, 1e-4f - 1.0001f * logf(share * 0.999f))));
-      // That counts every value at its most.  By the sampled values' octaves, the border lies above where less than
-      // four fifths of 1 - p lie below; if it does not, it is not found there.
+      // That counts every value at its most.  By the sampled values' octaves, the border lies above where seven
+      // tenths of 1 - p lie below; if it does not, it is not found there.
       bool estimated = false;
       if (w.drop == 0 && attempt == 0) {
         float below = 0.0f, sampled = 0.0f;   // of the lane's two octaves, down to the last
@@ -783,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           if (lane < kOctaves - 32) mine[1] += static_cast<float>(sh.from_octave[r][lane + 32]);
         }
         const float unit = static_cast<float>(v) / fmaxf(sampled, 1.0f) * static_cast<float>(1ull << (kFraction - 8));
-        const float enough = 0.8f * (1.0f - top_p) * static_cast<float>(mass_k);
+        const float enough = 0.7f * (1.0f - top_p) * static_cast<float>(mass_k);
         int cut = kOctaves;
 #pragma unroll
         for (int h = 1; h >= 0; --h) {
@@ -805,71 +898,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       if (attempt > 0) {
         __syncthreads();
         clear();
-        if (tid == 0) sh.n = 0;
-        __syncthreads();
       }
-      listed = INFINITY;
       const float reach = m - from, scale = reach > 0.0f ? fminf((kBins - 0.5f) / reach, 1e30f) : 0.0f;
       const auto bin_of = [&](float xi) { return min(static_cast<int>((m - xi) * scale), kBins - 1); };
-      // into the list, 32 values of a lane at a time
-      constexpr int kAtOnce = 32 / W;
       if (tid == 0) sh.few_n = 0;         // of top-k
-      for (int64_t i = w0 + lane; i - lane < w1; i += 32 * kAtOnce) {
-        uint32_t some = 0u;
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j)
-          if (i + 32 * j < w1) {
-            float o[W];
-            unpack(load_vec(i + 32 * j), o, T{});
-#pragma unroll
-            for (int e = 0; e < W; ++e)
-              if (o[e] >= from) some |= 1u << (j * W + e);
-          }
-        const int many = __popc(some);
-        int to = many;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-          const int b = __shfl_up_sync(0xffffffffu, to, s);
-          if (lane >= s) to += b;
-        }
-        const int all = __shfl_sync(0xffffffffu, to, 31);
-        if (all == 0) continue;
-        int first = 0;
-        if (lane == 0) first = atomicAdd(&sh.n, all);
-        first = __shfl_sync(0xffffffffu, first, 0);
-        if (first + all > a.band) break;   // too many for it
-        to += first - many;
-        for (; some != 0u; some &= some - 1) {
-          const int b = __ffs(some) - 1;
-          band[to++] = from_float<T>(value_at(i + 32 * (b / W), b % W));
-        }
-      }
-      __syncthreads();
-      const auto count_in = [&](float xi) {
+      many_from(w0, w1, from, [&](float xi) {
         const int bin = bin_of(xi);
         atomicAdd(&sh.h.count[bin], 1u);
         add_mass(sh, bin, weight<kHeld>(w, xi));
-      };
-      if (sh.n <= a.band) {
-        listed = from;
-        for (int i = tid; i < sh.n; i += kThreads) count_in(to_float(band[i]));
-      } else {
-        each_from(from, [&](float xi, int64_t) { count_in(xi); });
-      }
+      });
       Cross at;
       found = find_cross(sh, true, need, at);
       if (found && at.in <= kFew) {       // the bin's values to all CTAs
-        const auto hand = [&](float xi) {
-          if (xi >= from && bin_of(xi) == static_cast<int>(at.bin)) {
+        // its lower end, to the roundings of two products of at most kBins
+        const float low_end = fmaxf(from, m - (static_cast<float>(at.bin) + 1.001f) / scale);
+        each_from(w0, w1, low_end, [&](float xi, int64_t) {
+          if (bin_of(xi) == static_cast<int>(at.bin)) {
             const int place = static_cast<int>(at.place) + atomicAdd(&sh.few_n, 1);
             for (int r = 0; r < cs; ++r) peer_store32(peer_addr(&sh.few.x[place], r), __float_as_uint(xi));
           }
-        };
-        if (listed == from) {
-          for (int i = tid; i < sh.n; i += kThreads) hand(to_float(band[i]));
-        } else {
-          each_from(from, [&](float xi, int64_t) { hand(xi); });
-        }
+        });
         cluster_sync();
         const int n = static_cast<int>(at.in);
         if (tid < n) sh.few.mass[tid] = weight<kHeld>(w, sh.few.x[tid]);
@@ -927,19 +975,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 
   // kept mass and ties of the CTAs (the whole row's are known)
   if (!plain) {
-    unsigned long long mass = 0ull;
-    uint32_t equal = 0u;
-    if (t >= listed) {                    // what is kept is among the listed
-      for (int i = tid; i < sh.n; i += kThreads) {
-        const float xi = to_float(band[i]);
-        if (xi > t) mass += weight<kHeld>(w, xi);
-        equal += xi == t;
-      }
-      mass = warp_sum(mass);
-      equal = __reduce_add_sync(0xffffffffu, equal);
-    } else {
-      mass = part_kept(w0, w1, equal);
-    }
+    uint32_t equal;
+    const unsigned long long mass = part_kept(w0, w1, equal);
     __syncthreads();
     if (lane == 0) {
       sh.warp_mass[warp] = mass;
@@ -979,17 +1016,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     const unsigned long long l = left, add = sh.from_mass[cr] + kept_ties(sh.from_ties[cr]);
     if (target >= upto + add) return;
     left = l;
-  }
-  // its warp's part
-  if (t >= listed) {                      // sums of parts are still to come
-    uint32_t equal;
-    const unsigned long long mass = part_kept(w0, w1, equal);
-    __syncthreads();
-    if (lane == 0) {
-      sh.warp_mass[warp] = mass;
-      sh.warp_count[warp] = equal;
-    }
-    __syncthreads();
   }
   // the first of kWarps parts in which the sum passes the target; moves upto and left there
   const auto pass = [&]() {
@@ -1113,24 +1139,21 @@ template <typename T>
 cudaError_t launch_sample_read(const SampleArgs &a, int cs) {
   SampleArgs b = a;
   b.held_bytes = 0;
-  const int bytes = cs == 1 ? kBandAlone : kBandBytes;
-  b.band = bytes / static_cast<int>(sizeof(T));
-  return launch_sample_t<T, false>(b, cs, bytes);
+  return launch_sample_t<T, false>(b, cs, kQueue * kRead);
 }
 
 template <typename T>
 cudaError_t launch_sample_rows(const SampleArgs &a) {
-  const int64_t vecs = a.v / Vec<T>::W + 2, band = kBandBytes;
+  const int64_t vecs = a.v / Vec<T>::W + 2, queue = kQueue * kStaged;
   auto held = [&](int64_t cs) { return (vecs + cs - 1) / cs * 16; };   // a share is at most this
   if (a.n >= 2 * a.num_sms) return launch_sample_read<T>(a, 1);
   int cs = 1;
-  while (cs < kCluster && held(cs) + band > kHeldTwo) cs *= 2;
+  while (cs < kCluster && held(cs) + queue > kHeldTwo) cs *= 2;
   while (cs < kCluster && a.n * 2 * cs <= 2 * a.num_sms && a.v / (2 * cs) >= 2048) cs *= 2;
-  if (held(cs) + band > kHeldOne) return launch_sample_read<T>(a, 8);
+  if (held(cs) + queue > kHeldOne) return launch_sample_read<T>(a, 8);
   SampleArgs b = a;
   b.held_bytes = static_cast<int>(held(cs));
-  b.band = kBandBytes / static_cast<int>(sizeof(T));
-  return launch_sample_t<T, true>(b, cs, static_cast<size_t>(held(cs) + band));
+  return launch_sample_t<T, true>(b, cs, static_cast<size_t>(held(cs) + queue));
 }
 
 }  // namespace
