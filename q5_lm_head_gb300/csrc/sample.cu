@@ -102,6 +102,7 @@ struct Weigher {
   int drop;                // bits by which weights are shortened, so that 64 bits hold a row's sum
   float m;
   double c;                // log2(e) / T
+  float c0, e;             // the same in 32 bits; E
 };
 
 __device__ __noinline__ unsigned long long wide_weight(float x, float m, double c) {
@@ -109,8 +110,8 @@ __device__ __noinline__ unsigned long long wide_weight(float x, float m, double 
   return d < -kOrders ? 0ull : static_cast<unsigned long long>(rint(exp2(d) * static_cast<double>(1ull << kFraction)));
 }
 
-// The weight's upper part, a multiple of 2^22, and the rest; returns it to about a thousandth.
-__device__ __forceinline__ float weight_parts(const Weigher &w, float x, uint32_t &high, int &low) {
+// The weight's upper part, a multiple of 2^22, and the rest.
+__device__ __forceinline__ void weight_parts(const Weigher &w, float x, uint32_t &high, int &low) {
   x = fmaxf(x, w.floor);
   const float q = fmaf(x, w.c1, kShift), whole = q - kShift;
   const float v = fmaf(x, w.c2, fmaf(x, w.c1, -whole));
@@ -121,10 +122,9 @@ __device__ __forceinline__ float weight_parts(const Weigher &w, float x, uint32_
   const float a = t.x * s, up = a + kRound;
   high = __float_as_uint(up) - __float_as_uint(kRound);
   low = __float2int_rn(fmaf(fmaf(t.x, p, t.y), s, a - (up - kRound)));
-  return a;
 }
-// The same of two values at once, added to sums; returns the first one's to about a thousandth.
-__device__ __forceinline__ float weight_pair(const Weigher &w, float x0, float x1, uint32_t &highs, int &lows) {
+// The same of two values at once, added to sums.
+__device__ __forceinline__ void weight_pair(const Weigher &w, float x0, float x1, uint32_t &highs, int &lows) {
   const unsigned long long x = pack2(fmaxf(x0, w.floor), fmaxf(x1, w.floor)), c1 = pack2(w.c1, w.c1), shift = pack2(kShift, kShift),
                            minus = pack2(-1.0f, -1.0f), round = pack2(kRound, kRound);
   const unsigned long long q = fma2(x, c1, shift), v = fma2(x, pack2(w.c2, w.c2), fma2(x, c1, fma2(q, minus, shift)));
@@ -139,7 +139,6 @@ __device__ __forceinline__ float weight_pair(const Weigher &w, float x0, float x
   const float2 low = unpack2(fma2(fma2(t, p, pack2(t0.y, t1.y)), s, rest)), upf = unpack2(up);
   highs += __float_as_uint(upf.x) + __float_as_uint(upf.y) - 2u * __float_as_uint(kRound);
   lows += __float2int_rn(low.x) + __float2int_rn(low.y);
-  return unpack2(a).x;
 }
 template <bool kShort>                    // rows of at most 2^24 values
 __device__ __forceinline__ unsigned long long weight(const Weigher &w, float x) {
@@ -248,20 +247,23 @@ struct Shared {
   uint32_t number[kBins];
   uint16_t place[kBins];                 // of a slice's bin and a CTA: values of the CTAs before it, up to kFew
   uint32_t octave[kOctaves];             // mass of sampled values by the weight's power of two
+  unsigned long long above[kWarps];      // mass of the warps' parts from a value up that is certainly kept
   float group[kGroups];                  // of the cluster
   Weigher w;
   double least_off, inv_t;               // T log(min_p), 1 / T
   float bound, least;                    // of top-k, min-p
   int few_n;                             // listed
   uint32_t sampled;
-  unsigned long long warp_mass[kWarps];
+  unsigned long long warp_mass[kWarps], warp_tail[kWarps];
   uint32_t warp_count[kWarps];
   float edge;                            // settled: the threshold, how many of its equals
-  unsigned long long ties;
+  unsigned long long ties, reached;
   Cross cross;
   // from the cluster's CTAs
   unsigned long long from_total[kCluster], slice_mass[kCluster], from_mass[kCluster];
   uint32_t slice_count[kCluster], from_ties[kCluster], from_n[kCluster];
+  unsigned long long from_tail[kCluster];
+  float from_about[kCluster];
   uint32_t from_octave[kCluster][kOctaves], from_sampled[kCluster];
 };
 
@@ -296,12 +298,12 @@ __device__ __forceinline__ void add_mass(Shared &sh, uint32_t bin, unsigned long
 }
 
 // The first bin at which the cluster's histograms reach `target` (values, or mass
-// when by_mass), in every CTA; false when they do not.  Each CTA adds up a slice of
+// when by_mass), in every CTA; false when they do not.  To be called when all CTAs'
+// histograms are complete.  Each CTA adds up a slice of
 // the bins, a thread four bins of a CTA (single words from 16 CTAs took 8 us).
 __device__ __forceinline__ bool find_cross(Shared &sh, bool by_mass, unsigned long long target, Cross &out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cr = cluster_rank(), cs = cluster_size(), slice = kBins / cs;
-  cluster_sync();                         // the histograms are complete
   if (tid < kBins / 4) {
     const int r = tid & (cs - 1), bin = tid / cs * 4, at = cr * slice + bin;
     uint32_t count[4], low[4], high[4];
@@ -508,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     sh.w.c1 = static_cast<float>(c * kSteps);
     sh.w.c2 = static_cast<float>(c * kSteps - sh.w.c1);
     sh.w.c = c;
+    sh.w.c0 = static_cast<float>(c);
     sh.w.drop = v > (int64_t{1} << 24) ? 40 - __clzll(v - 1) : 0;   // bits of v - 1 beyond 24
     sh.inv_t = 1.0 / temperature;
     sh.least_off = by_m ? temperature * log(min_p < 1.0f ? static_cast<double>(min_p) : 1.0) : 0.0;
@@ -589,6 +592,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       sh.w.m = m;
       const uint32_t top = __float_as_uint(fmaf(m, sh.w.c1, kShift)) & ~(kSteps - 1u);
       sh.w.base = ((127u + kFraction) << 23) - top * (1u << 14);
+      sh.w.e = (__uint_as_float(top) - kShift) * (1.0f / kSteps);
       sh.bound = fmaxf(bound, sh.w.floor);
       sh.least = by_m ? __double2float_ru(m + sh.least_off) : -INFINITY;
     }
@@ -606,56 +610,75 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const auto drawn = [&](unsigned long long total) {
     return u >= 1.0f ? total - 1 : u > 0.0f ? part_of(u, total, false) : 0ull;
   };
-  // the values from `from` up of vectors [i0, i1), a few: each(value, index)
-  const auto each_from = [&](int64_t i0, int64_t i1, float from, auto &&each) {
-    const auto least_in = least_from(from, T{});
+  // the values of [from, to) of vectors [i0, i1), a few: each(value, index)
+  const auto each_in = [&](int64_t i0, int64_t i1, float from, float to, auto &&each) {
+    const auto least_in = least_from(from, T{}), least_over = least_from(to, T{});
     for (int64_t i = i0 + lane; i - lane < i1; i += 32 * kVecs) {
       uint4 r[kVecs];
       fetch(i, i1, r);
-      uint32_t some = 0u;
+      uint32_t some = 0u, over = 0u;
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) some |= values_from(r[j], j, least_in);
-      for (; some != 0u; some &= some - 1) {
+      if (__any_sync(0xffffffffu, some != 0u) == 0) continue;
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) over |= values_from(r[j], j, least_over);
+      for (some &= ~over; some != 0u; some &= some - 1) {
         const int bit = __ffs(some) - 1;
         const int64_t at = i + 32 * vector_of<T>(bit);
         each(value_at(at, value_of<T>(bit)), at * W + value_of<T>(bit) - off);
       }
     }
   };
-  // the same of many: through the warp's queue, so that all lanes have one at a time
-  const auto many_from = [&](int64_t i0, int64_t i1, float from, auto &&each) {
-    const auto least_in = least_from(from, T{});
+  // the same of many, through the warp's queue, so that all lanes have one at a time; look(vector) at all of them
+  const auto many_in = [&](int64_t i0, int64_t i1, float from, float to, auto &&look, auto &&each) {
+    const auto least_in = least_from(from, T{}), least_over = least_from(to, T{});
     for (int64_t i = i0 + lane; i - lane < i1; i += 32 * kVecs) {
       uint4 r[kVecs];
       fetch(i, i1, r);
-      uint32_t some = 0u;
+      uint32_t some = 0u, over = 0u;
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) some |= values_from(r[j], j, least_in);
+      for (int j = 0; j < kVecs; ++j) {
+        some |= values_from(r[j], j, least_in);
+        over |= values_from(r[j], j, least_over);
+        look(r[j]);
+      }
+      some &= ~over;
       const int many = __popc(some);
-      int to = many;
+      int at = many;
 #pragma unroll
       for (int s = 1; s < 32; s <<= 1) {
-        const int b = __shfl_up_sync(0xffffffffu, to, s);
-        if (lane >= s) to += b;
+        const int b = __shfl_up_sync(0xffffffffu, at, s);
+        if (lane >= s) at += b;
       }
-      const int all = __shfl_sync(0xffffffffu, to, 31);
+      const int all = __shfl_sync(0xffffffffu, at, 31);
       if (all == 0) continue;
-      to -= many;
-      for (; some != 0u; some &= some - 1) {
-        const int bit = __ffs(some) - 1;
-        queue[to++] = from_float<T>(value_at(i + 32 * vector_of<T>(bit), value_of<T>(bit)));
+      T *to_queue = queue + (at - many);
+      if (all < 32 * 2) {                 // from the bits that are set
+        for (; some != 0u; some &= some - 1) {
+          const int bit = __ffs(some) - 1;
+          *to_queue++ = from_float<T>(value_at(i + 32 * vector_of<T>(bit), value_of<T>(bit)));
+        }
+      } else {                            // from all of them
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+          const T *o = reinterpret_cast<const T *>(&r[j]);
+#pragma unroll
+          for (int e = 0; e < W; ++e)
+            if (some & (1u << (sizeof(T) == 4 ? 4 * j + e : 4 * j + e / 2 + 16 * (e & 1)))) *to_queue++ = o[e];
+        }
       }
       __syncwarp();
       for (int k = lane; k < all; k += 32) each(to_float(queue[k]));
       __syncwarp();
     }
   };
+  const auto no_look = [](const uint4 &) {};
 
   // top-k: what reaches the bound, to the first CTA
   if (few_k) {
     const int room = kBins / cs;
     const uint32_t to = peer_addr(&sh.mass[cr * room], 0);
-    each_from(w0, w1, sh.bound, [&](float xi, int64_t index) {
+    each_in(w0, w1, sh.bound, INFINITY, [&](float xi, int64_t index) {
       const int at = atomicAdd(&sh.few_n, 1);
       if (at < room)
         peer_store64(to + 8 * at, (static_cast<unsigned long long>(__float_as_uint(xi)) << 32) | static_cast<uint32_t>(index));
@@ -755,6 +778,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           }
         }
       }
+      cluster_sync();
       Cross at;
       if (!find_cross(sh, by_mass, target, at)) return false;   // only at the first level
       target -= by_mass ? at.mass : at.count;
@@ -768,8 +792,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     lower(edge_x, many);
     return true;
   };
-  // The mass of this warp's part; of some vectors' first values also what octave it is in.
-  const bool short_row = v <= 65536;
+  // the mass of this warp's part
   const auto part_mass = [&]() {
     unsigned long long s = 0ull;
     if (w.wide || w.drop > 0) {
@@ -778,7 +801,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         for (int e = 0; e < W; ++e) s += weight<kHeld>(w, value_at(i, e));
       }
     } else {
-      uint32_t sampled = 0u;
       uint32_t highs = 0u;                // parts of at most 2^17 each
       long long lows = 0ll;
       int steps = 0;
@@ -792,15 +814,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
           for (int e = 0; e < W; e += 4) {
             int low4 = 0;                 // below 2^29 each
-#pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-              const float about = weight_pair(w, o[e + k], o[e + k + 1], highs, low4);
-              if (e + k == 0 && (j == 0 || short_row) && i + 32 * j < w1) {
-                const uint32_t bits = __float_as_uint(about);
-                atomicAdd(&sh.octave[min(127u + kFraction - (bits >> 23), kOctaves - 1u)], 256u + ((bits >> 15) & 255u));
-                ++sampled;
-              }
-            }
+            weight_pair(w, o[e], o[e + 1], highs, low4);
+            weight_pair(w, o[e + 2], o[e + 3], highs, low4);
             lows += low4;
           }
         }
@@ -811,27 +826,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
       }
       s += (static_cast<unsigned long long>(highs) << kRoundBits) + static_cast<unsigned long long>(lows);
-      sampled = __reduce_add_sync(0xffffffffu, sampled);
-      if (lane == 0) atomicAdd(&sh.sampled, sampled);
     }
     return warp_sum(s);
   };
-  // the mass above t in vectors [i0, i1), and how many equal it
-  const auto part_kept = [&](int64_t i0, int64_t i1, uint32_t &equal) {
-    unsigned long long s = 0ull;
-    uint32_t n = 0u;
-    many_from(i0, i1, fmaxf(t, w.floor), [&](float xi) {
-      if (xi == t) ++n;
-      else s += weight<kHeld>(w, xi);
-    });
-    equal = __reduce_add_sync(0xffffffffu, n);
-    return warp_sum(s);
-  };
-
-  const bool plain = !by_k && !by_p && !by_m;
-  bool whole_row = !by_k;
-  if (by_k) whole_row = !select(false, static_cast<unsigned long long>(top_k), by_p);
-  if (plain || (by_p && whole_row)) {     // the mass of the whole row
+  // the mass of the CTAs, in from_mass, and of the row; parts' in warp_mass
+  const auto row_mass = [&]() {
     const unsigned long long s = part_mass();
     __syncthreads();
     if (lane == 0) {
@@ -846,137 +845,289 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       peer_store64(peer_addr(&sh.from_mass[cr], tid), sum);
       peer_store32(peer_addr(&sh.from_ties[cr], tid), 0u);
     }
-    if (by_p && !w.wide) {
-      for (int i = tid; i < cs * kOctaves; i += kThreads)
-        peer_store32(peer_addr(&sh.from_octave[cr][i % kOctaves], i / kOctaves), sh.octave[i % kOctaves]);
-      if (tid < cs) peer_store32(peer_addr(&sh.from_sampled[cr], tid), sh.sampled);
-    }
-    if (by_p) clear();
     cluster_sync();
-    mass_k = 0ull;
-    for (int i = 0; i < cs; ++i) mass_k += sh.from_mass[i];
-  }
-  if (by_p) {
-    const unsigned long long need = part_of(top_p, mass_k, true);
-    bool found = false;
-    // first above an estimate, then above what cannot fail but for too many equals
-    for (int attempt = 0; attempt < 2 && !found && whole_row && !w.wide; ++attempt) {
-      // below this a value cannot be the border: all such values together weigh less than 1 - p
-      const float share = (1.0f - top_p) * (static_cast<float>(mass_k) / static_cast<float>(weight<kHeld>(w, m))) / static_cast<float>(v);
-      float from = fmaxf(fmaxf(w.floor, least), __fsub_rd(m, __fmul_ru(temperature, 1e-4f - 1.0001f * logf(share * 0.999f))));
-      // That counts every value at its most.  By the sampled values' octaves, the border lies above where seven
-      // tenths of 1 - p lie below; if it does not, it is not found there.
-      bool estimated = false;
-      if (w.drop == 0 && attempt == 0) {
-        float below = 0.0f, sampled = 0.0f;   // of the lane's two octaves, down to the last
-        float mine[2] = {0.0f, 0.0f};
-        for (int r = 0; r < cs; ++r) {
-          sampled += static_cast<float>(sh.from_sampled[r]);
-          mine[0] += static_cast<float>(sh.from_octave[r][lane]);
-          if (lane < kOctaves - 32) mine[1] += static_cast<float>(sh.from_octave[r][lane + 32]);
-        }
-        const float unit = static_cast<float>(v) / fmaxf(sampled, 1.0f) * static_cast<float>(1ull << (kFraction - 8));
-        const float enough = 0.7f * (1.0f - top_p) * static_cast<float>(mass_k);
-        int cut = kOctaves;
+    sum = 0ull;
+    for (int i = 0; i < cs; ++i) sum += sh.from_mass[i];
+    return sum;
+  };
+  // the mass of the values in (t, to) of vectors [i0, i1), and how many equal t
+  const auto part_kept = [&](int64_t i0, int64_t i1, float to, uint32_t &equal) {
+    unsigned long long s = 0ull;
+    uint32_t n = 0u;
+    many_in(i0, i1, fmaxf(t, w.floor), to, no_look, [&](float xi) {
+      if (xi == t) ++n;
+      else s += weight<kHeld>(w, xi);
+    });
+    equal = __reduce_add_sync(0xffffffffu, n);
+    return warp_sum(s);
+  };
+
+  const bool plain = !by_k && !by_p && !by_m;
+  bool whole_row = !by_k;
+  if (by_k) whole_row = !select(false, static_cast<unsigned long long>(top_k), by_p);
+  if (plain) row_mass();
+  float sure = INFINITY;                  // from here up all is kept, its mass in sh.above
+  if (by_p && whole_row && !w.wide && w.drop == 0) {
+    // The row's mass and where it lies, about: exponentials in 32 bits, some of them by octave.
+    const unsigned long long c2 = pack2(w.c0, w.c0), e2 = pack2(-w.e, -w.e);
+    const int others = v <= 65536 ? 0 : 3;   // vectors that are not sampled for one that is
+    {
+      float about = 0.0f;
+      uint32_t sampled = 0u;
+      int step = 0;
+      for (int64_t i = w0 + lane; i - lane < w1; i += 32 * kVecs) {
+        uint4 r[kVecs];
+        fetch(i, w1, r);
+        unsigned long long sum = 0ull;
 #pragma unroll
-        for (int h = 1; h >= 0; --h) {
-          float s = mine[h] * unit * exp2f(-static_cast<float>(lane + 32 * h));
-          for (int o = 1; o < 32; o <<= 1) {
-            const float t = __shfl_down_sync(0xffffffffu, s, o);
-            if (lane + o < 32) s += t;
+        for (int j = 0; j < kVecs; ++j, ++step) {
+          float o[W];
+          unpack(r[j], o, T{});
+#pragma unroll
+          for (int e = 0; e < W; e += 2) {
+            const float2 y = unpack2(fma2(pack2(o[e], o[e + 1]), c2, e2));
+            const float one = exp2_approx(y.x);
+            sum = add2(sum, pack2(one, exp2_approx(y.y)));
+            if (e == 0 && (step & others) == 0 && i + 32 * j < w1) {
+              const uint32_t bits = __float_as_uint(one);
+              atomicAdd(&sh.octave[min(max(127 - static_cast<int>(bits >> 23), 0), kOctaves - 1)], 256u + ((bits >> 15) & 255u));
+              ++sampled;
+            }
           }
-          // an octave and all below it
-          const uint32_t little = __ballot_sync(0xffffffffu, s + below < enough);
-          if (little) cut = 32 * h + __ffs(little) - 1;
-          below += __shfl_sync(0xffffffffu, s, 0);
         }
-        const float top = __log2f(static_cast<float>(weight<kHeld>(w, m))) - kFraction;   // the maximum's place in its octave
-        const float above = cut < kOctaves ? fmaf(-temperature * 0.6931472f, cut - 1 + top + 0.01f, m) : from;
-        estimated = above > from;
-        from = fmaxf(from, above);
+        about += unpack2(sum).x + unpack2(sum).y;
       }
+      for (int o = 16; o > 0; o >>= 1) about += __shfl_xor_sync(0xffffffffu, about, o);
+      sampled = __reduce_add_sync(0xffffffffu, sampled);
+      if (lane == 0) {
+        atomicAdd(&sh.sampled, sampled);
+        sh.warp_mass[warp] = __float_as_uint(about);
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < cs * kOctaves; i += kThreads)
+      peer_store32(peer_addr(&sh.from_octave[cr][i % kOctaves], i / kOctaves), sh.octave[i % kOctaves]);
+    if (tid < cs) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) sum += __uint_as_float(static_cast<uint32_t>(sh.warp_mass[i]));
+      peer_store32(peer_addr(&sh.from_about[cr], tid), __float_as_uint(sum));
+      peer_store32(peer_addr(&sh.from_sampled[cr], tid), sh.sampled);
+    }
+    clear();
+    cluster_sync();
+    float about = 0.0f, sampled = 0.0f, mine[2] = {0.0f, 0.0f};   // of the lane's two octaves
+    for (int r = 0; r < cs; ++r) {
+      about += sh.from_about[r];
+      sampled += static_cast<float>(sh.from_sampled[r]);
+      mine[0] += static_cast<float>(sh.from_octave[r][lane]);
+      if (lane < kOctaves - 32) mine[1] += static_cast<float>(sh.from_octave[r][lane + 32]);
+    }
+    // Below this a value cannot be the border: all such values together weigh less than 1 - p.  It counts every
+    // value at its most.
+    const float share = (1.0f - top_p) * about / static_cast<float>(v);
+    const float lowest = fmaxf(fmaxf(w.floor, least), fmaf(__log2f(share * 0.99f) + w.e, 1.0f / w.c0, -1e-4f * temperature - 1e-5f * fabsf(m)));
+    // By the sampled octaves, the border lies above where seven tenths of 1 - p lie below, and below where that is
+    // fourteen; a border that is not there is not found there.
+    float guess = lowest, sure_guess = INFINITY;
+    {
+      const float unit = static_cast<float>(v) / fmaxf(sampled, 1.0f) / 256.0f;
+      const float enough = (1.0f - top_p) * about;
+      float below = 0.0f;
+      int low_cut = kOctaves, high_cut = -1;
+#pragma unroll
+      for (int h = 1; h >= 0; --h) {
+        float s = mine[h] * unit * exp2f(-static_cast<float>(lane + 32 * h));
+        for (int o = 1; o < 32; o <<= 1) {
+          const float t = __shfl_down_sync(0xffffffffu, s, o);
+          if (lane + o < 32) s += t;
+        }
+        // an octave and all below it
+        const uint32_t little = __ballot_sync(0xffffffffu, s + below < 0.7f * enough), much = __ballot_sync(0xffffffffu, s + below > 1.4f * enough);
+        if (little) low_cut = 32 * h + __ffs(little) - 1;
+        if (much && high_cut < 0) high_cut = 32 * h + 31 - __clz(much);
+        below += __shfl_sync(0xffffffffu, s, 0);
+      }
+      if (low_cut < kOctaves) guess = fmaxf(lowest, (w.e - static_cast<float>(low_cut - 1)) / w.c0);
+      if (high_cut > 0) sure_guess = (w.e - static_cast<float>(high_cut - 1)) / w.c0;
+      if (!(sure_guess > guess)) sure_guess = INFINITY;
+    }
+    // What the mass below may be off by: the products' roundings (of log2(e) / T too), 2 ulp of an exponential, 16 additions, and
+    // half of the last place of every weight.
+    const float off_by = 0.6931472f * 0x1p-24f * (44.0f + fmaxf(fabsf(m), fabsf(w.floor)) * w.c0) + 0x1p-22f + 0x1.1p-20f + 0x1p-32f;
+    bool exact = false, guessed = guess > lowest || sure_guess < INFINITY, found = false;
+#pragma unroll 1
+    for (int attempt = 0; attempt < 4; ++attempt) {
+      const float from = guessed ? guess : lowest, top = guessed ? sure_guess : INFINITY, base = fminf(top, m);
+      const float reach = base - from, scale = reach > 0.0f ? fminf((kBins - 0.5f) / reach, 1e30f) : 0.0f;
+      const auto bin_of = [&](float xi) { return min(static_cast<int>((base - xi) * scale), kBins - 1); };
       if (attempt > 0) {
-        __syncthreads();
+        cluster_sync();                   // all have read what came before
         clear();
       }
-      const float reach = m - from, scale = reach > 0.0f ? fminf((kBins - 0.5f) / reach, 1e30f) : 0.0f;
-      const auto bin_of = [&](float xi) { return min(static_cast<int>((m - xi) * scale), kBins - 1); };
-      if (tid == 0) sh.few_n = 0;         // of top-k
-      many_from(w0, w1, from, [&](float xi) {
-        const int bin = bin_of(xi);
-        atomicAdd(&sh.h.count[bin], 1u);
-        add_mass(sh, bin, weight<kHeld>(w, xi));
-      });
-      Cross at;
-      found = find_cross(sh, true, need, at);
-      if (found && at.in <= kFew) {       // the bin's values to all CTAs
-        // its lower end, to the roundings of two products of at most kBins
-        const float low_end = fmaxf(from, m - (static_cast<float>(at.bin) + 1.001f) / scale);
-        each_from(w0, w1, low_end, [&](float xi, int64_t) {
-          if (bin_of(xi) == static_cast<int>(at.bin)) {
-            const int place = static_cast<int>(at.place) + atomicAdd(&sh.few_n, 1);
-            for (int r = 0; r < cs; ++r) peer_store32(peer_addr(&sh.few.x[place], r), __float_as_uint(xi));
-          }
-        });
-        cluster_sync();
-        const int n = static_cast<int>(at.in);
-        if (tid < n) sh.few.mass[tid] = weight<kHeld>(w, sh.few.x[tid]);
-        __syncthreads();
-        if (warp == 0) {
-          // the largest key at which the mass from it up reaches what is needed: between the bin's ends, bit by bit
-          uint32_t high = 0u, low = ~0u;
-          for (int j = lane; j < n; j += 32) {
-            const uint32_t k = float_order_key(sh.few.x[j]);
-            high = max(high, k);
-            low = min(low, k);
-          }
-          high = __reduce_max_sync(0xffffffffu, high);
-          low = __reduce_min_sync(0xffffffffu, low);
-          const auto mass_from = [&](uint32_t k) {
-            unsigned long long s = 0ull;
-            for (int j = lane; j < n; j += 32)
-              if (float_order_key(sh.few.x[j]) >= k) s += sh.few.mass[j];
-            return at.mass + warp_sum(s);
-          };
-          if (n <= 32) {                  // a lane a value
-            const float xi = lane < n ? sh.few.x[lane] : 0.0f;
-            const unsigned long long mine = lane < n ? sh.few.mass[lane] : 0ull;
-            unsigned long long from_me = at.mass;   // of its equals and those above
-            for (int j = 0; j < n; ++j) {
-              const unsigned long long s = __shfl_sync(0xffffffffu, mine, j);
-              if (__shfl_sync(0xffffffffu, xi, j) >= xi) from_me += s;
+      if (tid == 0) sh.few_n = 0;
+      // mass from `top` up, and from `from` up; what lies below, about
+      unsigned long long above = 0ull, upper = 0ull, tail = 0ull;
+      unsigned long long sum = 0ull;
+      int looks = 0;
+      many_in(
+          w0, w1, from, INFINITY,
+          [&](const uint4 &r) {
+            if (exact) return;
+            float o[W];
+            unpack(r, o, T{});
+#pragma unroll
+            for (int e = 0; e < W; e += 2) {
+              const float2 y = unpack2(fma2(pack2(o[e], o[e + 1]), c2, e2));
+              const float one = exp2_approx(y.x), two = exp2_approx(y.y);
+              sum = add2(sum, pack2(o[e] < from ? one : 0.0f, o[e + 1] < from ? two : 0.0f));
             }
-            low = __reduce_max_sync(0xffffffffu, lane < n && from_me >= need ? float_order_key(xi) : 0u);
-            high = low;
-          }
-          while (low < high) {            // mass_from(low) reaches it
-            const uint32_t mid = low + (high - low) / 2 + 1;
-            if (mass_from(mid) >= need) low = mid;
-            else high = mid - 1;
-          }
-          const unsigned long long above = low == ~0u ? at.mass : mass_from(low + 1), of_one = weight<kHeld>(w, order_key_float(low));
-          if (lane == 0) {
-            sh.edge = order_key_float(low);
-            sh.ties = (need - above + of_one - 1) / of_one;
-          }
+            if (++looks % kVecs == 0) {
+              tail += static_cast<unsigned long long>((unpack2(sum).x + unpack2(sum).y) * static_cast<float>(1ull << kFraction));
+              sum = 0ull;
+            }
+          },
+          [&](float xi) {
+            const unsigned long long one = weight<kHeld>(w, xi);
+            upper += one;
+            if (xi >= top) {
+              above += one;
+            } else {
+              const int bin = bin_of(xi);
+              atomicAdd(&sh.h.count[bin], 1u);
+              add_mass(sh, bin, one);
+            }
+          });
+      above = warp_sum(above);
+      upper = warp_sum(upper);
+      tail = warp_sum(tail);
+      if (lane == 0) {
+        sh.above[warp] = above;
+        sh.warp_mass[warp] = upper;
+        sh.warp_tail[warp] = tail;
+      }
+      __syncthreads();
+      if (tid < cs) {
+        above = upper = tail = 0ull;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+          above += sh.above[i];
+          upper += sh.warp_mass[i];
+          tail += sh.warp_tail[i];
         }
-        __syncthreads();
-        lower(sh.edge, sh.ties);
-      } else if (found) {                 // too many of them
-        found = false;
-        break;
-      } else if (!estimated) {
+        peer_store64(peer_addr(&sh.from_total[cr], tid), above);
+        peer_store64(peer_addr(&sh.from_mass[cr], tid), upper);
+        peer_store64(peer_addr(&sh.from_tail[cr], tid), tail);
+      }
+      cluster_sync();
+      above = upper = tail = 0ull;
+      for (int i = 0; i < cs; ++i) {
+        above += sh.from_total[i];
+        upper += sh.from_mass[i];
+        tail += sh.from_tail[i];
+      }
+      // what top-p needs at least and at most
+      unsigned long long need, need_most;
+      if (exact) {
+        need = need_most = part_of(top_p, mass_k, true);
+      } else {
+        const unsigned long long slack = static_cast<unsigned long long>(static_cast<float>(tail) * off_by) + static_cast<unsigned long long>(v);
+        need = part_of(top_p, upper + (tail > slack ? tail - slack : 0ull), true);
+        need_most = part_of(top_p, upper + tail + slack, true);
+      }
+      Cross at;
+      if (need <= above) {                // above what is sure
+        guessed = false;
+        continue;
+      }
+      if (!find_cross(sh, true, need - above, at)) {
+        if (guessed) {
+          guessed = false;
+          continue;
+        }
         found = from == least;            // min-p keeps less
         break;
       }
+      if (at.in > kFew) break;
+      const unsigned long long before = above + at.mass;
+      // The bin's values to all CTAs: those between its ends, to the roundings of a difference and two products.
+      const float wide = 1e-6f * (fabsf(base) + fabsf(from));
+      each_in(w0, w1, fmaxf(from, base - (static_cast<float>(at.bin) + 1.01f) / scale - wide),
+              fminf(top, base - (static_cast<float>(at.bin) - 0.01f) / scale + wide), [&](float xi, int64_t) {
+                if (bin_of(xi) == static_cast<int>(at.bin)) {
+                  const int place = static_cast<int>(at.place) + atomicAdd(&sh.few_n, 1);
+                  for (int r = 0; r < cs; ++r) peer_store32(peer_addr(&sh.few.x[place], r), __float_as_uint(xi));
+                }
+              });
+      cluster_sync();
+      const int n = static_cast<int>(at.in);
+      if (tid < n) sh.few.mass[tid] = weight<kHeld>(w, sh.few.x[tid]);
+      __syncthreads();
+      if (warp == 0) {
+        // the largest key at which the mass from it up reaches what is needed: between the bin's ends, bit by bit
+        uint32_t high = 0u, low = ~0u;
+        for (int j = lane; j < n; j += 32) {
+          const uint32_t k = float_order_key(sh.few.x[j]);
+          high = max(high, k);
+          low = min(low, k);
+        }
+        high = __reduce_max_sync(0xffffffffu, high);
+        low = __reduce_min_sync(0xffffffffu, low);
+        const auto mass_from = [&](uint32_t k) {
+          unsigned long long s = 0ull;
+          for (int j = lane; j < n; j += 32)
+            if (float_order_key(sh.few.x[j]) >= k) s += sh.few.mass[j];
+          return before + warp_sum(s);
+        };
+        if (n <= 32) {                    // a lane a value
+          const float xi = lane < n ? sh.few.x[lane] : 0.0f;
+          const unsigned long long mine = lane < n ? sh.few.mass[lane] : 0ull;
+          unsigned long long from_me = before;   // of its equals and those above
+          for (int j = 0; j < n; ++j) {
+            const unsigned long long s = __shfl_sync(0xffffffffu, mine, j);
+            if (__shfl_sync(0xffffffffu, xi, j) >= xi) from_me += s;
+          }
+          low = __reduce_max_sync(0xffffffffu, lane < n && from_me >= need ? float_order_key(xi) : 0u);
+          high = low;
+        }
+        while (low < high) {              // mass_from(low) reaches it
+          const uint32_t mid = low + (high - low) / 2 + 1;
+          if (mass_from(mid) >= need) low = mid;
+          else high = mid - 1;
+        }
+        const unsigned long long over = low == ~0u ? before : mass_from(low + 1), of_one = weight<kHeld>(w, order_key_float(low));
+        if (lane == 0) {
+          sh.edge = order_key_float(low);
+          sh.ties = (need - over + of_one - 1) / of_one;
+          sh.reached = over + sh.ties * of_one;
+        }
+      }
+      __syncthreads();
+      if (sh.reached >= need_most) {      // the border of all that the mass may be
+        lower(sh.edge, sh.ties);
+        sure = top;
+        found = true;
+        break;
+      }
+      mass_k = row_mass();
+      exact = true;
     }
-    if (!found) select(true, need, true);
+    if (!found) {
+      sure = INFINITY;
+      cluster_sync();
+      if (!exact) mass_k = row_mass();
+      select(true, part_of(top_p, mass_k, true), true);
+    }
+  } else if (by_p) {
+    if (whole_row) mass_k = row_mass();
+    select(true, part_of(top_p, mass_k, true), true);
   }
 
   // kept mass and ties of the CTAs (the whole row's are known)
   if (!plain) {
     uint32_t equal;
-    const unsigned long long mass = part_kept(w0, w1, equal);
+    unsigned long long mass = part_kept(w0, w1, sure, equal);
+    if (sure < INFINITY) mass += sh.above[warp];
     __syncthreads();
     if (lane == 0) {
       sh.warp_mass[warp] = mass;
@@ -1033,7 +1184,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   {                                       // and of its sixteenths, a warp each
     const int64_t b0 = i0 + (i1 - i0) * warp / kWarps, b1 = i0 + (i1 - i0) * (warp + 1) / kWarps;
     uint32_t equal;
-    const unsigned long long mass = part_kept(b0, b1, equal);
+    const unsigned long long mass = part_kept(b0, b1, INFINITY, equal);
     __syncthreads();
     if (lane == 0) {
       sh.warp_mass[warp] = mass;
