@@ -36,6 +36,7 @@
 // ordered bits of the logits, 10 bits at a time.  Nothing is kept in global memory,
 // so calls may overlap.  A row that 16 CTAs cannot hold is read again for each pass.
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -49,9 +50,11 @@ constexpr int kCluster = 16;
 constexpr int kBins = 1024;
 constexpr int kFew = 512;                // values settled one by one
 constexpr int kGroups = 512;             // maxima of groups
+constexpr int kSample = 256;             // values of a warp that top-p's estimate takes
 constexpr int kStaged = 2;               // 16-byte vectors of a lane and step, of rows in shared memory
 constexpr int kRead = 4;                 // and of rows that are read again
 constexpr int kQueue = 32 * 16 * kWarps; // bytes of the warps' queues, for each vector of a step
+static_assert(kSample * 4 <= 32 * 16 * kStaged, "a warp's sample is in its queue");
 constexpr int kHeldTwo = 74 * 1024;      // bytes of a row in a CTA and its queues: two CTAs an SM
 constexpr int kHeldOne = 184 * 1024;     // one CTA an SM
 
@@ -123,8 +126,8 @@ __device__ __forceinline__ void weight_parts(const Weigher &w, float x, uint32_t
   high = __float_as_uint(up) - __float_as_uint(kRound);
   low = __float2int_rn(fmaf(fmaf(t.x, p, t.y), s, a - (up - kRound)));
 }
-// The same of two values at once, added to sums.
-__device__ __forceinline__ void weight_pair(const Weigher &w, float x0, float x1, uint32_t &highs, int &lows) {
+// The same of two values at once.
+__device__ __forceinline__ void weight_pair(const Weigher &w, float x0, float x1, uint32_t &high0, uint32_t &high1, int &low0, int &low1) {
   const unsigned long long x = pack2(fmaxf(x0, w.floor), fmaxf(x1, w.floor)), c1 = pack2(w.c1, w.c1), shift = pack2(kShift, kShift),
                            minus = pack2(-1.0f, -1.0f), round = pack2(kRound, kRound);
   const unsigned long long q = fma2(x, c1, shift), v = fma2(x, pack2(w.c2, w.c2), fma2(x, c1, fma2(q, minus, shift)));
@@ -137,8 +140,13 @@ __device__ __forceinline__ void weight_pair(const Weigher &w, float x0, float x1
   const unsigned long long t = pack2(t0.x, t1.x), a = mul2(t, s), up = add2(a, round);
   const unsigned long long rest = add2(a, fma2(up, minus, round));
   const float2 low = unpack2(fma2(fma2(t, p, pack2(t0.y, t1.y)), s, rest)), upf = unpack2(up);
-  highs += __float_as_uint(upf.x) + __float_as_uint(upf.y) - 2u * __float_as_uint(kRound);
-  lows += __float2int_rn(low.x) + __float2int_rn(low.y);
+  high0 = __float_as_uint(upf.x) - __float_as_uint(kRound);
+  high1 = __float_as_uint(upf.y) - __float_as_uint(kRound);
+  low0 = __float2int_rn(low.x);
+  low1 = __float2int_rn(low.y);
+}
+__device__ __forceinline__ unsigned long long whole_weight(uint32_t high, int low) {
+  return (static_cast<unsigned long long>(high) << kRoundBits) + static_cast<long long>(low);
 }
 template <bool kShort>                    // rows of at most 2^24 values
 __device__ __forceinline__ unsigned long long weight(const Weigher &w, float x) {
@@ -149,7 +157,7 @@ __device__ __forceinline__ unsigned long long weight(const Weigher &w, float x) 
     uint32_t high;
     int low;
     weight_parts(w, x, high, low);
-    r = (static_cast<unsigned long long>(high) << kRoundBits) + static_cast<long long>(low);
+    r = whole_weight(high, low);
   }
   return kShort ? r : r >> w.drop;
 }
@@ -237,16 +245,28 @@ struct Few {                             // values to settle one by one
   unsigned long long key[kFew], mass[kFew];
   float x[kFew];
 };
+struct Slice {                           // a CTA's bins of all CTAs' histograms
+  unsigned long long mass[kBins];
+  uint32_t number[kBins];
+};
+struct Edge {                            // top-p's last bin: all CTAs' values, and which warp this CTA's come from
+  unsigned long long mass[kFew];
+  float x[kFew];
+  uint8_t warp[kFew];
+};
 struct Shared {
   float2 table[kSteps];
-  union {                                // the few come from the histogram, when all CTAs have read it
+  union {                                // top-k does without a histogram
     Histogram h;
     Few few;
   };
-  unsigned long long mass[kBins];        // of the cluster, this CTA's slice; top-k's values, of all CTAs
-  uint32_t number[kBins];
+  union {                                // a slice is of no use once the bin is known
+    Slice slice;
+    Edge edge;
+    unsigned long long got[kBins];       // top-k's values, of all CTAs
+  };
   uint16_t place[kBins];                 // of a slice's bin and a CTA: values of the CTAs before it, up to kFew
-  uint32_t octave[kOctaves];             // mass of sampled values by the weight's power of two
+  uint32_t octave[2 * kOctaves];         // by the weight's power of two, in 256ths of it: sampled values; threads' maxima
   unsigned long long above[kWarps];      // mass of the warps' parts from a value up that is certainly kept
   float group[kGroups];                  // of the cluster
   Weigher w;
@@ -256,15 +276,14 @@ struct Shared {
   uint32_t sampled;
   unsigned long long warp_mass[kWarps], warp_tail[kWarps];
   uint32_t warp_count[kWarps];
-  float edge;                            // settled: the threshold, how many of its equals
+  float border;                          // settled: the threshold, how many of its equals, the mass up to there
   unsigned long long ties, reached;
   Cross cross;
   // from the cluster's CTAs
   unsigned long long from_total[kCluster], slice_mass[kCluster], from_mass[kCluster];
   uint32_t slice_count[kCluster], from_ties[kCluster], from_n[kCluster];
   unsigned long long from_tail[kCluster];
-  float from_about[kCluster];
-  uint32_t from_octave[kCluster][kOctaves], from_sampled[kCluster];
+  uint32_t from_octave[kCluster][2 * kOctaves], from_sampled[kCluster];
 };
 
 __device__ __forceinline__ void peer_load128(uint32_t a, uint32_t (&v)[4]) {
@@ -324,8 +343,8 @@ __device__ __forceinline__ bool find_cross(Shared &sh, bool by_mass, unsigned lo
       }
       sh.place[(bin + i) * cs + r] = static_cast<uint16_t>(min(count[i] - own, static_cast<uint32_t>(kFew)));
       if (r == cs - 1) {
-        sh.number[bin + i] = count[i];
-        sh.mass[bin + i] = mass;
+        sh.slice.number[bin + i] = count[i];
+        sh.slice.mass[bin + i] = mass;
       }
     }
   }
@@ -337,8 +356,8 @@ __device__ __forceinline__ bool find_cross(Shared &sh, bool by_mass, unsigned lo
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const bool in = i < each && tid * each + i < slice;
-    mass[i] = in ? sh.mass[tid * each + i] : 0ull;
-    count[i] = in ? sh.number[tid * each + i] : 0u;
+    mass[i] = in ? sh.slice.mass[tid * each + i] : 0ull;
+    count[i] = in ? sh.slice.number[tid * each + i] : 0u;
     sum += mass[i];
     number += count[i];
   }
@@ -477,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     sh.few_n = 0;
     sh.sampled = 0u;
   }
-  if (tid < kOctaves) sh.octave[tid] = 0u;
+  if (tid < 2 * kOctaves) sh.octave[tid] = 0u;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the logits and settings are complete
   if constexpr (kHeld) {
@@ -526,21 +545,37 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     for (int j = 0; j < kVecs; ++j) r[j] = i + 32 * j < end ? load_vec(i + 32 * j) : vec_lowest(T{});
   };
 
-  // the row's maximum, and those of its groups; a NaN stays one
+  // The row's maximum, and those of its groups; a NaN stays one.  For top-p also a sample: some vectors' first values,
+  // at most kSample of a warp, in its queue.
+  const bool estimate = by_p && !by_k;
+  const int apart = static_cast<int>((w1 - w0 + kSample - 1) / kSample);   // steps of which one is sampled
+  uint32_t sampled = 0u;
+  int samples = 0;
   float m = -INFINITY;
   {
     uint4 most = vec_lowest(T{});
+    int step = 0;
     for (int64_t i = w0 + lane; i - lane < w1; i += 32 * kVecs) {
       uint4 r[kVecs];
       fetch(i, w1, r);
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) most = vec_max_nan(most, r[j], T{});
+      if (estimate && --step < 0) {
+        step = apart - 1;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+          if (samples < kSample / 32) {
+            queue[samples++ * 32 + lane] = *reinterpret_cast<const T *>(&r[j]);
+            sampled += i + 32 * j < w1;
+          }
+      }
     }
     float o[W];
     unpack(most, o, T{});
 #pragma unroll
     for (int e = 0; e < W; ++e) m = max_nan(m, o[e]);
   }
+  const float own = m;
   for (int o = 16; o >= per_warp; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   cluster_wait();                         // every CTA of the cluster has started
   for (int i = lane; i < cs * per_warp; i += 32)   // a lane's m is its group's, of lane i mod per_warp
@@ -629,20 +664,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
     }
   };
-  // the same of many, through the warp's queue, so that all lanes have one at a time; look(vector) at all of them
-  const auto many_in = [&](int64_t i0, int64_t i1, float from, float to, auto &&look, auto &&each) {
+  // The same of many, through the warp's queue, so that all lanes have two at a time: pair(value, value), the second
+  // one -infinity where there is none, and done() after a step's.  look(vector) at all of them.
+  const auto many_in = [&](int64_t i0, int64_t i1, float from, auto bounded, float to, auto &&look, auto &&pair, auto &&done) {
     const auto least_in = least_from(from, T{}), least_over = least_from(to, T{});
     for (int64_t i = i0 + lane; i - lane < i1; i += 32 * kVecs) {
       uint4 r[kVecs];
       fetch(i, i1, r);
-      uint32_t some = 0u, over = 0u;
+      uint32_t some = 0u;
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) {
         some |= values_from(r[j], j, least_in);
-        over |= values_from(r[j], j, least_over);
         look(r[j]);
       }
-      some &= ~over;
+      if constexpr (decltype(bounded)::value) {
+        uint32_t over = 0u;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) over |= values_from(r[j], j, least_over);
+        some &= ~over;
+      }
       const int many = __popc(some);
       int at = many;
 #pragma unroll
@@ -651,33 +691,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         if (lane >= s) at += b;
       }
       const int all = __shfl_sync(0xffffffffu, at, 31);
-      if (all == 0) continue;
-      T *to_queue = queue + (at - many);
-      if (all < 32 * 2) {                 // from the bits that are set
-        for (; some != 0u; some &= some - 1) {
-          const int bit = __ffs(some) - 1;
-          *to_queue++ = from_float<T>(value_at(i + 32 * vector_of<T>(bit), value_of<T>(bit)));
-        }
-      } else {                            // from all of them
+      if (all > 0) {
+        T *to_queue = queue + (at - many);
+        if (all < 32 * 2) {               // from the bits that are set
+          for (; some != 0u; some &= some - 1) {
+            const int bit = __ffs(some) - 1;
+            *to_queue++ = from_float<T>(value_at(i + 32 * vector_of<T>(bit), value_of<T>(bit)));
+          }
+        } else {                          // from all of them
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-          const T *o = reinterpret_cast<const T *>(&r[j]);
+          for (int j = 0; j < kVecs; ++j) {
+            const T *o = reinterpret_cast<const T *>(&r[j]);
 #pragma unroll
-          for (int e = 0; e < W; ++e)
-            if (some & (1u << (sizeof(T) == 4 ? 4 * j + e : 4 * j + e / 2 + 16 * (e & 1)))) *to_queue++ = o[e];
+            for (int e = 0; e < W; ++e)
+              if (some & (1u << (sizeof(T) == 4 ? 4 * j + e : 4 * j + e / 2 + 16 * (e & 1)))) *to_queue++ = o[e];
+          }
         }
+        __syncwarp();
+        for (int k = lane; k < all; k += 64) pair(to_float(queue[k]), k + 32 < all ? to_float(queue[k + 32]) : -INFINITY);
+        __syncwarp();
       }
-      __syncwarp();
-      for (int k = lane; k < all; k += 32) each(to_float(queue[k]));
-      __syncwarp();
+      done();
     }
   };
-  const auto no_look = [](const uint4 &) {};
+  const auto nothing = [](const auto &...) {};
 
   // top-k: what reaches the bound, to the first CTA
   if (few_k) {
     const int room = kBins / cs;
-    const uint32_t to = peer_addr(&sh.mass[cr * room], 0);
+    const uint32_t to = peer_addr(&sh.got[cr * room], 0);
     each_in(w0, w1, sh.bound, INFINITY, [&](float xi, int64_t index) {
       const int at = atomicAdd(&sh.few_n, 1);
       if (at < room)
@@ -697,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       if (tid < n) {
         int r = 0, at = tid;
         for (; at >= static_cast<int>(sh.from_n[r]); ++r) at -= sh.from_n[r];
-        const unsigned long long entry = sh.mass[r * room + at];
+        const unsigned long long entry = sh.got[r * room + at];
         const float xi = __uint_as_float(static_cast<uint32_t>(entry >> 32));
         sh.few.x[tid] = xi;
         sh.few.key[tid] = argmax_key(xi, static_cast<uint32_t>(entry));
@@ -813,10 +855,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           unpack(r[j], o, T{});
 #pragma unroll
           for (int e = 0; e < W; e += 4) {
-            int low4 = 0;                 // below 2^29 each
-            weight_pair(w, o[e], o[e + 1], highs, low4);
-            weight_pair(w, o[e + 2], o[e + 3], highs, low4);
-            lows += low4;
+            uint32_t high[4];
+            int low[4];                   // below 2^29 each
+            weight_pair(w, o[e], o[e + 1], high[0], high[1], low[0], low[1]);
+            weight_pair(w, o[e + 2], o[e + 3], high[2], high[3], low[2], low[3]);
+            highs += high[0] + high[1] + high[2] + high[3];
+            lows += low[0] + low[1] + low[2] + low[3];
           }
         }
         if (++steps == 256) {             // 2^13 values
@@ -850,14 +894,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     for (int i = 0; i < cs; ++i) sum += sh.from_mass[i];
     return sum;
   };
-  // the mass of the values in (t, to) of vectors [i0, i1), and how many equal t
-  const auto part_kept = [&](int64_t i0, int64_t i1, float to, uint32_t &equal) {
+  // the mass of the values above t of vectors [i0, i1), and how many equal it
+  const auto part_kept = [&](int64_t i0, int64_t i1, uint32_t &equal) {
     unsigned long long s = 0ull;
     uint32_t n = 0u;
-    many_in(i0, i1, fmaxf(t, w.floor), to, no_look, [&](float xi) {
-      if (xi == t) ++n;
-      else s += weight<kHeld>(w, xi);
-    });
+    many_in(
+        i0, i1, fmaxf(t, w.floor), std::false_type{}, 0.0f, nothing,
+        [&](float xi, float xj) {
+          if (w.wide || w.drop > 0) {
+            s += xi == t ? 0ull : weight<kHeld>(w, xi);
+            s += xj == t || xj == -INFINITY ? 0ull : weight<kHeld>(w, xj);
+          } else {
+            uint32_t high[2];
+            int low[2];
+            weight_pair(w, xi == t ? -INFINITY : xi, xj == t ? -INFINITY : xj, high[0], high[1], low[0], low[1]);
+            s += whole_weight(high[0] + high[1], low[0] + low[1]);
+          }
+          n += (xi == t) + (xj == t && xj > -INFINITY);
+        },
+        nothing);
     equal = __reduce_add_sync(0xffffffffu, n);
     return warp_sum(s);
   };
@@ -866,78 +921,59 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   bool whole_row = !by_k;
   if (by_k) whole_row = !select(false, static_cast<unsigned long long>(top_k), by_p);
   if (plain) row_mass();
-  float sure = INFINITY;                  // from here up all is kept, its mass in sh.above
+  bool kept_known = false;                // the warps' kept mass and ties are in sh.above and sh.warp_count
   if (by_p && whole_row && !w.wide && w.drop == 0) {
-    // The row's mass and where it lies, about: exponentials in 32 bits, some of them by octave.
+    // Where the row's mass lies, about: by octave from the sample and, as that has few of the largest values, from the
+    // threads' maxima.
     const unsigned long long c2 = pack2(w.c0, w.c0), e2 = pack2(-w.e, -w.e);
-    const int others = v <= 65536 ? 0 : 3;   // vectors that are not sampled for one that is
-    {
-      float about = 0.0f;
-      uint32_t sampled = 0u;
-      int step = 0;
-      for (int64_t i = w0 + lane; i - lane < w1; i += 32 * kVecs) {
-        uint4 r[kVecs];
-        fetch(i, w1, r);
-        unsigned long long sum = 0ull;
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j, ++step) {
-          float o[W];
-          unpack(r[j], o, T{});
-#pragma unroll
-          for (int e = 0; e < W; e += 2) {
-            const float2 y = unpack2(fma2(pack2(o[e], o[e + 1]), c2, e2));
-            const float one = exp2_approx(y.x);
-            sum = add2(sum, pack2(one, exp2_approx(y.y)));
-            if (e == 0 && (step & others) == 0 && i + 32 * j < w1) {
-              const uint32_t bits = __float_as_uint(one);
-              atomicAdd(&sh.octave[min(max(127 - static_cast<int>(bits >> 23), 0), kOctaves - 1)], 256u + ((bits >> 15) & 255u));
-              ++sampled;
-            }
-          }
-        }
-        about += unpack2(sum).x + unpack2(sum).y;
-      }
-      for (int o = 16; o > 0; o >>= 1) about += __shfl_xor_sync(0xffffffffu, about, o);
-      sampled = __reduce_add_sync(0xffffffffu, sampled);
-      if (lane == 0) {
-        atomicAdd(&sh.sampled, sampled);
-        sh.warp_mass[warp] = __float_as_uint(about);
-      }
-    }
+    const auto into = [&](float xi, uint32_t *octave) {
+      const uint32_t bits = __float_as_uint(exp2_approx(fmaf(xi, w.c0, -w.e)));
+      const int o = max(127 - static_cast<int>(bits >> 23), 0);
+      if (o < kOctaves) atomicAdd(octave + o, 256u + ((bits >> 15) & 255u));
+    };
+    into(own, sh.octave + kOctaves);
+    for (int i = 0; i < samples; ++i) into(to_float(queue[i * 32 + lane]), sh.octave);
+    sampled = __reduce_add_sync(0xffffffffu, sampled);
+    if (lane == 0) atomicAdd(&sh.sampled, sampled);
     __syncthreads();
-    for (int i = tid; i < cs * kOctaves; i += kThreads)
-      peer_store32(peer_addr(&sh.from_octave[cr][i % kOctaves], i / kOctaves), sh.octave[i % kOctaves]);
-    if (tid < cs) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) sum += __uint_as_float(static_cast<uint32_t>(sh.warp_mass[i]));
-      peer_store32(peer_addr(&sh.from_about[cr], tid), __float_as_uint(sum));
-      peer_store32(peer_addr(&sh.from_sampled[cr], tid), sh.sampled);
-    }
+    for (int i = tid; i < cs * 2 * kOctaves; i += kThreads)
+      peer_store32(peer_addr(&sh.from_octave[cr][i % (2 * kOctaves)], i / (2 * kOctaves)), sh.octave[i % (2 * kOctaves)]);
+    if (tid < cs) peer_store32(peer_addr(&sh.from_sampled[cr], tid), sh.sampled);
     clear();
     cluster_sync();
-    float about = 0.0f, sampled = 0.0f, mine[2] = {0.0f, 0.0f};   // of the lane's two octaves
-    for (int r = 0; r < cs; ++r) {
-      about += sh.from_about[r];
-      sampled += static_cast<float>(sh.from_sampled[r]);
-      mine[0] += static_cast<float>(sh.from_octave[r][lane]);
-      if (lane < kOctaves - 32) mine[1] += static_cast<float>(sh.from_octave[r][lane + 32]);
+    float number = 0.0f, mine[2] = {0.0f, 0.0f}, largest = 0.0f;   // of the lane's two octaves
+    for (int r = 0; r < cs; ++r) number += static_cast<float>(sh.from_sampled[r]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (lane + 32 * h < kOctaves) {
+        float some = 0.0f, high = 0.0f;
+        for (int r = 0; r < cs; ++r) {
+          some += static_cast<float>(sh.from_octave[r][lane + 32 * h]);
+          high += static_cast<float>(sh.from_octave[r][kOctaves + lane + 32 * h]);
+        }
+        const float unit = exp2f(-8.0f - static_cast<float>(lane + 32 * h));
+        // one of the largest in the sample would stand for many that are not there: 16 at least
+        mine[h] = fmaxf(some >= 16.0f * 384.0f ? some * (static_cast<float>(v) / fmaxf(number, 1.0f)) : 0.0f, high) * unit;
+        largest += high * unit;
+      }
+    float about = mine[0] + mine[1];
+    for (int o = 16; o > 0; o >>= 1) {
+      about += __shfl_xor_sync(0xffffffffu, about, o);
+      largest += __shfl_xor_sync(0xffffffffu, largest, o);
     }
-    // Below this a value cannot be the border: all such values together weigh less than 1 - p.  It counts every
-    // value at its most.
-    const float share = (1.0f - top_p) * about / static_cast<float>(v);
-    const float lowest = fmaxf(fmaxf(w.floor, least), fmaf(__log2f(share * 0.99f) + w.e, 1.0f / w.c0, -1e-4f * temperature - 1e-5f * fabsf(m)));
-    // By the sampled octaves, the border lies above where seven tenths of 1 - p lie below, and below where that is
-    // fourteen; a border that is not there is not found there.
+    // Below this a value cannot be the border: all such values together weigh less than 1 - p of the maxima alone.
+    const float share = (1.0f - top_p) * largest / static_cast<float>(v);
+    const float lowest = fmaxf(fmaxf(w.floor, least), fmaf(__log2f(share * 0.98f) + w.e, 1.0f / w.c0, -1e-4f * temperature - 1e-5f * fabsf(m)));
+    // By the octaves, the border lies above where seven tenths of 1 - p lie below, and below where that is fourteen; a
+    // border that is not there is not found there.
     float guess = lowest, sure_guess = INFINITY;
     {
-      const float unit = static_cast<float>(v) / fmaxf(sampled, 1.0f) / 256.0f;
       const float enough = (1.0f - top_p) * about;
       float below = 0.0f;
       int low_cut = kOctaves, high_cut = -1;
 #pragma unroll
       for (int h = 1; h >= 0; --h) {
-        float s = mine[h] * unit * exp2f(-static_cast<float>(lane + 32 * h));
+        float s = mine[h];
         for (int o = 1; o < 32; o <<= 1) {
           const float t = __shfl_down_sync(0xffffffffu, s, o);
           if (lane + o < 32) s += t;
@@ -955,9 +991,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     // What the mass below may be off by: the products' roundings (of log2(e) / T too), 2 ulp of an exponential, 16 additions, and
     // half of the last place of every weight.
     const float off_by = 0.6931472f * 0x1p-24f * (44.0f + fmaxf(fabsf(m), fabsf(w.floor)) * w.c0) + 0x1p-22f + 0x1.1p-20f + 0x1p-32f;
-    bool exact = false, guessed = guess > lowest || sure_guess < INFINITY, found = false;
+    bool settled = false, guessed = guess > lowest || sure_guess < INFINITY, found = false;
 #pragma unroll 1
-    for (int attempt = 0; attempt < 4; ++attempt) {
+    for (int attempt = 0; attempt < 2 && !found; ++attempt) {
       const float from = guessed ? guess : lowest, top = guessed ? sure_guess : INFINITY, base = fminf(top, m);
       const float reach = base - from, scale = reach > 0.0f ? fminf((kBins - 0.5f) / reach, 1e30f) : 0.0f;
       const auto bin_of = [&](float xi) { return min(static_cast<int>((base - xi) * scale), kBins - 1); };
@@ -967,13 +1003,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
       if (tid == 0) sh.few_n = 0;
       // mass from `top` up, and from `from` up; what lies below, about
-      unsigned long long above = 0ull, upper = 0ull, tail = 0ull;
-      unsigned long long sum = 0ull;
-      int looks = 0;
+      unsigned long long above = 0ull, upper = 0ull, tail = 0ull, sum = 0ull;
+      const auto binned = [&](float xi, uint32_t high, int low) {
+        const unsigned long long one = whole_weight(high, low);
+        above -= one;                     // of all, what goes into the histogram
+        const int bin = bin_of(xi);
+        atomicAdd(&sh.h.count[bin], 1u);
+        add_mass(sh, bin, one);
+      };
       many_in(
-          w0, w1, from, INFINITY,
+          w0, w1, from, std::false_type{}, 0.0f,
           [&](const uint4 &r) {
-            if (exact) return;
             float o[W];
             unpack(r, o, T{});
 #pragma unroll
@@ -982,22 +1022,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
               const float one = exp2_approx(y.x), two = exp2_approx(y.y);
               sum = add2(sum, pack2(o[e] < from ? one : 0.0f, o[e + 1] < from ? two : 0.0f));
             }
-            if (++looks % kVecs == 0) {
-              tail += static_cast<unsigned long long>((unpack2(sum).x + unpack2(sum).y) * static_cast<float>(1ull << kFraction));
-              sum = 0ull;
-            }
           },
-          [&](float xi) {
-            const unsigned long long one = weight<kHeld>(w, xi);
-            upper += one;
-            if (xi >= top) {
-              above += one;
-            } else {
-              const int bin = bin_of(xi);
-              atomicAdd(&sh.h.count[bin], 1u);
-              add_mass(sh, bin, one);
-            }
+          [&](float xi, float xj) {
+            uint32_t high[2];
+            int low[2];
+            weight_pair(w, xi, xj, high[0], high[1], low[0], low[1]);
+            upper += whole_weight(high[0] + high[1], low[0] + low[1]);
+            if (xi < top) binned(xi, high[0], low[0]);
+            if (xj < top && xj > -INFINITY) binned(xj, high[1], low[1]);
+          },
+          [&]() {
+            tail += static_cast<unsigned long long>((unpack2(sum).x + unpack2(sum).y) * static_cast<float>(1ull << kFraction));
+            sum = 0ull;
           });
+      above += upper;
       above = warp_sum(above);
       upper = warp_sum(upper);
       tail = warp_sum(tail);
@@ -1026,98 +1064,129 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         upper += sh.from_mass[i];
         tail += sh.from_tail[i];
       }
-      // what top-p needs at least and at most
-      unsigned long long need, need_most;
-      if (exact) {
-        need = need_most = part_of(top_p, mass_k, true);
-      } else {
-        const unsigned long long slack = static_cast<unsigned long long>(static_cast<float>(tail) * off_by) + static_cast<unsigned long long>(v);
-        need = part_of(top_p, upper + (tail > slack ? tail - slack : 0ull), true);
-        need_most = part_of(top_p, upper + tail + slack, true);
-      }
-      Cross at;
-      if (need <= above) {                // above what is sure
-        guessed = false;
-        continue;
-      }
-      if (!find_cross(sh, true, need - above, at)) {
-        if (guessed) {
-          guessed = false;
-          continue;
+      // What top-p needs at least and at most; where that leaves two borders, the row's mass itself.
+#pragma unroll 1
+      for (int exact = 0; exact < 2 && !found; ++exact) {
+        const unsigned long long slack =
+            exact ? 0ull : static_cast<unsigned long long>(static_cast<float>(tail) * off_by) + static_cast<unsigned long long>(v);
+        if (exact) {
+          cluster_sync();                 // all have read what came before
+          mass_k = row_mass();
         }
-        found = from == least;            // min-p keeps less
-        break;
-      }
-      if (at.in > kFew) break;
-      const unsigned long long before = above + at.mass;
-      // The bin's values to all CTAs: those between its ends, to the roundings of a difference and two products.
-      const float wide = 1e-6f * (fabsf(base) + fabsf(from));
-      each_in(w0, w1, fmaxf(from, base - (static_cast<float>(at.bin) + 1.01f) / scale - wide),
-              fminf(top, base - (static_cast<float>(at.bin) - 0.01f) / scale + wide), [&](float xi, int64_t) {
-                if (bin_of(xi) == static_cast<int>(at.bin)) {
-                  const int place = static_cast<int>(at.place) + atomicAdd(&sh.few_n, 1);
-                  for (int r = 0; r < cs; ++r) peer_store32(peer_addr(&sh.few.x[place], r), __float_as_uint(xi));
-                }
-              });
-      cluster_sync();
-      const int n = static_cast<int>(at.in);
-      if (tid < n) sh.few.mass[tid] = weight<kHeld>(w, sh.few.x[tid]);
-      __syncthreads();
-      if (warp == 0) {
-        // the largest key at which the mass from it up reaches what is needed: between the bin's ends, bit by bit
-        uint32_t high = 0u, low = ~0u;
-        for (int j = lane; j < n; j += 32) {
-          const uint32_t k = float_order_key(sh.few.x[j]);
-          high = max(high, k);
-          low = min(low, k);
+        const unsigned long long need = part_of(top_p, exact ? mass_k : upper + (tail > slack ? tail - slack : 0ull), true),
+                                 need_most = exact ? need : part_of(top_p, upper + tail + slack, true);
+        if (need <= above) break;         // above what is sure
+        Cross at;
+        if (!find_cross(sh, true, need - above, at)) {
+          settled = !guessed && from == least;   // min-p keeps less
+          break;
         }
-        high = __reduce_max_sync(0xffffffffu, high);
-        low = __reduce_min_sync(0xffffffffu, low);
-        const auto mass_from = [&](uint32_t k) {
-          unsigned long long s = 0ull;
-          for (int j = lane; j < n; j += 32)
-            if (float_order_key(sh.few.x[j]) >= k) s += sh.few.mass[j];
-          return before + warp_sum(s);
+        if (at.in > kFew) break;
+        const unsigned long long before = above + at.mass;
+        // One more pass from the bin's lower end up, to the roundings of a difference and two products: the bin's values to
+        // all CTAs, and the mass between it and what is sure.
+        const float wide = 1e-6f * (fabsf(base) + fabsf(from));
+        const float low_end = fmaxf(from, base - (static_cast<float>(at.bin) + 1.01f) / scale - wide);
+        const float high_end = base - (static_cast<float>(at.bin) - 0.01f) / scale + wide;   // from here up no value is in the bin
+        const auto hand = [&](float xi) {
+          const int place = static_cast<int>(at.place) + atomicAdd(&sh.few_n, 1);
+          for (int r = 0; r < cs; ++r) peer_store32(peer_addr(&sh.edge.x[place], r), __float_as_uint(xi));
+          sh.edge.warp[place] = static_cast<uint8_t>(warp);
         };
-        if (n <= 32) {                    // a lane a value
-          const float xi = lane < n ? sh.few.x[lane] : 0.0f;
-          const unsigned long long mine = lane < n ? sh.few.mass[lane] : 0ull;
-          unsigned long long from_me = before;   // of its equals and those above
-          for (int j = 0; j < n; ++j) {
-            const unsigned long long s = __shfl_sync(0xffffffffu, mine, j);
-            if (__shfl_sync(0xffffffffu, xi, j) >= xi) from_me += s;
+        unsigned long long between = 0ull;
+        many_in(
+            w0, w1, low_end, std::true_type{}, top, nothing,
+            [&](float xi, float xj) {
+              // which side of the bin a value of its neighbourhood is on, the bins say
+              bool i_over = xi >= high_end, j_over = xj >= high_end;
+              if (!i_over) {
+                const int bin = bin_of(xi);
+                if (bin == static_cast<int>(at.bin)) hand(xi);
+                i_over = bin < static_cast<int>(at.bin);
+              }
+              if (!j_over && xj > -INFINITY) {
+                const int bin = bin_of(xj);
+                if (bin == static_cast<int>(at.bin)) hand(xj);
+                j_over = bin < static_cast<int>(at.bin);
+              }
+              uint32_t high[2];
+              int low[2];
+              weight_pair(w, i_over ? xi : -INFINITY, j_over ? xj : -INFINITY, high[0], high[1], low[0], low[1]);
+              between += whole_weight(high[0] + high[1], low[0] + low[1]);
+            },
+            nothing);
+        between = warp_sum(between);
+        cluster_sync();
+        const int n = static_cast<int>(at.in);
+        if (tid < n) sh.edge.mass[tid] = weight<kHeld>(w, sh.edge.x[tid]);
+        __syncthreads();
+        if (warp == 0) {
+          // the largest key at which the mass from it up reaches what is needed: between the bin's ends, bit by bit
+          uint32_t high = 0u, low = ~0u;
+          for (int j = lane; j < n; j += 32) {
+            const uint32_t k = float_order_key(sh.edge.x[j]);
+            high = max(high, k);
+            low = min(low, k);
           }
-          low = __reduce_max_sync(0xffffffffu, lane < n && from_me >= need ? float_order_key(xi) : 0u);
-          high = low;
+          high = __reduce_max_sync(0xffffffffu, high);
+          low = __reduce_min_sync(0xffffffffu, low);
+          const auto mass_from = [&](uint32_t k) {
+            unsigned long long s = 0ull;
+            for (int j = lane; j < n; j += 32)
+              if (float_order_key(sh.edge.x[j]) >= k) s += sh.edge.mass[j];
+            return before + warp_sum(s);
+          };
+          if (n <= 32) {                  // a lane a value
+            const float xi = lane < n ? sh.edge.x[lane] : 0.0f;
+            const unsigned long long mine = lane < n ? sh.edge.mass[lane] : 0ull;
+            unsigned long long from_me = before;   // of its equals and those above
+            for (int j = 0; j < n; ++j) {
+              const unsigned long long s = __shfl_sync(0xffffffffu, mine, j);
+              if (__shfl_sync(0xffffffffu, xi, j) >= xi) from_me += s;
+            }
+            low = __reduce_max_sync(0xffffffffu, lane < n && from_me >= need ? float_order_key(xi) : 0u);
+            high = low;
+          }
+          while (low < high) {            // mass_from(low) reaches it
+            const uint32_t mid = low + (high - low) / 2 + 1;
+            if (mass_from(mid) >= need) low = mid;
+            else high = mid - 1;
+          }
+          const unsigned long long over = low == ~0u ? before : mass_from(low + 1), of_one = weight<kHeld>(w, order_key_float(low));
+          if (lane == 0) {
+            sh.border = order_key_float(low);
+            sh.ties = (need - over + of_one - 1) / of_one;
+            sh.reached = over + sh.ties * of_one;
+          }
         }
-        while (low < high) {              // mass_from(low) reaches it
-          const uint32_t mid = low + (high - low) / 2 + 1;
-          if (mass_from(mid) >= need) low = mid;
-          else high = mid - 1;
+        __syncthreads();
+        if (sh.reached >= need_most) {    // the border of all that the mass may be
+          lower(sh.border, sh.ties);
+          found = true;
+          // what the warps keep: all above the bin, and of the bin
+          if (lane == 0) sh.above[warp] += between;
+          if (tid < kWarps) sh.warp_count[tid] = 0u;
+          __syncthreads();
+          const int own_n = sh.few_n;
+          for (int j = tid; j < own_n; j += kThreads) {
+            const int k = static_cast<int>(at.place) + j;
+            const float xi = sh.edge.x[k];
+            if (xi > t) atomicAdd(&sh.above[sh.edge.warp[k]], sh.edge.mass[k]);
+            else if (xi == t) atomicAdd(&sh.warp_count[sh.edge.warp[k]], 1u);
+          }
+          __syncthreads();
         }
-        const unsigned long long over = low == ~0u ? before : mass_from(low + 1), of_one = weight<kHeld>(w, order_key_float(low));
-        if (lane == 0) {
-          sh.edge = order_key_float(low);
-          sh.ties = (need - over + of_one - 1) / of_one;
-          sh.reached = over + sh.ties * of_one;
-        }
+        if (tid == 0) sh.few_n = 0;       // read before the barrier
       }
-      __syncthreads();
-      if (sh.reached >= need_most) {      // the border of all that the mass may be
-        lower(sh.edge, sh.ties);
-        sure = top;
-        found = true;
-        break;
-      }
-      mass_k = row_mass();
-      exact = true;
+      if (!found && (settled || !guessed)) break;
+      guessed = false;
     }
-    if (!found) {
-      sure = INFINITY;
+    if (!found && !settled) {
       cluster_sync();
-      if (!exact) mass_k = row_mass();
+      mass_k = row_mass();
       select(true, part_of(top_p, mass_k, true), true);
     }
+    kept_known = found;
   } else if (by_p) {
     if (whole_row) mass_k = row_mass();
     select(true, part_of(top_p, mass_k, true), true);
@@ -1125,13 +1194,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 
   // kept mass and ties of the CTAs (the whole row's are known)
   if (!plain) {
-    uint32_t equal;
-    unsigned long long mass = part_kept(w0, w1, sure, equal);
-    if (sure < INFINITY) mass += sh.above[warp];
+    uint32_t equal = 0u;
+    unsigned long long mass = 0ull;
+    if (!kept_known) mass = part_kept(w0, w1, equal);
     __syncthreads();
     if (lane == 0) {
-      sh.warp_mass[warp] = mass;
-      sh.warp_count[warp] = equal;
+      sh.warp_mass[warp] = kept_known ? sh.above[warp] : mass;
+      if (!kept_known) sh.warp_count[warp] = equal;
     }
     __syncthreads();
     unsigned long long sum = 0ull;
@@ -1184,7 +1253,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   {                                       // and of its sixteenths, a warp each
     const int64_t b0 = i0 + (i1 - i0) * warp / kWarps, b1 = i0 + (i1 - i0) * (warp + 1) / kWarps;
     uint32_t equal;
-    const unsigned long long mass = part_kept(b0, b1, INFINITY, equal);
+    const unsigned long long mass = part_kept(b0, b1, equal);
     __syncthreads();
     if (lane == 0) {
       sh.warp_mass[warp] = mass;
