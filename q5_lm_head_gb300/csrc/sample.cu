@@ -148,18 +148,13 @@ __device__ __forceinline__ void weight_pair(const Weigher &w, float x0, float x1
 __device__ __forceinline__ unsigned long long whole_weight(uint32_t high, int low) {
   return (static_cast<unsigned long long>(high) << kRoundBits) + static_cast<long long>(low);
 }
-template <bool kShort>                    // rows of at most 2^24 values
-__device__ __forceinline__ unsigned long long weight(const Weigher &w, float x) {
-  unsigned long long r;
-  if (w.wide) {
-    r = wide_weight(x, w.m, w.c);
-  } else {
-    uint32_t high;
-    int low;
-    weight_parts(w, x, high, low);
-    r = whole_weight(high, low);
-  }
-  return kShort ? r : r >> w.drop;
+// A weight by itself.  Out of line: a kernel full of them waits for its own code.
+__device__ __noinline__ unsigned long long weight(const Weigher &w, float x) {
+  if (w.wide) return wide_weight(x, w.m, w.c) >> w.drop;
+  uint32_t high;
+  int low;
+  weight_parts(w, x, high, low);
+  return whole_weight(high, low) >> w.drop;
 }
 
 // floor(f k), or the next whole number up, of 0 < f < 1.
@@ -216,21 +211,29 @@ __device__ __forceinline__ float least_from(float v, float) { return v; }
 __device__ __forceinline__ __half2 least_from(float v, __half) { return __half2half2(__float2half_ru(v)); }
 __device__ __forceinline__ __nv_bfloat162 least_from(float v, __nv_bfloat16) { return __bfloat162bfloat162(__float2bfloat16_ru(v)); }
 // Bits of a vector's values from there up: value e of vector j at bit 4 j + e, of 16-bit
-// types at 4 j + e / 2 + 16 (e mod 2).
-__device__ __forceinline__ uint32_t values_from(const uint4 &r, int j, float from) {
+// types at 4 j + e / 2 + 16 (e mod 2).  The vector keeps the others, -infinity for these.
+__device__ __forceinline__ uint32_t values_from(uint4 &r, int j, float from) {
   uint32_t m = 0u;
-  if (__uint_as_float(r.x) >= from) m |= 1u << (4 * j);
-  if (__uint_as_float(r.y) >= from) m |= 2u << (4 * j);
-  if (__uint_as_float(r.z) >= from) m |= 4u << (4 * j);
-  if (__uint_as_float(r.w) >= from) m |= 8u << (4 * j);
+  uint32_t *w = &r.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (__uint_as_float(w[i]) >= from) {
+      m |= 1u << (4 * j + i);
+      w[i] = 0xFF800000u;
+    }
   return m;
 }
 template <typename T2>
-__device__ __forceinline__ uint32_t values_from(const uint4 &r, int j, T2 from) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+__device__ __forceinline__ uint32_t values_from(uint4 &r, int j, T2 from) {
+  constexpr uint32_t kNone = sizeof(T2) == 4 && std::is_same_v<T2, __half2> ? 0xFC00FC00u : 0xFF80FF80u;
   uint32_t m = 0u;
+  uint32_t *w = &r.x;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m |= __hge2_mask(*reinterpret_cast<const T2 *>(&w[i]), from) & (0x00010001u << (4 * j + i));
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t over = __hge2_mask(*reinterpret_cast<const T2 *>(&w[i]), from);
+    m |= over & (0x00010001u << (4 * j + i));
+    w[i] = (w[i] & ~over) | (kNone & over);
+  }
   return m;
 }
 template <typename T>
@@ -279,6 +282,11 @@ struct Shared {
   float border;                          // settled: the threshold, how many of its equals, the mass up to there
   unsigned long long ties, reached;
   Cross cross;
+  int cross_found;
+  float lowest, guess, sure_guess;       // top-p's estimates
+  unsigned long long above_all, need, need_most;
+  unsigned long long total, target, upto, left, of_tie;   // of the draw
+  int part;
   // from the cluster's CTAs
   unsigned long long from_total[kCluster], slice_mass[kCluster], from_mass[kCluster];
   uint32_t slice_count[kCluster], from_ties[kCluster], from_n[kCluster];
@@ -349,101 +357,113 @@ __device__ __forceinline__ bool find_cross(Shared &sh, bool by_mass, unsigned lo
     }
   }
   __syncthreads();
-  constexpr int kEach = kBins / kThreads;   // bins of a thread, with one CTA
-  const int each = slice > kThreads ? slice / kThreads : 1;
-  unsigned long long mass[kEach], sum = 0ull;
-  uint32_t count[kEach], number = 0u;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const bool in = i < each && tid * each + i < slice;
-    mass[i] = in ? sh.slice.mass[tid * each + i] : 0ull;
-    count[i] = in ? sh.slice.number[tid * each + i] : 0u;
-    sum += mass[i];
-    number += count[i];
-  }
-  unsigned long long upto = sum;
-  uint32_t upto_n = number;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long a = __shfl_up_sync(0xffffffffu, upto, o);
-    const uint32_t b = __shfl_up_sync(0xffffffffu, upto_n, o);
-    if (lane >= o) {
-      upto += a;
-      upto_n += b;
+  // a warp's lanes take the slice's bins, up to 32 each
+  const int each = slice / 32;
+  unsigned long long before = 0ull;
+  uint32_t before_n = 0u;
+  if (warp == 0) {
+    unsigned long long sum = 0ull;
+    uint32_t number = 0u;
+    for (int i = 0; i < each; ++i) {      // each lane from a place of its own, on banks of its own
+      const int at = lane * each + ((i + lane) & (each - 1));
+      sum += sh.slice.mass[at];
+      number += sh.slice.number[at];
     }
-  }
-  if (lane == 31) {
-    sh.warp_mass[warp] = upto;
-    sh.warp_count[warp] = upto_n;
-  }
-  __syncthreads();
-  unsigned long long total = 0ull, before = upto - sum;
-  uint32_t total_n = 0u, before_n = upto_n - number;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < warp) {
-      before += sh.warp_mass[i];
-      before_n += sh.warp_count[i];
+    before = sum;
+    before_n = number;
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long a = __shfl_up_sync(0xffffffffu, before, o);
+      const uint32_t b = __shfl_up_sync(0xffffffffu, before_n, o);
+      if (lane >= o) {
+        before += a;
+        before_n += b;
+      }
     }
-    total += sh.warp_mass[i];
-    total_n += sh.warp_count[i];
-  }
-  if (tid < cs) {
-    peer_store64(peer_addr(&sh.slice_mass[cr], tid), total);
-    peer_store32(peer_addr(&sh.slice_count[cr], tid), total_n);
+    const unsigned long long all = __shfl_sync(0xffffffffu, before, 31);
+    const uint32_t all_n = __shfl_sync(0xffffffffu, before_n, 31);
+    if (lane < cs) {
+      peer_store64(peer_addr(&sh.slice_mass[cr], lane), all);
+      peer_store32(peer_addr(&sh.slice_count[cr], lane), all_n);
+    }
+    before -= sum;
+    before_n -= number;
   }
   cluster_sync();
-  total = 0ull;
-  total_n = 0u;
-#pragma unroll
-  for (int r = 0; r < kCluster; ++r) {
-    if (r >= cs) break;
-    if (r < cr) {
-      before += sh.slice_mass[r];
-      before_n += sh.slice_count[r];
-    }
-    total += sh.slice_mass[r];
-    total_n += sh.slice_count[r];
-  }
-  if ((by_mass ? total : total_n) < target) return false;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const unsigned long long b = by_mass ? before : before_n, in = by_mass ? mass[i] : count[i];
-    const uint32_t here = __ballot_sync(0xffffffffu, in > 0ull && b < target && b + in >= target);
-    if (here) {                           // a lane for each CTA
-      const int from = __ffs(here) - 1, at = __shfl_sync(0xffffffffu, tid * each + i, from);
-      const unsigned long long mass_before = __shfl_sync(0xffffffffu, before, from);
-      const uint32_t count_before = __shfl_sync(0xffffffffu, before_n, from), number_in = __shfl_sync(0xffffffffu, count[i], from);
+  if (warp == 0) {
+    unsigned long long mine = lane < cs ? sh.slice_mass[lane] : 0ull, total = mine;
+    uint32_t mine_n = lane < cs ? sh.slice_count[lane] : 0u;
+    total = warp_sum(mine);
+    const uint32_t total_n = __reduce_add_sync(0xffffffffu, mine_n);
+    before += warp_sum(lane < cr ? mine : 0ull);
+    before_n += __reduce_add_sync(0xffffffffu, lane < cr ? mine_n : 0u);
+    if (lane == 0) sh.cross_found = (by_mass ? total : total_n) >= target;
+    // the lane whose bins it is in, and the bin
+    unsigned long long sum = by_mass ? before : before_n;
+    int at = -1;
+    if (sum < target)
+      for (int i = 0; i < each; ++i) {
+        const unsigned long long m = sh.slice.mass[lane * each + i];
+        const uint32_t n = sh.slice.number[lane * each + i];
+        sum += by_mass ? m : n;
+        if (sum >= target) {
+          at = lane * each + i;
+          break;
+        }
+        before += m;
+        before_n += n;
+      }
+    const uint32_t here = __ballot_sync(0xffffffffu, at >= 0);
+    if (here) {                           // the first of them; a lane for each CTA
+      const int from = __ffs(here) - 1;
+      at = __shfl_sync(0xffffffffu, at, from);
+      before = __shfl_sync(0xffffffffu, before, from);
+      before_n = __shfl_sync(0xffffffffu, before_n, from);
       if (lane < cs) {
-        peer_store64(peer_addr(&sh.cross.mass, lane), mass_before);
-        peer_store32(peer_addr(&sh.cross.count, lane), count_before);
+        peer_store64(peer_addr(&sh.cross.mass, lane), before);
+        peer_store32(peer_addr(&sh.cross.count, lane), before_n);
         peer_store32(peer_addr(&sh.cross.bin, lane), cr * slice + at);
-        peer_store32(peer_addr(&sh.cross.in, lane), number_in);
+        peer_store32(peer_addr(&sh.cross.in, lane), sh.slice.number[at]);
         peer_store32(peer_addr(&sh.cross.place, lane), sh.place[at * cs + lane]);
       }
     }
-    before += mass[i];
-    before_n += count[i];
   }
   cluster_sync();
   out = sh.cross;
-  return true;
+  return sh.cross_found;
 }
 
-// log(total / one) of whole numbers, total >= one: 512ths of the exponent from the
-// table, what is left (below 2^-9) by its series.
-__device__ __forceinline__ double log_ratio(const float2 *table, unsigned long long total, unsigned long long one) {
-  const double r = static_cast<double>(total) / static_cast<double>(one);
-  const int e = static_cast<int>((__double_as_longlong(r) >> 52) & 2047) - 1023;
-  const double man = __longlong_as_double((__double_as_longlong(r) & 0xFFFFFFFFFFFFFll) | 0x3FF0000000000000ll);
-  int i = static_cast<int>(__log2f(static_cast<float>(man)) * kSteps);
-  i = min(max(i, 0), kSteps - 1);
-  const float2 t = table[i];
-  const double d = man - (static_cast<double>(t.x) + t.y);
-  const float f = static_cast<float>(d) / t.x;
-  const double correction = (d - static_cast<double>(f) * (static_cast<double>(t.x) + t.y));   // of the division, in units of t
-  return static_cast<double>(e * kSteps + i) * (0.6931471805599453 / kSteps) +
-         (static_cast<double>(f) + static_cast<double>(fmaf(f * f, fmaf(f, 1.0f / 3.0f, -0.5f), static_cast<float>(correction) / t.x)));
+// Parts of a sum one behind another, a lane's each: `mass` and `count` equals of the threshold, of which `left` are
+// still kept.  Returns the sum up to and with the lane's part; `add` is that part, `mine` what is left of the equals there.
+__device__ __noinline__ unsigned long long sum_parts(unsigned long long mass, uint32_t count, unsigned long long left,
+                                                     unsigned long long of_tie, unsigned long long &add, unsigned long long &mine) {
+  const int lane = threadIdx.x & 31;
+  uint32_t upto = count;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t n = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += n;
+  }
+  upto -= count;
+  mine = left > upto ? left - upto : 0ull;
+  add = mass + (count < mine ? count : mine) * of_tie;
+  unsigned long long sum = add;
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long n = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += n;
+  }
+  return sum;
+}
+
+// log(total / one) of whole numbers, total >= one: total against one 2^e 2^(i/512), with
+// 2^(i/512) next below it from the table; what is left (below 2^-8) by its series.  The
+// difference is taken in 64 bits, the rest of it has 32 bits of its own size.
+__device__ __noinline__ double log_ratio(const float2 *table, unsigned long long total, unsigned long long one) {
+  const float about = __log2f(static_cast<float>(total)) - __log2f(static_cast<float>(one));   // to 2^-16
+  const int steps = max(static_cast<int>(about * kSteps), 0), e = steps / kSteps;
+  const float2 t = table[steps % kSteps];
+  const double scale = __longlong_as_double(static_cast<long long>(1023 + e) << 52);
+  const double base = static_cast<double>(one) * (static_cast<double>(t.x) + t.y) * scale;
+  const float f = static_cast<float>(static_cast<double>(total) - base) / static_cast<float>(base);
+  return static_cast<double>(steps) * (0.6931471805599453 / kSteps) + static_cast<double>(f * fmaf(f, fmaf(f, 1.0f / 3.0f, -0.5f), 1.0f));
 }
 
 template <typename T, bool kHeld>
@@ -526,6 +546,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     while (kWarps * cs * per_warp < top_k) per_warp *= 2;
   if (tid == 0) {                         // 64 bits take their time: beside the loads
     const double c = 1.4426950408889634 / temperature;
+    sh.w.table = sh.table;
     sh.w.c1 = static_cast<float>(c * kSteps);
     sh.w.c2 = static_cast<float>(c * kSteps - sh.w.c1);
     sh.w.c = c;
@@ -634,13 +655,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
   __syncthreads();
   Weigher w = sh.w;
-  w.table = sh.table;                     // known to be in shared memory
+  w.table = sh.table;                     // known to be in shared memory here
   const float least = sh.least;
 
   const auto write = [&](float xi, int64_t index, unsigned long long total) {
     a.tokens[row] = static_cast<int32_t>(index);
     if (a.logprobs)
-      a.logprobs[row] = static_cast<float>((static_cast<double>(xi) - m) * sh.inv_t - log_ratio(sh.table, total, weight<kHeld>(w, m)));
+      a.logprobs[row] = static_cast<float>((static_cast<double>(xi) - m) * sh.inv_t - log_ratio(sh.table, total, weight(sh.w, m)));
   };
   const auto drawn = [&](unsigned long long total) {
     return u >= 1.0f ? total - 1 : u > 0.0f ? part_of(u, total, false) : 0ull;
@@ -653,7 +674,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       fetch(i, i1, r);
       uint32_t some = 0u, over = 0u;
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) some |= values_from(r[j], j, least_in);
+      for (int j = 0; j < kVecs; ++j) {
+        uint4 low = r[j];
+        some |= values_from(low, j, least_in);
+      }
       if (__any_sync(0xffffffffu, some != 0u) == 0) continue;
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) over |= values_from(r[j], j, least_over);
@@ -665,7 +689,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
   };
   // The same of many, through the warp's queue, so that all lanes have two at a time: pair(value, value), the second
-  // one -infinity where there is none, and done() after a step's.  look(vector) at all of them.
+  // one -infinity where there is none, and done() after a step's.  look(vector)
+  // at all of them, with -infinity for those of the range.
   const auto many_in = [&](int64_t i0, int64_t i1, float from, auto bounded, float to, auto &&look, auto &&pair, auto &&done) {
     const auto least_in = least_from(from, T{}), least_over = least_from(to, T{});
     for (int64_t i = i0 + lane; i - lane < i1; i += 32 * kVecs) {
@@ -674,13 +699,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       uint32_t some = 0u;
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) {
-        some |= values_from(r[j], j, least_in);
-        look(r[j]);
+        uint4 low = r[j];
+        some |= values_from(low, j, least_in);
+        look(low);
       }
       if constexpr (decltype(bounded)::value) {
         uint32_t over = 0u;
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) over |= values_from(r[j], j, least_over);
+        for (int j = 0; j < kVecs; ++j) {
+          uint4 low = r[j];
+          over |= values_from(low, j, least_over);
+        }
         some &= ~over;
       }
       const int many = __popc(some);
@@ -743,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         const float xi = __uint_as_float(static_cast<uint32_t>(entry >> 32));
         sh.few.x[tid] = xi;
         sh.few.key[tid] = argmax_key(xi, static_cast<uint32_t>(entry));
-        sh.few.mass[tid] = weight<kHeld>(w, xi);
+        sh.few.mass[tid] = weight(sh.w, xi);
       }
       __syncthreads();
       // a value's place in the order and the mass before it, by some threads each
@@ -816,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           const uint32_t k = ~float_order_key(xi);
           if (xi >= w.floor && (k & fixed) == key) {
             atomicAdd(&sh.h.count[(k >> shift) & mask], 1u);
-            if (want_mass) add_mass(sh, (k >> shift) & mask, weight<kHeld>(w, xi));
+            if (want_mass) add_mass(sh, (k >> shift) & mask, weight(sh.w, xi));
           }
         }
       }
@@ -828,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       key |= at.bin << shift;
     }
     const float edge_x = order_key_float(~key);
-    const unsigned long long of_one = weight<kHeld>(w, edge_x);
+    const unsigned long long of_one = weight(sh.w, edge_x);
     const unsigned long long many = by_mass ? (target + of_one - 1) / of_one : target;
     mass_k = mass + many * of_one;
     lower(edge_x, many);
@@ -840,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (w.wide || w.drop > 0) {
       for (int64_t i = w0 + lane; i < w1; i += 32) {
 #pragma unroll 1
-        for (int e = 0; e < W; ++e) s += weight<kHeld>(w, value_at(i, e));
+        for (int e = 0; e < W; ++e) s += weight(sh.w, value_at(i, e));
       }
     } else {
       uint32_t highs = 0u;                // parts of at most 2^17 each
@@ -873,7 +902,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     return warp_sum(s);
   };
-  // the mass of the CTAs, in from_mass, and of the row; parts' in warp_mass
+  // a CTA's sums, of its warps' in warp_mass and warp_count, to all CTAs
+  const auto hand_round = [&]() {
+    __syncthreads();
+    if (warp == 0) {
+      const unsigned long long sum = warp_sum(lane < kWarps ? sh.warp_mass[lane] : 0ull);
+      const uint32_t n = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_count[lane] : 0u);
+      if (lane < cs) {
+        peer_store64(peer_addr(&sh.from_mass[cr], lane), sum);
+        peer_store32(peer_addr(&sh.from_ties[cr], lane), n);
+      }
+    }
+    cluster_sync();
+  };
+  // the mass of the parts, of the CTAs
   const auto row_mass = [&]() {
     const unsigned long long s = part_mass();
     __syncthreads();
@@ -881,18 +923,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       sh.warp_mass[warp] = s;
       sh.warp_count[warp] = 0u;
     }
-    __syncthreads();
-    unsigned long long sum = 0ull;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) sum += sh.warp_mass[i];
-    if (tid < cs) {
-      peer_store64(peer_addr(&sh.from_mass[cr], tid), sum);
-      peer_store32(peer_addr(&sh.from_ties[cr], tid), 0u);
-    }
-    cluster_sync();
-    sum = 0ull;
-    for (int i = 0; i < cs; ++i) sum += sh.from_mass[i];
-    return sum;
+    hand_round();
+  };
+  const auto whole_mass = [&]() {
+    row_mass();
+    return warp_sum(lane < cs ? sh.from_mass[lane] : 0ull);
   };
   // the mass of the values above t of vectors [i0, i1), and how many equal it
   const auto part_kept = [&](int64_t i0, int64_t i1, uint32_t &equal) {
@@ -902,8 +937,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         i0, i1, fmaxf(t, w.floor), std::false_type{}, 0.0f, nothing,
         [&](float xi, float xj) {
           if (w.wide || w.drop > 0) {
-            s += xi == t ? 0ull : weight<kHeld>(w, xi);
-            s += xj == t || xj == -INFINITY ? 0ull : weight<kHeld>(w, xj);
+            s += xi == t ? 0ull : weight(sh.w, xi);
+            s += xj == t || xj == -INFINITY ? 0ull : weight(sh.w, xj);
           } else {
             uint32_t high[2];
             int low[2];
@@ -941,53 +976,62 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (tid < cs) peer_store32(peer_addr(&sh.from_sampled[cr], tid), sh.sampled);
     clear();
     cluster_sync();
-    float number = 0.0f, mine[2] = {0.0f, 0.0f}, largest = 0.0f;   // of the lane's two octaves
-    for (int r = 0; r < cs; ++r) number += static_cast<float>(sh.from_sampled[r]);
+    if (warp == 0) {
+      float number = 0.0f, mine[2] = {0.0f, 0.0f}, largest = 0.0f;   // of the lane's two octaves
+      for (int r = 0; r < cs; ++r) number += static_cast<float>(sh.from_sampled[r]);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (lane + 32 * h < kOctaves) {
-        float some = 0.0f, high = 0.0f;
-        for (int r = 0; r < cs; ++r) {
-          some += static_cast<float>(sh.from_octave[r][lane + 32 * h]);
-          high += static_cast<float>(sh.from_octave[r][kOctaves + lane + 32 * h]);
+      for (int h = 0; h < 2; ++h)
+        if (lane + 32 * h < kOctaves) {
+          float some = 0.0f, high = 0.0f;
+          for (int r = 0; r < cs; ++r) {
+            some += static_cast<float>(sh.from_octave[r][lane + 32 * h]);
+            high += static_cast<float>(sh.from_octave[r][kOctaves + lane + 32 * h]);
+          }
+          const float unit = exp2f(-8.0f - static_cast<float>(lane + 32 * h));
+          // one of the largest in the sample would stand for many that are not there: 16 at least
+          mine[h] = fmaxf(some >= 16.0f * 384.0f ? some * (static_cast<float>(v) / fmaxf(number, 1.0f)) : 0.0f, high) * unit;
+          largest += high * unit;
         }
-        const float unit = exp2f(-8.0f - static_cast<float>(lane + 32 * h));
-        // one of the largest in the sample would stand for many that are not there: 16 at least
-        mine[h] = fmaxf(some >= 16.0f * 384.0f ? some * (static_cast<float>(v) / fmaxf(number, 1.0f)) : 0.0f, high) * unit;
-        largest += high * unit;
+      float about = mine[0] + mine[1];
+      for (int o = 16; o > 0; o >>= 1) {
+        about += __shfl_xor_sync(0xffffffffu, about, o);
+        largest += __shfl_xor_sync(0xffffffffu, largest, o);
       }
-    float about = mine[0] + mine[1];
-    for (int o = 16; o > 0; o >>= 1) {
-      about += __shfl_xor_sync(0xffffffffu, about, o);
-      largest += __shfl_xor_sync(0xffffffffu, largest, o);
-    }
-    // Below this a value cannot be the border: all such values together weigh less than 1 - p of the maxima alone.
-    const float share = (1.0f - top_p) * largest / static_cast<float>(v);
-    const float lowest = fmaxf(fmaxf(w.floor, least), fmaf(__log2f(share * 0.98f) + w.e, 1.0f / w.c0, -1e-4f * temperature - 1e-5f * fabsf(m)));
-    // By the octaves, the border lies above where seven tenths of 1 - p lie below, and below where that is fourteen; a
-    // border that is not there is not found there.
-    float guess = lowest, sure_guess = INFINITY;
-    {
-      const float enough = (1.0f - top_p) * about;
-      float below = 0.0f;
-      int low_cut = kOctaves, high_cut = -1;
+      // Below this a value cannot be the border: all such values together weigh less than 1 - p of the maxima alone.
+      const float share = (1.0f - top_p) * largest / static_cast<float>(v);
+      const float low = fmaxf(fmaxf(w.floor, least), fmaf(__log2f(share * 0.98f) + w.e, 1.0f / w.c0, -1e-4f * temperature - 1e-5f * fabsf(m)));
+      // By the octaves, the border lies above where seven tenths of 1 - p lie below, and below where that is fourteen; a
+      // border that is not there is not found there.
+      float guess = low, sure_guess = INFINITY;
+      {
+        const float enough = (1.0f - top_p) * about;
+        float below = 0.0f;
+        int low_cut = kOctaves, high_cut = -1;
 #pragma unroll
-      for (int h = 1; h >= 0; --h) {
-        float s = mine[h];
-        for (int o = 1; o < 32; o <<= 1) {
-          const float t = __shfl_down_sync(0xffffffffu, s, o);
-          if (lane + o < 32) s += t;
+        for (int h = 1; h >= 0; --h) {
+          float s = mine[h];
+          for (int o = 1; o < 32; o <<= 1) {
+            const float t = __shfl_down_sync(0xffffffffu, s, o);
+            if (lane + o < 32) s += t;
+          }
+          // an octave and all below it
+          const uint32_t little = __ballot_sync(0xffffffffu, s + below < 0.7f * enough), much = __ballot_sync(0xffffffffu, s + below > 1.4f * enough);
+          if (little) low_cut = 32 * h + __ffs(little) - 1;
+          if (much && high_cut < 0) high_cut = 32 * h + 31 - __clz(much);
+          below += __shfl_sync(0xffffffffu, s, 0);
         }
-        // an octave and all below it
-        const uint32_t little = __ballot_sync(0xffffffffu, s + below < 0.7f * enough), much = __ballot_sync(0xffffffffu, s + below > 1.4f * enough);
-        if (little) low_cut = 32 * h + __ffs(little) - 1;
-        if (much && high_cut < 0) high_cut = 32 * h + 31 - __clz(much);
-        below += __shfl_sync(0xffffffffu, s, 0);
+        if (low_cut < kOctaves) guess = fmaxf(low, (w.e - static_cast<float>(low_cut - 1)) / w.c0);
+        if (high_cut > 0) sure_guess = (w.e - static_cast<float>(high_cut - 1)) / w.c0;
+        if (!(sure_guess > guess)) sure_guess = INFINITY;
       }
-      if (low_cut < kOctaves) guess = fmaxf(lowest, (w.e - static_cast<float>(low_cut - 1)) / w.c0);
-      if (high_cut > 0) sure_guess = (w.e - static_cast<float>(high_cut - 1)) / w.c0;
-      if (!(sure_guess > guess)) sure_guess = INFINITY;
+      if (lane == 0) {
+        sh.lowest = low;
+        sh.guess = guess;
+        sh.sure_guess = sure_guess;
+      }
     }
+    __syncthreads();
+    const float lowest = sh.lowest, guess = sh.guess, sure_guess = sh.sure_guess;
     // What the mass below may be off by: the products' roundings (of log2(e) / T too), 2 ulp of an exponential, 16 additions, and
     // half of the last place of every weight.
     const float off_by = 0.6931472f * 0x1p-24f * (44.0f + fmaxf(fabsf(m), fabsf(w.floor)) * w.c0) + 0x1p-22f + 0x1.1p-20f + 0x1p-32f;
@@ -1019,8 +1063,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
             for (int e = 0; e < W; e += 2) {
               const float2 y = unpack2(fma2(pack2(o[e], o[e + 1]), c2, e2));
-              const float one = exp2_approx(y.x), two = exp2_approx(y.y);
-              sum = add2(sum, pack2(o[e] < from ? one : 0.0f, o[e + 1] < from ? two : 0.0f));
+              sum = add2(sum, pack2(exp2_approx(y.x), exp2_approx(y.y)));
             }
           },
           [&](float xi, float xj) {
@@ -1045,36 +1088,39 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         sh.warp_tail[warp] = tail;
       }
       __syncthreads();
-      if (tid < cs) {
-        above = upper = tail = 0ull;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-          above += sh.above[i];
-          upper += sh.warp_mass[i];
-          tail += sh.warp_tail[i];
+      if (warp == 0) {
+        above = warp_sum(lane < kWarps ? sh.above[lane] : 0ull);
+        upper = warp_sum(lane < kWarps ? sh.warp_mass[lane] : 0ull);
+        tail = warp_sum(lane < kWarps ? sh.warp_tail[lane] : 0ull);
+        if (lane < cs) {
+          peer_store64(peer_addr(&sh.from_total[cr], lane), above);
+          peer_store64(peer_addr(&sh.from_mass[cr], lane), upper);
+          peer_store64(peer_addr(&sh.from_tail[cr], lane), tail);
         }
-        peer_store64(peer_addr(&sh.from_total[cr], tid), above);
-        peer_store64(peer_addr(&sh.from_mass[cr], tid), upper);
-        peer_store64(peer_addr(&sh.from_tail[cr], tid), tail);
       }
       cluster_sync();
-      above = upper = tail = 0ull;
-      for (int i = 0; i < cs; ++i) {
-        above += sh.from_total[i];
-        upper += sh.from_mass[i];
-        tail += sh.from_tail[i];
+      if (warp == 0) {
+        above = warp_sum(lane < cs ? sh.from_total[lane] : 0ull);
+        upper = warp_sum(lane < cs ? sh.from_mass[lane] : 0ull);
+        tail = warp_sum(lane < cs ? sh.from_tail[lane] : 0ull);
+        if (lane == 0) {
+          const unsigned long long slack = static_cast<unsigned long long>(static_cast<float>(tail) * off_by) + static_cast<unsigned long long>(v);
+          sh.above_all = above;
+          sh.need = part_of(top_p, upper + (tail > slack ? tail - slack : 0ull), true);
+          sh.need_most = part_of(top_p, upper + tail + slack, true);
+        }
       }
-      // What top-p needs at least and at most; where that leaves two borders, the row's mass itself.
+      __syncthreads();
+      above = sh.above_all;
+      // What top-p needs at least and at most; where that leaves two borders, by the row's mass itself.
 #pragma unroll 1
       for (int exact = 0; exact < 2 && !found; ++exact) {
-        const unsigned long long slack =
-            exact ? 0ull : static_cast<unsigned long long>(static_cast<float>(tail) * off_by) + static_cast<unsigned long long>(v);
+        unsigned long long need = sh.need, need_most = sh.need_most;
         if (exact) {
           cluster_sync();                 // all have read what came before
-          mass_k = row_mass();
+          mass_k = whole_mass();
+          need = need_most = part_of(top_p, mass_k, true);
         }
-        const unsigned long long need = part_of(top_p, exact ? mass_k : upper + (tail > slack ? tail - slack : 0ull), true),
-                                 need_most = exact ? need : part_of(top_p, upper + tail + slack, true);
         if (need <= above) break;         // above what is sure
         Cross at;
         if (!find_cross(sh, true, need - above, at)) {
@@ -1118,7 +1164,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         between = warp_sum(between);
         cluster_sync();
         const int n = static_cast<int>(at.in);
-        if (tid < n) sh.edge.mass[tid] = weight<kHeld>(w, sh.edge.x[tid]);
+        if (tid < n) sh.edge.mass[tid] = weight(sh.w, sh.edge.x[tid]);
         __syncthreads();
         if (warp == 0) {
           // the largest key at which the mass from it up reaches what is needed: between the bin's ends, bit by bit
@@ -1152,7 +1198,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             if (mass_from(mid) >= need) low = mid;
             else high = mid - 1;
           }
-          const unsigned long long over = low == ~0u ? before : mass_from(low + 1), of_one = weight<kHeld>(w, order_key_float(low));
+          const unsigned long long over = low == ~0u ? before : mass_from(low + 1), of_one = weight(sh.w, order_key_float(low));
           if (lane == 0) {
             sh.border = order_key_float(low);
             sh.ties = (need - over + of_one - 1) / of_one;
@@ -1183,12 +1229,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     if (!found && !settled) {
       cluster_sync();
-      mass_k = row_mass();
+      mass_k = whole_mass();
       select(true, part_of(top_p, mass_k, true), true);
     }
     kept_known = found;
   } else if (by_p) {
-    if (whole_row) mass_k = row_mass();
+    if (whole_row) mass_k = whole_mass();
     select(true, part_of(top_p, mass_k, true), true);
   }
 
@@ -1202,115 +1248,96 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       sh.warp_mass[warp] = kept_known ? sh.above[warp] : mass;
       if (!kept_known) sh.warp_count[warp] = equal;
     }
-    __syncthreads();
-    unsigned long long sum = 0ull;
-    uint32_t sum_n = 0u;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      sum += sh.warp_mass[i];
-      sum_n += sh.warp_count[i];
-    }
-    if (tid < cs) {
-      peer_store64(peer_addr(&sh.from_mass[cr], tid), sum);
-      peer_store32(peer_addr(&sh.from_ties[cr], tid), sum_n);
-    }
-    cluster_sync();
+    hand_round();
   }
-  const unsigned long long of_tie = t >= w.floor ? weight<kHeld>(w, t) : 0ull;
-  unsigned long long left = ties;
-  const auto kept_ties = [&](uint32_t n) {  // of the next n ties; takes them off what is left
-    const unsigned long long k = n < left ? n : left;
-    left -= k;
-    return k * of_tie;
-  };
-  unsigned long long total = 0ull;
-  for (int i = 0; i < cs; ++i) total += sh.from_mass[i] + kept_ties(sh.from_ties[i]);
-  const unsigned long long target = drawn(total);
-
-  // the CTA in which the sum passes the target
-  unsigned long long upto = 0ull;
-  left = ties;
-  for (int i = 0; i < cr; ++i) upto += sh.from_mass[i] + kept_ties(sh.from_ties[i]);
-  if (target < upto) return;
+  // The CTA in which the sum passes the number drawn, and the warp's part of it.
+  if (warp == 0) {
+    const unsigned long long of_tie = t >= w.floor ? weight(sh.w, t) : 0ull;
+    unsigned long long add, left;
+    unsigned long long sum = sum_parts(lane < cs ? sh.from_mass[lane] : 0ull, lane < cs ? sh.from_ties[lane] : 0u, ties, of_tie, add, left);
+    const unsigned long long total = __shfl_sync(0xffffffffu, sum, 31), target = drawn(total);
+    unsigned long long upto = __shfl_sync(0xffffffffu, sum - add, cr);
+    const bool here = target >= upto && target < upto + __shfl_sync(0xffffffffu, add, cr);
+    left = __shfl_sync(0xffffffffu, left, cr);
+    int part = -1;
+    if (here) {
+      const unsigned long long before = upto;
+      sum = before + sum_parts(lane < kWarps ? sh.warp_mass[lane] : 0ull, lane < kWarps ? sh.warp_count[lane] : 0u, left, of_tie, add, left);
+      part = __ffs(__ballot_sync(0xffffffffu, target < sum)) - 1;
+      upto = __shfl_sync(0xffffffffu, sum - add, part);
+      left = __shfl_sync(0xffffffffu, left, part);
+    }
+    if (lane == 0) {
+      sh.part = part;
+      sh.total = total;
+      sh.target = target;
+      sh.upto = upto;
+      sh.left = left;
+      sh.of_tie = of_tie;
+    }
+  }
+  __syncthreads();
+  if (sh.part < 0) return;
+  const unsigned long long target = sh.target, of_tie = sh.of_tie;
+  // its sixteenths, a warp each
+  const int64_t p0 = part_begin(sh.part), p1 = part_begin(sh.part + 1);
   {
-    const unsigned long long l = left, add = sh.from_mass[cr] + kept_ties(sh.from_ties[cr]);
-    if (target >= upto + add) return;
-    left = l;
-  }
-  // the first of kWarps parts in which the sum passes the target; moves upto and left there
-  const auto pass = [&]() {
-    for (int i = 0;; ++i) {
-      const unsigned long long l = left, add = sh.warp_mass[i] + kept_ties(sh.warp_count[i]);
-      if (i == kWarps - 1 || target < upto + add) {
-        left = l;
-        return i;
-      }
-      upto += add;
-    }
-  };
-  const int in_part = pass();
-  int64_t i0 = part_begin(in_part), i1 = part_begin(in_part + 1);
-  {                                       // and of its sixteenths, a warp each
-    const int64_t b0 = i0 + (i1 - i0) * warp / kWarps, b1 = i0 + (i1 - i0) * (warp + 1) / kWarps;
     uint32_t equal;
-    const unsigned long long mass = part_kept(b0, b1, equal);
-    __syncthreads();
+    const unsigned long long mass = part_kept(p0 + (p1 - p0) * warp / kWarps, p0 + (p1 - p0) * (warp + 1) / kWarps, equal);
     if (lane == 0) {
       sh.warp_mass[warp] = mass;
       sh.warp_count[warp] = equal;
     }
-    __syncthreads();
-    const int sixteenth = pass();
-    if (warp != sixteenth) return;
-    i0 = b0;
-    i1 = b1;
   }
+  __syncthreads();
+  if (warp != 0) return;
+  unsigned long long upto, left;
+  int64_t i0, i1;
+  {
+    unsigned long long add;
+    const unsigned long long sum = sh.upto + sum_parts(lane < kWarps ? sh.warp_mass[lane] : 0ull, lane < kWarps ? sh.warp_count[lane] : 0u,
+                                                       sh.left, of_tie, add, left);
+    const int part = __ffs(__ballot_sync(0xffffffffu, target < sum)) - 1;
+    upto = __shfl_sync(0xffffffffu, sum - add, part);
+    left = __shfl_sync(0xffffffffu, left, part);
+    i0 = p0 + (p1 - p0) * part / kWarps;
+    i1 = p0 + (p1 - p0) * (part + 1) / kWarps;
+  }
+  // and its values, 32 vectors at a time
   for (int64_t i = i0; i < i1; i += 32) {
-    float o[W];
-    unsigned long long weights[W], lane_sum = 0ull;
+    unsigned long long mass = 0ull, add;
     uint32_t n = 0u;
-    unpack(i + lane < i1 ? load_vec(i + lane) : vec_lowest(T{}), o, T{});
-#pragma unroll
-    for (int e = 0; e < W; ++e) {
-      weights[e] = o[e] > t && o[e] >= w.floor ? weight<kHeld>(w, o[e]) : 0ull;
-      n += o[e] == t && i + lane < i1;
-    }
-    uint32_t n_upto = n;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const uint32_t b = __shfl_up_sync(0xffffffffu, n_upto, s);
-      if (lane >= s) n_upto += b;
-    }
-    unsigned long long mine_left = left > n_upto - n ? left - (n_upto - n) : 0ull;
-#pragma unroll
-    for (int e = 0; e < W; ++e) {
-      if (o[e] == t && mine_left > 0ull) {
-        --mine_left;
-        weights[e] = of_tie;
-      }
-      lane_sum += weights[e];
-    }
-    unsigned long long s_upto = lane_sum;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const unsigned long long b = __shfl_up_sync(0xffffffffu, s_upto, s);
-      if (lane >= s) s_upto += b;
-    }
-    unsigned long long here = upto + s_upto - lane_sum;
-    if (target >= here && target < here + lane_sum) {
-      bool done = false;
-#pragma unroll
+    if (i + lane < i1) {
+#pragma unroll 1
       for (int e = 0; e < W; ++e) {
-        if (!done && target < here + weights[e]) {
-          write(o[e], (i + lane) * W + e - off, total);
-          done = true;
-        }
-        here += weights[e];
+        const float xi = value_at(i + lane, e);
+        if (xi > t && xi >= w.floor) mass += weight(sh.w, xi);
+        n += xi == t;
       }
     }
-    upto += __shfl_sync(0xffffffffu, s_upto, 31);
-    n_upto = __shfl_sync(0xffffffffu, n_upto, 31);
-    left = left > n_upto ? left - n_upto : 0ull;
+    unsigned long long mine;
+    const unsigned long long sum = upto + sum_parts(mass, n, left, of_tie, add, mine);
+    unsigned long long here = sum - add;
+    if (target >= here && target < sum) {
+#pragma unroll 1
+      for (int e = 0; e < W; ++e) {
+        const float xi = value_at(i + lane, e);
+        unsigned long long k = 0ull;
+        if (xi > t && xi >= w.floor) k = weight(sh.w, xi);
+        else if (xi == t && mine > 0ull) {
+          --mine;
+          k = of_tie;
+        }
+        if (target < here + k) {
+          write(xi, (i + lane) * W + e - off, sh.total);
+          break;
+        }
+        here += k;
+      }
+    }
+    upto = __shfl_sync(0xffffffffu, sum, 31);
+    const uint32_t all = __reduce_add_sync(0xffffffffu, n);
+    left = left > all ? left - all : 0ull;
     if (upto > target) return;
   }
 }
