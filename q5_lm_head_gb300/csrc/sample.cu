@@ -19,22 +19,24 @@
 // of 2^E; the same logit always has the same weight.  A row whose exponents pass
 // 2^13 (a low temperature, or logits of 1e5) takes its weights in 64 bits.
 //
-// Bound: HBM for many rows, latency for a few.  A cluster of CTAs holds a row in its
-// shared memory, each CTA a contiguous share, each warp a contiguous part of that, so
-// that prefix sums over CTAs and warps follow the index.  Passes over the share find
-//   the maximum;
-//   top-k up to 512: the k-th largest of at least k maxima of groups of threads is a
-//     bound that k values reach; what reaches it goes to the first CTA, which does the
-//     rest with these few;
-//   else the row's mass, where the whole of it or top-p wants that;
-//   top-p: a value below (1 - p) of the mean weight cannot be the border; the others go
-//     into a list, and by their distance from the maximum into a histogram of mass; the bin
-//     in which it reaches the share of the mass is handed round and settled value by value;
-//   the kept mass of each CTA, and in the one where the number falls, of its warps,
-//     sixteenths of the warp's part, and values.
-// What does not fit the lists (equal logits, wide borders) is selected by histograms over the
-// ordered bits of the logits, 10 bits at a time.  Nothing is kept in global memory,
-// so calls may overlap.  A row that 16 CTAs cannot hold is read again for each pass.
+// Bound: for few rows latency (a dozen cluster barriers and the passes' chains), for many the CUDA cores: one weight
+// takes 20 instructions and a table look-up of six bank cycles, so all passes but that of an unfiltered row avoid
+// them where they can.  A cluster of CTAs takes a row, each CTA a contiguous share, each warp a contiguous part of it,
+// so that prefix sums over CTAs and warps follow the index.  A share is held in shared memory where that fits, else
+// read again (from L2) by each pass.  The passes:
+//   - the maximum, maxima of groups of threads, a sample.
+//   - top-k up to 512: the k-th largest of at least k maxima is a bound that k values reach; what reaches it goes to
+//     the first CTA, which does the rest with these few (1 row of 202,048 f32 with top-k 50 and top-p 11.5 us).
+//   - no filter: the mass of the parts (16 rows 23 us).
+//   - top-p: by the sample and the maxima the border lies in an octave or two.  Values from there up are summed as
+//     weights, those in the octaves by a histogram of 1,024 bins, those below only about, by exponentials in 32 bits whose
+//     error has a bound: of the row's mass they are 1 - p.  Then the bin in which the sum reaches p of the least and
+//     of the most that the mass can be, and in one more pass its values, settled one by one.  Where the two differ (one
+//     row in eight of 202,048 bf16 values with 28,000 kept), the row's mass is summed as weights and the bin taken
+//     again.  1,024 such rows 637 us; with weights for every value and pass 1,169, with histograms over the ordered bits 2,296.
+//   - the CTA in whose kept mass the number falls, its warp's part, its sixteenth, its value.
+// What does not fit (equal logits by the thousand, a border in a crowd, weights in 64 bits) is selected by histograms
+// over the ordered bits of the logits, 10 bits at a time.  Nothing is kept in global memory, so calls may overlap.
 #include <atomic>
 #include <type_traits>
 
@@ -55,7 +57,7 @@ constexpr int kStaged = 2;               // 16-byte vectors of a lane and step, 
 constexpr int kRead = 4;                 // and of rows that are read again
 constexpr int kQueue = 32 * 16 * kWarps; // bytes of the warps' queues, for each vector of a step
 static_assert(kSample * 4 <= 32 * 16 * kStaged, "a warp's sample is in its queue");
-constexpr int kHeldTwo = 74 * 1024;      // bytes of a row in a CTA and its queues: two CTAs an SM
+constexpr int kHeldTwo = 72 * 1024;      // bytes of a row in a CTA and its queues: two CTAs an SM
 constexpr int kHeldOne = 184 * 1024;     // one CTA an SM
 
 constexpr int kSteps = 512;              // table: 2^(i / 512)
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   };
   const auto load_vec = [&](int64_t i) {
     if constexpr (kHeld) return vec_held[i - v0];
-    else return whole(i) ? __ldg(reinterpret_cast<const uint4 *>(x0) + i) : edge(i);
+    else return whole(i) ? reinterpret_cast<const uint4 *>(x0)[i] : edge(i);
   };
   const auto value_at = [&](int64_t i, int e) {   // of a vector: -infinity beside the row
     if constexpr (kHeld) {
@@ -1201,8 +1203,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           const unsigned long long over = low == ~0u ? before : mass_from(low + 1), of_one = weight(sh.w, order_key_float(low));
           if (lane == 0) {
             sh.border = order_key_float(low);
-            sh.ties = (need - over + of_one - 1) / of_one;
-            sh.reached = over + sh.ties * of_one;
+            // how many of its equals, at most kFew: a division in 64 bits costs as much as all of this
+            unsigned long long many = static_cast<unsigned long long>(static_cast<float>(need - over) / static_cast<float>(of_one));
+            while (many > 0ull && (many - 1) * of_one >= need - over) --many;
+            while (many * of_one < need - over) ++many;
+            sh.ties = many;
+            sh.reached = over + many * of_one;
           }
         }
         __syncthreads();
@@ -1342,11 +1348,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
 }
 
-template <typename T>
-cudaError_t launch_sample_read(const SampleArgs &a, int cs);
-
 template <typename T, bool kHeld>
-cudaError_t launch_sample_t(const SampleArgs &a, int cs, size_t shared) {
+cudaError_t sample_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int64_t n, int cs, size_t shared, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};   // one bit per device; host threads may race here
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1359,12 +1362,11 @@ cudaError_t launch_sample_t(const SampleArgs &a, int cs, size_t shared) {
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.n * cs));
+  cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(n * cs));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = shared;
-  cfg.stream = a.stream;
-  cudaLaunchAttribute attr[2];
+  cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // may start before the previous grid ends
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -1372,35 +1374,62 @@ cudaError_t launch_sample_t(const SampleArgs &a, int cs, size_t shared) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (kHeld && shared > kHeldTwo) {       // up to 16 SMs of one GPC at a time: not every device has them
-    int fit = 0;
-    e = cudaOccupancyMaxActiveClusters(&fit, sample_kernel<T, kHeld>, &cfg);
-    if (e != cudaSuccess) return e;
-    if (fit < 1) return launch_sample_read<T>(a, 8);
-  }
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T, kHeld>, a);
+  return cudaSuccess;
 }
 
-// Rows read again for each pass.
+template <typename T, bool kHeld>
+cudaError_t launch_sample_t(SampleArgs a, int cs, int64_t held) {
+  a.held_bytes = static_cast<int>(held);
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  const cudaError_t e = sample_config<T, kHeld>(cfg, attr, a.n, cs, static_cast<size_t>(held) + kQueue * (kHeld ? kStaged : kRead), a.stream);
+  return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, sample_kernel<T, kHeld>, a) : e;
+}
+
+// Clusters of cs CTAs that run at once, `shared` bytes each: the GPCs do not divide evenly (with two CTAs an
+// SM 304, 152, 74, 36, 14 of 1, 2, 4, 8, 16).  Asked once for each device.
 template <typename T>
-cudaError_t launch_sample_read(const SampleArgs &a, int cs) {
-  SampleArgs b = a;
-  b.held_bytes = 0;
-  return launch_sample_t<T, false>(b, cs, kQueue * kRead);
+cudaError_t clusters_at_once(int cs, bool two, int &fit) {
+  static std::atomic<int> known[64][2][5];
+  int dev = 0, log = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  while ((1 << log) < cs) ++log;
+  std::atomic<int> &k = known[dev & 63][two][log];
+  fit = k.load(std::memory_order_relaxed) - 1;
+  if (fit >= 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  e = sample_config<T, true>(cfg, attr, 1, cs, two ? kHeldTwo : kHeldOne, nullptr);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&fit, sample_kernel<T, true>, &cfg);
+  if (e == cudaSuccess) k.store(fit + 1, std::memory_order_relaxed);
+  return e;
 }
 
+// As many CTAs a row as let all rows run at once, two CTAs an SM (times in us for rows of 202,048 f32 with top-p, the
+// whole distribution, top-k, by CTAs a row: 32 rows 8 76, 26, 19, 16 112, 35, 31; 64 rows 4 104, 40, 25, 8 123,
+// 48, 33; 128 rows 2 195, 62, 39, 4 174, 74, 48), 1,024 values each at least; with a third more rows than two CTAs
+// each have room, two each still (200 rows 251, 103, 81, one each 316, 119, 71).  A share is held in shared memory where
+// two CTAs' fit into an SM's (16 rows of 202,048 bf16, 8 CTAs each: 51, 22, 15, read again 54, 24, 16), or for the
+// few rows that run at once with one CTA an SM.
 template <typename T>
 cudaError_t launch_sample_rows(const SampleArgs &a) {
   const int64_t vecs = a.v / Vec<T>::W + 2, queue = kQueue * kStaged;
   auto held = [&](int64_t cs) { return (vecs + cs - 1) / cs * 16; };   // a share is at most this
-  if (a.n >= 2 * a.num_sms) return launch_sample_read<T>(a, 1);
-  int cs = 1;
-  while (cs < kCluster && held(cs) + queue > kHeldTwo) cs *= 2;
-  while (cs < kCluster && a.n * 2 * cs <= 2 * a.num_sms && a.v / (2 * cs) >= 2048) cs *= 2;
-  if (held(cs) + queue > kHeldOne) return launch_sample_read<T>(a, 8);
-  SampleArgs b = a;
-  b.held_bytes = static_cast<int>(held(cs));
-  return launch_sample_t<T, true>(b, cs, static_cast<size_t>(held(cs) + queue));
+  int cs = 1, fit = 0;
+  for (int next = 2; next <= kCluster && a.v / next >= 1024; next *= 2) {
+    const cudaError_t e = clusters_at_once<T>(next, true, fit);
+    if (e != cudaSuccess) return e;
+    if (a.n > (next == 2 ? fit + fit / 3 : fit)) break;
+    cs = next;
+  }
+  if (held(cs) + queue <= kHeldTwo) return launch_sample_t<T, true>(a, cs, held(cs));
+  if (held(cs) + queue <= kHeldOne) {
+    const cudaError_t e = clusters_at_once<T>(cs, false, fit);
+    if (e != cudaSuccess) return e;
+    if (a.n <= fit) return launch_sample_t<T, true>(a, cs, held(cs));
+  }
+  return launch_sample_t<T, false>(a, cs, 0);
 }
 
 }  // namespace
