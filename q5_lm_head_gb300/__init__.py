@@ -779,8 +779,8 @@ class LMHead:
         ptr, dtype, n, ld = self._rows(logits, "logits")
         up = self._check(uniforms, "uniforms", torch.float32, (n,))
         how = self._sampling(n, temperature, top_k, top_p, min_p)
-        empty = self._allocator(stream, logits, uniforms, *(s for s in (temperature, top_k, top_p, min_p)
-                                                            if isinstance(s, torch.Tensor)))
+        empty = torch.empty if stream is None else self._allocator(
+            stream, logits, uniforms, *(s for s in (temperature, top_k, top_p, min_p) if isinstance(s, torch.Tensor)))
         tokens = empty((n,), dtype=torch.int32, device=logits.device)
         logprobs = empty((n,), dtype=torch.float32, device=logits.device)
         st = load_library().muse_lmhead_sample(self.handle, ptr, dtype, n, ld, how, up, tokens.data_ptr(),
@@ -840,7 +840,8 @@ class LMHead:
         if out is None:
             if dtype is None:
                 dtype = torch.float32 if kind == MUSE_DTYPE_BLOCKS else table.dtype
-            out = self._allocator(stream, tokens, table)((n, self.k), dtype=dtype, device=tokens.device)
+            empty = torch.empty if stream is None else self._allocator(stream, tokens, table)
+            out = empty((n, self.k), dtype=dtype, device=tokens.device)
         else:
             self._allocator(stream, tokens, table, out)
             if dtype is not None and out.dtype != dtype:
