@@ -1409,9 +1409,10 @@ cudaError_t clusters_at_once(int cs, bool two, int &fit) {
 // As many CTAs a row as let all rows run at once, two CTAs an SM (times in us for rows of 202,048 f32 with top-p, the
 // whole distribution, top-k, by CTAs a row: 32 rows 8 76, 26, 19, 16 112, 35, 31; 64 rows 4 104, 40, 25, 8 123,
 // 48, 33; 128 rows 2 195, 62, 39, 4 174, 74, 48), 1,024 values each at least; with a third more rows than two CTAs
-// each have room, two each still (200 rows 251, 103, 81, one each 316, 119, 71).  A share is held in shared memory where
-// two CTAs' fit into an SM's (16 rows of 202,048 bf16, 8 CTAs each: 51, 22, 15, read again 54, 24, 16), or for the
-// few rows that run at once with one CTA an SM.
+// each have room, two each still (200 rows 251, 103, 81, one each 316, 119, 71); 16 CTAs share an SM with others from
+// eight rows on, which only long rows make up for (8 rows of 50,257 f32 16 27, 12.8, 12.8, 8 26, 12.4, 11.3).  A share is
+// held in shared memory where two CTAs' fit into an SM's (16 rows of 202,048 bf16, 8 CTAs each: 51, 22, 15, read
+// again 54, 24, 16), or for the few rows that run at once with one CTA an SM.
 template <typename T>
 cudaError_t launch_sample_rows(const SampleArgs &a) {
   const int64_t vecs = a.v / Vec<T>::W + 2, queue = kQueue * kStaged;
@@ -1420,7 +1421,7 @@ cudaError_t launch_sample_rows(const SampleArgs &a) {
   for (int next = 2; next <= kCluster && a.v / next >= 1024; next *= 2) {
     const cudaError_t e = clusters_at_once<T>(next, true, fit);
     if (e != cudaSuccess) return e;
-    if (a.n > (next == 2 ? fit + fit / 3 : fit)) break;
+    if (a.n > (next == 2 ? fit + fit / 3 : next == 16 && a.v < 131072 ? fit / 2 : fit)) break;
     cs = next;
   }
   if (held(cs) + queue <= kHeldTwo) return launch_sample_t<T, true>(a, cs, held(cs));
