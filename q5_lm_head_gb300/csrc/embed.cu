@@ -9,7 +9,10 @@
 // type (sums of one token in the order of their positions).
 //
 // Lookup.  A warp takes 256 columns of a dense row (a lane eight), half a warp a block
-// of a quantised one (a lane 16).
+// of a quantised one (a lane 16).  Bound: the dense rows' bytes (4,099 rows of 6,656
+// bf16 16.3 us, 5.2 TB/s over reads and writes, most of which L2 still holds at the
+// end); of blocks the unpacking, 40 million warp instructions for 16,384 rows, with the
+// issue slots at 72 % and the integer pipe at 67 %: 49.4 us, 5.1 TB/s.  One token 1.4 us.
 //
 // Gradient.  The positions are sorted by token first, stable, so that a row of the
 // table is written once, by whoever holds its sum, and the order of the sum is
@@ -23,6 +26,9 @@
 // for each of its chunks; the warp that counts in last adds them up in order, so no
 // warp waits for another and the bits do not depend on which that is.  Behind them
 // in the same grid, a warp a row, CTAs write the zeros of rows without a token.
+// Bound: HBM for a large table (16,384 positions and 202,048 x 6,656 bf16 443 us, 6.55
+// TB/s, 97 % of a copy's rate), else the two kernels' chains (the order 5 us for 301
+// positions, 13 for 16,384; 301 positions and 2,048 rows of 6,656 f32 20.5 us).
 #include <atomic>
 
 #include "common.cuh"
@@ -36,7 +42,9 @@ constexpr int kTile = 256;                 // columns of a warp: a block
 constexpr int kLane = 8;                   // of a lane
 
 // Eight consecutive values of a lane: one access where rows lie on its size (kWide: 16
-// bytes, of f32 32), two of 16 bytes for other f32 rows on 16 bytes, else value by value.
+// bytes, of f32 32), two of 16 bytes for other f32 rows on 16 bytes, else value by value
+// (lookup of 4,099 f32 rows of 6,656 33.9, 34.3, 88 us; gradient of 4,096 bf16 rows of 768 by
+// 50,257 of f32 34.8, 38, 134 us).
 template <typename T>
 struct Lane8 {
   __align__(16) T v[kLane];
@@ -229,19 +237,22 @@ cudaError_t launch_after(void (*kernel)(A), int64_t grid, int threads, size_t sh
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// Four tiles a warp (two rounds of 16 blocks a CTA) where that leaves enough of them, else one.
+// Four tiles a warp from 24 warps of one tile an SM on, else one (times in us by rows of 6,656 bf16, one tile and
+// four: 16 1.47, 1.62; 128 1.73, 1.71; 256 2.40, 2.07; 1,024 6.5, 4.6; 16,384 91, 69).
 template <typename TT, typename TO>
 cudaError_t launch_embed_dense(const EmbedArgs &a) {
   const int64_t items = a.n * (a.k / kTile), most = int64_t{1} << 30;
-  const bool many = items >= 64 * static_cast<int64_t>(a.num_sms);
+  const bool many = items >= 24 * static_cast<int64_t>(a.num_sms);
   const int64_t blocks = (items + (many ? 31 : 7)) / (many ? 32 : 8);
   void (*kernel)(EmbedArgs) = many ? embed_dense_kernel<TT, TO, 4> : embed_dense_kernel<TT, TO, 1>;
   return launch_after(kernel, blocks < most ? blocks : most, 256, 0, a.stream, a);
 }
+// Four rounds of blocks a warp from 256 blocks an SM on, else one (Q5_K rows of 6,656 to bf16: 64 1.47, 2.65; 512
+// 2.58, 3.26; 1,024 3.95, 4.04; 4,099 14.9, 14.7; 16,384 54, 51).
 template <bool kQ4, typename TO>
 cudaError_t launch_embed_blocks(const EmbedArgs &a) {
   const int64_t items = a.n * (a.k / kTile);
-  const bool many = items >= 64 * static_cast<int64_t>(a.num_sms);
+  const bool many = items >= 256 * static_cast<int64_t>(a.num_sms);
   const int64_t blocks = (items + (many ? 63 : 15)) / (many ? 64 : 16);
   void (*kernel)(EmbedArgs) = many ? embed_blocks_kernel<kQ4, TO, 4> : embed_blocks_kernel<kQ4, TO, 1>;
   return launch_after(kernel, blocks, 256, 0, a.stream, a);
@@ -261,7 +272,10 @@ cudaError_t launch_embed_to(const EmbedArgs &a) {
 constexpr int kOrderThreads = 1024;
 constexpr int kOrderWarps = kOrderThreads / 32;
 constexpr int kMaxRange = 1536;            // tokens of a CTA: 34 words each, 204 KB
-constexpr int kUnroll = 16;                // positions of a lane in flight
+constexpr int kUnroll = 16;                // positions of a lane in flight; up to 16,384 positions are read once
+
+// One scan or two, as n allows, of all positions by every CTA; latency: loads, counters in shared memory, the prefix
+// sums of 32 warps' counters.
 
 __global__ void __launch_bounds__(kOrderThreads) token_order_kernel(const EmbedBackwardArgs a) {
   extern __shared__ int s_count[];         // [warps][range]: counts, then places; [range] runs' first places, [range] their ends
@@ -395,38 +409,61 @@ __device__ __forceinline__ void write_sum(const EmbedBackwardArgs &a, int64_t to
   store8(p, a.access_out, o);
 }
 
-// After a part of a run of several chunks is stored: the last warp to come adds them up.
+constexpr int kGroup = 32, kManyParts = 64;   // chunks of a group, parts that are joined by groups
+
+// After a chunk's part of a run of several chunks is stored: the last warp to come adds the parts up, in order.  From
+// kManyParts on the chunks of a group are joined first, its sum in place of its first part (16,384 times one token,
+// 1,024 columns: 57 us, all parts by one warp 161).  Counters: chunks that the run holds to the end count no
+// other one, so a group takes its first chunk's, the run the one it begins in, whose group then takes the next.
 template <typename TO>
-__device__ __forceinline__ void join_run(const EmbedBackwardArgs &a, int2 span, int tok, int tile) {
+__device__ __forceinline__ void join_run(const EmbedBackwardArgs &a, int2 span, int tok, int chunk, int tile) {
   const int lane = threadIdx.x & 31, tiles = a.k / kTile, col = tile * kTile + lane * kLane;
-  __threadfence();
-  const int64_t from = span.x / a.chunk, more = (span.y - 1) / a.chunk - from;
-  int came = 0;
-  __syncwarp();
-  if (lane == 0) came = atomicAdd(a.done + from * tiles + tile, 1);
-  if (__shfl_sync(0xffffffffu, came, 0) != more) return;
-  __threadfence();                         // all parts are there
-  const float *part = a.part + from * 2 * a.k + col;
-  float sum[kLane];
-  load8(part + a.k, kWide, sum);
-  constexpr int kParts = 6;                // in flight
-  for (int64_t c = 1; c <= more; c += kParts) {
-    float v[kParts][kLane];
+  const int from = span.x / a.chunk, last = (span.y - 1) / a.chunk;
+  const int group = chunk / kGroup * kGroup, g0 = group > from ? group : from, g1 = group + kGroup - 1 < last ? group + kGroup - 1 : last;
+  const bool many = last - from >= kManyParts;
+  // first of all a group's parts, where it has two or more
+  int first = g0, next = g0 + 1, step = 1, more = g1 - g0, counter = g0 == from ? from + 1 : g0;
+  for (bool whole = !many || more == 0;; whole = true) {
+    if (whole) {
+      first = counter = from;
+      next = many ? from / kGroup * kGroup + kGroup : from + 1;
+      step = many ? kGroup : 1;
+      more = many ? last / kGroup - from / kGroup : last - from;
+    }
+    __threadfence();
+    int came = 0;
+    __syncwarp();
+    if (lane == 0) came = atomicAdd(a.done + (static_cast<int64_t>(counter) * tiles + tile), 1);
+    if (__shfl_sync(0xffffffffu, came, 0) != more) return;
+    __threadfence();                       // all parts are there
+    float *to = a.part + (static_cast<int64_t>(first * 2 + (first == from)) * a.k + col);
+    const float *part = a.part + (static_cast<int64_t>(next) * 2 * a.k + col);
+    const int64_t far = static_cast<int64_t>(step) * 2 * a.k;
+    float sum[kLane];
+    load8(to, kWide, sum);
+    constexpr int kParts = 4;              // in flight
+    for (int c = 0; c < more; c += kParts, part += kParts * far) {
+      float v[kParts][kLane];
 #pragma unroll
-    for (int u = 0; u < kParts; ++u)
-      if (c + u <= more) load8(part + (c + u) * 2 * a.k, kWide, v[u]);
+      for (int u = 0; u < kParts; ++u)
+        if (c + u < more) load8(part + u * far, kWide, v[u]);
 #pragma unroll
-    for (int u = 0; u < kParts; ++u)
-      if (c + u <= more) {
+      for (int u = 0; u < kParts; ++u)
+        if (c + u < more) {
 #pragma unroll
-        for (int i = 0; i < kLane; ++i) sum[i] += v[u][i];
-      }
+          for (int i = 0; i < kLane; ++i) sum[i] += v[u][i];
+        }
+    }
+    if (whole) {
+      write_sum<TO>(a, tok, col, sum);
+      return;
+    }
+    store8(to, kWide, sum);
   }
-  write_sum<TO>(a, tok, col, sum);
 }
 
 template <typename TG, typename TO>
-__global__ void __launch_bounds__(256, 3) sum_runs_kernel(const __grid_constant__ const EmbedBackwardArgs a) {
+__global__ void __launch_bounds__(256, 3) sum_runs_kernel(const __grid_constant__ EmbedBackwardArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tiles = a.k / kTile;
   if (blockIdx.x >= a.sum_blocks) {        // rows without a token
@@ -497,15 +534,16 @@ __global__ void __launch_bounds__(256, 3) sum_runs_kernel(const __grid_constant_
     }
   }
   put(true);
-  if (begun) join_run<TO>(a, span0, a.sorted[j0], tile);
-  if (goes_on && !(first && begun)) join_run<TO>(a, span1, run, tile);
+  if (begun) join_run<TO>(a, span0, a.sorted[j0], static_cast<int>(chunk), tile);
+  if (goes_on && !(first && begun)) join_run<TO>(a, span1, run, static_cast<int>(chunk), tile);
 }
 
-// Sorted positions of a chunk: few, until there are warps for all SMs; at most 1,024
-// chunks, whose parts stay small beside the gradient.
+// Sorted positions of a chunk: few, until there are warps for all SMs (301 positions of 6,656 columns 4 20.0, 8
+// 22.4, 16 26.8 us; 1,024 of 6,656 4 20.7, 8 17.1, 16 19.5; 4,096 of 768 4 35.5, 8 34.8, 16 39; 16,384 of 6,656 16 450, 32 443);
+// at most 1,024 chunks, whose parts stay small beside the gradient.
 int64_t chunk_of(int64_t n, int tiles) {
-  int64_t c = 8;
-  while (c * 1024 < n || n / c * tiles > 16384) c *= 2;
+  int64_t c = 4;
+  while (c * 1024 < n || n / c * tiles > (c < 8 ? 2048 : 16384)) c *= 2;
   return c;
 }
 
@@ -533,7 +571,8 @@ BackwardSpace backward_space(int64_t n, int64_t v, int k) {
 template <typename TG, typename TO>
 cudaError_t launch_sum_runs(EmbedBackwardArgs a, int64_t chunks) {
   a.sum_blocks = static_cast<unsigned>((chunks * (a.k / kTile) + 7) / 8);
-  // a warp zeroes a row, or a part of it where there are few
+  // a warp zeroes a row, or a part of it where there are few (1,024 rows of 6,656 bf16, parts 1 17.5, 4 16.7 us; 50,257
+  // rows of 768 f32 parts 1 34.9, 2 43)
   const int tiles = a.k / kTile;
   a.zero_parts = 1;
   while (a.zero_parts < tiles && a.v * a.zero_parts < 48 * static_cast<int64_t>(a.num_sms)) a.zero_parts *= 2;
