@@ -527,7 +527,7 @@ int muse_lmhead_embed_backward(muse_lmhead *h, const void *grad, int dtype, int6
                                int64_t n, float scale, void *grad_table, int table_dtype, int64_t table_ld,
                                int accumulate, void *workspace, int64_t workspace_bytes, void *stream);
 
-/* Bytes of workspace for n positions (host-only query). */
+/* Bytes of workspace for n positions, enough for fewer too (host-only query). */
 int muse_lmhead_embed_backward_workspace(const muse_lmhead *h, int64_t n, int64_t *bytes);
 
 /* Argmax keys (muse_lmhead_set_argmax_key). */

@@ -19,8 +19,8 @@
 // fixed.  token_order_kernel: a CTA takes a range of tokens and scans all n
 // positions for them twice (counts, then places); a warp has a contiguous share of
 // the positions and a counter for each token of the range, whose prefix sums are
-// the places.  Reading n tokens in every CTA costs n * 4 bytes of L2 against the
-// n * k * 2 bytes of the gradient divided by the number of CTAs, 2 % at most.
+// the places.  Every CTA reads all n tokens, from L2, which takes 27 us for 100,000
+// positions of tokens spread evenly and 55 of uneven ones.
 // sum_runs_kernel: a warp adds up 256 columns of a chunk of sorted positions and
 // writes the runs of one token that lie inside.  A run that goes on leaves a part
 // for each of its chunks; the warp that counts in last adds them up in order, so no
@@ -538,33 +538,35 @@ __global__ void __launch_bounds__(256, 3) sum_runs_kernel(const __grid_constant_
   if (goes_on && !(first && begun)) join_run<TO>(a, span1, run, static_cast<int>(chunk), tile);
 }
 
-// Sorted positions of a chunk: few, until there are warps for all SMs (301 positions of 6,656 columns 4 20.0, 8
-// 22.4, 16 26.8 us; 1,024 of 6,656 4 20.7, 8 17.1, 16 19.5; 4,096 of 768 4 35.5, 8 34.8, 16 39; 16,384 of 6,656 16 450, 32 443);
-// at most 1,024 chunks, whose parts stay small beside the gradient.
-int64_t chunk_of(int64_t n, int tiles) {
-  int64_t c = 4;
-  while (c * 1024 < n || n / c * tiles > (c < 8 ? 2048 : 16384)) c *= 2;
-  return c;
+// Sorted positions of a chunk: as many as let all warps run at once, three CTAs an SM (16,384 positions of 1,024
+// columns f16 into f32 16 49.6, 18 45.8, 24 46.6, 32 52.2 us; 8,192 of 4,096 18 92, 36 90, 64 99; 16,384 of 6,656 32 442, 117
+// 437.5), from 3 (301 of 6,656 f32 3 19.0, 4 20.1, 8 22.4) to 128 (100,000 of 2,048 117 235, 256 244).
+constexpr int64_t kLeastChunk = 3, kMostChunk = 128;
+int64_t chunk_of(int64_t n, int tiles, int num_sms) {
+  const int64_t warps = 24 * static_cast<int64_t>(num_sms), c = (n * tiles + warps - 1) / warps;
+  return c < kLeastChunk ? kLeastChunk : c < kMostChunk ? c : kMostChunk;
 }
 
 // The workspace: count, order, sorted [n], span [n], used [v / 32], done [chunks][tiles], parts
-// [chunks][2][k], each from 256 bytes on.
+// [chunks][2][k], each from 256 bytes on; room for as many chunks as n positions or fewer have.
 struct BackwardSpace {
   size_t order, sorted, span, used, done, part, bytes;
   int64_t chunk, chunks;
 };
-BackwardSpace backward_space(int64_t n, int64_t v, int k) {
+BackwardSpace backward_space(int64_t n, int64_t v, int k, int num_sms) {
   auto up = [](int64_t words) { return (static_cast<size_t>(words) * 4 + 255) / 256 * 256; };
   BackwardSpace s;
-  s.chunk = chunk_of(n, k / kTile);
+  s.chunk = chunk_of(n, k / kTile, num_sms);
   s.chunks = (n + s.chunk - 1) / s.chunk;
+  const int64_t wave = 24 * static_cast<int64_t>(num_sms) / (k / kTile), most = wave > n / kMostChunk ? wave : n / kMostChunk;
+  const int64_t room = (most < n / kLeastChunk ? most : n / kLeastChunk) + 1;
   s.order = 256;
   s.sorted = s.order + up(n);
   s.span = s.sorted + up(n);
   s.used = s.span + up(2 * n);
   s.done = s.used + up((v + 31) / 32);
-  s.part = s.done + up(s.chunks * (k / kTile));
-  s.bytes = s.part + up(s.chunks * 2 * k);
+  s.part = s.done + up(room * (k / kTile));
+  s.bytes = s.part + up(room * 2 * k);
   return s;
 }
 
@@ -595,10 +597,10 @@ cudaError_t launch_embed(const EmbedArgs &a) {
   return launch_embed_to<__nv_bfloat16>(a);
 }
 
-size_t embed_backward_bytes(int64_t n, int64_t v, int k) { return backward_space(n, v, k).bytes; }
+size_t embed_backward_bytes(int64_t n, int64_t v, int k, int num_sms) { return backward_space(n, v, k, num_sms).bytes; }
 
 cudaError_t launch_embed_backward(EmbedBackwardArgs a, void *workspace) {
-  const BackwardSpace s = backward_space(a.n, a.v, a.k);
+  const BackwardSpace s = backward_space(a.n, a.v, a.k, a.num_sms);
   uint8_t *w = static_cast<uint8_t *>(workspace);
   a.count = reinterpret_cast<int *>(w);
   a.order = reinterpret_cast<int *>(w + s.order);

@@ -230,7 +230,7 @@ struct EmbedBackwardArgs {
   unsigned sum_blocks;
   int zero_parts;          // warps of a row of zeros
 };
-size_t embed_backward_bytes(int64_t n, int64_t v, int k);
+size_t embed_backward_bytes(int64_t n, int64_t v, int k, int num_sms);
 cudaError_t launch_embed_backward(EmbedBackwardArgs a, void *workspace);
 
 }  // namespace muse

@@ -771,7 +771,7 @@ int muse_lmhead_embed(muse_lmhead *h, const void *table, int table_type, int64_t
 int muse_lmhead_embed_backward_workspace(const muse_lmhead *h, int64_t n, int64_t *bytes) {
   if (!h || !bytes) return MUSE_ERR_NULL;
   if (n < 0 || n > kMaxPositions - (1 << 20)) return MUSE_ERR_SHAPE;
-  *bytes = static_cast<int64_t>(muse::embed_backward_bytes(n, h->n_rows, static_cast<int>(h->k)));
+  *bytes = static_cast<int64_t>(muse::embed_backward_bytes(n, h->n_rows, static_cast<int>(h->k), h->num_sms));
   return MUSE_OK;
 }
 

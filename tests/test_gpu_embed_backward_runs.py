@@ -53,3 +53,27 @@ def test_long_runs_side_by_side(lengths, k):
 def test_padded_batch_of_one_token():
     """65,536 positions, most of them of one token, others padded."""
     check([60000, 5, 5531], 64, 512, 3)
+
+
+@pytest.mark.parametrize("k", [256, 1024, 6656])
+def test_workspace_serves_fewer_positions(k):
+    """The workspace of n positions is no smaller than that of fewer, and a call with fewer runs in it."""
+    import q5_lm_head_gb300 as q
+    v, most = 40, 5000
+    with q.LMHead(v, k, 1) as head:
+        bytes_of = [q.muse_lmhead_embed_backward_workspace(head.handle, n) for n in range(0, 40000, 7)]
+        assert bytes_of == sorted(bytes_of)
+        large = [q.muse_lmhead_embed_backward_workspace(head.handle, n) for n in range(10 ** 6, 2 * 10 ** 9, 10 ** 7)]
+        assert large == sorted(large) and bytes_of[-1] <= large[0]
+        work = torch.empty((q.muse_lmhead_embed_backward_workspace(head.handle, most),), dtype=torch.uint8, device="cuda")
+        out = torch.empty((v, k), device="cuda")
+        for n in (most, 4999, 3700, 1001, 37, 3, 1, 0):
+            tokens = (torch.arange(n, device="cuda") % 2 * 7).to(torch.int32)
+            grad = torch.randint(-8, 9, (n, k), device="cuda")
+            want = torch.zeros((v, k), dtype=torch.int64, device="cuda").index_add_(0, tokens.long(), grad)
+            grad = grad.to(torch.float32)
+            st = q.muse_lmhead_embed_backward(head.handle, grad.data_ptr(), q.MUSE_DTYPE_F32, k, tokens.data_ptr(), n, 1.0,
+                                              out.data_ptr(), q.MUSE_DTYPE_F32, k, 0, work.data_ptr(), work.numel(),
+                                              torch.cuda.current_stream().cuda_stream)
+            assert st == 0
+            assert torch.equal(out.to(torch.int64), want)
