@@ -461,7 +461,7 @@ typedef struct muse_sampling {
  * A logit of -infinity is a masked one.  A row of nothing else has token -1 and
  * logprob -infinity; a row with a NaN or +infinity, or whose setting is a NaN or
  * a temperature outside its range, token -1 and logprob NaN.  Uses no workspace:
- * calls may overlap.  One launch.
+ * calls may overlap.  One launch, or two for more rows than run at once.
  */
 int muse_lmhead_sample(muse_lmhead *h, const void *logits, int dtype, int64_t n, int64_t ld, const muse_sampling *how,
                        const float *uniforms, int32_t *tokens, float *logprobs, void *stream);

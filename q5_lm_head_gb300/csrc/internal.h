@@ -179,7 +179,8 @@ struct SampleArgs {
   float *logprobs;         // [n] or nullptr
   int num_sms;
   cudaStream_t stream;
-  int held_bytes = 0;      // set at the launch: of a CTA's share in shared memory
+  // set at the launch: bytes of a CTA's share in shared memory; the call's only grid, its first or second
+  int held_bytes = 0, grid = 0;
 };
 cudaError_t launch_sample(const SampleArgs &a);
 

@@ -47,6 +47,7 @@
 namespace muse {
 namespace {
 
+constexpr int kOnly = 0, kFirst = 1, kSecond = 2;   // grids of a call
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kCluster = 16;
 constexpr int kBins = 1024;
@@ -478,39 +479,44 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const int64_t row = blockIdx.x >> cs_log;
   const T *x = static_cast<const T *>(a.logits) + row * a.ld;
   const int64_t v = a.v;
+  if (row >= a.n) {                       // behind the rows of a second grid: it ends no sooner than the first one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   cluster_arrive();                       // waited for before the first store to a peer
 
   // the row as 16-byte vectors from the boundary at or before its first value
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15) / static_cast<int>(sizeof(T));
   const T *x0 = x - off;
   const int64_t vecs = (off + v + W - 1) / W;
-  const int64_t v0 = (vecs * cr) >> cs_log, v1 = (vecs * (cr + 1)) >> cs_log;
+  const int v0 = static_cast<int>((vecs * cr) >> cs_log), v1 = static_cast<int>((vecs * (cr + 1)) >> cs_log);
   // a warp's part of this CTA's share
-  const auto part_begin = [&](int i) { return v0 + (((v1 - v0) * i) / kWarps); };
-  const int64_t w0 = part_begin(warp), w1 = part_begin(warp + 1);
+  const auto part_begin = [&](int i) { return v0 + static_cast<int>(static_cast<int64_t>(v1 - v0) * i / kWarps); };
+  const int w0 = part_begin(warp), w1 = part_begin(warp + 1);
   uint4 *vec_held = reinterpret_cast<uint4 *>(held);
   constexpr int kVecs = kHeld ? kStaged : kRead;
   T *queue = reinterpret_cast<T *>(held + a.held_bytes) + warp * (kVecs * 32 * W);
-  const auto whole = [&](int64_t i) { return i * W >= off && (i + 1) * W <= off + v; };
-  const auto edge = [&](int64_t i) {      // a vector that the row only begins or ends in
+  const int inner0 = off > 0, inner1 = static_cast<int>((off + v) / W);   // vectors that lie in the row entirely
+  const auto whole = [&](int i) { return i >= inner0 && i < inner1; };
+  const auto edge = [&](int i) {          // a vector that the row only begins or ends in
     float o[W];
 #pragma unroll
     for (int e = 0; e < W; ++e) {
-      const int64_t at = i * W + e - off;
+      const int64_t at = static_cast<int64_t>(i) * W + e - off;
       o[e] = at >= 0 && at < v ? to_float(x[at]) : -INFINITY;
     }
     return pack_vec(o, T{});
   };
-  const auto load_vec = [&](int64_t i) {
+  const auto load_vec = [&](int i) {
     if constexpr (kHeld) return vec_held[i - v0];
     else return whole(i) ? reinterpret_cast<const uint4 *>(x0)[i] : edge(i);
   };
-  const auto value_at = [&](int64_t i, int e) {   // of a vector: -infinity beside the row
+  const auto value_at = [&](int i, int e) {       // of a vector: -infinity beside the row
     if constexpr (kHeld) {
       return to_float(reinterpret_cast<const T *>(vec_held + (i - v0))[e]);
     } else {
-      const int64_t at = i * W + e - off;
-      return at >= 0 && at < v ? to_float(x[at]) : -INFINITY;
+      const uint32_t at = static_cast<uint32_t>(i) * W + e - off;
+      return at < static_cast<uint32_t>(v) ? to_float(x[at]) : -INFINITY;
     }
   };
   for (int i = tid; i < kSteps; i += kThreads) sh.table[i] = kPowers.at[i];
@@ -520,9 +526,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
   if (tid < 2 * kOctaves) sh.octave[tid] = 0u;
 
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the logits and settings are complete
+  // The logits and settings are complete; so they are for a second grid, which starts when all CTAs of the first one have
+  // come past here.
+  if (a.grid != kSecond) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (a.grid == kFirst) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if constexpr (kHeld) {
-    for (int64_t i = w0 + lane; i < w1; i += 32) {
+    for (int i = w0 + lane; i < w1; i += 32) {
       uint4 *to = vec_held + (i - v0);
       if (whole(i))
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))),
@@ -562,8 +571,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     __syncwarp();                         // a warp reads what it has fetched itself
   }
 
-  // a step's vectors of a lane from vector i on; nothing beside the part
-  const auto fetch = [&](int64_t i, int64_t end, uint4 (&r)[kVecs]) {
+  // A step's vectors of a lane from vector i on; nothing beside the part.  Where all of a warp's lie inside row and part,
+  // without a test of each (1,024 rows of 202,048 bf16 with top-p 570 us, tested one by one 640).
+  const auto fetch = [&](int i, int end, uint4 (&r)[kVecs]) {
+    const int first = i - lane, next = first + 32 * kVecs;
+    if (!kHeld && first >= inner0 && next <= inner1 && next <= end) {
+      const uint4 *p = reinterpret_cast<const uint4 *>(x0) + i;
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) r[j] = p[32 * j];
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) r[j] = i + 32 * j < end ? load_vec(i + 32 * j) : vec_lowest(T{});
   };
@@ -578,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   {
     uint4 most = vec_lowest(T{});
     int step = 0;
-    for (int64_t i = w0 + lane; i - lane < w1; i += 32 * kVecs) {
+    for (int i = w0 + lane; i - lane < w1; i += 32 * kVecs) {
       uint4 r[kVecs];
       fetch(i, w1, r);
 #pragma unroll
@@ -660,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   w.table = sh.table;                     // known to be in shared memory here
   const float least = sh.least;
 
-  const auto write = [&](float xi, int64_t index, unsigned long long total) {
+  const auto write = [&](float xi, uint32_t index, unsigned long long total) {
     a.tokens[row] = static_cast<int32_t>(index);
     if (a.logprobs)
       a.logprobs[row] = static_cast<float>((static_cast<double>(xi) - m) * sh.inv_t - log_ratio(sh.table, total, weight(sh.w, m)));
@@ -669,9 +686,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     return u >= 1.0f ? total - 1 : u > 0.0f ? part_of(u, total, false) : 0ull;
   };
   // the values of [from, to) of vectors [i0, i1), a few: each(value, index)
-  const auto each_in = [&](int64_t i0, int64_t i1, float from, float to, auto &&each) {
+  const auto each_in = [&](int i0, int i1, float from, float to, auto &&each) {
     const auto least_in = least_from(from, T{}), least_over = least_from(to, T{});
-    for (int64_t i = i0 + lane; i - lane < i1; i += 32 * kVecs) {
+    for (int i = i0 + lane; i - lane < i1; i += 32 * kVecs) {
       uint4 r[kVecs];
       fetch(i, i1, r);
       uint32_t some = 0u, over = 0u;
@@ -685,17 +702,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       for (int j = 0; j < kVecs; ++j) over |= values_from(r[j], j, least_over);
       for (some &= ~over; some != 0u; some &= some - 1) {
         const int bit = __ffs(some) - 1;
-        const int64_t at = i + 32 * vector_of<T>(bit);
-        each(value_at(at, value_of<T>(bit)), at * W + value_of<T>(bit) - off);
+        const int at = i + 32 * vector_of<T>(bit);
+        each(value_at(at, value_of<T>(bit)), static_cast<uint32_t>(at) * W + value_of<T>(bit) - off);
       }
     }
   };
   // The same of many, through the warp's queue, so that all lanes have two at a time: pair(value, value), the second
   // one -infinity where there is none, and done() after a step's.  look(vector)
   // at all of them, with -infinity for those of the range.
-  const auto many_in = [&](int64_t i0, int64_t i1, float from, auto bounded, float to, auto &&look, auto &&pair, auto &&done) {
+  const auto many_in = [&](int i0, int i1, float from, auto bounded, float to, auto &&look, auto &&pair, auto &&done) {
     const auto least_in = least_from(from, T{}), least_over = least_from(to, T{});
-    for (int64_t i = i0 + lane; i - lane < i1; i += 32 * kVecs) {
+    for (int i = i0 + lane; i - lane < i1; i += 32 * kVecs) {
       uint4 r[kVecs];
       fetch(i, i1, r);
       uint32_t some = 0u;
@@ -724,19 +741,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       const int all = __shfl_sync(0xffffffffu, at, 31);
       if (all > 0) {
         T *to_queue = queue + (at - many);
-        if (all < 32 * 2) {               // from the bits that are set
-          for (; some != 0u; some &= some - 1) {
-            const int bit = __ffs(some) - 1;
-            *to_queue++ = from_float<T>(value_at(i + 32 * vector_of<T>(bit), value_of<T>(bit)));
-          }
-        } else {                          // from all of them
 #pragma unroll
-          for (int j = 0; j < kVecs; ++j) {
-            const T *o = reinterpret_cast<const T *>(&r[j]);
+        for (int j = 0; j < kVecs; ++j) {   // bit by bit (a loop over those that are set is slower from a few on)
+          const T *o = reinterpret_cast<const T *>(&r[j]);
 #pragma unroll
-            for (int e = 0; e < W; ++e)
-              if (some & (1u << (sizeof(T) == 4 ? 4 * j + e : 4 * j + e / 2 + 16 * (e & 1)))) *to_queue++ = o[e];
-          }
+          for (int e = 0; e < W; ++e)
+            if (some & (1u << (sizeof(T) == 4 ? 4 * j + e : 4 * j + e / 2 + 16 * (e & 1)))) *to_queue++ = o[e];
         }
         __syncwarp();
         for (int k = lane; k < all; k += 64) pair(to_float(queue[k]), k + 32 < all ? to_float(queue[k + 32]) : -INFINITY);
@@ -751,10 +761,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (few_k) {
     const int room = kBins / cs;
     const uint32_t to = peer_addr(&sh.got[cr * room], 0);
-    each_in(w0, w1, sh.bound, INFINITY, [&](float xi, int64_t index) {
+    each_in(w0, w1, sh.bound, INFINITY, [&](float xi, uint32_t index) {
       const int at = atomicAdd(&sh.few_n, 1);
       if (at < room)
-        peer_store64(to + 8 * at, (static_cast<unsigned long long>(__float_as_uint(xi)) << 32) | static_cast<uint32_t>(index));
+        peer_store64(to + 8 * at, (static_cast<unsigned long long>(__float_as_uint(xi)) << 32) | index);
     });
     __syncthreads();
     if (tid < cs) peer_store32(peer_addr(&sh.from_n[cr], tid), sh.few_n);
@@ -840,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       const uint32_t mask = level < 3 ? 1023u : 3u, fixed = level == 0 ? 0u : ~0u << (32 - 10 * level);
       __syncthreads();
       clear();
-      for (int64_t i = w0 + lane; i < w1; i += 32) {
+      for (int i = w0 + lane; i < w1; i += 32) {
 #pragma unroll 1
         for (int e = 0; e < W; ++e) {
           const float xi = value_at(i, e);
@@ -869,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const auto part_mass = [&]() {
     unsigned long long s = 0ull;
     if (w.wide || w.drop > 0) {
-      for (int64_t i = w0 + lane; i < w1; i += 32) {
+      for (int i = w0 + lane; i < w1; i += 32) {
 #pragma unroll 1
         for (int e = 0; e < W; ++e) s += weight(sh.w, value_at(i, e));
       }
@@ -877,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       uint32_t highs = 0u;                // parts of at most 2^17 each
       long long lows = 0ll;
       int steps = 0;
-      for (int64_t i = w0 + lane; i - lane < w1; i += 32 * kVecs) {
+      for (int i = w0 + lane; i - lane < w1; i += 32 * kVecs) {
         uint4 r[kVecs];
         fetch(i, w1, r);
 #pragma unroll
@@ -932,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     return warp_sum(lane < cs ? sh.from_mass[lane] : 0ull);
   };
   // the mass of the values above t of vectors [i0, i1), and how many equal it
-  const auto part_kept = [&](int64_t i0, int64_t i1, uint32_t &equal) {
+  const auto part_kept = [&](int i0, int i1, uint32_t &equal) {
     unsigned long long s = 0ull;
     uint32_t n = 0u;
     many_in(
@@ -1286,7 +1296,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (sh.part < 0) return;
   const unsigned long long target = sh.target, of_tie = sh.of_tie;
   // its sixteenths, a warp each
-  const int64_t p0 = part_begin(sh.part), p1 = part_begin(sh.part + 1);
+  const int p0 = part_begin(sh.part), p1 = part_begin(sh.part + 1);
   {
     uint32_t equal;
     const unsigned long long mass = part_kept(p0 + (p1 - p0) * warp / kWarps, p0 + (p1 - p0) * (warp + 1) / kWarps, equal);
@@ -1298,7 +1308,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   __syncthreads();
   if (warp != 0) return;
   unsigned long long upto, left;
-  int64_t i0, i1;
+  int i0, i1;
   {
     unsigned long long add;
     const unsigned long long sum = sh.upto + sum_parts(lane < kWarps ? sh.warp_mass[lane] : 0ull, lane < kWarps ? sh.warp_count[lane] : 0u,
@@ -1310,7 +1320,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     i1 = p0 + (p1 - p0) * (part + 1) / kWarps;
   }
   // and its values, 32 vectors at a time
-  for (int64_t i = i0; i < i1; i += 32) {
+  for (int i = i0; i < i1; i += 32) {
     unsigned long long mass = 0ull, add;
     uint32_t n = 0u;
     if (i + lane < i1) {
@@ -1335,7 +1345,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           k = of_tie;
         }
         if (target < here + k) {
-          write(xi, (i + lane) * W + e - off, sh.total);
+          write(xi, static_cast<uint32_t>(i + lane) * W + e - off, sh.total);
           break;
         }
         here += k;
@@ -1382,7 +1392,7 @@ cudaError_t launch_sample_t(SampleArgs a, int cs, int64_t held) {
   a.held_bytes = static_cast<int>(held);
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  const cudaError_t e = sample_config<T, kHeld>(cfg, attr, a.n, cs, static_cast<size_t>(held) + kQueue * (kHeld ? kStaged : kRead), a.stream);
+  const cudaError_t e = sample_config<T, kHeld>(cfg, attr, a.n + (a.grid == kSecond), cs, static_cast<size_t>(held) + kQueue * (kHeld ? kStaged : kRead), a.stream);
   return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, sample_kernel<T, kHeld>, a) : e;
 }
 
@@ -1406,6 +1416,7 @@ cudaError_t clusters_at_once(int cs, bool two, int &fit) {
   return e;
 }
 
+constexpr int kWaves = 4, kLongRow = 32768;   // for a second grid
 // As many CTAs a row as let all rows run at once, two CTAs an SM (times in us for rows of 202,048 f32 with top-p, the
 // whole distribution, top-k, by CTAs a row: 32 rows 8 76, 26, 19, 16 112, 35, 31; 64 rows 4 104, 40, 25, 8 123,
 // 48, 33; 128 rows 2 195, 62, 39, 4 174, 74, 48), 1,024 values each at least; with a third more rows than two CTAs
@@ -1414,7 +1425,7 @@ cudaError_t clusters_at_once(int cs, bool two, int &fit) {
 // held in shared memory where two CTAs' fit into an SM's (16 rows of 202,048 bf16, 8 CTAs each: 51, 22, 15, read
 // again 54, 24, 16), or for the few rows that run at once with one CTA an SM.
 template <typename T>
-cudaError_t launch_sample_rows(const SampleArgs &a) {
+cudaError_t launch_sample_grid(const SampleArgs &a) {
   const int64_t vecs = a.v / Vec<T>::W + 2, queue = kQueue * kStaged;
   auto held = [&](int64_t cs) { return (vecs + cs - 1) / cs * 16; };   // a share is at most this
   int cs = 1, fit = 0;
@@ -1431,6 +1442,36 @@ cudaError_t launch_sample_rows(const SampleArgs &a) {
     if (a.n <= fit) return launch_sample_t<T, true>(a, cs, held(cs));
   }
   return launch_sample_t<T, false>(a, cs, 0);
+}
+
+// Rows that fill the SMs a few times go one to a CTA; what is left then would run by itself on half of the SMs, and
+// goes into a second grid, more CTAs a row, which begins as the first one's last rows end (202,048 bf16
+// with top-p, the whole distribution, top-k: 320 rows in one grid 278, 126, 70 us, in two 239, 117, 61; 400 305, 134, 77, two 268,
+// 138, 70; 1,024 589, 279, 164, two 570, 284, 158; 1,024 of 16,384 131, 59, 48, two 131, 62, 51).
+template <typename T>
+cudaError_t launch_sample_rows(SampleArgs a) {
+  int fit = 0, pairs = 0;
+  cudaError_t e = clusters_at_once<T>(1, true, fit);
+  if (e == cudaSuccess) e = clusters_at_once<T>(2, true, pairs);
+  if (e != cudaSuccess) return e;
+  const int64_t rest = a.n % fit, first = a.n - rest;
+  if (first == 0 || rest == 0 || rest > pairs || first > kWaves * fit || a.v < kLongRow) return launch_sample_grid<T>(a);
+  SampleArgs b = a;
+  a.grid = kFirst;
+  a.n = first;
+  e = launch_sample_grid<T>(a);
+  if (e != cudaSuccess) return e;
+  b.grid = kSecond;
+  b.n = rest;
+  b.logits = static_cast<const T *>(a.logits) + first * a.ld;
+  b.uniforms += first;
+  b.tokens += first;
+  if (b.logprobs) b.logprobs += first;
+  if (b.temperatures) b.temperatures += first;
+  if (b.top_ks) b.top_ks += first;
+  if (b.top_ps) b.top_ps += first;
+  if (b.min_ps) b.min_ps += first;
+  return launch_sample_grid<T>(b);
 }
 
 }  // namespace
