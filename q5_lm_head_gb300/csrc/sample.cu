@@ -286,6 +286,8 @@ struct Shared {
   unsigned long long ties, reached;
   Cross cross;
   int cross_found;
+  unsigned long long scan_mass[kWarps];
+  uint32_t scan_count[kWarps];
   float lowest, guess, sure_guess;       // top-p's estimates
   unsigned long long above_all, need, need_most;
   unsigned long long total, target, upto, left, of_tie;   // of the draw
@@ -327,13 +329,15 @@ __device__ __forceinline__ void add_mass(Shared &sh, uint32_t bin, unsigned long
   if (hi) atomicAdd(&sh.h.high[bin], hi);
 }
 
-// The first bin at which the cluster's histograms reach `target` (values, or mass
+// The first bin at which the cluster's histograms reach target() (values, or mass
 // when by_mass), in every CTA; false when they do not.  To be called when all CTAs'
-// histograms are complete.  Each CTA adds up a slice of
-// the bins, a thread four bins of a CTA (single words from 16 CTAs took 8 us).
-__device__ __forceinline__ bool find_cross(Shared &sh, bool by_mass, unsigned long long target, Cross &out) {
+// histograms are complete.  Each CTA adds up a slice of the bins, a thread four bins of a CTA
+// (single words from 16 CTAs took 8 us).  prepare() is for one warp that has none: target() may use what it wrote.
+template <typename Prepare, typename Target>
+__device__ __forceinline__ bool find_cross(Shared &sh, bool by_mass, const Prepare &prepare, const Target &target_of, Cross &out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cr = cluster_rank(), cs = cluster_size(), slice = kBins / cs;
+  static_assert(kBins / 4 <= kThreads - 32, "a warp is left");
   if (tid < kBins / 4) {
     const int r = tid & (cs - 1), bin = tid / cs * 4, at = cr * slice + bin;
     uint32_t count[4], low[4], high[4];
@@ -358,65 +362,79 @@ __device__ __forceinline__ bool find_cross(Shared &sh, bool by_mass, unsigned lo
         sh.slice.mass[bin + i] = mass;
       }
     }
+  } else if (warp == kWarps - 1) {
+    prepare();
   }
   __syncthreads();
-  // a warp's lanes take the slice's bins, up to 32 each
-  const int each = slice / 32;
-  unsigned long long before = 0ull;
-  uint32_t before_n = 0u;
-  if (warp == 0) {
-    unsigned long long sum = 0ull;
-    uint32_t number = 0u;
-    for (int i = 0; i < each; ++i) {      // each lane from a place of its own, on banks of its own
-      const int at = lane * each + ((i + lane) & (each - 1));
-      sum += sh.slice.mass[at];
-      number += sh.slice.number[at];
-    }
-    before = sum;
-    before_n = number;
+  // a thread a bin of the slice, of a CTA by itself two
+  const int each = slice > kThreads ? 2 : 1, bin = tid * each;
+  static_assert(kBins <= 2 * kThreads, "two bins a thread");
+  unsigned long long mass[2] = {0ull, 0ull}, upto = 0ull;
+  uint32_t number[2] = {0u, 0u}, upto_n = 0u;
+  if (warp * 32 * each < slice) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (i < each && bin + i < slice) {
+        mass[i] = sh.slice.mass[bin + i];
+        number[i] = sh.slice.number[bin + i];
+      }
+    upto = mass[0] + mass[1];
+    upto_n = number[0] + number[1];
     for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long a = __shfl_up_sync(0xffffffffu, before, o);
-      const uint32_t b = __shfl_up_sync(0xffffffffu, before_n, o);
+      const unsigned long long a = __shfl_up_sync(0xffffffffu, upto, o);
+      const uint32_t b = __shfl_up_sync(0xffffffffu, upto_n, o);
       if (lane >= o) {
-        before += a;
-        before_n += b;
+        upto += a;
+        upto_n += b;
       }
     }
-    const unsigned long long all = __shfl_sync(0xffffffffu, before, 31);
-    const uint32_t all_n = __shfl_sync(0xffffffffu, before_n, 31);
+  }
+  if (lane == 31) {
+    sh.scan_mass[warp] = upto;
+    sh.scan_count[warp] = upto_n;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const unsigned long long all = warp_sum(lane < kWarps ? sh.scan_mass[lane] : 0ull);
+    const uint32_t all_n = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.scan_count[lane] : 0u);
     if (lane < cs) {
       peer_store64(peer_addr(&sh.slice_mass[cr], lane), all);
       peer_store32(peer_addr(&sh.slice_count[cr], lane), all_n);
     }
-    before -= sum;
-    before_n -= number;
   }
   cluster_sync();
-  if (warp == 0) {
-    unsigned long long mine = lane < cs ? sh.slice_mass[lane] : 0ull, total = mine;
-    uint32_t mine_n = lane < cs ? sh.slice_count[lane] : 0u;
-    total = warp_sum(mine);
-    const uint32_t total_n = __reduce_add_sync(0xffffffffu, mine_n);
-    before += warp_sum(lane < cr ? mine : 0ull);
-    before_n += __reduce_add_sync(0xffffffffu, lane < cr ? mine_n : 0u);
-    if (lane == 0) sh.cross_found = (by_mass ? total : total_n) >= target;
-    // the lane whose bins it is in, and the bin
-    unsigned long long sum = by_mass ? before : before_n;
+  if (warp * 32 * each < slice) {
+    const unsigned long long target = target_of();
+    const unsigned long long mine = lane < cs ? sh.slice_mass[lane] : 0ull;
+    const uint32_t mine_n = lane < cs ? sh.slice_count[lane] : 0u;
+    if (warp == 0) {
+      const unsigned long long total = by_mass ? warp_sum(mine) : __reduce_add_sync(0xffffffffu, mine_n);
+      if (lane == 0) sh.cross_found = total >= target;
+    }
+    // before the thread's bins: the slices of the CTAs before, the warps before, the lanes before
+    static_assert(kWarps <= 16 && kCluster <= 16, "half a warp each");
+    unsigned long long before = lane < cr ? mine : 0ull;
+    uint32_t before_n = lane < cr ? mine_n : 0u;
+    if (lane >= 16 && lane - 16 < warp) {
+      before = sh.scan_mass[lane - 16];
+      before_n = sh.scan_count[lane - 16];
+    }
+    before = warp_sum(before) + upto - mass[0] - mass[1];
+    before_n = __reduce_add_sync(0xffffffffu, before_n) + upto_n - number[0] - number[1];
     int at = -1;
-    if (sum < target)
-      for (int i = 0; i < each; ++i) {
-        const unsigned long long m = sh.slice.mass[lane * each + i];
-        const uint32_t n = sh.slice.number[lane * each + i];
-        sum += by_mass ? m : n;
-        if (sum >= target) {
-          at = lane * each + i;
-          break;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (at < 0) {
+        const unsigned long long sum = by_mass ? before : before_n, one = by_mass ? mass[i] : number[i];
+        if (sum < target && target <= sum + one) {
+          at = bin + i;
+        } else if (i == 0) {
+          before += mass[0];
+          before_n += number[0];
         }
-        before += m;
-        before_n += n;
       }
     const uint32_t here = __ballot_sync(0xffffffffu, at >= 0);
-    if (here) {                           // the first of them; a lane for each CTA
+    if (here) {                           // a lane for each CTA
       const int from = __ffs(here) - 1;
       at = __shfl_sync(0xffffffffu, at, from);
       before = __shfl_sync(0xffffffffu, before, from);
@@ -863,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
       cluster_sync();
       Cross at;
-      if (!find_cross(sh, by_mass, target, at)) return false;   // only at the first level
+      if (!find_cross(sh, by_mass, [] {}, [&] { return target; }, at)) return false;   // only at the first level
       target -= by_mass ? at.mass : at.count;
       mass += at.mass;
       key |= at.bin << shift;
@@ -1111,31 +1129,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
       }
       cluster_sync();
-      if (warp == 0) {
-        above = warp_sum(lane < cs ? sh.from_total[lane] : 0ull);
-        upper = warp_sum(lane < cs ? sh.from_mass[lane] : 0ull);
-        tail = warp_sum(lane < cs ? sh.from_tail[lane] : 0ull);
-        if (lane == 0) {
-          const unsigned long long slack = static_cast<unsigned long long>(static_cast<float>(tail) * off_by) + static_cast<unsigned long long>(v);
-          sh.above_all = above;
-          sh.need = part_of(top_p, upper + (tail > slack ? tail - slack : 0ull), true);
-          sh.need_most = part_of(top_p, upper + tail + slack, true);
-        }
-      }
-      __syncthreads();
-      above = sh.above_all;
       // What top-p needs at least and at most; where that leaves two borders, by the row's mass itself.
 #pragma unroll 1
       for (int exact = 0; exact < 2 && !found; ++exact) {
-        unsigned long long need = sh.need, need_most = sh.need_most;
         if (exact) {
           cluster_sync();                 // all have read what came before
           mass_k = whole_mass();
-          need = need_most = part_of(top_p, mass_k, true);
         }
-        if (need <= above) break;         // above what is sure
+        const auto needed = [&] {         // by one warp
+          if (exact) {
+            if (lane == 0) sh.need = sh.need_most = part_of(top_p, mass_k, true);
+            return;
+          }
+          const unsigned long long sure = warp_sum(lane < cs ? sh.from_total[lane] : 0ull);
+          const unsigned long long known = warp_sum(lane < cs ? sh.from_mass[lane] : 0ull), rest = warp_sum(lane < cs ? sh.from_tail[lane] : 0ull);
+          const unsigned long long slack = static_cast<unsigned long long>(static_cast<float>(rest) * off_by) + static_cast<unsigned long long>(v);
+          if (lane == 0) {
+            sh.above_all = sure;
+            sh.need = part_of(top_p, known + (rest > slack ? rest - slack : 0ull), true);
+          }
+          if (lane == 1) sh.need_most = part_of(top_p, known + rest + slack, true);
+        };
         Cross at;
-        if (!find_cross(sh, true, need - above, at)) {
+        const bool there = find_cross(sh, true, needed, [&] { return sh.need > sh.above_all ? sh.need - sh.above_all : 0ull; }, at);
+        above = sh.above_all;
+        const unsigned long long need = sh.need, need_most = sh.need_most;
+        if (need <= above) break;         // above what is sure
+        if (!there) {
           settled = !guessed && from == least;   // min-p keeps less
           break;
         }
