@@ -277,6 +277,7 @@ struct Shared {
   float group[kGroups];                  // of the cluster
   Weigher w;
   double least_off, inv_t;               // T log(min_p), 1 / T
+  float c_off;                           // w.c0 is off by, at most
   float bound, least;                    // of top-k, min-p
   int few_n;                             // listed
   uint32_t sampled;
@@ -580,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     sh.w.c2 = static_cast<float>(c * kSteps - sh.w.c1);
     sh.w.c = c;
     sh.w.c0 = static_cast<float>(c);
+    sh.c_off = __double2float_ru(fabs(c - sh.w.c0) + 0x1p-50 * c);
     sh.w.drop = v > (int64_t{1} << 24) ? 40 - __clzll(v - 1) : 0;   // bits of v - 1 beyond 24
     sh.inv_t = 1.0 / temperature;
     sh.least_off = by_m ? temperature * log(min_p < 1.0f ? static_cast<double>(min_p) : 1.0) : 0.0;
@@ -1062,9 +1064,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     __syncthreads();
     const float lowest = sh.lowest, guess = sh.guess, sure_guess = sh.sure_guess;
-    // What the mass below may be off by: the products' roundings (of log2(e) / T too), 2 ulp of an exponential, 16 additions, and
-    // half of the last place of every weight.
-    const float off_by = 0.6931472f * 0x1p-24f * (44.0f + fmaxf(fabsf(m), fabsf(w.floor)) * w.c0) + 0x1p-22f + 0x1.1p-20f + 0x1p-32f;
+    // What the mass below may be off by, of itself: an exponent's rounding (half the last place of numbers up to 32; below
+    // 2^-32 of 2^E a weight has 64 units, and v units are added anyway), that of log2(e) / T, as it is, 2 ulp of an exponential, eight
+    // additions, and the weights' own 2^-32.
+    const float off_by = 0.6931472f * (0x1p-20f + fmaxf(fabsf(m), fabsf(m - 33.0f / w.c0)) * sh.c_off) + 0x1p-22f + 0x1.1p-21f + 0x1p-32f;
     bool settled = false, guessed = guess > lowest || sure_guess < INFINITY, found = false;
 #pragma unroll 1
     for (int attempt = 0; attempt < 2 && !found; ++attempt) {
@@ -1090,11 +1093,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           [&](const uint4 &r) {
             float o[W];
             unpack(r, o, T{});
+            unsigned long long of_vec = 0ull;   // at most three additions, four to the step's sum, one of its halves
 #pragma unroll
             for (int e = 0; e < W; e += 2) {
               const float2 y = unpack2(fma2(pack2(o[e], o[e + 1]), c2, e2));
-              sum = add2(sum, pack2(exp2_approx(y.x), exp2_approx(y.y)));
+              const unsigned long long two = pack2(exp2_approx(y.x), exp2_approx(y.y));
+              of_vec = e == 0 ? two : add2(of_vec, two);
             }
+            sum = add2(sum, of_vec);
           },
           [&](float xi, float xj) {
             uint32_t high[2];
