@@ -26,14 +26,14 @@
 // read again (from L2) by each pass.  The passes:
 //   - the maximum, maxima of groups of threads, a sample.
 //   - top-k up to 512: the k-th largest of at least k maxima is a bound that k values reach; what reaches it goes to
-//     the first CTA, which does the rest with these few (1 row of 202,048 f32 with top-k 50 and top-p 11.5 us).
-//   - no filter: the mass of the parts (16 rows 23 us).
+//     the first CTA, which does the rest with these few (1 row of 202,048 f32 with top-k 50 and top-p 11.1 us).
+//   - no filter: the mass of the parts (16 rows 21 us).
 //   - top-p: by the sample and the maxima the border lies in an octave or two.  Values from there up are summed as
 //     weights, those in the octaves by a histogram of 1,024 bins, those below only about, by exponentials in 32 bits whose
 //     error has a bound: of the row's mass they are 1 - p.  Then the bin in which the sum reaches p of the least and
 //     of the most that the mass can be, and in one more pass its values, settled one by one.  Where the two differ (one
-//     row in eight of 202,048 bf16 values with 28,000 kept), the row's mass is summed as weights and the bin taken
-//     again.  1,024 such rows 637 us; with weights for every value and pass 1,169, with histograms over the ordered bits 2,296.
+//     row in 13 of 202,048 bf16 values with 28,000 kept), the row's mass is summed as weights and the bin taken
+//     again.  1,024 such rows 518 us; with weights for every value and pass 1,169, with histograms over the ordered bits 2,296.
 //   - the CTA in whose kept mass the number falls, its warp's part, its sixteenth, its value.
 // What does not fit (equal logits by the thousand, a border in a crowd, weights in 64 bits) is selected by histograms
 // over the ordered bits of the logits, 10 bits at a time.  Nothing is kept in global memory, so calls may overlap.
@@ -1444,12 +1444,12 @@ cudaError_t clusters_at_once(int cs, bool two, int &fit) {
 
 constexpr int kWaves = 4, kLongRow = 32768;   // for a second grid
 // As many CTAs a row as let all rows run at once, two CTAs an SM (times in us for rows of 202,048 f32 with top-p, the
-// whole distribution, top-k, by CTAs a row: 32 rows 8 76, 26, 19, 16 112, 35, 31; 64 rows 4 104, 40, 25, 8 123,
-// 48, 33; 128 rows 2 195, 62, 39, 4 174, 74, 48), 1,024 values each at least; with a third more rows than two CTAs
-// each have room, two each still (200 rows 251, 103, 81, one each 316, 119, 71); 16 CTAs share an SM with others from
-// eight rows on, which only long rows make up for (8 rows of 50,257 f32 16 27, 12.8, 12.8, 8 26, 12.4, 11.3).  A share is
-// held in shared memory where two CTAs' fit into an SM's (16 rows of 202,048 bf16, 8 CTAs each: 51, 22, 15, read
-// again 54, 24, 16), or for the few rows that run at once with one CTA an SM.
+// whole distribution, top-k, by CTAs a row: 32 rows 4 64, 24, 16, 8 57, 23, 15, 16 89, 34, 28; 64 rows 2 97, 34, 21, 4 77, 33,
+// 20, 8 92, 41, 28; 128 rows 1 184, 67, 38, 2 142, 51, 30, 4 142, 63, 39), 1,024 values each at least; with a third more
+// rows than two CTAs each have room, two each still (200 rows 198, 93, 74, one each 219, 106, 64); 16 CTAs share an SM with others
+// from eight rows on, which only long rows make up for (8 rows of 50,257 f32 16 26, 11.7, 12.4, 8 24, 11.7, 10.7).  A share is
+// held in shared memory where two CTAs' fit into an SM's (16 rows of 202,048 bf16, 8 CTAs each: 39.8, 22.2, 13.7, read
+// again 40.9, 23.1, 14.1), or for the few rows that run at once with one CTA an SM.
 template <typename T>
 cudaError_t launch_sample_grid(const SampleArgs &a) {
   const int64_t vecs = a.v / Vec<T>::W + 2, queue = kQueue * kStaged;
@@ -1471,9 +1471,9 @@ cudaError_t launch_sample_grid(const SampleArgs &a) {
 }
 
 // Rows that fill the SMs a few times go one to a CTA; what is left then would run by itself on half of the SMs, and
-// goes into a second grid, more CTAs a row, which begins as the first one's last rows end (202,048 bf16
-// with top-p, the whole distribution, top-k: 320 rows in one grid 278, 126, 70 us, in two 239, 117, 61; 400 305, 134, 77, two 268,
-// 138, 70; 1,024 589, 279, 164, two 570, 284, 158; 1,024 of 16,384 131, 59, 48, two 131, 62, 51).
+// goes into a second grid, more CTAs a row, which begins as the first one's last rows end (202,048 bf16 with top-p, the whole
+// distribution, top-k: 320 rows in one grid 309, 128, 72 us, in two 207, 117, 63; 400 285, 134, 78, two 250, 139, 71; 1,024
+// 536, 280, 167, two 521, 285, 162; 1,024 rows of 16,384 131, 59, 48, two 131, 62, 51).
 template <typename T>
 cudaError_t launch_sample_rows(SampleArgs a) {
   int fit = 0, pairs = 0;
