@@ -28,14 +28,17 @@
 //   - top-k up to 512: the k-th largest of at least k maxima is a bound that k values reach; what reaches it goes to
 //     the first CTA, which does the rest with these few (1 row of 202,048 f32 with top-k 50 and top-p 11.1 us).
 //   - no filter: the mass of the parts (16 rows 21 us).
-//   - top-p: by the sample and the maxima the border lies in an octave or two.  Values from there up are summed as
+//   - top-p: by the sample and the maxima the border lies in an octave or so.  Values from there up are summed as
 //     weights, those in the octaves by a histogram of 1,024 bins, those below only about, by exponentials in 32 bits whose
 //     error has a bound: of the row's mass they are 1 - p.  Then the bin in which the sum reaches p of the least and
 //     of the most that the mass can be, and in one more pass its values, settled one by one.  Where the two differ (one
 //     row in 13 of 202,048 bf16 values with 28,000 kept), the row's mass is summed as weights and the bin taken
-//     again.  1,024 such rows 518 us; with weights for every value and pass 1,169, with histograms over the ordered bits 2,296.
+//     again.  1,024 such rows 516 us; with weights for every value and pass 1,169, with histograms over the ordered bits 2,296.
+//     A bin of more than 512 values is settled if they are all equal, as 16-bit logits far from 0 are (1,024 bf16 rows
+//     around 8 467 us, selected as below 3,373).
 //   - the CTA in whose kept mass the number falls, its warp's part, its sixteenth, its value.
-// What does not fit (equal logits by the thousand, a border in a crowd, weights in 64 bits) is selected by histograms
+// What does not fit (top-k's border among equal logits by the hundred, a crowd of different ones in a bin, weights in
+// 64 bits) is selected by histograms
 // over the ordered bits of the logits, 10 bits at a time.  Nothing is kept in global memory, so calls may overlap.
 #include <atomic>
 #include <type_traits>
@@ -1010,6 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     cluster_sync();
     if (warp == 0) {
       float number = 0.0f, mine[2] = {0.0f, 0.0f}, largest = 0.0f;   // of the lane's two octaves
+      bool known[2] = {false, false};
       for (int r = 0; r < cs; ++r) number += static_cast<float>(sh.from_sampled[r]);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -1023,6 +1027,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           // one of the largest in the sample would stand for many that are not there: 16 at least
           mine[h] = fmaxf(some >= 16.0f * 384.0f ? some * (static_cast<float>(v) / fmaxf(number, 1.0f)) : 0.0f, high) * unit;
           largest += high * unit;
+          known[h] = some >= 128.0f * 384.0f;
         }
       float about = mine[0] + mine[1];
       for (int o = 16; o > 0; o >>= 1) {
@@ -1037,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       float guess = low, sure_guess = INFINITY;
       {
         const float enough = (1.0f - top_p) * about;
-        float below = 0.0f;
+        float below = 0.0f, upto[2];
         int low_cut = kOctaves, high_cut = -1;
 #pragma unroll
         for (int h = 1; h >= 0; --h) {
@@ -1050,10 +1055,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           const uint32_t little = __ballot_sync(0xffffffffu, s + below < 0.7f * enough), much = __ballot_sync(0xffffffffu, s + below > 1.4f * enough);
           if (little) low_cut = 32 * h + __ffs(little) - 1;
           if (much && high_cut < 0) high_cut = 32 * h + 31 - __clz(much);
+          upto[h] = s + below;
           below += __shfl_sync(0xffffffffu, s, 0);
         }
-        if (low_cut < kOctaves) guess = fmaxf(low, (w.e - static_cast<float>(low_cut - 1)) / w.c0);
-        if (high_cut > 0) sure_guess = (w.e - static_cast<float>(high_cut - 1)) / w.c0;
+        // where in octave o a mass lies below, about, as a part of it; `other` where the sample has few values of it
+        const auto part = [&](int o, float mass, float other) {
+          const float all = __shfl_sync(0xffffffffu, upto[o >> 5], o & 31), one = __shfl_sync(0xffffffffu, mine[o >> 5], o & 31);
+          return __shfl_sync(0xffffffffu, known[o >> 5], o & 31) ? (mass - (all - one)) / one : other;
+        };
+        // with a quarter of the lower part less and a quarter of an octave more, as the mass need not be even in an octave
+        if (low_cut < kOctaves) {
+          const float in = low_cut > 0 ? fminf(fmaxf(0.75f * part(low_cut - 1, 0.7f * enough, 0.0f), 0.0f), 1.0f) : 0.0f;
+          guess = fmaxf(low, (w.e - static_cast<float>(low_cut - 1) + in) / w.c0);
+        }
+        if (high_cut > 0) sure_guess = (w.e - static_cast<float>(high_cut) + fminf(fmaxf(0.25f + part(high_cut, 1.4f * enough, 1.0f), 0.0f), 1.0f)) / w.c0;
         if (!(sure_guess > guess)) sure_guess = INFINITY;
       }
       if (lane == 0) {
@@ -1165,7 +1180,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           settled = !guessed && from == least;   // min-p keeps less
           break;
         }
-        if (at.in > kFew) break;
+        // More than there is room for are settled only if they are all equal (logits of 16 bits).
+        const bool crowd = at.in > kFew;
+        uint32_t crowd_low = ~0u, crowd_high = 0u, crowd_n = 0u;
         const unsigned long long before = above + at.mass;
         // One more pass from the bin's lower end up, to the roundings of a difference and two products: the bin's values to
         // all CTAs, and the mass between it and what is sure.
@@ -1173,6 +1190,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         const float low_end = fmaxf(from, base - (static_cast<float>(at.bin) + 1.01f) / scale - wide);
         const float high_end = base - (static_cast<float>(at.bin) - 0.01f) / scale + wide;   // from here up no value is in the bin
         const auto hand = [&](float xi) {
+          if (crowd) {
+            const uint32_t k = float_order_key(xi + 0.0f);   // -0 as 0
+            crowd_low = min(crowd_low, k);
+            crowd_high = max(crowd_high, k);
+            ++crowd_n;
+            return;
+          }
           const int place = static_cast<int>(at.place) + atomicAdd(&sh.few_n, 1);
           for (int r = 0; r < cs; ++r) peer_store32(peer_addr(&sh.edge.x[place], r), __float_as_uint(xi));
           sh.edge.warp[place] = static_cast<uint8_t>(warp);
@@ -1200,11 +1224,37 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             },
             nothing);
         between = warp_sum(between);
+        if (crowd) {
+          crowd_low = __reduce_min_sync(0xffffffffu, crowd_low);
+          crowd_high = __reduce_max_sync(0xffffffffu, crowd_high);
+          crowd_n = __reduce_add_sync(0xffffffffu, crowd_n);
+          if (lane == 0) sh.warp_tail[warp] = static_cast<unsigned long long>(crowd_low) << 32 | crowd_high;
+          __syncthreads();
+          if (warp == 0) {
+            const unsigned long long two = sh.warp_tail[lane & (kWarps - 1)];
+            const uint32_t low = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(two >> 32));
+            const uint32_t high = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(two));
+            if (lane < cs) peer_store64(peer_addr(&sh.from_tail[cr], lane), static_cast<unsigned long long>(low) << 32 | high);
+          }
+        }
         cluster_sync();
         const int n = static_cast<int>(at.in);
-        if (tid < n) sh.edge.mass[tid] = weight(sh.w, sh.edge.x[tid]);
+        if (crowd) {
+          const unsigned long long two = sh.from_tail[lane & (cs - 1)];
+          crowd_low = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(two >> 32));
+          crowd_high = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(two));
+          if (crowd_low != crowd_high) break;
+          if (tid == 0) {
+            const unsigned long long of_one = weight(sh.w, order_key_float(crowd_low)), many = (need - before + of_one - 1) / of_one;
+            sh.border = order_key_float(crowd_low);
+            sh.ties = many;
+            sh.reached = before + many * of_one;
+          }
+        } else if (tid < n) {
+          sh.edge.mass[tid] = weight(sh.w, sh.edge.x[tid]);
+        }
         __syncthreads();
-        if (warp == 0) {
+        if (warp == 0 && !crowd) {
           // the largest key at which the mass from it up reaches what is needed: between the bin's ends, bit by bit
           uint32_t high = 0u, low = ~0u;
           for (int j = lane; j < n; j += 32) {
@@ -1253,9 +1303,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           found = true;
           // what the warps keep: all above the bin, and of the bin
           if (lane == 0) sh.above[warp] += between;
-          if (tid < kWarps) sh.warp_count[tid] = 0u;
+          if (crowd) {
+            if (lane == 0) sh.warp_count[warp] = crowd_n;
+          } else if (tid < kWarps) {
+            sh.warp_count[tid] = 0u;
+          }
           __syncthreads();
-          const int own_n = sh.few_n;
+          const int own_n = crowd ? 0 : sh.few_n;
           for (int j = tid; j < own_n; j += kThreads) {
             const int k = static_cast<int>(at.place) + j;
             const float xi = sh.edge.x[k];
