@@ -26,14 +26,14 @@
 // read again (from L2) by each pass.  The passes:
 //   - the maximum, maxima of groups of threads, a sample.
 //   - top-k up to 512: the k-th largest of at least k maxima is a bound that k values reach; what reaches it goes to
-//     the first CTA, which does the rest with these few (1 row of 202,048 f32 with top-k 50 and top-p 11.1 us).
+//     the first CTA, which does the rest with these few (1 row of 202,048 f32 with top-k 50 and top-p 11.0 us).
 //   - no filter: the mass of the parts (16 rows 21 us).
 //   - top-p: by the sample and the maxima the border lies in an octave or so.  Values from there up are summed as
 //     weights, those in the octaves by a histogram of 1,024 bins, those below only about, by exponentials in 32 bits whose
 //     error has a bound: of the row's mass they are 1 - p.  Then the bin in which the sum reaches p of the least and
 //     of the most that the mass can be, and in one more pass its values, settled one by one.  Where the two differ (one
 //     row in 13 of 202,048 bf16 values with 28,000 kept), the row's mass is summed as weights and the bin taken
-//     again.  1,024 such rows 516 us; with weights for every value and pass 1,169, with histograms over the ordered bits 2,296.
+//     again.  1,024 such rows 512 us; with weights for every value and pass 1,169, with histograms over the ordered bits 2,296.
 //     A bin of more than 512 values is settled if they are all equal, as 16-bit logits far from 0 are (1,024 bf16 rows
 //     around 8 467 us, selected as below 3,373).
 //   - the CTA in whose kept mass the number falls, its warp's part, its sixteenth, its value.
@@ -459,7 +459,7 @@ __device__ __forceinline__ bool find_cross(Shared &sh, bool by_mass, const Prepa
 
 // Parts of a sum one behind another, a lane's each: `mass` and `count` equals of the threshold, of which `left` are
 // still kept.  Returns the sum up to and with the lane's part; `add` is that part, `mine` what is left of the equals there.
-__device__ __noinline__ unsigned long long sum_parts(unsigned long long mass, uint32_t count, unsigned long long left,
+__device__ __forceinline__ unsigned long long sum_parts(unsigned long long mass, uint32_t count, unsigned long long left,
                                                      unsigned long long of_tie, unsigned long long &add, unsigned long long &mine) {
   const int lane = threadIdx.x & 31;
   uint32_t upto = count;
@@ -586,16 +586,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     sh.w.c0 = static_cast<float>(c);
     sh.c_off = __double2float_ru(fabs(c - sh.w.c0) + 0x1p-50 * c);
     sh.w.drop = v > (int64_t{1} << 24) ? 40 - __clzll(v - 1) : 0;   // bits of v - 1 beyond 24
-    sh.inv_t = 1.0 / temperature;
-    sh.least_off = by_m ? temperature * log(min_p < 1.0f ? static_cast<double>(min_p) : 1.0) : 0.0;
+    sh.inv_t = c * 0.6931471805599453;
   }
+  if (tid == 32) sh.least_off = by_m ? temperature * log(min_p < 1.0f ? static_cast<double>(min_p) : 1.0) : 0.0;
   if constexpr (kHeld) {
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();                         // a warp reads what it has fetched itself
   }
 
   // A step's vectors of a lane from vector i on; nothing beside the part.  Where all of a warp's lie inside row and part,
-  // without a test of each (1,024 rows of 202,048 bf16 with top-p 570 us, tested one by one 640).
+  // without a test of each (1,024 rows of 202,048 bf16 with top-p 581 us, tested one by one 640).
   const auto fetch = [&](int i, int end, uint4 (&r)[kVecs]) {
     const int first = i - lane, next = first + 32 * kVecs;
     if (!kHeld && first >= inner0 && next <= inner1 && next <= end) {
