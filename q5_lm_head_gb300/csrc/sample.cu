@@ -25,7 +25,8 @@
 // so that prefix sums over CTAs and warps follow the index.  A share is held in shared memory where that fits, else
 // read again (from L2) by each pass.  The passes:
 //   - the maximum, maxima of groups of threads, a sample.
-//   - top-k up to 512: the k-th largest of at least k maxima is a bound that k values reach; what reaches it goes to
+//   - top-k up to 512 (few enough reach the bound up to about 300): the k-th largest of at least k maxima is a bound
+//     that k values reach; what reaches it goes to
 //     the first CTA, which does the rest with these few (1 row of 202,048 f32 with top-k 50 and top-p 11.0 us).
 //   - no filter: the mass of the parts (16 rows 21 us).
 //   - top-p: by the sample and the maxima the border lies in an octave or so.  Values from there up are summed as
@@ -38,7 +39,7 @@
 //     around 8 467 us, selected as below 3,373).
 //   - the CTA in whose kept mass the number falls, its warp's part, its sixteenth, its value.
 // What does not fit (top-k's border among equal logits by the hundred, a crowd of different ones in a bin, weights in
-// 64 bits) is selected by histograms
+// 64 bits, top-k beyond some 300) is selected by histograms
 // over the ordered bits of the logits, 10 bits at a time.  Nothing is kept in global memory, so calls may overlap.
 #include <atomic>
 #include <type_traits>
