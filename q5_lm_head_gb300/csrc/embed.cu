@@ -32,14 +32,14 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "embed_space.h"
 #include "internal.h"
 #include "rows.cuh"
 
 namespace muse {
 namespace {
 
-constexpr int kTile = 256;                 // columns of a warp: a block
-constexpr int kLane = 8;                   // of a lane
+constexpr int kLane = 8;                   // columns of a lane, of a warp's kTile
 
 // Eight consecutive values of a lane: one access where rows lie on its size (kWide: 16
 // bytes, of f32 32), two of 16 bytes for other f32 rows on 16 bytes, else value by value
@@ -538,38 +538,6 @@ __global__ void __launch_bounds__(256, 3) sum_runs_kernel(const __grid_constant_
   if (goes_on && !(first && begun)) join_run<TO>(a, span1, run, static_cast<int>(chunk), tile);
 }
 
-// Sorted positions of a chunk: as many as let all warps run at once, three CTAs an SM (16,384 positions of 1,024
-// columns f16 into f32 16 49.6, 18 45.8, 24 46.6, 32 52.2 us; 8,192 of 4,096 18 92, 36 90, 64 99; 16,384 of 6,656 32 442, 117
-// 437.5), from 3 (301 of 6,656 f32 3 19.0, 4 20.1, 8 22.4) to 128 (100,000 of 2,048 117 235, 256 244).
-constexpr int64_t kLeastChunk = 3, kMostChunk = 128;
-int64_t chunk_of(int64_t n, int tiles, int num_sms) {
-  const int64_t warps = 24 * static_cast<int64_t>(num_sms), c = (n * tiles + warps - 1) / warps;
-  return c < kLeastChunk ? kLeastChunk : c < kMostChunk ? c : kMostChunk;
-}
-
-// The workspace: count, order, sorted [n], span [n], used [v / 32], done [chunks][tiles], parts
-// [chunks][2][k], each from 256 bytes on; room for as many chunks as n positions or fewer have.
-struct BackwardSpace {
-  size_t order, sorted, span, used, done, part, bytes;
-  int64_t chunk, chunks;
-};
-BackwardSpace backward_space(int64_t n, int64_t v, int k, int num_sms) {
-  auto up = [](int64_t words) { return (static_cast<size_t>(words) * 4 + 255) / 256 * 256; };
-  BackwardSpace s;
-  s.chunk = chunk_of(n, k / kTile, num_sms);
-  s.chunks = (n + s.chunk - 1) / s.chunk;
-  const int64_t wave = 24 * static_cast<int64_t>(num_sms) / (k / kTile), most = wave > n / kMostChunk ? wave : n / kMostChunk;
-  const int64_t room = (most < n / kLeastChunk ? most : n / kLeastChunk) + 1;
-  s.order = 256;
-  s.sorted = s.order + up(n);
-  s.span = s.sorted + up(n);
-  s.used = s.span + up(2 * n);
-  s.done = s.used + up((v + 31) / 32);
-  s.part = s.done + up(room * (k / kTile));
-  s.bytes = s.part + up(room * 2 * k);
-  return s;
-}
-
 template <typename TG, typename TO>
 cudaError_t launch_sum_runs(EmbedBackwardArgs a, int64_t chunks) {
   a.sum_blocks = static_cast<unsigned>((chunks * (a.k / kTile) + 7) / 8);
@@ -601,7 +569,7 @@ size_t embed_backward_bytes(int64_t n, int64_t v, int k, int num_sms) { return b
 
 cudaError_t launch_embed_backward(EmbedBackwardArgs a, void *workspace) {
   const BackwardSpace s = backward_space(a.n, a.v, a.k, a.num_sms);
-  uint8_t *w = static_cast<uint8_t *>(workspace);
+  uint8_t *w = space_base(workspace);
   a.count = reinterpret_cast<int *>(w);
   a.order = reinterpret_cast<int *>(w + s.order);
   a.sorted = reinterpret_cast<int *>(w + s.sorted);
