@@ -86,10 +86,14 @@ struct Lane8 {
   }
 };
 
+// Of memory that the grid writes too: the wide load says nothing of what it reads to the compiler (the inputs' loads
+// are free to pass others), so nothing moves across this one.
 template <typename T>
 __device__ __forceinline__ void load8(const T *p, int access, float (&o)[kLane]) {
   Lane8<T> r;
+  asm volatile("" ::: "memory");
   r.load(p, access);
+  asm volatile("" ::: "memory");
   r.values(0, o);
 }
 template <typename T>
@@ -430,12 +434,13 @@ __device__ __forceinline__ void join_run(const EmbedBackwardArgs &a, int2 span, 
       step = many ? kGroup : 1;
       more = many ? last / kGroup - from / kGroup : last - from;
     }
-    __threadfence();
     int came = 0;
-    __syncwarp();
+    __syncwarp();                          // lane 0 counts for the stores of all
+    __threadfence();
     if (lane == 0) came = atomicAdd(a.done + (static_cast<int64_t>(counter) * tiles + tile), 1);
     if (__shfl_sync(0xffffffffu, came, 0) != more) return;
-    __threadfence();                       // all parts are there
+    __threadfence();                       // all parts are there, for lane 0
+    __syncwarp();                          // and so for the others
     float *to = a.part + (static_cast<int64_t>(first * 2 + (first == from)) * a.k + col);
     const float *part = a.part + (static_cast<int64_t>(next) * 2 * a.k + col);
     const int64_t far = static_cast<int64_t>(step) * 2 * a.k;
