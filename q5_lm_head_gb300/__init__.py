@@ -750,6 +750,8 @@ class LMHead:
             how.temperatures = self._check(temperature, "temperature", torch.float32, (n,))
         else:
             how.temperature = temperature
+            if how.temperature == 0.0 and temperature != 0:
+                raise ValueError(f"temperature: {temperature}, need 2^-20 .. 2^20, or 0")
         if isinstance(top_k, torch.Tensor):
             how.top_ks = self._check(top_k, "top_k", torch.int32, (n,))
         else:
