@@ -80,7 +80,7 @@ struct Lane8 {
       reinterpret_cast<uint4 *>(p)[1] = reinterpret_cast<const uint4 *>(v)[sizeof(T) / 4];
     }
   }
-  __device__ __forceinline__ void values(int, float (&o)[kLane]) const {
+  __device__ __forceinline__ void values(float (&o)[kLane]) const {
 #pragma unroll
     for (int i = 0; i < kLane; ++i) o[i] = to_float(v[i]);
   }
@@ -94,7 +94,7 @@ __device__ __forceinline__ void load8(const T *p, int access, float (&o)[kLane])
   asm volatile("" ::: "memory");
   r.load(p, access);
   asm volatile("" ::: "memory");
-  r.values(0, o);
+  r.values(o);
 }
 template <typename T>
 __device__ __forceinline__ void store8(T *p, int access, const float (&o)[kLane]) {
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(256) embed_dense_kernel(const EmbedArgs a) {
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) {
       float o[kLane];
-      raw[j].values(lane, o);
+      raw[j].values(o);
 #pragma unroll
       for (int e = 0; e < kLane; ++e) o[e] = ok[j] ? o[e] * a.scale : 0.0f;
       if (to[j] >= 0) store8(static_cast<TO *>(a.out) + to[j], a.access_out, o);
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(256, 3) sum_runs_kernel(const __grid_constant_
             run = t;
           }
           float v[kLane];
-          raw[u].values(lane, v);
+          raw[u].values(v);
 #pragma unroll
           for (int i = 0; i < kLane; ++i) s[i] += v[i];
         }

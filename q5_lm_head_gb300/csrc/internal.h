@@ -177,7 +177,6 @@ struct SampleArgs {
   const float *uniforms;   // [n]
   int32_t *tokens;         // [n]
   float *logprobs;         // [n] or nullptr
-  int num_sms;
   cudaStream_t stream;
   // set at the launch: bytes of a CTA's share in shared memory; the call's only grid, its first or second
   int held_bytes = 0, grid = 0;
@@ -224,7 +223,7 @@ struct EmbedBackwardArgs {
   int *count, *order, *sorted;   // valid positions; they and their tokens by (token, position)
   int2 *span;              // [n] first place and end of a place's run
   uint32_t *used;          // [v / 32] which rows have a token
-  int *done;               // [chunks][k / 256] parts of the run that begins in a chunk
+  int *done;               // [chunks][k / 256] arrivals: parts of the run, or its groups, that begins in a chunk; of a group's chunks
   int64_t done_n;
   float *part;             // [chunks][2][k] sums of runs that chunks share
   int chunk, range;        // sorted positions of a chunk, tokens of a CTA

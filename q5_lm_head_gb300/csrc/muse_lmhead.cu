@@ -675,7 +675,6 @@ int run_sample(const muse_lmhead *h, const void *logits, int dtype, int64_t n, i
   a.uniforms = uniforms;
   a.tokens = tokens;
   a.logprobs = logprobs;
-  a.num_sms = h->num_sms;
   a.stream = stream;
   const cudaError_t e = muse::launch_sample(a);
   return e == cudaSuccess ? MUSE_OK : cuda_fail(e);

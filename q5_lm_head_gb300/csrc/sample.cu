@@ -1192,7 +1192,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         const float high_end = base - (static_cast<float>(at.bin) - 0.01f) / scale + wide;   // from here up no value is in the bin
         const auto hand = [&](float xi) {
           if (crowd) {
-            const uint32_t k = float_order_key(xi + 0.0f);   // -0 as 0
+            const uint32_t k = float_order_key(xi);   // -0 as 0
             crowd_low = min(crowd_low, k);
             crowd_high = max(crowd_high, k);
             ++crowd_n;
