@@ -493,7 +493,7 @@ __device__ __noinline__ double log_ratio(const float2 *table, unsigned long long
 }
 
 template <typename T, bool kHeld>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
   constexpr int W = Vec<T>::W;
   extern __shared__ __align__(16) uint8_t held[];
   __shared__ Shared sh;
