@@ -12,7 +12,7 @@
 // of a quantised one (a lane 16).  Bound: the dense rows' bytes (4,099 rows of 6,656
 // bf16 16.3 us, 5.2 TB/s over reads and writes, most of which L2 still holds at the
 // end); of blocks the unpacking, 40 million warp instructions for 16,384 rows, with the
-// issue slots at 72 % and the integer pipe at 67 %: 49.4 us, 5.1 TB/s.  One token 1.4 us.
+// issue slots at 72 % and the integer pipe at 67 %: 48.9 us, 5.1 TB/s.  One token 1.4 us (2.4 with its row in HBM).
 //
 // Gradient.  The positions are sorted by token first, stable, so that a row of the
 // table is written once, by whoever holds its sum, and the order of the sum is
@@ -26,9 +26,11 @@
 // for each of its chunks; the warp that counts in last adds them up in order, so no
 // warp waits for another and the bits do not depend on which that is.  Behind them
 // in the same grid, a warp a row, CTAs write the zeros of rows without a token.
-// Bound: HBM for a large table (16,384 positions and 202,048 x 6,656 bf16 443 us, 6.55
-// TB/s, 97 % of a copy's rate), else the two kernels' chains (the order 5 us for 301
-// positions, 13 for 16,384; 301 positions and 2,048 rows of 6,656 f32 20.5 us).
+// Bound: HBM for a large table (16,384 positions and 202,048 x 6,656 bf16 437 us, 6.65
+// TB/s, 98 % of a copy's rate), else the two kernels' chains (the order 5 us for 301
+// positions, 13 for 16,384; 301 positions and 2,048 rows of 6,656 f32 19.7 us).
+// Added to a table that is there, no zeros are written: 15.2, 41.5 and 154 us for 301 positions, 16,384 f16 into 32,003 x
+// 1,024 f32 and into the large table, the sort first among it.
 #include <atomic>
 
 #include "common.cuh"

@@ -19,9 +19,9 @@
 // of 2^E; the same logit always has the same weight.  A row whose exponents pass
 // 2^13 (a low temperature, or logits of 1e5) takes its weights in 64 bits.
 //
-// Bound: for few rows latency (a dozen cluster barriers and the passes' chains), for many the CUDA cores: one weight
-// takes 20 instructions and a table look-up of six bank cycles, so all passes but that of an unfiltered row avoid
-// them where they can.  A cluster of CTAs takes a row, each CTA a contiguous share, each warp a contiguous part of it,
+// Bound: for few rows latency (three cluster barriers with top-k or no filter, eight with top-p, and the passes'
+// chains), for many the CUDA cores: one weight takes 20 instructions and a table look-up of six bank cycles, so all
+// passes but that of an unfiltered row avoid them where they can.  A cluster of CTAs takes a row, each CTA a contiguous share, each warp a contiguous part of it,
 // so that prefix sums over CTAs and warps follow the index.  A share is held in shared memory where that fits, else
 // read again (from L2) by each pass.  The passes:
 //   - the maximum, maxima of groups of threads, a sample.
@@ -34,13 +34,15 @@
 //     error has a bound: of the row's mass they are 1 - p.  Then the bin in which the sum reaches p of the least and
 //     of the most that the mass can be, and in one more pass its values, settled one by one.  Where the two differ (one
 //     row in 13 of 202,048 bf16 values with 28,000 kept), the row's mass is summed as weights and the bin taken
-//     again.  1,024 such rows 512 us; with weights for every value and pass 1,169, with histograms over the ordered bits 2,296.
+//     again.  1,024 such rows 511 us; with weights for every value and pass 1,169, with histograms over the ordered bits 2,296.
 //     A bin of more than 512 values is settled if they are all equal, as 16-bit logits far from 0 are (1,024 bf16 rows
-//     around 8 467 us, selected as below 3,373).
+//     around 8, top-p 0.9: 464 us with a deviation of 2.5, selected as below 3,373; with 0.5 803).
 //   - the CTA in whose kept mass the number falls, its warp's part, its sixteenth, its value.
 // What does not fit (top-k's border among equal logits by the hundred, a crowd of different ones in a bin, weights in
 // 64 bits, top-k beyond some 300) is selected by histograms
-// over the ordered bits of the logits, 10 bits at a time.  Nothing is kept in global memory, so calls may overlap.
+// over the ordered bits of the logits, 10 bits at a time (1,024 bf16 rows with top-k 1,000 1,560 us, in 64 bits with
+// top-p 2,620; 512 f32 rows with a deviation of 0.01 and top-p 3,260; one f32 row of these 38, 67, 108).
+// Nothing is kept in global memory, so calls may overlap.
 #include <atomic>
 #include <type_traits>
 
@@ -1502,7 +1504,9 @@ constexpr int kWaves = 4, kLongRow = 32768;   // for a second grid
 // whole distribution, top-k, by CTAs a row: 32 rows 4 64, 24, 16, 8 57, 23, 15, 16 89, 34, 28; 64 rows 2 97, 34, 21, 4 77, 33,
 // 20, 8 92, 41, 28; 128 rows 1 184, 67, 38, 2 142, 51, 30, 4 142, 63, 39), 1,024 values each at least; with a third more
 // rows than two CTAs each have room, two each still (200 rows 198, 93, 74, one each 219, 106, 64); 16 CTAs share an SM with others
-// from eight rows on, which only long rows make up for (8 rows of 50,257 f32 16 26, 11.7, 12.4, 8 24, 11.7, 10.7).  A share is
+// from eight rows on, which only top-p over long rows makes up for (8 f32 rows, 16 and 8: of 50,257 26.3, 24.5 with top-p, 13.1,
+// 11.6 with top-k; of 81,920 28.8, 27.6; of 100,003 28.9, 29.7; of 131,072 31.3, 32.1, top-k 13.9, 12.4; of 202,048 40.2, 43.6,
+// 14.9, 13.9; 14 bf16 rows of 100,003 31.9, 31.0, of 131,072 32.8, 32.5, of 202,048 40.9, 43.3).  A share is
 // held in shared memory where two CTAs' fit into an SM's (16 rows of 202,048 bf16, 8 CTAs each: 39.8, 22.2, 13.7, read
 // again 40.9, 23.1, 14.1), or for the few rows that run at once with one CTA an SM.
 template <typename T>
@@ -1527,8 +1531,10 @@ cudaError_t launch_sample_grid(const SampleArgs &a) {
 
 // Rows that fill the SMs a few times go one to a CTA; what is left then would run by itself on half of the SMs, and
 // goes into a second grid, more CTAs a row, which begins as the first one's last rows end (202,048 bf16 with top-p, the whole
-// distribution, top-k: 320 rows in one grid 309, 128, 72 us, in two 207, 117, 63; 400 285, 134, 78, two 250, 139, 71; 1,024
-// 536, 280, 167, two 521, 285, 162; 1,024 rows of 16,384 131, 59, 48, two 131, 62, 51).
+// distribution, top-k: 320 rows in one grid 260, 130, 71 us, in two 214, 119, 63; 400 265, 134, 78, two 239, 137, 71; 1,024
+// 507, 275, 166, two 495, 279, 161).  From kLongRow on that gains more with few rows and top-p than it costs others: of
+// 24,576 320 rows 54, 32, 25, two 53, 33, 25, 1,024 116, 67, 52, two 115, 72, 55; of 32,768 320 65, 38, 27, two 60, 37, 27,
+// 1,024 131, 79, 56, two 134, 84, 59, 700 of f32 120, 60, 52, two 108, 63, 52; of 50,257 320 84, 54, 33, two 74, 49, 31.
 template <typename T>
 cudaError_t launch_sample_rows(SampleArgs a) {
   int fit = 0, pairs = 0;
