@@ -759,7 +759,7 @@ int muse_lmhead_embed(muse_lmhead *h, const void *table, int table_type, int64_t
   a.out = out;
   a.out_dtype = out_dtype;
   a.out_ld = out_ld;
-  a.access_in = row_access(table, table_type, table_ld);
+  a.access_in = table_type == MUSE_DTYPE_BLOCKS ? muse::kNarrow : row_access(table, table_type, table_ld);   // blocks have no distance
   a.access_out = row_access(out, out_dtype, out_ld);
   a.num_sms = h->num_sms;
   a.stream = static_cast<cudaStream_t>(stream);
